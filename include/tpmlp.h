@@ -69,7 +69,7 @@ typedef enum {
   TPMLP_ERR_UNSUPPORTED = -8,  /* e.g. bf16 with more than TPMLP_MAX_SHARDS   */
   TPMLP_ERR_DEVICE = -9,       /* current device is not sm_103 / shards handle
                                   belongs to another device                   */
-  TPMLP_ERR_BOUNDS = -10       /* debug build: a device-side index check failed */
+  TPMLP_ERR_BOUNDS = -10       /* a token or target id at or above V; debug build: a device-side index check failed */
 } tpmlp_status;
 
 /* Largest shard count of the bf16 tensor-core path (the fp32 path has none). */
@@ -428,6 +428,100 @@ int tpmlp_attn_heads(const void* X, int64_t batch, int64_t seq, const tpmlp_attn
  * shards, mode). */
 int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_attn_shards* shards, void* Y,
                        tpmlp_mode mode, void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The two ends of a training step around the blocks: the embedding lookup and
+ * its gradient, the cross entropy over the vocabulary and its gradients, and
+ * the gradients' global norm and clipping. (The pages have no counterpart;
+ * they stand beside the block calls for the library's users.)
+ *
+ * Ids (tokens, targets) are int64 in device memory. A negative id marks a row
+ * that does not count: its lookup is zero, its loss is zero, and it gives no
+ * gradient. An id at or above V is left out in the same way and records
+ * TPMLP_ERR_BOUNDS (check 8 for a target, 9 for a token) for the next
+ * tpmlp_check_status(). T, D and V are at most 2^30.
+ * ---------------------------------------------------------------------- */
+
+/* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward
+ * (backward = 1); 0 for T = 0 and on bad arguments. It grows with T * V / 16
+ * bytes forward, and with T * min(V, max(8192, 2^28 / T)) * 2 bytes backward
+ * (fp32: more by copies of X and W in bf16 pieces). */
+size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, int backward);
+
+/* Softmax cross entropy over the vocabulary, without keeping the logits:
+ *   z_tv = X_t . W_v,  lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target.
+ *   X        device [T, D] of type dt; T >= 0 (0 enqueues nothing).
+ *   W        device [V, D] of type dt: one row per id (an embedding table
+ *            can serve as it is). D a multiple of 8 (TPMLP_ERR_SHAPE).
+ *   targets  device int64 [T].
+ *   loss     device fp32 [T], 0 in rows that do not count.
+ *   lse      device fp32 [T], of every row; tpmlp_xent_backward needs it.
+ *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 0) bytes.
+ * Products, maxima and sums in fp32 in both types (fp32: the tensor cores on
+ * data split into three bf16 pieces). Bitwise reproducible. */
+int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
+                       tpmlp_dtype dt, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                       tpmlp_stream_t stream);
+
+/* Gradients of L = sum_t dloss_t loss_t of tpmlp_xent_forward for the same X,
+ * W and targets:
+ *   dz_tv = dloss_t (exp(z_tv - lse_t) - [v = target_t]),  dX = dz W,  dW = dz^T X,
+ * z computed again, piece by piece of the vocabulary.
+ *   lse      device fp32 [T], as tpmlp_xent_forward wrote it.
+ *   dloss    device fp32 [T] (for the mean over the rows that count: 1 / their number).
+ *   dX       device [T, D], dW device [V, D], of type dt (dX is the upstream
+ *            gradient that tpmlp_block_backward takes); both are written. In
+ *            bf16 dz is rounded to bf16 as an operand and each result once.
+ *            T = 0 clears dW.
+ *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 1) bytes.
+ * Rows that do not count must still hold finite X: they enter dW's product
+ * with a factor of zero. */
+int tpmlp_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse, const float* dloss,
+                        int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW, void* workspace,
+                        size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* Embedding lookup out_t = scale * E[id_t].
+ *   E    device [V, D] of type dt, any D >= 1.
+ *   ids  device int64 [T], T >= 0 (0 enqueues nothing).
+ *   out  device [T, D] of type dt, zero in rows that do not count. */
+int tpmlp_embed_forward(const void* E, const int64_t* ids, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, float scale,
+                        void* out, tpmlp_stream_t stream);
+
+/* Workspace bytes of tpmlp_embed_backward; 0 for T = 0 and on bad arguments. */
+size_t tpmlp_embed_workspace_bytes(int64_t T, int64_t D, int64_t V);
+
+/* Gradient of the table: dE_v = scale * sum of dout_t over the t with id_t = v,
+ * in the order of t and in fp32, so bitwise reproducible; with accumulate != 0
+ * it is added to dE (rounded once, after the addition), else rows of ids that
+ * do not occur are zero.
+ *   dout  device [T, D] of type dout_dt (fp32 as tpmlp_block_backward gives it, or bf16).
+ *   dE    device [V, D] of type dE_dt.
+ *   workspace  at least tpmlp_embed_workspace_bytes(T, D, V) bytes. */
+int tpmlp_embed_backward(const void* dout, tpmlp_dtype dout_dt, const int64_t* ids, int64_t T, int64_t D, int64_t V,
+                         float scale, void* dE, tpmlp_dtype dE_dt, int accumulate, void* workspace,
+                         size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* Workspace bytes of tpmlp_grad_norm and tpmlp_grad_clip for n tensors. */
+size_t tpmlp_grad_workspace_bytes(int n);
+
+/* Global norm of n gradients: norm[0] = sqrt(sum of the squares of all their
+ * elements). Squares in fp32 (a square above the fp32 range makes the norm
+ * infinite), their sums in fp64, in a fixed order.
+ *   grads   host array of n device pointers; counts, dts their element counts
+ *           (0 allowed: the pointer is then not looked at) and types.
+ *   norm    device fp32 [1].
+ *   workspace  at least tpmlp_grad_workspace_bytes(n) bytes. */
+int tpmlp_grad_norm(const void* const* grads, const int64_t* counts, const tpmlp_dtype* dts, int n, float* norm,
+                    void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* Clipping by the global norm: out_i = min(1, max_norm / (norm + 1e-6)) grads_i.
+ *   out     host array of n device pointers of the gradients' types, or NULL:
+ *           in place. No written tensor may overlap another tensor of the call
+ *           (TPMLP_ERR_ARG); out_i may be grads_i.
+ *   norm    device fp32 [1]: the norm before clipping.
+ *   max_norm  finite, >= 0. Other arguments as for tpmlp_grad_norm. */
+int tpmlp_grad_clip(const void* const* grads, const int64_t* counts, const tpmlp_dtype* dts, int n, float max_norm,
+                    void* const* out, float* norm, void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
 
 /* Per-step timing, switched on by TPMLP_TRACE=1 in the environment (read once
  * per process; the method the pages use to find where a layer's time goes,

@@ -83,6 +83,16 @@ SIGNATURES = {
     "tpmlp_forward_sp": (_I, [ctypes.POINTER(_P), _I64, _P, ctypes.POINTER(_P), _I, _P, _SZ, _P]),
     "tpmlp_backward_sp": (_I, [ctypes.POINTER(_P), ctypes.POINTER(_P), _I64, _P, ctypes.POINTER(_P),
                                ctypes.POINTER(_P), ctypes.POINTER(_P), _I, _P, _SZ, _P]),
+    "tpmlp_xent_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "tpmlp_xent_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "tpmlp_xent_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "tpmlp_embed_forward": (_I, [_P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P, _P]),
+    "tpmlp_embed_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "tpmlp_embed_backward": (_I, [_P, _I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
+    "tpmlp_grad_workspace_bytes": (_SZ, [_I]),
+    "tpmlp_grad_norm": (_I, [ctypes.POINTER(_P), ctypes.POINTER(_I64), ctypes.POINTER(_I), _I, _P, _P, _SZ, _P]),
+    "tpmlp_grad_clip": (_I, [ctypes.POINTER(_P), ctypes.POINTER(_I64), ctypes.POINTER(_I), _I, ctypes.c_float,
+                             ctypes.POINTER(_P), _P, _P, _SZ, _P]),
     "tpmlp_trace_read": (_I, [ctypes.c_char_p, _SZ, ctypes.POINTER(_I)]),
     "tpmlp_trace_enabled": (_I, []),
     "tpmlp_build_flags": (_I, []),
@@ -523,6 +533,188 @@ def tpmlp_attn_forward(X: torch.Tensor, batch: int, shards: AttnShards, mode="fa
                                     ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
            "tpmlp_attn_forward")
     return Y
+
+
+# ------------------------------------------------- the two ends of a training step
+
+def _here(*tensors) -> torch.device:
+    """The current device, which every tensor of a call must be on."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if t.device.index != cur:
+            raise ValueError(f"a tensor is on {t.device}, but device {cur} is current")
+    return tensors[0].device if tensors else torch.device("cuda", cur)
+
+
+def _ids(t: torch.Tensor, T: int, name: str) -> int:
+    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != T:
+        raise ValueError(f"{name} must be an int64 tensor of {T} ids")
+    return _dev(t, name)
+
+
+def _like(t: torch.Tensor, shape, dtype: torch.dtype, name: str) -> int:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return _dev(t, name)
+
+
+class _On:
+    """Allocates a call's outputs and workspace on the call's stream, so that the
+    caching allocator does not hand their memory to another stream's work
+    while the call may still use it."""
+
+    def __init__(self, stream):
+        self.ctx = None
+        if stream is not None:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+            if s != torch.cuda.current_stream():
+                self.ctx = torch.cuda.stream(s)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def tpmlp_xent_workspace_bytes(T: int, D: int, V: int, dtype: torch.dtype, backward: int = 0) -> int:
+    return int(lib().tpmlp_xent_workspace_bytes(T, D, V, TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32,
+                                                int(backward)))
+
+
+def _xent_shapes(X: torch.Tensor, W: torch.Tensor):
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1] or X.dtype != W.dtype:
+        raise ValueError("X must be [T, D] and W [V, D], of one dtype")
+    return X.shape[0], X.shape[1], W.shape[0]
+
+
+def tpmlp_xent_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Cross entropy of softmax(X W^T) at the targets without keeping the logits:
+    (loss [T], lse [T]) fp32. A negative target's row has no loss."""
+    T, D, V = _xent_shapes(X, W)
+    dev = _here(X, W, targets)
+    dt = _dt(X)
+    with _On(stream):
+        loss = torch.empty(T, dtype=torch.float32, device=dev) if loss is None else loss
+        lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
+        ws = _workspace(int(lib().tpmlp_xent_workspace_bytes(T, D, V, dt, 0)), workspace)
+        _check(lib().tpmlp_xent_forward(_dev(X, "X"), _dev(W, "W"), _ids(targets, T, "targets"), T, D, V, dt,
+                                        _like(loss, (T,), torch.float32, "loss"),
+                                        _like(lse, (T,), torch.float32, "lse"), ws.data_ptr(),
+                                        ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_xent_forward")
+    return loss, lse
+
+
+def tpmlp_xent_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                        dloss: torch.Tensor, dX: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum(dloss * loss) of tpmlp_xent_forward: (dX [T, D], dW [V, D]) of X's dtype."""
+    T, D, V = _xent_shapes(X, W)
+    dev = _here(X, W, targets, lse, dloss)
+    dt = _dt(X)
+    with _On(stream):
+        dX = torch.empty((T, D), dtype=X.dtype, device=dev) if dX is None else dX
+        dW = torch.empty((V, D), dtype=X.dtype, device=dev) if dW is None else dW
+        ws = _workspace(int(lib().tpmlp_xent_workspace_bytes(T, D, V, dt, 1)), workspace)
+        _check(lib().tpmlp_xent_backward(_dev(X, "X"), _dev(W, "W"), _ids(targets, T, "targets"),
+                                         _like(lse, (T,), torch.float32, "lse"),
+                                         _like(dloss, (T,), torch.float32, "dloss"), T, D, V, dt,
+                                         _like(dX, (T, D), X.dtype, "dX"), _like(dW, (V, D), X.dtype, "dW"),
+                                         ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+               "tpmlp_xent_backward")
+    return dX, dW
+
+
+def tpmlp_embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """out[t] = scale * E[ids[t]], of E's dtype; zero rows for negative ids."""
+    V, D = E.shape
+    T = ids.shape[0]
+    dev = _here(E, ids)
+    with _On(stream):
+        out = torch.empty((T, D), dtype=E.dtype, device=dev) if out is None else out
+        _check(lib().tpmlp_embed_forward(_dev(E, "E"), _ids(ids, T, "ids"), T, D, V, _dt(E), float(scale),
+                                         _like(out, (T, D), E.dtype, "out"), _stream(stream)), "tpmlp_embed_forward")
+    return out
+
+
+def tpmlp_embed_workspace_bytes(T: int, D: int, V: int) -> int:
+    return int(lib().tpmlp_embed_workspace_bytes(T, D, V))
+
+
+def tpmlp_embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+                         dE: Optional[torch.Tensor] = None, accumulate: bool = False,
+                         dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """dE[v] = scale * sum of dout[t] over ids[t] = v, [V, D] of `dtype` (default
+    dout's); with accumulate, added to the given dE."""
+    T, D = dout.shape
+    dev = _here(dout, ids)
+    if accumulate and dE is None:
+        raise ValueError("accumulate needs dE")
+    if dE is None:
+        dtype = dout.dtype if dtype is None else dtype
+    elif dtype is not None and dtype != dE.dtype:
+        raise ValueError("dtype and dE disagree")
+    with _On(stream):
+        dE = torch.empty((V, D), dtype=dtype, device=dev) if dE is None else dE
+        ws = _workspace(tpmlp_embed_workspace_bytes(T, D, V), workspace)
+        _check(lib().tpmlp_embed_backward(_dev(dout, "dout"), _dt(dout), _ids(ids, T, "ids"), T, D, V, float(scale),
+                                          _like(dE, (V, D), dE.dtype, "dE"), _dt(dE), int(bool(accumulate)),
+                                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+               "tpmlp_embed_backward")
+    return dE
+
+
+def tpmlp_grad_workspace_bytes(n: int) -> int:
+    return int(lib().tpmlp_grad_workspace_bytes(n))
+
+
+def _grads(grads: Sequence[torch.Tensor]):
+    n = len(grads)
+    return ((ctypes.c_void_p * n)(*[_dev(g, "a gradient") for g in grads]),
+            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int * n)(*[_dt(g) for g in grads]), n)
+
+
+def tpmlp_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The global norm of all gradients (fp32 and bf16 tensors mixed): [1] fp32."""
+    dev = _here(*grads)
+    with _On(stream):
+        norm = torch.empty(1, dtype=torch.float32, device=dev) if norm is None else norm
+        p, c, d, n = _grads(grads)
+        ws = _workspace(tpmlp_grad_workspace_bytes(n), workspace)
+        _check(lib().tpmlp_grad_norm(p, c, d, n, _like(norm, (1,), torch.float32, "norm"), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_grad_norm")
+    return norm
+
+
+def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
+                    norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Scales all gradients by min(1, max_norm / (norm + 1e-6)), in place or into
+    `out`, and returns their global norm before that: [1] fp32."""
+    dev = _here(*grads)
+    if out is not None:
+        if len(out) != len(grads):
+            raise ValueError("out must have one tensor for each gradient")
+        _here(*out)
+        for g, o in zip(grads, out):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError("out must have the gradients' shapes and dtypes")
+    with _On(stream):
+        norm = torch.empty(1, dtype=torch.float32, device=dev) if norm is None else norm
+        p, c, d, n = _grads(grads)
+        ws = _workspace(tpmlp_grad_workspace_bytes(n), workspace)
+        _check(lib().tpmlp_grad_clip(p, c, d, n, float(max_norm), None if out is None else _ptrs(out, "out"),
+                                     _like(norm, (1,), torch.float32, "norm"), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_grad_clip")
+    return norm
 
 
 def tpmlp_selftest_gemm_withheld_fill(X: torch.Tensor, shards: Shards, H: torch.Tensor, fill: int, limit_ms: int,

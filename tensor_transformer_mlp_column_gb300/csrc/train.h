@@ -1,0 +1,128 @@
+// train.h — kernel launchers of the two ends of a training step: the
+// cross entropy over the vocabulary (xent.cu, xent_gemm.cu), the embedding
+// and its gradient (embed.cu), and the gradients' global norm and clipping
+// (clip.cu). Not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace tpmlp {
+
+// What the status word holds when an id (a target or a token) was at or above
+// V: its row is left out, as a negative id's is, and the next
+// tpmlp_check_status() returns TPMLP_ERR_BOUNDS.
+constexpr int kChkTarget = 8;
+constexpr int kChkToken = 9;
+
+// ------------------------------------------------------------------ clip.cu
+
+// One launch's worth of tensors, passed by value as a kernel parameter (so a
+// captured graph carries its own copy and nothing is copied to the device).
+constexpr int kClipBatch = 256;
+struct ClipTensors {
+  const void* src[kClipBatch];
+  void* dst[kClipBatch];
+  int64_t count[kClipBatch];       // elements, >= 1
+  int64_t first[kClipBatch + 1];   // index of the tensor's first chunk; first[n] = all chunks
+  uint8_t bf16[kClipBatch];
+  int n;
+};
+// Chunks of a tensor: the unit of work of one CTA.
+int64_t clip_chunks(int64_t count);
+// CTAs of a launch over `chunks` chunks (a function of the sizes alone, so the
+// order of the sums is too).
+int clip_grid(int64_t chunks);
+// part[b] = the sum of squares of CTA b's chunks.
+constexpr int kClipMaxGrid = 1024;
+cudaError_t launch_clip_sumsq(const ClipTensors& t, double* part, cudaStream_t s);
+// norm[0] = sqrt(sum of part[0 .. nparts)).
+cudaError_t launch_clip_norm(const double* part, int nparts, float* norm, cudaStream_t s);
+// dst = min(1, max_norm / (norm + 1e-6)) src; writes norm[0] too when it is given.
+cudaError_t launch_clip_scale(const ClipTensors& t, const double* part, int nparts, float max_norm, float* norm,
+                              cudaStream_t s);
+
+// ------------------------------------------------------------------ embed.cu
+
+// out[t] = scale * E[ids[t]], zero for a negative id; E and out of one type.
+cudaError_t launch_embed(const void* E, const int64_t* ids, int64_t T, int64_t D, int64_t V, int is_bf16, float scale,
+                         void* out, int* status, cudaStream_t s);
+
+// Byte offsets of the gradient's scratch.
+struct EmbedPlan {
+  size_t key[2], pos[2];  // int32 [T] each, twice: the sort's source and destination
+  size_t counts;          // the sort's digit counts
+  size_t part;            // fp32 [2 chunks][D]: sums of segments that cross a chunk's border
+  size_t total;
+};
+EmbedPlan plan_embed(int64_t T, int64_t D, int64_t V);
+// dE[v] (+)= scale * sum over t with ids[t] = v of dout[t], in the order of t.
+cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* ids, int64_t T, int64_t D, int64_t V,
+                              float scale, void* dE, int dE_bf16, int accumulate, void* ws, int* status,
+                              cudaStream_t s);
+
+// ------------------------------------------------------------------ xent.cu, xent_gemm.cu
+
+// One tensor-core product of the cross entropy (CTA pairs, 256 x 256 tiles):
+//   acc[m, n] = sum over the plane pairs (a, b), in order, of
+//               sum_k A_a[m, k] B_b[n, k]
+// with bf16 operands and fp32 accumulation. bf16 data have one plane and one
+// pair; fp32 data are split into three bf16 planes (high, middle, low) and
+// take the six pairs whose product is not below fp32 rounding. With slices >
+// 1 the K blocks are cut into that many runs, each its own output.
+enum XentEpilogue : int {
+  kXentStats = 0,    // per row and 128 columns: (max, sum of exponentials) of the logits; the target's logit
+  kXentGrad = 1,     // dz, bf16
+  kXentGradF32 = 2,  // dz in three bf16 planes
+  kXentOutBf16 = 3,  // out bf16 = scale * acc
+  kXentOutF32 = 4,   // out fp32 = scale * acc, or (add) out += acc
+};
+constexpr int kXentPlanes = 3;
+constexpr int kXentPairs = 6;
+constexpr int kXentPart = 128;    // columns of one (max, sum) part
+constexpr int kXentDmaxParts = 64;
+struct XentGemm {
+  CUtensorMap map_a[kXentPlanes], map_b[kXentPlanes];
+  CUtensorMap map_out[kXentPlanes];  // bf16: make_output_map_bf16; fp32: make_output_map_f32, slices stacked by rows
+  int pairs;                         // 1 or kXentPairs
+  int M, N, K;
+  int slices;                        // >= 1; more than the K blocks allow are not used
+  int64_t slice_rows;                // rows between two slices of the output map
+  int mn_major;                      // TcMajor bits
+  int group_m;
+  int epi;
+  int add;                           // kXentOutF32
+  // kXentStats, kXentGrad*
+  const int64_t* targets;            // [M]
+  int64_t V, col0;                   // all ids; the id of column 0
+  float2* stats;                     // [ceil(N / kXentPart)][M]: max in units of log2, sum of 2^(z - max)
+  float* zt;                         // [M]: the target's logit
+  const float* lse;                  // [M]
+  const float* dloss;                // [M]
+  const float* dmax;                 // [kXentDmaxParts] parts of the largest |dloss|; as the scale of kXentOut* (may be null)
+};
+// Slices that K is really cut into when `slices` are asked for.
+int xent_slices(int K, int slices);
+cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s);
+
+struct XentPlan {
+  size_t planes_x, planes_w;  // fp32: bf16 planes [3][T][D], [3][V][D]
+  size_t stats, zt;           // forward
+  size_t dmax, dz, dx, dw;    // backward
+  size_t total;
+  int64_t piece;              // columns of a piece of the vocabulary (a multiple of 256, or V)
+  int64_t dz_pitch;           // columns of dz's rows
+  int slices_x, slices_w;     // slices of the dX and dW products
+  bool dx_part;               // dX goes through fp32 partial sums
+};
+XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward);
+cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
+                             int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
+                             cudaStream_t s);
+cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,
+                              const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
+                              void* ws, uint64_t wait_ns, cudaStream_t s);
+
+}  // namespace tpmlp

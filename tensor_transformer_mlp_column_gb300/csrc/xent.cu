@@ -1,0 +1,430 @@
+// xent.cu — softmax cross entropy over a large vocabulary, without keeping
+// the logits, and its gradient:
+//
+//   z_tv = x_t . w_v,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target(t),
+//   dz_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),  dX = dz W,  dW = dz^T X.
+//
+// Forward: one tensor-core product whose epilogue reduces each row's 128
+// columns to (max, sum of exponentials) while the next tile is computed, then
+// one small kernel that joins the parts: 2 T V D operations, nothing of the
+// size T x V is written (8 bytes per 128 logits).
+//
+// Backward, in pieces of the vocabulary: the logits of a piece are computed
+// again (2 T V D) and leave the chip as dz in bf16, which the two products dX
+// += dz W and dW = dz^T X read (4 T V D). dz is divided by the largest |dloss|
+// before it is rounded and the products are multiplied by it: with the usual
+// equal row gradients dz of a target is then -(1 - p), which bf16 holds
+// closely where p is small, instead of a number whose rounding would scale
+// every target's gradient by the same up to 2^-8.
+//
+// fp32 data are split into three bf16 planes (24 bits in all) and every
+// product is the sum of the six plane products that are not below fp32
+// rounding, accumulated in one fp32 accumulator: six times the bf16 work,
+// where the CUDA cores would take about thirty times.
+#include "device.cuh"
+#include "internal.h"
+#include "tpmlp.h"
+#include "trace.h"
+#include "train.h"
+
+namespace tpmlp {
+
+namespace {
+
+// A launcher's status, passed on; the step is timed under TPMLP_TRACE=1.
+#define XENT_STEP(phase, s, expr)          \
+  do {                                     \
+    TraceScope trace_scope_(phase, s);     \
+    const cudaError_t e_ = (expr);         \
+    if (e_ != cudaSuccess) return e_;      \
+  } while (0)
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Row t's parts joined: lse = ln 2 (M + log2 sum_i s_i 2^(m_i - M)). A CTA
+// takes 32 rows, warp w the parts w, w + 8, ..., joined in the warps' order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2* __restrict__ stats, int parts, int64_t T,
+                                                                    const int64_t* __restrict__ targets, int64_t V,
+                                                                    const float* __restrict__ zt, float* __restrict__ loss,
+                                                                    float* __restrict__ lse, int* status) {
+  __shared__ float2 red[kJoinWarps][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * 32 + l;
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](float2 p) {
+    const float top = fmaxf(m, p.x);
+    const float base = top == -INFINITY ? 0.f : top;
+    s = s * exp2f(m - base) + p.y * exp2f(p.x - base);
+    m = top;
+  };
+  if (t < T) {
+#pragma unroll 4
+    for (int i = w; i < parts; i += kJoinWarps) add(stats[int64_t(i) * T + t]);
+  }
+  red[w][l] = make_float2(m, s);
+  __syncthreads();
+  if (w != 0 || t >= T) return;
+  for (int i = 1; i < kJoinWarps; ++i) add(red[i][l]);
+  const float v = kLn2 * (m + log2f(s));
+  const int64_t target = targets[t];
+  if (target >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkTarget);
+  lse[t] = v;
+  loss[t] = target >= 0 && target < V ? v - zt[t] : 0.f;
+}
+
+// parts[b] = the largest |dloss| among CTA b's rows that count.
+__global__ void __launch_bounds__(256) xent_dmax_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
+                                                        int64_t T, int64_t V, float* __restrict__ parts) {
+  __shared__ float red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  float m = 0.f;
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256) {
+    const int64_t id = targets[t];
+    if (id >= 0 && id < V) m = fmaxf(m, fabsf(dloss[t]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+    parts[blockIdx.x] = m;
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// x = high + middle + low, each the bf16 nearest to what the ones before
+// leave: 24 bits in all. n8 groups of 8 elements, planes n8 * 8 apart.
+__global__ void __launch_bounds__(256) xent_split_kernel(const float* __restrict__ x, int64_t n8, uint16_t* __restrict__ out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n8; i += int64_t(gridDim.x) * 256) {
+    const float4 a = reinterpret_cast<const float4*>(x)[2 * i], b = reinterpret_cast<const float4*>(x)[2 * i + 1];
+    float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int pl = 0; pl < kXentPlanes; ++pl) {
+      reinterpret_cast<uint4*>(out)[pl * n8 + i] =
+          make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] -= __bfloat162float(__float2bfloat16_rn(f[j]));
+    }
+  }
+}
+
+// out = dmax * (part[0] + part[1] + ...), n4 groups of 4 elements, slices
+// stride4 groups apart.
+template <typename E>
+__global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restrict__ part, int slices, int64_t stride4,
+                                                          int64_t n4, const float* __restrict__ dmax, E* __restrict__ out) {
+  __shared__ float scale_s;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x < 32) {
+    float m = 0.f;
+    for (int i = threadIdx.x; i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x == 0) scale_s = m;
+  }
+  __syncthreads();
+  const float scale = scale_s;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += int64_t(gridDim.x) * 256) {
+    float4 v = part[i];
+#pragma unroll 4
+    for (int k = 1; k < slices; ++k) {
+      const float4 a = part[k * stride4 + i];
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+    v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+    if constexpr (sizeof(E) == 4)
+      reinterpret_cast<float4*>(out)[i] = v;
+    else
+      reinterpret_cast<uint2*>(out)[i] = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+  }
+}
+
+int grid_for(int64_t items) {
+  const int64_t want = (items + 255) / 256, cap = int64_t(num_sms()) * 8;
+  return static_cast<int>(want < 1 ? 1 : want < cap ? want : cap);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+int64_t ceil_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// Rows of one slice of a product's fp32 partial sums: a warp's store covers 32.
+int64_t slice_rows(int64_t M) { return ceil_to(M, 32); }
+
+// Into how many runs a product's K is cut: few output tiles leave most of the
+// GPU idle for the whole of a long K, more runs cost their partial sums'
+// traffic. Cost in K blocks of a tile's work: the rounds over the CTA pairs
+// times (K blocks of a run + the fill of the pipeline and the epilogue, about
+// 8 of them), and the partial sums written and read back, one K block being
+// about 0.28 us, in which the GPU moves about 1.9 MB.
+int choose_slices(int64_t M, int64_t N, int64_t K, int pairs) {
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t kb = ((K + 63) / 64) * pairs;
+  const int64_t units = num_sms() > 1 ? num_sms() / 2 : 1;
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= 64 && s <= (K + 63) / 64; ++s) {
+    const double rounds = double((tiles * s + units - 1) / units);
+    double cost = rounds * (double(kb) / s + 8);
+    if (s > 1) cost += 2.0 * s * double(M) * double(N) * 4 / 1.9e6 + 12;
+    if (s == 1 || cost < 0.97 * best_cost) best = s, best_cost = cost;
+  }
+  return best;
+}
+
+bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+  return make_operand_map(m, base, rows, cols, pitch, 128);
+}
+// MN-major operand (a row-major [rows][cols] tensor contracted over its rows).
+bool mn_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, bool is_b, int* major) {
+  *major |= is_b ? kMnB : kMnA;
+  if (cols % 64 == 0 && make_operand_map_mn3d(m, base, rows, cols, pitch)) {
+    *major |= is_b ? kMnB3d : kMnA3d;
+    return true;
+  }
+  return make_operand_map(m, base, rows, cols, pitch, 64);
+}
+
+template <typename T>
+T* at(void* base, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(base) + off);
+}
+
+cudaError_t split(const void* x, int64_t n, void* out, cudaStream_t s) {
+  return launch_pdl(xent_split_kernel, dim3(grid_for(n / 8)), dim3(256), 0, s, static_cast<const float*>(x), n / 8,
+                    static_cast<uint16_t*>(out));
+}
+
+// The bf16 planes of X [T][D] and W [V][D]: the data themselves, or split.
+struct Planes {
+  const uint16_t *x[kXentPlanes], *w[kXentPlanes];
+  int n;
+};
+cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int is_bf16, void* ws,
+                      const XentPlan& p, Planes* out, cudaStream_t s) {
+  out->n = is_bf16 ? 1 : kXentPlanes;
+  if (is_bf16) {
+    out->x[0] = static_cast<const uint16_t*>(X);
+    out->w[0] = static_cast<const uint16_t*>(W);
+    return cudaSuccess;
+  }
+  XENT_STEP("xent_split", s, split(X, T * D, at<char>(ws, p.planes_x), s));
+  XENT_STEP("xent_split", s, split(W, V * D, at<char>(ws, p.planes_w), s));
+  for (int i = 0; i < kXentPlanes; ++i) {
+    out->x[i] = at<uint16_t>(ws, p.planes_x) + i * T * D;
+    out->w[i] = at<uint16_t>(ws, p.planes_w) + i * V * D;
+  }
+  return cudaSuccess;
+}
+
+// out [M][N] = dmax * acc (is_bf16: rounded once), through fp32 partial sums
+// where the K of g is cut.
+cudaError_t product_out(XentGemm& g, void* out, float* part, int is_bf16, uint64_t wait_ns, cudaStream_t s,
+                        const char* phase) {
+  const int slices = xent_slices(g.K, g.slices);
+  if (slices == 1) {
+    if (!(is_bf16 ? make_output_map_bf16(&g.map_out[0], out, g.M, g.N, g.N)
+                  : make_output_map_f32(&g.map_out[0], out, g.M, g.N, g.N)))
+      return cudaErrorInvalidValue;
+    g.epi = is_bf16 ? kXentOutBf16 : kXentOutF32;
+    g.slices = 1;
+    XENT_STEP(phase, s, launch_xent_gemm(g, wait_ns, s));
+    return cudaSuccess;
+  }
+  const int64_t rows = slice_rows(g.M);
+  if (!make_output_map_f32(&g.map_out[0], part, rows * slices, g.N, g.N)) return cudaErrorInvalidValue;
+  const float* dmax = g.dmax;
+  g.dmax = nullptr;
+  g.epi = kXentOutF32;
+  g.slice_rows = rows;
+  XENT_STEP(phase, s, launch_xent_gemm(g, wait_ns, s));
+  const int64_t n4 = int64_t(g.M) * g.N / 4, stride4 = rows * g.N / 4;
+  if (is_bf16)
+    XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<__nv_bfloat16>, dim3(grid_for(n4)), dim3(256), 0, s,
+                                           reinterpret_cast<const float4*>(part), slices, stride4, n4, dmax,
+                                           static_cast<__nv_bfloat16*>(out)));
+  else
+    XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s,
+                                           reinterpret_cast<const float4*>(part), slices, stride4, n4, dmax,
+                                           static_cast<float*>(out)));
+  return cudaSuccess;
+}
+
+}  // namespace
+
+XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
+  XentPlan p{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t a = off;
+    off = up256(off + bytes);
+    return a;
+  };
+  const int planes = is_bf16 ? 1 : kXentPlanes, pairs = is_bf16 ? 1 : kXentPairs;
+  if (!is_bf16) {
+    p.planes_x = take(size_t(T) * D * 2 * planes);
+    p.planes_w = take(size_t(V) * D * 2 * planes);
+  }
+  if (!backward) {
+    p.stats = take(size_t((V + kXentPart - 1) / kXentPart) * T * sizeof(float2));
+    p.zt = take(size_t(T) * 4);
+    p.total = off;
+    return p;
+  }
+  // A piece's dz takes at most 512 MB (all planes together), but a piece has
+  // at least 8192 columns: each piece adds its share of dX in fp32, 16 T D
+  // bytes of traffic against 4 T D 8192 operations.
+  int64_t piece = (int64_t(1) << 28) / (T * planes) / 256 * 256;
+  if (piece < 8192) piece = 8192;
+  if (piece >= V) piece = V;
+  p.piece = piece;
+  p.dz_pitch = ceil_to(piece, 64);
+  p.dmax = take(kXentDmaxParts * 4);
+  p.dz = take(size_t(T) * p.dz_pitch * 2 * planes);
+  p.slices_x = xent_slices(static_cast<int>(p.dz_pitch), choose_slices(T, D, p.dz_pitch, pairs));
+  p.slices_w = xent_slices(static_cast<int>(T), choose_slices(piece, D, T, pairs));
+  p.dx_part = piece < V || p.slices_x > 1;
+  if (p.dx_part) p.dx = take(size_t(p.slices_x) * slice_rows(T) * D * 4);
+  if (p.slices_w > 1) p.dw = take(size_t(p.slices_w) * slice_rows(piece) * D * 4);
+  p.total = off;
+  return p;
+}
+
+cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
+                             int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
+                             cudaStream_t s) {
+  const XentPlan p = plan_xent(T, D, V, is_bf16, 0);
+  Planes pl;
+  cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
+  if (e != cudaSuccess) return e;
+  XentGemm g{};
+  for (int i = 0; i < pl.n; ++i)
+    if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i], V, D, D))
+      return cudaErrorInvalidValue;
+  g.pairs = pl.n == 1 ? 1 : kXentPairs;
+  g.M = static_cast<int>(T);
+  g.N = static_cast<int>(V);
+  g.K = static_cast<int>(D);
+  g.slices = 1;
+  g.group_m = 16;
+  g.epi = kXentStats;
+  g.targets = targets;
+  g.V = V;
+  g.stats = at<float2>(ws, p.stats);
+  g.zt = at<float>(ws, p.zt);
+  XENT_STEP("xent_logits", s, launch_xent_gemm(g, wait_ns, s));
+  const int parts = static_cast<int>((V + kXentPart - 1) / kXentPart);
+  XENT_STEP("xent_join", s,
+            launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
+                       static_cast<const float2*>(g.stats), parts, T, targets, V, static_cast<const float*>(g.zt), loss,
+                       lse, status));
+  return cudaSuccess;
+}
+
+cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,
+                              const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
+                              void* ws, uint64_t wait_ns, cudaStream_t s) {
+  const XentPlan p = plan_xent(T, D, V, is_bf16, 1);
+  Planes pl;
+  cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
+  if (e != cudaSuccess) return e;
+  const int pairs = pl.n == 1 ? 1 : kXentPairs;
+  const size_t es = is_bf16 ? 2 : 4;
+  float* dmax = at<float>(ws, p.dmax);
+  XENT_STEP("xent_dmax", s, launch_pdl(xent_dmax_kernel, dim3(kXentDmaxParts), dim3(256), 0, s, dloss, targets, T, V, dmax));
+  uint16_t* dz[kXentPlanes];
+  for (int i = 0; i < pl.n; ++i) dz[i] = at<uint16_t>(ws, p.dz) + i * T * p.dz_pitch;
+  for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+    const int64_t vc = V - v0 < p.piece ? V - v0 : p.piece, vp = ceil_to(vc, 64);
+    // dz of the piece, from its logits computed again; columns vc .. vp are zeros.
+    XentGemm g{};
+    for (int i = 0; i < pl.n; ++i)
+      if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i] + v0 * D, vc, D, D) ||
+          !make_output_map_bf16(&g.map_out[i], dz[i], T, vp, p.dz_pitch))
+        return cudaErrorInvalidValue;
+    g.pairs = pairs;
+    g.M = static_cast<int>(T);
+    g.N = static_cast<int>(vc);
+    g.K = static_cast<int>(D);
+    g.slices = 1;
+    g.group_m = 16;
+    g.epi = is_bf16 ? kXentGrad : kXentGradF32;
+    g.targets = targets;
+    g.V = V;
+    g.col0 = v0;
+    g.lse = lse;
+    g.dloss = dloss;
+    g.dmax = dmax;
+    XENT_STEP("xent_dz", s, launch_xent_gemm(g, wait_ns, s));
+
+    // dW of the piece = dz^T X.
+    g = XentGemm{};
+    for (int i = 0; i < pl.n; ++i)
+      if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major) ||
+          !mn_map(&g.map_b[i], pl.x[i], T, D, D, true, &g.mn_major))
+        return cudaErrorInvalidValue;
+    g.pairs = pairs;
+    g.M = static_cast<int>(vc);
+    g.N = static_cast<int>(D);
+    g.K = static_cast<int>(T);
+    g.slices = p.slices_w;
+    g.group_m = 16;
+    g.dmax = dmax;
+    if ((e = product_out(g, static_cast<char*>(dW) + v0 * D * es, at<float>(ws, p.dw), is_bf16, wait_ns, s, "xent_dW")) !=
+        cudaSuccess)
+      return e;
+
+    // dX += dz W over the piece.
+    g = XentGemm{};
+    for (int i = 0; i < pl.n; ++i)
+      if (!operand_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch) ||
+          !mn_map(&g.map_b[i], pl.w[i] + v0 * D, vc, D, D, true, &g.mn_major))
+        return cudaErrorInvalidValue;
+    g.pairs = pairs;
+    g.M = static_cast<int>(T);
+    g.N = static_cast<int>(D);
+    g.K = static_cast<int>(vp);
+    g.group_m = 8;
+    g.dmax = dmax;
+    if (p.piece == V) {
+      g.slices = p.slices_x;
+      if ((e = product_out(g, dX, at<float>(ws, p.dx), is_bf16, wait_ns, s, "xent_dX")) != cudaSuccess) return e;
+      continue;
+    }
+    // Several pieces: the first one's slices are stored, the later ones' added.
+    const int64_t rows = slice_rows(T);
+    const int slices = xent_slices(static_cast<int>(vp), p.slices_x);
+    if (!make_output_map_f32(&g.map_out[0], at<float>(ws, p.dx), rows * p.slices_x, D, D)) return cudaErrorInvalidValue;
+    g.slices = slices;
+    g.dmax = nullptr;
+    g.epi = kXentOutF32;
+    g.add = v0 > 0;
+    g.slice_rows = rows;
+    XENT_STEP("xent_dX", s, launch_xent_gemm(g, wait_ns, s));
+    if (v0 + vc < V) continue;
+    const int64_t n4 = T * D / 4, stride4 = rows * D / 4;
+    const float4* part = at<float4>(ws, p.dx);
+    if (is_bf16)
+      XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<__nv_bfloat16>, dim3(grid_for(n4)), dim3(256), 0, s, part,
+                                             p.slices_x, stride4, n4, static_cast<const float*>(dmax),
+                                             static_cast<__nv_bfloat16*>(dX)));
+    else
+      XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s, part,
+                                             p.slices_x, stride4, n4, static_cast<const float*>(dmax),
+                                             static_cast<float*>(dX)));
+  }
+  return cudaSuccess;
+}
+
+}  // namespace tpmlp

@@ -1,0 +1,579 @@
+// xent_gemm.cu — the tensor-core products of the cross entropy over the
+// vocabulary: logits tiles that never leave the chip, and the products that
+// turn their gradient into dX and dW.
+//
+// A CTA pair (cta_group::2) computes 256 x 256 tiles, three 64 KB stages of
+// two 64-deep K blocks filled by TMA, fp32 accumulators in tensor memory (two,
+// so that one tile's epilogue runs under the next one's products):
+//   every CTA, warp 0 lane 0 : TMA producer of its own 128 + 128 operand rows
+//   even CTA, warp 1 lane 0  : issues the pair's MMAs
+//   every CTA, warps 2..9    : epilogue, two warps per tensor-memory lane
+//                              quarter, each 32 rows x 128 columns
+// The logits' epilogues take one exponential per element, 256 x 256 / 2 a CTA
+// at 16 a clock: 2048 clocks a tile, which four warps could not hide under
+// the 6144 clocks of a K = 768 tile's products once the loads from tensor
+// memory, the conversions and the stores are added; eight can.
+//
+// Waits are bounded; on a timeout the roles of both CTAs leave their loops,
+// copies and MMAs in flight are drained and tensor memory is freed.
+#include "gemm_common.cuh"
+#include "train.h"
+
+#include <atomic>
+#include <cstring>
+
+namespace tpmlp {
+
+namespace {
+
+constexpr int kXThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kEpiWarps = 8;
+constexpr int kSub = 2;         // K blocks of a stage
+constexpr uint32_t kSubBytes = 128 * BK * 2;
+constexpr uint32_t kOutBlock = 32 * 128;  // staging: 32 rows of 128 bytes
+constexpr int BN = 256;
+
+template <int EPI>
+struct Cfg {
+  // Staging blocks of an epilogue warp. The three planes of kXentGradF32 need
+  // 96 KB in all and leave room for two stages.
+  static constexpr int kOutBlocks = EPI == kXentStats ? 0 : EPI == kXentGradF32 ? 3 : 1;
+  static constexpr int STAGES = EPI == kXentGradF32 ? 2 : 3;
+  static constexpr uint32_t A_BYTES = kSub * kSubBytes;
+  static constexpr uint32_t STAGE_BYTES = 2 * A_BYTES;
+  static constexpr uint32_t STAGING = kEpiWarps * kOutBlocks * kOutBlock;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + STAGING + 256;
+};
+
+struct XParams {
+  XentGemm g;
+  int k_blocks, kb_per_slice, slices;
+  int m_blocks, n_blocks, tiles;
+  uint64_t wait_ns;
+  int* status;
+};
+
+// The plane pairs in the order in which they are added: small terms first, so
+// that they are not lost against the large ones. Plane 0 is the high one.
+__device__ __forceinline__ void plane_pair(int pairs, int i, int& a, int& b) {
+  if (pairs == 1) {
+    a = b = 0;
+    return;
+  }
+  // (1,1) (0,2) (2,0) (0,1) (1,0) (0,0)
+  constexpr uint32_t kA = 1u | 0u << 4 | 2u << 8 | 0u << 12 | 1u << 16 | 0u << 20;
+  constexpr uint32_t kB = 1u | 2u << 4 | 0u << 8 | 1u << 12 | 0u << 16 | 0u << 20;
+  a = (kA >> (4 * i)) & 15;
+  b = (kB >> (4 * i)) & 15;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+// The largest |dloss| of the rows that count, from its parts (whole warp).
+__device__ __forceinline__ float warp_dmax(const float* parts, int lane) {
+  float m = 0.f;
+  for (int i = lane; i < kXentDmaxParts; i += 32) m = fmaxf(m, parts[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
+  using C = Cfg<EPI>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
+  uint8_t* s_out = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_out + C::STAGING);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t pos = rank & 1u;
+  const int cluster = static_cast<int>(cluster_id_x());
+  const int nclusters = static_cast<int>(cluster_count_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full + s, 1);   // even CTA: its producer's arrival (and the pair's bytes)
+      mbar_init(empty + s, 1);  // the pair's commit once its MMAs have read the stage
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 2 * kEpiWarps);  // even CTA: one arrival per epilogue warp of the pair
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before_sync();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  const WaitGuard guard{abort_flag, p.wait_ns, p.status};
+  const uint32_t abort_addr = smem_addr(const_cast<int*>(abort_flag));
+  auto raise_abort_in_cluster = [&]() { st_cluster_u32(map_to_cta(abort_addr, rank ^ 1u), 1u); };
+  const TileGrid grid{0, kSharedNone, p.slices, p.m_blocks, p.n_blocks, p.g.group_m};
+  // First K block of a slice and their number.
+  auto k_first = [&](int slice) { return slice * p.kb_per_slice; };
+  auto k_count = [&](int slice) { return min(p.kb_per_slice, p.k_blocks - slice * p.kb_per_slice); };
+  bool aborted = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t armed = 0, parity_bits = 0;
+      const uint64_t pol = l2_policy(1);
+      const int mn = p.g.mn_major;
+      for (int tile = cluster; !aborted && tile < p.tiles; tile += nclusters) {
+        int slice, mb, nb;
+        decode_tile(grid, tile, slice, mb, nb);
+        if (!tile_ok(grid, p.status, slice, mb, nb)) continue;
+        const int m0 = mb * 256 + static_cast<int>(pos) * 128;
+        const int n0 = nb * BN + static_cast<int>(pos) * 128;
+        const int kbs = k_count(slice), k0 = k_first(slice);
+        const int total = p.g.pairs * kbs;
+        int pair = 0, kk = 0, a, b;
+        plane_pair(p.g.pairs, 0, a, b);
+        for (int q = 0; q < total; q += kSub) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, guard, kSiteProducer)) {
+            aborted = true;
+            break;
+          }
+          const uint32_t full_lead = map_to_cta(smem_addr(full + stage), 0);
+          const int nsub = total - q < kSub ? total - q : kSub;
+          if (pos == 0) {
+            mbar_arrive_expect_tx(full + stage, 2 * 2 * nsub * kSubBytes);  // both CTAs' A and B
+            armed |= 1u << stage;
+            parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+          }
+          for (int u = 0; u < nsub; ++u) {
+            uint8_t* da = sA + stage * C::A_BYTES + u * kSubBytes;
+            uint8_t* db = sB + stage * C::A_BYTES + u * kSubBytes;
+            const CUtensorMap* ma = &p.g.map_a[a];
+            const CUtensorMap* mbp = &p.g.map_b[b];
+            const int kx = (k0 + kk) * BK;
+            if (mn & kMnA3d) {
+              tma_load_3d_pair_hint(da, ma, 0, kx, m0 / 64, full_lead, pol);
+            } else if (mn & kMnA) {
+              tma_load_2d_pair_hint(da, ma, m0, kx, full_lead, pol);
+              tma_load_2d_pair_hint(da + kMnChunkBytes, ma, m0 + 64, kx, full_lead, pol);
+            } else {
+              tma_load_2d_pair_hint(da, ma, kx, m0, full_lead, pol);
+            }
+            if (mn & kMnB3d) {
+              tma_load_3d_pair_hint(db, mbp, 0, kx, n0 / 64, full_lead, pol);
+            } else if (mn & kMnB) {
+              tma_load_2d_pair_hint(db, mbp, n0, kx, full_lead, pol);
+              tma_load_2d_pair_hint(db + kMnChunkBytes, mbp, n0 + 64, kx, full_lead, pol);
+            } else {
+              tma_load_2d_pair_hint(db, mbp, kx, n0, full_lead, pol);
+            }
+            if (++kk == kbs) {
+              kk = 0;
+              if (++pair < p.g.pairs) plane_pair(p.g.pairs, pair, a, b);
+            }
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (aborted) {
+        raise_abort_in_cluster();
+        if (pos == 0) {
+          for (int s = 0; s < C::STAGES; ++s)
+            if (armed >> s & 1u) wait_drain(full + s, (parity_bits >> s) & 1u, p.wait_ns);
+        } else {
+          // This CTA's copies are counted on the even CTA's barriers; give any
+          // copy still in flight time to land before shared memory is released.
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 200000ull) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && pos == 0) {
+      // ---------------- MMA issuer
+      const bool a_mn = (p.g.mn_major & kMnA) != 0, b_mn = (p.g.mn_major & kMnB) != 0;
+      const uint32_t idesc = idesc_bf16_f32(256, BN, a_mn, b_mn);
+      constexpr uint16_t kPairMask = 0x3;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int tile = cluster; !aborted && tile < p.tiles; tile += nclusters) {
+        int slice, mb, nb;
+        decode_tile(grid, tile, slice, mb, nb);
+        if (!tile_ok(grid, p.status, slice, mb, nb)) continue;
+        const int total = p.g.pairs * k_count(slice);
+        if (!wait_bounded(acc_empty + acc, acc_phase ^ 1u, guard, kSiteMmaAcc)) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int q = 0; q < total; q += kSub) {
+          if (!wait_bounded(full + stage, phase, guard, kSiteMmaFull)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after_sync();
+          const int nsub = total - q < kSub ? total - q : kSub;
+          for (int u = 0; u < nsub; ++u) {
+            const uint32_t a0 = smem_addr(sA + stage * C::A_BYTES + u * kSubBytes);
+            const uint32_t b0 = smem_addr(sB + stage * C::A_BYTES + u * kSubBytes);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              tc_mma_bf16_pair(d_tmem, operand_desc(a0, k, a_mn), operand_desc(b0, k, b_mn), idesc,
+                               (q | u | k) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_multicast(empty + stage, kPairMask);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (aborted) break;
+        tc_commit_pair_multicast(acc_full + acc, kPairMask);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (aborted) {
+        raise_abort_in_cluster();
+        tc_commit_pair_multicast(drain, static_cast<uint16_t>(1u << rank));
+        wait_drain(drain, 0, p.wait_ns);
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9 of every CTA)
+    const int quarter = warp & 3;         // its tensor-memory lane quarter: rows quarter*32 .. +31 of this CTA's 128
+    const int half = (warp - 2) >> 2;     // columns half*128 .. +127 of the tile
+    uint8_t* stage_out = s_out + (warp - 2) * C::kOutBlocks * kOutBlock;
+    const uint32_t acc_empty_lead = map_to_cta(smem_addr(acc_empty), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    float scale = 1.f, inv_dmax = 0.f;  // kXentOut*: dmax; kXentGrad*: 1 / dmax
+    if constexpr (EPI == kXentOutBf16 || EPI == kXentOutF32) {
+      if (p.g.dmax) scale = warp_dmax(p.g.dmax, lane);
+    }
+    if constexpr (EPI == kXentGrad || EPI == kXentGradF32) {
+      const float d = warp_dmax(p.g.dmax, lane);
+      inv_dmax = d > 0.f ? 1.f / d : 0.f;
+    }
+    for (int tile = cluster; tile < p.tiles; tile += nclusters) {
+      int slice, mb, nb;
+      decode_tile(grid, tile, slice, mb, nb);
+      if (!tile_ok(grid, p.status, slice, mb, nb)) continue;
+      const int64_t m_warp = int64_t(mb) * 256 + int64_t(pos) * 128 + quarter * 32;
+      const int64_t m = m_warp + lane;
+      const bool row_ok = m < p.g.M;
+      const int nh = nb * BN + half * 128;  // first column of this warp
+      // Rows' own values, loaded while the products run.
+      int64_t hot = -1;  // the target's column, or none
+      float lse2 = 0.f, rs = 0.f;
+      if constexpr (EPI == kXentStats || EPI == kXentGrad || EPI == kXentGradF32) {
+        if (row_ok) {
+          const int64_t t = p.g.targets[m];
+          const bool counts = t >= 0 && t < p.g.V;
+          hot = counts ? t - p.g.col0 : -1;
+          if constexpr (EPI != kXentStats) {
+            lse2 = p.g.lse[m] * kLog2e;
+            rs = counts ? p.g.dloss[m] * inv_dmax : 0.f;
+          }
+        }
+      }
+      bool ok = wait_bounded(acc_full + acc, acc_phase, guard, kSiteEpilogue);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) raise_abort_in_cluster();
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t t_row =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN + half * 128);
+      const bool work = m_warp < p.g.M && nh < p.g.N;  // warp-uniform
+      float run_max = -INFINITY, run_sum = 0.f;  // kXentStats, in units of log2
+      // Columns n0 .. n0+31 of this thread's row.
+      auto finish = [&](int c, const uint32_t (&r)[32]) {
+        const int n0 = nh + c;
+        if (!work || n0 >= p.g.N) return;  // warp-uniform
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if constexpr (EPI == kXentStats) {
+          const int64_t h = hot - n0;
+          if (h >= 0 && h < 32) {
+            float z = v[0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) z = h == i ? v[i] : z;
+            p.g.zt[m] = z;
+          }
+          if (n0 + 32 > p.g.N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i >= p.g.N) v[i] = -INFINITY;
+          }
+          // Maximum, then the sum of the chunk's exponentials; the running sum
+          // is rescaled once per chunk.
+          float mx = v[0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx = fmaxf(mx, v[i]);
+          const float top = fmaxf(run_max, mx * kLog2e);
+          const float base = top == -INFINITY ? 0.f : top;  // a row of -inf so far: every term is 0, not NaN
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            s0 += exp2_approx(fmaf(v[i], kLog2e, -base));
+            s1 += exp2_approx(fmaf(v[i + 1], kLog2e, -base));
+          }
+          run_sum = fmaf(run_sum, exp2_approx(run_max - base), s0 + s1);
+          run_max = top;
+        } else if constexpr (EPI == kXentGrad || EPI == kXentGradF32) {
+          // dz = rs (softmax - [target]), rs = dloss / max |dloss|: exactly 0 in rows that do not count and past N.
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(v[i], kLog2e, -lse2));
+          const int64_t h = hot - n0;
+          if (h >= 0 && h < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = h == i ? v[i] - 1.f : v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = rs != 0.f ? v[i] * rs : 0.f;
+          if (n0 + 32 > p.g.N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i >= p.g.N) v[i] = 0.f;
+          }
+          const int hb = (c >> 5) & 1;  // half of the 64-column block
+          if (hb == 0) {
+            if (lane == 0) bulk_wait_group_read<0>();  // the staging blocks' previous stores have read them
+            __syncwarp();
+          }
+#pragma unroll
+          for (int pl = 0; pl < C::kOutBlocks; ++pl) {
+            uint8_t* buf = stage_out + pl * kOutBlock;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * hb + j) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+            if (pl + 1 < C::kOutBlocks) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+            }
+          }
+          // The block is stored when its second half is in, or when there is none.
+          if (hb == 1 || n0 + 32 >= p.g.N) {
+            if (hb == 0) {
+#pragma unroll
+              for (int pl = 0; pl < C::kOutBlocks; ++pl)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  *reinterpret_cast<uint4*>(stage_out + pl * kOutBlock + lane * 128 + (((4 + j) ^ (lane & 7)) << 4)) =
+                      make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+              for (int pl = 0; pl < C::kOutBlocks; ++pl)
+                tma_store_2d(&p.g.map_out[pl], stage_out + pl * kOutBlock, n0 - 32 * hb, static_cast<int32_t>(m_warp));
+              bulk_commit_group();
+            }
+          }
+        } else if constexpr (EPI == kXentOutBf16) {
+          const int hb = (c >> 5) & 1;
+          if (hb == 0) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= scale;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(stage_out + lane * 128 + (((4 * hb + j) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          if (hb == 1 || n0 + 32 >= p.g.N) {  // columns past N are clipped by the store
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&p.g.map_out[0], stage_out, n0 - 32 * hb, static_cast<int32_t>(m_warp));
+              bulk_commit_group();
+            }
+          }
+        } else {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(stage_out + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(__float_as_uint(v[4 * j] * scale), __float_as_uint(v[4 * j + 1] * scale),
+                           __float_as_uint(v[4 * j + 2] * scale), __float_as_uint(v[4 * j + 3] * scale));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int32_t row = static_cast<int32_t>(m_warp + slice * p.g.slice_rows);
+            if (p.g.add)
+              tma_reduce_add_2d(&p.g.map_out[0], stage_out, n0, row);
+            else
+              tma_store_2d(&p.g.map_out[0], stage_out, n0, row);
+            bulk_commit_group();
+          }
+        }
+      };
+      uint32_t ra[32], rb[32];
+      __syncwarp();
+      tmem_ld_32cols_issue(t_row, ra);
+      tmem_ld_wait(ra);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        __syncwarp();
+        tmem_ld_32cols_issue(t_row + static_cast<uint32_t>(c + 32), rb);
+        finish(c, ra);
+        __syncwarp();
+        tmem_ld_wait(rb);
+        if (c + 64 == 128) {
+          // This warp's columns are in registers: hand them back to the MMA issuer.
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_lead + 8u * static_cast<uint32_t>(acc));
+        } else {
+          tmem_ld_32cols_issue(t_row + static_cast<uint32_t>(c + 64), ra);
+        }
+        finish(c + 32, rb);
+        if (c + 64 < 128) {
+          __syncwarp();
+          tmem_ld_wait(ra);
+        }
+      }
+      if constexpr (EPI == kXentStats) {
+        if (work && row_ok) p.g.stats[int64_t(nh / kXentPart) * p.g.M + m] = make_float2(run_max, run_sum);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if constexpr (EPI != kXentStats) {
+      if (lane == 0) bulk_wait_group_all();
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int EPI>
+cudaError_t launch_epi(const XParams& p, cudaStream_t s) {
+  using C = Cfg<EPI>;
+  auto kern = xent_gemm_kernel<EPI>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kXThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  static std::atomic<int> max_clusters[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  int cached = max_clusters[dev].load(std::memory_order_relaxed);
+  if (!cached) {
+    cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
+    int n = 0;
+    cfg.numAttrs = 1;  // the query takes the cluster shape only
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    cfg.numAttrs = 2;
+    if (e != cudaSuccess) return e;
+    cached = n > 0 ? n : 1;
+    max_clusters[dev].store(cached, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3(2 * (p.tiles < cached ? p.tiles : cached), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+int xent_slices(int K, int slices) {
+  const int kb = (K + BK - 1) / BK;
+  const int per = (kb + slices - 1) / slices;
+  return (kb + per - 1) / per;
+}
+
+cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s) {
+  XParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = g;
+  p.k_blocks = (g.K + BK - 1) / BK;
+  p.kb_per_slice = (p.k_blocks + g.slices - 1) / g.slices;
+  p.slices = (p.k_blocks + p.kb_per_slice - 1) / p.kb_per_slice;
+  p.m_blocks = (g.M + 255) / 256;
+  p.n_blocks = (g.N + BN - 1) / BN;
+  const int64_t tiles = int64_t(p.m_blocks) * p.n_blocks * p.slices;
+  if (tiles <= 0 || tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  p.tiles = static_cast<int>(tiles);
+  p.wait_ns = wait_ns;
+  p.status = device_status_word();
+  if (!p.status) return cudaErrorInvalidSymbol;
+  switch (g.epi) {
+    case kXentStats:
+      return launch_epi<kXentStats>(p, s);
+    case kXentGrad:
+      return launch_epi<kXentGrad>(p, s);
+    case kXentGradF32:
+      return launch_epi<kXentGradF32>(p, s);
+    case kXentOutBf16:
+      return launch_epi<kXentOutBf16>(p, s);
+    case kXentOutF32:
+      return launch_epi<kXentOutF32>(p, s);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tpmlp
