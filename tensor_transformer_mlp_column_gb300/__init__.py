@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional, Sequence
 
 import torch
@@ -90,9 +91,8 @@ SIGNATURES = {
     "tpmlp_embed_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "tpmlp_embed_backward": (_I, [_P, _I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
     "tpmlp_grad_workspace_bytes": (_SZ, [_I]),
-    "tpmlp_grad_norm": (_I, [ctypes.POINTER(_P), ctypes.POINTER(_I64), ctypes.POINTER(_I), _I, _P, _P, _SZ, _P]),
-    "tpmlp_grad_clip": (_I, [ctypes.POINTER(_P), ctypes.POINTER(_I64), ctypes.POINTER(_I), _I, ctypes.c_float,
-                             ctypes.POINTER(_P), _P, _P, _SZ, _P]),
+    "tpmlp_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _SZ, _P]),
+    "tpmlp_grad_clip": (_I, [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "tpmlp_trace_read": (_I, [ctypes.c_char_p, _SZ, ctypes.POINTER(_I)]),
     "tpmlp_trace_enabled": (_I, []),
     "tpmlp_build_flags": (_I, []),
@@ -537,44 +537,76 @@ def tpmlp_attn_forward(X: torch.Tensor, batch: int, shards: AttnShards, mode="fa
 
 # ------------------------------------------------- the two ends of a training step
 
-def _here(*tensors) -> torch.device:
-    """The current device, which every tensor of a call must be on."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if t.device.index != cur:
-            raise ValueError(f"a tensor is on {t.device}, but device {cur} is current")
-    return tensors[0].device if tensors else torch.device("cuda", cur)
+# These calls may be a few microseconds of GPU work (one token's lookup, one
+# small layer's clipping), so the binding keeps its own part short: one pass
+# over the tensors, the raw stream, no array objects built element by element.
+
+_DTYPES = {torch.float32: TPMLP_F32, torch.bfloat16: TPMLP_BF16}
 
 
-def _ids(t: torch.Tensor, T: int, name: str) -> int:
+def _ptr(t: torch.Tensor, dev: int, name: str) -> int:
+    """Address of a contiguous tensor on device `dev`, the current one."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but CUDA device {dev} is current")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _type(t: torch.Tensor) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; use torch.float32 or torch.bfloat16")
+    return dt
+
+
+def _ids(t: torch.Tensor, T: int, dev: int, name: str) -> int:
     if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] != T:
         raise ValueError(f"{name} must be an int64 tensor of {T} ids")
-    return _dev(t, name)
+    return _ptr(t, dev, name)
 
 
-def _like(t: torch.Tensor, shape, dtype: torch.dtype, name: str) -> int:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+def _like(t: torch.Tensor, shape, dtype: torch.dtype, dev: int, name: str) -> int:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return _dev(t, name)
+    return _ptr(t, dev, name)
+
+
+def _space(nbytes: int, workspace: Optional[torch.Tensor], dev: int):
+    """(tensor, address, bytes) of a call's workspace."""
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+        return workspace, workspace.data_ptr(), workspace.numel()
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
+        raise ValueError(f"workspace too small: need {nbytes} bytes")
+    return workspace, _ptr(workspace, dev, "workspace"), have
 
 
 class _On:
-    """Allocates a call's outputs and workspace on the call's stream, so that the
-    caching allocator does not hand their memory to another stream's work
-    while the call may still use it."""
+    """A call's device and stream. Outputs and workspace are allocated with the
+    call's stream current, so that the caching allocator does not hand their
+    memory to another stream's work while the call may still use it."""
+
+    __slots__ = ("dev", "raw", "ctx")
 
     def __init__(self, stream):
         self.ctx = None
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        self.dev = torch._C._cuda_getDevice()
+        self.raw = torch._C._cuda_getCurrentRawStream(self.dev)
         if stream is not None:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-            if s != torch.cuda.current_stream():
+            raw = _stream(stream)
+            if raw != self.raw:
+                self.raw = raw
+                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
                 self.ctx = torch.cuda.stream(s)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
+        return self
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -597,16 +629,15 @@ def tpmlp_xent_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
     """Cross entropy of softmax(X W^T) at the targets without keeping the logits:
     (loss [T], lse [T]) fp32. A negative target's row has no loss."""
     T, D, V = _xent_shapes(X, W)
-    dev = _here(X, W, targets)
-    dt = _dt(X)
-    with _On(stream):
-        loss = torch.empty(T, dtype=torch.float32, device=dev) if loss is None else loss
-        lse = torch.empty(T, dtype=torch.float32, device=dev) if lse is None else lse
-        ws = _workspace(int(lib().tpmlp_xent_workspace_bytes(T, D, V, dt, 0)), workspace)
-        _check(lib().tpmlp_xent_forward(_dev(X, "X"), _dev(W, "W"), _ids(targets, T, "targets"), T, D, V, dt,
-                                        _like(loss, (T,), torch.float32, "loss"),
-                                        _like(lse, (T,), torch.float32, "lse"), ws.data_ptr(),
-                                        ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_xent_forward")
+    dt, l = _type(X), lib()
+    with _On(stream) as on:
+        dev = on.dev
+        x, w, t = _ptr(X, dev, "X"), _ptr(W, dev, "W"), _ids(targets, T, dev, "targets")
+        loss = torch.empty(T, dtype=torch.float32, device="cuda") if loss is None else loss
+        lse = torch.empty(T, dtype=torch.float32, device="cuda") if lse is None else lse
+        ws, wp, wn = _space(l.tpmlp_xent_workspace_bytes(T, D, V, dt, 0), workspace, dev)
+        _check(l.tpmlp_xent_forward(x, w, t, T, D, V, dt, _like(loss, (T,), torch.float32, dev, "loss"),
+                                    _like(lse, (T,), torch.float32, dev, "lse"), wp, wn, on.raw), "tpmlp_xent_forward")
     return loss, lse
 
 
@@ -615,18 +646,17 @@ def tpmlp_xent_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of sum(dloss * loss) of tpmlp_xent_forward: (dX [T, D], dW [V, D]) of X's dtype."""
     T, D, V = _xent_shapes(X, W)
-    dev = _here(X, W, targets, lse, dloss)
-    dt = _dt(X)
-    with _On(stream):
-        dX = torch.empty((T, D), dtype=X.dtype, device=dev) if dX is None else dX
-        dW = torch.empty((V, D), dtype=X.dtype, device=dev) if dW is None else dW
-        ws = _workspace(int(lib().tpmlp_xent_workspace_bytes(T, D, V, dt, 1)), workspace)
-        _check(lib().tpmlp_xent_backward(_dev(X, "X"), _dev(W, "W"), _ids(targets, T, "targets"),
-                                         _like(lse, (T,), torch.float32, "lse"),
-                                         _like(dloss, (T,), torch.float32, "dloss"), T, D, V, dt,
-                                         _like(dX, (T, D), X.dtype, "dX"), _like(dW, (V, D), X.dtype, "dW"),
-                                         ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
-               "tpmlp_xent_backward")
+    dt, l = _type(X), lib()
+    with _On(stream) as on:
+        dev = on.dev
+        x, w, t = _ptr(X, dev, "X"), _ptr(W, dev, "W"), _ids(targets, T, dev, "targets")
+        dX = torch.empty((T, D), dtype=X.dtype, device="cuda") if dX is None else dX
+        dW = torch.empty((V, D), dtype=X.dtype, device="cuda") if dW is None else dW
+        ws, wp, wn = _space(l.tpmlp_xent_workspace_bytes(T, D, V, dt, 1), workspace, dev)
+        _check(l.tpmlp_xent_backward(x, w, t, _like(lse, (T,), torch.float32, dev, "lse"),
+                                     _like(dloss, (T,), torch.float32, dev, "dloss"), T, D, V, dt,
+                                     _like(dX, (T, D), X.dtype, dev, "dX"), _like(dW, (V, D), X.dtype, dev, "dW"),
+                                     wp, wn, on.raw), "tpmlp_xent_backward")
     return dX, dW
 
 
@@ -634,12 +664,16 @@ def tpmlp_embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, 
                         stream=None) -> torch.Tensor:
     """out[t] = scale * E[ids[t]], of E's dtype; zero rows for negative ids."""
     V, D = E.shape
-    T = ids.shape[0]
-    dev = _here(E, ids)
-    with _On(stream):
-        out = torch.empty((T, D), dtype=E.dtype, device=dev) if out is None else out
-        _check(lib().tpmlp_embed_forward(_dev(E, "E"), _ids(ids, T, "ids"), T, D, V, _dt(E), float(scale),
-                                         _like(out, (T, D), E.dtype, "out"), _stream(stream)), "tpmlp_embed_forward")
+    T, dt = ids.shape[0], _type(E)
+    with _On(stream) as on:
+        dev = on.dev
+        e, i = _ptr(E, dev, "E"), _ids(ids, T, dev, "ids")
+        if out is None:
+            out = torch.empty((T, D), dtype=E.dtype, device="cuda")
+            o = out.data_ptr()
+        else:
+            o = _like(out, (T, D), E.dtype, dev, "out")
+        _check(lib().tpmlp_embed_forward(e, i, T, D, V, dt, scale, o, on.raw), "tpmlp_embed_forward")
     return out
 
 
@@ -654,20 +688,20 @@ def tpmlp_embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: f
     """dE[v] = scale * sum of dout[t] over ids[t] = v, [V, D] of `dtype` (default
     dout's); with accumulate, added to the given dE."""
     T, D = dout.shape
-    dev = _here(dout, ids)
     if accumulate and dE is None:
         raise ValueError("accumulate needs dE")
     if dE is None:
         dtype = dout.dtype if dtype is None else dtype
     elif dtype is not None and dtype != dE.dtype:
         raise ValueError("dtype and dE disagree")
-    with _On(stream):
-        dE = torch.empty((V, D), dtype=dtype, device=dev) if dE is None else dE
-        ws = _workspace(tpmlp_embed_workspace_bytes(T, D, V), workspace)
-        _check(lib().tpmlp_embed_backward(_dev(dout, "dout"), _dt(dout), _ids(ids, T, "ids"), T, D, V, float(scale),
-                                          _like(dE, (V, D), dE.dtype, "dE"), _dt(dE), int(bool(accumulate)),
-                                          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
-               "tpmlp_embed_backward")
+    l = lib()
+    with _On(stream) as on:
+        dev = on.dev
+        g, i = _ptr(dout, dev, "dout"), _ids(ids, T, dev, "ids")
+        dE = torch.empty((V, D), dtype=dtype, device="cuda") if dE is None else dE
+        ws, wp, wn = _space(l.tpmlp_embed_workspace_bytes(T, D, V), workspace, dev)
+        _check(l.tpmlp_embed_backward(g, _type(dout), i, T, D, V, scale, _like(dE, (V, D), dE.dtype, dev, "dE"),
+                                      _type(dE), 1 if accumulate else 0, wp, wn, on.raw), "tpmlp_embed_backward")
     return dE
 
 
@@ -675,22 +709,32 @@ def tpmlp_grad_workspace_bytes(n: int) -> int:
     return int(lib().tpmlp_grad_workspace_bytes(n))
 
 
-def _grads(grads: Sequence[torch.Tensor]):
-    n = len(grads)
-    return ((ctypes.c_void_p * n)(*[_dev(g, "a gradient") for g in grads]),
-            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int * n)(*[_dt(g) for g in grads]), n)
+def _addresses(ts: Sequence[torch.Tensor], dev: int, name: str) -> array:
+    for t in ts:
+        if t.get_device() != dev or not t.is_contiguous():
+            _ptr(t, dev, name)  # says what is wrong
+    return array("Q", [t.data_ptr() for t in ts])
+
+
+def _grads(grads: Sequence[torch.Tensor], dev: int):
+    """Addresses, element counts and types of the gradients, as arrays."""
+    try:
+        types = array("i", [_DTYPES[g.dtype] for g in grads])
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e}; use torch.float32 or torch.bfloat16") from None
+    return _addresses(grads, dev, "a gradient"), array("q", [g.numel() for g in grads]), types
 
 
 def tpmlp_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None,
                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The global norm of all gradients (fp32 and bf16 tensors mixed): [1] fp32."""
-    dev = _here(*grads)
-    with _On(stream):
-        norm = torch.empty(1, dtype=torch.float32, device=dev) if norm is None else norm
-        p, c, d, n = _grads(grads)
-        ws = _workspace(tpmlp_grad_workspace_bytes(n), workspace)
-        _check(lib().tpmlp_grad_norm(p, c, d, n, _like(norm, (1,), torch.float32, "norm"), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_grad_norm")
+    n, l = len(grads), lib()
+    with _On(stream) as on:
+        p, c, d = _grads(grads, on.dev)
+        norm = torch.empty(1, dtype=torch.float32, device="cuda") if norm is None else norm
+        ws, wp, wn = _space(l.tpmlp_grad_workspace_bytes(n), workspace, on.dev)
+        _check(l.tpmlp_grad_norm(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n,
+                                 _like(norm, (1,), torch.float32, on.dev, "norm"), wp, wn, on.raw), "tpmlp_grad_norm")
     return norm
 
 
@@ -699,21 +743,19 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
                     stream=None) -> torch.Tensor:
     """Scales all gradients by min(1, max_norm / (norm + 1e-6)), in place or into
     `out`, and returns their global norm before that: [1] fp32."""
-    dev = _here(*grads)
-    if out is not None:
-        if len(out) != len(grads):
-            raise ValueError("out must have one tensor for each gradient")
-        _here(*out)
-        for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.shape != g.shape:
-                raise ValueError("out must have the gradients' shapes and dtypes")
-    with _On(stream):
-        norm = torch.empty(1, dtype=torch.float32, device=dev) if norm is None else norm
-        p, c, d, n = _grads(grads)
-        ws = _workspace(tpmlp_grad_workspace_bytes(n), workspace)
-        _check(lib().tpmlp_grad_clip(p, c, d, n, float(max_norm), None if out is None else _ptrs(out, "out"),
-                                     _like(norm, (1,), torch.float32, "norm"), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), _stream(stream)), "tpmlp_grad_clip")
+    n, l = len(grads), lib()
+    with _On(stream) as on:
+        p, c, d = _grads(grads, on.dev)
+        o = None
+        if out is not None:
+            if len(out) != n or [t.numel() for t in out] != c.tolist() or [t.dtype for t in out] != [g.dtype for g in grads]:
+                raise ValueError("out must have a tensor of each gradient's size and dtype")
+            o = _addresses(out, on.dev, "an output")
+        norm = torch.empty(1, dtype=torch.float32, device="cuda") if norm is None else norm
+        ws, wp, wn = _space(l.tpmlp_grad_workspace_bytes(n), workspace, on.dev)
+        _check(l.tpmlp_grad_clip(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, max_norm,
+                                 None if o is None else o.buffer_info()[0],
+                                 _like(norm, (1,), torch.float32, on.dev, "norm"), wp, wn, on.raw), "tpmlp_grad_clip")
     return norm
 
 

@@ -79,6 +79,7 @@ enum XentEpilogue : int {
   kXentOutBf16 = 3,  // out bf16 = scale * acc
   kXentOutF32 = 4,   // out fp32 = scale * acc, or (add) out += acc
 };
+constexpr float kXentLog2e = 1.4426950408889634f;
 constexpr int kXentPlanes = 3;
 constexpr int kXentPairs = 6;
 constexpr int kXentPart = 128;    // columns of one (max, sum) part

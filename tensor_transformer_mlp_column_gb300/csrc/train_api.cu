@@ -5,6 +5,7 @@
 #include "tpmlp.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <new>
@@ -33,15 +34,19 @@ uint64_t wait_ns() {
   return static_cast<uint64_t>(ms) * 1000000ull;
 }
 
+// The current device is a GB300 (asked once per device) whose status word is known.
 int current_sm103() {
+  static std::atomic<bool> seen[64] = {};
   int dev = -1, major = 0, minor = 0;
   TRAIN_TRY(cudaGetDevice(&dev));
+  if (dev >= 0 && dev < 64 && seen[dev].load(std::memory_order_relaxed)) return TPMLP_OK;
   TRAIN_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
   TRAIN_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
   if (major != 10 || minor != 3)
     return set_error(TPMLP_ERR_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a (GB300)", dev, major,
                      minor);
   if (!device_status_word()) return set_error(TPMLP_ERR_CUDA, "the device status word is not available");
+  if (dev >= 0 && dev < 64) seen[dev].store(true, std::memory_order_relaxed);
   return TPMLP_OK;
 }
 

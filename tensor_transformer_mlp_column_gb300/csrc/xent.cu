@@ -39,11 +39,13 @@ namespace {
     if (e_ != cudaSuccess) return e_;      \
   } while (0)
 
-constexpr float kLn2 = 0.6931471805599453f;
-
-// Row t's parts joined: lse = ln 2 (M + log2 sum_i s_i 2^(m_i - M)). A CTA
-// takes 32 rows, warp w the parts w, w + 8, ..., joined in the warps' order.
-constexpr int kJoinWarps = 8;
+// Row t's parts joined: lse = (M + log2 sum_i s_i 2^(m_i - M)) / log2 e. A CTA
+// takes 32 rows, warp w the parts w, w + 16, ..., joined in the warps' order.
+// The last additions are in fp64: M is in units of log2, where a rounding to
+// fp32 weighs more than in lse, and a target that is nearly certain leaves a
+// loss far below lse, which the fp32 difference would lose. log2 e is the same
+// fp32 constant that scaled the logits.
+constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2* __restrict__ stats, int parts, int64_t T,
                                                                     const int64_t* __restrict__ targets, int64_t V,
                                                                     const float* __restrict__ zt, float* __restrict__ loss,
@@ -60,19 +62,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
     s = s * exp2f(m - base) + p.y * exp2f(p.x - base);
     m = top;
   };
+  const int64_t target = t < T && w == 0 ? targets[t] : -1;
+  const float z = target >= 0 && target < V ? zt[t] : 0.f;
   if (t < T) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = w; i < parts; i += kJoinWarps) add(stats[int64_t(i) * T + t]);
   }
   red[w][l] = make_float2(m, s);
   __syncthreads();
   if (w != 0 || t >= T) return;
   for (int i = 1; i < kJoinWarps; ++i) add(red[i][l]);
-  const float v = kLn2 * (m + log2f(s));
-  const int64_t target = targets[t];
+  const double v = (double(m) + double(log2f(s))) * (1.0 / double(kXentLog2e));
   if (target >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkTarget);
-  lse[t] = v;
-  loss[t] = target >= 0 && target < V ? v - zt[t] : 0.f;
+  lse[t] = static_cast<float>(v);
+  loss[t] = target >= 0 && target < V ? static_cast<float>(v - double(z)) : 0.f;
 }
 
 // parts[b] = the largest |dloss| among CTA b's rows that count.

@@ -7,12 +7,26 @@
 // so that one tile's epilogue runs under the next one's products):
 //   every CTA, warp 0 lane 0 : TMA producer of its own 128 + 128 operand rows
 //   even CTA, warp 1 lane 0  : issues the pair's MMAs
-//   every CTA, warps 2..9    : epilogue, two warps per tensor-memory lane
+//   every CTA, warps 4..11   : epilogue, two warps per tensor-memory lane
 //                              quarter, each 32 rows x 128 columns
 // The logits' epilogues take one exponential per element, 256 x 256 / 2 a CTA
 // at 16 a clock: 2048 clocks a tile, which four warps could not hide under
 // the 6144 clocks of a K = 768 tile's products once the loads from tensor
 // memory, the conversions and the stores are added; eight can.
+//
+// The tensor core cuts off what an addition to its fp32 accumulator shifts
+// out, always towards zero, so the error of a long sum grows with its length
+// (measured on the loss, one sum: 8.8e-7 at D = 1024, 1.7e-6 at 2056, 4.1e-6
+// at 3496, against 3e-7 to 4e-7 of an fp32 product). Where an fp32 result is
+// wanted a long sum is therefore cut into runs, alternating between the two
+// accumulators, and the epilogue warps add the runs in registers with
+// rounding to nearest: 128 sums a thread, for which the epilogue's two
+// warpgroups take registers over from the first one (384 x 168 at launch =
+// 128 x 56 + 256 x 224). A run read back keeps the tensor core from its
+// accumulators, about 500 clocks when the warps read all of it at once; spread
+// over the next run it costs a third of that (T = 8192, D = 4096, V = 128000:
+// one sum 4.71 ms, runs of 512 5.30 ms at once and 5.09 ms spread, runs of
+// 1024 4.84 ms spread).
 //
 // Waits are bounded; on a timeout the roles of both CTAs leave their loops,
 // copies and MMAs in flight are drained and tensor memory is freed.
@@ -26,14 +40,19 @@ namespace tpmlp {
 
 namespace {
 
-constexpr int kXThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kXThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 2, 3 idle, warps 4..11 epilogue
+constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kSub = 2;         // K blocks of a stage
 constexpr uint32_t kSubBytes = 128 * BK * 2;
 constexpr uint32_t kOutBlock = 32 * 128;  // staging: 32 rows of 128 bytes
 constexpr int BN = 256;
+// K blocks of a run, at most: sums of up to 1024 products of bf16 data; 512 of
+// fp32 data's planes, where the products are closer to what is wanted.
+constexpr int kRunBf16 = 16, kRunF32 = 8;
+constexpr int kDrainPauseNs = 25;  // per K block of a run, between a warp's reads of it
 
-template <int EPI>
+template <int EPI, bool RUNS>
 struct Cfg {
   // Staging blocks of an epilogue warp. The three planes of kXentGradF32 need
   // 96 KB in all and leave room for two stages.
@@ -49,6 +68,7 @@ struct XParams {
   XentGemm g;
   int k_blocks, kb_per_slice, slices;
   int m_blocks, n_blocks, tiles;
+  int run;  // RUNS: K blocks of a run, even
   uint64_t wait_ns;
   int* status;
 };
@@ -72,7 +92,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = kXentLog2e;
 
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -90,9 +110,10 @@ __device__ __forceinline__ float warp_dmax(const float* parts, int lane) {
   return m;
 }
 
-template <int EPI>
+// RUNS: a tile's sum may have several runs; else it has one.
+template <int EPI, bool RUNS>
 __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
-  using C = Cfg<EPI>;
+  using C = Cfg<EPI, RUNS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -142,8 +163,9 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
   auto k_count = [&](int slice) { return min(p.kb_per_slice, p.k_blocks - slice * p.kb_per_slice); };
   bool aborted = false;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiWarp0) {
+    if constexpr (RUNS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
       // ---------------- TMA producer
       int stage = 0;
       uint32_t phase = 0;
@@ -219,8 +241,7 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && pos == 0) {
+    if (warp == 1 && lane == 0 && pos == 0) {
       // ---------------- MMA issuer
       const bool a_mn = (p.g.mn_major & kMnA) != 0, b_mn = (p.g.mn_major & kMnB) != 0;
       const uint32_t idesc = idesc_bf16_f32(256, BN, a_mn, b_mn);
@@ -234,38 +255,41 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
         decode_tile(grid, tile, slice, mb, nb);
         if (!tile_ok(grid, p.status, slice, mb, nb)) continue;
         const int total = p.g.pairs * k_count(slice);
-        if (!wait_bounded(acc_empty + acc, acc_phase ^ 1u, guard, kSiteMmaAcc)) {
-          aborted = true;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        for (int q = 0; q < total; q += kSub) {
-          if (!wait_bounded(full + stage, phase, guard, kSiteMmaFull)) {
+        for (int run = 0; !aborted && run < total; run += RUNS ? p.run : total) {
+          const int end = RUNS ? min(total, run + p.run) : total;
+          if (!wait_bounded(acc_empty + acc, acc_phase ^ 1u, guard, kSiteMmaAcc)) {
             aborted = true;
             break;
           }
           tc_fence_after_sync();
-          const int nsub = total - q < kSub ? total - q : kSub;
-          for (int u = 0; u < nsub; ++u) {
-            const uint32_t a0 = smem_addr(sA + stage * C::A_BYTES + u * kSubBytes);
-            const uint32_t b0 = smem_addr(sB + stage * C::A_BYTES + u * kSubBytes);
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+          for (int q = run; q < end; q += kSub) {
+            if (!wait_bounded(full + stage, phase, guard, kSiteMmaFull)) {
+              aborted = true;
+              break;
+            }
+            tc_fence_after_sync();
+            const int nsub = total - q < kSub ? total - q : kSub;
+            for (int u = 0; u < nsub; ++u) {
+              const uint32_t a0 = smem_addr(sA + stage * C::A_BYTES + u * kSubBytes);
+              const uint32_t b0 = smem_addr(sB + stage * C::A_BYTES + u * kSubBytes);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              tc_mma_bf16_pair(d_tmem, operand_desc(a0, k, a_mn), operand_desc(b0, k, b_mn), idesc,
-                               (q | u | k) != 0 ? 1u : 0u);
+              for (int k = 0; k < BK / 16; ++k)
+                tc_mma_bf16_pair(d_tmem, operand_desc(a0, k, a_mn), operand_desc(b0, k, b_mn), idesc,
+                                 (q != run || (u | k) != 0) ? 1u : 0u);
+            }
+            tc_commit_pair_multicast(empty + stage, kPairMask);
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          tc_commit_pair_multicast(empty + stage, kPairMask);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          if (aborted) break;
+          tc_commit_pair_multicast(acc_full + acc, kPairMask);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
           }
-        }
-        if (aborted) break;
-        tc_commit_pair_multicast(acc_full + acc, kPairMask);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
         }
       }
       if (aborted) {
@@ -275,10 +299,11 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
       }
     }
   } else {
-    // ---------------- epilogue (warps 2..9 of every CTA)
+    if constexpr (RUNS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---------------- epilogue (warps 4..11 of every CTA)
     const int quarter = warp & 3;         // its tensor-memory lane quarter: rows quarter*32 .. +31 of this CTA's 128
-    const int half = (warp - 2) >> 2;     // columns half*128 .. +127 of the tile
-    uint8_t* stage_out = s_out + (warp - 2) * C::kOutBlocks * kOutBlock;
+    const int half = (warp - kEpiWarp0) >> 2;     // columns half*128 .. +127 of the tile
+    uint8_t* stage_out = s_out + (warp - kEpiWarp0) * C::kOutBlocks * kOutBlock;
     const uint32_t acc_empty_lead = map_to_cta(smem_addr(acc_empty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -307,28 +332,18 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           const bool counts = t >= 0 && t < p.g.V;
           hot = counts ? t - p.g.col0 : -1;
           if constexpr (EPI != kXentStats) {
-            lse2 = p.g.lse[m] * kLog2e;
+            // fp32: lse itself, see below.
+            lse2 = EPI == kXentGrad ? p.g.lse[m] * kLog2e : p.g.lse[m];
             rs = counts ? p.g.dloss[m] * inv_dmax : 0.f;
           }
         }
       }
-      bool ok = wait_bounded(acc_full + acc, acc_phase, guard, kSiteEpilogue);
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) raise_abort_in_cluster();
-        break;
-      }
-      tc_fence_after_sync();
-      const uint32_t t_row =
-          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN + half * 128);
       const bool work = m_warp < p.g.M && nh < p.g.N;  // warp-uniform
       float run_max = -INFINITY, run_sum = 0.f;  // kXentStats, in units of log2
       // Columns n0 .. n0+31 of this thread's row.
-      auto finish = [&](int c, const uint32_t (&r)[32]) {
+      auto finish = [&](int c, float (&v)[32]) {
         const int n0 = nh + c;
         if (!work || n0 >= p.g.N) return;  // warp-uniform
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
         if constexpr (EPI == kXentStats) {
           const int64_t h = hot - n0;
           if (h >= 0 && h < 32) {
@@ -359,8 +374,11 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           run_max = top;
         } else if constexpr (EPI == kXentGrad || EPI == kXentGradF32) {
           // dz = rs (softmax - [target]), rs = dloss / max |dloss|: exactly 0 in rows that do not count and past N.
+          // In fp32 the difference comes first and the library's expf follows: lse scaled and rounded
+          // would be off by 2^-24 of some 20, the same for the whole row.
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(v[i], kLog2e, -lse2));
+          for (int i = 0; i < 32; ++i)
+            v[i] = EPI == kXentGrad ? exp2_approx(fmaf(v[i], kLog2e, -lse2)) : expf(v[i] - lse2);
           const int64_t h = hot - n0;
           if (h >= 0 && h < 32) {
 #pragma unroll
@@ -451,37 +469,99 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           }
         }
       };
-      uint32_t ra[32], rb[32];
-      __syncwarp();
-      tmem_ld_32cols_issue(t_row, ra);
-      tmem_ld_wait(ra);
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        __syncwarp();
-        tmem_ld_32cols_issue(t_row + static_cast<uint32_t>(c + 32), rb);
-        finish(c, ra);
-        __syncwarp();
-        tmem_ld_wait(rb);
-        if (c + 64 == 128) {
-          // This warp's columns are in registers: hand them back to the MMA issuer.
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_lead + 8u * static_cast<uint32_t>(acc));
-        } else {
-          tmem_ld_32cols_issue(t_row + static_cast<uint32_t>(c + 64), ra);
+      // Waits for the accumulator of the tile's next run; false: give up.
+      auto acc_ready = [&]() {
+        const bool ok = wait_bounded(acc_full + acc, acc_phase, guard, kSiteEpilogue);
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) raise_abort_in_cluster();
+          return false;
         }
-        finish(c + 32, rb);
-        if (c + 64 < 128) {
+        tc_fence_after_sync();
+        return true;
+      };
+      // This warp's columns are in registers: hand them back to the MMA issuer.
+      auto acc_release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_lead + 8u * static_cast<uint32_t>(acc));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      };
+      auto t_row = [&](int c) {
+        return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN + half * 128 + c);
+      };
+      if constexpr (RUNS) {
+        float sum[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+        const int total = p.g.pairs * k_count(slice);
+        int run = 0;
+        bool ok = true;
+        for (; run + p.run < total; run += p.run) {
+          if (!(ok = acc_ready())) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c) __nanosleep(kDrainPauseNs * p.run);
+            float v[32];
+            __syncwarp();
+            tmem_ld_32cols(t_row(32 * c), v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c][i] += v[i];
+          }
+          acc_release();
+        }
+        if (!ok || !acc_ready()) break;
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32cols_issue(t_row(0), r);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+          if (c < 3)
+            tmem_ld_32cols_issue(t_row(32 * c + 32), r);  // in flight while this chunk is finished
+          else
+            acc_release();
+          finish(32 * c, sum[c]);
           __syncwarp();
-          tmem_ld_wait(ra);
+        }
+      } else {
+        if (!acc_ready()) break;
+        uint32_t ra[32], rb[32];
+        auto values = [&](int c, const uint32_t (&r)[32]) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          finish(c, v);
+        };
+        __syncwarp();
+        tmem_ld_32cols_issue(t_row(0), ra);
+        tmem_ld_wait(ra);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          __syncwarp();
+          tmem_ld_32cols_issue(t_row(c + 32), rb);
+          values(c, ra);
+          __syncwarp();
+          tmem_ld_wait(rb);
+          if (c + 64 == 128)
+            acc_release();
+          else
+            tmem_ld_32cols_issue(t_row(c + 64), ra);
+          values(c + 32, rb);
+          if (c + 64 < 128) {
+            __syncwarp();
+            tmem_ld_wait(ra);
+          }
         }
       }
       if constexpr (EPI == kXentStats) {
         if (work && row_ok) p.g.stats[int64_t(nh / kXentPart) * p.g.M + m] = make_float2(run_max, run_sum);
-      }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
       }
     }
     if constexpr (EPI != kXentStats) {
@@ -499,10 +579,10 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
   }
 }
 
-template <int EPI>
+template <int EPI, bool RUNS>
 cudaError_t launch_epi(const XParams& p, cudaStream_t s) {
-  using C = Cfg<EPI>;
-  auto kern = xent_gemm_kernel<EPI>;
+  using C = Cfg<EPI, RUNS>;
+  auto kern = xent_gemm_kernel<EPI, RUNS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -560,17 +640,24 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
   p.wait_ns = wait_ns;
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidSymbol;
+  // Runs where an fp32 result is wanted (the statistics and all of fp32) of a
+  // sum longer than one, cut evenly. dz and gradients that are rounded to bf16
+  // lose nothing by one long sum.
+  const int total = g.pairs * p.kb_per_slice, most = g.pairs > 1 ? kRunF32 : kRunBf16;
+  const int runs = (total + most - 1) / most;
+  p.run = ((total + runs - 1) / runs + 1) / 2 * 2;
+  const bool cut = total > most;
   switch (g.epi) {
     case kXentStats:
-      return launch_epi<kXentStats>(p, s);
+      return cut ? launch_epi<kXentStats, true>(p, s) : launch_epi<kXentStats, false>(p, s);
     case kXentGrad:
-      return launch_epi<kXentGrad>(p, s);
+      return launch_epi<kXentGrad, false>(p, s);
     case kXentGradF32:
-      return launch_epi<kXentGradF32>(p, s);
+      return cut ? launch_epi<kXentGradF32, true>(p, s) : launch_epi<kXentGradF32, false>(p, s);
     case kXentOutBf16:
-      return launch_epi<kXentOutBf16>(p, s);
+      return launch_epi<kXentOutBf16, false>(p, s);
     case kXentOutF32:
-      return launch_epi<kXentOutF32>(p, s);
+      return cut && g.pairs > 1 ? launch_epi<kXentOutF32, true>(p, s) : launch_epi<kXentOutF32, false>(p, s);
     default:
       return cudaErrorInvalidValue;
   }
