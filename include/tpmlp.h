@@ -439,7 +439,7 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  * that does not count: its lookup is zero, its loss is zero, and it gives no
  * gradient. An id at or above V is left out in the same way and records
  * TPMLP_ERR_BOUNDS (check 8 for a target, 9 for a token) for the next
- * tpmlp_check_status(). T, D and V are at most 2^30.
+ * tpmlp_check_status(). T and V are at most 2^30, D at most 2^20.
  * ---------------------------------------------------------------------- */
 
 /* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward

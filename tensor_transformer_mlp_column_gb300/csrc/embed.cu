@@ -8,14 +8,18 @@
 // The gradient is a sum over equal ids. The tokens are sorted by id (a stable
 // radix sort, so equal ids keep the order of t), which turns it into sums of
 // consecutive entries with no atomics: the order of every addition is fixed
-// by the ids alone. The sorted entries are cut into chunks of kRun; a CTA
-// walks one chunk over a slab of columns, keeps the running sum in fp32
-// registers, and writes a table row when the id changes. Where an id's
-// entries cross a chunk's border the partial sums go to scratch, and a second
-// kernel adds them in order: a chunk's work does not depend on how often its
-// ids occur, so one id repeated T times is split like any other input.
+// by the ids alone. The sorted entries are cut into chunks; a CTA walks one
+// chunk over a slab of columns, keeps the running sum in fp32 registers, and
+// writes a table row when the id changes. An id with more entries than two
+// chunks hold leaves partial sums in scratch, which a last kernel adds in
+// order, so that one id repeated T times is split like any other input.
+//
+// Most rows of a large table get no gradient and are cleared, by CTAs that
+// alternate with the summing ones, all but a first part that fills the time
+// of the sort.
 #include "device.cuh"
 #include "internal.h"
+#include "trace.h"
 #include "train.h"
 
 namespace tpmlp {
@@ -27,66 +31,97 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float v) { d = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
-// N consecutive elements as floats; N * sizeof(E) is 16 bytes or one element.
+// N consecutive elements as they are loaded: N * sizeof(E) is 8, 16 or 32
+// bytes, or one element.
+template <typename E, int N>
+struct Raw {
+  static constexpr int kBytes = N * sizeof(E);
+  static constexpr int kWords = kBytes >= 16 ? kBytes / 16 : 1;
+  uint4 w[kWords];
+};
+template <typename E, int N>
+__device__ __forceinline__ void fetch(const E* p, Raw<E, N>& r) {
+  if constexpr (N == 1)
+    *reinterpret_cast<E*>(r.w) = *p;
+  else if constexpr (Raw<E, N>::kBytes == 8)
+    *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(p);
+  else
+#pragma unroll
+    for (int i = 0; i < Raw<E, N>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+template <typename E, int N>
+__device__ __forceinline__ void unpack(const Raw<E, N>& r, float (&f)[N]) {
+  const E* e = reinterpret_cast<const E*>(r.w);
+#pragma unroll
+  for (int j = 0; j < N; ++j) f[j] = to_f(e[j]);
+}
 template <typename E, int N>
 __device__ __forceinline__ void load_n(const E* p, float (&f)[N]) {
-  if constexpr (N == 1) {
-    f[0] = to_f(*p);
-  } else {
-    constexpr int kWords = N * sizeof(E) / 16;
-    uint4 w[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
-    const E* e = reinterpret_cast<const E*>(w);
-#pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = to_f(e[j]);
-  }
+  Raw<E, N> r;
+  fetch<E, N>(p, r);
+  unpack<E, N>(r, f);
 }
 template <typename E, int N>
 __device__ __forceinline__ void store_n(E* p, const float (&f)[N]) {
-  if constexpr (N == 1) {
-    from_f(*p, f[0]);
-  } else {
-    constexpr int kWords = N * sizeof(E) / 16;
-    uint4 w[kWords];
-    E* e = reinterpret_cast<E*>(w);
+  Raw<E, N> r;
+  E* e = reinterpret_cast<E*>(r.w);
 #pragma unroll
-    for (int j = 0; j < N; ++j) from_f(e[j], f[j]);
+  for (int j = 0; j < N; ++j) from_f(e[j], f[j]);
+  if constexpr (N == 1)
+    *p = *e;
+  else if constexpr (Raw<E, N>::kBytes == 8)
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.w);
+  else
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
-  }
+    for (int i = 0; i < Raw<E, N>::kWords; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
 }
 
 // ------------------------------------------------------------------ lookup
 
 constexpr int kThreads = 256;
 
-// A group of `lanes` threads takes one token: pieces of N elements, `lanes`
-// apart. N = 8 where rows split into 16-byte pieces, else 1.
-template <typename E, int N>
+// Columns of slab blockIdx.y: 2^log_lanes threads take a token's pieces of N
+// elements (16 bytes, or one element where rows are not made of 16-byte
+// pieces), K tokens, all loaded before one is written.
+template <typename E, int N, int K>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const E* __restrict__ table, const int64_t* __restrict__ ids,
                                                          int64_t T, int64_t D, int64_t V, float scale,
-                                                         E* __restrict__ out, int lanes, int* status) {
+                                                         E* __restrict__ out, int log_lanes, int* status) {
   pdl_wait();
   pdl_launch_dependents();
-  const int per_cta = kThreads / lanes;
-  const int lane = threadIdx.x % lanes;
-  const int64_t pieces = D / N;
-  for (int64_t t = int64_t(blockIdx.x) * per_cta + threadIdx.x / lanes; t < T; t += int64_t(gridDim.x) * per_cta) {
-    const int64_t id = ids[t];
-    const bool on = id >= 0 && id < V;
-    if (id >= V && lane == 0) atomicCAS(status, 0, kSiteBoundsBase + kChkToken);
-    const E* src = table + (on ? id : 0) * D;
-    E* dst = out + t * D;
-    for (int64_t c = lane; c < pieces; c += lanes) {
-      float f[N];
+  const int groups = kThreads >> log_lanes;  // tokens side by side
+  const int64_t col = int64_t((blockIdx.y << log_lanes) + (threadIdx.x & ((1 << log_lanes) - 1))) * N;
+  if (col >= D) return;
+  const int64_t t0 = int64_t(blockIdx.x) * (groups * K) + (threadIdx.x >> log_lanes);
+  int row[K];  // -1: zero, -2: zero and to be reported
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = 0.f;
-      if (on) load_n<E, N>(src + c * N, f);
+  for (int k = 0; k < K; ++k) {
+    const int64_t id = t0 + k * groups < T ? ids[t0 + k * groups] : -1;
+    row[k] = id < 0 ? -1 : id < V ? static_cast<int>(id) : -2;
+  }
+  Raw<E, N> r[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (row[k] >= 0) fetch<E, N>(table + row[k] * D + col, r[k]);
+  E* dst = out + t0 * D + col;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (t0 + k * groups >= T) break;
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = 0.f;
+    if (row[k] >= 0) {
+      unpack<E, N>(r[k], f);
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] *= scale;
-      store_n<E, N>(dst + c * N, f);
     }
+    store_n<E, N>(dst, f);
+    dst += groups * D;
+  }
+  if (col == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (row[k] == -2) atomicCAS(status, 0, kSiteBoundsBase + kChkToken);
   }
 }
 
@@ -103,10 +138,12 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) {
   return id >= 0 && id < V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(V);
 }
 
-// counts[digit * tiles + tile] = entries of the tile with that digit.
+// counts[digit * tiles + tile] = entries of the tile with that digit; the
+// first pass (from the ids) also marks the ids in `present`.
 __global__ void __launch_bounds__(kThreads) count_kernel(const int64_t* __restrict__ ids, const uint32_t* __restrict__ key,
                                                          int64_t T, int64_t V, int shift, int tiles,
-                                                         uint32_t* __restrict__ counts, int* status) {
+                                                         uint32_t* __restrict__ counts, uint32_t* __restrict__ present,
+                                                         int* status) {
   __shared__ uint32_t hist[kDigits];
   pdl_wait();
   pdl_launch_dependents();
@@ -119,6 +156,9 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const int64_t* __restri
     if (i < T) {
       const uint32_t k = ids ? key_of(ids[i], V) : key[i];
       if (ids && ids[i] >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkToken);
+      // Looked at first: a frequent id would keep all its marks waiting for one word.
+      if (ids && k < V && !(*reinterpret_cast<volatile uint32_t*>(present + (k >> 5)) >> (k & 31) & 1u))
+        atomicOr(present + (k >> 5), 1u << (k & 31));
       atomicAdd(&hist[(k >> shift) & (kDigits - 1)], 1u);
     }
   }
@@ -223,49 +263,426 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(const int64_t* __rest
   }
 }
 
-// ------------------------------------------------------------------ sums of equal ids
+// ------------------------------------------------------------------ the sort in one cluster
 
-constexpr int kRun = 64;  // sorted entries of a chunk
+// CTA c of the first cluster holds the entries c P .. (c + 1) P - 1, P = 1024
+// ITEMS, in shared memory. A pass reads them into registers, ranks them by a
+// digit of up to 9 bits, puts them in the digit's order within the CTA, and
+// copies them to their places in the cluster's shared memory (the last pass:
+// to global memory), neighbours to neighbours: without the order within the
+// CTA every 4 bytes were a transaction of their own, and 65536 tokens took 70
+// us. Above the cluster's capacity a sort of three launches a digit follows.
+// The other clusters clear the first clear_bytes of `clear` meanwhile.
+constexpr int kSortCtas = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBins = 512;
+constexpr int kMaxItems = 8;
+constexpr int64_t kClusterSortMax = int64_t(kSortCtas) * kSortThreads * kMaxItems;
 
-// Chunk blockIdx.x, columns of slab blockIdx.y: thread x holds N consecutive
-// columns. A segment (run of equal ids) inside the chunk goes to its table
-// row; the part of a segment that began in an earlier chunk goes to part[2 b],
-// the part of one that goes on after this chunk (and began in it) to
-// part[2 b + 1]; the whole chunk inside one segment counts as the former.
-template <typename G, typename E, int N>
-__global__ void __launch_bounds__(kThreads) segment_kernel(const G* __restrict__ dout, const uint32_t* __restrict__ key,
-                                                           const uint32_t* __restrict__ pos, int64_t T, int64_t D,
-                                                           int64_t V, float scale, E* __restrict__ dE, int accumulate,
-                                                           float* __restrict__ part) {
-  __shared__ uint32_t skey[kRun + 2], spos[kRun];
+__host__ __device__ constexpr size_t sort_smem(int items) {
+  return 2 * size_t(items) * kSortThreads * 8 + size_t(kSortWarps) * kMaxBins * 2 + 3 * kMaxBins * 4 + 64 * 4;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint2 v) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const int64_t* __restrict__ ids, int64_t T, int64_t V,
+                                                               int bits, int passes, uint32_t* __restrict__ key_out,
+                                                               uint32_t* __restrict__ pos_out,
+                                                               uint32_t* __restrict__ present, void* clear,
+                                                               int64_t clear_bytes, int* status) {
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t first = int64_t(blockIdx.x) * kRun;
-  const int n = static_cast<int>(T - first < kRun ? T - first : kRun);
-  // skey[0] and skey[n + 1]: the neighbours' keys (all ones where there is none).
-  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
-    const int64_t at = first + i - 1;
+  if (blockIdx.x >= kSortCtas) {
+    // In consecutive blocks of 64 KB.
+    constexpr int64_t kBlock = 4096;
+    const int64_t n16 = clear_bytes / 16;
+    for (int64_t b = int64_t(blockIdx.x - kSortCtas) * kBlock; b < n16; b += int64_t(gridDim.x - kSortCtas) * kBlock)
+#pragma unroll
+      for (int u = 0; u < kBlock / kSortThreads; ++u) {
+        const int64_t i = b + u * kSortThreads + threadIdx.x;
+        if (i < n16) reinterpret_cast<uint4*>(clear)[i] = make_uint4(0, 0, 0, 0);
+      }
+    return;
+  }
+  constexpr int P = ITEMS * kSortThreads;
+  uint2* entry = reinterpret_cast<uint2*>(smem);  // (key, position)
+  uint2* staged = entry + P;
+  uint16_t* seen = reinterpret_cast<uint16_t*>(staged + P);                     // [warp][bin]
+  uint32_t* count = reinterpret_cast<uint32_t*>(seen + kSortWarps * kMaxBins);  // this CTA's entries of a bin
+  uint32_t* local = count + kMaxBins;  // place of the bin's first entry within the CTA
+  uint32_t* move = local + kMaxBins;   // from there to its place in the cluster
+  uint32_t* sums = move + kMaxBins;    // two scans of 16 warps
+  const uint32_t cta = cluster_ctarank();
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, tid = threadIdx.x;
+  const int64_t left = T - int64_t(cta) * P;
+  const int n = left < 0 ? 0 : left < P ? static_cast<int>(left) : P;  // this CTA's entries
+  const int mine = w * (32 * ITEMS) + l;                               // this thread's: mine + 32 r
+  const int bins = 1 << bits;
+  for (int64_t i = int64_t(cta) * kSortThreads + tid; i < (V + 31) / 32; i += kSortCtas * kSortThreads) present[i] = 0;
+  cluster_sync_all();  // orders the clearing of `present` before the cluster's marks
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    uint2 e[ITEMS];
+    uint32_t place[ITEMS];
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      const int i = mine + 32 * r;
+      e[r] = make_uint2(0, 0);
+      if (i >= n) continue;
+      if (pass == 0) {
+        const int64_t id = ids[int64_t(cta) * P + i];
+        if (id >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkToken);
+        e[r] = make_uint2(key_of(id, V), cta * P + i);
+      } else {
+        e[r] = entry[i];
+      }
+    }
+    for (int d = l; d < bins; d += 32) seen[w * kMaxBins + d] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      const bool on = mine + 32 * r < n;
+      const uint32_t d = (e[r].x >> shift) & (bins - 1);
+      // Lanes with the same digit, bit by bit.
+      uint32_t same = __ballot_sync(0xffffffffu, on);
+      for (int bit = 0; bit < bits; ++bit) {
+        const bool set = d >> bit & 1u;
+        const uint32_t b = __ballot_sync(0xffffffffu, set);
+        same &= set ? b : ~b;
+      }
+      const uint32_t before = __popc(same & ((1u << l) - 1u));
+      uint32_t at = 0;
+      if (on) at = seen[w * kMaxBins + d];
+      __syncwarp();
+      if (on && before == 0) seen[w * kMaxBins + d] = static_cast<uint16_t>(at + __popc(same));
+      __syncwarp();
+      place[r] = at + before;
+    }
+    __syncthreads();
+    if (tid < bins) {  // the warps' counts -> the warps' first places within the bin
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int v = 0; v < kSortWarps; ++v) {
+        const uint32_t c = seen[v * kMaxBins + tid];
+        seen[v * kMaxBins + tid] = static_cast<uint16_t>(run);
+        run += c;
+      }
+      count[tid] = run;
+    }
+    cluster_sync_all();  // every CTA's counts are there, every entry is in registers
+    // Places: bin by bin in the cluster, within a bin CTA by CTA; and within this CTA.
+    uint32_t total = 0, ahead = 0, own = 0, x = 0, y = 0;
+    if (tid < kMaxBins) {
+      if (tid < bins) {
+        own = count[tid];
+#pragma unroll
+        for (uint32_t c = 0; c < kSortCtas; ++c) {
+          const uint32_t v = ld_cluster_u32(map_to_cta(smem_addr(count + tid), c));
+          if (c < cta) ahead += v;
+          total += v;
+        }
+      }
+      x = total, y = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+        if (l >= o) x += a, y += b;
+      }
+      if (l == 31) sums[w] = x, sums[16 + w] = y;
+    }
+    __syncthreads();
+    if (tid < bins) {
+      uint32_t lx = 0, ly = 0;
+      for (int v = 0; v < w; ++v) lx += sums[v], ly += sums[16 + v];
+      local[tid] = ly + y - own;
+      move[tid] = (lx + x - total + ahead) - (ly + y - own);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      if (mine + 32 * r >= n) continue;
+      const uint32_t d = (e[r].x >> shift) & (bins - 1);
+      staged[local[d] + seen[w * kMaxBins + d] + place[r]] = e[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      const int i = r * kSortThreads + tid;
+      if (i >= n) continue;
+      const uint2 v = staged[i];
+      const uint32_t to = i + move[(v.x >> shift) & (bins - 1)];
+      if (pass + 1 < passes) {
+        st_cluster_v2(map_to_cta(smem_addr(entry + to % P), to / P), v);
+      } else {
+        key_out[to] = v.x;
+        pos_out[to] = v.y;
+        // In the last pass the CTA's entries are in the order of their keys: one mark for each.
+        if (v.x < V && (i == 0 || staged[i - 1].x != v.x)) atomicOr(present + (v.x >> 5), 1u << (v.x & 31));
+      }
+    }
+    cluster_sync_all();  // entries in place, counts read
+  }
+}
+
+template <int ITEMS>
+cudaError_t cluster_sort(const int64_t* ids, int64_t T, int64_t V, uint32_t* key, uint32_t* pos, uint32_t* present,
+                         void* clear, int64_t clear_bytes, int* status, cudaStream_t s) {
+  auto kern = sort_kernel<ITEMS>;
+  constexpr size_t smem = sort_smem(ITEMS);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  int all = 1;
+  while ((V >> all) != 0) ++all;  // bits of the keys 0 .. V
+  const int passes = (all + 8) / 9, bits = (all + passes - 1) / passes;
+  // One CTA an SM; clearing takes as many clusters as 64 KB for each of their CTAs justify.
+  int64_t clusters = 1 + (clear_bytes + 65536 * kSortCtas - 1) / (65536 * kSortCtas);
+  const int64_t cap = num_sms() / kSortCtas > 2 ? num_sms() / kSortCtas : 2;
+  if (clusters > cap) clusters = cap;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSortCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kSortCtas));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, ids, T, V, bits, passes, key, pos, present, clear, clear_bytes, status);
+}
+
+// ------------------------------------------------------------------ sums of equal ids
+
+constexpr int kMaxRun = 64;
+constexpr int kBatch = 8;
+// Sorted entries of a chunk: few where there are few tokens, so that the
+// chunks still spread over the SMs.
+int run_of(int64_t T) { return T <= 16384 ? 16 : kMaxRun; }
+
+// What the clearing CTAs of segment_kernel do: table rows from `row0` on that
+// are not marked in `present`, in pieces of `piece` bytes (16, or an element
+// where rows are not made of 16-byte pieces), kClearPieces a CTA.
+constexpr int kClearUnroll = 8;
+constexpr int kClearPieces = kThreads * kClearUnroll;
+struct Clear {
+  const uint32_t* present;
+  int64_t row0, pieces;     // pieces of all rows from row0 on
+  uint32_t row_pieces;      // pieces of a row
+  int piece;
+  int64_t ctas;
+};
+
+__device__ __forceinline__ void clear_rows(const Clear& c, int64_t cta, char* dE) {
+  const int64_t first = cta * kClearPieces;
+  const int n = static_cast<int>(c.pieces - first < kClearPieces ? c.pieces - first : kClearPieces);
+  const int64_t row = first / c.row_pieces;
+  const uint32_t skip = static_cast<uint32_t>(first - row * c.row_pieces);
+  char* base = dE + (c.row0 * c.row_pieces + first) * c.piece;
+  uint32_t marks[kClearUnroll];
+#pragma unroll
+  for (int u = 0; u < kClearUnroll; ++u) {
+    const int i = threadIdx.x + u * kThreads;
+    const int64_t v = c.row0 + row + (skip + static_cast<uint32_t>(i)) / c.row_pieces;
+    marks[u] = i < n ? __ldg(c.present + (v >> 5)) >> (v & 31) & 1u : 1u;
+  }
+#pragma unroll
+  for (int u = 0; u < kClearUnroll; ++u) {
+    if (marks[u]) continue;
+    char* p = base + int64_t(threadIdx.x + u * kThreads) * c.piece;
+    if (c.piece == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+    else if (c.piece == 4)
+      *reinterpret_cast<uint32_t*>(p) = 0;
+    else
+      *reinterpret_cast<uint16_t*>(p) = 0;
+  }
+}
+
+// Chunk b (`run` sorted entries), columns of slab y: thread x holds N
+// consecutive columns. A segment (run of equal ids) of up to 2 run entries
+// belongs to the chunk in which it begins, whose CTA follows it past the
+// chunk's end. Of a longer one every chunk sums its part: the part of a segment
+// that began in an earlier chunk goes to part[2 b], the part of one that
+// begins in it to part[2 b + 1], and goes_on[b] says that there is such a
+// one. The clearing CTAs alternate with these evenly over the grid.
+template <typename G, typename E, int N>
+__global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restrict__ dout, const uint32_t* __restrict__ key,
+                                                           const uint32_t* __restrict__ pos, int64_t T, int64_t D,
+                                                           int64_t V, float scale, E* __restrict__ dE, int accumulate,
+                                                           float* __restrict__ part, uint8_t* __restrict__ goes_on,
+                                                           int run, int slabs, const __grid_constant__ Clear clear) {
+  __shared__ uint32_t skey[5 * kMaxRun], spos[3 * kMaxRun];
+  pdl_wait();
+  pdl_launch_dependents();
+  int64_t job = blockIdx.x;
+  if (clear.ctas > 0) {
+    const int64_t all = gridDim.x, sums = all - clear.ctas;
+    job = blockIdx.x * sums / all;  // summing CTAs before this one
+    if ((blockIdx.x + 1) * sums / all == job) {
+      clear_rows(clear, blockIdx.x - job, reinterpret_cast<char*>(dE));
+      return;
+    }
+  }
+  const int64_t chunk = job / slabs;
+  const int64_t first = chunk * run;
+  const int n = static_cast<int>(T - first < run ? T - first : run);
+  const int most = 2 * run;
+  // skey[most + i]: the key of entry first + i, from `most` entries before the
+  // chunk to `most` after it (all ones past the end).
+  for (int i = threadIdx.x; i < run + 2 * most; i += blockDim.x) {
+    const int64_t at = first + i - most;
     skey[i] = at >= 0 && at < T ? key[at] : 0xffffffffu;
-    if (i >= 1 && i <= n) spos[i - 1] = pos[at];
+    if (i >= most && at < T) spos[i - most] = pos[at];
   }
   __syncthreads();
-  const int64_t col = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * N;
+  const uint32_t* k_at = skey + most;
+  // First index in [lo, hi) whose key is at least (after = 0) or above (1) k.
+  auto bound = [&](int lo, int hi, uint32_t k, bool after) {
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (after ? k_at[mid] <= k : k_at[mid] < k)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+  const int lowest = first < most ? -static_cast<int>(first) : -most;
+  int start = 0, stop = n;
+  bool began = true;  // whether the running segment began in this chunk
+  {
+    const uint32_t k = k_at[0];
+    const int a = bound(lowest, 0, k, false);
+    if (a < 0) {  // it began earlier: summed there, unless it is a long one
+      began = a > -most && k_at[a + most] != k;
+      if (began) start = bound(0, n, k, true);
+    }
+  }
+  bool long_on = false;
+  if (start < n && n == run && k_at[n] == k_at[n - 1]) {
+    const uint32_t k = k_at[n - 1];
+    const int a = bound(lowest, n, k, false);
+    if (a >= 0) {  // it begins in this chunk
+      long_on = k_at[a + most] == k;
+      if (!long_on) stop = bound(n, n + most, k, true);
+    }
+  }
+  if (job == chunk * slabs && threadIdx.x == 0) goes_on[chunk] = long_on && k_at[n - 1] < V;
+  const int64_t col = ((job - chunk * slabs) * blockDim.x + threadIdx.x) * N;
   if (col >= D) return;
   float sum[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) sum[j] = 0.f;
-  bool began = skey[0] != skey[1];  // whether the running segment began in this chunk
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const uint32_t k = skey[i + 1];
-    if (k >= V) break;  // entries without a row, sorted last
-    float f[N];
-    load_n<G, N>(dout + int64_t(spos[i]) * D + col, f);
+  // A ring of kBatch rows on their way: row i + kBatch is fetched when row i is added.
+  Raw<G, N> r[kBatch];
+  auto issue = [&](int i, Raw<G, N>& to) {
+    if (i >= stop || k_at[i] >= V) return;
+    fetch<G, N>(dout + int64_t(spos[i]) * D + col, to);
+    if (accumulate && k_at[i + 1] != k_at[i])
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(dE + int64_t(k_at[i]) * D + col));
+  };
 #pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] += f[j];
-    const bool last = skey[i + 2] != k;
-    if (!last && i + 1 < n) continue;
-    if (last && began) {
+  for (int b = 0; b < kBatch; ++b) issue(start + b, r[b]);
+  for (int i0 = start; i0 < stop; i0 += kBatch) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b;
+      if (i >= stop) return;
+      const uint32_t k = k_at[i];
+      if (k >= V) return;  // entries without a row, sorted last
+      float f[N];
+      unpack<G, N>(r[b], f);
+      issue(i + kBatch, r[b]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[j] += f[j];
+      const bool last = k_at[i + 1] != k;
+      if (!last && i + 1 < stop) continue;
+      if (last && began) {
+        E* row = dE + int64_t(k) * D + col;
+        float old[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) old[j] = 0.f;
+        if (accumulate) load_n<E, N>(row, old);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[j] = fmaf(sum[j], scale, old[j]);
+        store_n<E, N>(row, sum);
+      } else {
+        store_n<float, N>(part + (2 * chunk + (began ? 1 : 0)) * D + col, sum);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum[j] = 0.f;
+      began = true;
+    }
+  }
+}
+
+// The long segments that begin in one of the chunks 32 blockIdx.x .. + 31: adds
+// their parts in order and writes the table row. A CTA takes 32 N columns;
+// its eight warps take consecutive eighths of a segment's parts and their
+// sums are added in the warps' order, so that one id repeated T times is
+// still spread over the GPU.
+constexpr int kJoinChunks = 32;
+template <typename E, int N>
+__global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restrict__ key, int64_t T, int64_t D, int run,
+                                                        float scale, E* __restrict__ dE, int accumulate,
+                                                        const float* __restrict__ part,
+                                                        const uint8_t* __restrict__ goes_on, int64_t chunks) {
+  __shared__ float red[kThreads / 32][32 * N];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  // Lane l looks at chunk 32 blockIdx.x + l (every warp alike).
+  const int64_t mine = int64_t(blockIdx.x) * kJoinChunks + l;
+  const bool owns = mine < chunks && goes_on[mine];
+  uint32_t todo = __ballot_sync(0xffffffffu, owns);
+  const int64_t col = (int64_t(blockIdx.y) * 32 + l) * N;
+  for (; todo; todo &= todo - 1) {
+    const int64_t b = int64_t(blockIdx.x) * kJoinChunks + __ffs(todo) - 1;
+    const uint32_t k = key[(b + 1) * run - 1];
+    // The chunks that the segment reaches are those after b whose first key is k.
+    int64_t reach = b + 1;
+    for (;;) {
+      const int64_t c = reach + threadIdx.x;
+      const int more = __syncthreads_count(c * run < T && key[c * run] == k);
+      reach += more;
+      if (more < kThreads) break;
+    }
+    // Parts: part[2 b + 1], then part[2 c] for c = b + 1 .. reach - 1.
+    const int64_t parts = reach - b, per = (parts + 7) / 8;
+    const int64_t from = w * per, to = from + per < parts ? from + per : parts;
+    float sum[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum[j] = 0.f;
+    if (col < D) {
+#pragma unroll 4
+      for (int64_t i = from; i < to; ++i) {
+        float f[N];
+        load_n<float, N>(part + (i == 0 ? 2 * b + 1 : 2 * (b + i)) * D + col, f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[j] += f[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) red[w][l * N + j] = sum[j];
+    __syncthreads();
+    if (w == 0 && col < D) {
+      for (int v = 1; v < kThreads / 32; ++v)
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[j] += red[v][l * N + j];
       E* row = dE + int64_t(k) * D + col;
       float old[N];
 #pragma unroll
@@ -274,82 +691,74 @@ __global__ void __launch_bounds__(kThreads) segment_kernel(const G* __restrict__
 #pragma unroll
       for (int j = 0; j < N; ++j) sum[j] = fmaf(sum[j], scale, old[j]);
       store_n<E, N>(row, sum);
-    } else {
-      store_n<float, N>(part + (2 * int64_t(blockIdx.x) + (began ? 1 : 0)) * D + col, sum);
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] = 0.f;
-    began = true;
+    __syncthreads();
   }
 }
 
-// Chunk blockIdx.x where a segment begins that goes on after it: adds its
-// parts in order and writes the table row.
 template <typename E, int N>
-__global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restrict__ key, int64_t T, int64_t D, int64_t V,
-                                                        float scale, E* __restrict__ dE, int accumulate,
-                                                        const float* __restrict__ part) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t b = blockIdx.x, end = (b + 1) * kRun;  // the chunk's end
-  if (end >= T) return;
-  const uint32_t k = key[end - 1];
-  if (k >= V || key[end] != k) return;              // no segment goes on
-  if (key[b * kRun] == k && b > 0 && key[b * kRun - 1] == k) return;  // it began earlier
-  const int64_t col = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * N;
-  if (col >= D) return;
-  float sum[N];
-  load_n<float, N>(part + (2 * b + 1) * D + col, sum);
-  for (int64_t c = b + 1; c * kRun < T && key[c * kRun] == k; ++c) {
-    float f[N];
-    load_n<float, N>(part + 2 * c * D + col, f);
-#pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] += f[j];
-  }
-  E* row = dE + int64_t(k) * D + col;
-  float old[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) old[j] = 0.f;
-  if (accumulate) load_n<E, N>(row, old);
-#pragma unroll
-  for (int j = 0; j < N; ++j) sum[j] = fmaf(sum[j], scale, old[j]);
-  store_n<E, N>(row, sum);
+cudaError_t lookup(const E* table, const int64_t* ids, int64_t T, int64_t D, int64_t V, float scale, E* out, int* status,
+                   cudaStream_t s) {
+  const int64_t pieces = D / N;
+  int log_lanes = 0;
+  while ((1 << log_lanes) < kThreads && (1 << log_lanes) < pieces) ++log_lanes;
+  const int64_t lanes = int64_t(1) << log_lanes;
+  const int64_t slabs = (pieces + lanes - 1) / lanes, groups = kThreads / lanes;
+  // Four tokens a thread where that still leaves eight CTAs an SM.
+  const int64_t per4 = (T + groups * 4 - 1) / (groups * 4);
+  const bool four = per4 * slabs >= int64_t(num_sms()) * 8;
+  const int64_t x = four ? per4 : (T + groups - 1) / groups;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(slabs));
+  return four ? launch_pdl(embed_kernel<E, N, 4>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status)
+              : launch_pdl(embed_kernel<E, N, 1>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status);
 }
 
 template <typename E>
 cudaError_t embed_dispatch(const E* table, const int64_t* ids, int64_t T, int64_t D, int64_t V, float scale, E* out,
                            int* status, cudaStream_t s) {
-  const bool vec = D * static_cast<int64_t>(sizeof(E)) % 16 == 0 && D % 8 == 0;
-  const int64_t pieces = vec ? D / 8 : D;
-  int lanes = 1;
-  while (lanes < kThreads && lanes < pieces) lanes <<= 1;
-  const int64_t want = (T + kThreads / lanes - 1) / (kThreads / lanes), cap = int64_t(num_sms()) * 8;
-  const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
-  return vec ? launch_pdl(embed_kernel<E, 8>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, lanes, status)
-             : launch_pdl(embed_kernel<E, 1>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, lanes, status);
+  constexpr int N = 16 / sizeof(E);
+  return D % N == 0 ? lookup<E, N>(table, ids, T, D, V, scale, out, status, s)
+                    : lookup<E, 1>(table, ids, T, D, V, scale, out, status, s);
 }
 
 template <typename G, typename E, int N>
 cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, int64_t T, int64_t D, int64_t V,
-                     float scale, E* dE, int accumulate, float* part, cudaStream_t s) {
+                     float scale, E* dE, int accumulate, float* part, uint8_t* goes_on, const Clear& clear,
+                     cudaStream_t s) {
+  const int run = run_of(T);
   const int64_t pieces = D / N;
   int threads = 32;
   while (threads < kThreads && threads < pieces) threads <<= 1;
-  const dim3 grid(static_cast<unsigned>((T + kRun - 1) / kRun), static_cast<unsigned>((pieces + threads - 1) / threads));
-  cudaError_t e = launch_pdl(segment_kernel<G, E, N>, grid, dim3(threads), 0, s, dout, key, pos, T, D, V, scale, dE,
-                             accumulate, part);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<E, N>, grid, dim3(threads), 0, s, key, T, D, V, scale, dE, accumulate,
-                    static_cast<const float*>(part));
+  if (clear.ctas > 0) threads = kThreads;  // the clearing CTAs'
+  const int64_t slabs = (pieces + threads - 1) / threads, chunks = (T + run - 1) / run;
+  const int64_t grid = chunks * slabs + clear.ctas;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  {
+    TraceScope trace("embed_segments", s);
+    const cudaError_t e = launch_pdl(segment_kernel<G, E, N>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, dout,
+                                     key, pos, T, D, V, scale, dE, accumulate, part, goes_on, run, static_cast<int>(slabs), clear);
+    if (e != cudaSuccess) return e;
+  }
+  if (T <= 2 * run) return cudaSuccess;  // no segment is longer than that
+  TraceScope trace("embed_join", s);
+  // Four columns a thread where rows allow, whatever dout's pieces are.
+  const dim3 join4(static_cast<unsigned>((chunks + kJoinChunks - 1) / kJoinChunks), static_cast<unsigned>((D + 127) / 128));
+  const dim3 join1(join4.x, static_cast<unsigned>((D + 31) / 32));
+  const float* p = part;
+  const uint8_t* on = goes_on;
+  return D % 4 == 0
+             ? launch_pdl(join_kernel<E, 4>, join4, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks)
+             : launch_pdl(join_kernel<E, 1>, join1, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks);
 }
 
 template <typename G, typename E>
 cudaError_t segments_dispatch(const void* dout, const uint32_t* key, const uint32_t* pos, int64_t T, int64_t D, int64_t V,
-                              float scale, void* dE, int accumulate, float* part, cudaStream_t s) {
+                              float scale, void* dE, int accumulate, float* part, uint8_t* goes_on, const Clear& clear, cudaStream_t s) {
   const G* g = static_cast<const G*>(dout);
   E* e = static_cast<E*>(dE);
-  return D % 8 == 0 ? segments<G, E, 8>(g, key, pos, T, D, V, scale, e, accumulate, part, s)
-                    : segments<G, E, 1>(g, key, pos, T, D, V, scale, e, accumulate, part, s);
+  constexpr int N = 16 / sizeof(G);
+  return D % N == 0 ? segments<G, E, N>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s)
+                    : segments<G, E, 1>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -365,7 +774,6 @@ cudaError_t launch_embed(const void* E, const int64_t* ids, int64_t T, int64_t D
 }
 
 EmbedPlan plan_embed(int64_t T, int64_t D, int64_t V) {
-  (void)V;
   EmbedPlan p{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -377,8 +785,11 @@ EmbedPlan plan_embed(int64_t T, int64_t D, int64_t V) {
     p.key[i] = take(size_t(T) * 4);
     p.pos[i] = take(size_t(T) * 4);
   }
+  p.present = take(size_t((V + 31) / 32) * 4);
   p.counts = take(size_t((T + kTile - 1) / kTile) * kDigits * 4);
-  p.part = take(size_t((T + kRun - 1) / kRun) * 2 * size_t(D) * 4);
+  const size_t chunks = size_t((T + run_of(T) - 1) / run_of(T));
+  p.goes_on = take(chunks);
+  p.part = take(chunks * 2 * size_t(D) * 4);
   p.total = off;
   return p;
 }
@@ -387,35 +798,63 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
                               float scale, void* dE, int dE_bf16, int accumulate, void* ws, int* status,
                               cudaStream_t s) {
   cudaError_t e;
-  if (!accumulate) {
-    e = cudaMemsetAsync(dE, 0, size_t(V) * size_t(D) * (dE_bf16 ? 2 : 4), s);
-    if (e != cudaSuccess || T == 0) return e;
-  }
+  const size_t bytes = size_t(V) * size_t(D) * (dE_bf16 ? 2 : 4);
+  if (T == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dE, 0, bytes, s);
   const EmbedPlan p = plan_embed(T, D, V);
   char* base = static_cast<char*>(ws);
   uint32_t* key[2] = {reinterpret_cast<uint32_t*>(base + p.key[0]), reinterpret_cast<uint32_t*>(base + p.key[1])};
   uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(base + p.pos[0]), reinterpret_cast<uint32_t*>(base + p.pos[1])};
   uint32_t* counts = reinterpret_cast<uint32_t*>(base + p.counts);
-  const int tiles = static_cast<int>((T + kTile - 1) / kTile);
+  uint32_t* present = reinterpret_cast<uint32_t*>(base + p.present);
+  // Rows are cleared in pieces of 16 bytes, or of one element where a row does not divide into those.
+  const int64_t row_bytes = D * (dE_bf16 ? 2 : 4);
+  Clear clear{};
+  clear.present = present;
+  clear.piece = row_bytes % 16 == 0 ? 16 : dE_bf16 ? 2 : 4;
+  clear.row_pieces = static_cast<uint32_t>(row_bytes / clear.piece);
+  const bool cluster = T <= kClusterSortMax;
+  if (!accumulate) {
+    // The sort in the cluster takes about 8 us and 2 us per 8192 tokens, in which the other SMs write 4 MB a us.
+    if (cluster && clear.piece == 16) clear.row0 = (int64_t(8) + 2 * T / 8192) * (4 << 20) / row_bytes;
+    if (clear.row0 > V) clear.row0 = V;
+    clear.pieces = (V - clear.row0) * clear.row_pieces;
+    clear.ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
+  }
   int at = 0;
-  for (int shift = 0; shift == 0 || (V >> shift) != 0; shift += 8) {  // keys are 0 .. V
-    const int64_t* from = shift == 0 ? ids : nullptr;
-    if ((e = launch_pdl(count_kernel, dim3(tiles), dim3(kThreads), 0, s, from, static_cast<const uint32_t*>(key[at]), T, V,
-                        shift, tiles, counts, status)) != cudaSuccess)
-      return e;
-    if ((e = launch_pdl(scan_kernel, dim3(1), dim3(1024), 0, s, counts, int64_t(tiles) * kDigits)) != cudaSuccess) return e;
-    if ((e = launch_pdl(scatter_kernel, dim3(tiles), dim3(kThreads), 0, s, from, static_cast<const uint32_t*>(key[at]),
-                        static_cast<const uint32_t*>(pos[at]), T, V, shift, tiles, static_cast<const uint32_t*>(counts),
-                        key[at ^ 1], pos[at ^ 1])) != cudaSuccess)
-      return e;
-    at ^= 1;
+  {
+    TraceScope trace("embed_sort", s);
+    if (cluster) {
+      const int64_t first = clear.row0 * row_bytes, per_cta = (T + kSortCtas - 1) / kSortCtas;
+      e = per_cta <= kSortThreads       ? cluster_sort<1>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+          : per_cta <= 2 * kSortThreads ? cluster_sort<2>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+          : per_cta <= 4 * kSortThreads ? cluster_sort<4>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+                                        : cluster_sort<kMaxItems>(ids, T, V, key[0], pos[0], present, dE, first, status, s);
+      if (e != cudaSuccess) return e;
+    } else {
+      if ((e = cudaMemsetAsync(present, 0, size_t((V + 31) / 32) * 4, s)) != cudaSuccess) return e;
+      const int tiles = static_cast<int>((T + kTile - 1) / kTile);
+      for (int shift = 0; shift == 0 || (V >> shift) != 0; shift += 8) {  // keys are 0 .. V
+        const int64_t* from = shift == 0 ? ids : nullptr;
+        if ((e = launch_pdl(count_kernel, dim3(tiles), dim3(kThreads), 0, s, from, static_cast<const uint32_t*>(key[at]), T,
+                            V, shift, tiles, counts, present, status)) != cudaSuccess)
+          return e;
+        if ((e = launch_pdl(scan_kernel, dim3(1), dim3(1024), 0, s, counts, int64_t(tiles) * kDigits)) != cudaSuccess)
+          return e;
+        if ((e = launch_pdl(scatter_kernel, dim3(tiles), dim3(kThreads), 0, s, from, static_cast<const uint32_t*>(key[at]),
+                            static_cast<const uint32_t*>(pos[at]), T, V, shift, tiles,
+                            static_cast<const uint32_t*>(counts), key[at ^ 1], pos[at ^ 1])) != cudaSuccess)
+          return e;
+        at ^= 1;
+      }
+    }
   }
   float* part = reinterpret_cast<float*>(base + p.part);
+  uint8_t* goes_on = reinterpret_cast<uint8_t*>(base + p.goes_on);
   if (dout_bf16)
-    return dE_bf16 ? segments_dispatch<__nv_bfloat16, __nv_bfloat16>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, s)
-                   : segments_dispatch<__nv_bfloat16, float>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, s);
-  return dE_bf16 ? segments_dispatch<float, __nv_bfloat16>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, s)
-                 : segments_dispatch<float, float>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, s);
+    return dE_bf16 ? segments_dispatch<__nv_bfloat16, __nv_bfloat16>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, goes_on, clear, s)
+                   : segments_dispatch<__nv_bfloat16, float>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, goes_on, clear, s);
+  return dE_bf16 ? segments_dispatch<float, __nv_bfloat16>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, goes_on, clear, s)
+                 : segments_dispatch<float, float>(dout, key[at], pos[at], T, D, V, scale, dE, accumulate, part, goes_on, clear, s);
 }
 
 }  // namespace tpmlp

@@ -53,8 +53,10 @@ cudaError_t launch_embed(const void* E, const int64_t* ids, int64_t T, int64_t D
 // Byte offsets of the gradient's scratch.
 struct EmbedPlan {
   size_t key[2], pos[2];  // int32 [T] each, twice: the sort's source and destination
+  size_t present;         // one bit for each id: whether it occurs
   size_t counts;          // the sort's digit counts
-  size_t part;            // fp32 [2 chunks][D]: sums of segments that cross a chunk's border
+  size_t goes_on;         // a byte for each chunk of sorted entries: whether a long segment begins in it
+  size_t part;            // fp32 [2 chunks][D]: the chunks' parts of long segments
   size_t total;
 };
 EmbedPlan plan_embed(int64_t T, int64_t D, int64_t V);

@@ -52,13 +52,13 @@ int current_sm103() {
 
 bool known(tpmlp_dtype dt) { return dt == TPMLP_F32 || dt == TPMLP_BF16; }
 
-// Sizes of the cross entropy and of the embedding; at most 2^30 each, so that
-// ids, rows and tile coordinates fit 32 bits.
-constexpr int64_t kMaxSize = int64_t(1) << 30;
+// Sizes of the cross entropy and of the embedding: ids, rows and tile
+// coordinates fit 32 bits, slabs of columns a grid's second dimension.
+constexpr int64_t kMaxSize = int64_t(1) << 30, kMaxD = int64_t(1) << 20;
 int check_sizes(int64_t T, int64_t D, int64_t V) {
   if (T < 0 || T > kMaxSize) return set_error(TPMLP_ERR_ARG, "T = %lld must be in [0, 2^30]", static_cast<long long>(T));
-  if (D < 1 || D > kMaxSize || V < 1 || V > kMaxSize)
-    return set_error(TPMLP_ERR_ARG, "D = %lld and V = %lld must be in [1, 2^30]", static_cast<long long>(D),
+  if (D < 1 || D > kMaxD || V < 1 || V > kMaxSize)
+    return set_error(TPMLP_ERR_ARG, "D = %lld must be in [1, 2^20] and V = %lld in [1, 2^30]", static_cast<long long>(D),
                      static_cast<long long>(V));
   return TPMLP_OK;
 }
@@ -277,7 +277,6 @@ int tpmlp_embed_backward(const void* dout, tpmlp_dtype dout_dt, const int64_t* i
     return TPMLP_OK;
   }
   if ((rc = current_sm103())) return rc;
-  TraceScope trace("embed_backward", stream);
   TRAIN_TRY(launch_embed_grad(dout, dout_dt == TPMLP_BF16, ids, T, D, V, scale, dE, dE_dt == TPMLP_BF16,
                               accumulate != 0, ws, device_status_word(), stream));
   return TPMLP_OK;

@@ -282,6 +282,32 @@ def test_embed_gradient(tp, T, D, V, kind, types):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("kind", ["words", "one", "each"])
+@pytest.mark.parametrize("T,D,V", [
+    (8192, 8, 511), (8193, 8, 512), (32769, 16, 70000), (60000, 4, 262143), (65536, 136, 1000),  # one cluster sorts
+    (65537, 8, 262144), (300001, 8, 90), (70000, 5, 3000),                                       # three launches a digit
+])
+def test_embed_gradient_of_many_tokens(tp, T, D, V, kind):
+    # Around the limits of the two sorts and of their digits.
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    dout = torch.randn(T, D, generator=g, device="cuda")
+    ids = _ids(T, V, T + 2, kind)
+    got = _check_embed_grad(tp, dout, ids, V, 1.0, torch.float32)
+    assert torch.equal(got, tp.tpmlp_embed_backward(dout, ids, V))
+    dE0 = torch.randn(V, D, generator=g, device="cuda")
+    _check_embed_grad(tp, dout, ids, V, 1.0, torch.float32, dE0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_embed_lookup_of_many_tokens(tp, dtype):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for T, D, V in ((70001, 136, 500), (20000, 1500, 3000)):
+        E = torch.randn(V, D, generator=g, device="cuda").to(DT[dtype])
+        ids = _ids(T, V, T, "words")
+        ref = torch.where((ids >= 0)[:, None], E[ids.clamp(min=0)].float() * 0.3, torch.zeros((), device="cuda")).to(E.dtype)
+        assert torch.equal(tp.tpmlp_embed_forward(E, ids, 0.3), ref)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_embed_gradient_added_to_a_tied_table(tp, dtype):
     g = torch.Generator(device="cuda").manual_seed(3)

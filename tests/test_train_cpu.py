@@ -43,6 +43,7 @@ SIZES = [
     (dict(T=-1), "TPMLP_ERR_ARG"),
     (dict(T=(1 << 30) + 1), "TPMLP_ERR_ARG"),
     (dict(D=0), "TPMLP_ERR_ARG"),
+    (dict(D=(1 << 20) + 8), "TPMLP_ERR_ARG"),
     (dict(V=0), "TPMLP_ERR_ARG"),
     (dict(V=(1 << 30) + 1), "TPMLP_ERR_ARG"),
 ]
