@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(256) xent_split_kernel(const float* __restrict
   }
 }
 
-// out = dmax * (part[0] + part[1] + ...), n4 groups of 4 elements, slices
-// stride4 groups apart.
+// out = dmax * (part[0] + part[1] + ...) (without dmax: the sum), n4 groups of
+// 4 elements, slices stride4 groups apart.
 template <typename E>
 __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restrict__ part, int slices, int64_t stride4,
                                                           int64_t n4, const float* __restrict__ dmax, E* __restrict__ out) {
@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restri
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
-    float m = 0.f;
-    for (int i = threadIdx.x; i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
+    float m = dmax ? 0.f : 1.f;
+    for (int i = threadIdx.x; dmax && i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (threadIdx.x == 0) scale_s = m;
@@ -209,7 +209,8 @@ cudaError_t split(const void* x, int64_t n, void* out, cudaStream_t s) {
                     static_cast<uint16_t*>(out));
 }
 
-// The bf16 planes of X [T][D] and W [V][D]: the data themselves, or split.
+// The bf16 planes of X [T][D] and W [V][D]: the data themselves, or split (of
+// W only where the products read planes of it).
 struct Planes {
   const uint16_t *x[kXentPlanes], *w[kXentPlanes];
   int n;
@@ -223,12 +224,44 @@ cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_
     return cudaSuccess;
   }
   XENT_STEP("xent_split", s, split(X, T * D, at<char>(ws, p.planes_x), s));
-  XENT_STEP("xent_split", s, split(W, V * D, at<char>(ws, p.planes_w), s));
+  if (!p.thin) XENT_STEP("xent_split", s, split(W, V * D, at<char>(ws, p.planes_w), s));
   for (int i = 0; i < kXentPlanes; ++i) {
     out->x[i] = at<uint16_t>(ws, p.planes_x) + i * T * D;
     out->w[i] = at<uint16_t>(ws, p.planes_w) + i * V * D;
   }
   return cudaSuccess;
+}
+
+cudaError_t run_join(const float2* stats, int parts, int64_t T, const int64_t* targets, int64_t V, const float* zt,
+                            float* loss, float* lse, int* status, cudaStream_t s) {
+  XENT_STEP("xent_join", s,
+            launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(32 * kJoinWarps), 0, s, stats,
+                       parts, T, targets, V, zt, loss, lse, status));
+  return cudaSuccess;
+}
+
+cudaError_t run_reduce(const float* part, int slices, int64_t stride, int64_t n, const float* dmax, int is_bf16,
+                              void* out, cudaStream_t s) {
+  const float4* p4 = reinterpret_cast<const float4*>(part);
+  const dim3 grid(grid_for(n / 4));
+  XENT_STEP("xent_reduce", s,
+            is_bf16 ? launch_pdl(xent_reduce_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p4, slices, stride / 4, n / 4,
+                                 dmax, static_cast<__nv_bfloat16*>(out))
+                    : launch_pdl(xent_reduce_kernel<float>, grid, dim3(256), 0, s, p4, slices, stride / 4, n / 4, dmax,
+                                 static_cast<float*>(out)));
+  return cudaSuccess;
+}
+
+// The operands of the logits of ids [0, n) of W for up to kXentThinMax rows.
+bool thin_maps(XentThin* h, const void* W, const Planes& pl, int64_t T, int64_t n, int64_t D) {
+  h->f32 = pl.n > 1;
+  h->T = static_cast<int>(T);
+  h->M = static_cast<int>(n);
+  h->K = static_cast<int>(D);
+  h->slices = 1;
+  for (int i = 0; i < pl.n; ++i)
+    if (!make_operand_map(&h->map_b[i], pl.x[i], T, D, D, xent_thin_columns(T))) return false;
+  return h->f32 ? make_output_map_f32(&h->map_w, const_cast<void*>(W), n, D, D) : make_operand_map(&h->map_w, W, n, D, D, 128);
 }
 
 // out [M][N] = dmax * acc (is_bf16: rounded once), through fp32 partial sums
@@ -252,16 +285,12 @@ cudaError_t product_out(XentGemm& g, void* out, float* part, int is_bf16, uint64
   g.epi = kXentOutF32;
   g.slice_rows = rows;
   XENT_STEP(phase, s, launch_xent_gemm(g, wait_ns, s));
-  const int64_t n4 = int64_t(g.M) * g.N / 4, stride4 = rows * g.N / 4;
-  if (is_bf16)
-    XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<__nv_bfloat16>, dim3(grid_for(n4)), dim3(256), 0, s,
-                                           reinterpret_cast<const float4*>(part), slices, stride4, n4, dmax,
-                                           static_cast<__nv_bfloat16*>(out)));
-  else
-    XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s,
-                                           reinterpret_cast<const float4*>(part), slices, stride4, n4, dmax,
-                                           static_cast<float*>(out)));
-  return cudaSuccess;
+  return run_reduce(part, slices, rows * g.N, int64_t(g.M) * g.N, dmax, is_bf16, out, s);
+}
+
+// Few enough rows for the form that streams W through registers.
+bool use_rows(int64_t T, int64_t D, int is_bf16) {
+  return T <= (is_bf16 ? 0 : 0) && (D + 63) / 64 * 64 * 4 <= kXentRowsSmem;
 }
 
 }  // namespace
@@ -275,12 +304,27 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
     return a;
   };
   const int planes = is_bf16 ? 1 : kXentPlanes, pairs = is_bf16 ? 1 : kXentPairs;
+  p.rows = use_rows(T, D, is_bf16);
+  if (p.rows) {
+    if (backward) {
+      const int64_t per = xent_rows_ids(D, V);
+      p.dz = take(size_t(V) * xent_rows_tp(T) * 4);
+      p.dx = take(size_t((V + per - 1) / per) * T * D * 4);
+    } else {
+      p.stats = take(size_t(xent_rows_parts(V)) * T * sizeof(float2));
+      p.zt = take(size_t(T) * 4);
+    }
+    p.total = off;
+    return p;
+  }
+  p.thin = T <= kXentThinMax;
   if (!is_bf16) {
     p.planes_x = take(size_t(T) * D * 2 * planes);
-    p.planes_w = take(size_t(V) * D * 2 * planes);
+    if (!p.thin) p.planes_w = take(size_t(V) * D * 2 * planes);
   }
   if (!backward) {
-    p.stats = take(size_t((V + kXentPart - 1) / kXentPart) * T * sizeof(float2));
+    const int64_t parts = p.thin ? xent_thin_parts(V) : (V + kXentPart - 1) / kXentPart;
+    p.stats = take(size_t(parts) * T * sizeof(float2));
     p.zt = take(size_t(T) * 4);
     p.total = off;
     return p;
@@ -295,10 +339,11 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
   p.dz_pitch = ceil_to(piece, 64);
   p.dmax = take(kXentDmaxParts * 4);
   p.dz = take(size_t(T) * p.dz_pitch * 2 * planes);
-  p.slices_x = xent_slices(static_cast<int>(p.dz_pitch), choose_slices(T, D, p.dz_pitch, pairs));
+  p.slices_x = p.thin ? xent_thin_slices(D, p.dz_pitch)
+                      : xent_slices(static_cast<int>(p.dz_pitch), choose_slices(T, D, p.dz_pitch, pairs));
   p.slices_w = xent_slices(static_cast<int>(T), choose_slices(piece, D, T, pairs));
-  p.dx_part = piece < V || p.slices_x > 1;
-  if (p.dx_part) p.dx = take(size_t(p.slices_x) * slice_rows(T) * D * 4);
+  p.dx_part = piece < V || p.slices_x > 1 || p.thin;
+  if (p.dx_part) p.dx = take(size_t(p.slices_x) * (p.thin ? T : slice_rows(T)) * D * 4);
   if (p.slices_w > 1) p.dw = take(size_t(p.slices_w) * slice_rows(piece) * D * 4);
   p.total = off;
   return p;
@@ -308,9 +353,25 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
                              int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
                              cudaStream_t s) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 0);
+  if (p.rows) {
+    float2* stats = at<float2>(ws, p.stats);
+    float* zt = at<float>(ws, p.zt);
+    XENT_STEP("xent_logits", s, launch_xent_rows_stats(X, W, targets, T, D, V, is_bf16, stats, zt, s));
+    return run_join(stats, xent_rows_parts(V), T, targets, V, zt, loss, lse, status, s);
+  }
   Planes pl;
   cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
   if (e != cudaSuccess) return e;
+  if (p.thin) {
+    XentThin h{};
+    if (!thin_maps(&h, W, pl, T, V, D)) return cudaErrorInvalidValue;
+    h.targets = targets;
+    h.V = V;
+    h.stats = at<float2>(ws, p.stats);
+    h.zt = at<float>(ws, p.zt);
+    XENT_STEP("xent_logits", s, launch_xent_thin_stats(h, wait_ns, s));
+    return run_join(h.stats, xent_thin_parts(V), T, targets, V, h.zt, loss, lse, status, s);
+  }
   XentGemm g{};
   for (int i = 0; i < pl.n; ++i)
     if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i], V, D, D))
@@ -328,17 +389,22 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
   g.zt = at<float>(ws, p.zt);
   XENT_STEP("xent_logits", s, launch_xent_gemm(g, wait_ns, s));
   const int parts = static_cast<int>((V + kXentPart - 1) / kXentPart);
-  XENT_STEP("xent_join", s,
-            launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
-                       static_cast<const float2*>(g.stats), parts, T, targets, V, static_cast<const float*>(g.zt), loss,
-                       lse, status));
-  return cudaSuccess;
+  return run_join(g.stats, parts, T, targets, V, g.zt, loss, lse, status, s);
 }
 
 cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,
                               const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
                               void* ws, uint64_t wait_ns, cudaStream_t s) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 1);
+  if (p.rows) {
+    float *dz = at<float>(ws, p.dz), *part = at<float>(ws, p.dx);
+    const int64_t per = xent_rows_ids(D, V);
+    if (xent_rows_tp(T) != T)  // the rows that dz is padded with
+      XENT_STEP("xent_dz", s, cudaMemsetAsync(dz, 0, size_t(V) * xent_rows_tp(T) * 4, s));
+    XENT_STEP("xent_dz", s, launch_xent_rows_dz(X, W, targets, lse, dloss, T, D, V, is_bf16, dz, s));
+    XENT_STEP("xent_dX_dW", s, launch_xent_rows_products(dz, X, W, T, D, V, is_bf16, part, dW, s));
+    return run_reduce(part, static_cast<int>((V + per - 1) / per), T * D, T * D, nullptr, is_bf16, dX, s);
+  }
   Planes pl;
   cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
   if (e != cudaSuccess) return e;
@@ -350,9 +416,24 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
   for (int i = 0; i < pl.n; ++i) dz[i] = at<uint16_t>(ws, p.dz) + i * T * p.dz_pitch;
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
     const int64_t vc = V - v0 < p.piece ? V - v0 : p.piece, vp = ceil_to(vc, 64);
+    const void* W0 = static_cast<const char*>(W) + v0 * D * es;
     // dz of the piece, from its logits computed again; columns vc .. vp are zeros.
     XentGemm g{};
-    for (int i = 0; i < pl.n; ++i)
+    if (p.thin) {
+      XentThin h{};
+      if (!thin_maps(&h, W0, pl, T, vc, D)) return cudaErrorInvalidValue;
+      h.targets = targets;
+      h.V = V;
+      h.col0 = v0;
+      h.lse = lse;
+      h.dloss = dloss;
+      h.dmax = dmax;
+      h.dz = reinterpret_cast<__nv_bfloat16*>(dz[0]);
+      h.pitch = p.dz_pitch;
+      h.dz_columns = vp;
+      XENT_STEP("xent_dz", s, launch_xent_thin_dz(h, wait_ns, s));
+    }
+    for (int i = 0; !p.thin && i < pl.n; ++i)
       if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i] + v0 * D, vc, D, D) ||
           !make_output_map_bf16(&g.map_out[i], dz[i], T, vp, p.dz_pitch))
         return cudaErrorInvalidValue;
@@ -369,7 +450,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g.lse = lse;
     g.dloss = dloss;
     g.dmax = dmax;
-    XENT_STEP("xent_dz", s, launch_xent_gemm(g, wait_ns, s));
+    if (!p.thin) XENT_STEP("xent_dz", s, launch_xent_gemm(g, wait_ns, s));
 
     // dW of the piece = dz^T X.
     g = XentGemm{};
@@ -389,6 +470,24 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
       return e;
 
     // dX += dz W over the piece.
+    if (p.thin) {
+      XentThin h{};
+      h.f32 = pl.n > 1;
+      h.T = static_cast<int>(T);
+      h.M = static_cast<int>(D);
+      h.K = static_cast<int>(vp);
+      h.slices = p.slices_x;
+      h.part = at<float>(ws, p.dx);
+      h.add = v0 > 0;
+      if (!(h.f32 ? make_output_map_f32(&h.map_w, const_cast<void*>(W0), vc, D, D) : make_operand_map(&h.map_w, W0, vc, D, D, 64)))
+        return cudaErrorInvalidValue;
+      for (int i = 0; i < pl.n; ++i)
+        if (!make_operand_map(&h.map_b[i], dz[i], T, vp, p.dz_pitch, xent_thin_columns(T))) return cudaErrorInvalidValue;
+      XENT_STEP("xent_dX", s, launch_xent_thin_dx(h, wait_ns, s));
+      if (v0 + vc < V) continue;
+      if ((e = run_reduce(h.part, p.slices_x, T * D, T * D, dmax, is_bf16, dX, s)) != cudaSuccess) return e;
+      continue;
+    }
     g = XentGemm{};
     for (int i = 0; i < pl.n; ++i)
       if (!operand_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch) ||
@@ -416,16 +515,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g.slice_rows = rows;
     XENT_STEP("xent_dX", s, launch_xent_gemm(g, wait_ns, s));
     if (v0 + vc < V) continue;
-    const int64_t n4 = T * D / 4, stride4 = rows * D / 4;
-    const float4* part = at<float4>(ws, p.dx);
-    if (is_bf16)
-      XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<__nv_bfloat16>, dim3(grid_for(n4)), dim3(256), 0, s, part,
-                                             p.slices_x, stride4, n4, static_cast<const float*>(dmax),
-                                             static_cast<__nv_bfloat16*>(dX)));
-    else
-      XENT_STEP("xent_reduce", s, launch_pdl(xent_reduce_kernel<float>, dim3(grid_for(n4)), dim3(256), 0, s, part,
-                                             p.slices_x, stride4, n4, static_cast<const float*>(dmax),
-                                             static_cast<float*>(dX)));
+    if ((e = run_reduce(at<float>(ws, p.dx), p.slices_x, rows * D, T * D, dmax, is_bf16, dX, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -1,0 +1,541 @@
+// xent_thin.cu — the products of the cross entropy over the vocabulary with W
+// for up to 64 rows of X, on the tensor cores with W's side as the 128 rows of
+// a tile and the rows of X (or of dz) as its N = 32 or 64 columns.
+//
+// With so few rows each product is a pass over W, bound by HBM: 256 x 256
+// tiles would multiply mostly nothing, and planes of an fp32 W written to
+// memory beforehand would cost more traffic than W. Here W is read once, by
+// TMA, in its own type; fp32 tiles are split into their three bf16 planes on
+// the way from one part of shared memory to another.
+//
+//   logits, dz : A = W [V][D] K-major, B = X planes [T][D], tiles of 128 ids
+//   dX^T       : A = W MN-major (128 columns of W), B = dz planes [T][V], the
+//                ids cut into slices, each its own fp32 partial sum [T][D]
+//
+// One CTA per SM:
+//   warp 0       : TMA of W (fp32: tiles of 32 K; bf16: of 64 K, with B)
+//   warp 1       : issues the MMAs
+//   warp 2       : fp32: TMA of the B planes
+//   warps 4..11  : fp32: convert, 256 threads, 64 K of 128 rows at a time
+//   warps 12..15 : epilogue
+// Per 64 K of fp32 a tile is 32 KB from HBM (about 1400 clocks of an SM's
+// share), 768 clocks of MMAs at N = 64 (six plane pairs) and about 650 clocks
+// of shared memory for the conversion, so HBM stays the bound.
+//
+// The high planes' product has an accumulator of its own: the five small ones
+// would each time cut off what the large sum shifts out. Runs of sums as in
+// xent_gemm.cu: 512 fp32 products, 1024 of bf16 for the logits' statistics.
+#include "gemm_common.cuh"
+#include "train.h"
+
+#include <atomic>
+#include <cstring>
+
+namespace tpmlp {
+
+namespace {
+
+constexpr int kTThreads = 512;
+constexpr int kConvWarp0 = 4, kConvWarps = 8, kEpiWarp0 = 12;
+constexpr uint32_t kRawBytes = 128 * 32 * 4;    // fp32: 128 x 32 of W
+constexpr uint32_t kPlaneBytes = 128 * 64 * 2;  // bf16: 128 x 64
+
+enum ThinKind : int { kThinStats = 0, kThinGrad = 1, kThinDx = 2 };
+
+template <bool F32, int N>
+struct TCfg {
+  static constexpr int PL = F32 ? kXentPlanes : 1;
+  static constexpr int RAW = F32 ? 4 : 0;                             // stages of raw W
+  static constexpr uint32_t B_BYTES = N * 64 * 2;                     // one plane of B, 64 K
+  static constexpr uint32_t STAGE = PL * (kPlaneBytes + B_BYTES);     // operands of 64 K
+  static constexpr int STAGES = F32 ? 2 : 8;
+  static constexpr uint32_t ACC = F32 ? 2 * N : N;                    // columns of one accumulator (large, small)
+  static constexpr uint32_t TMEM = 2 * ACC < 32 ? 32 : 2 * ACC;
+  static constexpr size_t SMEM = 1024 + size_t(RAW) * kRawBytes + size_t(STAGES) * STAGE + 512;
+};
+
+struct TParams {
+  XentThin g;
+  int tiles_m, slices, kb_per_slice, k_blocks, tiles;
+  int run;
+  uint64_t wait_ns;
+  int* status;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The reductions of 32 columns over the 32 lanes: lane l ends up with column
+// l's. 31 shuffles: each step halves the columns that a lane still holds.
+template <bool MAX>
+__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+      const float got = __shfl_xor_sync(0xffffffffu, give, o);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
+
+// Whether `ok` holds in all 128 epilogue threads.
+__device__ __forceinline__ bool all_of_epilogue(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+template <bool F32, int N, int KIND>
+__global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constant__ TParams p) {
+  using C = TCfg<F32, N>;
+  constexpr bool MN = KIND == kThinDx;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_stage = smem;                                // [STAGES][planes of A, planes of B]
+  uint8_t* s_raw = smem + C::STAGES * C::STAGE;           // [RAW]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_raw + C::RAW * kRawBytes);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* raw_full = empty + C::STAGES;
+  uint64_t* raw_empty = raw_full + 4;
+  uint64_t* acc_full = raw_empty + 4;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ int64_t s_target[64];
+  __shared__ float s_lse[64], s_rs[64], s_ref[4][64], s_sum[4][64];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full + s, F32 ? 1 + kConvWarps : 1);  // B's (or all) bytes; the converters
+      mbar_init(empty + s, 1);                        // commit of the MMAs that read it
+    }
+    for (int s = 0; s < C::RAW; ++s) {
+      mbar_init(raw_full + s, 1);
+      mbar_init(raw_empty + s, kConvWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  const WaitGuard guard{abort_flag, p.wait_ns, p.status};
+  // Tile -> rows m0 .. of the A side, K blocks k0 .. k0 + kbs.
+  auto decode = [&](int tile, int& slice, int& m0, int& k0, int& kbs) {
+    slice = tile / p.tiles_m;
+    m0 = (tile - slice * p.tiles_m) * 128;
+    k0 = slice * p.kb_per_slice;
+    kbs = min(p.kb_per_slice, p.k_blocks - k0);
+  };
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA of W (and, bf16, of B)
+      constexpr int ST = F32 ? C::RAW : C::STAGES;
+      uint64_t* f = F32 ? raw_full : full;
+      uint64_t* e = F32 ? raw_empty : empty;
+      int st = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      const uint64_t keep = l2_policy(1), stream = l2_policy(0);
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        int slice, m0, k0, kbs;
+        decode(tile, slice, m0, k0, kbs);
+        for (int q = 0; ok && q < kbs * (F32 ? 2 : 1); ++q) {
+          if (!(ok = wait_bounded(e + st, phase ^ 1u, guard, kSiteProducer))) break;
+          issued |= 1u << st;
+          parity = (parity & ~(1u << st)) | (phase << st);
+          if constexpr (F32) {
+            // Four boxes of 32 x 32, 4 KB each.
+            mbar_arrive_expect_tx(f + st, kRawBytes);
+            uint8_t* dst = s_raw + st * kRawBytes;
+            const int kx = k0 * 64 + q * 32;
+            for (int b = 0; b < 4; ++b)
+              if constexpr (MN)
+                tma_load_2d_hint(dst + b * 4096, &p.g.map_w, m0 + 32 * b, kx, f + st, stream);
+              else
+                tma_load_2d_hint(dst + b * 4096, &p.g.map_w, kx, m0 + 32 * b, f + st, stream);
+          } else {
+            mbar_arrive_expect_tx(f + st, C::STAGE);
+            uint8_t* dst = s_stage + st * C::STAGE;
+            const int kx = (k0 + q) * 64;
+            if constexpr (MN) {
+              tma_load_2d_hint(dst, &p.g.map_w, m0, kx, f + st, stream);
+              tma_load_2d_hint(dst + kMnChunkBytes, &p.g.map_w, m0 + 64, kx, f + st, stream);
+            } else {
+              tma_load_2d_hint(dst, &p.g.map_w, kx, m0, f + st, stream);
+            }
+            tma_load_2d_hint(dst + kPlaneBytes, &p.g.map_b[0], kx, 0, f + st, keep);
+          }
+          if (++st == ST) st = 0, phase ^= 1u;
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < ST; ++s)
+          if (issued >> s & 1u) wait_drain(f + s, (parity >> s) & 1u, p.wait_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer
+      const uint32_t idesc = idesc_bf16_f32(128, N, MN ? 1 : 0, 0);
+      int st = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        int slice, m0, k0, kbs;
+        decode(tile, slice, m0, k0, kbs);
+        for (int r = 0; ok && r < kbs; r += p.run) {
+          if (!(ok = wait_bounded(acc_empty + acc, acc_phase ^ 1u, guard, kSiteMmaAcc))) break;
+          tc_fence_after_sync();
+          const uint32_t d_large = tmem_base + static_cast<uint32_t>(acc) * C::ACC;
+          const uint32_t d_small = d_large + N;
+          const int end = min(kbs, r + p.run);
+          for (int q = r; q < end; ++q) {
+            if (!(ok = wait_bounded(full + st, phase, guard, kSiteMmaFull))) break;
+            tc_fence_after_sync();
+            const uint32_t a0 = smem_addr(s_stage + st * C::STAGE), b0 = a0 + C::PL * kPlaneBytes;
+            auto mma = [&](uint32_t d, int pa, int pb, bool first) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_bf16(d, operand_desc(a0 + pa * kPlaneBytes, k, MN), operand_desc(b0 + pb * C::B_BYTES, k, false),
+                            idesc, (!first || k != 0) ? 1u : 0u);
+            };
+            if constexpr (F32) {
+              mma(d_small, 1, 1, q == r);
+              mma(d_small, 0, 2, false);
+              mma(d_small, 2, 0, false);
+              mma(d_small, 0, 1, false);
+              mma(d_small, 1, 0, false);
+            }
+            mma(d_large, 0, 0, q == r);
+            tc_commit(empty + st);
+            if (++st == C::STAGES) st = 0, phase ^= 1u;
+          }
+          if (!ok) break;
+          tc_commit(acc_full + acc);
+          if (++acc == 2) acc = 0, acc_phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        tc_commit(drain);
+        wait_drain(drain, 0, p.wait_ns);
+      }
+    }
+  } else if (warp == 2) {
+    if (F32 && lane == 0) {
+      // ---------------- TMA of the B planes
+      int st = 0;
+      uint32_t phase = 0;
+      const uint64_t keep = l2_policy(1);
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        int slice, m0, k0, kbs;
+        decode(tile, slice, m0, k0, kbs);
+        for (int q = 0; ok && q < kbs; ++q) {
+          if (!(ok = wait_bounded(empty + st, phase ^ 1u, guard, kSiteProducer))) break;
+          mbar_arrive_expect_tx(full + st, C::PL * C::B_BYTES);
+          uint8_t* dst = s_stage + st * C::STAGE + C::PL * kPlaneBytes;
+          for (int b = 0; b < C::PL; ++b)
+            tma_load_2d_hint(dst + b * C::B_BYTES, &p.g.map_b[b], (k0 + q) * 64, 0, full + st, keep);
+          if (++st == C::STAGES) st = 0, phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // The stage barriers also count the converters, which stop too: give copies in flight time to land.
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp >= kConvWarp0 && warp < kEpiWarp0) {
+    if constexpr (F32) {
+      // ---------------- converters: fp32 tiles into planes
+      const int tid = threadIdx.x - kConvWarp0 * 32;
+      int st = 0, rs = 0;
+      uint32_t phase = 0, raw_phase = 0;
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        int slice, m0, k0, kbs;
+        decode(tile, slice, m0, k0, kbs);
+        for (int q = 0; ok && q < kbs; ++q) {
+          ok = __all_sync(0xffffffffu, wait_bounded(empty + st, phase ^ 1u, guard, kSiteProducer));
+          if (!ok) break;
+          uint8_t* planes = s_stage + st * C::STAGE;
+          for (int half = 0; half < 2; ++half) {
+            ok = __all_sync(0xffffffffu, wait_bounded(raw_full + rs, raw_phase, guard, kSiteMmaFull));
+            if (!ok) break;
+            const uint8_t* raw = s_raw + rs * kRawBytes;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+              // 512 items of 8 floats; neighbouring threads take neighbouring lines of 128 bytes.
+              const int item = tid + it * 256;
+              const uint8_t* src;
+              uint8_t* dst;
+              int line;  // swizzle phase of the source's two 16-byte chunks
+              int c;     // first of them
+              if constexpr (MN) {
+                const int v = item & 31, grp = item >> 5;  // id of this half, 8 columns
+                src = raw + (grp >> 2) * 4096 + v * 128;
+                line = v & 7;
+                c = (grp & 3) * 2;
+                const int k = half * 32 + v;
+                dst = planes + (grp >> 3) * kMnChunkBytes + k * 128 + (((grp & 7) ^ (k & 7)) << 4);
+              } else {
+                const int r = item & 127, grp = item >> 7;  // row, 8 of this half's 32 K
+                src = raw + (r >> 5) * 4096 + (r & 31) * 128;
+                line = r & 7;
+                c = grp * 2;
+                dst = planes + r * 128 + (((half * 4 + grp) ^ (r & 7)) << 4);
+              }
+              const float4 x = *reinterpret_cast<const float4*>(src + ((c ^ line) << 4));
+              const float4 y = *reinterpret_cast<const float4*>(src + (((c + 1) ^ line) << 4));
+              float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int pl = 0; pl < C::PL; ++pl) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  h[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+                  if (pl + 1 < C::PL) {
+                    f[2 * i] -= __uint_as_float(h[i] << 16);
+                    f[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+                  }
+                }
+                *reinterpret_cast<uint4*>(dst + pl * kPlaneBytes) = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_empty + rs);
+            if (++rs == C::RAW) rs = 0, raw_phase ^= 1u;
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();  // the tensor core reads what these threads wrote
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + st);
+          if (++st == C::STAGES) st = 0, phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ---------------- epilogue: lane = row of the tile's quarter, columns = rows of X
+    const int quarter = warp & 3, et = threadIdx.x - kEpiWarp0 * 32;
+    if constexpr (KIND != kThinDx) {
+      float dmax = 0.f;
+      if constexpr (KIND == kThinGrad) {
+        for (int i = 0; i < kXentDmaxParts; ++i) dmax = fmaxf(dmax, p.g.dmax[i]);
+      }
+      if (et < 64) {
+        const bool in = et < p.g.T;
+        const int64_t t = in ? p.g.targets[et] : -1;
+        const bool counts = t >= 0 && t < p.g.V;
+        s_target[et] = counts ? t - p.g.col0 : -1;
+        if constexpr (KIND == kThinGrad) {
+          s_lse[et] = in ? p.g.lse[et] : 0.f;
+          s_rs[et] = counts && dmax > 0.f ? p.g.dloss[et] * (1.f / dmax) : 0.f;
+        }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    float run_max = -INFINITY, run_sum = 0.f;  // kThinStats: of row et of X, in units of log2
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+      int slice, m0, k0, kbs;
+      decode(tile, slice, m0, k0, kbs);
+      float sum[N / 32][32];
+#pragma unroll
+      for (int c = 0; c < N / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+      for (int r = 0; r < kbs; r += p.run) {
+        // The four warps go on, or give up, together: they meet at barriers below.
+        ok = all_of_epilogue(wait_bounded(acc_full + acc, acc_phase, guard, kSiteEpilogue));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t t0 = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc) * C::ACC;
+#pragma unroll
+        for (int c = 0; c < static_cast<int>(C::ACC / 32); ++c) {
+          float v[32];
+          __syncwarp();
+          tmem_ld_32cols(t0 + 32 * c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c % (N / 32)][i] += v[i];
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(acc_empty + acc);
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
+      }
+      if (!ok) break;
+      const int64_t m = m0 + quarter * 32 + lane;  // id, or column of dX
+      if constexpr (KIND == kThinDx) {
+        if (m < p.g.M) {
+          float* out = p.g.part + int64_t(slice) * p.g.T * p.g.M + m;
+#pragma unroll
+          for (int c = 0; c < N / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i < p.g.T) {
+                float* o = out + int64_t(32 * c + i) * p.g.M;
+                *o = p.g.add ? *o + sum[c][i] : sum[c][i];
+              }
+        }
+      } else if constexpr (KIND == kThinGrad) {
+        if (m < p.g.dz_columns) {
+          __nv_bfloat16* dz = p.g.dz + m;
+#pragma unroll
+          for (int c = 0; c < N / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int t = 32 * c + i;
+              if (t >= p.g.T) continue;
+              const float rs = s_rs[t];
+              float d = F32 ? expf(sum[c][i] - s_lse[t]) : exp2_approx((sum[c][i] - s_lse[t]) * kXentLog2e);
+              if (m == s_target[t]) d -= 1.f;
+              d = rs != 0.f && m < p.g.M ? d * rs : 0.f;
+#pragma unroll
+              for (int pl = 0; pl < C::PL; ++pl) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(d);
+                dz[(int64_t(pl) * p.g.T + t) * p.g.pitch] = h;
+                d -= __bfloat162float(h);
+              }
+            }
+        }
+      } else {
+        // (max, sum of exponentials) of each column over the tile's 128 ids.
+#pragma unroll
+        for (int c = 0; c < N / 32; ++c) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (m == s_target[32 * c + i] && 32 * c + i < p.g.T) p.g.zt[32 * c + i] = sum[c][i];
+            sum[c][i] = m < p.g.M ? sum[c][i] * kXentLog2e : -INFINITY;
+            v[i] = sum[c][i];
+          }
+          s_ref[quarter][32 * c + lane] = reduce_columns<true>(v, lane);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < N / 32; ++c) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int t = 32 * c + i;
+            float ref = fmaxf(fmaxf(s_ref[0][t], s_ref[1][t]), fmaxf(s_ref[2][t], s_ref[3][t]));
+            if (ref == -INFINITY) ref = 0.f;
+            v[i] = exp2_approx(sum[c][i] - ref);
+          }
+          s_sum[quarter][32 * c + lane] = reduce_columns<false>(v, lane);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (et < N) {
+          const float top_tile = fmaxf(fmaxf(s_ref[0][et], s_ref[1][et]), fmaxf(s_ref[2][et], s_ref[3][et]));
+          const float add = (s_sum[0][et] + s_sum[1][et]) + (s_sum[2][et] + s_sum[3][et]);
+          const float top = fmaxf(run_max, top_tile);
+          const float base = top == -INFINITY ? 0.f : top;
+          run_sum = run_sum * exp2_approx(run_max - base) + add * exp2_approx((top_tile == -INFINITY ? 0.f : top_tile) - base);
+          run_max = top;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // s_ref and s_sum are free again
+      }
+    }
+    if constexpr (KIND == kThinStats) {
+      if (et < p.g.T) p.g.stats[int64_t(blockIdx.x) * p.g.T + et] = make_float2(run_max, run_sum);
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, C::TMEM);
+  }
+}
+
+template <bool F32, int N, int KIND>
+cudaError_t launch_kind(const TParams& p, cudaStream_t s) {
+  using C = TCfg<F32, N>;
+  auto kern = thin_kernel<F32, N, KIND>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
+  if (e != cudaSuccess) return e;
+  const int grid = p.tiles < num_sms() ? p.tiles : num_sms();
+  return launch_pdl(kern, dim3(grid), dim3(kTThreads), C::SMEM, s, p);
+}
+
+template <bool F32, int N>
+cudaError_t launch_n(const TParams& p, int kind, cudaStream_t s) {
+  return kind == kThinStats  ? launch_kind<F32, N, kThinStats>(p, s)
+         : kind == kThinGrad ? launch_kind<F32, N, kThinGrad>(p, s)
+                             : launch_kind<F32, N, kThinDx>(p, s);
+}
+
+cudaError_t launch_thin(const XentThin& g, int kind, uint64_t wait_ns, cudaStream_t s) {
+  TParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = g;
+  p.tiles_m = static_cast<int>((g.M + 127) / 128);
+  p.k_blocks = static_cast<int>((g.K + 63) / 64);
+  p.slices = g.slices;
+  p.kb_per_slice = (p.k_blocks + g.slices - 1) / g.slices;
+  p.slices = (p.k_blocks + p.kb_per_slice - 1) / p.kb_per_slice;
+  p.tiles = p.tiles_m * p.slices;
+  p.run = g.f32 ? 8 : kind == kThinStats ? 16 : p.k_blocks;
+  p.wait_ns = wait_ns;
+  p.status = device_status_word();
+  if (!p.status) return cudaErrorInvalidSymbol;
+  if (g.T <= 32) return g.f32 ? launch_n<true, 32>(p, kind, s) : launch_n<false, 32>(p, kind, s);
+  return g.f32 ? launch_n<true, 64>(p, kind, s) : launch_n<false, 64>(p, kind, s);
+}
+
+}  // namespace
+
+int xent_thin_columns(int64_t T) { return T <= 32 ? 32 : 64; }
+
+int xent_thin_parts(int64_t V) {
+  const int64_t tiles = (V + 127) / 128;
+  return static_cast<int>(tiles < num_sms() ? tiles : num_sms());
+}
+
+int xent_thin_slices(int64_t D, int64_t K) {
+  const int64_t tiles = (D + 127) / 128, kb = (K + 63) / 64;
+  // Two tiles' worth for every SM, of at least eight K blocks each.
+  int64_t s = (2 * int64_t(num_sms()) + tiles - 1) / tiles;
+  if (s > kb / 8) s = kb / 8;
+  if (s < 1) s = 1;
+  const int64_t per = (kb + s - 1) / s;
+  return static_cast<int>((kb + per - 1) / per);
+}
+
+cudaError_t launch_xent_thin_stats(const XentThin& g, uint64_t wait_ns, cudaStream_t s) {
+  return launch_thin(g, kThinStats, wait_ns, s);
+}
+cudaError_t launch_xent_thin_dz(const XentThin& g, uint64_t wait_ns, cudaStream_t s) {
+  return launch_thin(g, kThinGrad, wait_ns, s);
+}
+cudaError_t launch_xent_thin_dx(const XentThin& g, uint64_t wait_ns, cudaStream_t s) {
+  return launch_thin(g, kThinDx, wait_ns, s);
+}
+
+}  // namespace tpmlp

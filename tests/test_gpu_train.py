@@ -119,6 +119,36 @@ def test_xent_against_64_bits(tp, T, D, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,V", [
+    (1, 1000, 5000), (2, 72, 15), (3, 4104, 700), (4, 64, 16), (5, 8, 17), (7, 520, 2049), (8, 1032, 4000), (9, 72, 64),
+    (16, 4096, 300), (17, 256, 1000), (31, 40, 129), (32, 768, 3000), (6, 12000, 90), (32, 6400, 200), (2, 60000, 40),
+])
+def test_xent_of_a_few_rows(tp, T, D, V, dtype):
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + D + V)
+    a = _check_xent(tp, X, W, t, dloss, dtype)
+    b = _check_xent(tp, X, W, t, dloss, dtype)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_xent_of_a_few_rows_that_do_not_count(tp, dtype):
+    X, W, t, dloss = _xent_inputs(6, 64, 300, dtype, seed=18, masked=0.0)
+    t[1], t[4], dloss[1], dloss[4] = -100, 300, float("nan"), float("inf")
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    with pytest.raises(tp.TpmlpError) as e:
+        tp.tpmlp_check_status()
+    assert e.value.code == tp.TPMLP_ERR_BOUNDS
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, dloss)
+    assert bool((loss[[1, 4]] == 0).all()) and bool(torch.isfinite(lse).all())
+    assert bool((dX[[1, 4]] == 0).all()) and bool(torch.isfinite(dW).all())
+    keep = [0, 2, 3, 5]
+    loss2, lse2 = tp.tpmlp_xent_forward(X[keep], W, t[keep])
+    dX2, dW2 = tp.tpmlp_xent_backward(X[keep], W, t[keep], lse2, dloss[keep])
+    assert torch.equal(loss2, loss[keep]) and torch.equal(dX2, dX[keep]) and torch.equal(dW2, dW)
+    tp.tpmlp_check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_xent_in_pieces_of_the_vocabulary(tp, dtype):
     # 34000 rows: 2^28 / 34000 < 8192 columns a piece; 9000 ids make two, the second ragged.
     X, W, t, dloss = _xent_inputs(34000, 16, 9000, dtype, seed=5)
