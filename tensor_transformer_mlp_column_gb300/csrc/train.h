@@ -111,7 +111,7 @@ struct XentGemm {
 int xent_slices(int K, int slices);
 cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s);
 
-// The products with W for up to kXentThinMax rows of X (xent_thin.cu).
+// The products with W for up to kXentThinMax rows of X at a time (xent_thin.cu).
 constexpr int kXentThinMax = 64;
 struct XentThin {
   CUtensorMap map_w;                // W: fp32, make_output_map_f32 (32 x 32 boxes); bf16, make_operand_map (K-major: 128
@@ -125,9 +125,10 @@ struct XentThin {
   float2* stats;                    // [xent_thin_parts(M)][T]
   float* zt;
   const float *lse, *dloss, *dmax;
-  __nv_bfloat16* dz;                // planes [T][pitch]
-  int64_t pitch, dz_columns;        // columns of dz's rows, and how many of them are written (zeros from M on)
-  float* part;                      // dX: [slices][T][M]
+  __nv_bfloat16* dz;                // rows [T][pitch] of planes that are `plane` apart
+  int64_t plane, pitch, dz_columns; // of dz's columns dz_columns are written (zeros from M on)
+  float* part;                      // dX: rows [T][M] of slices that are part_rows rows apart
+  int64_t part_rows;
   int add;                          // dX: add to part
 };
 int xent_thin_columns(int64_t T);
@@ -137,22 +138,8 @@ cudaError_t launch_xent_thin_stats(const XentThin& g, uint64_t wait_ns, cudaStre
 cudaError_t launch_xent_thin_dz(const XentThin& g, uint64_t wait_ns, cudaStream_t s);
 cudaError_t launch_xent_thin_dx(const XentThin& g, uint64_t wait_ns, cudaStream_t s);
 
-// The same for a few rows of X (xent_rows.cu), bound by HBM.
-constexpr int64_t kXentRowsSmem = 200 * 1024;  // X in fp32 in shared memory
-constexpr int kXentRowsMax = 32;
-int xent_rows_tp(int64_t T);                  // rows that dz [V][tp] is laid out for; rows T .. tp hold zeros
-int xent_rows_parts(int64_t V);               // (max, sum) parts of a row
-int64_t xent_rows_ids(int64_t D, int64_t V);  // ids of a slice of dX's sum
-cudaError_t launch_xent_rows_stats(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
-                                   int is_bf16, float2* stats, float* zt, cudaStream_t s);
-cudaError_t launch_xent_rows_dz(const void* X, const void* W, const int64_t* targets, const float* lse, const float* dloss,
-                                int64_t T, int64_t D, int64_t V, int is_bf16, float* dz, cudaStream_t s);
-// part [slices][T][D]: dX's slices; dW: the whole.
-cudaError_t launch_xent_rows_products(const float* dz, const void* X, const void* W, int64_t T, int64_t D, int64_t V,
-                                      int is_bf16, float* part, void* dW, cudaStream_t s);
-
 struct XentPlan {
-  bool rows, thin;            // the forms for a few rows, for up to kXentThinMax
+  bool thin;                  // the products with W by groups of kXentThinMax rows
   size_t planes_x, planes_w;  // fp32: bf16 planes [3][T][D], [3][V][D]
   size_t stats, zt;           // forward
   size_t dmax, dz, dx, dw;    // backward

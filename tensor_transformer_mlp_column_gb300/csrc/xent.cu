@@ -40,21 +40,25 @@ namespace {
   } while (0)
 
 // Row t's parts joined: lse = (M + log2 sum_i s_i 2^(m_i - M)) / log2 e. A CTA
-// takes 32 rows, warp w the parts w, w + 16, ..., joined in the warps' order.
+// takes R rows, its warps (and the lanes that share a row) every so many parts
+// each, joined in a fixed order.
 // The last additions are in fp64: M is in units of log2, where a rounding to
 // fp32 weighs more than in lse, and a target that is nearly certain leaves a
 // loss far below lse, which the fp32 difference would lose. log2 e is the same
 // fp32 constant that scaled the logits.
+// R = 4 rows a CTA where there are few rows: 128 threads share a row's parts.
 constexpr int kJoinWarps = 16;
+template <int R>
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2* __restrict__ stats, int parts, int64_t T,
                                                                     const int64_t* __restrict__ targets, int64_t V,
                                                                     const float* __restrict__ zt, float* __restrict__ loss,
                                                                     float* __restrict__ lse, int* status) {
-  __shared__ float2 red[kJoinWarps][32];
+  constexpr int S = 32 / R;  // lanes that share a row
+  __shared__ float2 red[kJoinWarps][R];
   pdl_wait();
   pdl_launch_dependents();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int64_t t = int64_t(blockIdx.x) * 32 + l;
+  const int64_t t = int64_t(blockIdx.x) * R + l % R;
   float m = -INFINITY, s = 0.f;
   auto add = [&](float2 p) {
     const float top = fmaxf(m, p.x);
@@ -66,11 +70,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   const float z = target >= 0 && target < V ? zt[t] : 0.f;
   if (t < T) {
 #pragma unroll 8
-    for (int i = w; i < parts; i += kJoinWarps) add(stats[int64_t(i) * T + t]);
+    for (int i = w * S + l / R; i < parts; i += kJoinWarps * S) add(stats[int64_t(i) * T + t]);
   }
-  red[w][l] = make_float2(m, s);
+#pragma unroll
+  for (int o = R; o < 32; o <<= 1)
+    add(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+  if (l < R) red[w][l] = make_float2(m, s);
   __syncthreads();
-  if (w != 0 || t >= T) return;
+  if (w != 0 || l >= R || t >= T) return;
   for (int i = 1; i < kJoinWarps; ++i) add(red[i][l]);
   const double v = (double(m) + double(log2f(s))) * (1.0 / double(kXentLog2e));
   if (target >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkTarget);
@@ -122,8 +129,8 @@ __global__ void __launch_bounds__(256) xent_split_kernel(const float* __restrict
   }
 }
 
-// out = dmax * (part[0] + part[1] + ...) (without dmax: the sum), n4 groups of
-// 4 elements, slices stride4 groups apart.
+// out = dmax * (part[0] + part[1] + ...), n4 groups of 4 elements, slices
+// stride4 groups apart.
 template <typename E>
 __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restrict__ part, int slices, int64_t stride4,
                                                           int64_t n4, const float* __restrict__ dmax, E* __restrict__ out) {
@@ -131,8 +138,8 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restri
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
-    float m = dmax ? 0.f : 1.f;
-    for (int i = threadIdx.x; dmax && i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
+    float m = 0.f;
+    for (int i = threadIdx.x; i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (threadIdx.x == 0) scale_s = m;
@@ -234,9 +241,11 @@ cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_
 
 cudaError_t run_join(const float2* stats, int parts, int64_t T, const int64_t* targets, int64_t V, const float* zt,
                             float* loss, float* lse, int* status, cudaStream_t s) {
+  const bool few = T < 2048;
+  const dim3 grid(static_cast<unsigned>(few ? (T + 3) / 4 : (T + 31) / 32));
   XENT_STEP("xent_join", s,
-            launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(32 * kJoinWarps), 0, s, stats,
-                       parts, T, targets, V, zt, loss, lse, status));
+            launch_pdl(few ? xent_join_kernel<4> : xent_join_kernel<32>, grid, dim3(32 * kJoinWarps), 0, s, stats, parts, T,
+                       targets, V, zt, loss, lse, status));
   return cudaSuccess;
 }
 
@@ -252,15 +261,16 @@ cudaError_t run_reduce(const float* part, int slices, int64_t stride, int64_t n,
   return cudaSuccess;
 }
 
-// The operands of the logits of ids [0, n) of W for up to kXentThinMax rows.
-bool thin_maps(XentThin* h, const void* W, const Planes& pl, int64_t T, int64_t n, int64_t D) {
+// The operands of the logits of ids [0, n) of W for the group of rows from t0.
+bool thin_maps(XentThin* h, const void* W, const Planes& pl, int64_t t0, int64_t T, int64_t n, int64_t D) {
+  const int64_t rows = T - t0 < kXentThinMax ? T - t0 : kXentThinMax;
   h->f32 = pl.n > 1;
-  h->T = static_cast<int>(T);
+  h->T = static_cast<int>(rows);
   h->M = static_cast<int>(n);
   h->K = static_cast<int>(D);
   h->slices = 1;
   for (int i = 0; i < pl.n; ++i)
-    if (!make_operand_map(&h->map_b[i], pl.x[i], T, D, D, xent_thin_columns(T))) return false;
+    if (!make_operand_map(&h->map_b[i], pl.x[i] + t0 * D, rows, D, D, xent_thin_columns(rows))) return false;
   return h->f32 ? make_output_map_f32(&h->map_w, const_cast<void*>(W), n, D, D) : make_operand_map(&h->map_w, W, n, D, D, 128);
 }
 
@@ -288,12 +298,18 @@ cudaError_t product_out(XentGemm& g, void* out, float* part, int is_bf16, uint64
   return run_reduce(part, slices, rows * g.N, int64_t(g.M) * g.N, dmax, is_bf16, out, s);
 }
 
-// Few enough rows for the form that streams W through registers.
-bool use_rows(int64_t T, int64_t D, int is_bf16) {
-  return T <= (is_bf16 ? 0 : 0) && (D + 63) / 64 * 64 * 4 <= kXentRowsSmem;
-}
-
 }  // namespace
+
+// Whether the products with W go by groups of kXentThinMax rows, each a pass
+// over W. bf16: one group (64 rows, V = 128000, D = 1024: the logits 54 us
+// either way, 32 rows 50 against 59). fp32, where the other form splits W into
+// planes in memory first: up to three groups of a W that is more than a few
+// launches' worth (V = 128000, D = 1024, a whole step: 64 rows 0.47 against
+// 1.46 ms, 128 rows 0.86 / 1.46, 192 rows 1.23 / 1.6, 256 rows 1.61 / 1.64; V =
+// 3000, D = 256, 128 rows: 150 us against 126).
+static bool use_thin(int64_t T, int64_t D, int64_t V, int is_bf16) {
+  return T <= kXentThinMax || (!is_bf16 && T <= 3 * kXentThinMax && V * D >= (int64_t(1) << 24));
+}
 
 XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
   XentPlan p{};
@@ -304,20 +320,7 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
     return a;
   };
   const int planes = is_bf16 ? 1 : kXentPlanes, pairs = is_bf16 ? 1 : kXentPairs;
-  p.rows = use_rows(T, D, is_bf16);
-  if (p.rows) {
-    if (backward) {
-      const int64_t per = xent_rows_ids(D, V);
-      p.dz = take(size_t(V) * xent_rows_tp(T) * 4);
-      p.dx = take(size_t((V + per - 1) / per) * T * D * 4);
-    } else {
-      p.stats = take(size_t(xent_rows_parts(V)) * T * sizeof(float2));
-      p.zt = take(size_t(T) * 4);
-    }
-    p.total = off;
-    return p;
-  }
-  p.thin = T <= kXentThinMax;
+  p.thin = use_thin(T, D, V, is_bf16);
   if (!is_bf16) {
     p.planes_x = take(size_t(T) * D * 2 * planes);
     if (!p.thin) p.planes_w = take(size_t(V) * D * 2 * planes);
@@ -353,24 +356,24 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
                              int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
                              cudaStream_t s) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 0);
-  if (p.rows) {
-    float2* stats = at<float2>(ws, p.stats);
-    float* zt = at<float>(ws, p.zt);
-    XENT_STEP("xent_logits", s, launch_xent_rows_stats(X, W, targets, T, D, V, is_bf16, stats, zt, s));
-    return run_join(stats, xent_rows_parts(V), T, targets, V, zt, loss, lse, status, s);
-  }
   Planes pl;
   cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
   if (e != cudaSuccess) return e;
   if (p.thin) {
-    XentThin h{};
-    if (!thin_maps(&h, W, pl, T, V, D)) return cudaErrorInvalidValue;
-    h.targets = targets;
-    h.V = V;
-    h.stats = at<float2>(ws, p.stats);
-    h.zt = at<float>(ws, p.zt);
-    XENT_STEP("xent_logits", s, launch_xent_thin_stats(h, wait_ns, s));
-    return run_join(h.stats, xent_thin_parts(V), T, targets, V, h.zt, loss, lse, status, s);
+    float2* stats = at<float2>(ws, p.stats);
+    float* zt = at<float>(ws, p.zt);
+    for (int64_t t0 = 0; t0 < T; t0 += kXentThinMax) {
+      XentThin h{};
+      if (!thin_maps(&h, W, pl, t0, T, V, D)) return cudaErrorInvalidValue;
+      h.targets = targets + t0;
+      h.V = V;
+      h.stats = stats + t0 * xent_thin_parts(V);
+      h.zt = zt + t0;
+      XENT_STEP("xent_logits", s, launch_xent_thin_stats(h, wait_ns, s));
+      if ((e = run_join(h.stats, xent_thin_parts(V), h.T, h.targets, V, h.zt, loss + t0, lse + t0, status, s)) != cudaSuccess)
+        return e;
+    }
+    return cudaSuccess;
   }
   XentGemm g{};
   for (int i = 0; i < pl.n; ++i)
@@ -396,15 +399,6 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
                               const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
                               void* ws, uint64_t wait_ns, cudaStream_t s) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 1);
-  if (p.rows) {
-    float *dz = at<float>(ws, p.dz), *part = at<float>(ws, p.dx);
-    const int64_t per = xent_rows_ids(D, V);
-    if (xent_rows_tp(T) != T)  // the rows that dz is padded with
-      XENT_STEP("xent_dz", s, cudaMemsetAsync(dz, 0, size_t(V) * xent_rows_tp(T) * 4, s));
-    XENT_STEP("xent_dz", s, launch_xent_rows_dz(X, W, targets, lse, dloss, T, D, V, is_bf16, dz, s));
-    XENT_STEP("xent_dX_dW", s, launch_xent_rows_products(dz, X, W, T, D, V, is_bf16, part, dW, s));
-    return run_reduce(part, static_cast<int>((V + per - 1) / per), T * D, T * D, nullptr, is_bf16, dX, s);
-  }
   Planes pl;
   cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
   if (e != cudaSuccess) return e;
@@ -419,16 +413,17 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     const void* W0 = static_cast<const char*>(W) + v0 * D * es;
     // dz of the piece, from its logits computed again; columns vc .. vp are zeros.
     XentGemm g{};
-    if (p.thin) {
+    for (int64_t t0 = 0; p.thin && t0 < T; t0 += kXentThinMax) {
       XentThin h{};
-      if (!thin_maps(&h, W0, pl, T, vc, D)) return cudaErrorInvalidValue;
-      h.targets = targets;
+      if (!thin_maps(&h, W0, pl, t0, T, vc, D)) return cudaErrorInvalidValue;
+      h.targets = targets + t0;
       h.V = V;
       h.col0 = v0;
-      h.lse = lse;
-      h.dloss = dloss;
+      h.lse = lse + t0;
+      h.dloss = dloss + t0;
       h.dmax = dmax;
-      h.dz = reinterpret_cast<__nv_bfloat16*>(dz[0]);
+      h.dz = reinterpret_cast<__nv_bfloat16*>(dz[0]) + t0 * p.dz_pitch;
+      h.plane = T * p.dz_pitch;
       h.pitch = p.dz_pitch;
       h.dz_columns = vp;
       XENT_STEP("xent_dz", s, launch_xent_thin_dz(h, wait_ns, s));
@@ -471,21 +466,27 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
 
     // dX += dz W over the piece.
     if (p.thin) {
-      XentThin h{};
-      h.f32 = pl.n > 1;
-      h.T = static_cast<int>(T);
-      h.M = static_cast<int>(D);
-      h.K = static_cast<int>(vp);
-      h.slices = p.slices_x;
-      h.part = at<float>(ws, p.dx);
-      h.add = v0 > 0;
-      if (!(h.f32 ? make_output_map_f32(&h.map_w, const_cast<void*>(W0), vc, D, D) : make_operand_map(&h.map_w, W0, vc, D, D, 64)))
-        return cudaErrorInvalidValue;
-      for (int i = 0; i < pl.n; ++i)
-        if (!make_operand_map(&h.map_b[i], dz[i], T, vp, p.dz_pitch, xent_thin_columns(T))) return cudaErrorInvalidValue;
-      XENT_STEP("xent_dX", s, launch_xent_thin_dx(h, wait_ns, s));
+      const bool f32 = pl.n > 1;
+      for (int64_t t0 = 0; t0 < T; t0 += kXentThinMax) {
+        XentThin h{};
+        h.f32 = f32;
+        h.T = static_cast<int>(T - t0 < kXentThinMax ? T - t0 : kXentThinMax);
+        h.M = static_cast<int>(D);
+        h.K = static_cast<int>(vp);
+        h.slices = p.slices_x;
+        h.part = at<float>(ws, p.dx) + t0 * D;
+        h.part_rows = T;
+        h.add = v0 > 0;
+        if (!(f32 ? make_output_map_f32(&h.map_w, const_cast<void*>(W0), vc, D, D)
+                  : make_operand_map(&h.map_w, W0, vc, D, D, 64)))
+          return cudaErrorInvalidValue;
+        for (int i = 0; i < pl.n; ++i)
+          if (!make_operand_map(&h.map_b[i], dz[i] + t0 * p.dz_pitch, h.T, vp, p.dz_pitch, xent_thin_columns(h.T)))
+            return cudaErrorInvalidValue;
+        XENT_STEP("xent_dX", s, launch_xent_thin_dx(h, wait_ns, s));
+      }
       if (v0 + vc < V) continue;
-      if ((e = run_reduce(h.part, p.slices_x, T * D, T * D, dmax, is_bf16, dX, s)) != cudaSuccess) return e;
+      if ((e = run_reduce(at<float>(ws, p.dx), p.slices_x, T * D, T * D, dmax, is_bf16, dX, s)) != cudaSuccess) return e;
       continue;
     }
     g = XentGemm{};

@@ -122,6 +122,8 @@ def test_xent_against_64_bits(tp, T, D, V, dtype):
 @pytest.mark.parametrize("T,D,V", [
     (1, 1000, 5000), (2, 72, 15), (3, 4104, 700), (4, 64, 16), (5, 8, 17), (7, 520, 2049), (8, 1032, 4000), (9, 72, 64),
     (16, 4096, 300), (17, 256, 1000), (31, 40, 129), (32, 768, 3000), (6, 12000, 90), (32, 6400, 200), (2, 60000, 40),
+    (33, 264, 1000), (64, 1024, 2000), (65, 72, 500), (128, 136, 1300), (150, 520, 700), (193, 64, 900), (256, 48, 260),
+    (257, 64, 300), (129, 4200, 4001), (192, 2048, 8200),
 ])
 def test_xent_of_a_few_rows(tp, T, D, V, dtype):
     X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + D + V)
