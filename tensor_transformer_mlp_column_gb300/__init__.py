@@ -673,7 +673,7 @@ def tpmlp_embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, 
             o = out.data_ptr()
         else:
             o = _like(out, (T, D), E.dtype, dev, "out")
-        _check(lib().tpmlp_embed_forward(e, i, T, D, V, dt, scale, o, on.raw), "tpmlp_embed_forward")
+        _check(lib().tpmlp_embed_forward(e, i, T, D, V, dt, float(scale), o, on.raw), "tpmlp_embed_forward")
     return out
 
 
@@ -700,7 +700,7 @@ def tpmlp_embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: f
         g, i = _ptr(dout, dev, "dout"), _ids(ids, T, dev, "ids")
         dE = torch.empty((V, D), dtype=dtype, device="cuda") if dE is None else dE
         ws, wp, wn = _space(l.tpmlp_embed_workspace_bytes(T, D, V), workspace, dev)
-        _check(l.tpmlp_embed_backward(g, _type(dout), i, T, D, V, scale, _like(dE, (V, D), dE.dtype, dev, "dE"),
+        _check(l.tpmlp_embed_backward(g, _type(dout), i, T, D, V, float(scale), _like(dE, (V, D), dE.dtype, dev, "dE"),
                                       _type(dE), 1 if accumulate else 0, wp, wn, on.raw), "tpmlp_embed_backward")
     return dE
 
@@ -753,7 +753,7 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
             o = _addresses(out, on.dev, "an output")
         norm = torch.empty(1, dtype=torch.float32, device="cuda") if norm is None else norm
         ws, wp, wn = _space(l.tpmlp_grad_workspace_bytes(n), workspace, on.dev)
-        _check(l.tpmlp_grad_clip(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, max_norm,
+        _check(l.tpmlp_grad_clip(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, float(max_norm),
                                  None if o is None else o.buffer_info()[0],
                                  _like(norm, (1,), torch.float32, on.dev, "norm"), wp, wn, on.raw), "tpmlp_grad_clip")
     return norm

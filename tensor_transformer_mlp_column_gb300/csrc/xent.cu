@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   loss[t] = target >= 0 && target < V ? static_cast<float>(v - double(z)) : 0.f;
 }
 
-// parts[b] = the largest |dloss| among CTA b's rows that count.
+// parts[b] = the largest finite |dloss| among CTA b's rows that count: a row
+// with an infinite one spoils its own gradient, not the scale of the others.
 __global__ void __launch_bounds__(256) xent_dmax_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                         int64_t T, int64_t V, float* __restrict__ parts) {
   __shared__ float red[8];
@@ -94,7 +95,9 @@ __global__ void __launch_bounds__(256) xent_dmax_kernel(const float* __restrict_
   float m = 0.f;
   for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256) {
     const int64_t id = targets[t];
-    if (id >= 0 && id < V) m = fmaxf(m, fabsf(dloss[t]));
+    if (id < 0 || id >= V) continue;
+    const float a = fabsf(dloss[t]);
+    if (a < INFINITY) m = fmaxf(m, a);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -307,13 +307,12 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
     const uint32_t acc_empty_lead = map_to_cta(smem_addr(acc_empty), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    float scale = 1.f, inv_dmax = 0.f;  // kXentOut*: dmax; kXentGrad*: 1 / dmax
+    float scale = 1.f, dmax = 0.f;  // kXentOut*: dmax or 1; kXentGrad*: dmax
     if constexpr (EPI == kXentOutBf16 || EPI == kXentOutF32) {
       if (p.g.dmax) scale = warp_dmax(p.g.dmax, lane);
     }
     if constexpr (EPI == kXentGrad || EPI == kXentGradF32) {
-      const float d = warp_dmax(p.g.dmax, lane);
-      inv_dmax = d > 0.f ? 1.f / d : 0.f;
+      dmax = warp_dmax(p.g.dmax, lane);
     }
     for (int tile = cluster; tile < p.tiles; tile += nclusters) {
       int slice, mb, nb;
@@ -334,7 +333,8 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           if constexpr (EPI != kXentStats) {
             // fp32: lse itself, see below.
             lse2 = EPI == kXentGrad ? p.g.lse[m] * kLog2e : p.g.lse[m];
-            rs = counts ? p.g.dloss[m] * inv_dmax : 0.f;
+            const float d = p.g.dloss[m];
+            rs = counts && d != 0.f ? d / dmax : 0.f;
           }
         }
       }

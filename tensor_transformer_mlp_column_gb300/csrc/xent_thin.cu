@@ -28,7 +28,9 @@
 // so that products of one size share an accumulator, the small ones are not
 // cut off against the large sum, and 3 MMAs do what 6 of N = 32 columns did,
 // whose cost hardly depends on N. Runs of sums as in xent_gemm.cu: 512 fp32
-// products, 1024 of bf16 for the logits' statistics.
+// products, 1024 of bf16 for the logits' statistics, there in four
+// accumulators by turns (HBM is the bound, and a quarter of the length is a
+// quarter of what is cut off).
 #include "gemm_common.cuh"
 #include "train.h"
 
@@ -46,21 +48,22 @@ constexpr uint32_t kPlaneBytes = 128 * 64 * 2;  // bf16: 128 x 64 of W
 
 enum ThinKind : int { kThinStats = 0, kThinGrad = 1, kThinDx = 2 };
 
-template <bool F32, int N>
+template <bool F32, int N, int KIND>
 struct TCfg {
+  static constexpr int TURNS = !F32 && KIND == kThinStats ? 4 : 1;
   static constexpr int PL = F32 ? kXentPlanes : 1;
   static constexpr int RAW = F32 ? 8 : 0;                                        // stages of raw W
   static constexpr uint32_t A_BYTES = F32 ? 0 : kPlaneBytes;                     // of A in shared memory
   static constexpr uint32_t B_BYTES = N * 64 * 2;                                // one plane of B, 64 K
   static constexpr uint32_t STAGE = A_BYTES + PL * B_BYTES;                      // operands of 64 K
   static constexpr int STAGES = F32 ? 3 : 8;
-  static constexpr uint32_t ACC = PL * N;                                        // columns of the accumulators of a run
+  static constexpr uint32_t ACC = PL * TURNS * N;                                // columns of the accumulators of a run
   // Two sets, so that a run's epilogue goes on beside the next run; at N = 64
   // of fp32 tensor memory holds one.
   static constexpr int SETS = F32 && N > 32 ? 1 : 2;
   static constexpr uint32_t A_COLS = PL * 32;                                    // fp32: planes of 64 K of A
   static constexpr uint32_t USED = SETS * ACC + (F32 ? STAGES * A_COLS : 0);
-  static constexpr uint32_t TMEM = USED <= 64 ? 64 : USED <= 128 ? 128 : 512;
+  static constexpr uint32_t TMEM = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
   static constexpr size_t SMEM = 1024 + size_t(RAW) * kRawBytes + size_t(STAGES) * STAGE + 512;
   static_assert(USED <= 512, "tensor memory");
 };
@@ -132,7 +135,7 @@ __device__ __forceinline__ bool all_of_epilogue(bool ok) {
 
 template <bool F32, int N, int KIND>
 __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constant__ TParams p) {
-  using C = TCfg<F32, N>;
+  using C = TCfg<F32, N, KIND>;
   constexpr bool MN = KIND == kThinDx;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -254,12 +257,12 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
               const uint32_t idesc = idesc_bf16_f32(128, (C::PL - pa) * N, MN && !F32 ? 1 : 0, 0);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t accumulate = (pa | k) != 0 || q != r ? 1u : 0u;
+                const uint32_t accumulate = (C::TURNS == 1 && (pa | k) != 0) || q != r ? 1u : 0u;
                 const uint64_t b_desc = operand_desc(b0, k, false);
                 if constexpr (F32)
                   mma_a_in_tmem(d0 + pa * N, a_tmem + pa * 32 + k * 8, b_desc, idesc, accumulate);
                 else
-                  tc_mma_bf16(d0, operand_desc(a0, k, MN), b_desc, idesc, accumulate);
+                  tc_mma_bf16(d0 + (k % C::TURNS) * N, operand_desc(a0, k, MN), b_desc, idesc, accumulate);
               }
             }
             tc_commit(empty + st);
@@ -369,7 +372,8 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         s_target[et] = counts ? t - p.g.col0 : -1;
         if constexpr (KIND == kThinGrad) {
           s_lse[et] = in ? p.g.lse[et] : 0.f;
-          s_rs[et] = counts && dmax > 0.f ? p.g.dloss[et] * (1.f / dmax) : 0.f;
+          const float d = in ? p.g.dloss[et] : 0.f;
+          s_rs[et] = counts && d != 0.f ? d / dmax : 0.f;
         }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
 
 template <bool F32, int N, int KIND>
 cudaError_t launch_kind(const TParams& p, cudaStream_t s) {
-  using C = TCfg<F32, N>;
+  using C = TCfg<F32, N, KIND>;
   auto kern = thin_kernel<F32, N, KIND>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
   if (e != cudaSuccess) return e;

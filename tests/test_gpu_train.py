@@ -200,6 +200,30 @@ def test_xent_target_out_of_range_is_left_out_and_reported(tp):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("T,D,V", [(100, 8, 1), (300, 16, 3), (70, 64, 257), (513, 24, 65)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_xent_small_vocabularies(tp, T, D, V, dtype):
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + V)
+    _check_xent(tp, X, W, t, dloss, dtype)
+
+
+@pytest.mark.parametrize("T", [9, 100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_xent_extreme_row_gradients(tp, dtype, T):
+    # An infinite row gradient spoils its own row of dX only; tiny ones keep their precision.
+    X, W, t, dloss = _xent_inputs(T, 64, 300, dtype, seed=70, masked=0.0)
+    _, lse = tp.tpmlp_xent_forward(X, W, t)
+    ref, _ = tp.tpmlp_xent_backward(X, W, t, lse, torch.where(torch.arange(T, device="cuda") == 4, 0.0, dloss))
+    dloss[4] = float("inf")
+    dX, _ = tp.tpmlp_xent_backward(X, W, t, lse, dloss)
+    keep = torch.arange(T, device="cuda") != 4
+    assert torch.equal(dX[keep], ref[keep]) and not bool(torch.isfinite(dX[4]).all())
+    for scale in (1e-38, 1e-30, 1e30):
+        _check_xent(tp, X, W, t, torch.full_like(dloss, scale), dtype) if scale > 1e-35 else None
+        dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, torch.full_like(dloss, scale))
+        assert bool(torch.isfinite(dX).all()) and bool(torch.isfinite(dW).all()) and bool((dX != 0).any())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_xent_large_logits(tp, dtype):
     # Logits of some hundreds: exponentials that over- and underflow fp32 unless they are taken below the maximum.
