@@ -13,6 +13,7 @@ Function names are those of the C ABI.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from array import array
 from typing import Optional, Sequence
@@ -572,6 +573,14 @@ def _like(t: torch.Tensor, shape, dtype: torch.dtype, dev: int, name: str) -> in
     return _ptr(t, dev, name)
 
 
+def _output(t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev: int, name: str):
+    """(tensor, address) of an output, the caller's or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+        return t, t.data_ptr()
+    return t, _like(t, shape, dtype, dev, name)
+
+
 def _space(nbytes: int, workspace: Optional[torch.Tensor], dev: int):
     """(tensor, address, bytes) of a call's workspace."""
     if workspace is None:
@@ -619,9 +628,15 @@ def tpmlp_xent_workspace_bytes(T: int, D: int, V: int, dtype: torch.dtype, backw
 
 
 def _xent_shapes(X: torch.Tensor, W: torch.Tensor):
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1] or X.dtype != W.dtype:
+    xs, vs = X.shape, W.shape
+    if len(xs) != 2 or len(vs) != 2 or xs[1] != vs[1] or X.dtype != W.dtype:
         raise ValueError("X must be [T, D] and W [V, D], of one dtype")
-    return X.shape[0], X.shape[1], W.shape[0]
+    return xs[0], xs[1], vs[0]
+
+
+@functools.lru_cache(maxsize=1024)
+def _xent_workspace(dev: int, T: int, D: int, V: int, dt: int, backward: int) -> int:
+    return int(lib().tpmlp_xent_workspace_bytes(T, D, V, dt, backward))
 
 
 def tpmlp_xent_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: Optional[torch.Tensor] = None,
@@ -633,11 +648,10 @@ def tpmlp_xent_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
     with _On(stream) as on:
         dev = on.dev
         x, w, t = _ptr(X, dev, "X"), _ptr(W, dev, "W"), _ids(targets, T, dev, "targets")
-        loss = torch.empty(T, dtype=torch.float32, device="cuda") if loss is None else loss
-        lse = torch.empty(T, dtype=torch.float32, device="cuda") if lse is None else lse
-        ws, wp, wn = _space(l.tpmlp_xent_workspace_bytes(T, D, V, dt, 0), workspace, dev)
-        _check(l.tpmlp_xent_forward(x, w, t, T, D, V, dt, _like(loss, (T,), torch.float32, dev, "loss"),
-                                    _like(lse, (T,), torch.float32, dev, "lse"), wp, wn, on.raw), "tpmlp_xent_forward")
+        loss, lp = _output(loss, (T,), torch.float32, dev, "loss")
+        lse, ep = _output(lse, (T,), torch.float32, dev, "lse")
+        ws, wp, wn = _space(_xent_workspace(dev, T, D, V, dt, 0), workspace, dev)
+        _check(l.tpmlp_xent_forward(x, w, t, T, D, V, dt, lp, ep, wp, wn, on.raw), "tpmlp_xent_forward")
     return loss, lse
 
 
@@ -650,13 +664,12 @@ def tpmlp_xent_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
     with _On(stream) as on:
         dev = on.dev
         x, w, t = _ptr(X, dev, "X"), _ptr(W, dev, "W"), _ids(targets, T, dev, "targets")
-        dX = torch.empty((T, D), dtype=X.dtype, device="cuda") if dX is None else dX
-        dW = torch.empty((V, D), dtype=X.dtype, device="cuda") if dW is None else dW
-        ws, wp, wn = _space(l.tpmlp_xent_workspace_bytes(T, D, V, dt, 1), workspace, dev)
+        dX, xp = _output(dX, (T, D), X.dtype, dev, "dX")
+        dW, vp = _output(dW, (V, D), X.dtype, dev, "dW")
+        ws, wp, wn = _space(_xent_workspace(dev, T, D, V, dt, 1), workspace, dev)
         _check(l.tpmlp_xent_backward(x, w, t, _like(lse, (T,), torch.float32, dev, "lse"),
-                                     _like(dloss, (T,), torch.float32, dev, "dloss"), T, D, V, dt,
-                                     _like(dX, (T, D), X.dtype, dev, "dX"), _like(dW, (V, D), X.dtype, dev, "dW"),
-                                     wp, wn, on.raw), "tpmlp_xent_backward")
+                                     _like(dloss, (T,), torch.float32, dev, "dloss"), T, D, V, dt, xp, vp, wp, wn,
+                                     on.raw), "tpmlp_xent_backward")
     return dX, dW
 
 
@@ -668,11 +681,7 @@ def tpmlp_embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, 
     with _On(stream) as on:
         dev = on.dev
         e, i = _ptr(E, dev, "E"), _ids(ids, T, dev, "ids")
-        if out is None:
-            out = torch.empty((T, D), dtype=E.dtype, device="cuda")
-            o = out.data_ptr()
-        else:
-            o = _like(out, (T, D), E.dtype, dev, "out")
+        out, o = _output(out, (T, D), E.dtype, dev, "out")
         _check(lib().tpmlp_embed_forward(e, i, T, D, V, dt, float(scale), o, on.raw), "tpmlp_embed_forward")
     return out
 
@@ -698,10 +707,10 @@ def tpmlp_embed_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: f
     with _On(stream) as on:
         dev = on.dev
         g, i = _ptr(dout, dev, "dout"), _ids(ids, T, dev, "ids")
-        dE = torch.empty((V, D), dtype=dtype, device="cuda") if dE is None else dE
+        dE, e = _output(dE, (V, D), dtype if dE is None else dE.dtype, dev, "dE")
         ws, wp, wn = _space(l.tpmlp_embed_workspace_bytes(T, D, V), workspace, dev)
-        _check(l.tpmlp_embed_backward(g, _type(dout), i, T, D, V, float(scale), _like(dE, (V, D), dE.dtype, dev, "dE"),
-                                      _type(dE), 1 if accumulate else 0, wp, wn, on.raw), "tpmlp_embed_backward")
+        _check(l.tpmlp_embed_backward(g, _type(dout), i, T, D, V, float(scale), e, _type(dE), 1 if accumulate else 0,
+                                      wp, wn, on.raw), "tpmlp_embed_backward")
     return dE
 
 
@@ -731,10 +740,10 @@ def tpmlp_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] 
     n, l = len(grads), lib()
     with _On(stream) as on:
         p, c, d = _grads(grads, on.dev)
-        norm = torch.empty(1, dtype=torch.float32, device="cuda") if norm is None else norm
+        norm, np_ = _output(norm, (1,), torch.float32, on.dev, "norm")
         ws, wp, wn = _space(l.tpmlp_grad_workspace_bytes(n), workspace, on.dev)
-        _check(l.tpmlp_grad_norm(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n,
-                                 _like(norm, (1,), torch.float32, on.dev, "norm"), wp, wn, on.raw), "tpmlp_grad_norm")
+        _check(l.tpmlp_grad_norm(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, np_, wp, wn, on.raw),
+               "tpmlp_grad_norm")
     return norm
 
 
@@ -751,11 +760,10 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
             if len(out) != n or [t.numel() for t in out] != c.tolist() or [t.dtype for t in out] != [g.dtype for g in grads]:
                 raise ValueError("out must have a tensor of each gradient's size and dtype")
             o = _addresses(out, on.dev, "an output")
-        norm = torch.empty(1, dtype=torch.float32, device="cuda") if norm is None else norm
+        norm, np_ = _output(norm, (1,), torch.float32, on.dev, "norm")
         ws, wp, wn = _space(l.tpmlp_grad_workspace_bytes(n), workspace, on.dev)
         _check(l.tpmlp_grad_clip(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, float(max_norm),
-                                 None if o is None else o.buffer_info()[0],
-                                 _like(norm, (1,), torch.float32, on.dev, "norm"), wp, wn, on.raw), "tpmlp_grad_clip")
+                                 None if o is None else o.buffer_info()[0], np_, wp, wn, on.raw), "tpmlp_grad_clip")
     return norm
 
 

@@ -87,6 +87,14 @@ constexpr int kXentPlanes = 3;
 constexpr int kXentPairs = 6;
 constexpr int kXentPart = 128;    // columns of one (max, sum) part
 constexpr int kXentDmaxParts = 64;
+// Up to kXentDmaxRows rows the kernels of dz find the largest |dloss| themselves.
+constexpr int kXentDmaxRows = 512;
+struct XentDmax {
+  const float* dloss;      // [rows]
+  const int64_t* targets;  // [rows]
+  int rows;                // 0: read it from the parts
+  float* out;              // [kXentDmaxParts], for the products
+};
 struct XentGemm {
   CUtensorMap map_a[kXentPlanes], map_b[kXentPlanes];
   CUtensorMap map_out[kXentPlanes];  // bf16: make_output_map_bf16; fp32: make_output_map_f32, slices stacked by rows
@@ -106,6 +114,7 @@ struct XentGemm {
   const float* lse;                  // [M]
   const float* dloss;                // [M]
   const float* dmax;                 // [kXentDmaxParts] parts of the largest |dloss|; as the scale of kXentOut* (may be null)
+  XentDmax rows;                     // kXentGrad*: in the place of dmax
 };
 // Slices that K is really cut into when `slices` are asked for.
 int xent_slices(int K, int slices);
@@ -125,6 +134,7 @@ struct XentThin {
   float2* stats;                    // [xent_thin_parts(M)][T]
   float* zt;
   const float *lse, *dloss, *dmax;
+  XentDmax rows;                    // as in XentGemm, of all groups
   __nv_bfloat16* dz;                // rows [T][pitch] of planes that are `plane` apart
   int64_t plane, pitch, dz_columns; // of dz's columns dz_columns are written (zeros from M on)
   float* part;                      // dX: rows [T][M] of slices that are part_rows rows apart

@@ -25,7 +25,7 @@
 #include "internal.h"
 #include "tpmlp.h"
 #include "trace.h"
-#include "train.h"
+#include "xent_device.cuh"
 
 namespace tpmlp {
 
@@ -85,22 +85,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   loss[t] = target >= 0 && target < V ? static_cast<float>(v - double(z)) : 0.f;
 }
 
-// parts[b] = the largest finite |dloss| among CTA b's rows that count: a row
-// with an infinite one spoils its own gradient, not the scale of the others.
+// parts[b] = the largest finite |dloss| among CTA b's rows that count.
 __global__ void __launch_bounds__(256) xent_dmax_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                         int64_t T, int64_t V, float* __restrict__ parts) {
   __shared__ float red[8];
   pdl_wait();
   pdl_launch_dependents();
   float m = 0.f;
-  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256) {
-    const int64_t id = targets[t];
-    if (id < 0 || id >= V) continue;
-    const float a = fabsf(dloss[t]);
-    if (a < INFINITY) m = fmaxf(m, a);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < T; t += int64_t(gridDim.x) * 256)
+    m = fmaxf(m, finite_dloss(dloss, targets, t, V));
+  m = warp_max(m);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -141,10 +135,7 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restri
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
-    float m = 0.f;
-    for (int i = threadIdx.x; i < kXentDmaxParts; i += 32) m = fmaxf(m, dmax[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float m = warp_dmax(dmax, threadIdx.x);
     if (threadIdx.x == 0) scale_s = m;
   }
   __syncthreads();
@@ -408,7 +399,11 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
   const int pairs = pl.n == 1 ? 1 : kXentPairs;
   const size_t es = is_bf16 ? 2 : 4;
   float* dmax = at<float>(ws, p.dmax);
-  XENT_STEP("xent_dmax", s, launch_pdl(xent_dmax_kernel, dim3(kXentDmaxParts), dim3(256), 0, s, dloss, targets, T, V, dmax));
+  XentDmax rows{dloss, targets, static_cast<int>(T), dmax};
+  if (T > kXentDmaxRows) {
+    XENT_STEP("xent_dmax", s, launch_pdl(xent_dmax_kernel, dim3(kXentDmaxParts), dim3(256), 0, s, dloss, targets, T, V, dmax));
+    rows.rows = 0;
+  }
   uint16_t* dz[kXentPlanes];
   for (int i = 0; i < pl.n; ++i) dz[i] = at<uint16_t>(ws, p.dz) + i * T * p.dz_pitch;
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
@@ -425,6 +420,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
       h.lse = lse + t0;
       h.dloss = dloss + t0;
       h.dmax = dmax;
+      h.rows = rows;
       h.dz = reinterpret_cast<__nv_bfloat16*>(dz[0]) + t0 * p.dz_pitch;
       h.plane = T * p.dz_pitch;
       h.pitch = p.dz_pitch;
@@ -448,6 +444,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g.lse = lse;
     g.dloss = dloss;
     g.dmax = dmax;
+    g.rows = rows;
     if (!p.thin) XENT_STEP("xent_dz", s, launch_xent_gemm(g, wait_ns, s));
 
     // dW of the piece = dz^T X.

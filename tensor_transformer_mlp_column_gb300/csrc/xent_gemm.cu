@@ -31,7 +31,7 @@
 // Waits are bounded; on a timeout the roles of both CTAs leave their loops,
 // copies and MMAs in flight are drained and tensor memory is freed.
 #include "gemm_common.cuh"
-#include "train.h"
+#include "xent_device.cuh"
 
 #include <atomic>
 #include <cstring>
@@ -54,10 +54,8 @@ constexpr int kDrainPauseNs = 25;  // per K block of a run, between a warp's rea
 
 template <int EPI, bool RUNS>
 struct Cfg {
-  // Staging blocks of an epilogue warp. The three planes of kXentGradF32 need
-  // 96 KB in all and leave room for two stages.
-  static constexpr int kOutBlocks = EPI == kXentStats ? 0 : EPI == kXentGradF32 ? 3 : 1;
-  static constexpr int STAGES = EPI == kXentGradF32 ? 2 : 3;
+  static constexpr int kOutBlocks = EPI == kXentStats ? 0 : 1;  // staging blocks of an epilogue warp
+  static constexpr int STAGES = 3;
   static constexpr uint32_t A_BYTES = kSub * kSubBytes;
   static constexpr uint32_t STAGE_BYTES = 2 * A_BYTES;
   static constexpr uint32_t STAGING = kEpiWarps * kOutBlocks * kOutBlock;
@@ -87,11 +85,6 @@ __device__ __forceinline__ void plane_pair(int pairs, int i, int& a, int& b) {
   b = (kB >> (4 * i)) & 15;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 constexpr float kLog2e = kXentLog2e;
 
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
@@ -99,15 +92,6 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const 
                    reinterpret_cast<uint64_t>(map)),
                "r"(smem_addr(src)), "r"(x), "r"(y)
                : "memory");
-}
-
-// The largest |dloss| of the rows that count, from its parts (whole warp).
-__device__ __forceinline__ float warp_dmax(const float* parts, int lane) {
-  float m = 0.f;
-  for (int i = lane; i < kXentDmaxParts; i += 32) m = fmaxf(m, parts[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
 }
 
 // RUNS: a tile's sum may have several runs; else it has one.
@@ -312,7 +296,8 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
       if (p.g.dmax) scale = warp_dmax(p.g.dmax, lane);
     }
     if constexpr (EPI == kXentGrad || EPI == kXentGradF32) {
-      dmax = warp_dmax(p.g.dmax, lane);
+      dmax = p.g.rows.rows ? warp_dmax_of_rows(p.g.rows, p.g.V, lane, blockIdx.x == 0 && warp == kEpiWarp0)
+                           : warp_dmax(p.g.dmax, lane);
     }
     for (int tile = cluster; tile < p.tiles; tile += nclusters) {
       int slice, mb, nb;
@@ -340,6 +325,42 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
       }
       const bool work = m_warp < p.g.M && nh < p.g.N;  // warp-uniform
       float run_max = -INFINITY, run_sum = 0.f;  // kXentStats, in units of log2
+      // 32 columns of this thread's row, as bf16, into a half of the staging block (128-byte swizzle).
+      auto stage_half = [&](int hb, const float (&v)[32]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(stage_out + lane * 128 + (((4 * hb + j) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+      };
+      // kXentGradF32: the planes of columns nh + c .. + 63, one after the other through the staging block.
+      auto store_planes = [&](int c, float (&a)[32], float (&b)[32]) {
+        if (!work || nh + c >= p.g.N) return;  // warp-uniform
+        if (nh + c + 32 >= p.g.N) {            // finish() left the second half alone
+#pragma unroll
+          for (int i = 0; i < 32; ++i) b[i] = 0.f;
+        }
+#pragma unroll
+        for (int pl = 0; pl < kXentPlanes; ++pl) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          stage_half(0, a);
+          stage_half(1, b);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.g.map_out[pl], stage_out, nh + c, static_cast<int32_t>(m_warp));
+            bulk_commit_group();
+          }
+          if (pl + 1 < kXentPlanes) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              a[i] -= __bfloat162float(__float2bfloat16_rn(a[i]));
+              b[i] -= __bfloat162float(__float2bfloat16_rn(b[i]));
+            }
+          }
+        }
+      };
       // Columns n0 .. n0+31 of this thread's row.
       auto finish = [&](int c, float (&v)[32]) {
         const int n0 = nh + c;
@@ -391,40 +412,23 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
             for (int i = 0; i < 32; ++i)
               if (n0 + i >= p.g.N) v[i] = 0.f;
           }
+          if constexpr (EPI == kXentGradF32) return;  // stored by store_planes
           const int hb = (c >> 5) & 1;  // half of the 64-column block
           if (hb == 0) {
-            if (lane == 0) bulk_wait_group_read<0>();  // the staging blocks' previous stores have read them
+            if (lane == 0) bulk_wait_group_read<0>();  // the staging block's previous store has read it
             __syncwarp();
           }
-#pragma unroll
-          for (int pl = 0; pl < C::kOutBlocks; ++pl) {
-            uint8_t* buf = stage_out + pl * kOutBlock;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * hb + j) ^ (lane & 7)) << 4)) =
-                  make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-            if (pl + 1 < C::kOutBlocks) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
-            }
-          }
+          stage_half(hb, v);
           // The block is stored when its second half is in, or when there is none.
           if (hb == 1 || n0 + 32 >= p.g.N) {
             if (hb == 0) {
-#pragma unroll
-              for (int pl = 0; pl < C::kOutBlocks; ++pl)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  *reinterpret_cast<uint4*>(stage_out + pl * kOutBlock + lane * 128 + (((4 + j) ^ (lane & 7)) << 4)) =
-                      make_uint4(0, 0, 0, 0);
+              float none[32] = {};
+              stage_half(1, none);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-#pragma unroll
-              for (int pl = 0; pl < C::kOutBlocks; ++pl)
-                tma_store_2d(&p.g.map_out[pl], stage_out + pl * kOutBlock, n0 - 32 * hb, static_cast<int32_t>(m_warp));
+              tma_store_2d(&p.g.map_out[0], stage_out, n0 - 32 * hb, static_cast<int32_t>(m_warp));
               bulk_commit_group();
             }
           }
@@ -436,11 +440,7 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= scale;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(stage_out + lane * 128 + (((4 * hb + j) ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          stage_half(hb, v);
           if (hb == 1 || n0 + 32 >= p.g.N) {  // columns past N are clipped by the store
             fence_proxy_async_smem();
             __syncwarp();
@@ -528,6 +528,9 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           else
             acc_release();
           finish(32 * c, sum[c]);
+          if constexpr (EPI == kXentGradF32) {
+            if (c & 1) store_planes(32 * c - 32, sum[c - 1], sum[c]);
+          }
           __syncwarp();
         }
       } else {
@@ -653,7 +656,7 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
     case kXentGrad:
       return launch_epi<kXentGrad, false>(p, s);
     case kXentGradF32:
-      return cut ? launch_epi<kXentGradF32, true>(p, s) : launch_epi<kXentGradF32, false>(p, s);
+      return launch_epi<kXentGradF32, true>(p, s);  // it holds a warp's columns in registers anyway
     case kXentOutBf16:
       return launch_epi<kXentOutBf16, false>(p, s);
     case kXentOutF32:

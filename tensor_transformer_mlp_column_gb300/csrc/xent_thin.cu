@@ -32,7 +32,7 @@
 // accumulators by turns (HBM is the bound, and a quarter of the length is a
 // quarter of what is cut off).
 #include "gemm_common.cuh"
-#include "train.h"
+#include "xent_device.cuh"
 
 #include <atomic>
 #include <cstring>
@@ -75,12 +75,6 @@ struct TParams {
   uint64_t wait_ns;
   int* status;
 };
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: row i of A in lane i, two K in each 32-bit column.
 __device__ __forceinline__ void mma_a_in_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -362,9 +356,9 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
     const int quarter = warp & 3, et = threadIdx.x - kEpiWarp0 * 32;
     if constexpr (KIND != kThinDx) {
       float dmax = 0.f;
-      if constexpr (KIND == kThinGrad) {
-        for (int i = 0; i < kXentDmaxParts; ++i) dmax = fmaxf(dmax, p.g.dmax[i]);
-      }
+      if constexpr (KIND == kThinGrad)
+        dmax = p.g.rows.rows ? warp_dmax_of_rows(p.g.rows, p.g.V, lane, blockIdx.x == 0 && warp == kEpiWarp0)
+                             : warp_dmax(p.g.dmax, lane);
       if (et < 64) {
         const bool in = et < p.g.T;
         const int64_t t = in ? p.g.targets[et] : -1;
