@@ -294,6 +294,26 @@ cudaError_t product_out(XentGemm& g, void* out, float* part, int is_bf16, uint64
 
 }  // namespace
 
+// Columns of a piece of the vocabulary. A piece's dz takes at most 512 MB (all
+// planes together), but a piece has at least 8192 columns: each piece adds its
+// share of dX in fp32, 16 T D bytes of traffic against 4 T D 8192 operations.
+// Among the pieces from half of that to all of it the one whose dW products,
+// all pieces together, take the fewest rounds over the CTA pairs (T = 8000, D =
+// 512, V = 100000: 33536 columns make 12, 29184 make 11 of at least 10.3).
+int64_t choose_piece(int64_t T, int64_t D, int64_t V, int planes) {
+  int64_t most = (int64_t(1) << 28) / (T * planes) / 256;
+  if (most < 32) most = 32;
+  const int64_t blocks = (V + 255) / 256, across = (D + 255) / 256, pairs = num_sms() > 1 ? num_sms() / 2 : 1;
+  if (most >= blocks) return V;
+  int64_t best = most, best_rounds = 0;
+  for (int64_t b = most; b >= 32 && b >= most / 2; --b) {
+    const int64_t full = blocks / b, rest = blocks - full * b;
+    const int64_t rounds = full * ((b * across + pairs - 1) / pairs) + (rest * across + pairs - 1) / pairs;
+    if (best_rounds == 0 || rounds < best_rounds) best = b, best_rounds = rounds;
+  }
+  return best * 256;
+}
+
 // Whether the products with W go by groups of kXentThinMax rows, each a pass
 // over W. bf16: one group (64 rows, V = 128000, D = 1024: the logits 54 us
 // either way, 32 rows 50 against 59). fp32, where the other form splits W into
@@ -326,13 +346,8 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
     p.total = off;
     return p;
   }
-  // A piece's dz takes at most 512 MB (all planes together), but a piece has
-  // at least 8192 columns: each piece adds its share of dX in fp32, 16 T D
-  // bytes of traffic against 4 T D 8192 operations.
-  int64_t piece = (int64_t(1) << 28) / (T * planes) / 256 * 256;
-  if (piece < 8192) piece = 8192;
-  if (piece >= V) piece = V;
-  p.piece = piece;
+  p.piece = choose_piece(T, D, V, planes);
+  const int64_t piece = p.piece;
   p.dz_pitch = ceil_to(piece, 64);
   p.dmax = take(kXentDmaxParts * 4);
   p.dz = take(size_t(T) * p.dz_pitch * 2 * planes);
