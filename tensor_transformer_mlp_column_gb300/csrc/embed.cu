@@ -480,23 +480,30 @@ constexpr int kClearUnroll = 8;
 constexpr int kClearPieces = kThreads * kClearUnroll;
 struct Clear {
   const uint32_t* present;
-  int64_t row0, pieces;     // pieces of all rows from row0 on
-  uint32_t row_pieces;      // pieces of a row
+  int64_t row0, pieces;  // pieces of all rows from row0 on
+  uint32_t row_pieces;   // pieces of a row
+  uint32_t magic;        // ceil(2^32 / row_pieces), where 1 < row_pieces < kClearPieces, else 0
   int piece;
-  int64_t ctas;
+  int ctas;
+  // The CTAs in their order: every `period`-th one is of the rarer kind, as long as there are any.
+  int period, sums_rare;
 };
 
 __device__ __forceinline__ void clear_rows(const Clear& c, int64_t cta, char* dE) {
   const int64_t first = cta * kClearPieces;
   const int n = static_cast<int>(c.pieces - first < kClearPieces ? c.pieces - first : kClearPieces);
-  const int64_t row = first / c.row_pieces;
+  const int64_t row = c.pieces >> 32 ? first / c.row_pieces : static_cast<uint32_t>(first) / c.row_pieces;
   const uint32_t skip = static_cast<uint32_t>(first - row * c.row_pieces);
   char* base = dE + (c.row0 * c.row_pieces + first) * c.piece;
   uint32_t marks[kClearUnroll];
 #pragma unroll
   for (int u = 0; u < kClearUnroll; ++u) {
     const int i = threadIdx.x + u * kThreads;
-    const int64_t v = c.row0 + row + (skip + static_cast<uint32_t>(i)) / c.row_pieces;
+    // (skip + i) / row_pieces: long rows meet at most one border here, short ones divide by multiplying
+    // (exact while numerator * row_pieces < 2^32).
+    const uint32_t x = skip + static_cast<uint32_t>(i);
+    const uint32_t down = c.row_pieces == 1 ? x : c.magic ? __umulhi(x, c.magic) : (x >= c.row_pieces ? 1u : 0u);
+    const int64_t v = c.row0 + row + down;
     marks[u] = i < n ? __ldg(c.present + (v >> 5)) >> (v & 31) & 1u : 1u;
   }
 #pragma unroll
@@ -526,18 +533,26 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
                                                            float* __restrict__ part, uint8_t* __restrict__ goes_on,
                                                            int run, int slabs, const __grid_constant__ Clear clear) {
   __shared__ uint32_t skey[5 * kMaxRun], spos[3 * kMaxRun];
+  __shared__ int s_start, s_stop, s_began;
   pdl_wait();
   pdl_launch_dependents();
-  int64_t job = blockIdx.x;
+  uint32_t job = blockIdx.x;
   if (clear.ctas > 0) {
-    const int64_t all = gridDim.x, sums = all - clear.ctas;
-    job = blockIdx.x * sums / all;  // summing CTAs before this one
-    if ((blockIdx.x + 1) * sums / all == job) {
-      clear_rows(clear, blockIdx.x - job, reinterpret_cast<char*>(dE));
+    // q CTAs of the rarer kind before this one; is it one itself?
+    const uint32_t rare = clear.sums_rare ? gridDim.x - clear.ctas : clear.ctas;
+    const uint32_t turn = job / clear.period;
+    const bool is_rare = job == turn * clear.period && turn < rare;
+    const uint32_t q = min(turn + (job > turn * clear.period ? 1u : 0u), rare);
+    const uint32_t index = is_rare ? turn : job - q;
+    if (is_rare != static_cast<bool>(clear.sums_rare)) {
+      clear_rows(clear, index, reinterpret_cast<char*>(dE));
       return;
     }
+    job = index;
   }
-  const int64_t chunk = job / slabs;
+  const uint32_t chunk32 = job / static_cast<uint32_t>(slabs);
+  const int slab = job - chunk32 * slabs;
+  const int64_t chunk = chunk32;
   const int64_t first = chunk * run;
   const int n = static_cast<int>(T - first < run ? T - first : run);
   const int most = 2 * run;
@@ -561,28 +576,34 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
     }
     return lo;
   };
-  const int lowest = first < most ? -static_cast<int>(first) : -most;
-  int start = 0, stop = n;
-  bool began = true;  // whether the running segment began in this chunk
-  {
-    const uint32_t k = k_at[0];
-    const int a = bound(lowest, 0, k, false);
-    if (a < 0) {  // it began earlier: summed there, unless it is a long one
-      began = a > -most && k_at[a + most] != k;
-      if (began) start = bound(0, n, k, true);
+  if (threadIdx.x < 32) {  // one warp looks, the others wait
+    const int lowest = first < most ? -static_cast<int>(first) : -most;
+    int start = 0, stop = n;
+    bool began = true;  // whether the running segment began in this chunk
+    const uint32_t k0 = k_at[0];
+    const int a0 = bound(lowest, 0, k0, false);
+    if (a0 < 0) {  // it began earlier: summed there, unless it is a long one
+      began = a0 > -most && k_at[a0 + most] != k0;
+      if (began) start = bound(0, n, k0, true);
+    }
+    bool long_on = false;
+    if (start < n && n == run && k_at[n] == k_at[n - 1]) {
+      const uint32_t k = k_at[n - 1];
+      const int a = bound(lowest, n, k, false);
+      if (a >= 0) {  // it begins in this chunk
+        long_on = k_at[a + most] == k;
+        if (!long_on) stop = bound(n, n + most, k, true);
+      }
+    }
+    if (threadIdx.x == 0) {
+      s_start = start, s_stop = stop, s_began = began;
+      if (slab == 0) goes_on[chunk] = long_on && k_at[n - 1] < V;
     }
   }
-  bool long_on = false;
-  if (start < n && n == run && k_at[n] == k_at[n - 1]) {
-    const uint32_t k = k_at[n - 1];
-    const int a = bound(lowest, n, k, false);
-    if (a >= 0) {  // it begins in this chunk
-      long_on = k_at[a + most] == k;
-      if (!long_on) stop = bound(n, n + most, k, true);
-    }
-  }
-  if (job == chunk * slabs && threadIdx.x == 0) goes_on[chunk] = long_on && k_at[n - 1] < V;
-  const int64_t col = ((job - chunk * slabs) * blockDim.x + threadIdx.x) * N;
+  __syncthreads();
+  const int start = s_start, stop = s_stop;
+  bool began = s_began;
+  const int64_t col = (int64_t(slab) * blockDim.x + threadIdx.x) * N;
   if (col >= D) return;
   float sum[N];
 #pragma unroll
@@ -733,10 +754,16 @@ cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, in
   const int64_t slabs = (pieces + threads - 1) / threads, chunks = (T + run - 1) / run;
   const int64_t grid = chunks * slabs + clear.ctas;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  Clear c = clear;
+  if (c.ctas > 0) {
+    const int64_t sums = chunks * slabs;
+    c.sums_rare = sums <= c.ctas;
+    c.period = static_cast<int>(c.sums_rare ? c.ctas / sums : sums / c.ctas) + 1;
+  }
   {
     TraceScope trace("embed_segments", s);
     const cudaError_t e = launch_pdl(segment_kernel<G, E, N>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, dout,
-                                     key, pos, T, D, V, scale, dE, accumulate, part, goes_on, run, static_cast<int>(slabs), clear);
+                                     key, pos, T, D, V, scale, dE, accumulate, part, goes_on, run, static_cast<int>(slabs), c);
     if (e != cudaSuccess) return e;
   }
   if (T <= 2 * run) return cudaSuccess;  // no segment is longer than that
@@ -818,7 +845,10 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
     if (cluster && clear.piece == 16) clear.row0 = (int64_t(8) + 2 * T / 8192) * (4 << 20) / row_bytes;
     if (clear.row0 > V) clear.row0 = V;
     clear.pieces = (V - clear.row0) * clear.row_pieces;
-    clear.ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
+    const int64_t ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    clear.ctas = static_cast<int>(ctas);
+    clear.magic = clear.row_pieces > 1 && clear.row_pieces < kClearPieces ? static_cast<uint32_t>(((1ull << 32) + clear.row_pieces - 1) / clear.row_pieces) : 0;
   }
   int at = 0;
   {

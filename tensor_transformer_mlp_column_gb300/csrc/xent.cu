@@ -127,11 +127,15 @@ __global__ void __launch_bounds__(256) xent_split_kernel(const float* __restrict
 }
 
 // out = dmax * (part[0] + part[1] + ...), n4 groups of 4 elements, slices
-// stride4 groups apart.
-template <typename E>
+// stride4 groups apart. LANES threads share a group's slices, a consecutive
+// part each, and their sums are added in order: with little output (few rows)
+// one thread a group would leave most of the GPU idle behind a chain of loads.
+template <typename E, int LANES>
 __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restrict__ part, int slices, int64_t stride4,
                                                           int64_t n4, const float* __restrict__ dmax, E* __restrict__ out) {
+  constexpr int kGroups = 256 / LANES;
   __shared__ float scale_s;
+  __shared__ float4 red[LANES > 1 ? 256 : 1];
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
@@ -140,13 +144,31 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restri
   }
   __syncthreads();
   const float scale = scale_s;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += int64_t(gridDim.x) * 256) {
-    float4 v = part[i];
+  const int lane = threadIdx.x / kGroups;  // which part of the slices
+  const int per = (slices + LANES - 1) / LANES, from = lane * per, to = min(slices, from + per);
+  for (int64_t i0 = int64_t(blockIdx.x) * kGroups; i0 < n4; i0 += int64_t(gridDim.x) * kGroups) {
+    const int64_t i = i0 + threadIdx.x % kGroups;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n4) {
 #pragma unroll 4
-    for (int k = 1; k < slices; ++k) {
-      const float4 a = part[k * stride4 + i];
-      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      for (int k = from; k < to; ++k) {
+        const float4 a = part[k * stride4 + i];
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      }
     }
+    if constexpr (LANES > 1) {
+      __syncthreads();
+      red[threadIdx.x] = v;
+      __syncthreads();
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 1; k < LANES; ++k) {
+          const float4 a = red[k * kGroups + threadIdx.x];
+          v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+        }
+      }
+    }
+    if (lane != 0 || i >= n4) continue;
     v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
     if constexpr (sizeof(E) == 4)
       reinterpret_cast<float4*>(out)[i] = v;
@@ -246,12 +268,14 @@ cudaError_t run_join(const float2* stats, int parts, int64_t T, const int64_t* t
 cudaError_t run_reduce(const float* part, int slices, int64_t stride, int64_t n, const float* dmax, int is_bf16,
                               void* out, cudaStream_t s) {
   const float4* p4 = reinterpret_cast<const float4*>(part);
-  const dim3 grid(grid_for(n / 4));
+  const int64_t n4 = n / 4, stride4 = stride / 4;
+  const bool shared = slices >= 8 && n4 < int64_t(num_sms()) * 1024;
+  const dim3 grid(grid_for(shared ? 8 * n4 : n4));
+  auto go = [&](auto kern, auto* o) { return launch_pdl(kern, grid, dim3(256), 0, s, p4, slices, stride4, n4, dmax, o); };
   XENT_STEP("xent_reduce", s,
-            is_bf16 ? launch_pdl(xent_reduce_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p4, slices, stride / 4, n / 4,
-                                 dmax, static_cast<__nv_bfloat16*>(out))
-                    : launch_pdl(xent_reduce_kernel<float>, grid, dim3(256), 0, s, p4, slices, stride / 4, n / 4, dmax,
-                                 static_cast<float*>(out)));
+            is_bf16 ? go(shared ? xent_reduce_kernel<__nv_bfloat16, 8> : xent_reduce_kernel<__nv_bfloat16, 1>,
+                         static_cast<__nv_bfloat16*>(out))
+                    : go(shared ? xent_reduce_kernel<float, 8> : xent_reduce_kernel<float, 1>, static_cast<float*>(out)));
   return cudaSuccess;
 }
 
