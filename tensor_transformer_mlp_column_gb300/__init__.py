@@ -718,11 +718,16 @@ def tpmlp_grad_workspace_bytes(n: int) -> int:
     return int(lib().tpmlp_grad_workspace_bytes(n))
 
 
+_DATA_PTR, _NUMEL = torch.Tensor.data_ptr, torch.Tensor.numel
+_DEVICE, _CONTIGUOUS = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
 def _addresses(ts: Sequence[torch.Tensor], dev: int, name: str) -> array:
-    for t in ts:
-        if t.get_device() != dev or not t.is_contiguous():
+    devices = list(map(_DEVICE, ts))
+    if devices.count(dev) != len(devices) or not all(map(_CONTIGUOUS, ts)):
+        for t in ts:
             _ptr(t, dev, name)  # says what is wrong
-    return array("Q", [t.data_ptr() for t in ts])
+    return array("Q", list(map(_DATA_PTR, ts)))
 
 
 def _grads(grads: Sequence[torch.Tensor], dev: int):
@@ -731,7 +736,7 @@ def _grads(grads: Sequence[torch.Tensor], dev: int):
         types = array("i", [_DTYPES[g.dtype] for g in grads])
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e}; use torch.float32 or torch.bfloat16") from None
-    return _addresses(grads, dev, "a gradient"), array("q", [g.numel() for g in grads]), types
+    return _addresses(grads, dev, "a gradient"), array("q", list(map(_NUMEL, grads))), types
 
 
 def tpmlp_grad_norm(grads: Sequence[torch.Tensor], norm: Optional[torch.Tensor] = None,
@@ -757,7 +762,7 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
         p, c, d = _grads(grads, on.dev)
         o = None
         if out is not None:
-            if len(out) != n or [t.numel() for t in out] != c.tolist() or [t.dtype for t in out] != [g.dtype for g in grads]:
+            if len(out) != n or list(map(_NUMEL, out)) != c.tolist() or [t.dtype for t in out] != [g.dtype for g in grads]:
                 raise ValueError("out must have a tensor of each gradient's size and dtype")
             o = _addresses(out, on.dev, "an output")
         norm, np_ = _output(norm, (1,), torch.float32, on.dev, "norm")

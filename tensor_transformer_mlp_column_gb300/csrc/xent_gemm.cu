@@ -48,8 +48,11 @@ constexpr uint32_t kSubBytes = 128 * BK * 2;
 constexpr uint32_t kOutBlock = 32 * 128;  // staging: 32 rows of 128 bytes
 constexpr int BN = 256;
 // K blocks of a run, at most: sums of up to 1024 products of bf16 data; 512 of
-// fp32 data's planes, where the products are closer to what is wanted.
-constexpr int kRunBf16 = 16, kRunF32 = 8;
+// fp32 data's high planes, where more is wanted; 8192 of the five other plane
+// pairs, which come first and whose sums are at most 2^-8 of the whole (cut like
+// the high planes' they made six runs of K = 512 instead of two: T = 1000, V =
+// 32001, logits 124 -> 114 us).
+constexpr int kRunBf16 = 16, kRunF32 = 8, kRunSmall = 128;
 constexpr int kDrainPauseNs = 25;  // per K block of a run, between a warp's reads of it
 
 template <int EPI, bool RUNS>
@@ -92,6 +95,13 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const 
                    reinterpret_cast<uint64_t>(map)),
                "r"(smem_addr(src)), "r"(x), "r"(y)
                : "memory");
+}
+
+// End of the run that begins at K block q of the `total` of a tile's plane
+// pairs. Runs end where stages of kSub = 2 K blocks do: q and `run` are even.
+__device__ __forceinline__ int run_end(int q, int total, int pairs, int run) {
+  const int small = pairs > 1 ? total / kXentPairs * (kXentPairs - 1) & ~1 : 0;
+  return q < small ? min(q + kRunSmall, small) : min(q + run, total);
 }
 
 // RUNS: a tile's sum may have several runs; else it has one.
@@ -239,8 +249,8 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
         decode_tile(grid, tile, slice, mb, nb);
         if (!tile_ok(grid, p.status, slice, mb, nb)) continue;
         const int total = p.g.pairs * k_count(slice);
-        for (int run = 0; !aborted && run < total; run += RUNS ? p.run : total) {
-          const int end = RUNS ? min(total, run + p.run) : total;
+        for (int run = 0, end; !aborted && run < total; run = end) {
+          end = RUNS ? run_end(run, total, p.g.pairs, p.run) : total;
           if (!wait_bounded(acc_empty + acc, acc_phase ^ 1u, guard, kSiteMmaAcc)) {
             aborted = true;
             break;
@@ -499,9 +509,8 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
         const int total = p.g.pairs * k_count(slice);
-        int run = 0;
         bool ok = true;
-        for (; run + p.run < total; run += p.run) {
+        for (int run = 0, end; (end = run_end(run, total, p.g.pairs, p.run)) < total; run = end) {
           if (!(ok = acc_ready())) break;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
