@@ -102,7 +102,8 @@ struct XentGemm {
   int M, N, K;
   int slices;                        // >= 1; more than the K blocks allow are not used
   int64_t slice_rows;                // rows between two slices of the output map
-  int mn_major;                      // TcMajor bits
+  int mn_major;                      // TcMajor bits; kMnB3d only where N is a multiple of 256 (tiles of other widths
+                                     // do not begin at its 64-column chunks)
   int group_m;
   int epi;
   int add;                           // kXentOutF32

@@ -215,7 +215,7 @@ bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
 // MN-major operand (a row-major [rows][cols] tensor contracted over its rows).
 bool mn_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, bool is_b, int* major) {
   *major |= is_b ? kMnB : kMnA;
-  if (cols % 64 == 0 && make_operand_map_mn3d(m, base, rows, cols, pitch)) {
+  if (cols % (is_b ? 256 : 64) == 0 && make_operand_map_mn3d(m, base, rows, cols, pitch)) {
     *major |= is_b ? kMnB3d : kMnA3d;
     return true;
   }

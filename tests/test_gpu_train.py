@@ -119,6 +119,14 @@ def test_xent_against_64_bits(tp, T, D, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [264, 288, 296, 320, 328, 376, 384, 392, 416, 448, 504, 512])
+def test_xent_widths_of_the_last_tiles(tp, D, dtype):
+    # The gradients' products have a last column of tiles of every width, in steps of 32.
+    X, W, t, dloss = _xent_inputs(270, D, 520, dtype, seed=D)
+    _check_xent(tp, X, W, t, dloss, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,D,V", [
     (1, 1000, 5000), (2, 72, 15), (3, 4104, 700), (4, 64, 16), (5, 8, 17), (7, 520, 2049), (8, 1032, 4000), (9, 72, 64),
     (16, 4096, 300), (17, 256, 1000), (31, 40, 129), (32, 768, 3000), (6, 12000, 90), (32, 6400, 200), (2, 60000, 40),
