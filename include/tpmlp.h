@@ -440,6 +440,10 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  * gradient. An id at or above V is left out in the same way and records
  * TPMLP_ERR_BOUNDS (check 8 for a target, 9 for a token) for the next
  * tpmlp_check_status(). T and V are at most 2^30, D at most 2^20.
+ *
+ * Ids may stand on any 8-byte boundary (targets = ids + 1) and loss, lse, dloss
+ * and norm on any 4-byte one. Outputs and workspace overlap neither an input
+ * nor one another, unless a call says so.
  * ---------------------------------------------------------------------- */
 
 /* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward

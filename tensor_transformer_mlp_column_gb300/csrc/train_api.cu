@@ -25,7 +25,11 @@ namespace {
     if (e_ != cudaSuccess) return set_error(TPMLP_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_));   \
   } while (0)
 
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool al16(const void* p) { return aligned(p, 16); }
+// Ids and one value a row are loaded one at a time: targets may be ids + 1.
+bool al_ids(const int64_t* p) { return aligned(p, 8); }
+bool al_rows(const float* p) { return aligned(p, 4); }
 
 uint64_t wait_ns() {
   const char* s = getenv("TPMLP_WAIT_LIMIT_MS");
@@ -174,7 +178,7 @@ int grad_call(const void* const* grads, const int64_t* counts, const tpmlp_dtype
   if (clip && !(max_norm >= 0.f && std::isfinite(max_norm)))
     return set_error(TPMLP_ERR_ARG, "max_norm = %g must be finite and >= 0", double(max_norm));
   if (!norm || !ws) return set_error(TPMLP_ERR_ARG, "norm and workspace must not be NULL");
-  if (!al16(norm) || !al16(ws)) return set_error(TPMLP_ERR_ALIGN, "norm and workspace must be 16-byte aligned");
+  if (!al_rows(norm) || !al16(ws)) return set_error(TPMLP_ERR_ALIGN, "workspace must be 16-byte aligned, norm 4");
   const size_t need = clip_workspace(nonempty(counts, n));
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if (clip && (rc = check_overlap(grads, counts, dts, n, out))) return rc;
@@ -208,8 +212,8 @@ int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int
   if (rc) return rc;
   if (T == 0) return TPMLP_OK;
   if (!X || !W || !targets || !loss || !lse || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
-  if (!al16(X) || !al16(W) || !al16(targets) || !al16(loss) || !al16(lse) || !al16(ws))
-    return set_error(TPMLP_ERR_ALIGN, "X, W, targets, loss, lse and workspace must be 16-byte aligned");
+  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(loss) || !al_rows(lse) || !al16(ws))
+    return set_error(TPMLP_ERR_ALIGN, "X, W and workspace must be 16-byte aligned, targets 8, loss and lse 4");
   const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 0).total;
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if ((rc = current_sm103())) return rc;
@@ -231,8 +235,8 @@ int tpmlp_xent_backward(const void* X, const void* W, const int64_t* targets, co
     return TPMLP_OK;
   }
   if (!X || !W || !targets || !lse || !dloss || !dX || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
-  if (!al16(X) || !al16(W) || !al16(targets) || !al16(lse) || !al16(dloss) || !al16(dX) || !al16(ws))
-    return set_error(TPMLP_ERR_ALIGN, "X, W, targets, lse, dloss, dX and workspace must be 16-byte aligned");
+  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(lse) || !al_rows(dloss) || !al16(dX) || !al16(ws))
+    return set_error(TPMLP_ERR_ALIGN, "X, W, dX and workspace must be 16-byte aligned, targets 8, lse and dloss 4");
   const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 1).total;
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if ((rc = current_sm103())) return rc;
@@ -247,7 +251,7 @@ int tpmlp_embed_forward(const void* E, const int64_t* ids, int64_t T, int64_t D,
   if (!known(dt)) return set_error(TPMLP_ERR_ARG, "unknown dtype %d", int(dt));
   if (T == 0) return TPMLP_OK;
   if (!E || !ids || !out) return set_error(TPMLP_ERR_ARG, "E, ids and out must not be NULL");
-  if (!al16(E) || !al16(ids) || !al16(out)) return set_error(TPMLP_ERR_ALIGN, "E, ids and out must be 16-byte aligned");
+  if (!al16(E) || !al_ids(ids) || !al16(out)) return set_error(TPMLP_ERR_ALIGN, "E and out must be 16-byte aligned, ids 8");
   if ((rc = current_sm103())) return rc;
   TraceScope trace("embed", stream);
   TRAIN_TRY(launch_embed(E, ids, T, D, V, dt == TPMLP_BF16, scale, out, device_status_word(), stream));
@@ -269,8 +273,8 @@ int tpmlp_embed_backward(const void* dout, tpmlp_dtype dout_dt, const int64_t* i
     return set_error(dE ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "dE must not be NULL and must be 16-byte aligned");
   if (T > 0) {
     if (!dout || !ids || !ws) return set_error(TPMLP_ERR_ARG, "dout, ids and workspace must not be NULL");
-    if (!al16(dout) || !al16(ids) || !al16(ws))
-      return set_error(TPMLP_ERR_ALIGN, "dout, ids and workspace must be 16-byte aligned");
+    if (!al16(dout) || !al_ids(ids) || !al16(ws))
+      return set_error(TPMLP_ERR_ALIGN, "dout and workspace must be 16-byte aligned, ids 8");
     const size_t need = plan_embed(T, D, V).total;
     if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   } else if (accumulate) {

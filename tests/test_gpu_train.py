@@ -496,6 +496,75 @@ def test_clip_of_views_and_refusals(tp):
         tp.tpmlp_grad_clip([flat], 1.0, out=[flat[:10]])
 
 
+# ------------------------------------------------------------------ beyond 2^31 elements
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_xent_of_more_than_2_31_weights(tp, T):
+    D, V = 8, (1 << 28) + 77
+    g = torch.Generator(device="cuda").manual_seed(T)
+    W = torch.randn(V, D, generator=g, device="cuda").bfloat16()
+    X = torch.randn(T, D, generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    t[0], t[1], t[2] = V - 1, 0, (1 << 28) + 3
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, dloss)
+    tp.tpmlp_check_status()
+    x, step = X.double(), 1 << 22
+    sums = torch.zeros(T, dtype=torch.float64, device="cuda")
+    for v in range(0, V, step):
+        sums += torch.exp(x @ W[v:v + step].double().T).sum(1)
+    ref = torch.log(sums)
+    zt = (x * W[t].double()).sum(1)
+    # A thread adds at most 2^21 / 128 parts one after the other (3 rows: fewer); logits and logarithm as above.
+    ez = 16 * U32 * ((x.abs() @ W[:step].double().abs().T).max(1).values + 40)
+    el = (1 << 14) * 2 * U32 + ez
+    _close(lse, ref, el, "lse")
+    _close(loss, ref - zt, el + ez, "loss")
+    rX, mag = torch.zeros_like(x), torch.zeros_like(x)
+    for v in range(0, V, step):
+        w = W[v:v + step].double()
+        dz = torch.exp(x @ w.T - ref[:, None])
+        here = (t >= v) & (t < v + step)
+        dz[here, t[here] - v] -= 1
+        dz *= dloss.double()[:, None]
+        rX += dz @ w
+        mag += dz.abs() @ w.abs()
+        if v == 0 or v + 2 * step > V:  # the first piece and what lies around and behind 2^31 elements
+            r, m = dz.T @ x, dz.abs().T @ x.abs()
+            _close(dW[v:v + step], r, m * (1.01 * U16 + 2 * (ez + el).max() + 1e-5) + 1.01 * U16 * r.abs() + 1e-30, "dW")
+    # dX: dz's rounding, and sums in slices of under 2^22 ids, 16 to an addition, then of at most 80 pieces.
+    _close(dX, rX, mag * (1.01 * U16 + 2 * (ez + el).max() + (2 ** 18 + 80) * 2 * U32) + 1.01 * U16 * rX.abs(), "dX")
+
+
+def test_embed_of_more_than_2_31_elements(tp):
+    D, V = 4096, (1 << 19) + 1000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    E = torch.randn(V, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randperm(V, generator=g, device="cuda")
+    assert torch.equal(tp.tpmlp_embed_forward(E, ids), E[ids])
+    dE = tp.tpmlp_embed_backward(E, ids, V)
+    assert torch.equal(dE[ids], E)  # each id once: its row of dout
+    few = torch.tensor([V - 1, 3, V - 1, 1 << 19], device="cuda")
+    dE = tp.tpmlp_embed_backward(E[:4], few, V)
+    ref = torch.zeros_like(E)
+    ref[V - 1], ref[3], ref[1 << 19] = (E[0].float() + E[2].float()).bfloat16(), E[1], E[3]
+    assert torch.equal(dE, ref)
+    tp.tpmlp_check_status()
+
+
+def test_clip_of_more_than_2_31_elements(tp):
+    a = torch.full(((1 << 31) + 4099,), 0.5, device="cuda", dtype=torch.bfloat16)
+    a[-1] = -1.5
+    norm = tp.tpmlp_grad_clip([a[:8], a[8:]], 2.0 ** 13)
+    want = math.sqrt(0.25 * (a.numel() - 1) + 2.25)  # every partial sum is exact
+    assert abs(norm.item() - want) <= U32 * want
+    c = 2.0 ** 13 / (want + 1e-6)
+    for got, v in ((a[:-1].amax(), 0.5), (a[:-1].amin(), 0.5), (a[-1], -1.5)):
+        assert abs(got.item() - c * v) <= (1.01 * U16 + 4 * U32) * abs(c * v)
+
+
 # ------------------------------------------------------------------ together
 
 
@@ -645,6 +714,33 @@ def test_calls_in_two_streams_at_once(tp):
         for k, x, y in got:
             assert all(torch.equal(u, v) for u, v in zip(x, ra[k])), k
             assert all(torch.equal(u, v) for u, v in zip(y, rb[k])), k
+    tp.tpmlp_check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,V", [(63, 64, 300), (300, 264, 1000), (2101, 72, 700)])
+def test_ids_and_rows_on_their_own_boundaries(tp, T, D, V, dtype):
+    # The targets of next-token prediction are the ids one further on; loss, lse and dloss parts of larger tensors.
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T)
+    row = torch.cat([t[:1], t])
+
+    def shifted(v):
+        return torch.cat([v[:1], v])[1:]
+
+    loss, lse = (torch.zeros(T + 2, device="cuda") for _ in range(2))
+    tp.tpmlp_xent_forward(X, W, row[1:], loss=loss[1:-1], lse=lse[1:-1])
+    ref = tp.tpmlp_xent_forward(X, W, t)
+    assert torch.equal(loss[1:-1], ref[0]) and torch.equal(lse[1:-1], ref[1])
+    assert loss[0] == loss[-1] == lse[0] == lse[-1] == 0
+    got = tp.tpmlp_xent_backward(X, W, row[1:], lse[1:-1], shifted(dloss))
+    for a, b in zip(got, tp.tpmlp_xent_backward(X, W, t, ref[1], dloss)):
+        assert torch.equal(a, b)
+    ids = t.clamp(min=0)
+    assert torch.equal(tp.tpmlp_embed_forward(W, shifted(ids)), tp.tpmlp_embed_forward(W, ids))
+    assert torch.equal(tp.tpmlp_embed_backward(X, shifted(ids), V), tp.tpmlp_embed_backward(X, ids, V))
+    norms = torch.zeros(3, device="cuda")
+    tp.tpmlp_grad_norm([X, W], norm=norms[1:2])
+    assert norms[1] == tp.tpmlp_grad_norm([X, W])[0] and norms[0] == norms[2] == 0
     tp.tpmlp_check_status()
 
 

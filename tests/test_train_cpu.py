@@ -60,8 +60,8 @@ SIZES = [
     (dict(lse=None), "TPMLP_ERR_ARG"),
     (dict(ws=None), "TPMLP_ERR_ARG"),
     (dict(X=FAKE + 2), "TPMLP_ERR_ALIGN"),
-    (dict(t=FAKE + 8), "TPMLP_ERR_ALIGN"),
-    (dict(lse=FAKE + 4), "TPMLP_ERR_ALIGN"),
+    (dict(t=FAKE + 4), "TPMLP_ERR_ALIGN"),
+    (dict(lse=FAKE + 2), "TPMLP_ERR_ALIGN"),
     (dict(nb=0), "TPMLP_ERR_WORKSPACE"),
     (dict(T=0, X=None, loss=None, ws=None, nb=0), "TPMLP_OK"),  # no rows: nothing enqueued
 ])
@@ -77,7 +77,7 @@ def test_xent_forward_argument_errors(tp, kw, code):
     (dict(dW=None, T=0), "TPMLP_ERR_ARG"),
     (dict(dloss=None), "TPMLP_ERR_ARG"),
     (dict(dW=FAKE + 8), "TPMLP_ERR_ALIGN"),
-    (dict(dloss=FAKE + 4), "TPMLP_ERR_ALIGN"),
+    (dict(dloss=FAKE + 2), "TPMLP_ERR_ALIGN"),
     (dict(nb=16), "TPMLP_ERR_WORKSPACE"),
 ])
 def test_xent_backward_argument_errors(tp, kw, code):
@@ -102,7 +102,7 @@ def test_embed_forward_argument_errors(tp, kw, code):
     (dict(dE=None), "TPMLP_ERR_ARG"),
     (dict(dE=None, T=0), "TPMLP_ERR_ARG"),
     (dict(dout=None), "TPMLP_ERR_ARG"),
-    (dict(ids=FAKE + 8), "TPMLP_ERR_ALIGN"),
+    (dict(ids=FAKE + 4), "TPMLP_ERR_ALIGN"),
     (dict(dE=FAKE + 4), "TPMLP_ERR_ALIGN"),
     (dict(nb=8), "TPMLP_ERR_WORKSPACE"),
     (dict(T=0, acc=1, dout=None, ids=None, ws=None, nb=0), "TPMLP_OK"),  # adds nothing
@@ -153,7 +153,7 @@ def test_clip_argument_errors(tp):
         assert _clip(tp, **ok, max_norm=bad) == "TPMLP_ERR_ARG"
     assert _clip(tp, **ok, norm=None) == "TPMLP_ERR_ARG"
     assert _clip(tp, **ok, ws=None) == "TPMLP_ERR_ARG"
-    assert _clip(tp, **ok, norm=FAKE - 4092) == "TPMLP_ERR_ALIGN"
+    assert _clip(tp, **ok, norm=FAKE - 4094) == "TPMLP_ERR_ALIGN"
     assert _clip(tp, **ok, nb=8) == "TPMLP_ERR_WORKSPACE"
     assert _clip(tp, **ok, nb=8, clip=False) == "TPMLP_ERR_WORKSPACE"
     assert _clip(tp, [FAKE], [4], [7], clip=False) == "TPMLP_ERR_ARG"
