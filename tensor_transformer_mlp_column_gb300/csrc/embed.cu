@@ -17,6 +17,8 @@
 // Most rows of a large table get no gradient and are cleared, by CTAs that
 // alternate with the summing ones, all but a first part that fills the time
 // of the sort.
+#include <atomic>
+
 #include "device.cuh"
 #include "internal.h"
 #include "trace.h"
@@ -444,10 +446,6 @@ cudaError_t cluster_sort(const int64_t* ids, int64_t T, int64_t V, uint32_t* key
   int all = 1;
   while ((V >> all) != 0) ++all;  // bits of the keys 0 .. V
   const int passes = (all + 8) / 9, bits = (all + passes - 1) / passes;
-  // One CTA an SM; clearing takes as many clusters as 64 KB for each of their CTAs justify.
-  int64_t clusters = 1 + (clear_bytes + 65536 * kSortCtas - 1) / (65536 * kSortCtas);
-  const int64_t cap = num_sms() / kSortCtas > 2 ? num_sms() / kSortCtas : 2;
-  if (clusters > cap) clusters = cap;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kSortCtas;
@@ -456,11 +454,31 @@ cudaError_t cluster_sort(const int64_t* ids, int64_t T, int64_t V, uint32_t* key
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kSortCtas));
+  cfg.gridDim = dim3(kSortCtas);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
+  // Clearing takes as many clusters as 64 KB for each of their CTAs justify and
+  // as run at once: not every SM finds seven others for one (15 clusters; two
+  // more begin when the first are done, T = 4096, V = 50257, D = 768: the sort
+  // 14.6 -> 18.7 us).
+  int64_t clusters = 1 + (clear_bytes + 65536 * kSortCtas - 1) / (65536 * kSortCtas);
+  if (clusters > 1) {
+    static std::atomic<int> max_clusters[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    int cap = max_clusters[dev].load(std::memory_order_relaxed);
+    if (!cap) {
+      cfg.numAttrs = 1;  // the query takes the cluster shape only
+      if ((e = cudaOccupancyMaxActiveClusters(&cap, kern, &cfg)) != cudaSuccess) return e;
+      if (cap < 2) cap = 2;
+      max_clusters[dev].store(cap, std::memory_order_relaxed);
+    }
+    if (clusters > cap) clusters = cap;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kSortCtas));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, ids, T, V, bits, passes, key, pos, present, clear, clear_bytes, status);
 }
@@ -485,7 +503,10 @@ struct Clear {
   uint32_t magic;        // ceil(2^32 / row_pieces), where 1 < row_pieces < kClearPieces, else 0
   int piece;
   int ctas;
-  // The CTAs in their order: every `period`-th one is of the rarer kind, as long as there are any.
+  // The CTAs in their order: every `period`-th one is of the rarer kind, as
+  // long as there are any. Rare summing CTAs are every second one at first:
+  // theirs are the long chains of loads (T = 4096, V = 50257, D = 768: 30 us
+  // spread over the grid, 26.5 so).
   int period, sums_rare;
 };
 
@@ -651,28 +672,31 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
   }
 }
 
-// The long segments that begin in one of the chunks 32 blockIdx.x .. + 31: adds
+// The long segments that begin in one of `span` consecutive chunks: adds
 // their parts in order and writes the table row. A CTA takes 32 N columns;
 // its eight warps take consecutive eighths of a segment's parts and their
 // sums are added in the warps' order, so that one id repeated T times is
 // still spread over the GPU.
-constexpr int kJoinChunks = 32;
+// Few chunks a CTA where that makes no more than a round or two of CTAs: the
+// segments of one CTA go one after the other (T = 16384, D = 1024, bf16: 10.5
+// us with 32, 8.4 with 4).
+int join_span(int64_t chunks, int64_t columns) { return (chunks + 3) / 4 * columns <= 2048 ? 4 : 32; }
 template <typename E, int N>
 __global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restrict__ key, int64_t T, int64_t D, int run,
                                                         float scale, E* __restrict__ dE, int accumulate,
                                                         const float* __restrict__ part,
-                                                        const uint8_t* __restrict__ goes_on, int64_t chunks) {
+                                                        const uint8_t* __restrict__ goes_on, int64_t chunks, int span) {
   __shared__ float red[kThreads / 32][32 * N];
   pdl_wait();
   pdl_launch_dependents();
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  // Lane l looks at chunk 32 blockIdx.x + l (every warp alike).
-  const int64_t mine = int64_t(blockIdx.x) * kJoinChunks + l;
-  const bool owns = mine < chunks && goes_on[mine];
+  // Lane l looks at the CTA's chunk l (every warp alike).
+  const int64_t mine = int64_t(blockIdx.x) * span + l;
+  const bool owns = l < span && mine < chunks && goes_on[mine];
   uint32_t todo = __ballot_sync(0xffffffffu, owns);
   const int64_t col = (int64_t(blockIdx.y) * 32 + l) * N;
   for (; todo; todo &= todo - 1) {
-    const int64_t b = int64_t(blockIdx.x) * kJoinChunks + __ffs(todo) - 1;
+    const int64_t b = int64_t(blockIdx.x) * span + __ffs(todo) - 1;
     const uint32_t k = key[(b + 1) * run - 1];
     // The chunks that the segment reaches are those after b whose first key is k.
     int64_t reach = b + 1;
@@ -758,7 +782,7 @@ cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, in
   if (c.ctas > 0) {
     const int64_t sums = chunks * slabs;
     c.sums_rare = sums <= c.ctas;
-    c.period = static_cast<int>(c.sums_rare ? c.ctas / sums : sums / c.ctas) + 1;
+    c.period = c.sums_rare ? 2 : static_cast<int>(sums / c.ctas) + 1;
   }
   {
     TraceScope trace("embed_segments", s);
@@ -769,13 +793,14 @@ cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, in
   if (T <= 2 * run) return cudaSuccess;  // no segment is longer than that
   TraceScope trace("embed_join", s);
   // Four columns a thread where rows allow, whatever dout's pieces are.
-  const dim3 join4(static_cast<unsigned>((chunks + kJoinChunks - 1) / kJoinChunks), static_cast<unsigned>((D + 127) / 128));
-  const dim3 join1(join4.x, static_cast<unsigned>((D + 31) / 32));
+  const unsigned columns = static_cast<unsigned>(D % 4 == 0 ? (D + 127) / 128 : (D + 31) / 32);
+  const int span = join_span(chunks, columns);
+  const dim3 join(static_cast<unsigned>((chunks + span - 1) / span), columns);
   const float* p = part;
   const uint8_t* on = goes_on;
   return D % 4 == 0
-             ? launch_pdl(join_kernel<E, 4>, join4, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks)
-             : launch_pdl(join_kernel<E, 1>, join1, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks);
+             ? launch_pdl(join_kernel<E, 4>, join, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks, span)
+             : launch_pdl(join_kernel<E, 1>, join, dim3(kThreads), 0, s, key, T, D, run, scale, dE, accumulate, p, on, chunks, span);
 }
 
 template <typename G, typename E>
@@ -841,8 +866,8 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
   clear.row_pieces = static_cast<uint32_t>(row_bytes / clear.piece);
   const bool cluster = T <= kClusterSortMax;
   if (!accumulate) {
-    // The sort in the cluster takes about 8 us and 2 us per 8192 tokens, in which the other SMs write 4 MB a us.
-    if (cluster && clear.piece == 16) clear.row0 = (int64_t(8) + 2 * T / 8192) * (4 << 20) / row_bytes;
+    // The sort in the cluster takes about 8 us and 2 us per 8192 tokens, in which the other SMs write 7 MB a us.
+    if (cluster && clear.piece == 16) clear.row0 = (int64_t(8) + 2 * T / 8192) * (7 << 20) / row_bytes;
     if (clear.row0 > V) clear.row0 = V;
     clear.pieces = (V - clear.row0) * clear.row_pieces;
     const int64_t ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
