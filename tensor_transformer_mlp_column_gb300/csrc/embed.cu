@@ -865,9 +865,12 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
   clear.piece = row_bytes % 16 == 0 ? 16 : dE_bf16 ? 2 : 4;
   clear.row_pieces = static_cast<uint32_t>(row_bytes / clear.piece);
   const bool cluster = T <= kClusterSortMax;
+  int items = 1;  // of a thread in the cluster's sort
+  while (items < kMaxItems && T > int64_t(kSortCtas) * kSortThreads * items) items *= 2;
   if (!accumulate) {
-    // The sort in the cluster takes about 8 us and 2 us per 8192 tokens, in which the other SMs write 7 MB a us.
-    if (cluster && clear.piece == 16) clear.row0 = (int64_t(8) + 2 * T / 8192) * (7 << 20) / row_bytes;
+    // The sort in the cluster takes about 6 + 3 items us, in which the other SMs write 7 MB a us (T = 40000, D =
+    // 4096, V = 128000: 4 MB a us for 8 us and 2 more per 8192 tokens left 239 us in all, this 226).
+    if (cluster && clear.piece == 16) clear.row0 = int64_t(6 + 3 * items) * (7 << 20) / row_bytes;
     if (clear.row0 > V) clear.row0 = V;
     clear.pieces = (V - clear.row0) * clear.row_pieces;
     const int64_t ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
@@ -879,11 +882,11 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
   {
     TraceScope trace("embed_sort", s);
     if (cluster) {
-      const int64_t first = clear.row0 * row_bytes, per_cta = (T + kSortCtas - 1) / kSortCtas;
-      e = per_cta <= kSortThreads       ? cluster_sort<1>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
-          : per_cta <= 2 * kSortThreads ? cluster_sort<2>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
-          : per_cta <= 4 * kSortThreads ? cluster_sort<4>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
-                                        : cluster_sort<kMaxItems>(ids, T, V, key[0], pos[0], present, dE, first, status, s);
+      const int64_t first = clear.row0 * row_bytes;
+      e = items == 1   ? cluster_sort<1>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+          : items == 2 ? cluster_sort<2>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+          : items == 4 ? cluster_sort<4>(ids, T, V, key[0], pos[0], present, dE, first, status, s)
+                       : cluster_sort<kMaxItems>(ids, T, V, key[0], pos[0], present, dE, first, status, s);
       if (e != cudaSuccess) return e;
     } else {
       if ((e = cudaMemsetAsync(present, 0, size_t((V + 31) / 32) * 4, s)) != cudaSuccess) return e;
