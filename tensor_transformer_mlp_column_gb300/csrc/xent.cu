@@ -109,13 +109,23 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 }
 
 // x = high + middle + low, each the bf16 nearest to what the ones before
-// leave: 24 bits in all. n8 groups of 8 elements, planes n8 * 8 apart.
-__global__ void __launch_bounds__(256) xent_split_kernel(const float* __restrict__ x, int64_t n8, uint16_t* __restrict__ out) {
+// leave: 24 bits in all. n8 groups of 8 elements, planes n8 * 8 apart; then
+// the same of a second tensor.
+struct Split {
+  const float* x;
+  int64_t n8;
+  uint16_t* out;
+};
+__global__ void __launch_bounds__(256) xent_split_kernel(Split a, Split b) {
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n8; i += int64_t(gridDim.x) * 256) {
-    const float4 a = reinterpret_cast<const float4*>(x)[2 * i], b = reinterpret_cast<const float4*>(x)[2 * i + 1];
-    float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < a.n8 + b.n8; k += int64_t(gridDim.x) * 256) {
+    const bool first = k < a.n8;
+    const float* __restrict__ x = first ? a.x : b.x;
+    uint16_t* __restrict__ out = first ? a.out : b.out;
+    const int64_t i = first ? k : k - a.n8, n8 = first ? a.n8 : b.n8;
+    const float4 u = reinterpret_cast<const float4*>(x)[2 * i], v = reinterpret_cast<const float4*>(x)[2 * i + 1];
+    float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int pl = 0; pl < kXentPlanes; ++pl) {
       reinterpret_cast<uint4*>(out)[pl * n8 + i] =
@@ -227,11 +237,6 @@ T* at(void* base, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(base) + off);
 }
 
-cudaError_t split(const void* x, int64_t n, void* out, cudaStream_t s) {
-  return launch_pdl(xent_split_kernel, dim3(grid_for(n / 8)), dim3(256), 0, s, static_cast<const float*>(x), n / 8,
-                    static_cast<uint16_t*>(out));
-}
-
 // The bf16 planes of X [T][D] and W [V][D]: the data themselves, or split (of
 // W only where the products read planes of it).
 struct Planes {
@@ -246,8 +251,9 @@ cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_
     out->w[0] = static_cast<const uint16_t*>(W);
     return cudaSuccess;
   }
-  XENT_STEP("xent_split", s, split(X, T * D, at<char>(ws, p.planes_x), s));
-  if (!p.thin) XENT_STEP("xent_split", s, split(W, V * D, at<char>(ws, p.planes_w), s));
+  const Split x{static_cast<const float*>(X), T * D / 8, at<uint16_t>(ws, p.planes_x)};
+  const Split w{static_cast<const float*>(W), p.thin ? 0 : V * D / 8, at<uint16_t>(ws, p.planes_w)};
+  XENT_STEP("xent_split", s, launch_pdl(xent_split_kernel, dim3(grid_for(x.n8 + w.n8)), dim3(256), 0, s, x, w));
   for (int i = 0; i < kXentPlanes; ++i) {
     out->x[i] = at<uint16_t>(ws, p.planes_x) + i * T * D;
     out->w[i] = at<uint16_t>(ws, p.planes_w) + i * V * D;
