@@ -449,7 +449,8 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
 /* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward
  * (backward = 1); 0 for T = 0 and on bad arguments. It grows with T * V / 16
  * bytes forward, and with T * min(V, max(8192, 2^28 / T)) * 2 bytes backward
- * (fp32: more by copies of X and W in bf16 pieces). */
+ * (fp32: more by copies of X and W in bf16 pieces; bf16 with a D off a multiple
+ * of 16: by a copy of X). */
 size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, int backward);
 
 /* Softmax cross entropy over the vocabulary, without keeping the logits:

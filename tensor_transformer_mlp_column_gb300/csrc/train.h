@@ -151,7 +151,9 @@ cudaError_t launch_xent_thin_dx(const XentThin& g, uint64_t wait_ns, cudaStream_
 
 struct XentPlan {
   bool thin;                  // the products with W by groups of kXentThinMax rows
-  size_t planes_x, planes_w;  // fp32: bf16 planes [3][T][D], [3][V][D]
+  bool copy_x, copy_w;        // the products read planes of X, of W (else the data themselves)
+  int64_t pitch_x, pitch_w;   // elements from one of their rows to the next
+  size_t planes_x, planes_w;  // the planes: [3][T][pitch_x], [3][V][pitch_w] of fp32 data, else one
   size_t stats, zt;           // forward
   size_t dmax, dz, dx, dw;    // backward
   size_t total;

@@ -108,30 +108,40 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// x = high + middle + low, each the bf16 nearest to what the ones before
-// leave: 24 bits in all. n8 groups of 8 elements, planes n8 * 8 apart; then
-// the same of a second tensor.
-struct Split {
-  const float* x;
-  int64_t n8;
+// A tensor's rows of d8 groups of 8 elements, copied into one (bf16) or three
+// planes (fp32) with rows pitch8 groups apart, `plane` groups from one to the
+// next.
+struct PlaneCopy {
+  const void* x;
+  int64_t rows, d8, pitch8, plane;
   uint16_t* out;
 };
-__global__ void __launch_bounds__(256) xent_split_kernel(Split a, Split b) {
+
+// Planes of two tensors. fp32: x = high + middle + low, each the bf16 nearest
+// to what the ones before leave, 24 bits in all.
+template <bool F32>
+__global__ void __launch_bounds__(256) xent_planes_kernel(PlaneCopy a, PlaneCopy b) {
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < a.n8 + b.n8; k += int64_t(gridDim.x) * 256) {
-    const bool first = k < a.n8;
-    const float* __restrict__ x = first ? a.x : b.x;
-    uint16_t* __restrict__ out = first ? a.out : b.out;
-    const int64_t i = first ? k : k - a.n8, n8 = first ? a.n8 : b.n8;
-    const float4 u = reinterpret_cast<const float4*>(x)[2 * i], v = reinterpret_cast<const float4*>(x)[2 * i + 1];
-    float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  const int64_t na = a.rows * a.d8, n = na + b.rows * b.d8;
+  for (int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x; k < n; k += int64_t(gridDim.x) * 256) {
+    const PlaneCopy& c = k < na ? a : b;
+    const int64_t i = k < na ? k : k - na;
+    int64_t to = i;
+    if (c.pitch8 != c.d8) to += (i >> 32 ? i / c.d8 : static_cast<uint32_t>(i) / static_cast<uint32_t>(c.d8)) * (c.pitch8 - c.d8);
+    uint4* out = reinterpret_cast<uint4*>(c.out) + to;
+    if constexpr (!F32) {
+      *out = static_cast<const uint4*>(c.x)[i];
+    } else {
+      const float4 u = static_cast<const float4*>(c.x)[2 * i], v = static_cast<const float4*>(c.x)[2 * i + 1];
+      float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int pl = 0; pl < kXentPlanes; ++pl) {
-      reinterpret_cast<uint4*>(out)[pl * n8 + i] =
-          make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+      for (int pl = 0; pl < kXentPlanes; ++pl) {
+        out[pl * c.plane] =
+            make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] -= __bfloat162float(__float2bfloat16_rn(f[j]));
+        for (int j = 0; j < 8; ++j) f[j] -= __bfloat162float(__float2bfloat16_rn(f[j]));
+      }
     }
   }
 }
@@ -237,26 +247,28 @@ T* at(void* base, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(base) + off);
 }
 
-// The bf16 planes of X [T][D] and W [V][D]: the data themselves, or split (of
-// W only where the products read planes of it).
+// The bf16 planes of X [T][D] and W [V][D], rows pitch_x and pitch_w apart:
+// the data themselves, or copies (of W only where the products read planes of
+// it).
 struct Planes {
   const uint16_t *x[kXentPlanes], *w[kXentPlanes];
+  int64_t pitch_x, pitch_w;
   int n;
 };
 cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int is_bf16, void* ws,
                       const XentPlan& p, Planes* out, cudaStream_t s) {
   out->n = is_bf16 ? 1 : kXentPlanes;
-  if (is_bf16) {
-    out->x[0] = static_cast<const uint16_t*>(X);
-    out->w[0] = static_cast<const uint16_t*>(W);
-    return cudaSuccess;
-  }
-  const Split x{static_cast<const float*>(X), T * D / 8, at<uint16_t>(ws, p.planes_x)};
-  const Split w{static_cast<const float*>(W), p.thin ? 0 : V * D / 8, at<uint16_t>(ws, p.planes_w)};
-  XENT_STEP("xent_split", s, launch_pdl(xent_split_kernel, dim3(grid_for(x.n8 + w.n8)), dim3(256), 0, s, x, w));
-  for (int i = 0; i < kXentPlanes; ++i) {
-    out->x[i] = at<uint16_t>(ws, p.planes_x) + i * T * D;
-    out->w[i] = at<uint16_t>(ws, p.planes_w) + i * V * D;
+  out->pitch_x = p.pitch_x;
+  out->pitch_w = p.pitch_w;
+  const PlaneCopy x{X, p.copy_x ? T : 0, D / 8, p.pitch_x / 8, T * p.pitch_x / 8, at<uint16_t>(ws, p.planes_x)};
+  const PlaneCopy w{W, p.copy_w ? V : 0, D / 8, p.pitch_w / 8, V * p.pitch_w / 8, at<uint16_t>(ws, p.planes_w)};
+  if (p.copy_x || p.copy_w)
+    XENT_STEP("xent_planes", s,
+              launch_pdl(is_bf16 ? xent_planes_kernel<false> : xent_planes_kernel<true>,
+                         dim3(grid_for((x.rows + w.rows) * x.d8)), dim3(256), 0, s, x, w));
+  for (int i = 0; i < out->n; ++i) {
+    out->x[i] = p.copy_x ? x.out + i * T * p.pitch_x : static_cast<const uint16_t*>(X);
+    out->w[i] = p.copy_w ? w.out + i * V * p.pitch_w : static_cast<const uint16_t*>(W);
   }
   return cudaSuccess;
 }
@@ -294,7 +306,7 @@ bool thin_maps(XentThin* h, const void* W, const Planes& pl, int64_t t0, int64_t
   h->K = static_cast<int>(D);
   h->slices = 1;
   for (int i = 0; i < pl.n; ++i)
-    if (!make_operand_map(&h->map_b[i], pl.x[i] + t0 * D, rows, D, D, xent_thin_columns(rows))) return false;
+    if (!make_operand_map(&h->map_b[i], pl.x[i] + t0 * pl.pitch_x, rows, D, pl.pitch_x, xent_thin_columns(rows))) return false;
   return h->f32 ? make_output_map_f32(&h->map_w, const_cast<void*>(W), n, D, D) : make_operand_map(&h->map_w, W, n, D, D, 128);
 }
 
@@ -355,6 +367,16 @@ static bool use_thin(int64_t T, int64_t D, int64_t V, int is_bf16) {
   return T <= kXentThinMax || (!is_bf16 && T <= 3 * kXentThinMax && V * D >= (int64_t(1) << 24));
 }
 
+// Whether the products read a copy of bf16 X, on rows of whole 128-byte lines:
+// rows that begin off the 32-byte sectors of the L2 slow TMA's loads. A copy
+// costs a launch and T D, it saves a part of T V D (V = 30011, D = 1032, loss
+// and gradients: T = 200 100 -> 98.5 us, 1000 245 -> 238, 8000 1.46 -> 1.40 ms;
+// V = 3001, T = 1000 57 -> 59 us, 8000 192 -> 198). A copy of W saves less than
+// it costs up to T = 8000.
+static bool copies_x(int64_t T, int64_t D, int64_t V, int thin) {
+  return !thin && D % 16 != 0 && V >= 8192 && T * V >= (int64_t(1) << 32) / D;
+}
+
 XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
   XentPlan p{};
   size_t off = 0;
@@ -365,10 +387,12 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
   };
   const int planes = is_bf16 ? 1 : kXentPlanes, pairs = is_bf16 ? 1 : kXentPairs;
   p.thin = use_thin(T, D, V, is_bf16);
-  if (!is_bf16) {
-    p.planes_x = take(size_t(T) * D * 2 * planes);
-    if (!p.thin) p.planes_w = take(size_t(V) * D * 2 * planes);
-  }
+  p.copy_x = !is_bf16 || copies_x(T, D, V, p.thin);
+  p.copy_w = !p.thin && !is_bf16;
+  p.pitch_x = p.copy_x ? ceil_to(D, 64) : D;
+  p.pitch_w = p.copy_w ? ceil_to(D, 64) : D;
+  if (p.copy_x) p.planes_x = take(size_t(T) * p.pitch_x * 2 * planes);
+  if (p.copy_w) p.planes_w = take(size_t(V) * p.pitch_w * 2 * planes);
   if (!backward) {
     const int64_t parts = p.thin ? xent_thin_parts(V) : (V + kXentPart - 1) / kXentPart;
     p.stats = take(size_t(parts) * T * sizeof(float2));
@@ -416,7 +440,7 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
   }
   XentGemm g{};
   for (int i = 0; i < pl.n; ++i)
-    if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i], V, D, D))
+    if (!operand_map(&g.map_a[i], pl.x[i], T, D, pl.pitch_x) || !operand_map(&g.map_b[i], pl.w[i], V, D, pl.pitch_w))
       return cudaErrorInvalidValue;
   g.pairs = pl.n == 1 ? 1 : kXentPairs;
   g.M = static_cast<int>(T);
@@ -473,7 +497,8 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
       XENT_STEP("xent_dz", s, launch_xent_thin_dz(h, wait_ns, s));
     }
     for (int i = 0; !p.thin && i < pl.n; ++i)
-      if (!operand_map(&g.map_a[i], pl.x[i], T, D, D) || !operand_map(&g.map_b[i], pl.w[i] + v0 * D, vc, D, D) ||
+      if (!operand_map(&g.map_a[i], pl.x[i], T, D, pl.pitch_x) ||
+          !operand_map(&g.map_b[i], pl.w[i] + v0 * pl.pitch_w, vc, D, pl.pitch_w) ||
           !make_output_map_bf16(&g.map_out[i], dz[i], T, vp, p.dz_pitch))
         return cudaErrorInvalidValue;
     g.pairs = pairs;
@@ -496,7 +521,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g = XentGemm{};
     for (int i = 0; i < pl.n; ++i)
       if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major) ||
-          !mn_map(&g.map_b[i], pl.x[i], T, D, D, true, &g.mn_major))
+          !mn_map(&g.map_b[i], pl.x[i], T, D, pl.pitch_x, true, &g.mn_major))
         return cudaErrorInvalidValue;
     g.pairs = pairs;
     g.M = static_cast<int>(vc);
@@ -537,7 +562,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g = XentGemm{};
     for (int i = 0; i < pl.n; ++i)
       if (!operand_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch) ||
-          !mn_map(&g.map_b[i], pl.w[i] + v0 * D, vc, D, D, true, &g.mn_major))
+          !mn_map(&g.map_b[i], pl.w[i] + v0 * pl.pitch_w, vc, D, pl.pitch_w, true, &g.mn_major))
         return cudaErrorInvalidValue;
     g.pairs = pairs;
     g.M = static_cast<int>(T);

@@ -127,6 +127,14 @@ def test_xent_widths_of_the_last_tiles(tp, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,V", [(600, 1032, 8300), (2100, 56, 70001), (70, 7400, 8300), (9000, 24, 30001)])
+def test_xent_rows_off_the_sectors(tp, T, D, V, dtype):
+    # The products read X (fp32: and W) from copies on rows of whole lines.
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=D)
+    _check_xent(tp, X, W, t, dloss, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,D,V", [
     (1, 1000, 5000), (2, 72, 15), (3, 4104, 700), (4, 64, 16), (5, 8, 17), (7, 520, 2049), (8, 1032, 4000), (9, 72, 64),
     (16, 4096, 300), (17, 256, 1000), (31, 40, 129), (32, 768, 3000), (6, 12000, 90), (32, 6400, 200), (2, 60000, 40),
