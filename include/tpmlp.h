@@ -449,8 +449,8 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
 /* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward
  * (backward = 1); 0 for T = 0 and on bad arguments. It grows with T * V / 16
  * bytes forward, and with T * min(V, max(8192, 2^28 / T)) * 2 bytes backward
- * (fp32: more by copies of X and W in bf16 pieces; bf16 with a D off a multiple
- * of 16: by a copy of X). */
+ * (twice that for up to 64 rows; fp32: more by copies of X and W in bf16 pieces;
+ * bf16 with a D off a multiple of 16: by a copy of X). */
 size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, int backward);
 
 /* Softmax cross entropy over the vocabulary, without keeping the logits:
@@ -476,7 +476,8 @@ int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int
  *   dloss    device fp32 [T] (for the mean over the rows that count: 1 / their number).
  *   dX       device [T, D], dW device [V, D], of type dt (dX is the upstream
  *            gradient that tpmlp_block_backward takes); both are written. In
- *            bf16 dz is rounded to bf16 as an operand and each result once.
+ *            bf16 dz is rounded to bf16 as an operand (for up to 64 rows to two
+ *            bf16 pieces) and each result once.
  *            T = 0 clears dW.
  *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 1) bytes.
  * Rows that do not count must still hold finite X: they enter dW's product

@@ -98,7 +98,7 @@ struct XentDmax {
 struct XentGemm {
   CUtensorMap map_a[kXentPlanes], map_b[kXentPlanes];
   CUtensorMap map_out[kXentPlanes];  // bf16: make_output_map_bf16; fp32: make_output_map_f32, slices stacked by rows
-  int pairs;                         // 1 or kXentPairs
+  int pairs;                         // of planes: 1; kThinDzPlanes of A with one of B; kXentPairs
   int M, N, K;
   int slices;                        // >= 1; more than the K blocks allow are not used
   int64_t slice_rows;                // rows between two slices of the output map
@@ -123,6 +123,10 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
 
 // The products with W for up to kXentThinMax rows of X at a time (xent_thin.cu).
 constexpr int kXentThinMax = 64;
+// Planes of their dz of bf16 data: a single row's gradient of a target would
+// carry the rounding of its dz as a whole (2^-9), where those of many rows and
+// ids average out, and the products are bound by W either way.
+constexpr int kThinDzPlanes = 2;
 struct XentThin {
   CUtensorMap map_w;                // W: fp32, make_output_map_f32 (32 x 32 boxes); bf16, make_operand_map (K-major: 128
                                     // rows; for dX: 64 rows)
@@ -159,6 +163,7 @@ struct XentPlan {
   size_t total;
   int64_t piece;              // columns of a piece of the vocabulary (a multiple of 256, or V)
   int64_t dz_pitch;           // columns of dz's rows
+  int dz_planes;
   int slices_x, slices_w;     // slices of the dX and dW products
   bool dx_part;               // dX goes through fp32 partial sums
 };

@@ -39,13 +39,16 @@ namespace {
     if (e_ != cudaSuccess) return e_;      \
   } while (0)
 
-// Row t's parts joined: lse = (M + log2 sum_i s_i 2^(m_i - M)) / log2 e. A CTA
-// takes R rows, its warps (and the lanes that share a row) every so many parts
-// each, joined in a fixed order.
-// The last additions are in fp64: M is in units of log2, where a rounding to
-// fp32 weighs more than in lse, and a target that is nearly certain leaves a
-// loss far below lse, which the fp32 difference would lose. log2 e is the same
-// fp32 constant that scaled the logits.
+// Row t's parts joined. They hold every id but the target: with S 2^M their
+// sum of exponentials (M in units of log2) and e = S 2^M / exp(z) of the
+// target's z,
+//   loss = log(1 + e),   lse = z + loss,
+// which keeps its digits where the target is nearly certain and lse - z would
+// lose them. A row that does not count has lse = (M + log2 S) / log2 e. log2 e
+// is the same fp32 constant that scaled the logits. A CTA takes R rows, its
+// warps (and the lanes that share a row) every so many parts each, joined in a
+// fixed order.
+// M - z log2 e is in fp64: a rounding to fp32 would weigh as much as one of z.
 // R = 4 rows a CTA where there are few rows: 128 threads share a row's parts.
 constexpr int kJoinWarps = 16;
 template <int R>
@@ -79,10 +82,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   __syncthreads();
   if (w != 0 || l >= R || t >= T) return;
   for (int i = 1; i < kJoinWarps; ++i) add(red[i][l]);
-  const double v = (double(m) + double(log2f(s))) * (1.0 / double(kXentLog2e));
   if (target >= V) atomicCAS(status, 0, kSiteBoundsBase + kChkTarget);
-  lse[t] = static_cast<float>(v);
-  loss[t] = target >= 0 && target < V ? static_cast<float>(v - double(z)) : 0.f;
+  // log2 of s with its exponent apart, where a rounding to fp32 weighs less.
+  const int k = s >= 1.f && s < INFINITY ? ilogbf(s) : 0;
+  const double ln2 = 1.0 / double(kXentLog2e);
+  double whole = (double(m) + double(k) + double(log2f(ldexpf(s, -k)))) * ln2, own = 0.0;
+  if (target >= 0 && target < V) {
+    const double x = double(m) - double(z) * double(kXentLog2e);  // log2 (e / S)
+    if (!(z < INFINITY)) {
+      whole = own = double(z - z);
+    } else if (m == -INFINITY) {
+      whole = double(z);  // there is no other id
+    } else if (x < 30.0) {
+      const double i = rint(fmax(x, -200.0));
+      const float e = ldexpf(s * exp2f(static_cast<float>(fmax(x, -200.0) - i)), static_cast<int>(i));
+      own = double(log1pf(e));
+      whole = double(z) + own;
+    } else {  // the target's own share of the sum is below the rounding
+      own = whole - double(z);
+    }
+  }
+  lse[t] = static_cast<float>(whole);
+  loss[t] = static_cast<float>(own);
 }
 
 // parts[b] = the largest finite |dloss| among CTA b's rows that count.
@@ -400,14 +421,15 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
     p.total = off;
     return p;
   }
-  p.piece = choose_piece(T, D, V, planes);
+  p.dz_planes = is_bf16 && p.thin ? kThinDzPlanes : planes;
+  p.piece = choose_piece(T, D, V, p.dz_planes);
   const int64_t piece = p.piece;
   p.dz_pitch = ceil_to(piece, 64);
   p.dmax = take(kXentDmaxParts * 4);
-  p.dz = take(size_t(T) * p.dz_pitch * 2 * planes);
+  p.dz = take(size_t(T) * p.dz_pitch * 2 * p.dz_planes);
   p.slices_x = p.thin ? xent_thin_slices(D, p.dz_pitch)
                       : xent_slices(static_cast<int>(p.dz_pitch), choose_slices(T, D, p.dz_pitch, pairs));
-  p.slices_w = xent_slices(static_cast<int>(T), choose_slices(piece, D, T, pairs));
+  p.slices_w = xent_slices(static_cast<int>(T), choose_slices(piece, D, T, is_bf16 ? p.dz_planes : pairs));
   p.dx_part = piece < V || p.slices_x > 1 || p.thin;
   if (p.dx_part) p.dx = take(size_t(p.slices_x) * (p.thin ? T : slice_rows(T)) * D * 4);
   if (p.slices_w > 1) p.dw = take(size_t(p.slices_w) * slice_rows(piece) * D * 4);
@@ -474,7 +496,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     rows.rows = 0;
   }
   uint16_t* dz[kXentPlanes];
-  for (int i = 0; i < pl.n; ++i) dz[i] = at<uint16_t>(ws, p.dz) + i * T * p.dz_pitch;
+  for (int i = 0; i < p.dz_planes; ++i) dz[i] = at<uint16_t>(ws, p.dz) + i * T * p.dz_pitch;
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
     const int64_t vc = V - v0 < p.piece ? V - v0 : p.piece, vp = ceil_to(vc, 64);
     const void* W0 = static_cast<const char*>(W) + v0 * D * es;
@@ -519,11 +541,11 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
 
     // dW of the piece = dz^T X.
     g = XentGemm{};
+    for (int i = 0; i < p.dz_planes; ++i)
+      if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major)) return cudaErrorInvalidValue;
     for (int i = 0; i < pl.n; ++i)
-      if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major) ||
-          !mn_map(&g.map_b[i], pl.x[i], T, D, pl.pitch_x, true, &g.mn_major))
-        return cudaErrorInvalidValue;
-    g.pairs = pairs;
+      if (!mn_map(&g.map_b[i], pl.x[i], T, D, pl.pitch_x, true, &g.mn_major)) return cudaErrorInvalidValue;
+    g.pairs = is_bf16 ? p.dz_planes : pairs;
     g.M = static_cast<int>(vc);
     g.N = static_cast<int>(D);
     g.K = static_cast<int>(T);
@@ -550,7 +572,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
         if (!(f32 ? make_output_map_f32(&h.map_w, const_cast<void*>(W0), vc, D, D)
                   : make_operand_map(&h.map_w, W0, vc, D, D, 64)))
           return cudaErrorInvalidValue;
-        for (int i = 0; i < pl.n; ++i)
+        for (int i = 0; i < p.dz_planes; ++i)
           if (!make_operand_map(&h.map_b[i], dz[i] + t0 * p.dz_pitch, h.T, vp, p.dz_pitch, xent_thin_columns(h.T)))
             return cudaErrorInvalidValue;
         XENT_STEP("xent_dX", s, launch_xent_thin_dx(h, wait_ns, s));

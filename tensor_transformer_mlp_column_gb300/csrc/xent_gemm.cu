@@ -84,8 +84,9 @@ struct XParams {
 // The plane pairs in the order in which they are added: small terms first, so
 // that they are not lost against the large ones. Plane 0 is the high one.
 __device__ __forceinline__ void plane_pair(int pairs, int i, int& a, int& b) {
-  if (pairs == 1) {
-    a = b = 0;
+  if (pairs < kXentPairs) {  // A's planes, the small one first
+    a = pairs - 1 - i;
+    b = 0;
     return;
   }
   // (1,1) (0,2) (2,0) (0,1) (1,0) (0,0)
@@ -396,7 +397,10 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           if (h >= 0 && h < 32) {
             float z = v[0];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) z = h == i ? v[i] : z;
+            for (int i = 0; i < 32; ++i) {
+              z = h == i ? v[i] : z;
+              v[i] = h == i ? -INFINITY : v[i];  // left to the join
+            }
             p.g.zt[m] = z;
           }
           if (n0 + 32 > p.g.N) {

@@ -35,6 +35,7 @@
 #include "xent_device.cuh"
 
 #include <atomic>
+#include <climits>
 #include <cstring>
 
 namespace tpmlp {
@@ -51,13 +52,14 @@ enum ThinKind : int { kThinStats = 0, kThinGrad = 1, kThinDx = 2 };
 template <bool F32, int N, int KIND>
 struct TCfg {
   static constexpr int TURNS = !F32 && KIND == kThinStats ? 4 : 1;
-  static constexpr int PL = F32 ? kXentPlanes : 1;
+  static constexpr int PL = F32 ? kXentPlanes : 1;                               // planes of A
+  static constexpr int PLB = F32 ? kXentPlanes : KIND == kThinDx ? kThinDzPlanes : 1;  // of B
   static constexpr int RAW = F32 ? 8 : 0;                                        // stages of raw W
   static constexpr uint32_t A_BYTES = F32 ? 0 : kPlaneBytes;                     // of A in shared memory
   static constexpr uint32_t B_BYTES = N * 64 * 2;                                // one plane of B, 64 K
-  static constexpr uint32_t STAGE = A_BYTES + PL * B_BYTES;                      // operands of 64 K
-  static constexpr int STAGES = F32 ? 3 : 8;
-  static constexpr uint32_t ACC = PL * TURNS * N;                                // columns of the accumulators of a run
+  static constexpr uint32_t STAGE = A_BYTES + PLB * B_BYTES;                     // operands of 64 K
+  static constexpr int STAGES = F32 ? 3 : STAGE > 24576 ? 6 : 8;
+  static constexpr uint32_t ACC = PLB * TURNS * N;                               // columns of the accumulators of a run
   // Two sets, so that a run's epilogue goes on beside the next run; at N = 64
   // of fp32 tensor memory holds one.
   static constexpr int SETS = F32 && N > 32 ? 1 : 2;
@@ -66,6 +68,7 @@ struct TCfg {
   static constexpr uint32_t TMEM = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
   static constexpr size_t SMEM = 1024 + size_t(RAW) * kRawBytes + size_t(STAGES) * STAGE + 512;
   static_assert(USED <= 512, "tensor memory");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct TParams {
@@ -144,8 +147,8 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  __shared__ int64_t s_target[64];
-  __shared__ float s_lse[64], s_rs[64], s_ref[4][64], s_sum[4][64];
+  __shared__ int s_target[64];
+  __shared__ float s_lse[64], s_rs[64], s_ref[4][64], s_sum[4][64], s_base[64];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -218,7 +221,8 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
             } else {
               tma_load_2d_hint(dst, &p.g.map_w, kx, m0, f + st, stream);
             }
-            tma_load_2d_hint(dst + kPlaneBytes, &p.g.map_b[0], kx, 0, f + st, keep);
+            for (int b = 0; b < C::PLB; ++b)
+              tma_load_2d_hint(dst + kPlaneBytes + b * C::B_BYTES, &p.g.map_b[b], kx, 0, f + st, keep);
           }
           if (++st == ST) st = 0, phase ^= 1u;
         }
@@ -245,10 +249,10 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
             tc_fence_after_sync();
             const uint32_t a0 = smem_addr(s_stage + st * C::STAGE), b0 = a0 + C::A_BYTES;
             const uint32_t a_tmem = tmem_base + C::SETS * C::ACC + st * C::A_COLS;
-            // Plane pa of A and the first PL - pa planes of B.
+            // Plane pa of A and the first PLB - pa planes of B.
 #pragma unroll
             for (int pa = 0; pa < C::PL; ++pa) {
-              const uint32_t idesc = idesc_bf16_f32(128, (C::PL - pa) * N, MN && !F32 ? 1 : 0, 0);
+              const uint32_t idesc = idesc_bf16_f32(128, (C::PLB - pa) * N, MN && !F32 ? 1 : 0, 0);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t accumulate = (C::TURNS == 1 && (pa | k) != 0) || q != r ? 1u : 0u;
@@ -283,9 +287,9 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         decode(tile, slice, m0, k0, kbs);
         for (int q = 0; ok && q < kbs; ++q) {
           if (!(ok = wait_bounded(empty + st, phase ^ 1u, guard, kSiteProducer))) break;
-          mbar_arrive_expect_tx(full + st, C::PL * C::B_BYTES);
+          mbar_arrive_expect_tx(full + st, C::PLB * C::B_BYTES);
           uint8_t* dst = s_stage + st * C::STAGE;
-          for (int b = 0; b < C::PL; ++b)
+          for (int b = 0; b < C::PLB; ++b)
             tma_load_2d_hint(dst + b * C::B_BYTES, &p.g.map_b[b], (k0 + q) * 64, 0, full + st, keep);
           if (++st == C::STAGES) st = 0, phase ^= 1u;
         }
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         const bool in = et < p.g.T;
         const int64_t t = in ? p.g.targets[et] : -1;
         const bool counts = t >= 0 && t < p.g.V;
-        s_target[et] = counts ? t - p.g.col0 : -1;
+        s_target[et] = counts ? static_cast<int>(t - p.g.col0) : INT_MIN;  // below 0 too for an earlier piece's
         if constexpr (KIND == kThinGrad) {
           s_lse[et] = in ? p.g.lse[et] : 0.f;
           const float d = in ? p.g.dloss[et] : 0.f;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         if (++acc == C::SETS) acc = 0, acc_phase ^= 1u;
       }
       if (!ok) break;
-      const int64_t m = m0 + quarter * 32 + lane;  // id, or column of dX
+      const int m = m0 + quarter * 32 + lane;  // id, or column of dX
       if constexpr (KIND == kThinDx) {
         if (m < p.g.M) {
           float* out = p.g.part + int64_t(slice) * p.g.part_rows * p.g.M + m;
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
                 if (m == s_target[t]) d -= 1.f;
                 d = rs != 0.f && m < p.g.M ? d * rs : 0.f;
 #pragma unroll
-                for (int pl = 0; pl < C::PL; ++pl) {
+                for (int pl = 0; pl < (F32 ? kXentPlanes : kThinDzPlanes); ++pl) {
                   const __nv_bfloat16 h = __float2bfloat16_rn(d);
                   dz[pl * p.g.plane] = h;
                   d -= __bfloat162float(h);
@@ -443,41 +447,42 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
           }
         }
       } else {
-        // (max, sum of exponentials) of each column over the tile's 128 ids.
+        // (max, sum of exponentials) of each column over the tile's 128 ids, the target's left to the join.
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) {
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            if (m == s_target[32 * c + i] && 32 * c + i < p.g.T) p.g.zt[32 * c + i] = sum[c][i];
-            sum[c][i] = m < p.g.M ? sum[c][i] * kXentLog2e : -INFINITY;
+            const bool hot = m == s_target[32 * c + i];
+            if (hot) p.g.zt[32 * c + i] = sum[c][i];
+            if (hot || m >= p.g.M) sum[c][i] = -INFINITY;
             v[i] = sum[c][i];
           }
           s_ref[quarter][32 * c + lane] = reduce_columns<true>(v, lane);
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
+        float top_tile = 0.f;
+        if (et < N) {
+          top_tile = fmaxf(fmaxf(s_ref[0][et], s_ref[1][et]), fmaxf(s_ref[2][et], s_ref[3][et])) * kXentLog2e;
+          s_base[et] = top_tile == -INFINITY ? 0.f : top_tile;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int t = 32 * c + i;
-            float ref = fmaxf(fmaxf(s_ref[0][t], s_ref[1][t]), fmaxf(s_ref[2][t], s_ref[3][t]));
-            if (ref == -INFINITY) ref = 0.f;
-            v[i] = exp2_approx(sum[c][i] - ref);
-          }
+          for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(sum[c][i], kXentLog2e, -s_base[32 * c + i]));
           s_sum[quarter][32 * c + lane] = reduce_columns<false>(v, lane);
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
         if (et < N) {
-          const float top_tile = fmaxf(fmaxf(s_ref[0][et], s_ref[1][et]), fmaxf(s_ref[2][et], s_ref[3][et]));
           const float add = (s_sum[0][et] + s_sum[1][et]) + (s_sum[2][et] + s_sum[3][et]);
           const float top = fmaxf(run_max, top_tile);
           const float base = top == -INFINITY ? 0.f : top;
           run_sum = run_sum * exp2_approx(run_max - base) + add * exp2_approx((top_tile == -INFINITY ? 0.f : top_tile) - base);
           run_max = top;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // s_ref and s_sum are free again
+        // The next tile's writes of s_ref, s_base and s_sum each come a barrier or more after their last reads here.
       }
     }
     if constexpr (KIND == kThinStats) {
@@ -520,7 +525,7 @@ cudaError_t launch_thin(const XentThin& g, int kind, uint64_t wait_ns, cudaStrea
   p.kb_per_slice = (p.k_blocks + g.slices - 1) / g.slices;
   p.slices = (p.k_blocks + p.kb_per_slice - 1) / p.kb_per_slice;
   p.tiles = p.tiles_m * p.slices;
-  p.run = g.f32 ? 8 : kind == kThinStats ? 16 : p.k_blocks;
+  p.run = g.f32 ? (g.T <= 32 ? 4 : 8) : kind == kThinStats ? 16 : p.k_blocks;
   p.wait_ns = wait_ns;
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidSymbol;
