@@ -218,6 +218,68 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float4* __restri
   }
 }
 
+// dW of up to T rows: out [n][D] = dmax * sum_t dz_tv X_t on the CUDA cores, a
+// thread N columns of X's rows in registers, kOuterRows rows of out at a time.
+// It is the writing of dW, where the tensor cores' tiles load and multiply 64
+// rows (V = 64000, D = 1024, with the launch: fp32, T = 1 76 -> 43 us, T = 8 57
+// -> 43, but T = 16 57 -> 69; bf16, T = 1 39 -> 24, T = 2 38 -> 24; the tensor
+// cores need 31 from T = 3 on, this form 38 at T = 8).
+constexpr int kOuterRows = 64;
+int64_t outer_max(int is_bf16) { return is_bf16 ? 2 : 8; }
+template <typename E, int T>
+__global__ void __launch_bounds__(256) xent_outer_kernel(const __nv_bfloat16* __restrict__ dz, int planes, int64_t plane,
+                                                         int64_t pitch, const E* __restrict__ X, int rows, int64_t D,
+                                                         int64_t n, const float* __restrict__ dmax, E* __restrict__ out) {
+  constexpr int N = 16 / sizeof(E);
+  __shared__ __align__(16) float s_dz[kOuterRows][T];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int64_t col = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * N;
+  const float scale = warp_dmax(dmax, tid & 31);
+  float x[T][N];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[t][j] = 0.f;
+    if (t >= rows || col >= D) continue;
+    const uint4 w = *reinterpret_cast<const uint4*>(X + t * D + col);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      x[t][j] = sizeof(E) == 4 ? __uint_as_float(u[j]) : __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+  }
+  for (int64_t base = int64_t(blockIdx.x) * kOuterRows; base < n; base += int64_t(gridDim.x) * kOuterRows) {
+    const int here = n - base < kOuterRows ? static_cast<int>(n - base) : kOuterRows;
+    __syncthreads();
+    for (int i = tid; i < T * kOuterRows; i += blockDim.x * blockDim.y) {
+      const int t = i / kOuterRows, r = i % kOuterRows;
+      float d = 0.f;
+      if (t < rows && r < here)
+        for (int pl = planes - 1; pl >= 0; --pl) d += __bfloat162float(dz[pl * plane + t * pitch + base + r]);
+      s_dz[r][t] = d * scale;
+    }
+    __syncthreads();
+    if (col >= D) continue;
+#pragma unroll 4
+    for (int r = threadIdx.y; r < here; r += blockDim.y) {
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = s_dz[r][0] * x[0][j];
+#pragma unroll
+      for (int t = 1; t < T; ++t)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = fmaf(s_dz[r][t], x[t][j], v[j]);
+      uint4 w;
+      if constexpr (sizeof(E) == 4)
+        w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      else
+        w = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+      *reinterpret_cast<uint4*>(out + (base + r) * D + col) = w;
+    }
+  }
+}
+
 int grid_for(int64_t items) {
   const int64_t want = (items + 255) / 256, cap = int64_t(num_sms()) * 8;
   return static_cast<int>(want < 1 ? 1 : want < cap ? want : cap);
@@ -316,6 +378,24 @@ cudaError_t run_reduce(const float* part, int slices, int64_t stride, int64_t n,
                          static_cast<__nv_bfloat16*>(out))
                     : go(shared ? xent_reduce_kernel<float, 8> : xent_reduce_kernel<float, 1>, static_cast<float*>(out)));
   return cudaSuccess;
+}
+
+template <typename E>
+cudaError_t run_outer(const uint16_t* dz, int planes, int64_t plane, int64_t pitch, const void* X, int64_t T, int64_t D,
+                      int64_t n, const float* dmax, void* out, cudaStream_t s) {
+  const int64_t threads = D / (16 / static_cast<int>(sizeof(E)));
+  const int across = threads >= 256 ? 256 : static_cast<int>(ceil_to(threads, 32));
+  const int64_t slabs = (threads + across - 1) / across, most = int64_t(num_sms()) * 16 / slabs + 1;
+  int64_t blocks = (n + kOuterRows - 1) / kOuterRows;
+  if (blocks > most) blocks = most;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(slabs)), block(across, 256 / across);
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, grid, block, 0, s, reinterpret_cast<const __nv_bfloat16*>(dz), planes, plane, pitch,
+                      static_cast<const E*>(X), static_cast<int>(T), D, n, dmax, static_cast<E*>(out));
+  };
+  if constexpr (sizeof(E) == 4)
+    if (T > 2) return T <= 4 ? go(xent_outer_kernel<E, 4>) : go(xent_outer_kernel<E, 8>);
+  return T == 1 ? go(xent_outer_kernel<E, 1>) : go(xent_outer_kernel<E, 2>);
 }
 
 // The operands of the logits of ids [0, n) of W for the group of rows from t0.
@@ -540,21 +620,28 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     if (!p.thin) XENT_STEP("xent_dz", s, launch_xent_gemm(g, wait_ns, s));
 
     // dW of the piece = dz^T X.
-    g = XentGemm{};
-    for (int i = 0; i < p.dz_planes; ++i)
-      if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major)) return cudaErrorInvalidValue;
-    for (int i = 0; i < pl.n; ++i)
-      if (!mn_map(&g.map_b[i], pl.x[i], T, D, pl.pitch_x, true, &g.mn_major)) return cudaErrorInvalidValue;
-    g.pairs = is_bf16 ? p.dz_planes : pairs;
-    g.M = static_cast<int>(vc);
-    g.N = static_cast<int>(D);
-    g.K = static_cast<int>(T);
-    g.slices = p.slices_w;
-    g.group_m = 16;
-    g.dmax = dmax;
-    if ((e = product_out(g, static_cast<char*>(dW) + v0 * D * es, at<float>(ws, p.dw), is_bf16, wait_ns, s, "xent_dW")) !=
-        cudaSuccess)
-      return e;
+    if (T <= outer_max(is_bf16)) {
+      void* out = static_cast<char*>(dW) + v0 * D * es;
+      XENT_STEP("xent_dW", s,
+                is_bf16 ? run_outer<__nv_bfloat16>(dz[0], p.dz_planes, T * p.dz_pitch, p.dz_pitch, X, T, D, vc, dmax, out, s)
+                        : run_outer<float>(dz[0], p.dz_planes, T * p.dz_pitch, p.dz_pitch, X, T, D, vc, dmax, out, s));
+    } else {
+      g = XentGemm{};
+      for (int i = 0; i < p.dz_planes; ++i)
+        if (!mn_map(&g.map_a[i], dz[i], T, vp, p.dz_pitch, false, &g.mn_major)) return cudaErrorInvalidValue;
+      for (int i = 0; i < pl.n; ++i)
+        if (!mn_map(&g.map_b[i], pl.x[i], T, D, pl.pitch_x, true, &g.mn_major)) return cudaErrorInvalidValue;
+      g.pairs = is_bf16 ? p.dz_planes : pairs;
+      g.M = static_cast<int>(vc);
+      g.N = static_cast<int>(D);
+      g.K = static_cast<int>(T);
+      g.slices = p.slices_w;
+      g.group_m = 16;
+      g.dmax = dmax;
+      if ((e = product_out(g, static_cast<char*>(dW) + v0 * D * es, at<float>(ws, p.dw), is_bf16, wait_ns, s, "xent_dW")) !=
+          cudaSuccess)
+        return e;
+    }
 
     // dX += dz W over the piece.
     if (p.thin) {
