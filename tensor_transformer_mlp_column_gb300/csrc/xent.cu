@@ -15,7 +15,8 @@
 // before it is rounded and the products are multiplied by it: with the usual
 // equal row gradients dz of a target is then -(1 - p), which bf16 holds
 // closely where p is small, instead of a number whose rounding would scale
-// every target's gradient by the same up to 2^-8.
+// every target's gradient by the same up to 2^-8. Of up to 64 rows dz is two
+// bf16 pieces.
 //
 // fp32 data are split into three bf16 planes (24 bits in all) and every
 // product is the sum of the six plane products that are not below fp32
