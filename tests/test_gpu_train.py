@@ -250,6 +250,27 @@ def test_xent_large_logits(tp, dtype):
     _check_xent(tp, X, W, t, dloss, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(1, 300), (3, 5000), (40, 5000), (100, 300), (300, 5000), (2100, 300)])
+def test_xent_loss_of_nearly_certain_rows(tp, T, V, dtype):
+    # Entries -1, 0 and 1 and X_t = W_target: every logit is an exact integer, the target's about 40, and the losses are
+    # down to 1e-12: differences of fp32 numbers near 40 could not show them.
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    W = torch.randint(-1, 2, (V, 64), generator=g, device="cuda").to(DT[dtype])
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = W[t].contiguous()
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    z = X.double() @ W.double().T
+    e = z - z.gather(1, t[:, None])
+    gap = e.abs().max(dim=1).values
+    e.scatter_(1, t[:, None], -math.inf)
+    ref = torch.log1p(torch.exp(e).sum(1))
+    # log2 e as an fp32 constant and each exponent's rounding are off by the exponent times U32, an exponential by 4, the
+    # sums of parts and their joining by 64 U32 (as above), the result's functions by 8.
+    _close(loss, ref, ref * (3 * gap + 80) * U32, "loss")
+    _close(lse, z.gather(1, t[:, None])[:, 0] + ref, 2 * U32 * (lse.double().abs() + ref), "lse")
+
+
 def test_xent_infinities_stay_in_their_row(tp):
     X, W, t, dloss = _xent_inputs(40, 64, 300, "bf16", seed=12, masked=0.0)
     loss, lse = tp.tpmlp_xent_forward(X, W, t)
