@@ -543,13 +543,16 @@ int xent_thin_parts(int64_t V) {
 }
 
 int xent_thin_slices(int64_t D, int64_t K) {
-  const int64_t tiles = (D + 127) / 128, kb = (K + 63) / 64;
-  // Two tiles' worth for every SM, of at least eight K blocks each.
-  int64_t s = (2 * int64_t(num_sms()) + tiles - 1) / tiles;
-  if (s > kb / 8) s = kb / 8;
-  if (s < 1) s = 1;
-  const int64_t per = (kb + s - 1) / s;
-  return static_cast<int>((kb + per - 1) / per);
+  const int64_t tiles = (D + 127) / 128, kb = (K + 63) / 64, sms = num_sms();
+  // The shortest rounds over the SMs, of slices of at least eight K blocks (V =
+  // 64000, D = 4096, one row: ten slices in three rounds 239 us of fp32 and 118
+  // of bf16; nine in two 181 and 97).
+  int64_t best = kb, best_cost = INT64_MAX;
+  for (int64_t s = 1; s == 1 || (s <= kb / 8 && s <= 4 * sms / tiles + 1); ++s) {
+    const int64_t per = (kb + s - 1) / s, cost = (tiles * ((kb + per - 1) / per) + sms - 1) / sms * (per + 6);
+    if (cost < best_cost) best = per, best_cost = cost;
+  }
+  return static_cast<int>((kb + best - 1) / best);
 }
 
 cudaError_t launch_xent_thin_stats(const XentThin& g, uint64_t wait_ns, cudaStream_t s) {
