@@ -463,7 +463,8 @@ size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype d
  *   lse      device fp32 [T], of every row; tpmlp_xent_backward needs it.
  *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 0) bytes.
  * Products, maxima and sums in fp32 in both types (fp32: the tensor cores on
- * data split into three bf16 pieces). Bitwise reproducible. */
+ * data split into three bf16 pieces, which an infinite entry does not have: its
+ * products are not numbers). Bitwise reproducible. */
 int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                        tpmlp_dtype dt, float* loss, float* lse, void* workspace, size_t workspace_bytes,
                        tpmlp_stream_t stream);

@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
     const double x = double(m) - double(z) * double(kXentLog2e);  // log2 (e / S)
     if (!(z < INFINITY)) {
       whole = own = double(z - z);
-    } else if (m == -INFINITY) {
-      whole = double(z);  // there is no other id
+    } else if (s == 0.f) {
+      whole = double(z);  // there is no other id, or none that counts
     } else if (x < 30.0) {
       const double i = rint(fmax(x, -200.0));
       const float e = ldexpf(s * exp2f(static_cast<float>(fmax(x, -200.0) - i)), static_cast<int>(i));

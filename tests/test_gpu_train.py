@@ -284,6 +284,27 @@ def test_xent_infinities_stay_in_their_row(tp):
     assert bool(torch.isnan(loss2[11:13]).all())
 
 
+@pytest.mark.parametrize("T", [1, 100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_xent_infinities_and_nans_among_the_logits(tp, dtype, T):
+    # One column each: of every row's logits, the targets at id 0.
+    X = torch.zeros(T, 64, device="cuda", dtype=DT[dtype])
+    X[:, 0] = 1
+    t = torch.zeros(T, dtype=torch.int64, device="cuda")
+    inf, nan = float("inf"), float("nan")
+    for column, want in (([0.0, nan], (nan, nan)), ([nan, 0.0], (nan, nan)), ([0.0, -inf], (0.0, 0.0)),
+                         ([-inf, 0.0], (inf, 0.0)), ([0.0, inf], (nan, nan)), ([inf, 0.0], (nan, nan)),
+                         ([0.0, 0.0, -inf], (math.log(2.0), math.log(2.0))), ([2.0], (0.0, 2.0)), ([nan], (nan, nan))):
+        W = torch.zeros(len(column), 64, device="cuda", dtype=DT[dtype])
+        W[:, 0] = torch.tensor(column, device="cuda")
+        if dtype == "f32" and any(map(math.isinf, column)):
+            continue  # the pieces of an infinity are not numbers
+        loss, lse = tp.tpmlp_xent_forward(X, W, t)
+        for got, ref in zip((loss, lse), want):
+            ref = torch.full((T,), ref, device="cuda")
+            assert torch.allclose(got, ref, rtol=1e-6, atol=0, equal_nan=True), (column, got[0].item(), ref[0].item())
+
+
 def test_xent_gradient_against_differences(tp):
     # d/de L(X + e U, W + e V') at 0, by central differences of the fp32 losses. With s the
     # largest change rate of a logit, the third derivative of a row's loss is at most 2 s^3
