@@ -747,6 +747,92 @@ def test_calls_captured_into_graphs_and_replayed(tp):
     tp.tpmlp_check_status()
 
 
+def _other_calls(tp):
+    calls = {}
+
+    def xent(T, D, V, dtype):
+        X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + V)
+        _, lse = tp.tpmlp_xent_forward(X, W, t)
+        calls[f"xent {T} {D} {V} {dtype}"] = lambda s=None: [
+            *tp.tpmlp_xent_forward(X, W, t, stream=s), *tp.tpmlp_xent_backward(X, W, t, lse, dloss, stream=s)]
+
+    def embed(T, D, V, dtype):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        ids, dout = _ids(T, V, T, "words"), torch.randn(T, D, generator=g, device="cuda").to(DT[dtype])
+        calls[f"embed {T} {D} {V} {dtype}"] = lambda s=None: [tp.tpmlp_embed_backward(dout, ids, V, 2.0, stream=s)]
+
+    for dtype in DT:
+        for T, D, V in ((1, 64, 3000), (7, 200, 5000), (40, 1000, 700), (150, 72, 900), (9000, 24, 30001)):
+            xent(T, D, V, dtype)
+        for T, D, V in ((1, 768, 3000), (600, 33, 100), (5000, 256, 60000), (70000, 64, 5000)):
+            embed(T, D, V, dtype)
+    xent(600, 1032, 8300, "bf16")
+    return calls
+
+
+def test_other_sizes_captured_replayed_and_side_by_side(tp):
+    calls = _other_calls(tp)
+    ref = {k: [v.clone() for v in f()] for k, f in calls.items()}
+    torch.cuda.synchronize()
+    graphs = {}
+    for k, f in calls.items():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphs[k] = graph, f(torch.cuda.current_stream())
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    names = list(calls)
+    for _ in range(2):
+        for k in names:
+            for v in graphs[k][1]:
+                v.fill_(3.0)
+        torch.cuda.synchronize()
+        got = []
+        for a, b in zip(names, reversed(names)):  # one replayed while another runs
+            with torch.cuda.stream(s):
+                graphs[a][0].replay()
+            with torch.cuda.stream(r):
+                got.append((b, calls[b](r)))
+        torch.cuda.synchronize()
+        for k, out in got + [(k, graphs[k][1]) for k in names]:
+            assert all(torch.equal(u, v) for u, v in zip(out, ref[k])), k
+    tp.tpmlp_check_status()
+
+
+FIRST_IN_A_GRAPH = r'''
+import torch
+import tensor_transformer_mlp_column_gb300 as tp
+X, W = torch.randn(100, 64, device="cuda"), torch.randn(300, 64, device="cuda")
+t = torch.arange(100, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, torch.ones_like(loss))
+    dE = tp.tpmlp_embed_backward(X, t, 300, dE=dW, accumulate=True)
+    norm = tp.tpmlp_grad_clip([dW, dX], 1e6)
+graph.replay()
+torch.cuda.synchronize()
+out = [v.clone() for v in (loss, dX, dW, norm)]
+loss, lse = tp.tpmlp_xent_forward(X, W, t)
+dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, torch.ones_like(loss))
+tp.tpmlp_embed_backward(X, t, 300, dE=dW, accumulate=True)
+norm = tp.tpmlp_grad_clip([dW, dX], 1e6)
+assert all(torch.equal(a, b) for a, b in zip(out, (loss, dX, dW, norm)))
+tp.tpmlp_check_status()
+print("ok")
+'''
+
+
+def test_first_calls_of_a_process_in_a_graph(tp):
+    import os
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], capture_output=True, text=True, timeout=600,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-2000:] + r.stderr[-4000:]
+
+
 def test_calls_in_two_streams_at_once(tp):
     a, b = _train_calls(tp, seed=51), _train_calls(tp, seed=52)
     ra, rb = {k: f() for k, f in a.items()}, {k: f() for k, f in b.items()}
