@@ -54,12 +54,14 @@ constexpr int kSub = 2;         // K blocks of a stage
 constexpr uint32_t kSubBytes = 128 * BK * 2;
 constexpr uint32_t kOutBlock = 32 * 128;  // staging: 32 rows of 128 bytes
 constexpr int BN = 256;
-// K blocks of a run, at most: sums of up to 1024 products of bf16 data; 512 of
-// fp32 data's high planes, where more is wanted; 8192 of the five other plane
-// pairs, which come first and whose sums are at most 2^-8 of the whole (cut like
-// the high planes' they made six runs of K = 512 instead of two: T = 1000, V =
-// 32001, logits 124 -> 114 us).
-constexpr int kRunBf16 = 16, kRunF32 = 8, kRunSmall = 128;
+// K blocks of a run, at most. Of bf16 data 16, sums of up to 1024 products; 8
+// where there is one row of tiles, which waits for W anyway (T = 200, V = 32000,
+// D = 1024: 24.6 -> 25.3 us, the losses off by 3.8e-7 in the place of 8.0e-7; T =
+// 1000 48.4 -> 52.4). Of fp32 data's high planes 8, where more is wanted; 128 of
+// the five other plane pairs, which come first and whose sums are at most 2^-8
+// of the whole (cut like the high planes' they made six runs of K = 512 instead
+// of two: T = 1000, V = 32001, logits 124 -> 114 us).
+constexpr int kRunLong = 16, kRunShort = 8, kRunSmall = 128;
 constexpr int kDrainPauseNs = 25;  // per K block of a run, between a warp's reads of it
 
 template <int EPI, bool RUNS>
@@ -675,7 +677,7 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
   // Runs where an fp32 result is wanted (the statistics and all of fp32) of a
   // sum longer than one, cut evenly. dz and gradients that are rounded to bf16
   // lose nothing by one long sum.
-  const int total = g.pairs * p.kb_per_slice, most = g.pairs > 1 ? kRunF32 : kRunBf16;
+  const int total = g.pairs * p.kb_per_slice, most = g.pairs > 1 || g.M <= 256 ? kRunShort : kRunLong;
   const int runs = (total + most - 1) / most;
   p.run = ((total + runs - 1) / runs + 1) / 2 * 2;
   const bool cut = total > most;
