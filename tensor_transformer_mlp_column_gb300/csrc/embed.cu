@@ -33,67 +33,107 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float v) { d = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
-// N consecutive elements as they are loaded: N * sizeof(E) is 8, 16 or 32
-// bytes, or one element.
-template <typename E, int N>
+// A thread's N columns of a row. S = false: consecutive ones, loaded as 8, 16 or
+// 32 bytes, or one element. S = true, where rows are not made of such pieces:
+// `stride` columns apart (the threads that share the row), the first `count` of
+// them within the row; a warp's access then covers 32 neighbours.
+template <typename E, int N, bool S>
 struct Raw {
   static constexpr int kBytes = N * sizeof(E);
   static constexpr int kWords = kBytes >= 16 ? kBytes / 16 : 1;
   uint4 w[kWords];
 };
 template <typename E, int N>
-__device__ __forceinline__ void fetch(const E* p, Raw<E, N>& r) {
-  if constexpr (N == 1)
+struct Raw<E, N, true> {
+  E e[N];
+};
+struct Columns {
+  int stride, count;
+};
+// Columns of thread `lane` of `lanes`, from its first one.
+template <int N, bool S>
+__device__ __forceinline__ Columns columns(int64_t first, int lanes, int64_t D) {
+  Columns c{1, N};
+  if constexpr (S) {
+    c.stride = lanes;
+    c.count = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) c.count += first + int64_t(j) * lanes < D;
+  }
+  return c;
+}
+template <typename E, int N, bool S>
+__device__ __forceinline__ void fetch(const E* p, const Columns& c, Raw<E, N, S>& r) {
+  if constexpr (S) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < c.count) r.e[j] = p[j * c.stride];
+  } else if constexpr (N == 1) {
     *reinterpret_cast<E*>(r.w) = *p;
-  else if constexpr (Raw<E, N>::kBytes == 8)
+  } else if constexpr (Raw<E, N, S>::kBytes == 8) {
     *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(p);
-  else
+  } else {
 #pragma unroll
-    for (int i = 0; i < Raw<E, N>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < Raw<E, N, S>::kWords; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
 }
-template <typename E, int N>
-__device__ __forceinline__ void unpack(const Raw<E, N>& r, float (&f)[N]) {
-  const E* e = reinterpret_cast<const E*>(r.w);
+template <typename E, int N, bool S>
+__device__ __forceinline__ void unpack(const Columns& c, const Raw<E, N, S>& r, float (&f)[N]) {
+  if constexpr (S) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) f[j] = to_f(e[j]);
-}
-template <typename E, int N>
-__device__ __forceinline__ void load_n(const E* p, float (&f)[N]) {
-  Raw<E, N> r;
-  fetch<E, N>(p, r);
-  unpack<E, N>(r, f);
-}
-template <typename E, int N>
-__device__ __forceinline__ void store_n(E* p, const float (&f)[N]) {
-  Raw<E, N> r;
-  E* e = reinterpret_cast<E*>(r.w);
+    for (int j = 0; j < N; ++j) f[j] = j < c.count ? to_f(r.e[j]) : 0.f;
+  } else {
+    const E* e = reinterpret_cast<const E*>(r.w);
 #pragma unroll
-  for (int j = 0; j < N; ++j) from_f(e[j], f[j]);
-  if constexpr (N == 1)
-    *p = *e;
-  else if constexpr (Raw<E, N>::kBytes == 8)
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.w);
-  else
-#pragma unroll
-    for (int i = 0; i < Raw<E, N>::kWords; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    for (int j = 0; j < N; ++j) f[j] = to_f(e[j]);
+  }
 }
-
+template <typename E, int N, bool S>
+__device__ __forceinline__ void load_n(const E* p, const Columns& c, float (&f)[N]) {
+  Raw<E, N, S> r;
+  fetch<E, N, S>(p, c, r);
+  unpack<E, N, S>(c, r, f);
+}
+template <typename E, int N, bool S>
+__device__ __forceinline__ void store_n(E* p, const Columns& c, const float (&f)[N]) {
+  Raw<E, N, S> r;
+  if constexpr (S) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      from_f(r.e[j], f[j]);
+      if (j < c.count) p[j * c.stride] = r.e[j];
+    }
+  } else {
+    E* e = reinterpret_cast<E*>(r.w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) from_f(e[j], f[j]);
+    if constexpr (N == 1) {
+      *p = *e;
+    } else if constexpr (Raw<E, N, S>::kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Raw<E, N, S>::kWords; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    }
+  }
+}
 // ------------------------------------------------------------------ lookup
 
 constexpr int kThreads = 256;
 
 // Columns of slab blockIdx.y: 2^log_lanes threads take a token's pieces of N
-// elements (16 bytes, or one element where rows are not made of 16-byte
-// pieces), K tokens, all loaded before one is written.
-template <typename E, int N, int K>
+// elements (16 bytes; S: see Raw), K tokens, all loaded before one is written.
+template <typename E, int N, bool S, int K>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const E* __restrict__ table, const int64_t* __restrict__ ids,
                                                          int64_t T, int64_t D, int64_t V, float scale,
                                                          E* __restrict__ out, int log_lanes, int* status) {
   pdl_wait();
   pdl_launch_dependents();
   const int groups = kThreads >> log_lanes;  // tokens side by side
-  const int64_t col = int64_t((blockIdx.y << log_lanes) + (threadIdx.x & ((1 << log_lanes) - 1))) * N;
+  const int lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t col = S ? int64_t(blockIdx.y) * lanes * N + lane : (int64_t(blockIdx.y) * lanes + lane) * N;
   if (col >= D) return;
+  const Columns cols = columns<N, S>(col, lanes, D);
   const int64_t t0 = int64_t(blockIdx.x) * (groups * K) + (threadIdx.x >> log_lanes);
   int row[K];  // -1: zero, -2: zero and to be reported
 #pragma unroll
@@ -101,10 +141,10 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const E* __restrict__ t
     const int64_t id = t0 + k * groups < T ? ids[t0 + k * groups] : -1;
     row[k] = id < 0 ? -1 : id < V ? static_cast<int>(id) : -2;
   }
-  Raw<E, N> r[K];
+  Raw<E, N, S> r[K];
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (row[k] >= 0) fetch<E, N>(table + row[k] * D + col, r[k]);
+    if (row[k] >= 0) fetch<E, N, S>(table + row[k] * D + col, cols, r[k]);
   E* dst = out + t0 * D + col;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -113,11 +153,11 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const E* __restrict__ t
 #pragma unroll
     for (int j = 0; j < N; ++j) f[j] = 0.f;
     if (row[k] >= 0) {
-      unpack<E, N>(r[k], f);
+      unpack<E, N, S>(cols, r[k], f);
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] *= scale;
     }
-    store_n<E, N>(dst, f);
+    store_n<E, N, S>(dst, cols, f);
     dst += groups * D;
   }
   if (col == 0) {
@@ -492,16 +532,20 @@ constexpr int kBatch = 8;
 int run_of(int64_t T) { return T <= 16384 ? 16 : kMaxRun; }
 
 // What the clearing CTAs of segment_kernel do: table rows from `row0` on that
-// are not marked in `present`, in pieces of `piece` bytes (16, or an element
-// where rows are not made of 16-byte pieces), kClearPieces a CTA.
+// are not marked in `present`, in pieces of 16 bytes, kClearPieces a CTA, of the
+// rows' bytes as a whole. A piece that holds parts of two rows, or the table's
+// end, goes element by element. (One element at a time for all of a table with
+// such rows: D = 1074, V = 111592, T = 391, fp32, the sums with the clearing 178
+// us.)
 constexpr int kClearUnroll = 8;
 constexpr int kClearPieces = kThreads * kClearUnroll;
 struct Clear {
   const uint32_t* present;
-  int64_t row0, pieces;  // pieces of all rows from row0 on
-  uint32_t row_pieces;   // pieces of a row
-  uint32_t magic;        // ceil(2^32 / row_pieces), where 1 < row_pieces < kClearPieces, else 0
-  int piece;
+  int64_t row0, rows;   // rows [row0, rows); row0 rows are a multiple of 16 bytes
+  int64_t bytes;        // of those
+  uint32_t row_bytes;
+  uint32_t magic;       // ceil(2^32 / row_bytes), where 1 < row_bytes < 16 kClearPieces, else 0
+  int element;          // bytes
   int ctas;
   // The CTAs in their order: every `period`-th one is of the rarer kind, as
   // long as there are any. Rare summing CTAs are every second one at first:
@@ -511,43 +555,49 @@ struct Clear {
 };
 
 __device__ __forceinline__ void clear_rows(const Clear& c, int64_t cta, char* dE) {
-  const int64_t first = cta * kClearPieces;
-  const int n = static_cast<int>(c.pieces - first < kClearPieces ? c.pieces - first : kClearPieces);
-  const int64_t row = c.pieces >> 32 ? first / c.row_pieces : static_cast<uint32_t>(first) / c.row_pieces;
-  const uint32_t skip = static_cast<uint32_t>(first - row * c.row_pieces);
-  char* base = dE + (c.row0 * c.row_pieces + first) * c.piece;
-  uint32_t marks[kClearUnroll];
+  const int64_t first = cta * (16 * kClearPieces);  // byte
+  const int n = static_cast<int>(c.bytes - first < 16 * kClearPieces ? c.bytes - first : 16 * kClearPieces);
+  const int64_t row = c.bytes >> 32 ? first / c.row_bytes : static_cast<uint32_t>(first) / c.row_bytes;
+  const uint32_t skip = static_cast<uint32_t>(first - row * c.row_bytes);
+  char* base = dE + c.row0 * c.row_bytes + first;
+  auto marked = [&](int64_t v) { return v < c.rows ? __ldg(c.present + (v >> 5)) >> (v & 31) & 1u : 1u; };
+  // How many rows below `row` byte skip + i is: long rows meet at most one border here, short ones divide by
+  // multiplying (exact while numerator * row_bytes < 2^32).
+  auto down_of = [&](uint32_t x) { return c.magic ? __umulhi(x, c.magic) : (x >= c.row_bytes ? 1u : 0u); };
+  uint32_t marks[kClearUnroll];  // bit 0: the row is marked; bit 1: not of one whole row
 #pragma unroll
   for (int u = 0; u < kClearUnroll; ++u) {
-    const int i = threadIdx.x + u * kThreads;
-    // (skip + i) / row_pieces: long rows meet at most one border here, short ones divide by multiplying
-    // (exact while numerator * row_pieces < 2^32).
-    const uint32_t x = skip + static_cast<uint32_t>(i);
-    const uint32_t down = c.row_pieces == 1 ? x : c.magic ? __umulhi(x, c.magic) : (x >= c.row_pieces ? 1u : 0u);
-    const int64_t v = c.row0 + row + down;
-    marks[u] = i < n ? __ldg(c.present + (v >> 5)) >> (v & 31) & 1u : 1u;
+    const int i = (threadIdx.x + u * kThreads) * 16;
+    const uint32_t x = skip + static_cast<uint32_t>(i), down = down_of(x);
+    const bool whole = x - down * c.row_bytes + 16 <= c.row_bytes && i + 16 <= n;
+    marks[u] = i >= n ? 1u : whole ? marked(c.row0 + row + down) : 2u;
   }
 #pragma unroll
   for (int u = 0; u < kClearUnroll; ++u) {
-    if (marks[u]) continue;
-    char* p = base + int64_t(threadIdx.x + u * kThreads) * c.piece;
-    if (c.piece == 16)
-      *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-    else if (c.piece == 4)
-      *reinterpret_cast<uint32_t*>(p) = 0;
-    else
-      *reinterpret_cast<uint16_t*>(p) = 0;
+    if (marks[u] & 1u) continue;
+    const int i = (threadIdx.x + u * kThreads) * 16;
+    if (marks[u] == 0) {
+      *reinterpret_cast<uint4*>(base + i) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    for (int o = i; o < i + 16 && o < n; o += c.element) {
+      if (marked(c.row0 + row + down_of(skip + static_cast<uint32_t>(o)))) continue;
+      if (c.element == 4)
+        *reinterpret_cast<uint32_t*>(base + o) = 0;
+      else
+        *reinterpret_cast<uint16_t*>(base + o) = 0;
+    }
   }
 }
 
-// Chunk b (`run` sorted entries), columns of slab y: thread x holds N
-// consecutive columns. A segment (run of equal ids) of up to 2 run entries
+// Chunk b (`run` sorted entries), columns of slab y: thread x holds N columns
+// (S: see Raw). A segment (run of equal ids) of up to 2 run entries
 // belongs to the chunk in which it begins, whose CTA follows it past the
 // chunk's end. Of a longer one every chunk sums its part: the part of a segment
 // that began in an earlier chunk goes to part[2 b], the part of one that
 // begins in it to part[2 b + 1], and goes_on[b] says that there is such a
 // one. The clearing CTAs alternate with these evenly over the grid.
-template <typename G, typename E, int N>
+template <typename G, typename E, int N, bool S>
 __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restrict__ dout, const uint32_t* __restrict__ key,
                                                            const uint32_t* __restrict__ pos, int64_t T, int64_t D,
                                                            int64_t V, float scale, E* __restrict__ dE, int accumulate,
@@ -624,16 +674,18 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
   __syncthreads();
   const int start = s_start, stop = s_stop;
   bool began = s_began;
-  const int64_t col = (int64_t(slab) * blockDim.x + threadIdx.x) * N;
+  const int64_t col =
+      S ? int64_t(slab) * blockDim.x * N + threadIdx.x : (int64_t(slab) * blockDim.x + threadIdx.x) * N;
   if (col >= D) return;
+  const Columns cols = columns<N, S>(col, blockDim.x, D);
   float sum[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) sum[j] = 0.f;
   // A ring of kBatch rows on their way: row i + kBatch is fetched when row i is added.
-  Raw<G, N> r[kBatch];
-  auto issue = [&](int i, Raw<G, N>& to) {
+  Raw<G, N, S> r[kBatch];
+  auto issue = [&](int i, Raw<G, N, S>& to) {
     if (i >= stop || k_at[i] >= V) return;
-    fetch<G, N>(dout + int64_t(spos[i]) * D + col, to);
+    fetch<G, N, S>(dout + int64_t(spos[i]) * D + col, cols, to);
     if (accumulate && k_at[i + 1] != k_at[i])
       asm volatile("prefetch.global.L2 [%0];" ::"l"(dE + int64_t(k_at[i]) * D + col));
   };
@@ -647,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
       const uint32_t k = k_at[i];
       if (k >= V) return;  // entries without a row, sorted last
       float f[N];
-      unpack<G, N>(r[b], f);
+      unpack<G, N, S>(cols, r[b], f);
       issue(i + kBatch, r[b]);
 #pragma unroll
       for (int j = 0; j < N; ++j) sum[j] += f[j];
@@ -658,12 +710,12 @@ __global__ void __launch_bounds__(kThreads, 4) segment_kernel(const G* __restric
         float old[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) old[j] = 0.f;
-        if (accumulate) load_n<E, N>(row, old);
+        if (accumulate) load_n<E, N, S>(row, cols, old);
 #pragma unroll
         for (int j = 0; j < N; ++j) sum[j] = fmaf(sum[j], scale, old[j]);
-        store_n<E, N>(row, sum);
+        store_n<E, N, S>(row, cols, sum);
       } else {
-        store_n<float, N>(part + (2 * chunk + (began ? 1 : 0)) * D + col, sum);
+        store_n<float, N, S>(part + (2 * chunk + (began ? 1 : 0)) * D + col, cols, sum);
       }
 #pragma unroll
       for (int j = 0; j < N; ++j) sum[j] = 0.f;
@@ -716,7 +768,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restri
 #pragma unroll 4
       for (int64_t i = from; i < to; ++i) {
         float f[N];
-        load_n<float, N>(part + (i == 0 ? 2 * b + 1 : 2 * (b + i)) * D + col, f);
+        load_n<float, N, false>(part + (i == 0 ? 2 * b + 1 : 2 * (b + i)) * D + col, Columns{}, f);
 #pragma unroll
         for (int j = 0; j < N; ++j) sum[j] += f[j];
       }
@@ -732,19 +784,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const uint32_t* __restri
       float old[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) old[j] = 0.f;
-      if (accumulate) load_n<E, N>(row, old);
+      if (accumulate) load_n<E, N, false>(row, Columns{}, old);
 #pragma unroll
       for (int j = 0; j < N; ++j) sum[j] = fmaf(sum[j], scale, old[j]);
-      store_n<E, N>(row, sum);
+      store_n<E, N, false>(row, Columns{}, sum);
     }
     __syncthreads();
   }
 }
 
-template <typename E, int N>
+template <typename E, int N, bool S>
 cudaError_t lookup(const E* table, const int64_t* ids, int64_t T, int64_t D, int64_t V, float scale, E* out, int* status,
                    cudaStream_t s) {
-  const int64_t pieces = D / N;
+  const int64_t pieces = (D + N - 1) / N;
   int log_lanes = 0;
   while ((1 << log_lanes) < kThreads && (1 << log_lanes) < pieces) ++log_lanes;
   const int64_t lanes = int64_t(1) << log_lanes;
@@ -754,24 +806,24 @@ cudaError_t lookup(const E* table, const int64_t* ids, int64_t T, int64_t D, int
   const bool four = per4 * slabs >= int64_t(num_sms()) * 8;
   const int64_t x = four ? per4 : (T + groups - 1) / groups;
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(slabs));
-  return four ? launch_pdl(embed_kernel<E, N, 4>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status)
-              : launch_pdl(embed_kernel<E, N, 1>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status);
+  return four ? launch_pdl(embed_kernel<E, N, S, 4>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status)
+              : launch_pdl(embed_kernel<E, N, S, 1>, grid, dim3(kThreads), 0, s, table, ids, T, D, V, scale, out, log_lanes, status);
 }
 
 template <typename E>
 cudaError_t embed_dispatch(const E* table, const int64_t* ids, int64_t T, int64_t D, int64_t V, float scale, E* out,
                            int* status, cudaStream_t s) {
   constexpr int N = 16 / sizeof(E);
-  return D % N == 0 ? lookup<E, N>(table, ids, T, D, V, scale, out, status, s)
-                    : lookup<E, 1>(table, ids, T, D, V, scale, out, status, s);
+  return D % N == 0 ? lookup<E, N, false>(table, ids, T, D, V, scale, out, status, s)
+                    : lookup<E, 4, true>(table, ids, T, D, V, scale, out, status, s);
 }
 
-template <typename G, typename E, int N>
+template <typename G, typename E, int N, bool S>
 cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, int64_t T, int64_t D, int64_t V,
                      float scale, E* dE, int accumulate, float* part, uint8_t* goes_on, const Clear& clear,
                      cudaStream_t s) {
   const int run = run_of(T);
-  const int64_t pieces = D / N;
+  const int64_t pieces = (D + N - 1) / N;
   int threads = 32;
   while (threads < kThreads && threads < pieces) threads <<= 1;
   if (clear.ctas > 0) threads = kThreads;  // the clearing CTAs'
@@ -786,7 +838,7 @@ cudaError_t segments(const G* dout, const uint32_t* key, const uint32_t* pos, in
   }
   {
     TraceScope trace("embed_segments", s);
-    const cudaError_t e = launch_pdl(segment_kernel<G, E, N>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, dout,
+    const cudaError_t e = launch_pdl(segment_kernel<G, E, N, S>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s, dout,
                                      key, pos, T, D, V, scale, dE, accumulate, part, goes_on, run, static_cast<int>(slabs), c);
     if (e != cudaSuccess) return e;
   }
@@ -808,9 +860,11 @@ cudaError_t segments_dispatch(const void* dout, const uint32_t* key, const uint3
                               float scale, void* dE, int accumulate, float* part, uint8_t* goes_on, const Clear& clear, cudaStream_t s) {
   const G* g = static_cast<const G*>(dout);
   E* e = static_cast<E*>(dE);
+  // Strided columns: eight bytes a thread (16 of fp32 spill beside the ring of rows: T = 65536, D = 1074, V = 50000,
+  // 271 us, and 125 so; one element a thread 201).
   constexpr int N = 16 / sizeof(G);
-  return D % N == 0 ? segments<G, E, N>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s)
-                    : segments<G, E, 1>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s);
+  return D % N == 0 ? segments<G, E, N, false>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s)
+                    : segments<G, E, 8 / static_cast<int>(sizeof(G)), true>(g, key, pos, T, D, V, scale, e, accumulate, part, goes_on, clear, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -858,25 +912,27 @@ cudaError_t launch_embed_grad(const void* dout, int dout_bf16, const int64_t* id
   uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(base + p.pos[0]), reinterpret_cast<uint32_t*>(base + p.pos[1])};
   uint32_t* counts = reinterpret_cast<uint32_t*>(base + p.counts);
   uint32_t* present = reinterpret_cast<uint32_t*>(base + p.present);
-  // Rows are cleared in pieces of 16 bytes, or of one element where a row does not divide into those.
   const int64_t row_bytes = D * (dE_bf16 ? 2 : 4);
   Clear clear{};
   clear.present = present;
-  clear.piece = row_bytes % 16 == 0 ? 16 : dE_bf16 ? 2 : 4;
-  clear.row_pieces = static_cast<uint32_t>(row_bytes / clear.piece);
+  clear.element = dE_bf16 ? 2 : 4;
+  clear.row_bytes = static_cast<uint32_t>(row_bytes);
+  clear.rows = V;
   const bool cluster = T <= kClusterSortMax;
   int items = 1;  // of a thread in the cluster's sort
   while (items < kMaxItems && T > int64_t(kSortCtas) * kSortThreads * items) items *= 2;
   if (!accumulate) {
     // The sort in the cluster takes about 6 + 3 items us, in which the other SMs write 7 MB a us (T = 40000, D =
     // 4096, V = 128000: 4 MB a us for 8 us and 2 more per 8192 tokens left 239 us in all, this 226).
-    if (cluster && clear.piece == 16) clear.row0 = int64_t(6 + 3 * items) * (7 << 20) / row_bytes;
+    if (cluster) clear.row0 = int64_t(6 + 3 * items) * (7 << 20) / row_bytes;
     if (clear.row0 > V) clear.row0 = V;
-    clear.pieces = (V - clear.row0) * clear.row_pieces;
-    const int64_t ctas = (clear.pieces + kClearPieces - 1) / kClearPieces;
+    if (row_bytes % 16 != 0) clear.row0 &= ~int64_t(7);  // eight rows are a multiple of 16 bytes
+    clear.bytes = (V - clear.row0) * row_bytes;
+    const int64_t ctas = (clear.bytes + 16 * kClearPieces - 1) / (16 * kClearPieces);
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
     clear.ctas = static_cast<int>(ctas);
-    clear.magic = clear.row_pieces > 1 && clear.row_pieces < kClearPieces ? static_cast<uint32_t>(((1ull << 32) + clear.row_pieces - 1) / clear.row_pieces) : 0;
+    clear.magic =
+        row_bytes < 16 * kClearPieces ? static_cast<uint32_t>(((1ull << 32) + clear.row_bytes - 1) / clear.row_bytes) : 0;
   }
   int at = 0;
   {

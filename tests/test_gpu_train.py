@@ -412,6 +412,30 @@ def test_embed_gradient_of_many_tokens(tp, T, D, V, kind):
     _check_embed_grad(tp, dout, ids, V, 1.0, torch.float32, dE0)
 
 
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")], ids="-".join)
+@pytest.mark.parametrize("T,D,V", [(391, 1074, 40001), (100, 1075, 36000), (5000, 4095, 12345), (70000, 1001, 3000),
+                                   (66000, 3, 100001), (9, 1, 70), (40, 2, 30000000), (300, 8201, 4000)])
+def test_embed_gradient_of_rows_off_16_bytes(tp, T, D, V, types):
+    # Rows that begin anywhere: summed with strided columns, cleared in 16 bytes at a time across the rows' borders;
+    # the table's last bytes and what lies behind them too.
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ids[0], ids[-1] = V - 1, -1
+    dout = torch.randint(-8, 9, (T, D), generator=g, device="cuda").to(DT[types[0]])  # sums of small integers are exact
+    whole = torch.full((V * D + 64,), 7.0, device="cuda", dtype=DT[types[1]])
+    dE = whole[:V * D].view(V, D)
+    keep = ids >= 0
+    ref = torch.zeros(V, D, device="cuda").index_add_(0, ids[keep], dout[keep].float() * 0.5).to(DT[types[1]])
+    tp.tpmlp_embed_backward(dout, ids, V, 0.5, dE=dE)
+    assert torch.equal(dE, ref) and bool((whole[V * D:] == 7).all())
+    got = tp.tpmlp_embed_forward(ref, ids, 2.0)
+    want = torch.where(keep[:, None], ref[ids.clamp(min=0)].float() * 2, torch.zeros((), device="cuda")).to(ref.dtype)
+    assert torch.equal(got, want)
+    tp.tpmlp_embed_backward(dout, ids, V, 0.5, dE=dE, accumulate=True)
+    assert torch.equal(dE, (ref.float() * 2).to(ref.dtype))
+    tp.tpmlp_check_status()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_embed_lookup_of_many_tokens(tp, dtype):
     g = torch.Generator(device="cuda").manual_seed(2)
