@@ -138,6 +138,7 @@ struct XentThin {
   int64_t V, col0;                  // all ids; the id of the first row of W
   float2* stats;                    // [xent_thin_parts(M)][T]
   float* zt;
+  float* zt_rest;                   // bf16, up to 32 rows: what zt's rounding left out
   const float *lse, *dloss, *dmax;
   XentDmax rows;                    // as in XentGemm, of all groups
   __nv_bfloat16* dz;                // rows [T][pitch] of planes that are `plane` apart

@@ -50,13 +50,14 @@ namespace {
 // warps (and the lanes that share a row) every so many parts each, joined in a
 // fixed order.
 // M - z log2 e is in fp64: a rounding to fp32 would weigh as much as one of z.
+// With `rest` the loss's place holds what z's own rounding left out.
 // R = 4 rows a CTA where there are few rows: 128 threads share a row's parts.
 constexpr int kJoinWarps = 16;
 template <int R>
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2* __restrict__ stats, int parts, int64_t T,
                                                                     const int64_t* __restrict__ targets, int64_t V,
                                                                     const float* __restrict__ zt, float* __restrict__ loss,
-                                                                    float* __restrict__ lse, int* status) {
+                                                                    float* __restrict__ lse, int rest, int* status) {
   constexpr int S = 32 / R;  // lanes that share a row
   __shared__ float2 red[kJoinWarps][R];
   pdl_wait();
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   };
   const int64_t target = t < T && w == 0 ? targets[t] : -1;
   const float z = target >= 0 && target < V ? zt[t] : 0.f;
+  const float z_rest = rest && target >= 0 && target < V ? loss[t] : 0.f;
   if (t < T) {
 #pragma unroll 8
     for (int i = w * S + l / R; i < parts; i += kJoinWarps * S) add(stats[int64_t(i) * T + t]);
@@ -89,18 +91,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const float2
   const double ln2 = 1.0 / double(kXentLog2e);
   double whole = (double(m) + double(k) + double(log2f(ldexpf(s, -k)))) * ln2, own = 0.0;
   if (target >= 0 && target < V) {
-    const double x = double(m) - double(z) * double(kXentLog2e);  // log2 (e / S)
+    const double zd = double(z) + double(z_rest);
+    const double x = double(m) - zd * double(kXentLog2e);  // log2 (e / S)
     if (!(z < INFINITY)) {
       whole = own = double(z - z);
     } else if (s == 0.f) {
-      whole = double(z);  // there is no other id, or none that counts
+      whole = zd;  // there is no other id, or none that counts
     } else if (x < 30.0) {
       const double i = rint(fmax(x, -200.0));
       const float e = ldexpf(s * exp2f(static_cast<float>(fmax(x, -200.0) - i)), static_cast<int>(i));
       own = double(log1pf(e));
-      whole = double(z) + own;
+      whole = zd + own;
     } else {  // the target's own share of the sum is below the rounding
-      own = whole - double(z);
+      own = whole - zd;
     }
   }
   lse[t] = static_cast<float>(whole);
@@ -358,12 +361,12 @@ cudaError_t planes_of(const void* X, const void* W, int64_t T, int64_t D, int64_
 }
 
 cudaError_t run_join(const float2* stats, int parts, int64_t T, const int64_t* targets, int64_t V, const float* zt,
-                            float* loss, float* lse, int* status, cudaStream_t s) {
+                            float* loss, float* lse, int rest, int* status, cudaStream_t s) {
   const bool few = T < 2048;
   const dim3 grid(static_cast<unsigned>(few ? (T + 3) / 4 : (T + 31) / 32));
   XENT_STEP("xent_join", s,
             launch_pdl(few ? xent_join_kernel<4> : xent_join_kernel<32>, grid, dim3(32 * kJoinWarps), 0, s, stats, parts, T,
-                       targets, V, zt, loss, lse, status));
+                       targets, V, zt, loss, lse, rest, status));
   return cudaSuccess;
 }
 
@@ -535,8 +538,10 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
       h.V = V;
       h.stats = stats + t0 * xent_thin_parts(V);
       h.zt = zt + t0;
+      h.zt_rest = loss + t0;
       XENT_STEP("xent_logits", s, launch_xent_thin_stats(h, wait_ns, s));
-      if ((e = run_join(h.stats, xent_thin_parts(V), h.T, h.targets, V, h.zt, loss + t0, lse + t0, status, s)) != cudaSuccess)
+      if ((e = run_join(h.stats, xent_thin_parts(V), h.T, h.targets, V, h.zt, loss + t0, lse + t0, is_bf16 && xent_thin_columns(h.T) == 32,
+                        status, s)) != cudaSuccess)
         return e;
     }
     return cudaSuccess;
@@ -558,7 +563,7 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
   g.zt = at<float>(ws, p.zt);
   XENT_STEP("xent_logits", s, launch_xent_gemm(g, wait_ns, s));
   const int parts = static_cast<int>((V + kXentPart - 1) / kXentPart);
-  return run_join(g.stats, parts, T, targets, V, g.zt, loss, lse, status, s);
+  return run_join(g.stats, parts, T, targets, V, g.zt, loss, lse, 0, status, s);
 }
 
 cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,

@@ -30,7 +30,12 @@
 // whose cost hardly depends on N. Runs of sums as in xent_gemm.cu: 512 fp32
 // products, 1024 of bf16 for the logits' statistics, there in four
 // accumulators by turns (HBM is the bound, and a quarter of the length is a
-// quarter of what is cut off).
+// quarter of what is cut off). Few rows have no mean over many to hide an error
+// in: up to 32 of fp32 256 products (V = 64000, D = 1024: dz 60.6 us with 512,
+// 61.8 with 256, 69.9 with 128); of bf16 512, up to two rows 256, with what
+// each addition of a run leaves out carried over (the largest error of 64
+// losses, T = 1: 2.4e-6 in runs of 1024, 1.4e-6 of 512, 8.6e-7 of 256; V =
+// 64000, D = 4096: 98 us without, 100, 103 and 113).
 #include "gemm_common.cuh"
 #include "xent_device.cuh"
 
@@ -382,11 +387,15 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
     for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
       int slice, m0, k0, kbs;
       decode(tile, slice, m0, k0, kbs);
-      float sum[N / 32][32];
+      // What the additions of runs to `sum` have left out.
+      constexpr bool CARRY = !F32 && KIND == kThinStats && N == 32;
+      float sum[N / 32][32], rest[CARRY ? 32 : 1];
 #pragma unroll
       for (int c = 0; c < N / 32; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < (CARRY ? 32 : 1); ++i) rest[i] = 0.f;
       for (int r = 0; r < kbs; r += p.run) {
         // The four warps go on, or give up, together: they meet at barriers below.
         ok = all_of_epilogue(wait_bounded(acc_full + acc, acc_phase, guard, kSiteEpilogue));
@@ -399,7 +408,15 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
           __syncwarp();
           tmem_ld_32cols(t0 + 32 * c, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[c % (N / 32)][i] += v[i];
+          for (int i = 0; i < 32; ++i) {
+            if constexpr (CARRY) {
+              const float add = v[i] + rest[i], s = sum[0][i] + add;
+              rest[i] = fabsf(s) < INFINITY ? add - (s - sum[0][i]) : 0.f;
+              sum[0][i] = s;
+            } else {
+              sum[c % (N / 32)][i] += v[i];
+            }
+          }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -454,7 +471,10 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const bool hot = m == s_target[32 * c + i];
-            if (hot) p.g.zt[32 * c + i] = sum[c][i];
+            if (hot) {
+              p.g.zt[32 * c + i] = sum[c][i];
+              if constexpr (CARRY) p.g.zt_rest[i] = rest[i];
+            }
             if (hot || m >= p.g.M) sum[c][i] = -INFINITY;
             v[i] = sum[c][i];
           }
@@ -525,7 +545,7 @@ cudaError_t launch_thin(const XentThin& g, int kind, uint64_t wait_ns, cudaStrea
   p.kb_per_slice = (p.k_blocks + g.slices - 1) / g.slices;
   p.slices = (p.k_blocks + p.kb_per_slice - 1) / p.kb_per_slice;
   p.tiles = p.tiles_m * p.slices;
-  p.run = g.f32 ? (g.T <= 32 ? 4 : 8) : kind == kThinStats ? 16 : p.k_blocks;
+  p.run = g.f32 ? (g.T <= 32 ? 4 : 8) : kind == kThinStats ? (g.T <= 2 ? 4 : g.T <= 32 ? 8 : 16) : p.k_blocks;
   p.wait_ns = wait_ns;
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidSymbol;
