@@ -482,10 +482,21 @@ int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int
  *            T = 0 clears dW.
  *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 1) bytes.
  * Rows that do not count must still hold finite X: they enter dW's product
- * with a factor of zero. */
+ * with a factor of zero.
+ * The target's exp(z - lse) - 1 is off by up to 2^-22 (1 + |lse|), from lse's
+ * rounding: of a row whose loss is not far above that it holds few digits or
+ * none. tpmlp_xent_backward_saved keeps them. */
 int tpmlp_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse, const float* dloss,
                         int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW, void* workspace,
                         size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* The same with the loss that tpmlp_xent_forward wrote beside lse: the target's
+ * dz is dloss_t expm1(-loss_t), which keeps its digits however certain the row.
+ *   loss     device fp32 [T], as tpmlp_xent_forward wrote it.
+ * Other arguments and the workspace as for tpmlp_xent_backward. */
+int tpmlp_xent_backward_saved(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
+                              const float* dloss, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW,
+                              void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
 
 /* Embedding lookup out_t = scale * E[id_t].
  *   E    device [V, D] of type dt, any D >= 1.

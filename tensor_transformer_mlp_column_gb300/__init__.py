@@ -88,6 +88,7 @@ SIGNATURES = {
     "tpmlp_xent_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "tpmlp_xent_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "tpmlp_xent_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "tpmlp_xent_backward_saved": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "tpmlp_embed_forward": (_I, [_P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P, _P]),
     "tpmlp_embed_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "tpmlp_embed_backward": (_I, [_P, _I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
@@ -657,8 +658,9 @@ def tpmlp_xent_forward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
 
 def tpmlp_xent_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
                         dloss: torch.Tensor, dX: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
-                        workspace: Optional[torch.Tensor] = None, stream=None):
-    """Gradients of sum(dloss * loss) of tpmlp_xent_forward: (dX [T, D], dW [V, D]) of X's dtype."""
+                        workspace: Optional[torch.Tensor] = None, stream=None, loss: Optional[torch.Tensor] = None):
+    """Gradients of sum(dloss * loss) of tpmlp_xent_forward: (dX [T, D], dW [V, D]) of X's dtype.
+    With the forward's loss (tpmlp_xent_backward_saved) nearly certain rows keep their target's part."""
     T, D, V = _xent_shapes(X, W)
     dt, l = _type(X), lib()
     with _On(stream) as on:
@@ -667,9 +669,13 @@ def tpmlp_xent_backward(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
         dX, xp = _output(dX, (T, D), X.dtype, dev, "dX")
         dW, vp = _output(dW, (V, D), X.dtype, dev, "dW")
         ws, wp, wn = _space(_xent_workspace(dev, T, D, V, dt, 1), workspace, dev)
-        _check(l.tpmlp_xent_backward(x, w, t, _like(lse, (T,), torch.float32, dev, "lse"),
-                                     _like(dloss, (T,), torch.float32, dev, "dloss"), T, D, V, dt, xp, vp, wp, wn,
-                                     on.raw), "tpmlp_xent_backward")
+        rest = (_like(lse, (T,), torch.float32, dev, "lse"), _like(dloss, (T,), torch.float32, dev, "dloss"), T, D, V, dt,
+                xp, vp, wp, wn, on.raw)
+        if loss is None:
+            _check(l.tpmlp_xent_backward(x, w, t, *rest), "tpmlp_xent_backward")
+        else:
+            _check(l.tpmlp_xent_backward_saved(x, w, t, _like(loss, (T,), torch.float32, dev, "loss"), *rest),
+                   "tpmlp_xent_backward_saved")
     return dX, dW
 
 

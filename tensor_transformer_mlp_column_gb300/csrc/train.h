@@ -113,6 +113,7 @@ struct XentGemm {
   float2* stats;                     // [ceil(N / kXentPart)][M]: max in units of log2, sum of 2^(z - max)
   float* zt;                         // [M]: the target's logit
   const float* lse;                  // [M]
+  const float* loss;                 // [M] or null: of a target dz from it, see kXentGrad
   const float* dloss;                // [M]
   const float* dmax;                 // [kXentDmaxParts] parts of the largest |dloss|; as the scale of kXentOut* (may be null)
   XentDmax rows;                     // kXentGrad*: in the place of dmax
@@ -139,7 +140,7 @@ struct XentThin {
   float2* stats;                    // [xent_thin_parts(M)][T]
   float* zt;
   float* zt_rest;                   // bf16, up to 32 rows: what zt's rounding left out
-  const float *lse, *dloss, *dmax;
+  const float *lse, *loss, *dloss, *dmax;  // loss may be null
   XentDmax rows;                    // as in XentGemm, of all groups
   __nv_bfloat16* dz;                // rows [T][pitch] of planes that are `plane` apart
   int64_t plane, pitch, dz_columns; // of dz's columns dz_columns are written (zeros from M on)
@@ -172,7 +173,8 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward);
 cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                              int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
                              cudaStream_t s);
-cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,
+// loss: as the forward wrote it, or null.
+cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
                               const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
                               void* ws, uint64_t wait_ns, cudaStream_t s);
 

@@ -197,6 +197,30 @@ int grad_call(const void* const* grads, const int64_t* counts, const tpmlp_dtype
   return TPMLP_OK;
 }
 
+// loss: the forward's, or null.
+int xent_backward(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
+                  const float* dloss, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW, void* ws,
+                  size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_xent(T, D, V, dt);
+  if (rc) return rc;
+  if (!dW || !al16(dW))
+    return set_error(dW ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "dW must not be NULL and must be 16-byte aligned");
+  if (T == 0) {
+    if ((rc = current_sm103())) return rc;
+    TRAIN_TRY(cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * D * (dt == TPMLP_BF16 ? 2 : 4), stream));
+    return TPMLP_OK;
+  }
+  if (!X || !W || !targets || !lse || !dloss || !dX || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
+  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(lse) || !al_rows(dloss) || !al16(dX) || !al16(ws))
+    return set_error(TPMLP_ERR_ALIGN, "X, W, dX and workspace must be 16-byte aligned, targets 8, lse and dloss 4");
+  const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 1).total;
+  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if ((rc = current_sm103())) return rc;
+  TRAIN_TRY(run_xent_backward(X, W, targets, loss, lse, dloss, T, D, V, dt == TPMLP_BF16, dX, dW, ws, wait_ns(),
+                              stream));
+  return TPMLP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -225,23 +249,15 @@ int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int
 int tpmlp_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse, const float* dloss,
                         int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW, void* ws, size_t ws_bytes,
                         tpmlp_stream_t stream) {
-  int rc = check_xent(T, D, V, dt);
-  if (rc) return rc;
-  if (!dW || !al16(dW))
-    return set_error(dW ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "dW must not be NULL and must be 16-byte aligned");
-  if (T == 0) {
-    if ((rc = current_sm103())) return rc;
-    TRAIN_TRY(cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * D * (dt == TPMLP_BF16 ? 2 : 4), stream));
-    return TPMLP_OK;
-  }
-  if (!X || !W || !targets || !lse || !dloss || !dX || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
-  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(lse) || !al_rows(dloss) || !al16(dX) || !al16(ws))
-    return set_error(TPMLP_ERR_ALIGN, "X, W, dX and workspace must be 16-byte aligned, targets 8, lse and dloss 4");
-  const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 1).total;
-  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
-  if ((rc = current_sm103())) return rc;
-  TRAIN_TRY(run_xent_backward(X, W, targets, lse, dloss, T, D, V, dt == TPMLP_BF16, dX, dW, ws, wait_ns(), stream));
-  return TPMLP_OK;
+  return xent_backward(X, W, targets, nullptr, lse, dloss, T, D, V, dt, dX, dW, ws, ws_bytes, stream);
+}
+
+int tpmlp_xent_backward_saved(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
+                              const float* dloss, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW,
+                              void* ws, size_t ws_bytes, tpmlp_stream_t stream) {
+  if (T > 0 && !loss) return set_error(TPMLP_ERR_ARG, "loss must not be NULL");
+  if (T > 0 && !al_rows(loss)) return set_error(TPMLP_ERR_ALIGN, "loss must be 4-byte aligned");
+  return xent_backward(X, W, targets, loss, lse, dloss, T, D, V, dt, dX, dW, ws, ws_bytes, stream);
 }
 
 int tpmlp_embed_forward(const void* E, const int64_t* ids, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, float scale,

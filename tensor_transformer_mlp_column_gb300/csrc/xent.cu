@@ -566,7 +566,7 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
   return run_join(g.stats, parts, T, targets, V, g.zt, loss, lse, 0, status, s);
 }
 
-cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse,
+cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
                               const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,
                               void* ws, uint64_t wait_ns, cudaStream_t s) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 1);
@@ -595,6 +595,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
       h.V = V;
       h.col0 = v0;
       h.lse = lse + t0;
+      h.loss = loss ? loss + t0 : nullptr;
       h.dloss = dloss + t0;
       h.dmax = dmax;
       h.rows = rows;
@@ -620,6 +621,7 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
     g.V = V;
     g.col0 = v0;
     g.lse = lse;
+    g.loss = loss;
     g.dloss = dloss;
     g.dmax = dmax;
     g.rows = rows;

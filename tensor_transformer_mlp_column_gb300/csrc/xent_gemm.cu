@@ -339,6 +339,9 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
       // Rows' own values, loaded while the products run.
       int64_t hot = -1;  // the target's column, or none
       float lse2 = 0.f, rs = 0.f;
+      // The target's dz / rs = exp(z - lse) - 1, or from the loss, of which it is -(1 - p) = expm1(-loss): where the row
+      // is nearly certain, the former has only the digits that lse's rounding leaves (loss 1e-6 at z = 40: none).
+      float own = -1.f;
       if constexpr (EPI == kXentStats || EPI == kXentGrad || EPI == kXentGradF32) {
         if (row_ok) {
           const int64_t t = p.g.targets[m];
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
           if constexpr (EPI != kXentStats) {
             // fp32: lse itself, see below.
             lse2 = EPI == kXentGrad ? p.g.lse[m] * kLog2e : p.g.lse[m];
+            if (counts && p.g.loss) own = expm1f(-p.g.loss[m]);
             const float d = p.g.dloss[m];
             rs = counts && d != 0.f ? d / dmax : 0.f;
           }
@@ -434,8 +438,9 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
             v[i] = EPI == kXentGrad ? exp2_approx(fmaf(v[i], kLog2e, -lse2)) : expf(v[i] - lse2);
           const int64_t h = hot - n0;
           if (h >= 0 && h < 32) {
+            const float keep = p.g.loss ? 0.f : 1.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = h == i ? v[i] - 1.f : v[i];
+            for (int i = 0; i < 32; ++i) v[i] = h == i ? fmaf(v[i], keep, own) : v[i];
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = rs != 0.f ? v[i] * rs : 0.f;

@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ int s_target[64];
-  __shared__ float s_lse[64], s_rs[64], s_ref[4][64], s_sum[4][64], s_base[64];
+  __shared__ float s_lse[64], s_rs[64], s_own[64];  // own: as in xent_gemm.cu
+  __shared__ float s_ref[4][64], s_sum[4][64], s_base[64];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -374,9 +375,10 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         const bool counts = t >= 0 && t < p.g.V;
         s_target[et] = counts ? static_cast<int>(t - p.g.col0) : INT_MIN;  // below 0 too for an earlier piece's
         if constexpr (KIND == kThinGrad) {
-          s_lse[et] = in ? p.g.lse[et] : 0.f;
           const float d = in ? p.g.dloss[et] : 0.f;
+          s_lse[et] = in ? p.g.lse[et] : 0.f;
           s_rs[et] = counts && d != 0.f ? d / dmax : 0.f;
+          s_own[et] = in && p.g.loss ? expm1f(-p.g.loss[et]) : -1.f;
         }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -439,6 +441,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         }
       } else if constexpr (KIND == kThinGrad) {
         if (m < p.g.dz_columns) {
+          const float keep = p.g.loss ? 0.f : 1.f;
           // Once for both halves of N = 64: the code of 64 columns in a row does not fit the instruction cache
           // (T = 64, V = 128000, D = 1024, fp32: 158 us, and 124 so).
 #pragma unroll 1
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
               if (t < p.g.T) {
                 const float z = c == 0 ? sum[0][i] : sum[N / 32 - 1][i], rs = s_rs[t];
                 float d = F32 ? expf(z - s_lse[t]) : exp2_approx((z - s_lse[t]) * kXentLog2e);
-                if (m == s_target[t]) d -= 1.f;
+                if (m == s_target[t]) d = fmaf(d, keep, s_own[t]);
                 d = rs != 0.f && m < p.g.M ? d * rs : 0.f;
 #pragma unroll
                 for (int pl = 0; pl < (F32 ? kXentPlanes : kThinDzPlanes); ++pl) {

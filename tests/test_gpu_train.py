@@ -271,6 +271,65 @@ def test_xent_loss_of_nearly_certain_rows(tp, T, V, dtype):
     _close(lse, z.gather(1, t[:, None])[:, 0] + ref, 2 * U32 * (lse.double().abs() + ref), "lse")
 
 
+class _WithLoss:
+    """The library with the forward's loss handed to the backward."""
+
+    def __init__(self, tp):
+        self.tp = tp
+
+    def __getattr__(self, name):
+        return getattr(self.tp, name)
+
+    def tpmlp_xent_forward(self, *a, **kw):
+        self.loss, lse = self.tp.tpmlp_xent_forward(*a, **kw)
+        return self.loss, lse
+
+    def tpmlp_xent_backward(self, *a, **kw):
+        return self.tp.tpmlp_xent_backward(*a, loss=self.loss, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,V", [(1, 64, 257), (1, 8, 1), (9, 1032, 4000), (33, 264, 1000), (150, 520, 700), (257, 136, 1000),
+                                   (192, 2048, 8200), (600, 1032, 8300), (34000, 16, 9000)])
+def test_xent_gradients_from_the_loss(tp, T, D, V, dtype):
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + D + V)
+    _check_xent(_WithLoss(tp), X, W, t, dloss, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(1, 300), (3, 5000), (40, 5000), (64, 300), (150, 600), (300, 5000), (2100, 300)])
+def test_xent_gradients_of_nearly_certain_rows(tp, T, V, dtype):
+    # The rows of the loss's test above: 1 - p down to 1e-12, which the fp32 exp(z - lse) - 1 near 40 does not hold, and
+    # which is as large as all other ids' parts together. Bounds relative to each entry of dz.
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    W = torch.randint(-1, 2, (V, 64), generator=g, device="cuda").to(DT[dtype])
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = W[t].contiguous()
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, dloss, loss=loss)
+    tp.tpmlp_check_status()
+    z = X.double() @ W.double().T
+    e = z - z.gather(1, t[:, None])
+    gap = e.abs().max(dim=1).values[:, None]
+    e.scatter_(1, t[:, None], -math.inf)
+    ref = torch.log1p(torch.exp(e).sum(1))[:, None]
+    dz = torch.exp(e - ref)
+    dz.scatter_(1, t[:, None], torch.expm1(-ref))
+    dz *= dloss.double()[:, None]
+    # Exponents: lse's rounding, log2 e as a constant, its products and the difference, each off by its size times U32;
+    # the exponential by 4 U32; the loss as in its test, expm1 2 U32 more; dloss / max and the product 2. Then dz's rounding.
+    size = gap + z.abs().max(dim=1).values[:, None]
+    half = 4 * U32 if dtype == "f32" else 1.01 * U16 if T > 64 else 1.01 * U16 ** 2
+    edz = dz.abs() * ((4 * size + 3 * gap + 90) * U32 + half)
+    out = U16 * 1.01 if dtype == "bf16" else 2 * U32
+    for got, a, b, k, what in ((dX, dz, W.double(), V, "dX"), (dW, dz.T, X.double(), T, "dW")):
+        want = a @ b
+        err = edz if what == "dX" else edz.T
+        tol = err @ b.abs() + (a.abs() @ b.abs()) * (_sum_bound(k, dtype) + 80 * U32) + out * want.abs()
+        _close(got, want, tol + 1e-30, what)
+
+
 def test_xent_infinities_stay_in_their_row(tp):
     X, W, t, dloss = _xent_inputs(40, 64, 300, "bf16", seed=12, masked=0.0)
     loss, lse = tp.tpmlp_xent_forward(X, W, t)
@@ -926,4 +985,13 @@ def test_binding_refuses_wrong_tensors(tp):
         tp.tpmlp_embed_backward(X, t, 50, accumulate=True)
     with pytest.raises(ValueError):
         tp.tpmlp_embed_forward(W, t.to(torch.int32))
+    tp.tpmlp_check_status()
+
+
+def test_binding_refuses_a_wrong_loss(tp):
+    X, W, t, dloss = _xent_inputs(16, 64, 50, "bf16", seed=62)
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    for bad in (loss[:5], loss.double(), loss.cpu(), torch.stack([loss, loss], 1)[:, 0]):
+        with pytest.raises(ValueError):
+            tp.tpmlp_xent_backward(X, W, t, lse, dloss, loss=bad)
     tp.tpmlp_check_status()

@@ -190,3 +190,18 @@ def test_calls_without_a_gpu_report_errors(tp):
     assert _embed_forward(tp) in bad
     assert _embed_backward(tp) in bad
     assert _embed_backward(tp, T=0) in bad
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(loss=None), "TPMLP_ERR_ARG"),
+    (dict(loss=FAKE + 2), "TPMLP_ERR_ALIGN"),
+    (dict(lse=None), "TPMLP_ERR_ARG"),
+    (dict(dloss=FAKE + 2), "TPMLP_ERR_ALIGN"),
+    (dict(D=12), "TPMLP_ERR_SHAPE"),
+    (dict(dW=None, T=0), "TPMLP_ERR_ARG"),
+    (dict(nb=16), "TPMLP_ERR_WORKSPACE"),
+])
+def test_xent_backward_saved_argument_errors(tp, kw, code):
+    a = dict(X=FAKE, W=FAKE, t=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, T=8, D=64, V=100, dt=1, dX=FAKE, dW=FAKE, ws=FAKE, nb=WS)
+    a.update(kw)
+    assert tp.STATUS_NAMES[tp.lib().tpmlp_xent_backward_saved(*a.values(), None)] == code, tp.tpmlp_last_error()
