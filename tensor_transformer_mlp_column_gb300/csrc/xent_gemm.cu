@@ -50,6 +50,8 @@ namespace {
 constexpr int kXThreads = 384;  // warp 0 TMA, warp 1 MMA, warps 2, 3 idle, warps 4..11 epilogue
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
+constexpr int kRunsRegsFirst = 56, kRunsRegsEpi = 224;  // registers of a thread of the first four warps, of the epilogue's
+constexpr int kRunsRegs = 128 * kRunsRegsFirst + 256 * kRunsRegsEpi;
 constexpr int kSub = 2;         // K blocks of a stage
 constexpr uint32_t kSubBytes = 128 * BK * 2;
 constexpr uint32_t kOutBlock = 32 * 128;  // staging: 32 rows of 128 bytes
@@ -58,10 +60,16 @@ constexpr int BN = 256;
 // where there is one row of tiles, which waits for W anyway (T = 200, V = 32000,
 // D = 1024: 24.6 -> 25.3 us, the losses off by 3.8e-7 in the place of 8.0e-7; T =
 // 1000 48.4 -> 52.4). Of fp32 data's high planes 8, where more is wanted; 128 of
-// the five other plane pairs, which come first and whose sums are at most 2^-8
-// of the whole (cut like the high planes' they made six runs of K = 512 instead
-// of two: T = 1000, V = 32001, logits 124 -> 114 us).
+// the five other plane pairs, which come first and whose sums are at most 2^-7
+// of the sum of magnitudes (cut like the high planes' they made six runs of K =
+// 512 instead of two: T = 1000, V = 32001, logits 124 -> 114 us).
 constexpr int kRunLong = 16, kRunShort = 8, kRunSmall = 128;
+// What is rounded to bf16 afterwards stays one sum up to kWhole K blocks: over N
+// additions of 16 products of one sign it loses 1.4 N 2^-24 of itself. dz: 4096
+// products, 2.1e-5 of a logit, so 6e-4 of a share of softmax at logits of 30,
+// where the rounding of dz is up to 3.9e-3 (uncut, D = 262144 put them off by 9
+// %). dX and dW: 65536, 3.4e-4.
+constexpr int kWholeGrad = 64, kWholeOut = 1024, kRunOut = 256;
 constexpr int kDrainPauseNs = 25;  // per K block of a run, between a warp's reads of it
 
 template <int EPI, bool RUNS>
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
   bool aborted = false;
 
   if (warp < kEpiWarp0) {
-    if constexpr (RUNS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (RUNS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRunsRegsFirst));
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer
       int stage = 0;
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
       }
     }
   } else {
-    if constexpr (RUNS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (RUNS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRunsRegsEpi));
     // ---------------- epilogue (warps 4..11 of every CTA)
     const int quarter = warp & 3;         // its tensor-memory lane quarter: rows quarter*32 .. +31 of this CTA's 128
     const int half = (warp - kEpiWarp0) >> 2;     // columns half*128 .. +127 of the tile
@@ -643,6 +651,10 @@ cudaError_t launch_epi(const XParams& p, cudaStream_t s) {
   if (dev < 0 || dev >= 64) dev = 0;
   int cached = max_clusters[dev].load(std::memory_order_relaxed);
   if (!cached) {
+    // The epilogue's registers come out of what the block was launched with: with less, setmaxnreg would wait for ever.
+    cudaFuncAttributes a;
+    if (RUNS && (e = cudaFuncGetAttributes(&a, kern)) != cudaSuccess) return e;
+    if (RUNS && a.numRegs * kXThreads < kRunsRegs) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
     int n = 0;
     cfg.numAttrs = 1;  // the query takes the cluster shape only
@@ -679,24 +691,27 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
   p.wait_ns = wait_ns;
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidSymbol;
-  // Runs where an fp32 result is wanted (the statistics and all of fp32) of a
-  // sum longer than one, cut evenly. dz and gradients that are rounded to bf16
-  // lose nothing by one long sum.
-  const int total = g.pairs * p.kb_per_slice, most = g.pairs > 1 || g.M <= 256 ? kRunShort : kRunLong;
+  // Runs of a sum longer than one where an fp32 result is wanted (the statistics
+  // and all of fp32), and of one longer than `whole` elsewhere, cut evenly.
+  const int total = g.pairs * p.kb_per_slice;
+  const bool f32 = g.pairs == kXentPairs;
+  int most = f32 || g.M <= 256 ? kRunShort : kRunLong, whole = most;
+  if (!f32 && g.epi == kXentGrad) most = kRunLong, whole = kWholeGrad;
+  if (!f32 && (g.epi == kXentOutBf16 || g.epi == kXentOutF32)) most = kRunOut, whole = kWholeOut;
   const int runs = (total + most - 1) / most;
   p.run = ((total + runs - 1) / runs + 1) / 2 * 2;
-  const bool cut = total > most;
+  const bool cut = total > whole;
   switch (g.epi) {
     case kXentStats:
       return cut ? launch_epi<kXentStats, true>(p, s) : launch_epi<kXentStats, false>(p, s);
     case kXentGrad:
-      return launch_epi<kXentGrad, false>(p, s);
+      return cut ? launch_epi<kXentGrad, true>(p, s) : launch_epi<kXentGrad, false>(p, s);
     case kXentGradF32:
       return launch_epi<kXentGradF32, true>(p, s);  // it holds a warp's columns in registers anyway
     case kXentOutBf16:
-      return launch_epi<kXentOutBf16, false>(p, s);
+      return cut ? launch_epi<kXentOutBf16, true>(p, s) : launch_epi<kXentOutBf16, false>(p, s);
     case kXentOutF32:
-      return cut && g.pairs > 1 ? launch_epi<kXentOutF32, true>(p, s) : launch_epi<kXentOutF32, false>(p, s);
+      return cut ? launch_epi<kXentOutF32, true>(p, s) : launch_epi<kXentOutF32, false>(p, s);
     default:
       return cudaErrorInvalidValue;
   }

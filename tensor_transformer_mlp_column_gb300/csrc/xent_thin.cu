@@ -28,7 +28,7 @@
 // so that products of one size share an accumulator, the small ones are not
 // cut off against the large sum, and 3 MMAs do what 6 of N = 32 columns did,
 // whose cost hardly depends on N. Runs of sums as in xent_gemm.cu: 512 fp32
-// products, 1024 of bf16 for the logits' statistics, there in four
+// products; of bf16 16384 for dX, 1024 for dz and the logits' statistics, there in four
 // accumulators by turns (HBM is the bound, and a quarter of the length is a
 // quarter of what is cut off). Few rows have no mean over many to hide an error
 // in: up to 32 of fp32 256 products (V = 64000, D = 1024: dz 60.6 us with 512,
@@ -548,7 +548,12 @@ cudaError_t launch_thin(const XentThin& g, int kind, uint64_t wait_ns, cudaStrea
   p.kb_per_slice = (p.k_blocks + g.slices - 1) / g.slices;
   p.slices = (p.k_blocks + p.kb_per_slice - 1) / p.kb_per_slice;
   p.tiles = p.tiles_m * p.slices;
-  p.run = g.f32 ? (g.T <= 32 ? 4 : 8) : kind == kThinStats ? (g.T <= 2 ? 4 : g.T <= 32 ? 8 : 16) : p.k_blocks;
+  if (g.f32)
+    p.run = g.T <= 32 ? 4 : 8;
+  else if (kind == kThinStats)
+    p.run = g.T <= 2 ? 4 : g.T <= 32 ? 8 : 16;
+  else
+    p.run = kind == kThinGrad ? 16 : 256;
   p.wait_ns = wait_ns;
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidSymbol;

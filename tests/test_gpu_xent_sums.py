@@ -101,6 +101,70 @@ def test_statistics_of_long_sums(tp, dtype, T, D, bound):
     tp.tpmlp_check_status()
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 20), ("bf16", 64), ("bf16", 100), ("bf16", 600), ("f32", 1),
+                                     ("f32", 64), ("f32", 300)])
+def test_gradients_of_long_sums(tp, dtype, T):
+    # Two ids with long sums share each row's softmax about evenly, the target has neither: dX is their rows times their
+    # shares. The backward's own logits have to be about as good as those of lse: 16384 uncut additions lose 1.4 * 16384
+    # U32 of 72, and the shares 10 %.
+    D = 1 << 18 if dtype == "bf16" else 1 << 16
+    g = torch.Generator(device="cuda").manual_seed(T)
+    X = _ones(g, (T, D), dtype)
+    W = torch.zeros(V, D, device="cuda", dtype=DT[dtype])
+    W[3], W[17] = _ones(g, (D,), dtype) * _scale(D), _ones(g, (D,), dtype) * _scale(D)
+    t = torch.full((T,), V - 1, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, dloss)
+    tp.tpmlp_check_status()
+    z = X.double() @ W.double().T
+    ref = torch.logsumexp(z, 1)[:, None]
+    dz = torch.exp(z - ref)
+    dz.scatter_add_(1, t[:, None], -torch.ones_like(ref))
+    dz *= dloss.double()[:, None]
+    # lse: the loosest of the forward's bounds above at this length; the logits: bf16 runs of 16 K blocks, fp32 as above.
+    if dtype == "bf16":
+        lse_bound, z_bound = _run(64) + _joined(4 * D // 1024), _run(64) + _joined(D // 1024)
+        half = 1.01 * (U16 if T > 64 else U16 ** 2)
+    else:
+        lse_bound = z_bound = _run(32) + _run(512) * 2.0 ** -6 + _joined(3 * D // 256) + 4
+        half = 4 * U32
+    share = (lse_bound + z_bound + 12) * U32 * z.max()
+    edz = dz.abs() * (torch.expm1(share) + half + 16 * U32)
+    out = 1.01 * U16 if dtype == "bf16" else 2 * U32
+    for got, a, e, b, k in ((dX, dz, edz, W.double(), V), (dW, dz.T, edz.T, X.double(), T)):
+        want = a @ b
+        # Sums of few terms, T or V of them: as many whole steps at most.
+        tol = e @ b.abs() + (a.abs() @ b.abs()) * (6 * k / 16 + 84) * 2 * U32 + out * want.abs() + 1e-30
+        err = (got.double() - want).abs()
+        assert bool((err <= tol).all()), ((err / tol).max().item(), share.item())
+
+
+def test_gradient_of_a_long_vocabulary(tp):
+    # X = 0: every share is 2^-18 and dX the mean of W's rows (the targets' is zero), sums of one sign over 16384 additions
+    # in tiles that fill the GPU, so that nothing is gained by slices of them. The rounding to bf16 averages out over the
+    # columns, whose sums have all mantissas: U16 / sqrt(3 * 19456) and less. A run of 256 K blocks has 1024 additions, which
+    # lose 1.4 * 1024 U32 = 8.5e-5 of it at most (the products have few bits here); in one sum they lost 4.0e-4.
+    T, D, V = 100, 19456, 1 << 18
+    g = torch.Generator(device="cuda").manual_seed(1)
+    f = 1 + torch.rand(D, generator=g, device="cuda")
+    W = torch.empty(V, D, device="cuda", dtype=torch.bfloat16)
+    total = torch.zeros(D, device="cuda", dtype=torch.float64)
+    for v in range(0, V, 8192):
+        W[v:v + 8192] = _ones(g, (8192, D), "bf16") * f
+        W[V - 1] = 0
+        total += W[v:v + 8192].sum(0, dtype=torch.float64)
+    X = torch.zeros(T, D, device="cuda", dtype=torch.bfloat16)
+    t = torch.full((T,), V - 1, device="cuda")
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+    dX, dW = tp.tpmlp_xent_backward(X, W, t, lse, torch.ones_like(loss), loss=loss)
+    tp.tpmlp_check_status()
+    assert bool((dW == 0).all())
+    rel = dX.double() / (total / V) - 1
+    assert rel.abs().max().item() <= 1.01 * U16 + 1e-3
+    assert rel.mean(1).abs().max().item() <= 2 * 8.5e-5 + 5 * U16 / (3 * D) ** 0.5
+
+
 @pytest.mark.parametrize("T,D,V", [(1, 264, 300), (2, 1032, 1000), (3, 264, 2000), (32, 520, 1000), (64, 264, 3000)])
 def test_gradients_of_few_bf16_rows_are_rounded_once(tp, T, D, V):
     # dz of up to 64 rows is two bf16 pieces, off by U16^2 at most, so that what shows in the gradients is their own
