@@ -199,8 +199,8 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 }
 // Waits until every committed bulk group has completed.
 __device__ __forceinline__ void bulk_wait_group_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Orders this thread's generic-proxy shared-memory writes before later
-// async-proxy (TMA) reads of them.
+// Orders this thread's generic-proxy accesses to shared memory before later
+// async-proxy (TMA) ones: writes before reads of them, reads before writes.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

@@ -333,6 +333,9 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
               f[4 * c] = x.x, f[4 * c + 1] = x.y, f[4 * c + 2] = x.z, f[4 * c + 3] = x.w;
             }
           }
+          // TMA writes this stage next: its writes are ordered behind these reads by the fence, not by the barrier alone.
+          // (Without it a lane's last 16 bytes came, once in some thousand calls, from the stage's next fill.)
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(raw_empty + rs);
           if ((rs += 2) >= C::RAW) rs = half, raw_phase ^= 1u;

@@ -149,6 +149,26 @@ def test_xent_of_a_few_rows(tp, T, D, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(64, 1024), (64, 512), (20, 512)])
+def test_xent_of_a_few_rows_is_the_same_every_time(tp, dtype, T, D):
+    # Several tiles a CTA, many calls: a stage of operands that is filled again while it is still being read shows in one
+    # call of some thousands.
+    V = 50257
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + D)
+    ref = tp.tpmlp_xent_forward(X, W, t)
+    gref = tp.tpmlp_xent_backward(X, W, t, ref[1], dloss)
+    differs = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(8000):
+        for a, b in zip(tp.tpmlp_xent_forward(X, W, t), ref):
+            differs += (a != b).any()
+        if i % 4 == 0:
+            for a, b in zip(tp.tpmlp_xent_backward(X, W, t, ref[1], dloss), gref):
+                differs += (a != b).any()
+    assert differs.item() == 0
+    tp.tpmlp_check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_xent_of_a_few_rows_that_do_not_count(tp, dtype):
     X, W, t, dloss = _xent_inputs(6, 64, 300, dtype, seed=18, masked=0.0)
     t[1], t[4], dloss[1], dloss[4] = -100, 300, float("nan"), float("inf")
