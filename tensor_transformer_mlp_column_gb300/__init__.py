@@ -89,6 +89,7 @@ SIGNATURES = {
     "tpmlp_xent_forward": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "tpmlp_xent_backward": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "tpmlp_xent_backward_saved": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "tpmlp_selftest_xent_stage_timeout": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _I, _I, _P, _SZ, _P]),
     "tpmlp_embed_forward": (_I, [_P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P, _P]),
     "tpmlp_embed_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "tpmlp_embed_backward": (_I, [_P, _I, _P, _I64, _I64, _I64, ctypes.c_float, _P, _I, _I, _P, _SZ, _P]),
@@ -836,3 +837,18 @@ def tpmlp_selftest_backward_withheld_fill(X: torch.Tensor, dY: torch.Tensor, sha
     _check(lib().tpmlp_selftest_backward_withheld_fill(_dev(X, "X"), _dev(dY, "dY"), X.shape[0], shards.handle,
                                                        fill, limit_ms, ws.data_ptr(), ws.numel() * ws.element_size(),
                                                        _stream(stream)), "tpmlp_selftest_backward_withheld_fill")
+
+
+def tpmlp_selftest_xent_stage_timeout(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, stage: int, limit_ms: int,
+                                      stream=None) -> None:
+    """Runs the cross entropy's logits with stage `stage` of the operands' ring never complete (test hook)."""
+    T, D, V = _xent_shapes(X, W)
+    dt, l = _type(X), lib()
+    with _On(stream) as on:
+        dev = on.dev
+        x, w, t = _ptr(X, dev, "X"), _ptr(W, dev, "W"), _ids(targets, T, dev, "targets")
+        loss, lp = _output(None, (T,), torch.float32, dev, "loss")
+        lse, ep = _output(None, (T,), torch.float32, dev, "lse")
+        ws, wp, wn = _space(_xent_workspace(dev, T, D, V, dt, 0), None, dev)
+        _check(l.tpmlp_selftest_xent_stage_timeout(x, w, t, T, D, V, dt, lp, ep, stage, limit_ms, wp, wn, on.raw),
+               "tpmlp_selftest_xent_stage_timeout")

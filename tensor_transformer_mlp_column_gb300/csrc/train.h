@@ -107,6 +107,7 @@ struct XentGemm {
   int group_m;
   int epi;
   int add;                           // kXentOutF32
+  int inject;                        // test hook: > 0: that stage (1-based) of every CTA's ring is never complete
   // kXentStats, kXentGrad*
   const int64_t* targets;            // [M]
   int64_t V, col0;                   // all ids; the id of column 0
@@ -147,6 +148,7 @@ struct XentThin {
   float* part;                      // dX: rows [T][M] of slices that are part_rows rows apart
   int64_t part_rows;
   int add;                          // dX: add to part
+  int inject;                       // test hook, as in XentGemm, of W's ring
 };
 int xent_thin_columns(int64_t T);
 int xent_thin_parts(int64_t V);
@@ -170,9 +172,10 @@ struct XentPlan {
   bool dx_part;               // dX goes through fp32 partial sums
 };
 XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward);
+// inject > 0 (test hook): only the first launch of the logits' product, with that stage never complete.
 cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                              int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
-                             cudaStream_t s);
+                             cudaStream_t s, int inject = 0);
 // loss: as the forward wrote it, or null.
 cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
                               const float* dloss, int64_t T, int64_t D, int64_t V, int is_bf16, void* dX, void* dW,

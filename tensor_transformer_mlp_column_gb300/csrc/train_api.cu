@@ -197,6 +197,22 @@ int grad_call(const void* const* grads, const int64_t* counts, const tpmlp_dtype
   return TPMLP_OK;
 }
 
+int xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt,
+                 float* loss, float* lse, void* ws, size_t ws_bytes, uint64_t limit_ns, int inject, cudaStream_t stream) {
+  int rc = check_xent(T, D, V, dt);
+  if (rc) return rc;
+  if (T == 0) return TPMLP_OK;
+  if (!X || !W || !targets || !loss || !lse || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
+  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(loss) || !al_rows(lse) || !al16(ws))
+    return set_error(TPMLP_ERR_ALIGN, "X, W and workspace must be 16-byte aligned, targets 8, loss and lse 4");
+  const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 0).total;
+  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if ((rc = current_sm103())) return rc;
+  TRAIN_TRY(run_xent_forward(X, W, targets, T, D, V, dt == TPMLP_BF16, loss, lse, ws, device_status_word(), limit_ns,
+                             stream, inject));
+  return TPMLP_OK;
+}
+
 // loss: the forward's, or null.
 int xent_backward(const void* X, const void* W, const int64_t* targets, const float* loss, const float* lse,
                   const float* dloss, int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, void* dX, void* dW, void* ws,
@@ -232,18 +248,17 @@ size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype d
 
 int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                        tpmlp_dtype dt, float* loss, float* lse, void* ws, size_t ws_bytes, tpmlp_stream_t stream) {
-  int rc = check_xent(T, D, V, dt);
-  if (rc) return rc;
-  if (T == 0) return TPMLP_OK;
-  if (!X || !W || !targets || !loss || !lse || !ws) return set_error(TPMLP_ERR_ARG, "a required pointer is NULL");
-  if (!al16(X) || !al16(W) || !al_ids(targets) || !al_rows(loss) || !al_rows(lse) || !al16(ws))
-    return set_error(TPMLP_ERR_ALIGN, "X, W and workspace must be 16-byte aligned, targets 8, loss and lse 4");
-  const size_t need = plan_xent(T, D, V, dt == TPMLP_BF16, 0).total;
-  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
-  if ((rc = current_sm103())) return rc;
-  TRAIN_TRY(run_xent_forward(X, W, targets, T, D, V, dt == TPMLP_BF16, loss, lse, ws, device_status_word(), wait_ns(),
-                             stream));
-  return TPMLP_OK;
+  return xent_forward(X, W, targets, T, D, V, dt, loss, lse, ws, ws_bytes, wait_ns(), 0, stream);
+}
+
+int tpmlp_selftest_xent_stage_timeout(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D,
+                                      int64_t V, tpmlp_dtype dt, float* loss, float* lse, int stage, int limit_ms,
+                                      void* ws, size_t ws_bytes, tpmlp_stream_t stream) {
+  if (T < 1) return set_error(TPMLP_ERR_ARG, "T = %lld must be >= 1", static_cast<long long>(T));
+  if (stage < 1 || stage > 3) return set_error(TPMLP_ERR_ARG, "stage = %d outside 1..3", stage);
+  if (limit_ms < 1 || limit_ms > 10000) return set_error(TPMLP_ERR_ARG, "limit_ms = %d outside 1..10000", limit_ms);
+  return xent_forward(X, W, targets, T, D, V, dt, loss, lse, ws, ws_bytes, static_cast<uint64_t>(limit_ms) * 1000000ull,
+                      stage, stream);
 }
 
 int tpmlp_xent_backward(const void* X, const void* W, const int64_t* targets, const float* lse, const float* dloss,

@@ -523,7 +523,7 @@ XentPlan plan_xent(int64_t T, int64_t D, int64_t V, int is_bf16, int backward) {
 
 cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                              int is_bf16, float* loss, float* lse, void* ws, int* status, uint64_t wait_ns,
-                             cudaStream_t s) {
+                             cudaStream_t s, int inject) {
   const XentPlan p = plan_xent(T, D, V, is_bf16, 0);
   Planes pl;
   cudaError_t e = planes_of(X, W, T, D, V, is_bf16, ws, p, &pl, s);
@@ -539,7 +539,9 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
       h.stats = stats + t0 * xent_thin_parts(V);
       h.zt = zt + t0;
       h.zt_rest = loss + t0;
+      h.inject = inject;
       XENT_STEP("xent_logits", s, launch_xent_thin_stats(h, wait_ns, s));
+      if (inject > 0) return cudaSuccess;
       if ((e = run_join(h.stats, xent_thin_parts(V), h.T, h.targets, V, h.zt, loss + t0, lse + t0, is_bf16 && xent_thin_columns(h.T) == 32,
                         status, s)) != cudaSuccess)
         return e;
@@ -561,7 +563,9 @@ cudaError_t run_xent_forward(const void* X, const void* W, const int64_t* target
   g.V = V;
   g.stats = at<float2>(ws, p.stats);
   g.zt = at<float>(ws, p.zt);
+  g.inject = inject;
   XENT_STEP("xent_logits", s, launch_xent_gemm(g, wait_ns, s));
+  if (inject > 0) return cudaSuccess;
   const int parts = static_cast<int>((V + kXentPart - 1) / kXentPart);
   return run_join(g.stats, parts, T, targets, V, g.zt, loss, lse, 0, status, s);
 }

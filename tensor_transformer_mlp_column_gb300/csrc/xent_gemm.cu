@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kXThreads, 1) xent_gemm_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(full + s, 1);   // even CTA: its producer's arrival (and the pair's bytes)
+      // Even CTA: its producer's arrival (and the pair's bytes). The test hook's stage waits for one that never comes.
+      mbar_init(full + s, p.g.inject == s + 1 ? 2 : 1);
       mbar_init(empty + s, 1);  // the pair's commit once its MMAs have read the stage
     }
     for (int b = 0; b < 2; ++b) {

@@ -152,18 +152,23 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ int s_issued, s_arrived[kConvWarps];  // fp32: K blocks of B issued, converted by each warp
   __shared__ int s_target[64];
   __shared__ float s_lse[64], s_rs[64], s_own[64];  // own: as in xent_gemm.cu
   __shared__ float s_ref[4][64], s_sum[4][64], s_base[64];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    // The test hook's stage of W's ring waits for an arrival that never comes.
+    auto more = [&](int s) { return p.g.inject == s + 1 ? 1 : 0; };
+#pragma unroll 1
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(full + s, F32 ? 1 + kConvWarps : 1);  // B's (or all) bytes; the converters
-      mbar_init(empty + s, 1);                        // commit of the MMAs that read it
+      mbar_init(full + s, F32 ? 1 + kConvWarps : 1 + more(s));  // B's (or all) bytes; the converters
+      mbar_init(empty + s, 1);                                  // commit of the MMAs that read it
     }
+#pragma unroll 1
     for (int s = 0; s < C::RAW; ++s) {
-      mbar_init(raw_full + s, 1);
+      mbar_init(raw_full + s, 1 + more(s));
       mbar_init(raw_empty + s, kConvWarps / 2);  // one half's warps take a stage
     }
     for (int b = 0; b < 2; ++b) {
@@ -172,6 +177,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    for (int w = 0; w < kConvWarps; ++w) s_arrived[w] = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, C::TMEM);
@@ -234,6 +240,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         }
       }
       if (!ok)
+#pragma unroll 1
         for (int s = 0; s < ST; ++s)
           if (issued >> s & 1u) wait_drain(f + s, (parity >> s) & 1u, p.wait_ns);
     }
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
   } else if (warp == 2) {
     if (F32 && lane == 0) {
       // ---------------- TMA of the B planes
-      int st = 0;
+      int st = 0, issued = 0;
       uint32_t phase = 0;
       const uint64_t keep = l2_policy(1);
       for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
@@ -293,6 +300,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
         decode(tile, slice, m0, k0, kbs);
         for (int q = 0; ok && q < kbs; ++q) {
           if (!(ok = wait_bounded(empty + st, phase ^ 1u, guard, kSiteProducer))) break;
+          ++issued;
           mbar_arrive_expect_tx(full + st, C::PLB * C::B_BYTES);
           uint8_t* dst = s_stage + st * C::STAGE;
           for (int b = 0; b < C::PLB; ++b)
@@ -300,12 +308,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
           if (++st == C::STAGES) st = 0, phase ^= 1u;
         }
       }
-      if (!ok) {
-        // The stage barriers also count the converters, which stop too: give copies in flight time to land.
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 200000ull) {
-        }
-      }
+      s_issued = issued;
     }
   } else if (warp >= kConvWarp0 && warp < kEpiWarp0) {
     if constexpr (F32) {
@@ -359,7 +362,10 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full + st);
+          if (lane == 0) {
+            mbar_arrive(full + st);
+            atomicAdd(&s_arrived[warp - kConvWarp0], 1);  // here, not in a register of each thread
+          }
           if (++st == C::STAGES) st = 0, phase ^= 1u;
         }
       }
@@ -518,6 +524,18 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
 
   tc_fence_before_sync();
   __syncthreads();
+  if (F32 && threadIdx.x == 0 && *abort_flag) {
+    // B's copies in flight: their stages' barriers lack the converters that gave up, whose arrivals are made here.
+#pragma unroll 1
+    for (int s = 0; s < C::STAGES; ++s) {
+      if (s_issued <= s) break;
+      const int last = s_issued - 1 - (s_issued - 1 - s) % C::STAGES;  // the stage's last K block
+#pragma unroll 1
+      for (int w = 0; w < kConvWarps; ++w)
+        if (s_arrived[w] <= last) mbar_arrive(full + s);
+      wait_drain(full + s, static_cast<uint32_t>(last / C::STAGES) & 1u, p.wait_ns);
+    }
+  }
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, C::TMEM);

@@ -111,3 +111,33 @@ def test_dual_backward_withheld_fill_times_out_and_library_recovers(tp):
     assert e.value.code == tp.TPMLP_ERR_TIMEOUT
     tp.tpmlp_check_status()
     _check_forward_and_backward(tp, inp, d, sh, w.N)
+
+
+# The cross entropy's products: CTA pairs (T > 64; fp32 and D > 1024 with sums in runs, two accumulators by turns), and W's
+# side as the tile for up to 64 rows (fp32: planes of W made on the way, of X loaded beside them). A stage of the operands'
+# ring never completes; every case has the six K blocks or more a tile that fill three stages of two.
+@pytest.mark.parametrize("dtype,T,D,V,stage", [
+    ("bf16", 300, 768, 5003, 1), ("bf16", 300, 2056, 5003, 3), ("f32", 300, 512, 5003, 2), ("f32", 600, 512, 60000, 3),
+    ("bf16", 20, 512, 5003, 3), ("bf16", 1, 512, 50257, 1), ("bf16", 50, 512, 50257, 2),
+    ("f32", 20, 512, 5003, 3), ("f32", 1, 512, 50257, 2), ("f32", 50, 512, 50257, 1)])
+def test_xent_stage_times_out_and_library_recovers(tp, dtype, T, D, V, stage):
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    X = torch.randn(T, D, generator=g, device="cuda").to(dt)
+    W = (torch.randn(V, D, generator=g, device="cuda") * 0.05).to(dt)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    dloss = torch.ones(T, device="cuda")
+
+    def step():
+        loss, lse = tp.tpmlp_xent_forward(X, W, t)
+        return [loss, lse, *tp.tpmlp_xent_backward(X, W, t, lse, dloss, loss=loss)]
+
+    ref = step()
+    tp.tpmlp_check_status()  # clean start
+    tp.tpmlp_selftest_xent_stage_timeout(X, W, t, stage, limit_ms=100)
+    with pytest.raises(tp.TpmlpError) as e:
+        tp.tpmlp_check_status()
+    assert e.value.code == tp.TPMLP_ERR_TIMEOUT
+    tp.tpmlp_check_status()
+    assert all(torch.equal(a, b) for a, b in zip(step(), ref))
+    tp.tpmlp_check_status()

@@ -205,3 +205,19 @@ def test_xent_backward_saved_argument_errors(tp, kw, code):
     a = dict(X=FAKE, W=FAKE, t=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, T=8, D=64, V=100, dt=1, dX=FAKE, dW=FAKE, ws=FAKE, nb=WS)
     a.update(kw)
     assert tp.STATUS_NAMES[tp.lib().tpmlp_xent_backward_saved(*a.values(), None)] == code, tp.tpmlp_last_error()
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(T=0), "TPMLP_ERR_ARG"),
+    (dict(stage=0), "TPMLP_ERR_ARG"),
+    (dict(stage=4), "TPMLP_ERR_ARG"),
+    (dict(limit_ms=0), "TPMLP_ERR_ARG"),
+    (dict(limit_ms=10001), "TPMLP_ERR_ARG"),
+    (dict(lse=None), "TPMLP_ERR_ARG"),
+    (dict(X=FAKE + 2), "TPMLP_ERR_ALIGN"),
+    (dict(nb=0), "TPMLP_ERR_WORKSPACE"),
+])
+def test_xent_stage_timeout_argument_errors(tp, kw, code):
+    a = dict(X=FAKE, W=FAKE, t=FAKE, T=8, D=64, V=100, dt=1, loss=FAKE, lse=FAKE, stage=1, limit_ms=100, ws=FAKE, nb=WS)
+    a.update(kw)
+    assert tp.STATUS_NAMES[tp.lib().tpmlp_selftest_xent_stage_timeout(*a.values(), None)] == code, tp.tpmlp_last_error()
