@@ -141,8 +141,8 @@ struct XentThin {
   float2* stats;                    // [xent_thin_parts(M)][T]
   float* zt;
   float* zt_rest;                   // bf16, up to 32 rows: what zt's rounding left out
-  const float *lse, *loss, *dloss, *dmax;  // loss may be null
-  XentDmax rows;                    // as in XentGemm, of all groups
+  const float *lse, *loss, *dloss;  // loss may be null
+  XentDmax rows;                    // of all groups: 3 kXentThinMax rows at most
   __nv_bfloat16* dz;                // rows [T][pitch] of planes that are `plane` apart
   int64_t plane, pitch, dz_columns; // of dz's columns dz_columns are written (zeros from M on)
   float* part;                      // dX: rows [T][M] of slices that are part_rows rows apart

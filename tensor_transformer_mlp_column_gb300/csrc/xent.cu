@@ -468,6 +468,7 @@ int64_t choose_piece(int64_t T, int64_t D, int64_t V, int planes) {
 // launches' worth (V = 128000, D = 1024, a whole step: 64 rows 0.47 against
 // 1.46 ms, 128 rows 0.86 / 1.46, 192 rows 1.23 / 1.6, 256 rows 1.61 / 1.64; V =
 // 3000, D = 256, 128 rows: 150 us against 126).
+static_assert(3 * kXentThinMax <= kXentDmaxRows, "the few-row kernel of dz finds the largest |dloss| itself");
 static bool use_thin(int64_t T, int64_t D, int64_t V, int is_bf16) {
   return T <= kXentThinMax || (!is_bf16 && T <= 3 * kXentThinMax && V * D >= (int64_t(1) << 24));
 }
@@ -601,7 +602,6 @@ cudaError_t run_xent_backward(const void* X, const void* W, const int64_t* targe
       h.lse = lse + t0;
       h.loss = loss ? loss + t0 : nullptr;
       h.dloss = dloss + t0;
-      h.dmax = dmax;
       h.rows = rows;
       h.dz = reinterpret_cast<__nv_bfloat16*>(dz[0]) + t0 * p.dz_pitch;
       h.plane = T * p.dz_pitch;

@@ -376,8 +376,7 @@ __global__ void __launch_bounds__(kTThreads, 1) thin_kernel(const __grid_constan
     if constexpr (KIND != kThinDx) {
       float dmax = 0.f;
       if constexpr (KIND == kThinGrad)
-        dmax = p.g.rows.rows ? warp_dmax_of_rows(p.g.rows, p.g.V, lane, blockIdx.x == 0 && warp == kEpiWarp0)
-                             : warp_dmax(p.g.dmax, lane);
+        dmax = warp_dmax_of_rows(p.g.rows, p.g.V, lane, blockIdx.x == 0 && warp == kEpiWarp0);
       if (et < 64) {
         const bool in = et < p.g.T;
         const int64_t t = in ? p.g.targets[et] : -1;
