@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "trace.h"
+#include "train.h"
 
 using namespace tpmlp;
 
@@ -506,6 +507,9 @@ int tpmlp_check_status(tpmlp_stream_t stream) {
         "?", "GEMM tile outside the tile grid", "TMA coordinate not 16-byte aligned", "epilogue store outside the output",
         "reduce index outside its slice", "attention tile outside the launch", "self-test index outside its array"};
     const int c = v - kSiteBoundsBase;
+    if (c == kChkTarget || c == kChkToken)
+      return fail(TPMLP_ERR_BOUNDS, "a %s id at or above V; its row was left out (check %d)",
+                  c == kChkTarget ? "target" : "token", c);
     return fail(TPMLP_ERR_BOUNDS, "a device-side check failed: %s (check %d)", c > 0 && c < kChkCount ? kNames[c] : "?",
                 c);
   }

@@ -1015,3 +1015,16 @@ def test_binding_refuses_a_wrong_loss(tp):
         with pytest.raises(ValueError):
             tp.tpmlp_xent_backward(X, W, t, lse, dloss, loss=bad)
     tp.tpmlp_check_status()
+
+
+def test_ids_out_of_range_are_named(tp):
+    X, W, t, _ = _xent_inputs(9, 64, 50, "bf16", seed=63, masked=0.0)
+    ids = t.clone()
+    ids[3] = 50
+    for call, what in ((lambda: tp.tpmlp_xent_forward(X, W, ids), "target id"), (lambda: tp.tpmlp_embed_forward(W, ids), "token id"),
+                       (lambda: tp.tpmlp_embed_backward(X, ids, 50), "token id")):
+        call()
+        with pytest.raises(tp.TpmlpError, match=what) as e:
+            tp.tpmlp_check_status()
+        assert e.value.code == tp.TPMLP_ERR_BOUNDS
+        tp.tpmlp_check_status()
