@@ -437,9 +437,11 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  *
  * Ids (tokens, targets) are int64 in device memory. A negative id marks a row
  * that does not count: its lookup is zero, its loss is zero, and it gives no
- * gradient. An id at or above V is left out in the same way and records
- * TPMLP_ERR_BOUNDS (check 8 for a target, 9 for a token) for the next
- * tpmlp_check_status(). T and V are at most 2^30, D at most 2^20.
+ * gradient. An id at or above V is left out in the same way, and
+ * tpmlp_xent_forward and both embedding calls record TPMLP_ERR_BOUNDS (check 8
+ * for a target, 9 for a token) for the next tpmlp_check_status(); the cross
+ * entropy's backward calls do not report the forward's targets again. T and V
+ * are at most 2^30, D at most 2^20.
  *
  * Ids may stand on any 8-byte boundary (targets = ids + 1) and loss, lse, dloss
  * and norm on any 4-byte one. Outputs and workspace overlap neither an input
@@ -448,9 +450,16 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
 
 /* Workspace bytes of tpmlp_xent_forward (backward = 0) or tpmlp_xent_backward
  * (backward = 1); 0 for T = 0 and on bad arguments. It grows with T * V / 16
- * bytes forward, and with T * min(V, max(8192, 2^28 / T)) * 2 bytes backward
- * (twice that for up to 64 rows; fp32: more by copies of X and W in bf16 pieces;
- * bf16 with a D off a multiple of 16: by a copy of X). */
+ * bytes forward. Backward takes
+ *   dz: T * C * 2 bytes, C = min(V, max(8192, 2^28 / T)) ids at a time (up to 64
+ *   rows twice, fp32 three times that, within the same 2^29 bytes where C is
+ *   above 8192);
+ *   fp32 partial sums: s * T * D * 4 bytes for dX where C < V, where its sums are
+ *   cut and for the few rows of a pass over W (64 rows, fp32 up to 192), and
+ *   s * C * D * 4 for dW where its sums are cut; s is up to 64 (dX of few rows: up
+ *   to 1 + 512 * SMs / D where that is more), and small where T, C and D are not.
+ * fp32 adds copies of X and W in bf16 pieces, bf16 with a D off a multiple of 16
+ * a copy of X. */
 size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype dt, int backward);
 
 /* Softmax cross entropy over the vocabulary, without keeping the logits:
@@ -464,7 +473,9 @@ size_t tpmlp_xent_workspace_bytes(int64_t T, int64_t D, int64_t V, tpmlp_dtype d
  *   workspace  at least tpmlp_xent_workspace_bytes(T, D, V, dt, 0) bytes.
  * Products, maxima and sums in fp32 in both types (fp32: the tensor cores on
  * data split into three bf16 pieces, which an infinite entry does not have: its
- * products are not numbers). Bitwise reproducible. */
+ * products are not numbers). Bitwise reproducible in calls of the same T, D and V;
+ * how long sums are cut follows the sizes, so a row's last bits can differ between
+ * calls of different T. */
 int tpmlp_xent_forward(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D, int64_t V,
                        tpmlp_dtype dt, float* loss, float* lse, void* workspace, size_t workspace_bytes,
                        tpmlp_stream_t stream);
@@ -534,7 +545,8 @@ size_t tpmlp_grad_workspace_bytes(int n);
 
 /* Global norm of n gradients: norm[0] = sqrt(sum of the squares of all their
  * elements). Squares in fp32 (a square above the fp32 range makes the norm
- * infinite), their sums in fp64, in a fixed order.
+ * infinite; elements below about 1e-19 in magnitude lose digits of theirs, and
+ * below 2.6e-23 count as zero), their sums in fp64, in a fixed order.
  *   grads   host array of n device pointers; counts, dts their element counts
  *           (0 allowed: the pointer is then not looked at) and types.
  *   norm    device fp32 [1].

@@ -8,9 +8,10 @@
 // GPU evenly. A thread squares and adds in fp32 within one chunk (two sums of
 // 32 terms) and across chunks in fp64 (one fp64 addition per 64 elements: the
 // fp64 rate is too low for more), and the CTAs' fp64 sums are added in their
-// order, so the norm is the same on every run. 64 KB of fp32 a CTA are on
-// their way at once (chunks of half that: 339 and 665 us for the two passes
-// over 2.1 GB instead of 322 and 653).
+// order, so the norm is the same on every run. A chunk is 64 KB of fp32, all of
+// which a scaling CTA has on its way at once, a squaring one as much as 34
+// registers hold (chunks of half that: 339 and 665 us for the two passes over
+// 2.1 GB instead of 322 and 653).
 #include "device.cuh"
 #include "internal.h"
 #include "train.h"

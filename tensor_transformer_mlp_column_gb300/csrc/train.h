@@ -126,8 +126,8 @@ cudaError_t launch_xent_gemm(const XentGemm& g, uint64_t wait_ns, cudaStream_t s
 // The products with W for up to kXentThinMax rows of X at a time (xent_thin.cu).
 constexpr int kXentThinMax = 64;
 // Planes of their dz of bf16 data: a single row's gradient of a target would
-// carry the rounding of its dz as a whole (2^-9), where those of many rows and
-// ids average out, and the products are bound by W either way.
+// carry the rounding of its dz as a whole (up to 2^-8), where those of many rows
+// and ids average out, and the products are bound by W either way.
 constexpr int kThinDzPlanes = 2;
 struct XentThin {
   CUtensorMap map_w;                // W: fp32, make_output_map_f32 (32 x 32 boxes); bf16, make_operand_map (K-major: 128

@@ -20,8 +20,9 @@
 //
 // fp32 data are split into three bf16 planes (24 bits in all) and every
 // product is the sum of the six plane products that are not below fp32
-// rounding, accumulated in one fp32 accumulator: six times the bf16 work,
-// where the CUDA cores would take about thirty times.
+// rounding, accumulated in fp32 (in runs over two accumulators, for few rows
+// over three by the products' size): six times the bf16 work, where the CUDA
+// cores would take about thirty times.
 #include "device.cuh"
 #include "internal.h"
 #include "tpmlp.h"
@@ -468,8 +469,8 @@ int64_t choose_piece(int64_t T, int64_t D, int64_t V, int planes) {
 // launches' worth (V = 128000, D = 1024, a whole step: 64 rows 0.47 against
 // 1.46 ms, 128 rows 0.86 / 1.46, 192 rows 1.23 / 1.6, 256 rows 1.61 / 1.64; V =
 // 3000, D = 256, 128 rows: 150 us against 126).
-static_assert(3 * kXentThinMax <= kXentDmaxRows, "the few-row kernel of dz finds the largest |dloss| itself");
 static bool use_thin(int64_t T, int64_t D, int64_t V, int is_bf16) {
+  static_assert(3 * kXentThinMax <= kXentDmaxRows, "the few-row kernel of dz finds the largest |dloss| itself");
   return T <= kXentThinMax || (!is_bf16 && T <= 3 * kXentThinMax && V * D >= (int64_t(1) << 24));
 }
 

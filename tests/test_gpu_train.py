@@ -1028,3 +1028,9 @@ def test_ids_out_of_range_are_named(tp):
             tp.tpmlp_check_status()
         assert e.value.code == tp.TPMLP_ERR_BOUNDS
         tp.tpmlp_check_status()
+
+def test_xent_backward_workspace_holds_partial_sums(tp):
+    # How many follows the SMs. Sizes at which they are the largest part: dX's of few rows, dW's of many rows and a small vocabulary.
+    ws = tp.lib().tpmlp_xent_workspace_bytes
+    assert ws(64, 4096, 2000, 1, 1) > 64 * 2000 * 4 + 2 * 64 * 4096 * 4
+    assert ws(8192, 512, 300, 1, 1) > 8192 * 300 * 2 + 2 * 300 * 512 * 4

@@ -221,3 +221,19 @@ def test_xent_stage_timeout_argument_errors(tp, kw, code):
     a = dict(X=FAKE, W=FAKE, t=FAKE, T=8, D=64, V=100, dt=1, loss=FAKE, lse=FAKE, stage=1, limit_ms=100, ws=FAKE, nb=WS)
     a.update(kw)
     assert tp.STATUS_NAMES[tp.lib().tpmlp_selftest_xent_stage_timeout(*a.values(), None)] == code, tp.tpmlp_last_error()
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("T,D,V", [(1, 64, 100), (64, 4096, 2000), (64, 8, 100000), (8192, 512, 300), (192, 1024, 64000),
+                                   (300, 4096, 5000), (34000, 16, 9000), (4096, 768, 50257), (65, 1 << 15, 300)])
+def test_xent_backward_workspace_is_within_what_the_header_says(tp, T, D, V, dt):
+    got = tp.lib().tpmlp_xent_workspace_bytes(T, D, V, dt, 1)
+    planes = 3 if dt == 0 else 2 if T <= 64 else 1
+    few = T <= (192 if dt == 0 else 64)
+    C = min(V, max(8192, 2 ** 28 // (T * planes)))
+    dz = T * C * 2 * planes
+    copies = 6 * (T + V) * (D + 64) if dt == 0 else 2 * T * (D + 64)
+    s = max(64, 1 + 512 * 152 // D) if few else 64
+    # Rows of whole 64 columns, partial sums of whole 32 rows, parts on 256 bytes.
+    assert got <= copies + dz + 64 * 2 * planes * T + s * (T + 32) * D * 4 + 64 * (C + 32) * D * 4 + 4096
+    assert got >= dz - 256 * 2 * planes * T + (T * D * 4 if few or C < V else 0)
