@@ -512,9 +512,10 @@ int tpmlp_xent_backward_saved(const void* X, const void* W, const int64_t* targe
 /* Test hook for the time limits inside the cross entropy's products: the first
  * launch of tpmlp_xent_forward's logits with one stage (1..3) of every CTA's ring
  * of operands never complete, and a wait limit of limit_ms (1..10000). Every CTA
- * gives up there, drains its copies and MMAs, frees its tensor memory and records
- * TPMLP_ERR_TIMEOUT for the next tpmlp_check_status(). loss and lse are left
- * undefined. Other arguments as for tpmlp_xent_forward, T >= 1. */
+ * that reaches it (all of them where D is at least 384) gives up there, drains its
+ * copies and MMAs, frees its tensor memory and records TPMLP_ERR_TIMEOUT for the
+ * next tpmlp_check_status(). loss and lse are left undefined. Other arguments as
+ * for tpmlp_xent_forward, T >= 1. */
 int tpmlp_selftest_xent_stage_timeout(const void* X, const void* W, const int64_t* targets, int64_t T, int64_t D,
                                       int64_t V, tpmlp_dtype dt, float* loss, float* lse, int stage, int limit_ms,
                                       void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);

@@ -1034,3 +1034,31 @@ def test_xent_backward_workspace_holds_partial_sums(tp):
     ws = tp.lib().tpmlp_xent_workspace_bytes
     assert ws(64, 4096, 2000, 1, 1) > 64 * 2000 * 4 + 2 * 64 * 4096 * 4
     assert ws(8192, 512, 300, 1, 1) > 8192 * 300 * 2 + 2 * 300 * 512 * 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,V", [(1, 64, 3000), (40, 512, 50257), (150, 1000, 20000), (300, 264, 3000), (70, 4200, 2000)])
+def test_gradients_from_the_loss_captured_replayed_and_side_by_side(tp, T, D, V, dtype):
+    X, W, t, dloss = _xent_inputs(T, D, V, dtype, seed=T + D)
+    loss, lse = tp.tpmlp_xent_forward(X, W, t)
+
+    def call(s=None):
+        return list(tp.tpmlp_xent_backward(X, W, t, lse, dloss, loss=loss, stream=s))
+
+    ref = [v.clone() for v in call()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(torch.cuda.current_stream())
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for v in out:
+            v.fill_(5.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(a):
+            graph.replay()
+        with torch.cuda.stream(b):
+            other = call(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(out, ref)) and all(torch.equal(u, v) for u, v in zip(other, ref))
+    tp.tpmlp_check_status()
