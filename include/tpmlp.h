@@ -69,7 +69,8 @@ typedef enum {
   TPMLP_ERR_UNSUPPORTED = -8,  /* e.g. bf16 with more than TPMLP_MAX_SHARDS   */
   TPMLP_ERR_DEVICE = -9,       /* current device is not sm_103 / shards handle
                                   belongs to another device                   */
-  TPMLP_ERR_BOUNDS = -10       /* a token or target id at or above V; debug build: a device-side index check failed */
+  TPMLP_ERR_BOUNDS = -10       /* a token or target id at or above V, a sequence outside its rows; debug build: a
+                                  device-side index check failed */
 } tpmlp_status;
 
 /* Largest shard count of the bf16 tensor-core path (the fp32 path has none). */
@@ -428,6 +429,113 @@ int tpmlp_attn_heads(const void* X, int64_t batch, int64_t seq, const tpmlp_attn
  * shards, mode). */
 int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_attn_shards* shards, void* Y,
                        tpmlp_mode mode, void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The attention of a training step, on queries, keys and values that the
+ * caller has (the pages have no counterpart; they stand beside the head-split
+ * attention above for callers that train it): norms and rotation of the
+ * queries and keys, softmax attention, and the gradients of both.
+ *
+ * A tensor [T, heads, head_dim] is given by its address and two strides, in
+ * elements: element (t, h, e) stands at p[t * token + h * head + e]. So q, k and
+ * v may be parts of one buffer [T, heads + 2 kv_heads, head_dim] as a projection
+ * writes it, or [heads, T, head_dim]. `strides` is a host array of (token, head)
+ * pairs, in the order of the call's tensors. Strides are positive multiples of
+ * 16 bytes (TPMLP_ERR_ALIGN; the one over a single token or head is not looked
+ * at), rows of heads may not overlap (TPMLP_ERR_ARG), and the addresses are
+ * 16-byte aligned. lse, dwq, dwk: 4 bytes, pos: 8. Outputs and workspace overlap
+ * neither an input nor one another, unless a call says so. T is at most 2^30,
+ * heads and kv_heads at most 4096.
+ * ---------------------------------------------------------------------- */
+
+/* Softmax attention, for each sequence and each query head h, which reads kv
+ * head h / (heads / kv_heads):
+ *   s_ij = scale q_i . k_j (j a token of i's sequence; causal != 0: j <= i),
+ *   lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j.
+ *   q, o      device [T, heads, head_dim], k, v device [T, kv_heads, head_dim], of
+ *             type dt; heads % kv_heads == 0 (TPMLP_ERR_DIVISIBILITY); head_dim a
+ *             multiple of 8 in 8 .. 128 (TPMLP_ERR_SHAPE).
+ *   strides   of q, k, v, o.
+ *   starts    device int32 [batch + 1]: sequence b is the tokens starts[b] ..
+ *             starts[b + 1] - 1, at most max_seq (a host value, at most T) of them,
+ *             possibly none. NULL: T = batch * max_seq tokens in equal sequences.
+ *             A sequence that is out of order, outside the T rows or longer than
+ *             max_seq is left out and recorded as TPMLP_ERR_BOUNDS (check 10) for
+ *             the next tpmlp_check_status().
+ *   scale     finite, > 0 (1 / sqrt(head_dim) is usual).
+ *   lse       device fp32 [heads, T]; tpmlp_attn_core_backward needs it.
+ * Rows of no sequence are neither read nor written, whatever they hold. A value
+ * that is not finite spreads within its own sequence only.
+ * Products, maxima and sums in fp32; bf16 rounds the probabilities (at most 1,
+ * or 2^8 while a row's maximum still grows) to bf16 as an operand, and o once. */
+int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* starts,
+                            int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
+                            int causal, tpmlp_dtype dt, void* o, float* lse, tpmlp_stream_t stream);
+
+/* Workspace bytes of tpmlp_attn_core_backward; 0 for T = 0 and on bad arguments. */
+size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt);
+
+/* Gradients of L = sum(o * do) of tpmlp_attn_core_forward for the same q, k, v,
+ * sequences, scale and mask. The probabilities p_ij = exp(s_ij - lse_i) are made
+ * again, no matrix of them is stored:
+ *   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i,
+ * dk and dv summed over the query heads of their kv head.
+ *   o, lse    as tpmlp_attn_core_forward wrote them.
+ *   do        device [T, heads, head_dim] of type dt.
+ *   dq, dk, dv  device, as q, k, v, written.
+ *   strides   of q, k, v, o, do, dq, dk, dv.
+ *   workspace at least tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim, dt) bytes.
+ * Every sum has a fixed order: bitwise reproducible. bf16 rounds p and ds to bf16
+ * as operands and each result once. */
+int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                             const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq,
+                             int heads, int kv_heads, int head_dim, float scale, int causal, tpmlp_dtype dt, void* dq,
+                             void* dk, void* dv, void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* The norm of every head of q and k, and the rotation of its pairs by their
+ * tokens' positions:
+ *   z = w * x / sqrt(mean(x^2) + eps)  (wq for q's heads, wk for k's; both NULL: z = x),
+ *   pair i of z's first `rot` elements, (z_i, z_{i + rot/2}), or (z_{2i}, z_{2i+1})
+ *   if interleaved != 0, is turned by the angle pos[axis[i]][t] * freqs[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos). The other elements of z stay.
+ *   q, yq     device [T, heads, head_dim], k, yk device [T, kv_heads, head_dim], of
+ *             type dt; head_dim a multiple of 8 in 8 .. 256, rot one in 0 ..
+ *             head_dim (TPMLP_ERR_SHAPE). yq may be q and yk may be k, with the
+ *             same strides.
+ *   strides   of q, k, yq, yk.
+ *   wq, wk    device [head_dim] of type dt, 16-byte aligned, or both NULL.
+ *   pos       device int64 [axes, T], axes in 1 .. 8; any value.
+ *   freqs     host [rot / 2], radians per position, finite (theta^(-2i / rot), or
+ *             scaled for long contexts); read during the call.
+ *   axis      host [rot / 2], below axes, or NULL: all 0; read during the call.
+ * Computed in fp32 and rounded once. An angle keeps its fraction of a turn to
+ * about 2^-53 |pos| turns, however far the position. */
+int tpmlp_qk_rope_forward(const void* q, const void* k, const int64_t* strides, const void* wq, const void* wk, float eps,
+                          const int64_t* pos, const double* freqs, const uint8_t* axis, int64_t T, int heads, int kv_heads,
+                          int head_dim, int rot, int axes, int interleaved, tpmlp_dtype dt, void* yq, void* yk,
+                          tpmlp_stream_t stream);
+
+/* Workspace bytes of tpmlp_qk_rope_backward; 0 for T = 0 and on bad arguments. */
+size_t tpmlp_qk_rope_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim);
+
+/* Gradients of L = sum(yq * dyq) + sum(yk * dyk) of tpmlp_qk_rope_forward for the
+ * same q, k, weights and positions: with n = x / sqrt(mean(x^2) + eps) and g the
+ * gradient turned back,
+ *   dw = sum over tokens and heads of g * n,
+ *   dx = (g * w - n mean(g * w * n)) / sqrt(mean(x^2) + eps)  (no norm: dx = g).
+ *   dyq, dyk  device, of type dt; dq, dk device, of type dt, written; dq may be
+ *             dyq (or q) and dk dyk (or k), with the same strides.
+ *   strides   of q, k, dyq, dyk, dq, dk.
+ *   dwq, dwk  device fp32 [head_dim], written (zero for T = 0); with wq and wk NULL not looked at.
+ *   workspace at least tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim)
+ *             bytes; with wq and wk NULL not looked at.
+ * Sums in fp32, those of many parts in fp64, in a fixed order: bitwise reproducible. */
+int tpmlp_qk_rope_backward(const void* dyq, const void* dyk, const void* q, const void* k, const int64_t* strides,
+                           const void* wq, const void* wk, float eps, const int64_t* pos, const double* freqs,
+                           const uint8_t* axis, int64_t T, int heads, int kv_heads, int head_dim, int rot, int axes,
+                           int interleaved, tpmlp_dtype dt, void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                           size_t workspace_bytes, tpmlp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The two ends of a training step around the blocks: the embedding lookup and

@@ -96,6 +96,12 @@ SIGNATURES = {
     "tpmlp_grad_workspace_bytes": (_SZ, [_I]),
     "tpmlp_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _SZ, _P]),
     "tpmlp_grad_clip": (_I, [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "tpmlp_attn_core_forward": (_I, [_P] * 5 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I, _P, _P, _P]),
+    "tpmlp_attn_core_workspace_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "tpmlp_attn_core_backward": (_I, [_P] * 8 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I] + [_P] * 4 + [_SZ, _P]),
+    "tpmlp_qk_rope_forward": (_I, [_P] * 5 + [ctypes.c_float] + [_P] * 3 + [_I64] + [_I] * 7 + [_P] * 3),
+    "tpmlp_qk_rope_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
+    "tpmlp_qk_rope_backward": (_I, [_P] * 7 + [ctypes.c_float] + [_P] * 3 + [_I64] + [_I] * 7 + [_P] * 5 + [_SZ, _P]),
     "tpmlp_trace_read": (_I, [ctypes.c_char_p, _SZ, ctypes.POINTER(_I)]),
     "tpmlp_trace_enabled": (_I, []),
     "tpmlp_build_flags": (_I, []),
@@ -777,6 +783,183 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
         _check(l.tpmlp_grad_clip(p.buffer_info()[0], c.buffer_info()[0], d.buffer_info()[0], n, float(max_norm),
                                  None if o is None else o.buffer_info()[0], np_, wp, wn, on.raw), "tpmlp_grad_clip")
     return norm
+
+
+# ------------------------------------------------- the attention of a training step
+
+
+def _heads(t: torch.Tensor, T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: array, name: str) -> int:
+    """Address of a tensor [T, heads, dim] on device `dev`; its two strides go to `strides`."""
+    if t.dtype != dtype or t.shape != (T, heads, dim):
+        raise ValueError(f"{name} must be {dtype} of shape {(T, heads, dim)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but CUDA device {dev} is current")
+    token, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    strides.append(token)
+    strides.append(head)
+    return t.data_ptr()
+
+
+def _heads_output(t: Optional[torch.Tensor], T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: array,
+                  name: str):
+    """(tensor, address) of an output [T, heads, dim], the caller's or a new one."""
+    if t is None:
+        t = torch.empty((T, heads, dim), dtype=dtype, device="cuda")
+    return t, _heads(t, T, heads, dim, dtype, dev, strides, name)
+
+
+def _qkv_shape(q: torch.Tensor, k: torch.Tensor):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, heads, head_dim] and k [T, kv_heads, head_dim]")
+    T, heads, dim = q.shape
+    return T, heads, k.shape[1], dim
+
+
+def _sequences(starts: Optional[torch.Tensor], max_seq: Optional[int], batch: Optional[int], T: int, dev: int):
+    """(address of starts or 0, batch, max_seq)."""
+    if starts is None:
+        batch = 1 if batch is None else int(batch)
+        if batch < 1 or T % batch != 0 or max_seq not in (None, T // batch):
+            raise ValueError(f"without starts the {T} tokens must be {batch} equal sequences")
+        return 0, batch, T // batch
+    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be an int32 tensor of one more element than there are sequences")
+    if batch not in (None, starts.shape[0] - 1):
+        raise ValueError("batch and starts disagree")
+    return _ptr(starts, dev, "starts"), starts.shape[0] - 1, T if max_seq is None else min(int(max_seq), T)
+
+
+def tpmlp_attn_core_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: Optional[torch.Tensor] = None,
+                            max_seq: Optional[int] = None, batch: Optional[int] = None, scale: Optional[float] = None,
+                            causal: bool = True, o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            stream=None):
+    """Softmax attention of q [T, heads, head_dim] over k, v [T, kv_heads, head_dim]: (o as q, lse [heads, T] fp32).
+
+    The T tokens are `batch` equal sequences (default 1), or those from starts[b] to starts[b + 1] - 1 (int32 on the
+    GPU), none longer than max_seq (default T). Rows of no sequence are left as they were: undefined in an o or lse
+    that the call allocates. scale is 1 / sqrt(head_dim) by default."""
+    T, heads, kv, dim = _qkv_shape(q, k)
+    dt, strides = _type(q), array("q")
+    with _On(stream) as on:
+        dev = on.dev
+        qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
+        kp, vp = (_heads(t, T, kv, dim, q.dtype, dev, strides, n) for t, n in ((k, "k"), (v, "v")))
+        sp, n, most = _sequences(starts, max_seq, batch, T, dev)
+        o, op = _heads_output(o, T, heads, dim, q.dtype, dev, strides, "o")
+        lse, lp = _output(lse, (heads, T), torch.float32, dev, "lse")
+        _check(lib().tpmlp_attn_core_forward(qp, kp, vp, strides.buffer_info()[0], sp, T, n, most, heads, kv, dim,
+                                             dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, dt, op,
+                                             lp, on.raw), "tpmlp_attn_core_forward")
+    return o, lse
+
+
+def tpmlp_attn_core_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype) -> int:
+    return int(lib().tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim,
+                                                     TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32))
+
+
+def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                             do: torch.Tensor, starts: Optional[torch.Tensor] = None, max_seq: Optional[int] = None,
+                             batch: Optional[int] = None, scale: Optional[float] = None, causal: bool = True,
+                             dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                             dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum(o * do) of tpmlp_attn_core_forward with the same arguments: (dq, dk, dv), as q, k, v. The
+    probabilities are made again from lse. Rows of no sequence are left as they were."""
+    T, heads, kv, dim = _qkv_shape(q, k)
+    dt, l, strides = _type(q), lib(), array("q")
+    with _On(stream) as on:
+        dev = on.dev
+        qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
+        kp, vp = (_heads(t, T, kv, dim, q.dtype, dev, strides, n) for t, n in ((k, "k"), (v, "v")))
+        op, gp = (_heads(t, T, heads, dim, q.dtype, dev, strides, n) for t, n in ((o, "o"), (do, "do")))
+        sp, n, most = _sequences(starts, max_seq, batch, T, dev)
+        dq, dqp = _heads_output(dq, T, heads, dim, q.dtype, dev, strides, "dq")
+        dk, dkp = _heads_output(dk, T, kv, dim, q.dtype, dev, strides, "dk")
+        dv, dvp = _heads_output(dv, T, kv, dim, q.dtype, dev, strides, "dv")
+        ws, wp, wn = _space(l.tpmlp_attn_core_workspace_bytes(T, heads, kv, dim, dt), workspace, dev)
+        _check(l.tpmlp_attn_core_backward(qp, kp, vp, op, _like(lse, (heads, T), torch.float32, dev, "lse"), gp,
+                                          strides.buffer_info()[0], sp, T, n, most, heads, kv, dim,
+                                          dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, dt, dqp, dkp,
+                                          dvp, wp, wn, on.raw), "tpmlp_attn_core_backward")
+    return dq, dk, dv
+
+
+@functools.lru_cache(maxsize=64)
+def _turns(freqs: tuple, axis: Optional[tuple], axes: int):
+    """The frequencies and their axes as host arrays."""
+    if axis is not None and (len(axis) != len(freqs) or any(a < 0 or a >= axes for a in axis)):
+        raise ValueError(f"axis must give one of {axes} axes for each of the {len(freqs)} frequencies")
+    return array("d", freqs), None if axis is None else array("B", axis)
+
+
+def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
+    """What both calls take: the shape and the arguments between the strides and the outputs."""
+    T, heads, kv, dim = _qkv_shape(q, k)
+    if pos.dtype != torch.int64 or pos.shape[-1:] != (T,) or pos.dim() > 2:
+        raise ValueError(f"pos must be an int64 tensor of {T} positions, or [axes, {T}]")
+    axes = pos.shape[0] if pos.dim() == 2 else 1
+    f, a = _turns(tuple(freqs), None if axis is None else tuple(axis), axes)
+    w = [0 if t is None else _like(t, (dim,), q.dtype, dev, n) for t, n in ((wq, "wq"), (wk, "wk"))]
+    return (T, heads, kv, dim), (*w, float(eps), _ptr(pos, dev, "pos"), f.buffer_info()[0],
+                                 None if a is None else a.buffer_info()[0], T, heads, kv, dim, 2 * len(f), axes,
+                                 1 if interleaved else 0, _type(q)), (f, a)
+
+
+def tpmlp_qk_rope_forward(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, freqs: Sequence[float],
+                          axis: Optional[Sequence[int]] = None, interleaved: bool = False,
+                          wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          yq: Optional[torch.Tensor] = None, yk: Optional[torch.Tensor] = None, stream=None):
+    """Every head of q [T, heads, head_dim] and k [T, kv_heads, head_dim] normed (root mean square) and scaled by wq or
+    wk (both None: not), then its pairs turned by pos * freqs: (yq, yk). Pair i is (i, i + len(freqs)), or
+    (2 i, 2 i + 1) when interleaved. pos is int64 [T], or [axes, T] with axis[i] naming the axis that turns pair i.
+    yq may be q and yk may be k."""
+    strides = array("q")
+    with _On(stream) as on:
+        dev = on.dev
+        (T, heads, kv, dim), args, keep = _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev)
+        qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
+        kp = _heads(k, T, kv, dim, q.dtype, dev, strides, "k")
+        yq, yqp = _heads_output(yq, T, heads, dim, q.dtype, dev, strides, "yq")
+        yk, ykp = _heads_output(yk, T, kv, dim, q.dtype, dev, strides, "yk")
+        _check(lib().tpmlp_qk_rope_forward(qp, kp, strides.buffer_info()[0], *args, yqp, ykp, on.raw),
+               "tpmlp_qk_rope_forward")
+    return yq, yk
+
+
+def tpmlp_qk_rope_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim))
+
+
+def tpmlp_qk_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor,
+                           freqs: Sequence[float], axis: Optional[Sequence[int]] = None, interleaved: bool = False,
+                           wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                           dwq: Optional[torch.Tensor] = None, dwk: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of sum(yq * dyq) + sum(yk * dyk) of tpmlp_qk_rope_forward: (dq, dk, dwq, dwk), the weights' in fp32 and
+    None without weights. dq may be dyq and dk may be dyk."""
+    l, strides = lib(), array("q")
+    with _On(stream) as on:
+        dev = on.dev
+        (T, heads, kv, dim), args, keep = _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev)
+        qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
+        kp = _heads(k, T, kv, dim, q.dtype, dev, strides, "k")
+        gq = _heads(dyq, T, heads, dim, q.dtype, dev, strides, "dyq")
+        gk = _heads(dyk, T, kv, dim, q.dtype, dev, strides, "dyk")
+        dq, dqp = _heads_output(dq, T, heads, dim, q.dtype, dev, strides, "dq")
+        dk, dkp = _heads_output(dk, T, kv, dim, q.dtype, dev, strides, "dk")
+        wqp = wkp = wp = wn = 0
+        if wq is not None:
+            dwq, wqp = _output(dwq, (dim,), torch.float32, dev, "dwq")
+            dwk, wkp = _output(dwk, (dim,), torch.float32, dev, "dwk")
+            ws, wp, wn = _space(l.tpmlp_qk_rope_workspace_bytes(T, heads, kv, dim), workspace, dev)
+        elif dwq is not None or dwk is not None:
+            raise ValueError("dwq and dwk need wq and wk")
+        _check(l.tpmlp_qk_rope_backward(gq, gk, qp, kp, strides.buffer_info()[0], *args, dqp, dkp, wqp, wkp, wp, wn, on.raw),
+               "tpmlp_qk_rope_backward")
+    return dq, dk, dwq, dwk
 
 
 def tpmlp_selftest_gemm_withheld_fill(X: torch.Tensor, shards: Shards, H: torch.Tensor, fill: int, limit_ms: int,

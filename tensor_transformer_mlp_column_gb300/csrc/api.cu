@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "trace.h"
+#include "attn_core.h"
 #include "train.h"
 
 using namespace tpmlp;
@@ -510,6 +511,8 @@ int tpmlp_check_status(tpmlp_stream_t stream) {
     if (c == kChkTarget || c == kChkToken)
       return fail(TPMLP_ERR_BOUNDS, "a %s id at or above V; its row was left out (check %d)",
                   c == kChkTarget ? "target" : "token", c);
+    if (c == kChkSequence)
+      return fail(TPMLP_ERR_BOUNDS, "a sequence outside its rows or longer than max_seq; it was left out (check %d)", c);
     return fail(TPMLP_ERR_BOUNDS, "a device-side check failed: %s (check %d)", c > 0 && c < kChkCount ? kNames[c] : "?",
                 c);
   }

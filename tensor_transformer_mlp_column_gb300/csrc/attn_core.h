@@ -1,0 +1,99 @@
+// attn_core.h — launchers of the attention on given queries, keys and values
+// and its backward pass (attn_core.cu, attn_core_tc.cu), and of the norms and
+// rotation of queries and keys (qk_rope.cu). Not part of the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace tpmlp {
+
+// What the status word holds when a sequence's start and end are not in order,
+// lie outside the T rows or are further apart than max_seq: the sequence is
+// left out, and the next tpmlp_check_status() returns TPMLP_ERR_BOUNDS.
+constexpr int kChkSequence = 10;
+
+// A tensor [T][heads][dim]: element (t, h, e) at p[t * token + h * head + e].
+struct HeadsView {
+  void* p;
+  int64_t token, head;
+};
+
+struct CoreShape {
+  const int32_t* starts;  // device [batch + 1], or null: sequence b in rows b * max_seq ..
+  int64_t T;
+  int batch, max_seq;
+  int heads, kv_heads, dim;
+  float scale;
+  int causal;
+};
+
+// A sequence's first row and length; length 0 (and a recorded failure) if the
+// starts do not describe one.
+__device__ __forceinline__ int core_sequence(const CoreShape& s, int b, int64_t& row0, int* status) {
+  if (!s.starts) {
+    row0 = int64_t(b) * s.max_seq;
+    return s.max_seq;
+  }
+  const int64_t begin = s.starts[b], end = s.starts[b + 1];
+  row0 = begin;
+  if (begin >= 0 && end >= begin && end <= s.T && end - begin <= s.max_seq) return static_cast<int>(end - begin);
+  if (threadIdx.x == 0) atomicCAS(status, 0, kSiteBoundsBase + kChkSequence);
+  return 0;
+}
+
+struct CoreForward {
+  CoreShape s;
+  HeadsView q, k, v, o;
+  float* lse;  // [heads][T]
+  int bf16;
+  uint64_t wait_ns;
+  int* status;
+};
+cudaError_t run_core_forward(const CoreForward& c, cudaStream_t stream);
+
+struct CoreBackward {
+  CoreShape s;
+  HeadsView q, k, v, o, d_o, dq, dk, dv;
+  const float* lse;
+  int bf16;
+  void* ws;
+  uint64_t wait_ns;
+  int* status;
+};
+size_t core_backward_workspace(int64_t T, int heads);
+cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t stream);
+
+// ------------------------------------------------------------------ qk_rope.cu
+
+constexpr int kRopeMaxDim = 256;
+
+// Norm (where w is given) and rotation of the heads of q and k. The first
+// `rot` elements of a head are turned in pairs: pair i by pos[axis[i]][t]
+// times turn[i] / 2^64 of a full turn.
+struct RopeShape {
+  int64_t T;
+  int heads[2], dim, rot;       // of q, of k
+  int interleaved;              // pairs (2i, 2i + 1) in the place of (i, i + rot / 2)
+  float eps;
+  const int64_t* pos;           // device [axes][T]
+  uint64_t turn[kRopeMaxDim / 2];
+  uint8_t axis[kRopeMaxDim / 2];
+};
+struct RopeCall {
+  RopeShape s;
+  int backward;
+  HeadsView x[2], y[2];         // forward: y from x; backward: y is dx, made from x and dy
+  HeadsView dy[2];
+  const void* w[2];             // [dim], or both null: no norm
+  float* dw[2];                 // [dim]
+  void* ws;
+  int bf16;
+};
+size_t rope_backward_workspace(int64_t T, int heads, int kv_heads, int dim);
+cudaError_t run_qk_rope(const RopeCall& c, cudaStream_t stream);
+
+}  // namespace tpmlp
