@@ -420,9 +420,13 @@ cudaError_t simt_forward(const CoreForward& c, cudaStream_t s) {
 template <typename T, int DH>
 cudaError_t simt_backward(const CoreBackward& c, const float* delta, cudaStream_t s) {
   const int64_t tiles = (c.s.max_seq + kTile - 1) / kTile;
-  cudaError_t e = launch(core_dkv_kernel<T, DH>, tiles * c.s.kv_heads * c.s.batch, 4 * tile_bytes<DH>() + 2 * kMatrixBytes,
-                         s, c, delta);
-  if (e != cudaSuccess) return e;
+  {
+    TraceScope trace("attn_core_dkv", s);
+    cudaError_t e = launch(core_dkv_kernel<T, DH>, tiles * c.s.kv_heads * c.s.batch,
+                           4 * tile_bytes<DH>() + 2 * kMatrixBytes, s, c, delta);
+    if (e != cudaSuccess) return e;
+  }
+  TraceScope trace("attn_core_dq", s);
   return launch(core_dq_kernel<T, DH>, tiles * c.s.heads * c.s.batch, 4 * tile_bytes<DH>() + kMatrixBytes, s, c, delta);
 }
 
@@ -432,8 +436,7 @@ size_t core_backward_workspace(int64_t T, int heads) { return static_cast<size_t
 
 cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {
   TraceScope trace("attn_core_forward", s);
-  if (c.bf16)
-    return c.s.dim <= 64 ? simt_forward<__nv_bfloat16, 64>(c, s) : simt_forward<__nv_bfloat16, 128>(c, s);
+  if (c.bf16) return launch_core_forward_tc(c, s);
   return c.s.dim <= 64 ? simt_forward<float, 64>(c, s) : simt_forward<float, 128>(c, s);
 }
 
@@ -446,9 +449,7 @@ cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
                                s, c.o, c.d_o, c.s.T, c.s.heads, c.s.dim, delta);
     if (e != cudaSuccess) return e;
   }
-  TraceScope trace("attn_core_backward", s);
-  if (c.bf16)
-    return c.s.dim <= 64 ? simt_backward<__nv_bfloat16, 64>(c, delta, s) : simt_backward<__nv_bfloat16, 128>(c, delta, s);
+  if (c.bf16) return launch_core_backward_tc(c, delta, s);
   return c.s.dim <= 64 ? simt_backward<float, 64>(c, delta, s) : simt_backward<float, 128>(c, delta, s);
 }
 

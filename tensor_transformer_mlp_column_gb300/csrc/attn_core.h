@@ -50,6 +50,7 @@ struct CoreForward {
   HeadsView q, k, v, o;
   float* lse;  // [heads][T]
   int bf16;
+  int withhold;  // test hook, bf16: > 0: that load of every CTA's keys and values is never issued
   uint64_t wait_ns;
   int* status;
 };
@@ -61,11 +62,15 @@ struct CoreBackward {
   const float* lse;
   int bf16;
   void* ws;
+  int withhold;  // test hook, bf16: > 0: that load of every CTA's first ring is never issued
   uint64_t wait_ns;
   int* status;
 };
 size_t core_backward_workspace(int64_t T, int heads);
 cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t stream);
+// The bf16 forms (attn_core_tc.cu). delta [heads][T]: the row sums of dO . O.
+cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t stream);
+cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStream_t stream);
 
 // ------------------------------------------------------------------ qk_rope.cu
 

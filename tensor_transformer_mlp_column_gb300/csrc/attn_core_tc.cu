@@ -1,0 +1,1062 @@
+// attn_core_tc.cu — attention on given queries, keys and values and its
+// backward pass on the tensor cores (bf16, head sizes up to 128; the formulas
+// stand in attn_core.cu).
+//
+// Three kernels, tiles of 128 tokens, head sizes padded to DH = 64 or 128 by
+// TMA's zero fill:
+//   forward  a CTA per NQ query tiles of one head: S = Q K^T, P = exp(S - max),
+//            O += P V, with a running maximum and sum for each row.
+//   dQ       a CTA per query tile: S = Q K^T, dP = dO V^T, dS = P (dP - delta),
+//            dQ += dS K.
+//   dK, dV   a CTA per key tile of a kv head, over the query tiles of all heads
+//            that share it: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+// Making S and dP twice costs 7 products in the place of 5, but every sum has
+// one owner: no atomics, no order that changes, no fp32 dQ in memory.
+//
+// All tiles come by TMA through a 3-D map (element, head, token) that knows any
+// strides. P and dS never leave the SM: the threads that read S from tensor
+// memory write them back there as bf16, and the next product takes them as its
+// A operand from tensor memory. A tile in shared memory serves as a K-major
+// operand (contraction over the head) and as an MN-major one (contraction over
+// its tokens) without a copy.
+//
+// A tile's last rows can belong to the next sequence. Scores there are dropped
+// by a comparison, and the rows of a tile that enters a contraction over its
+// tokens are cleared in shared memory, so that no value of another sequence, not
+// even a NaN, meets a weight of zero.
+//
+// Warps: 8 for the softmax (warp w reads tensor memory lanes 32 (w % 4) ..), one
+// issuing products, one issuing loads. Every wait is bounded; after a failure
+// copies and products in flight are waited for and tensor memory is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "attn_core.h"
+#include "device.cuh"
+#include "internal.h"
+#include "trace.h"
+
+namespace tpmlp {
+
+namespace {
+
+constexpr int kRows = 128;                   // tokens of a tile
+constexpr uint32_t kChunk = kRows * 128;     // 64 elements of its rows
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
+constexpr int kTcThreads = (kSoftWarps + 2) * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ------------------------------------------------------------------ pieces
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Box of 64 elements x 1 head x 128 tokens.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t token,
+                                              uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_addr(bar))
+      : "memory");
+}
+// A whole tile; the barrier's arrival is the caller's.
+template <int DH>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int64_t token, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < DH / 64; ++c)
+    tma_load_rows(dst + c * kChunk, map, 64 * c, head, static_cast<int32_t>(token), bar);
+}
+
+// A in tensor memory (row i in lane i, two K in each 32-bit column), B in shared memory.
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A tile as an MN-major operand: 64 elements of N a line, 8 tokens (K) a group
+// of 1024 bytes, the next 64 elements a chunk further.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(kChunk >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
+}
+
+// d = A B^T over the head's DH elements, both tiles K-major: a 128 x 128 matrix.
+template <int DH>
+__device__ __forceinline__ void product_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
+  constexpr uint32_t id = idesc_bf16_f32(128, 128);
+  const uint32_t sa = smem_addr(a), sb = smem_addr(b);
+#pragma unroll
+  for (int k = 0; k < DH / 16; ++k) {
+    const uint32_t off = (k / 4) * kChunk + (k % 4) * 32;
+    tc_mma_bf16(d, smem_desc_sw128(sa + off), smem_desc_sw128(sb + off), id, k > 0);
+  }
+}
+// d (+)= M B over 128 tokens: M a bf16 matrix in tensor memory whose columns 64 h .. of 32 bits hold half h.
+template <int DH>
+__device__ __forceinline__ void product_tokens(uint32_t d, uint32_t m, const uint8_t* b, bool accumulate, uint32_t half_columns) {
+  constexpr uint32_t id = idesc_bf16_f32(128, DH, 0, 1);
+  const uint32_t sb = smem_addr(b);
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    mma_tmem_a(d, m + (k / 4) * half_columns + (k % 4) * 8, desc_mn(sb + 2048 * k), id, accumulate || k > 0);
+}
+
+// Clears a tile's rows from `from` on; all lanes of a warp, before a product by its lane 0.
+template <int DH>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int lane) {
+  for (int i = from * 8 + lane; i < kRows * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < DH / 64; ++c) *reinterpret_cast<uint4*>(tile + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 64 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[64]) {
+  uint32_t a[32], b[32];
+  tmem_ld_32cols_issue(taddr, a);
+  tmem_ld_32cols_issue(taddr + 32, b);
+  tmem_ld_wait(a);
+  tmem_ld_wait(b);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]), v[32 + i] = __uint_as_float(b[i]);
+}
+
+// Packed pairs of fp32.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g, int site) {
+  return __all_sync(kAll, wait_bounded(bar, parity, g, site));
+}
+
+// A ring of SLOTS buffers: position n is buffer n % SLOTS in its n / SLOTS-th use.
+template <int SLOTS>
+struct Ring {
+  uint64_t *full, *empty;
+  __device__ __forceinline__ void init(uint32_t full_count = 1) const {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(full + i, full_count);
+      mbar_init(empty + i, 1);
+    }
+  }
+  __device__ __forceinline__ bool wait_full(int n, const WaitGuard& g) const {
+    return warp_wait(full + n % SLOTS, (n / SLOTS) & 1, g, kSiteMmaFull);
+  }
+  __device__ __forceinline__ bool wait_empty(int n, const WaitGuard& g) const {
+    return warp_wait(empty + n % SLOTS, ((n / SLOTS) & 1) ^ 1u, g, kSiteProducer);
+  }
+  // After a failure: the last fill of every buffer among the first n.
+  __device__ __forceinline__ void drain(int n, uint64_t limit_ns) const {
+    for (int i = n > SLOTS ? n - SLOTS : 0; i < n; ++i) wait_drain(full + i % SLOTS, (i / SLOTS) & 1, limit_ns);
+  }
+};
+
+// The first `dim` of a row's columns at `column` .. column + 31 as bf16, times f.
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[32], float f, int column, int dim) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (column + 8 * u < dim)
+      *reinterpret_cast<uint4*>(dst + column + 8 * u) =
+          make_uint4(pack_bf16(v[8 * u] * f, v[8 * u + 1] * f), pack_bf16(v[8 * u + 2] * f, v[8 * u + 3] * f),
+                     pack_bf16(v[8 * u + 4] * f, v[8 * u + 5] * f), pack_bf16(v[8 * u + 6] * f, v[8 * u + 7] * f));
+}
+
+struct TcParams {
+  CoreShape s;
+  CUtensorMap q, k, v, d_o;
+  HeadsView o, dq, dk, dv;
+  float* lse;    // forward: written; backward: read
+  float* delta;  // backward
+  float scale_log2;
+  int tiles;     // tiles (forward: runs of NQ tiles) of the longest sequence
+  int withhold;  // test hook: > 0: that load of the CTA's first ring is not issued
+  uint64_t wait_ns;
+  int* status;
+};
+
+// What a CTA works on. Items of one tile index follow one another, those with
+// the most work first.
+struct Item {
+  int tile, head, len;
+  int64_t row0;
+};
+__device__ __forceinline__ Item item_of(const TcParams& p, int heads, bool last_first) {
+  Item it;
+  const int64_t per = int64_t(heads) * p.s.batch;
+  const int64_t i = blockIdx.x;
+  it.tile = static_cast<int>(i / per);
+  if (last_first) it.tile = p.tiles - 1 - it.tile;
+  it.head = static_cast<int>(i % per % heads);
+  it.len = core_sequence(p.s, static_cast<int>(i % per / heads), it.row0, p.status);
+  return it;
+}
+
+// Shared memory of a kernel: tiles, then rows of floats, then barriers.
+constexpr size_t kSlack = 1024;
+
+// ------------------------------------------------------------------ forward
+
+template <int DH, int NQ>
+struct FwdCfg {
+  static constexpr uint32_t TILE = DH / 64 * kChunk;
+  static constexpr int SLOTS = 4;  // K_0, V_0, K_1, ..
+  static constexpr uint32_t TMEM = NQ == 2 ? 512 : 256;
+  static constexpr uint32_t O = NQ * 128;  // columns: S of each tile, then O of each
+  static constexpr size_t SMEM = kSlack + (NQ + SLOTS) * TILE + 256;
+  static constexpr int THREADS = (4 * NQ + 2) * 32;
+  static_assert(O + NQ * DH <= TMEM, "tensor memory");
+};
+
+// The row's maximum so far, raised where the tile's is above it by more than
+// 2^8 in weight: until then weights stay below 2^8 and O needs no factor.
+template <int DH, int NQ>
+__global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, 1) fwd_kernel(const __grid_constant__ TcParams p) {
+  using C = FwdCfg<DH, NQ>;
+  constexpr int kMma = 4 * NQ, kLoad = 4 * NQ + 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;
+  uint8_t* s_ring = smem + NQ * C::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ring + C::SLOTS * C::TILE);
+  const Ring<C::SLOTS> ring{bars, bars + C::SLOTS};
+  uint64_t* q_full = bars + 2 * C::SLOTS;
+  uint64_t* s_full = q_full + 1;   // [NQ] scores of a tile are there
+  uint64_t* p_full = s_full + NQ;  // [NQ] its probabilities are there, and O has the new maximum
+  uint64_t* o_done = p_full + NQ;  // [NQ]
+  uint64_t* drain = o_done + NQ;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    ring.init();
+    mbar_init(q_full, 1);
+    for (int a = 0; a < NQ; ++a) {
+      mbar_init(s_full + a, 1);
+      mbar_init(p_full + a, 4);
+      mbar_init(o_done + a, 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Item it = item_of(p, p.s.heads, p.s.causal);
+  const int q0 = it.tile * NQ * kRows;
+  if (q0 >= it.len) return;  // every thread, before tensor memory is taken
+  if (warp == kMma) tmem_alloc(tmem_slot, C::TMEM);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard guard{abort_flag, p.wait_ns, p.status};
+  const int kv = it.head / (p.s.heads / p.s.kv_heads);
+  // Key tiles of each query tile.
+  int n[NQ], n_max = 0;
+#pragma unroll
+  for (int a = 0; a < NQ; ++a) {
+    const int first = q0 + a * kRows;
+    n[a] = first >= it.len ? 0 : (p.s.causal ? min(it.len, first + kRows) + kRows - 1 : it.len + kRows - 1) / kRows;
+    n_max = max(n_max, n[a]);
+  }
+  int issued = 0;  // fills of the ring (loading warp)
+
+  if (warp == kLoad) {
+    if (lane == 0) {
+      int tiles = 0;
+      for (int a = 0; a < NQ; ++a) tiles += n[a] > 0;
+      mbar_arrive_expect_tx(q_full, tiles * C::TILE);
+      for (int a = 0; a < tiles; ++a) load_tile<DH>(s_q + a * C::TILE, &p.q, it.head, it.row0 + q0 + a * kRows, q_full);
+    }
+    for (int i = 0; i < 2 * n_max; ++i) {
+      if (!ring.wait_empty(i, guard)) break;
+      if (i + 1 == p.withhold) continue;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(ring.full + i % C::SLOTS, C::TILE);
+        load_tile<DH>(s_ring + (i % C::SLOTS) * C::TILE, i & 1 ? &p.v : &p.k, kv, it.row0 + (i >> 1) * kRows,
+                      ring.full + i % C::SLOTS);
+      }
+      issued = i + 1;
+    }
+  } else if (warp == kMma) {
+    bool ok = warp_wait(q_full, 0, guard, kSiteMmaFull) && ring.wait_full(0, guard);
+    if (ok) {
+      tc_fence_after_sync();
+      if (lane == 0) {
+#pragma unroll
+        for (int a = 0; a < NQ; ++a)
+          if (n[a] > 0) {
+            product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, s_ring);
+            tc_commit(s_full + a);
+          }
+        tc_commit(ring.empty);
+      }
+      for (int j = 0; j < n_max; ++j) {
+        const int kn = 2 * j + 2, vn = 2 * j + 1;
+        uint8_t* v_tile = s_ring + (vn % C::SLOTS) * C::TILE;
+        const uint8_t* k_next = s_ring + (kn % C::SLOTS) * C::TILE;
+        if (!ring.wait_full(vn, guard)) break;
+        if (it.len - j * kRows < kRows) clear_rows<DH>(v_tile, it.len - j * kRows, lane);
+        if (j + 1 < n_max && !ring.wait_full(kn, guard)) break;
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) {
+          if (j >= n[a]) continue;
+          ok = ok && warp_wait(p_full + a, j & 1, guard, kSiteMmaAcc);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (lane == 0) {
+            product_tokens<DH>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 32);
+            if (j + 1 == n[a]) tc_commit(o_done + a);
+            if (j + 1 < n[a]) {  // over P, whose product comes first
+              product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, k_next);
+              tc_commit(s_full + a);
+            }
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(ring.empty + vn % C::SLOTS);
+          if (j + 1 < n_max) tc_commit(ring.empty + kn % C::SLOTS);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    const int a = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + a * 128, t_o = tmem + lanes + C::O + a * DH;
+    const int first = q0 + a * kRows, tiles = n[a];
+    const int qi = first + row;
+    const float c = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      ok = warp_wait(s_full + a, j & 1, guard, kSiteMmaFull);
+      if (!ok) break;
+      tc_fence_after_sync();
+      float s[128];
+      {
+        uint32_t r[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld_32cols_issue(t_s + 32 * x, r[x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          tmem_ld_wait(r[x]);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[32 * x + e] = __uint_as_float(r[x][e]);
+        }
+      }
+      const int k0 = j * kRows;
+      if (k0 + kRows > it.len || (p.s.causal && k0 + kRows > first)) {
+        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0;  // columns that count
+#pragma unroll
+        for (int e = 0; e < 128; ++e) s[e] = e < end ? s[e] : -INFINITY;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; e += 2)
+        asm("max.f32 %0, %0, %1, %2;" : "+f"(m4[(e >> 1) & 3]) : "f"(s[e]), "f"(s[e + 1]));
+      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      const float m_new = (top - m) * c > 8.f ? top : m;  // at a row's first finite score: top
+      const float alpha = m_new == m ? 1.f : exp2_fast((m - m_new) * c);
+      const float base = m_new == -INFINITY ? 0.f : m_new * c;  // no score above -inf yet: weights of zero, not NaN
+      m = m_new;
+      if (j > 0 && __any_sync(kAll, alpha != 1.f)) {
+        // The scores' arrival came after the previous product's end: O holds still.
+#pragma unroll 1
+        for (int x = 0; x < DH; x += 32) {
+          float o[32];
+          uint32_t w[32];
+          tmem_ld_32cols(t_o + x, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
+          tmem_st_32(t_o + x, w);
+        }
+      }
+      const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float e0, e1;
+          unpair(fma_pair(pair(s[64 * x + e], s[64 * x + e + 1]), c2, b2), e0, e1);
+          e0 = exp2_fast(e0);
+          e1 = exp2_fast(e1);
+          sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], pair(e0, e1));
+          w[e / 2] = pack_bf16(e0, e1);
+        }
+        tmem_st_32(t_s + 32 * x, w);
+      }
+      float x0, x1;
+      unpair(add_pair(sum[0], sum[1]), x0, x1);
+      l = l * alpha + (x0 + x1);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + a);
+    }
+    ok = ok && tiles > 0 && warp_wait(o_done + a, 0, guard, kSiteEpilogue);
+    if (ok) {
+      tc_fence_after_sync();
+      const float inv = 1.f / l;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o.p) + (it.row0 + qi) * p.o.token + it.head * p.o.head;
+#pragma unroll 1
+      for (int x = 0; x < DH; x += 32) {
+        float o[32];
+        tmem_ld_32cols(t_o + x, o);
+        if (qi < it.len) store_row(dst, o, inv, x, p.s.dim);
+      }
+      if (qi < it.len) p.lse[int64_t(it.head) * p.s.T + it.row0 + qi] = m * p.s.scale + logf(l);
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    if (warp == kLoad && lane == 0) {
+      wait_drain(q_full, 0, p.wait_ns);
+      ring.drain(issued, p.wait_ns);
+    }
+    if (warp == kMma && lane == 0) {
+      tc_commit(drain);
+      wait_drain(drain, 0, p.wait_ns);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+
+template <int DH>
+struct DqCfg {
+  static constexpr uint32_t TILE = DH / 64 * kChunk;
+  static constexpr int KS = DH == 64 ? 4 : 3, VS = DH == 64 ? 4 : 2;
+  static constexpr uint32_t S = 0, DP = 256, DQ = 384;  // columns: S twice, dP, dQ
+  static constexpr size_t SMEM = kSlack + (2 + KS + VS) * TILE + 1024 + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// Tile j: the products of tile j + 1 run while the softmax warps work on j. dS
+// goes over the scores it came from. delta comes in as dO . O with the O that the
+// forward rounded; the row's sum of dS, zero for the exact delta, says how far it
+// is off, and is added to it for the kernel of dK. Rows with a single key tile
+// take their own sum of P dP from the start.
+template <int DH>
+__global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant__ TcParams p) {
+  using C = DqCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;
+  uint8_t* s_do = s_q + C::TILE;
+  uint8_t* s_k = s_do + C::TILE;
+  uint8_t* s_v = s_k + C::KS * C::TILE;
+  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::TILE);  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_sum + 2 * kRows);
+  const Ring<C::KS> ring_k{bars, bars + C::KS};
+  bars += 2 * C::KS;
+  const Ring<C::VS> ring_v{bars, bars + C::VS};
+  bars += 2 * C::VS;
+  uint64_t* q_full = bars;       // Q and dO
+  uint64_t* sd_full = bars + 1;  // S and dP of a tile
+  uint64_t* dp_read = bars + 2;  // dP is in registers
+  uint64_t* ds_full = bars + 3;
+  uint64_t* done = bars + 4;
+  uint64_t* drain = bars + 5;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    ring_k.init();
+    ring_v.init();
+    mbar_init(q_full, 1);
+    mbar_init(sd_full, 1);
+    mbar_init(dp_read, kSoftWarps);
+    mbar_init(ds_full, kSoftWarps);
+    mbar_init(done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Item it = item_of(p, p.s.heads, p.s.causal);
+  const int q0 = it.tile * kRows;
+  if (q0 >= it.len) return;
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard guard{abort_flag, p.wait_ns, p.status};
+  const int kv = it.head / (p.s.heads / p.s.kv_heads);
+  const int n = ((p.s.causal ? min(it.len, q0 + kRows) : it.len) + kRows - 1) / kRows;
+  int issued_k = 0, issued_v = 0;
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+      load_tile<DH>(s_q, &p.q, it.head, it.row0 + q0, q_full);
+      load_tile<DH>(s_do, &p.d_o, it.head, it.row0 + q0, q_full);
+    }
+    for (int j = 0; j < n; ++j) {
+      if (!ring_k.wait_empty(j, guard)) break;
+      if (j + 1 != p.withhold) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(ring_k.full + j % C::KS, C::TILE);
+          load_tile<DH>(s_k + (j % C::KS) * C::TILE, &p.k, kv, it.row0 + j * kRows, ring_k.full + j % C::KS);
+        }
+        issued_k = j + 1;
+      }
+      if (!ring_v.wait_empty(j, guard)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(ring_v.full + j % C::VS, C::TILE);
+        load_tile<DH>(s_v + (j % C::VS) * C::TILE, &p.v, kv, it.row0 + j * kRows, ring_v.full + j % C::VS);
+      }
+      issued_v = j + 1;
+    }
+  } else if (warp == kMmaWarp) {
+    bool ok = warp_wait(q_full, 0, guard, kSiteMmaFull);
+    for (int j = 0; ok && j <= n; ++j) {
+      if (j < n) {
+        ok = ring_k.wait_full(j, guard);
+        if (!ok) break;
+        uint8_t* k_tile = s_k + (j % C::KS) * C::TILE;
+        if (it.len - j * kRows < kRows) clear_rows<DH>(k_tile, it.len - j * kRows, lane);
+        // S_j over dS_{j-2}, whose product was issued before.
+        if (lane == 0) product_rows<DH>(tmem + C::S + (j & 1) * 128, s_q, k_tile);
+        ok = ring_v.wait_full(j, guard) && (j == 0 || warp_wait(dp_read, (j - 1) & 1, guard, kSiteMmaAcc));
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          product_rows<DH>(tmem + C::DP, s_do, s_v + (j % C::VS) * C::TILE);
+          tc_commit(sd_full);
+          tc_commit(ring_v.empty + j % C::VS);
+        }
+        __syncwarp();
+      }
+      if (j > 0) {
+        ok = warp_wait(ds_full, (j - 1) & 1, guard, kSiteMmaAcc);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          product_tokens<DH>(tmem + C::DQ, tmem + C::S + ((j - 1) & 1) * 128, s_k + ((j - 1) % C::KS) * C::TILE, j > 1, 64);
+          tc_commit(ring_k.empty + (j - 1) % C::KS);
+          if (j == n) tc_commit(done);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int qi = q0 + row;
+    const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
+    const float nl = -p.lse[at] * kLog2e;
+    float delta = p.delta[at];
+    float total = 0.f;  // of dS
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = warp_wait(sd_full, j & 1, guard, kSiteMmaFull);
+      if (!ok) {
+        if (n == 1) asm volatile("barrier.cta.sync 1, 256;" ::: "memory");  // the others may stand at it
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * 128 + 64 * half;
+      float s[64], dp[64];
+      tmem_ld_64(tmem + lanes + C::DP + 64 * half, dp);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dp_read);
+      tmem_ld_64(t_s, s);
+      const int k0 = j * kRows;
+      const uint64_t c2 = pair(p.scale_log2, p.scale_log2), n2 = pair(nl, nl);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        unpair(fma_pair(pair(s[e], s[e + 1]), c2, n2), s[e], s[e + 1]);
+        s[e] = exp2_fast(s[e]);
+        s[e + 1] = exp2_fast(s[e + 1]);
+      }
+      if (k0 + kRows > it.len || (p.s.causal && k0 + kRows > q0)) {
+        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - 64 * half;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          s[e] = e < end ? s[e] : 0.f;
+          dp[e] = e < end ? dp[e] : 0.f;
+        }
+      }
+      if (n == 1) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) sum = fmaf(s[e], dp[e], sum);
+        s_sum[half * kRows + row] = sum;
+        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+        delta = s_sum[row] + s_sum[kRows + row];
+      }
+      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+      const uint64_t d2 = pair(-delta, -delta);
+      uint32_t w[32];
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
+        sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], ds);
+        float x0, x1;
+        unpair(ds, x0, x1);
+        w[e / 2] = pack_bf16(x0, x1);
+      }
+      tmem_st_32(t_s, w);
+      float x0, x1;
+      unpair(add_pair(sum[0], sum[1]), x0, x1);
+      total += x0 + x1;
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    // All softmax warps come here alike: a failed wait ends in the same barrier.
+    if (n > 1) s_sum[half * kRows + row] = total;
+    asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+    ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
+    if (ok) {
+      tc_fence_after_sync();
+      if (half == 0 && qi < it.len) p.delta[at] = n > 1 ? delta + (s_sum[row] + s_sum[kRows + row]) : delta;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
+#pragma unroll 1
+      for (int x = half * (DH / 2); x < (half + 1) * (DH / 2); x += 32) {
+        float o[32];
+        tmem_ld_32cols(tmem + lanes + C::DQ + x, o);
+        if (qi < it.len) store_row(dst, o, p.s.scale, x, p.s.dim);
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    if (warp == kLoadWarp && lane == 0) {
+      wait_drain(q_full, 0, p.wait_ns);
+      ring_k.drain(issued_k, p.wait_ns);
+      ring_v.drain(issued_v, p.wait_ns);
+    }
+    if (warp == kMmaWarp && lane == 0) {
+      tc_commit(drain);
+      wait_drain(drain, 0, p.wait_ns);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+
+template <int DH>
+struct DkvCfg {
+  static constexpr uint32_t TILE = DH / 64 * kChunk;
+  static constexpr int QS = DH == 64 ? 4 : 2, DS = DH == 64 ? 4 : 2;
+  static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 256 + DH;
+  static constexpr size_t SMEM = kSlack + (2 + QS + DS) * TILE + QS * 1024 + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// Query tile i: P^T goes over S^T, dS^T over dP^T. The scores of tile i + 1 are
+// made while the threads work on dS of tile i, its dP while they work on P of
+// tile i + 1.
+template <int DH>
+__global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constant__ TcParams p) {
+  using C = DkvCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_k = smem;
+  uint8_t* s_v = s_k + C::TILE;
+  uint8_t* s_q = s_v + C::TILE;
+  uint8_t* s_do = s_q + C::QS * C::TILE;
+  float* s_row = reinterpret_cast<float*>(s_do + C::DS * C::TILE);  // [QS][2][128]: -lse log2(e), -delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_row + C::QS * 2 * kRows);
+  const Ring<C::QS> ring_q{bars, bars + C::QS};  // full: the tile, and the 32 lanes' rows
+  bars += 2 * C::QS;
+  const Ring<C::DS> ring_d{bars, bars + C::DS};
+  bars += 2 * C::DS;
+  uint64_t* kv_full = bars;
+  uint64_t* s_full = bars + 1;
+  uint64_t* p_full = bars + 2;
+  uint64_t* dp_full = bars + 3;
+  uint64_t* ds_full = bars + 4;
+  uint64_t* done = bars + 5;
+  uint64_t* drain = bars + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    ring_q.init(33);
+    ring_d.init();
+    mbar_init(kv_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, kSoftWarps);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, kSoftWarps);
+    mbar_init(done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const Item it = item_of(p, p.s.kv_heads, false);
+  const int k0 = it.tile * kRows;
+  if (k0 >= it.len) return;
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard guard{abort_flag, p.wait_ns, p.status};
+  const int group = p.s.heads / p.s.kv_heads;
+  // Query tiles first .. last of every head of the group; pass i is head i / per, tile first + i % per.
+  const int first = p.s.causal ? it.tile : 0;
+  const int per = (it.len + kRows - 1) / kRows - first;
+  const int n = per * group;
+  int issued_q = 0, issued_d = 0;
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+      load_tile<DH>(s_k, &p.k, it.head, it.row0 + k0, kv_full);
+      load_tile<DH>(s_v, &p.v, it.head, it.row0 + k0, kv_full);
+    }
+    for (int i = 0; i < n; ++i) {
+      const int h = it.head * group + i / per, q0 = (first + i % per) * kRows;
+      if (!ring_q.wait_empty(i, guard)) break;
+      uint64_t* full = ring_q.full + i % C::QS;
+      if (i + 1 != p.withhold) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, C::TILE);
+          load_tile<DH>(s_q + (i % C::QS) * C::TILE, &p.q, h, it.row0 + q0, full);
+        }
+        issued_q = i + 1;
+      }
+      float* rows = s_row + (i % C::QS) * 2 * kRows;
+      const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = x * 32 + lane;
+        const bool on = q0 + r < it.len;
+        rows[r] = on ? -p.lse[at + r] * kLog2e : 0.f;
+        rows[kRows + r] = on ? -p.delta[at + r] : 0.f;
+      }
+      mbar_arrive(full);
+      if (!ring_d.wait_empty(i, guard)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(ring_d.full + i % C::DS, C::TILE);
+        load_tile<DH>(s_do + (i % C::DS) * C::TILE, &p.d_o, h, it.row0 + q0, ring_d.full + i % C::DS);
+      }
+      issued_d = i + 1;
+    }
+  } else if (warp == kMmaWarp) {
+    // Tile i of a ring, its rows of the next sequence cleared.
+    auto take_q = [&](int i) {
+      if (!ring_q.wait_full(i, guard)) return false;
+      const int rows = it.len - (first + i % per) * kRows;
+      if (rows < kRows) clear_rows<DH>(s_q + (i % C::QS) * C::TILE, rows, lane);
+      return true;
+    };
+    auto take_d = [&](int i) {
+      if (!ring_d.wait_full(i, guard)) return false;
+      const int rows = it.len - (first + i % per) * kRows;
+      if (rows < kRows) clear_rows<DH>(s_do + (i % C::DS) * C::TILE, rows, lane);
+      return true;
+    };
+    bool ok = warp_wait(kv_full, 0, guard, kSiteMmaFull) && take_q(0);
+    if (ok) {
+      if (lane == 0) {
+        product_rows<DH>(tmem + C::S, s_k, s_q);
+        tc_commit(s_full);
+      }
+      __syncwarp();
+      ok = take_d(0);
+    }
+    if (ok) {
+      if (lane == 0) {
+        product_rows<DH>(tmem + C::DP, s_v, s_do);
+        tc_commit(dp_full);
+      }
+      __syncwarp();
+      for (int i = 0; i < n; ++i) {
+        const uint8_t* d_tile = s_do + (i % C::DS) * C::TILE;
+        const uint8_t* q_tile = s_q + (i % C::QS) * C::TILE;
+        ok = warp_wait(p_full, i & 1, guard, kSiteMmaAcc);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          product_tokens<DH>(tmem + C::DV, tmem + C::S, d_tile, i > 0, 64);
+          tc_commit(ring_d.empty + i % C::DS);
+        }
+        __syncwarp();
+        if (i + 1 < n) {
+          ok = take_q(i + 1);
+          if (!ok) break;
+          if (lane == 0) {
+            product_rows<DH>(tmem + C::S, s_k, s_q + ((i + 1) % C::QS) * C::TILE);
+            tc_commit(s_full);
+          }
+          __syncwarp();
+        }
+        ok = warp_wait(ds_full, i & 1, guard, kSiteMmaAcc);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          product_tokens<DH>(tmem + C::DK, tmem + C::DP, q_tile, i > 0, 64);
+          tc_commit(ring_q.empty + i % C::QS);
+          if (i + 1 == n) tc_commit(done);
+        }
+        __syncwarp();
+        if (i + 1 < n) {
+          ok = take_d(i + 1);
+          if (!ok) break;
+          if (lane == 0) {
+            product_rows<DH>(tmem + C::DP, s_v, s_do + ((i + 1) % C::DS) * C::TILE);
+            tc_commit(dp_full);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + C::S + 64 * half, t_dp = tmem + lanes + C::DP + 64 * half;
+    const int kj = k0 + row;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int q0 = (first + i % per) * kRows + 64 * half;  // of this warp's columns
+      const float* rows = s_row + (i % C::QS) * 2 * kRows + 64 * half;
+      ok = ring_q.wait_full(i, guard) && warp_wait(s_full, i & 1, guard, kSiteMmaFull);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
+      float s[64];
+      tmem_ld_64(t_s, s);
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(rows + e);
+        unpair(fma_pair(pair(s[e], s[e + 1]), c2, nl.x), s[e], s[e + 1]);
+        unpair(fma_pair(pair(s[e + 2], s[e + 3]), c2, nl.y), s[e + 2], s[e + 3]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[e + x] = exp2_fast(s[e + x]);
+      }
+      const int begin = p.s.causal ? kj - q0 : 0, end = it.len - q0;  // columns that count
+      const bool masked = end < 64 || (p.s.causal && q0 < k0 + kRows);
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) s[e] = e >= begin && e < end ? s[e] : 0.f;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
+      tmem_st_32(t_s, w);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      ok = warp_wait(dp_full, i & 1, guard, kSiteMmaFull);
+      if (!ok) break;
+      tc_fence_after_sync();
+      float dp[64];
+      tmem_ld_64(t_dp, dp);
+      if (masked) {  // what stands there may be no number
+#pragma unroll
+        for (int e = 0; e < 64; ++e) dp[e] = e >= begin && e < end ? dp[e] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + kRows + e);
+        float x0, x1, x2, x3;
+        unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), x0, x1);
+        unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), x2, x3);
+        w[e / 2] = pack_bf16(x0, x1);
+        w[e / 2 + 1] = pack_bf16(x2, x3);
+      }
+      tmem_st_32(t_dp, w);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
+    if (ok) {
+      tc_fence_after_sync();
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + (it.row0 + kj) * p.dv.token + it.head * p.dv.head;
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + (it.row0 + kj) * p.dk.token + it.head * p.dk.head;
+#pragma unroll 1
+      for (int x = half * (DH / 2); x < (half + 1) * (DH / 2); x += 32) {
+        float o[32];
+        tmem_ld_32cols(tmem + lanes + C::DV + x, o);
+        if (kj < it.len) store_row(dv, o, 1.f, x, p.s.dim);
+        tmem_ld_32cols(tmem + lanes + C::DK + x, o);
+        if (kj < it.len) store_row(dk, o, p.s.scale, x, p.s.dim);
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    if (warp == kLoadWarp && lane == 0) {
+      wait_drain(kv_full, 0, p.wait_ns);
+      ring_q.drain(issued_q, p.wait_ns);
+      ring_d.drain(issued_d, p.wait_ns);
+    }
+    if (warp == kMmaWarp && lane == 0) {
+      tc_commit(drain);
+      wait_drain(drain, 0, p.wait_ns);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+bool heads_map(CUtensorMap* map, const HeadsView& v, int64_t T, int heads, int dim) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(v.head * 2), static_cast<cuuint64_t>(v.token * 2)};
+  const cuuint32_t box[3] = {64, 1, kRows};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <typename C>
+cudaError_t params_of(const C& c, TcParams* p) {
+  memset(p, 0, sizeof(*p));
+  p->s = c.s;
+  p->o = c.o;
+  p->lse = const_cast<float*>(c.lse);
+  p->scale_log2 = c.s.scale * kLog2e;
+  p->withhold = c.withhold;
+  p->wait_ns = c.wait_ns;
+  p->status = c.status;
+  return heads_map(&p->q, c.q, c.s.T, c.s.heads, c.s.dim) && heads_map(&p->k, c.k, c.s.T, c.s.kv_heads, c.s.dim) &&
+                 heads_map(&p->v, c.v, c.s.T, c.s.kv_heads, c.s.dim)
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <typename K>
+cudaError_t launch(K kernel, TcParams& p, int rows, int heads, int threads, size_t smem, cudaStream_t s) {
+  p.tiles = (p.s.max_seq + rows - 1) / rows;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t items = int64_t(p.tiles) * heads * p.s.batch;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(threads), smem, s, p);
+}
+
+template <int DH, int NQ>
+cudaError_t launch_fwd(TcParams& p, cudaStream_t s) {
+  using C = FwdCfg<DH, NQ>;
+  return launch(fwd_kernel<DH, NQ>, p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, s);
+}
+
+}  // namespace
+
+cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t s) {
+  TcParams p;
+  cudaError_t e = params_of(c, &p);
+  if (e != cudaSuccess) return e;
+  return c.s.dim <= 64 ? launch_fwd<64, 2>(p, s) : launch_fwd<128, 2>(p, s);
+}
+
+cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStream_t s) {
+  TcParams p;
+  cudaError_t e = params_of(c, &p);
+  if (e != cudaSuccess) return e;
+  if (!heads_map(&p.d_o, c.d_o, c.s.T, c.s.heads, c.s.dim)) return cudaErrorInvalidValue;
+  p.dq = c.dq;
+  p.dk = c.dk;
+  p.dv = c.dv;
+  p.delta = delta;
+  const bool small = c.s.dim <= 64;
+  {
+    TraceScope trace("attn_core_dq", s);
+    e = small ? launch(dq_kernel<64>, p, kRows, c.s.heads, kTcThreads, DqCfg<64>::SMEM, s)
+              : launch(dq_kernel<128>, p, kRows, c.s.heads, kTcThreads, DqCfg<128>::SMEM, s);
+  }
+  if (e != cudaSuccess) return e;
+  TraceScope trace("attn_core_dkv", s);
+  return small ? launch(dkv_kernel<64>, p, kRows, c.s.kv_heads, kTcThreads, DkvCfg<64>::SMEM, s)
+               : launch(dkv_kernel<128>, p, kRows, c.s.kv_heads, kTcThreads, DkvCfg<128>::SMEM, s);
+}
+
+}  // namespace tpmlp
