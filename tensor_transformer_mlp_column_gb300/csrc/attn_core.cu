@@ -31,32 +31,22 @@ constexpr int kThreads = 256;
 constexpr int kPitchP = kTile + 4;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 __device__ __forceinline__ float at(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <typename T>
-__device__ __forceinline__ T* row_of(const HeadsView& v, int64_t row, int head) {
-  return static_cast<T*>(v.p) + row * v.token + head * v.head;
+__device__ __forceinline__ float* row_of(const HeadsView& v, int64_t row, int head) {
+  return static_cast<float*>(v.p) + row * v.token + head * v.head;
 }
 
 // Rows first .. first + 63 of a sequence's tile, zero from row `len` on and from column `dim` on.
-template <typename T, int DH>
+template <int DH>
 __device__ __forceinline__ void load_tile(float* dst, const HeadsView& v, int64_t row0, int first, int len, int head,
                                           int dim) {
   for (int i = threadIdx.x; i < kTile * (DH / 4); i += kThreads) {
     const int r = i / (DH / 4), c = i % (DH / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (first + r < len && c < dim) x = load4(row_of<T>(v, row0 + first + r, head) + c);
+    if (first + r < len && c < dim) x = load4(row_of(v, row0 + first + r, head) + c);
     *reinterpret_cast<float4*>(dst + r * (DH + 4) + c) = x;
   }
 }
@@ -138,13 +128,13 @@ __device__ __forceinline__ void clear(float4 (&acc)[4][DH / 64]) {
 }
 
 // Rows 4 ty .. of the accumulators, times a factor for each.
-template <typename T, int DH>
+template <int DH>
 __device__ __forceinline__ void store_rows(const HeadsView& v, int64_t row0, int first, int len, int head, int dim,
                                            const float4 (&acc)[4][DH / 64], const float (&f)[4], int ty, int tx) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (first + 4 * ty + i >= len) continue;
-    T* dst = row_of<T>(v, row0 + first + 4 * ty + i, head);
+    float* dst = row_of(v, row0 + first + 4 * ty + i, head);
 #pragma unroll
     for (int u = 0; u < DH / 64; ++u)
       if (4 * tx + 64 * u < dim)
@@ -180,7 +170,7 @@ __device__ __forceinline__ void item_of(int64_t i, int tiles, int heads, bool la
   b = static_cast<int>(i % per / heads);
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kThreads) core_forward_kernel(const __grid_constant__ CoreForward c) {
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
@@ -197,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) core_forward_kernel(const __grid_con
   if (q0 >= len) return;
   const int kv = h / (c.s.heads / c.s.kv_heads);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, DH>(sq, c.q, row0, q0, len, h, c.s.dim);
+  load_tile<DH>(sq, c.q, row0, q0, len, h, c.s.dim);
   float m[4], l[4];
   float4 acc[4][DH / 64];
   clear<DH>(acc);
@@ -206,8 +196,8 @@ __global__ void __launch_bounds__(kThreads) core_forward_kernel(const __grid_con
   const int k_end = c.s.causal ? min(len, q0 + kTile) : len;
   for (int k0 = 0; k0 < k_end; k0 += kTile) {
     __syncthreads();
-    load_tile<T, DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
-    load_tile<T, DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
+    load_tile<DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
+    load_tile<DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
     __syncthreads();
     float s[4][4];
     dot_tiles<DH>(s, sq, sk, ty, tx);
@@ -251,11 +241,10 @@ __global__ void __launch_bounds__(kThreads) core_forward_kernel(const __grid_con
     const int qi = q0 + 4 * ty + i;
     if (tx == 0 && qi < len) c.lse[int64_t(h) * c.s.T + row0 + qi] = m[i] + logf(l[i]);
   }
-  store_rows<T, DH>(c.o, row0, q0, len, h, c.s.dim, acc, f, ty, tx);
+  store_rows<DH>(c.o, row0, q0, len, h, c.s.dim, acc, f, ty, tx);
 }
 
 // delta[h][t] = sum over the head of dO * O: eight lanes a row of a head.
-template <typename T>
 __global__ void __launch_bounds__(256) core_delta_kernel(HeadsView o, HeadsView d_o, int64_t T_, int heads, int dim,
                                                          float* delta) {
   pdl_wait();
@@ -264,8 +253,8 @@ __global__ void __launch_bounds__(256) core_delta_kernel(HeadsView o, HeadsView 
   if (i >= T_ * heads) return;  // all eight lanes of a row at once, and the shuffles name only them
   const int lane = threadIdx.x & 7, h = static_cast<int>(i % heads);
   const int64_t t = i / heads;
-  const T* a = row_of<T>(o, t, h);
-  const T* b = row_of<T>(d_o, t, h);
+  const float* a = row_of(o, t, h);
+  const float* b = row_of(d_o, t, h);
   float sum = 0.f;
   for (int c = 4 * lane; c < dim; c += 32) {
     const float4 x = load4(a + c), y = load4(b + c);
@@ -296,7 +285,7 @@ __device__ __forceinline__ void probabilities(const CoreShape& c, float (&s)[4][
   }
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kThreads) core_dkv_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   extern __shared__ __align__(16) float smem[];
   float* sk = smem;
@@ -315,16 +304,16 @@ __global__ void __launch_bounds__(kThreads) core_dkv_kernel(const __grid_constan
   if (k0 >= len) return;
   const int group = c.s.heads / c.s.kv_heads;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
-  load_tile<T, DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
+  load_tile<DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
+  load_tile<DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
   float4 dk[4][DH / 64], dv[4][DH / 64];
   clear<DH>(dk);
   clear<DH>(dv);
   for (int h = kv * group; h < (kv + 1) * group; ++h) {
     for (int q0 = c.s.causal ? k0 : 0; q0 < len; q0 += kTile) {
       __syncthreads();
-      load_tile<T, DH>(sq, c.q, row0, q0, len, h, c.s.dim);
-      load_tile<T, DH>(sd, c.d_o, row0, q0, len, h, c.s.dim);
+      load_tile<DH>(sq, c.q, row0, q0, len, h, c.s.dim);
+      load_tile<DH>(sd, c.d_o, row0, q0, len, h, c.s.dim);
       float lse[4], del[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -350,11 +339,11 @@ __global__ void __launch_bounds__(kThreads) core_dkv_kernel(const __grid_constan
     }
   }
   const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
-  store_rows<T, DH>(c.dv, row0, k0, len, kv, c.s.dim, dv, one, ty, tx);
-  store_rows<T, DH>(c.dk, row0, k0, len, kv, c.s.dim, dk, sc, ty, tx);
+  store_rows<DH>(c.dv, row0, k0, len, kv, c.s.dim, dv, one, ty, tx);
+  store_rows<DH>(c.dk, row0, k0, len, kv, c.s.dim, dk, sc, ty, tx);
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kThreads) core_dq_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
@@ -372,8 +361,8 @@ __global__ void __launch_bounds__(kThreads) core_dq_kernel(const __grid_constant
   if (q0 >= len) return;
   const int kv = h / (c.s.heads / c.s.kv_heads);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, DH>(sq, c.q, row0, q0, len, h, c.s.dim);
-  load_tile<T, DH>(sd, c.d_o, row0, q0, len, h, c.s.dim);
+  load_tile<DH>(sq, c.q, row0, q0, len, h, c.s.dim);
+  load_tile<DH>(sd, c.d_o, row0, q0, len, h, c.s.dim);
   float lse[4], del[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -386,8 +375,8 @@ __global__ void __launch_bounds__(kThreads) core_dq_kernel(const __grid_constant
   const int k_end = c.s.causal ? min(len, q0 + kTile) : len;
   for (int k0 = 0; k0 < k_end; k0 += kTile) {
     __syncthreads();
-    load_tile<T, DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
-    load_tile<T, DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
+    load_tile<DH>(sk, c.k, row0, k0, len, kv, c.s.dim);
+    load_tile<DH>(sv, c.v, row0, k0, len, kv, c.s.dim);
     __syncthreads();
     float s[4][4], dp[4][4], ds[4][4];
     dot_tiles<DH>(s, sq, sk, ty, tx);
@@ -401,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) core_dq_kernel(const __grid_constant
     add_rows<DH>(dq, ss, sk, ty, tx);
   }
   const float sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
-  store_rows<T, DH>(c.dq, row0, q0, len, h, c.s.dim, dq, sc, ty, tx);
+  store_rows<DH>(c.dq, row0, q0, len, h, c.s.dim, dq, sc, ty, tx);
 }
 
 template <typename K, typename... Args>
@@ -411,23 +400,23 @@ cudaError_t launch(K kernel, int64_t items, size_t smem, cudaStream_t s, Args...
   return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kThreads), smem, s, args...);
 }
 
-template <typename T, int DH>
+template <int DH>
 cudaError_t simt_forward(const CoreForward& c, cudaStream_t s) {
   const int64_t tiles = (c.s.max_seq + kTile - 1) / kTile;
-  return launch(core_forward_kernel<T, DH>, tiles * c.s.heads * c.s.batch, 3 * tile_bytes<DH>() + kMatrixBytes, s, c);
+  return launch(core_forward_kernel<DH>, tiles * c.s.heads * c.s.batch, 3 * tile_bytes<DH>() + kMatrixBytes, s, c);
 }
 
-template <typename T, int DH>
+template <int DH>
 cudaError_t simt_backward(const CoreBackward& c, const float* delta, cudaStream_t s) {
   const int64_t tiles = (c.s.max_seq + kTile - 1) / kTile;
   {
     TraceScope trace("attn_core_dkv", s);
-    cudaError_t e = launch(core_dkv_kernel<T, DH>, tiles * c.s.kv_heads * c.s.batch,
+    cudaError_t e = launch(core_dkv_kernel<DH>, tiles * c.s.kv_heads * c.s.batch,
                            4 * tile_bytes<DH>() + 2 * kMatrixBytes, s, c, delta);
     if (e != cudaSuccess) return e;
   }
   TraceScope trace("attn_core_dq", s);
-  return launch(core_dq_kernel<T, DH>, tiles * c.s.heads * c.s.batch, 4 * tile_bytes<DH>() + kMatrixBytes, s, c, delta);
+  return launch(core_dq_kernel<DH>, tiles * c.s.heads * c.s.batch, 4 * tile_bytes<DH>() + kMatrixBytes, s, c, delta);
 }
 
 }  // namespace
@@ -437,20 +426,19 @@ size_t core_backward_workspace(int64_t T, int heads) { return static_cast<size_t
 cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {
   TraceScope trace("attn_core_forward", s);
   if (c.bf16) return launch_core_forward_tc(c, s);
-  return c.s.dim <= 64 ? simt_forward<float, 64>(c, s) : simt_forward<float, 128>(c, s);
+  return c.s.dim <= 64 ? simt_forward<64>(c, s) : simt_forward<128>(c, s);
 }
 
 cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
   float* delta = static_cast<float*>(c.ws);
+  if (c.bf16) return launch_core_backward_tc(c, delta, s);
   {
     TraceScope trace("attn_core_delta", s);
     const unsigned grid = static_cast<unsigned>((c.s.T * c.s.heads + 31) / 32);
-    cudaError_t e = launch_pdl(c.bf16 ? core_delta_kernel<__nv_bfloat16> : core_delta_kernel<float>, dim3(grid), dim3(256), 0,
-                               s, c.o, c.d_o, c.s.T, c.s.heads, c.s.dim, delta);
+    cudaError_t e = launch_pdl(core_delta_kernel, dim3(grid), dim3(256), 0, s, c.o, c.d_o, c.s.T, c.s.heads, c.s.dim, delta);
     if (e != cudaSuccess) return e;
   }
-  if (c.bf16) return launch_core_backward_tc(c, delta, s);
-  return c.s.dim <= 64 ? simt_backward<float, 64>(c, delta, s) : simt_backward<float, 128>(c, delta, s);
+  return c.s.dim <= 64 ? simt_backward<64>(c, delta, s) : simt_backward<128>(c, delta, s);
 }
 
 }  // namespace tpmlp

@@ -47,6 +47,8 @@ constexpr uint32_t kChunk = kRows * 128;     // 64 elements of its rows
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 constexpr int kTcThreads = (kSoftWarps + 2) * 32;
+constexpr int kRowWarp = kSoftWarps + 2;  // dK, dV: lse and delta of the queries
+constexpr int kDkvThreads = (kSoftWarps + 3) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -62,7 +64,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Box of 64 elements x 1 head x 128 tokens.
+// Box of 64 elements x 1 head x 64 tokens.
 __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t token,
                                               uint64_t* bar) {
   asm volatile(
@@ -71,12 +73,14 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_addr(bar))
       : "memory");
 }
-// A whole tile; the barrier's arrival is the caller's.
-template <int DH>
+// A tile of ROWS tokens, 64 elements of all of them after another; the barrier's arrival is the caller's.
+template <int DH, int ROWS = kRows>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int64_t token, uint64_t* bar) {
 #pragma unroll
   for (int c = 0; c < DH / 64; ++c)
-    tma_load_rows(dst + c * kChunk, map, 64 * c, head, static_cast<int32_t>(token), bar);
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 64)
+      tma_load_rows(dst + (c * ROWS + r) * 128, map, 64 * c, head, static_cast<int32_t>(token) + r, bar);
 }
 
 // A in tensor memory (row i in lane i, two K in each 32-bit column), B in shared memory.
@@ -90,39 +94,40 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_de
 }
 
 // A tile as an MN-major operand: 64 elements of N a line, 8 tokens (K) a group
-// of 1024 bytes, the next 64 elements a chunk further.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-  return (static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(kChunk >> 4) << 16) |
+// of 1024 bytes, the next 64 elements `chunk` bytes further.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
+  return (static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4)) | (static_cast<uint64_t>(chunk >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
 }
 
-// d = A B^T over the head's DH elements, both tiles K-major: a 128 x 128 matrix.
-template <int DH>
+// d = A B^T over the head's DH elements, both tiles K-major, A of 128 tokens, B of W: a 128 x W matrix.
+template <int DH, int W = kRows>
 __device__ __forceinline__ void product_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
-  constexpr uint32_t id = idesc_bf16_f32(128, 128);
+  constexpr uint32_t id = idesc_bf16_f32(128, W);
   const uint32_t sa = smem_addr(a), sb = smem_addr(b);
 #pragma unroll
-  for (int k = 0; k < DH / 16; ++k) {
-    const uint32_t off = (k / 4) * kChunk + (k % 4) * 32;
-    tc_mma_bf16(d, smem_desc_sw128(sa + off), smem_desc_sw128(sb + off), id, k > 0);
-  }
+  for (int k = 0; k < DH / 16; ++k)
+    tc_mma_bf16(d, smem_desc_sw128(sa + (k / 4) * kChunk + (k % 4) * 32),
+                smem_desc_sw128(sb + (k / 4) * (W * 128) + (k % 4) * 32), id, k > 0);
 }
-// d (+)= M B over 128 tokens: M a bf16 matrix in tensor memory whose columns 64 h .. of 32 bits hold half h.
-template <int DH>
-__device__ __forceinline__ void product_tokens(uint32_t d, uint32_t m, const uint8_t* b, bool accumulate, uint32_t half_columns) {
+// d (+)= M B over W tokens: M a 128 x W bf16 matrix in tensor memory, its columns in runs of RUN (of 16 bits) that
+// begin `step` columns (of 32 bits) apart.
+template <int DH, int W, int RUN>
+__device__ __forceinline__ void product_tokens(uint32_t d, uint32_t m, const uint8_t* b, bool accumulate, uint32_t step) {
   constexpr uint32_t id = idesc_bf16_f32(128, DH, 0, 1);
   const uint32_t sb = smem_addr(b);
 #pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
-    mma_tmem_a(d, m + (k / 4) * half_columns + (k % 4) * 8, desc_mn(sb + 2048 * k), id, accumulate || k > 0);
+  for (int k = 0; k < W / 16; ++k)
+    mma_tmem_a(d, m + (k / (RUN / 16)) * step + (k % (RUN / 16)) * 8, desc_mn(sb + 2048 * k, W * 128), id,
+               accumulate || k > 0);
 }
 
 // Clears a tile's rows from `from` on; all lanes of a warp, before a product by its lane 0.
-template <int DH>
+template <int DH, int ROWS = kRows>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int lane) {
-  for (int i = from * 8 + lane; i < kRows * 8; i += 32)
+  for (int i = from * 8 + lane; i < ROWS * 8; i += 32)
 #pragma unroll
-    for (int c = 0; c < DH / 64; ++c) *reinterpret_cast<uint4*>(tile + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < DH / 64; ++c) *reinterpret_cast<uint4*>(tile + c * ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
 }
@@ -140,15 +145,28 @@ __device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&v)[3
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 64 columns of this warp's lanes.
-__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[64]) {
-  uint32_t a[32], b[32];
-  tmem_ld_32cols_issue(taddr, a);
-  tmem_ld_32cols_issue(taddr + 32, b);
-  tmem_ld_wait(a);
-  tmem_ld_wait(b);
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[32]) { tmem_st_32(taddr, v); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st_16(taddr, v); }
+
+// N = 32 or 64 columns of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  uint32_t r[N / 32][32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]), v[32 + i] = __uint_as_float(b[i]);
+  for (int x = 0; x < N / 32; ++x) tmem_ld_32cols_issue(taddr + 32 * x, r[x]);
+#pragma unroll
+  for (int x = 0; x < N / 32; ++x) {
+    tmem_ld_wait(r[x]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[32 * x + i] = __uint_as_float(r[x][i]);
+  }
 }
 
 // Packed pairs of fp32.
@@ -184,10 +202,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 template <int SLOTS>
 struct Ring {
   uint64_t *full, *empty;
-  __device__ __forceinline__ void init(uint32_t full_count = 1) const {
+  __device__ __forceinline__ void init(uint32_t full_count = 1, uint32_t empty_count = 1) const {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(full + i, full_count);
-      mbar_init(empty + i, 1);
+      mbar_init(empty + i, empty_count);
     }
   }
   __device__ __forceinline__ bool wait_full(int n, const WaitGuard& g) const {
@@ -201,6 +219,17 @@ struct Ring {
     for (int i = n > SLOTS ? n - SLOTS : 0; i < n; ++i) wait_drain(full + i % SLOTS, (i / SLOTS) & 1, limit_ns);
   }
 };
+
+// sum + the products of eight bf16 pairs.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float sum) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+    sum = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), sum);
+  }
+  return sum;
+}
 
 // The first `dim` of a row's columns at `column` .. column + 31 as bf16, times f.
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[32], float f, int column, int dim) {
@@ -242,8 +271,13 @@ __device__ __forceinline__ Item item_of(const TcParams& p, int heads, bool last_
   return it;
 }
 
-// Shared memory of a kernel: tiles, then rows of floats, then barriers.
-constexpr size_t kSlack = 1024;
+// Shared memory of a kernel: tiles, then rows of floats, then barriers. There is no slack to align it in: the dynamic
+// shared memory begins on a multiple of 1024 bytes, which the swizzled tiles need, and which is checked.
+__device__ __forceinline__ bool misaligned(const uint8_t* smem, int* status) {
+  if (!(smem_addr(smem) & 1023u)) return false;
+  if (threadIdx.x == 0) atomicCAS(status, 0, kSiteSmemAlign);
+  return true;
+}
 
 // ------------------------------------------------------------------ forward
 
@@ -252,8 +286,9 @@ struct FwdCfg {
   static constexpr uint32_t TILE = DH / 64 * kChunk;
   static constexpr int SLOTS = 4;  // K_0, V_0, K_1, ..
   static constexpr uint32_t TMEM = NQ == 2 ? 512 : 256;
+  static constexpr int CTAS = NQ == 1 && DH == 64 ? 2 : 1;  // an SM's
   static constexpr uint32_t O = NQ * 128;  // columns: S of each tile, then O of each
-  static constexpr size_t SMEM = kSlack + (NQ + SLOTS) * TILE + 256;
+  static constexpr size_t SMEM = (NQ + SLOTS) * TILE + 256;
   static constexpr int THREADS = (4 * NQ + 2) * 32;
   static_assert(O + NQ * DH <= TMEM, "tensor memory");
 };
@@ -261,11 +296,11 @@ struct FwdCfg {
 // The row's maximum so far, raised where the tile's is above it by more than
 // 2^8 in weight: until then weights stay below 2^8 and O needs no factor.
 template <int DH, int NQ>
-__global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, 1) fwd_kernel(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS) fwd_kernel(const __grid_constant__ TcParams p) {
   using C = FwdCfg<DH, NQ>;
   constexpr int kMma = 4 * NQ, kLoad = 4 * NQ + 1;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (misaligned(smem, p.status)) return;
   uint8_t* s_q = smem;
   uint8_t* s_ring = smem + NQ * C::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ring + C::SLOTS * C::TILE);
@@ -357,7 +392,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, 1) fwd_kernel(const _
           if (!ok) break;
           tc_fence_after_sync();
           if (lane == 0) {
-            product_tokens<DH>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 32);
+            product_tokens<DH, kRows, kRows>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 0);
             if (j + 1 == n[a]) tc_commit(o_done + a);
             if (j + 1 < n[a]) {  // over P, whose product comes first
               product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, k_next);
@@ -484,13 +519,15 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, 1) fwd_kernel(const _
 
 // ------------------------------------------------------------------ dQ
 
-template <int DH>
+template <int DH, int W>
 struct DqCfg {
-  static constexpr uint32_t TILE = DH / 64 * kChunk;
-  static constexpr int KS = DH == 64 ? 4 : 3, VS = DH == 64 ? 4 : 2;
-  static constexpr uint32_t S = 0, DP = 256, DQ = 384;  // columns: S twice, dP, dQ
-  static constexpr size_t SMEM = kSlack + (2 + KS + VS) * TILE + 1024 + 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TILE = DH / 64 * kChunk, NARROW = DH / 64 * W * 128;  // of the queries, of the keys
+  static constexpr int KS = DH == 64 ? 4 : 3, VS = DH == 64 ? 3 : 2;
+  static constexpr uint32_t S = 0, DP = 2 * W, DQ = 3 * W;  // columns: S twice, dP, dQ
+  static constexpr uint32_t TMEM = 3 * W + DH <= 256 ? 256 : 512;
+  static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
+  static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + 1024 + 256;
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Tile j: the products of tile j + 1 run while the softmax warps work on j. dS
@@ -498,16 +535,17 @@ struct DqCfg {
 // forward rounded; the row's sum of dS, zero for the exact delta, says how far it
 // is off, and is added to it for the kernel of dK. Rows with a single key tile
 // take their own sum of P dP from the start.
-template <int DH>
-__global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant__ TcParams p) {
-  using C = DqCfg<DH>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+template <int DH, int W>
+__global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
+  using C = DqCfg<DH, W>;
+  constexpr int H = W / 2;  // columns of a thread
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (misaligned(smem, p.status)) return;
   uint8_t* s_q = smem;
   uint8_t* s_do = s_q + C::TILE;
   uint8_t* s_k = s_do + C::TILE;
-  uint8_t* s_v = s_k + C::KS * C::TILE;
-  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::TILE);  // [2][128]
+  uint8_t* s_v = s_k + C::KS * C::NARROW;
+  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::NARROW);  // [2][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_sum + 2 * kRows);
   const Ring<C::KS> ring_k{bars, bars + C::KS};
   bars += 2 * C::KS;
@@ -540,14 +578,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
   const Item it = item_of(p, p.s.heads, p.s.causal);
   const int q0 = it.tile * kRows;
   if (q0 >= it.len) return;
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::TMEM);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int kv = it.head / (p.s.heads / p.s.kv_heads);
-  const int n = ((p.s.causal ? min(it.len, q0 + kRows) : it.len) + kRows - 1) / kRows;
+  const int n = ((p.s.causal ? min(it.len, q0 + kRows) : it.len) + W - 1) / W;
   int issued_k = 0, issued_v = 0;
 
   if (warp == kLoadWarp) {
@@ -560,15 +598,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
       if (!ring_k.wait_empty(j, guard)) break;
       if (j + 1 != p.withhold) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(ring_k.full + j % C::KS, C::TILE);
-          load_tile<DH>(s_k + (j % C::KS) * C::TILE, &p.k, kv, it.row0 + j * kRows, ring_k.full + j % C::KS);
+          mbar_arrive_expect_tx(ring_k.full + j % C::KS, C::NARROW);
+          load_tile<DH, W>(s_k + (j % C::KS) * C::NARROW, &p.k, kv, it.row0 + j * W, ring_k.full + j % C::KS);
         }
         issued_k = j + 1;
       }
       if (!ring_v.wait_empty(j, guard)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(ring_v.full + j % C::VS, C::TILE);
-        load_tile<DH>(s_v + (j % C::VS) * C::TILE, &p.v, kv, it.row0 + j * kRows, ring_v.full + j % C::VS);
+        mbar_arrive_expect_tx(ring_v.full + j % C::VS, C::NARROW);
+        load_tile<DH, W>(s_v + (j % C::VS) * C::NARROW, &p.v, kv, it.row0 + j * W, ring_v.full + j % C::VS);
       }
       issued_v = j + 1;
     }
@@ -578,15 +616,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
       if (j < n) {
         ok = ring_k.wait_full(j, guard);
         if (!ok) break;
-        uint8_t* k_tile = s_k + (j % C::KS) * C::TILE;
-        if (it.len - j * kRows < kRows) clear_rows<DH>(k_tile, it.len - j * kRows, lane);
+        uint8_t* k_tile = s_k + (j % C::KS) * C::NARROW;
+        if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
         // S_j over dS_{j-2}, whose product was issued before.
-        if (lane == 0) product_rows<DH>(tmem + C::S + (j & 1) * 128, s_q, k_tile);
+        if (lane == 0) product_rows<DH, W>(tmem + C::S + (j & 1) * W, s_q, k_tile);
         ok = ring_v.wait_full(j, guard) && (j == 0 || warp_wait(dp_read, (j - 1) & 1, guard, kSiteMmaAcc));
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          product_rows<DH>(tmem + C::DP, s_do, s_v + (j % C::VS) * C::TILE);
+          product_rows<DH, W>(tmem + C::DP, s_do, s_v + (j % C::VS) * C::NARROW);
           tc_commit(sd_full);
           tc_commit(ring_v.empty + j % C::VS);
         }
@@ -597,7 +635,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          product_tokens<DH>(tmem + C::DQ, tmem + C::S + ((j - 1) & 1) * 128, s_k + ((j - 1) % C::KS) * C::TILE, j > 1, 64);
+          product_tokens<DH, W, H>(tmem + C::DQ, tmem + C::S + ((j - 1) & 1) * W, s_k + ((j - 1) % C::KS) * C::NARROW, j > 1, H);
           tc_commit(ring_k.empty + (j - 1) % C::KS);
           if (j == n) tc_commit(done);
         }
@@ -610,35 +648,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
     const int qi = q0 + row;
     const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
     const float nl = -p.lse[at] * kLog2e;
-    float delta = p.delta[at];
-    float total = 0.f;  // of dS
+    float delta = 0.f;
     bool ok = true;
+    if (n > 1) {
+      // delta of 16 rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
+      uint4 o[DH / 16];
+#pragma unroll
+      for (int x = 0; x < DH / 16; ++x) {
+        const int r = warp * 16 + (x & 3) * 4 + (lane >> 3), e = (x >> 2) * 64 + (lane & 7) * 8;
+        o[x] = make_uint4(0, 0, 0, 0);
+        if (q0 + r < it.len && e < p.s.dim)
+          o[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o.p) + (it.row0 + q0 + r) * p.o.token +
+                                                 it.head * p.o.head + e);
+      }
+      ok = warp_wait(q_full, 0, guard, kSiteMmaFull);
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < DH / 16; ++x) {
+        const int r = warp * 16 + (x & 3) * 4 + (lane >> 3);
+        const uint4 g = *reinterpret_cast<const uint4*>(s_do + (x >> 2) * kChunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        part[x & 3] = dot8(o[x], g, part[x & 3]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        part[x] += __shfl_xor_sync(kAll, part[x], 4);
+        part[x] += __shfl_xor_sync(kAll, part[x], 2);
+        part[x] += __shfl_xor_sync(kAll, part[x], 1);
+        if ((lane & 7) == 0) s_sum[warp * 16 + x * 4 + (lane >> 3)] = part[x];
+      }
+      asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+      // The sums of dS go there no sooner than every warp has read dP of the first tile, which is after this.
+      delta = s_sum[row];
+    }
+    float total = 0.f;  // of dS
     for (int j = 0; j < n; ++j) {
-      ok = warp_wait(sd_full, j & 1, guard, kSiteMmaFull);
+      ok = ok && warp_wait(sd_full, j & 1, guard, kSiteMmaFull);
       if (!ok) {
         if (n == 1) asm volatile("barrier.cta.sync 1, 256;" ::: "memory");  // the others may stand at it
         break;
       }
       tc_fence_after_sync();
-      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * 128 + 64 * half;
-      float s[64], dp[64];
-      tmem_ld_64(tmem + lanes + C::DP + 64 * half, dp);
+      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * W + H * half;
+      float s[H], dp[H];
+      tmem_ld<H>(tmem + lanes + C::DP + H * half, dp);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(dp_read);
-      tmem_ld_64(t_s, s);
-      const int k0 = j * kRows;
+      tmem_ld<H>(t_s, s);
+      const int k0 = j * W;
       const uint64_t c2 = pair(p.scale_log2, p.scale_log2), n2 = pair(nl, nl);
 #pragma unroll
-      for (int e = 0; e < 64; e += 2) {
+      for (int e = 0; e < H; e += 2) {
         unpair(fma_pair(pair(s[e], s[e + 1]), c2, n2), s[e], s[e + 1]);
         s[e] = exp2_fast(s[e]);
         s[e + 1] = exp2_fast(s[e + 1]);
       }
-      if (k0 + kRows > it.len || (p.s.causal && k0 + kRows > q0)) {
-        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - 64 * half;
+      if (k0 + W > it.len || (p.s.causal && k0 + W > q0)) {
+        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * half;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
+        for (int e = 0; e < H; ++e) {
           s[e] = e < end ? s[e] : 0.f;
           dp[e] = e < end ? dp[e] : 0.f;
         }
@@ -646,23 +714,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
       if (n == 1) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) sum = fmaf(s[e], dp[e], sum);
+        for (int e = 0; e < H; ++e) sum = fmaf(s[e], dp[e], sum);
         s_sum[half * kRows + row] = sum;
         asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
         delta = s_sum[row] + s_sum[kRows + row];
       }
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       const uint64_t d2 = pair(-delta, -delta);
-      uint32_t w[32];
+      uint32_t w[H / 2];
 #pragma unroll
-      for (int e = 0; e < 64; e += 2) {
+      for (int e = 0; e < H; e += 2) {
         const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
         sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], ds);
         float x0, x1;
         unpair(ds, x0, x1);
         w[e / 2] = pack_bf16(x0, x1);
       }
-      tmem_st_32(t_s, w);
+      tmem_st(t_s, w);
       float x0, x1;
       unpair(add_pair(sum[0], sum[1]), x0, x1);
       total += x0 + x1;
@@ -703,39 +771,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) dq_kernel(const __grid_constant
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::TMEM);
   }
 }
 
 // ------------------------------------------------------------------ dK, dV
 
-template <int DH>
+template <int DH, int W>
 struct DkvCfg {
-  static constexpr uint32_t TILE = DH / 64 * kChunk;
-  static constexpr int QS = DH == 64 ? 4 : 2, DS = DH == 64 ? 4 : 2;
-  static constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 256 + DH;
-  static constexpr size_t SMEM = kSlack + (2 + QS + DS) * TILE + QS * 1024 + 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TILE = DH / 64 * kChunk, NARROW = DH / 64 * W * 128;  // of the keys, of the queries
+  static constexpr int QS = DH == 64 ? 4 : 3, DS = DH == 64 ? 4 : 2, RS = QS == 3 ? 2 : 4;
+  static constexpr uint32_t S = 0, DP = W, DV = 2 * W, DK = 2 * W + DH;
+  static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
+  static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
+  static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + 256;
+  static_assert(SMEM <= 227 * 1024 && CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Query tile i: P^T goes over S^T, dS^T over dP^T. The scores of tile i + 1 are
 // made while the threads work on dS of tile i, its dP while they work on P of
 // tile i + 1.
-template <int DH>
-__global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constant__ TcParams p) {
-  using C = DkvCfg<DH>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+template <int DH, int W>
+__global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(const __grid_constant__ TcParams p) {
+  using C = DkvCfg<DH, W>;
+  constexpr int H = W / 2;  // columns of a thread
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (misaligned(smem, p.status)) return;
   uint8_t* s_k = smem;
   uint8_t* s_v = s_k + C::TILE;
   uint8_t* s_q = s_v + C::TILE;
-  uint8_t* s_do = s_q + C::QS * C::TILE;
-  float* s_row = reinterpret_cast<float*>(s_do + C::DS * C::TILE);  // [QS][2][128]: -lse log2(e), -delta
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_row + C::QS * 2 * kRows);
-  const Ring<C::QS> ring_q{bars, bars + C::QS};  // full: the tile, and the 32 lanes' rows
+  uint8_t* s_do = s_q + C::QS * C::NARROW;
+  float* s_row = reinterpret_cast<float*>(s_do + C::DS * C::NARROW);  // [RS][2][W]: -lse log2(e), -delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_row + C::RS * 2 * W);
+  const Ring<C::QS> ring_q{bars, bars + C::QS};
   bars += 2 * C::QS;
   const Ring<C::DS> ring_d{bars, bars + C::DS};
   bars += 2 * C::DS;
+  const Ring<C::RS> ring_r{bars, bars + C::RS};
+  bars += 2 * C::RS;
   uint64_t* kv_full = bars;
   uint64_t* s_full = bars + 1;
   uint64_t* p_full = bars + 2;
@@ -748,8 +821,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    ring_q.init(33);
+    ring_q.init();
     ring_d.init();
+    ring_r.init(32, kSoftWarps);
     mbar_init(kv_full, 1);
     mbar_init(s_full, 1);
     mbar_init(p_full, kSoftWarps);
@@ -765,7 +839,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
   const Item it = item_of(p, p.s.kv_heads, false);
   const int k0 = it.tile * kRows;
   if (k0 >= it.len) return;
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::TMEM);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -773,8 +847,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
   // Query tiles first .. last of every head of the group; pass i is head i / per, tile first + i % per.
-  const int first = p.s.causal ? it.tile : 0;
-  const int per = (it.len + kRows - 1) / kRows - first;
+  const int first = p.s.causal ? k0 / W : 0;
+  const int per = (it.len + W - 1) / W - first;
   const int n = per * group;
   int issued_q = 0, issued_d = 0;
 
@@ -785,51 +859,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
       load_tile<DH>(s_v, &p.v, it.head, it.row0 + k0, kv_full);
     }
     for (int i = 0; i < n; ++i) {
-      const int h = it.head * group + i / per, q0 = (first + i % per) * kRows;
+      const int h = it.head * group + i / per;
+      const int64_t row = it.row0 + (first + i % per) * W;
       if (!ring_q.wait_empty(i, guard)) break;
-      uint64_t* full = ring_q.full + i % C::QS;
       if (i + 1 != p.withhold) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, C::TILE);
-          load_tile<DH>(s_q + (i % C::QS) * C::TILE, &p.q, h, it.row0 + q0, full);
+          mbar_arrive_expect_tx(ring_q.full + i % C::QS, C::NARROW);
+          load_tile<DH, W>(s_q + (i % C::QS) * C::NARROW, &p.q, h, row, ring_q.full + i % C::QS);
         }
         issued_q = i + 1;
       }
-      float* rows = s_row + (i % C::QS) * 2 * kRows;
-      const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int r = x * 32 + lane;
-        const bool on = q0 + r < it.len;
-        rows[r] = on ? -p.lse[at + r] * kLog2e : 0.f;
-        rows[kRows + r] = on ? -p.delta[at + r] : 0.f;
-      }
-      mbar_arrive(full);
       if (!ring_d.wait_empty(i, guard)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(ring_d.full + i % C::DS, C::TILE);
-        load_tile<DH>(s_do + (i % C::DS) * C::TILE, &p.d_o, h, it.row0 + q0, ring_d.full + i % C::DS);
+        mbar_arrive_expect_tx(ring_d.full + i % C::DS, C::NARROW);
+        load_tile<DH, W>(s_do + (i % C::DS) * C::NARROW, &p.d_o, h, row, ring_d.full + i % C::DS);
       }
       issued_d = i + 1;
+    }
+  } else if (warp == kRowWarp) {
+    // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them.
+    for (int i = 0; i < n; ++i) {
+      const int h = it.head * group + i / per, q0 = (first + i % per) * W;
+      const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
+      float nl[W / 32], nd[W / 32];
+#pragma unroll
+      for (int x = 0; x < W / 32; ++x) {
+        const int r = x * 32 + lane;
+        const bool on = q0 + r < it.len;
+        nl[x] = on ? -p.lse[at + r] * kLog2e : 0.f;
+        nd[x] = on ? -p.delta[at + r] : 0.f;
+      }
+      if (!ring_r.wait_empty(i, guard)) break;
+      float* rows = s_row + (i % C::RS) * 2 * W;
+#pragma unroll
+      for (int x = 0; x < W / 32; ++x) {
+        rows[x * 32 + lane] = nl[x];
+        rows[W + x * 32 + lane] = nd[x];
+      }
+      mbar_arrive(ring_r.full + i % C::RS);
     }
   } else if (warp == kMmaWarp) {
     // Tile i of a ring, its rows of the next sequence cleared.
     auto take_q = [&](int i) {
       if (!ring_q.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + i % per) * kRows;
-      if (rows < kRows) clear_rows<DH>(s_q + (i % C::QS) * C::TILE, rows, lane);
+      const int rows = it.len - (first + i % per) * W;
+      if (rows < W) clear_rows<DH, W>(s_q + (i % C::QS) * C::NARROW, rows, lane);
       return true;
     };
     auto take_d = [&](int i) {
       if (!ring_d.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + i % per) * kRows;
-      if (rows < kRows) clear_rows<DH>(s_do + (i % C::DS) * C::TILE, rows, lane);
+      const int rows = it.len - (first + i % per) * W;
+      if (rows < W) clear_rows<DH, W>(s_do + (i % C::DS) * C::NARROW, rows, lane);
       return true;
     };
     bool ok = warp_wait(kv_full, 0, guard, kSiteMmaFull) && take_q(0);
     if (ok) {
       if (lane == 0) {
-        product_rows<DH>(tmem + C::S, s_k, s_q);
+        product_rows<DH, W>(tmem + C::S, s_k, s_q);
         tc_commit(s_full);
       }
       __syncwarp();
@@ -837,18 +923,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
     }
     if (ok) {
       if (lane == 0) {
-        product_rows<DH>(tmem + C::DP, s_v, s_do);
+        product_rows<DH, W>(tmem + C::DP, s_v, s_do);
         tc_commit(dp_full);
       }
       __syncwarp();
       for (int i = 0; i < n; ++i) {
-        const uint8_t* d_tile = s_do + (i % C::DS) * C::TILE;
-        const uint8_t* q_tile = s_q + (i % C::QS) * C::TILE;
+        const uint8_t* d_tile = s_do + (i % C::DS) * C::NARROW;
+        const uint8_t* q_tile = s_q + (i % C::QS) * C::NARROW;
         ok = warp_wait(p_full, i & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          product_tokens<DH>(tmem + C::DV, tmem + C::S, d_tile, i > 0, 64);
+          product_tokens<DH, W, H>(tmem + C::DV, tmem + C::S, d_tile, i > 0, H);
           tc_commit(ring_d.empty + i % C::DS);
         }
         __syncwarp();
@@ -856,7 +942,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
           ok = take_q(i + 1);
           if (!ok) break;
           if (lane == 0) {
-            product_rows<DH>(tmem + C::S, s_k, s_q + ((i + 1) % C::QS) * C::TILE);
+            product_rows<DH, W>(tmem + C::S, s_k, s_q + ((i + 1) % C::QS) * C::NARROW);
             tc_commit(s_full);
           }
           __syncwarp();
@@ -865,7 +951,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
         if (!ok) break;
         tc_fence_after_sync();
         if (lane == 0) {
-          product_tokens<DH>(tmem + C::DK, tmem + C::DP, q_tile, i > 0, 64);
+          product_tokens<DH, W, H>(tmem + C::DK, tmem + C::DP, q_tile, i > 0, H);
           tc_commit(ring_q.empty + i % C::QS);
           if (i + 1 == n) tc_commit(done);
         }
@@ -874,7 +960,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
           ok = take_d(i + 1);
           if (!ok) break;
           if (lane == 0) {
-            product_rows<DH>(tmem + C::DP, s_v, s_do + ((i + 1) % C::DS) * C::TILE);
+            product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((i + 1) % C::DS) * C::NARROW);
             tc_commit(dp_full);
           }
           __syncwarp();
@@ -884,20 +970,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
   } else {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + C::S + 64 * half, t_dp = tmem + lanes + C::DP + 64 * half;
+    const uint32_t t_s = tmem + lanes + C::S + H * half, t_dp = tmem + lanes + C::DP + H * half;
     const int kj = k0 + row;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int q0 = (first + i % per) * kRows + 64 * half;  // of this warp's columns
-      const float* rows = s_row + (i % C::QS) * 2 * kRows + 64 * half;
-      ok = ring_q.wait_full(i, guard) && warp_wait(s_full, i & 1, guard, kSiteMmaFull);
+      const int q0 = (first + i % per) * W + H * half;  // of this warp's columns
+      const float* rows = s_row + (i % C::RS) * 2 * W + H * half;
+      ok = ring_r.wait_full(i, guard) && warp_wait(s_full, i & 1, guard, kSiteMmaFull);
       if (!ok) break;
       tc_fence_after_sync();
       const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
-      float s[64];
-      tmem_ld_64(t_s, s);
+      float s[H];
+      tmem_ld<H>(t_s, s);
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
+      for (int e = 0; e < H; e += 4) {
         const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(rows + e);
         unpair(fma_pair(pair(s[e], s[e + 1]), c2, nl.x), s[e], s[e + 1]);
         unpair(fma_pair(pair(s[e + 2], s[e + 3]), c2, nl.y), s[e + 2], s[e + 3]);
@@ -905,15 +991,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
         for (int x = 0; x < 4; ++x) s[e + x] = exp2_fast(s[e + x]);
       }
       const int begin = p.s.causal ? kj - q0 : 0, end = it.len - q0;  // columns that count
-      const bool masked = end < 64 || (p.s.causal && q0 < k0 + kRows);
+      const bool masked = end < H || (p.s.causal && q0 < k0 + kRows);
       if (masked) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] = e >= begin && e < end ? s[e] : 0.f;
+        for (int e = 0; e < H; ++e) s[e] = e >= begin && e < end ? s[e] : 0.f;
       }
-      uint32_t w[32];
+      uint32_t w[H / 2];
 #pragma unroll
-      for (int e = 0; e < 64; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
-      tmem_st_32(t_s, w);
+      for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
+      tmem_st(t_s, w);
       tmem_wait_st();
       tc_fence_before_sync();
       __syncwarp();
@@ -921,26 +1007,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
       ok = warp_wait(dp_full, i & 1, guard, kSiteMmaFull);
       if (!ok) break;
       tc_fence_after_sync();
-      float dp[64];
-      tmem_ld_64(t_dp, dp);
+      float dp[H];
+      tmem_ld<H>(t_dp, dp);
       if (masked) {  // what stands there may be no number
 #pragma unroll
-        for (int e = 0; e < 64; ++e) dp[e] = e >= begin && e < end ? dp[e] : 0.f;
+        for (int e = 0; e < H; ++e) dp[e] = e >= begin && e < end ? dp[e] : 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + kRows + e);
+      for (int e = 0; e < H; e += 4) {
+        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + W + e);
         float x0, x1, x2, x3;
         unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), x0, x1);
         unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), x2, x3);
         w[e / 2] = pack_bf16(x0, x1);
         w[e / 2 + 1] = pack_bf16(x2, x3);
       }
-      tmem_st_32(t_dp, w);
+      tmem_st(t_dp, w);
       tmem_wait_st();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (lane == 0) {
+        mbar_arrive(ds_full);
+        mbar_arrive(ring_r.empty + i % C::RS);
+      }
     }
     ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
     if (ok) {
@@ -973,7 +1062,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) dkv_kernel(const __grid_constan
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::TMEM);
   }
 }
 
@@ -991,7 +1080,7 @@ bool heads_map(CUtensorMap* map, const HeadsView& v, int64_t T, int heads, int d
   if (!encode) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(v.head * 2), static_cast<cuuint64_t>(v.token * 2)};
-  const cuuint32_t box[3] = {64, 1, kRows};
+  const cuuint32_t box[3] = {64, 1, 64};
   const cuuint32_t step[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -1035,7 +1124,7 @@ cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t s) {
   TcParams p;
   cudaError_t e = params_of(c, &p);
   if (e != cudaSuccess) return e;
-  return c.s.dim <= 64 ? launch_fwd<64, 2>(p, s) : launch_fwd<128, 2>(p, s);
+  return c.s.dim <= 64 ? launch_fwd<64, 1>(p, s) : launch_fwd<128, 2>(p, s);
 }
 
 cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStream_t s) {
@@ -1047,16 +1136,17 @@ cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStr
   p.dk = c.dk;
   p.dv = c.dv;
   p.delta = delta;
+  // Heads of up to 64 elements: 64 keys (queries) at a time and half of the tensor memory, so that two CTAs share an SM.
   const bool small = c.s.dim <= 64;
   {
     TraceScope trace("attn_core_dq", s);
-    e = small ? launch(dq_kernel<64>, p, kRows, c.s.heads, kTcThreads, DqCfg<64>::SMEM, s)
-              : launch(dq_kernel<128>, p, kRows, c.s.heads, kTcThreads, DqCfg<128>::SMEM, s);
+    e = small ? launch(dq_kernel<64, 64>, p, kRows, c.s.heads, kTcThreads, DqCfg<64, 64>::SMEM, s)
+              : launch(dq_kernel<128, 128>, p, kRows, c.s.heads, kTcThreads, DqCfg<128, 128>::SMEM, s);
   }
   if (e != cudaSuccess) return e;
   TraceScope trace("attn_core_dkv", s);
-  return small ? launch(dkv_kernel<64>, p, kRows, c.s.kv_heads, kTcThreads, DkvCfg<64>::SMEM, s)
-               : launch(dkv_kernel<128>, p, kRows, c.s.kv_heads, kTcThreads, DkvCfg<128>::SMEM, s);
+  return small ? launch(dkv_kernel<64, 64>, p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<64, 64>::SMEM, s)
+               : launch(dkv_kernel<128, 128>, p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<128, 128>::SMEM, s);
 }
 
 }  // namespace tpmlp
