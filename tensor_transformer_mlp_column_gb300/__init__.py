@@ -788,7 +788,7 @@ def tpmlp_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, out: Optiona
 # ------------------------------------------------- the attention of a training step
 
 
-def _heads(t: torch.Tensor, T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: array, name: str) -> int:
+def _heads(t: torch.Tensor, T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: list, name: str) -> int:
     """Address of a tensor [T, heads, dim] on device `dev`; its two strides go to `strides`."""
     if t.dtype != dtype or t.shape != (T, heads, dim):
         raise ValueError(f"{name} must be {dtype} of shape {(T, heads, dim)}")
@@ -797,16 +797,17 @@ def _heads(t: torch.Tensor, T: int, heads: int, dim: int, dtype: torch.dtype, de
     token, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    strides.append(token)
-    strides.append(head)
+    strides += (token, head)
     return t.data_ptr()
 
 
-def _heads_output(t: Optional[torch.Tensor], T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: array,
+def _heads_output(t: Optional[torch.Tensor], T: int, heads: int, dim: int, dtype: torch.dtype, dev: int, strides: list,
                   name: str):
     """(tensor, address) of an output [T, heads, dim], the caller's or a new one."""
     if t is None:
         t = torch.empty((T, heads, dim), dtype=dtype, device="cuda")
+        strides += (heads * dim, dim)
+        return t, t.data_ptr()
     return t, _heads(t, T, heads, dim, dtype, dev, strides, name)
 
 
@@ -824,11 +825,12 @@ def _sequences(starts: Optional[torch.Tensor], max_seq: Optional[int], batch: Op
         if batch < 1 or T % batch != 0 or max_seq not in (None, T // batch):
             raise ValueError(f"without starts the {T} tokens must be {batch} equal sequences")
         return 0, batch, T // batch
-    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] < 1:
+    shape = starts.shape
+    if starts.dtype != torch.int32 or len(shape) != 1 or shape[0] < 1:
         raise ValueError("starts must be an int32 tensor of one more element than there are sequences")
-    if batch not in (None, starts.shape[0] - 1):
+    if batch not in (None, shape[0] - 1):
         raise ValueError("batch and starts disagree")
-    return _ptr(starts, dev, "starts"), starts.shape[0] - 1, T if max_seq is None else min(int(max_seq), T)
+    return _ptr(starts, dev, "starts"), shape[0] - 1, T if max_seq is None else min(int(max_seq), T)
 
 
 def tpmlp_attn_core_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: Optional[torch.Tensor] = None,
@@ -841,14 +843,16 @@ def tpmlp_attn_core_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s
     GPU), none longer than max_seq (default T). Rows of no sequence are left as they were: undefined in an o or lse
     that the call allocates. scale is 1 / sqrt(head_dim) by default."""
     T, heads, kv, dim = _qkv_shape(q, k)
-    dt, strides = _type(q), array("q")
+    dt, strides = _type(q), []
     with _On(stream) as on:
         dev = on.dev
         qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
-        kp, vp = (_heads(t, T, kv, dim, q.dtype, dev, strides, n) for t, n in ((k, "k"), (v, "v")))
+        kp = _heads(k, T, kv, dim, q.dtype, dev, strides, "k")
+        vp = _heads(v, T, kv, dim, q.dtype, dev, strides, "v")
         sp, n, most = _sequences(starts, max_seq, batch, T, dev)
         o, op = _heads_output(o, T, heads, dim, q.dtype, dev, strides, "o")
         lse, lp = _output(lse, (heads, T), torch.float32, dev, "lse")
+        strides = array("q", strides)
         _check(lib().tpmlp_attn_core_forward(qp, kp, vp, strides.buffer_info()[0], sp, T, n, most, heads, kv, dim,
                                              dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, dt, op,
                                              lp, on.raw), "tpmlp_attn_core_forward")
@@ -860,6 +864,11 @@ def tpmlp_attn_core_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim:
                                                      TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32))
 
 
+@functools.lru_cache(maxsize=1024)
+def _core_workspace(T: int, heads: int, kv_heads: int, head_dim: int, dt: int) -> int:
+    return int(lib().tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim, dt))
+
+
 def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
                              do: torch.Tensor, starts: Optional[torch.Tensor] = None, max_seq: Optional[int] = None,
                              batch: Optional[int] = None, scale: Optional[float] = None, causal: bool = True,
@@ -868,17 +877,20 @@ def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """Gradients of sum(o * do) of tpmlp_attn_core_forward with the same arguments: (dq, dk, dv), as q, k, v. The
     probabilities are made again from lse. Rows of no sequence are left as they were."""
     T, heads, kv, dim = _qkv_shape(q, k)
-    dt, l, strides = _type(q), lib(), array("q")
+    dt, l, strides = _type(q), lib(), []
     with _On(stream) as on:
         dev = on.dev
         qp = _heads(q, T, heads, dim, q.dtype, dev, strides, "q")
-        kp, vp = (_heads(t, T, kv, dim, q.dtype, dev, strides, n) for t, n in ((k, "k"), (v, "v")))
-        op, gp = (_heads(t, T, heads, dim, q.dtype, dev, strides, n) for t, n in ((o, "o"), (do, "do")))
+        kp = _heads(k, T, kv, dim, q.dtype, dev, strides, "k")
+        vp = _heads(v, T, kv, dim, q.dtype, dev, strides, "v")
+        op = _heads(o, T, heads, dim, q.dtype, dev, strides, "o")
+        gp = _heads(do, T, heads, dim, q.dtype, dev, strides, "do")
         sp, n, most = _sequences(starts, max_seq, batch, T, dev)
         dq, dqp = _heads_output(dq, T, heads, dim, q.dtype, dev, strides, "dq")
         dk, dkp = _heads_output(dk, T, kv, dim, q.dtype, dev, strides, "dk")
         dv, dvp = _heads_output(dv, T, kv, dim, q.dtype, dev, strides, "dv")
-        ws, wp, wn = _space(l.tpmlp_attn_core_workspace_bytes(T, heads, kv, dim, dt), workspace, dev)
+        ws, wp, wn = _space(_core_workspace(T, heads, kv, dim, dt), workspace, dev)
+        strides = array("q", strides)
         _check(l.tpmlp_attn_core_backward(qp, kp, vp, op, _like(lse, (heads, T), torch.float32, dev, "lse"), gp,
                                           strides.buffer_info()[0], sp, T, n, most, heads, kv, dim,
                                           dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, dt, dqp, dkp,
@@ -888,23 +900,36 @@ def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 
 @functools.lru_cache(maxsize=64)
 def _turns(freqs: tuple, axis: Optional[tuple], axes: int):
-    """The frequencies and their axes as host arrays."""
+    """The frequencies and their axes as host arrays, and the arrays' addresses."""
     if axis is not None and (len(axis) != len(freqs) or any(a < 0 or a >= axes for a in axis)):
         raise ValueError(f"axis must give one of {axes} axes for each of the {len(freqs)} frequencies")
-    return array("d", freqs), None if axis is None else array("B", axis)
+    f, a = array("d", freqs), None if axis is None else array("B", axis)
+    return f, a, f.buffer_info()[0], None if a is None else a.buffer_info()[0]
+
+
+_last_turns = (None, None, 0, None)
 
 
 def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
     """What both calls take: the shape and the arguments between the strides and the outputs."""
     T, heads, kv, dim = _qkv_shape(q, k)
-    if pos.dtype != torch.int64 or pos.shape[-1:] != (T,) or pos.dim() > 2:
+    at = pos.shape
+    if pos.dtype != torch.int64 or len(at) not in (1, 2) or at[-1] != T:
         raise ValueError(f"pos must be an int64 tensor of {T} positions, or [axes, {T}]")
-    axes = pos.shape[0] if pos.dim() == 2 else 1
-    f, a = _turns(tuple(freqs), None if axis is None else tuple(axis), axes)
-    w = [0 if t is None else _like(t, (dim,), q.dtype, dev, n) for t, n in ((wq, "wq"), (wk, "wk"))]
-    return (T, heads, kv, dim), (*w, float(eps), _ptr(pos, dev, "pos"), f.buffer_info()[0],
-                                 None if a is None else a.buffer_info()[0], T, heads, kv, dim, 2 * len(f), axes,
-                                 1 if interleaved else 0, _type(q)), (f, a)
+    axes = at[0] if len(at) == 2 else 1
+    # A program's frequencies are the same in every call: the last call's arrays serve while its values are equal.
+    global _last_turns
+    last = _last_turns
+    if last[0] == freqs and last[1] == axis and last[2] == axes:
+        keep = last[3]
+    else:
+        keep = _turns(tuple(freqs), None if axis is None else tuple(axis), axes)
+        if isinstance(freqs, (list, tuple)) and (axis is None or isinstance(axis, (list, tuple))):
+            _last_turns = (freqs[:], None if axis is None else axis[:], axes, keep)
+    wqp = 0 if wq is None else _like(wq, (dim,), q.dtype, dev, "wq")
+    wkp = 0 if wk is None else _like(wk, (dim,), q.dtype, dev, "wk")
+    return (T, heads, kv, dim), (wqp, wkp, eps, _ptr(pos, dev, "pos"), keep[2], keep[3], T, heads, kv, dim,
+                                 2 * len(keep[0]), axes, 1 if interleaved else 0, _type(q)), keep
 
 
 def tpmlp_qk_rope_forward(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, freqs: Sequence[float],
@@ -915,7 +940,7 @@ def tpmlp_qk_rope_forward(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, f
     wk (both None: not), then its pairs turned by pos * freqs: (yq, yk). Pair i is (i, i + len(freqs)), or
     (2 i, 2 i + 1) when interleaved. pos is int64 [T], or [axes, T] with axis[i] naming the axis that turns pair i.
     yq may be q and yk may be k."""
-    strides = array("q")
+    strides = []
     with _On(stream) as on:
         dev = on.dev
         (T, heads, kv, dim), args, keep = _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev)
@@ -923,12 +948,18 @@ def tpmlp_qk_rope_forward(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, f
         kp = _heads(k, T, kv, dim, q.dtype, dev, strides, "k")
         yq, yqp = _heads_output(yq, T, heads, dim, q.dtype, dev, strides, "yq")
         yk, ykp = _heads_output(yk, T, kv, dim, q.dtype, dev, strides, "yk")
+        strides = array("q", strides)
         _check(lib().tpmlp_qk_rope_forward(qp, kp, strides.buffer_info()[0], *args, yqp, ykp, on.raw),
                "tpmlp_qk_rope_forward")
     return yq, yk
 
 
 def tpmlp_qk_rope_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim))
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_workspace(T: int, heads: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim))
 
 
@@ -940,7 +971,7 @@ def tpmlp_qk_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor
                            workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of sum(yq * dyq) + sum(yk * dyk) of tpmlp_qk_rope_forward: (dq, dk, dwq, dwk), the weights' in fp32 and
     None without weights. dq may be dyq and dk may be dyk."""
-    l, strides = lib(), array("q")
+    l, strides = lib(), []
     with _On(stream) as on:
         dev = on.dev
         (T, heads, kv, dim), args, keep = _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev)
@@ -954,9 +985,10 @@ def tpmlp_qk_rope_backward(dyq: torch.Tensor, dyk: torch.Tensor, q: torch.Tensor
         if wq is not None:
             dwq, wqp = _output(dwq, (dim,), torch.float32, dev, "dwq")
             dwk, wkp = _output(dwk, (dim,), torch.float32, dev, "dwk")
-            ws, wp, wn = _space(l.tpmlp_qk_rope_workspace_bytes(T, heads, kv, dim), workspace, dev)
+            ws, wp, wn = _space(_rope_workspace(T, heads, kv, dim), workspace, dev)
         elif dwq is not None or dwk is not None:
             raise ValueError("dwq and dwk need wq and wk")
+        strides = array("q", strides)
         _check(l.tpmlp_qk_rope_backward(gq, gk, qp, kp, strides.buffer_info()[0], *args, dqp, dkp, wqp, wkp, wp, wn, on.raw),
                "tpmlp_qk_rope_backward")
     return dq, dk, dwq, dwk

@@ -393,17 +393,18 @@ __global__ void __launch_bounds__(kThreads) core_dq_kernel(const __grid_constant
   store_rows<DH>(c.dq, row0, q0, len, h, c.s.dim, dq, sc, ty, tx);
 }
 
-template <typename K, typename... Args>
-cudaError_t launch(K kernel, int64_t items, size_t smem, cudaStream_t s, Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <auto Kernel, typename... Args>
+cudaError_t launch(int64_t items, size_t smem, cudaStream_t s, Args... args) {
+  static std::atomic<uint64_t> devices{0};
+  cudaError_t e = allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(kThreads), smem, s, args...);
+  return launch_pdl(Kernel, dim3(static_cast<unsigned>(items)), dim3(kThreads), smem, s, args...);
 }
 
 template <int DH>
 cudaError_t simt_forward(const CoreForward& c, cudaStream_t s) {
   const int64_t tiles = (c.s.max_seq + kTile - 1) / kTile;
-  return launch(core_forward_kernel<DH>, tiles * c.s.heads * c.s.batch, 3 * tile_bytes<DH>() + kMatrixBytes, s, c);
+  return launch<core_forward_kernel<DH>>(tiles * c.s.heads * c.s.batch, 3 * tile_bytes<DH>() + kMatrixBytes, s, c);
 }
 
 template <int DH>
@@ -411,12 +412,11 @@ cudaError_t simt_backward(const CoreBackward& c, const float* delta, cudaStream_
   const int64_t tiles = (c.s.max_seq + kTile - 1) / kTile;
   {
     TraceScope trace("attn_core_dkv", s);
-    cudaError_t e = launch(core_dkv_kernel<DH>, tiles * c.s.kv_heads * c.s.batch,
-                           4 * tile_bytes<DH>() + 2 * kMatrixBytes, s, c, delta);
+    cudaError_t e = launch<core_dkv_kernel<DH>>(tiles * c.s.kv_heads * c.s.batch, 4 * tile_bytes<DH>() + 2 * kMatrixBytes, s, c, delta);
     if (e != cudaSuccess) return e;
   }
   TraceScope trace("attn_core_dq", s);
-  return launch(core_dq_kernel<DH>, tiles * c.s.heads * c.s.batch, 4 * tile_bytes<DH>() + kMatrixBytes, s, c, delta);
+  return launch<core_dq_kernel<DH>>(tiles * c.s.heads * c.s.batch, 4 * tile_bytes<DH>() + kMatrixBytes, s, c, delta);
 }
 
 }  // namespace

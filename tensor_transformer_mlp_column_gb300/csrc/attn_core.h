@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace tpmlp {
@@ -43,6 +45,19 @@ __device__ __forceinline__ int core_sequence(const CoreShape& s, int b, int64_t&
   if (begin >= 0 && end >= begin && end <= s.T && end - begin <= s.max_seq) return static_cast<int>(end - begin);
   if (threadIdx.x == 0) atomicCAS(status, 0, kSiteBoundsBase + kChkSequence);
   return 0;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device and kernel.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& devices) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (devices.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 struct CoreForward {

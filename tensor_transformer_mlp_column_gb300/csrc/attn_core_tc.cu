@@ -1103,19 +1103,20 @@ cudaError_t params_of(const C& c, TcParams* p) {
              : cudaErrorInvalidValue;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, TcParams& p, int rows, int heads, int threads, size_t smem, cudaStream_t s) {
+template <auto Kernel>
+cudaError_t launch(TcParams& p, int rows, int heads, int threads, size_t smem, cudaStream_t s) {
+  static std::atomic<uint64_t> devices{0};
   p.tiles = (p.s.max_seq + rows - 1) / rows;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
   const int64_t items = int64_t(p.tiles) * heads * p.s.batch;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(items)), dim3(threads), smem, s, p);
+  return launch_pdl(Kernel, dim3(static_cast<unsigned>(items)), dim3(threads), smem, s, p);
 }
 
 template <int DH, int NQ>
 cudaError_t launch_fwd(TcParams& p, cudaStream_t s) {
   using C = FwdCfg<DH, NQ>;
-  return launch(fwd_kernel<DH, NQ>, p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, s);
+  return launch<fwd_kernel<DH, NQ>>(p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, s);
 }
 
 }  // namespace
@@ -1140,13 +1141,13 @@ cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStr
   const bool small = c.s.dim <= 64;
   {
     TraceScope trace("attn_core_dq", s);
-    e = small ? launch(dq_kernel<64, 64>, p, kRows, c.s.heads, kTcThreads, DqCfg<64, 64>::SMEM, s)
-              : launch(dq_kernel<128, 128>, p, kRows, c.s.heads, kTcThreads, DqCfg<128, 128>::SMEM, s);
+    e = small ? launch<dq_kernel<64, 64>>(p, kRows, c.s.heads, kTcThreads, DqCfg<64, 64>::SMEM, s)
+              : launch<dq_kernel<128, 128>>(p, kRows, c.s.heads, kTcThreads, DqCfg<128, 128>::SMEM, s);
   }
   if (e != cudaSuccess) return e;
   TraceScope trace("attn_core_dkv", s);
-  return small ? launch(dkv_kernel<64, 64>, p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<64, 64>::SMEM, s)
-               : launch(dkv_kernel<128, 128>, p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<128, 128>::SMEM, s);
+  return small ? launch<dkv_kernel<64, 64>>(p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<64, 64>::SMEM, s)
+               : launch<dkv_kernel<128, 128>>(p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<128, 128>::SMEM, s);
 }
 
 }  // namespace tpmlp

@@ -11,14 +11,16 @@
 // modulo 2^64 is that fraction to 2^-64 pos, at any position, without 64-bit
 // floating point.
 //
-// Bound by memory: x is read once (backward: x and dy) and y written once. A
-// head belongs to a group of 8, 16 or 32 lanes, eight elements a lane, held in
-// registers between the sums and the result: the two runs of four whose pairs
-// they are (4 i and rot / 2 + 4 i) or eight in a row. A group takes several
-// heads of one token, so that a lane makes its four angles once for them, and
-// has several heads' loads in flight. The gradients of the weights are summed by
-// each lane over the heads it takes, then over the CTA's groups, then (in 64
-// bits) over the CTAs, in an order that the sizes fix.
+// Bound by memory: x is read once (backward: x and dy) and y written once; what
+// costs beside it is the instructions. A head belongs to a group of lanes, 2 RUN
+// elements a lane, held in registers between the sums and the result: two runs
+// of RUN whose pairs they are (i and rot / 2 + i), or 2 RUN in a row. RUN is 8
+// for bf16 where the halves begin on 16 bytes (rot and head_dim multiples of 16),
+// else 4. A CTA has heads of q or of k; a group takes up to 8 heads of one token,
+// so that a lane makes its angles once for them, and has several heads' loads in
+// flight while it does. The gradients of the weights are summed by each lane over
+// the heads it takes, then over the CTA's groups, then (in 64 bits) over the
+// CTAs, in an order that the sizes fix.
 #include "attn_core.h"
 
 #include <cuda_bf16.h>
@@ -32,86 +34,82 @@ namespace tpmlp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxGrid = 152 * 4;  // of the backward: CTAs whose sums are added at the end
 
-template <typename T>
-struct Raw;
+template <typename T, int RUN>
+struct RawOf {
+  using type = uint4;  // 8 bf16 or 4 fp32
+};
 template <>
-struct Raw<__nv_bfloat16> {
+struct RawOf<__nv_bfloat16, 4> {
   using type = uint2;
 };
-template <>
-struct Raw<float> {
-  using type = uint4;
-};
 
-__device__ __forceinline__ void unpack(uint2 u, float* v) {
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float* v) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      v[2 * i] = __uint_as_float(x[i] << 16);
+      v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    } else {
+      v[i] = __uint_as_float(x[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const uint2& u, float* v) {
   v[0] = __uint_as_float(u.x << 16);
   v[1] = __uint_as_float(u.x & 0xffff0000u);
   v[2] = __uint_as_float(u.y << 16);
   v[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ void unpack(uint4 u, float* v) {
-  v[0] = __uint_as_float(u.x);
-  v[1] = __uint_as_float(u.y);
-  v[2] = __uint_as_float(u.z);
-  v[3] = __uint_as_float(u.w);
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void pack(uint2& u, const float* v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
+template <typename T>
 __device__ __forceinline__ void pack(uint4& u, const float* v) {
-  u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  if constexpr (sizeof(T) == 2)
+    u = make_uint4(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]), pack_pair(v[4], v[5]), pack_pair(v[6], v[7]));
+  else
+    u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <typename T>
+__device__ __forceinline__ void pack(uint2& u, const float* v) {
+  u = make_uint2(pack_pair(v[0], v[1]), pack_pair(v[2], v[3]));
 }
 
-// What a lane does with a head: its elements at a .. a + 3 and b .. b + 3, and their four angles.
-struct Lane {
-  int a, b;
-  bool on, turned;
-  float cos[4], sin[4];
-};
-
-template <int G>
-__device__ __forceinline__ Lane lane_of(const RopeShape& s, int u) {
-  Lane l;
-  l.on = 8 * u < s.dim;
-  l.turned = 8 * u < s.rot;
-  const bool halves = l.turned && !s.interleaved;
-  l.a = halves ? 4 * u : 8 * u;
-  l.b = halves ? s.rot / 2 + 4 * u : 8 * u + 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l.cos[i] = 1.f, l.sin[i] = 0.f;  // of a lane that gets no token
-  return l;
-}
-
-__device__ __forceinline__ void angles(const RopeShape& s, int64_t t, int u, Lane& l) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    l.cos[i] = 1.f;
-    l.sin[i] = 0.f;
-    if (l.turned) {
-      const uint64_t turn = static_cast<uint64_t>(s.pos[s.axis[4 * u + i] * s.T + t]) * s.turn[4 * u + i];
-      // turn / 2^64 of a full turn, as half turns in [-1, 1).
-      sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f, &l.sin[i], &l.cos[i]);
-    }
+// cos and sin of `turn` / 2^64 of a full turn. For bf16 the upper 32 bits and the special-function unit, off by at
+// most 2^-20: a thousandth of the result's rounding.
+template <typename T>
+__device__ __forceinline__ void angle(uint64_t turn, float& cos, float& sin) {
+  if constexpr (sizeof(T) == 2) {
+    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * (3.14159265358979f * 0x1p-31f);
+    cos = __cosf(x);
+    sin = __sinf(x);
+  } else {
+    sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f, &sin, &cos);
   }
 }
 
-// The pairs of v (4 elements at a, 4 at b) turned by the angles, `back` by their negatives.
-__device__ __forceinline__ void turn(float (&v)[8], const Lane& l, bool interleaved, bool back) {
+__device__ __forceinline__ void turn_pair(float& a, float& b, float cos, float sin) {
+  const float x = a;
+  a = fmaf(x, cos, -(b * sin));
+  b = fmaf(x, sin, b * cos);
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// A lane's weights, from shared memory: they would take 16 of the registers that loads in flight need.
+template <int RUN>
+__device__ __forceinline__ void weights(const float* s_w, int a, int b, float (&w)[2 * RUN]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float c = l.cos[i], s = back ? -l.sin[i] : l.sin[i];
-    if (interleaved) {
-      const float x = v[2 * i], y = v[2 * i + 1];
-      v[2 * i] = fmaf(x, c, -(y * s));
-      v[2 * i + 1] = fmaf(x, s, y * c);
-    } else {
-      const float x = v[i], y = v[4 + i];
-      v[i] = fmaf(x, c, -(y * s));
-      v[4 + i] = fmaf(x, s, y * c);
-    }
+  for (int i = 0; i < RUN; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(s_w + a + i), y = *reinterpret_cast<const float4*>(s_w + b + i);
+    w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+    w[RUN + i] = y.x, w[RUN + i + 1] = y.y, w[RUN + i + 2] = y.z, w[RUN + i + 3] = y.w;
   }
 }
 
@@ -122,196 +120,255 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Items: (token, run of heads); item i is token i / runs, and its j-th head is i % runs + j runs, q's heads first.
-template <typename T, int G, bool BACK>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeCall c, int runs, int per,
-                                                        float* part) {
+// How the heads are handed out. Items of a kind (q, k): (token, run of heads); item i is token i / runs, and its j-th
+// head is i % runs + j runs.
+struct RopePlan {
+  int run, group;  // elements of a run; lanes of a group
+  int runs[2], per[2];
+  int ctas[2];
+};
+
+template <typename T, int RUN, int G, bool BACK>
+__global__ void __launch_bounds__(kThreads, BACK ? 2 : 3) rope_kernel(const __grid_constant__ RopeCall c,
+                                                           const __grid_constant__ RopePlan plan, float* part) {
   constexpr int kGroups = kThreads / G;
-  constexpr int kAhead = BACK ? 2 : 4;  // heads whose loads are in flight
-  using R = typename Raw<T>::type;
-  __shared__ float sums[BACK ? kThreads / 32 : 1][BACK ? 2 : 1][BACK ? 8 * G : 1];
+  constexpr int kAhead = 2;  // heads whose loads are in flight
+  constexpr int N = 2 * RUN;            // elements of a lane
+  using R = typename RawOf<T, RUN>::type;
+  __shared__ uint64_t s_turn[kRopeMaxDim / 2];
+  __shared__ uint8_t s_axis[kRopeMaxDim / 2];
+  __shared__ __align__(16) float s_w[kRopeMaxDim];
+  __shared__ float sums[BACK ? kThreads / 32 : 1][BACK ? N * G : 1];
   const RopeShape& s = c.s;
+  const int kind = static_cast<int>(blockIdx.x) >= plan.ctas[0];
+  const int cta = blockIdx.x - (kind ? plan.ctas[0] : 0);
+  const int heads = s.heads[kind], runs = plan.runs[kind], per = plan.per[kind];
   const int u = threadIdx.x % G;
-  Lane l = lane_of<G>(s, u);
-  const bool norm = c.w[0] != nullptr;
-  const int all = s.heads[0] + s.heads[1];
+  // A lane's elements: a .. a + RUN - 1 and b .. b + RUN - 1.
+  const bool on = N * u < s.dim, turned = N * u < s.rot, halves = turned && !s.interleaved;
+  const int a = halves ? RUN * u : N * u, b = halves ? s.rot / 2 + RUN * u : N * u + RUN;
   const float inv_dim = 1.f / static_cast<float>(s.dim);
+  for (int i = threadIdx.x; i < s.rot / 2; i += kThreads) {
+    s_turn[i] = s.turn[i];
+    s_axis[i] = s.axis[i];
+  }
   pdl_wait();
   pdl_launch_dependents();
-  float w[2][8], dw[2][8];
+  const bool norm = c.w[0] != nullptr;
+  for (int i = threadIdx.x; norm && i < kRopeMaxDim; i += kThreads)
+    s_w[i] = i < s.dim ? to_float(static_cast<const T*>(c.w[kind])[i]) : 0.f;
+  __syncthreads();
+  bool alike = turned;  // one axis turns all pairs of this lane
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int i = 1; i < RUN; ++i) alike = alike && s_axis[RUN * u + i] == s_axis[RUN * u];
+  float dw[N], cos[RUN], sin[RUN];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[k][e] = 1.f, dw[k][e] = 0.f;
-  if (norm && l.on) {
+  for (int e = 0; e < N; ++e) dw[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      unpack(*reinterpret_cast<const R*>(static_cast<const T*>(c.w[k]) + l.a), w[k]);
-      unpack(*reinterpret_cast<const R*>(static_cast<const T*>(c.w[k]) + l.b), w[k] + 4);
-    }
-  }
+  for (int e = 0; e < RUN; ++e) cos[e] = 1.f, sin[e] = 0.f;  // of a lane that gets no token or turns nothing
+  const HeadsView xv = c.x[kind], gv = c.dy[kind], yv = c.y[kind];
   const int64_t items = s.T * runs;
-  // Every lane of a warp goes through the same number of items: the sums of a head are over the warp's shuffles.
-  const int64_t step = int64_t(gridDim.x) * kGroups;
-  for (int64_t base = int64_t(blockIdx.x) * kGroups; base < items; base += step) {
-    const int64_t item = base + threadIdx.x / G;
-    const bool live = item < items && l.on;
-    const int64_t t = item < items ? item / runs : 0;
-    const int h0 = static_cast<int>(item - t * runs);
-    if (live) angles(s, t, u, l);
+  // Every lane of a warp goes through the same number of items: the sums of a head are over the warp's shuffles. The
+  // item's token and run follow from the last one's, without a division.
+  const int64_t step = int64_t(plan.ctas[kind]) * kGroups;
+  const int64_t step_t = step / runs;
+  const int step_r = static_cast<int>(step - step_t * runs);
+  int64_t item = int64_t(cta) * kGroups + threadIdx.x / G;
+  int64_t t = item / runs;
+  int h0 = static_cast<int>(item - t * runs);
+  for (int64_t base = int64_t(cta) * kGroups; base < items; base += step) {
+    const bool live = item < items && on;
+    const int64_t pos = live && alike ? s.pos[s_axis[RUN * u] * s.T + t] : 0;
+    const T* x = static_cast<const T*>(xv.p) + t * xv.token + h0 * xv.head;
+    const T* g = BACK ? static_cast<const T*>(gv.p) + t * gv.token + h0 * gv.head : nullptr;
+    T* y = static_cast<T*>(yv.p) + t * yv.token + h0 * yv.head;
     for (int j0 = 0; j0 < per; j0 += kAhead) {
-      R xa[kAhead], xb[kAhead], ga[kAhead], gb[kAhead];
+      R xa[kAhead], xb[kAhead], ga[BACK ? kAhead : 1], gb[BACK ? kAhead : 1];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int h = h0 + (j0 + j) * runs;
-        if (live && j0 + j < per && h < all) {
-          const int k = h >= s.heads[0];
-          const int hk = h - (k ? s.heads[0] : 0);
-          const T* x = static_cast<const T*>(c.x[k].p) + t * c.x[k].token + hk * c.x[k].head;
-          xa[j] = *reinterpret_cast<const R*>(x + l.a);
-          xb[j] = *reinterpret_cast<const R*>(x + l.b);
-          if (BACK) {
-            const T* g = static_cast<const T*>(c.dy[k].p) + t * c.dy[k].token + hk * c.dy[k].head;
-            ga[j] = *reinterpret_cast<const R*>(g + l.a);
-            gb[j] = *reinterpret_cast<const R*>(g + l.b);
+        if (live && j0 + j < per && h0 + (j0 + j) * runs < heads) {
+          xa[j] = *reinterpret_cast<const R*>(x + a);
+          xb[j] = *reinterpret_cast<const R*>(x + b);
+          if constexpr (BACK) {
+            ga[j] = *reinterpret_cast<const R*>(g + a);
+            gb[j] = *reinterpret_cast<const R*>(g + b);
           }
         } else {
           xa[j] = xb[j] = R{};
-          if (BACK) ga[j] = gb[j] = R{};
+          if constexpr (BACK) ga[j] = gb[j] = R{};
+        }
+        x += runs * xv.head;
+        if constexpr (BACK) g += runs * gv.head;
+      }
+      if (j0 == 0 && live && turned) {  // while the first heads come
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+          const int64_t at = alike ? pos : s.pos[s_axis[RUN * u + i] * s.T + t];
+          angle<T>(static_cast<uint64_t>(at) * s_turn[RUN * u + i], cos[i], sin[i]);
+          if (BACK) sin[i] = -sin[i];
         }
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int h = h0 + (j0 + j) * runs;
-        const bool mine = live && j0 + j < per && h < all;
-        const int k = h >= s.heads[0];
-        float x[8], y[8];
-        unpack(xa[j], x);
-        unpack(xb[j], x + 4);
-        if (!BACK) {
-          float r = 1.f;
-          if (norm) {
-            float q = 0.f;
+        const bool mine = live && j0 + j < per && h0 + (j0 + j) * runs < heads;
+        float v[N], z[N];
+        unpack<T>(xa[j], v);
+        unpack<T>(xb[j], v + RUN);
+        float r = 1.f;
+        if (norm) {
+          float q = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
-            r = 1.0f / sqrtf(fmaf(group_sum<G>(q), inv_dim, s.eps));
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e] * r * (k ? w[1][e] : w[0][e]);
-          if (l.turned) turn(y, l, s.interleaved, false);
+          for (int e = 0; e < N; ++e) q = fmaf(v[e], v[e], q);
+          r = rsqrtf(fmaf(group_sum<G>(q), inv_dim, s.eps));
+        }
+        if constexpr (BACK) {
+          unpack<T>(ga[j], z);
+          unpack<T>(gb[j], z + RUN);
         } else {
-          unpack(ga[j], y);
-          unpack(gb[j], y + 4);
-          if (l.turned) turn(y, l, s.interleaved, true);
           if (norm) {
-            float q = 0.f, d = 0.f;
+            float w[N];
+            weights<RUN>(s_w, a, b, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              q = fmaf(x[e], x[e], q);
-              d = fmaf(y[e] * (k ? w[1][e] : w[0][e]), x[e], d);
-            }
-            const float root = sqrtf(fmaf(group_sum<G>(q), inv_dim, s.eps));
-            const float r = mine ? 1.0f / root : 0.f;  // a lane without a head adds nothing to dw, even at eps = 0
-            const float m = group_sum<G>(d) * r * inv_dim;  // mean(g * w * n)
+            for (int e = 0; e < N; ++e) z[e] = v[e] * (r * w[e]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float n = x[e] * r;
-              if (k)
-                dw[1][e] = fmaf(y[e], n, dw[1][e]);
-              else
-                dw[0][e] = fmaf(y[e], n, dw[0][e]);
-              y[e] = r * fmaf(-n, m, y[e] * (k ? w[1][e] : w[0][e]));
+            for (int e = 0; e < N; ++e) z[e] = v[e];
+          }
+        }
+        if (turned) {
+          if (s.interleaved) {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) turn_pair(z[2 * i], z[2 * i + 1], cos[i], sin[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) turn_pair(z[i], z[RUN + i], cos[i], sin[i]);
+          }
+        }
+        if constexpr (BACK) {
+          if (norm) {
+            if (!mine) r = 0.f;  // a lane without a head adds nothing to dw, even at eps = 0
+            float d = 0.f, w[N];
+            weights<RUN>(s_w, a, b, w);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              v[e] *= r;
+              dw[e] = fmaf(z[e], v[e], dw[e]);
+              z[e] *= w[e];
+              d = fmaf(z[e], v[e], d);
             }
+            const float m = group_sum<G>(d) * inv_dim;
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] = r * fmaf(-v[e], m, z[e]);
           }
         }
         if (mine) {
-          const int hk = h - (k ? s.heads[0] : 0);
-          T* o = static_cast<T*>(c.y[k].p) + t * c.y[k].token + hk * c.y[k].head;
-          R v;
-          pack(v, y);
-          *reinterpret_cast<R*>(o + l.a) = v;
-          pack(v, y + 4);
-          *reinterpret_cast<R*>(o + l.b) = v;
+          R o;
+          pack<T>(o, z);
+          *reinterpret_cast<R*>(y + a) = o;
+          pack<T>(o, z + RUN);
+          *reinterpret_cast<R*>(y + b) = o;
         }
+        y += runs * yv.head;
       }
     }
+    item += step;
+    t += step_t;
+    h0 += step_r;
+    if (h0 >= runs) h0 -= runs, ++t;
   }
   if constexpr (BACK) {
     if (!norm) return;
     // The groups of a warp, then the CTA's warps, in order.
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int e = 0; e < N; ++e) {
+      float v = dw[e];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float v = dw[k][e];
-#pragma unroll
-        for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (threadIdx.x % 32 < G && l.on) sums[threadIdx.x / 32][k][(e < 4 ? l.a : l.b - 4) + e] = v;
-      }
+      for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (threadIdx.x % 32 < G && on) sums[threadIdx.x / 32][(e < RUN ? a : b - RUN) + e] = v;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * s.dim; i += kThreads) {
-      const int k = i / s.dim, e = i % s.dim;
+    for (int e = threadIdx.x; e < s.dim; e += kThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < kThreads / 32; ++q) v += sums[q][k][e];
-      part[int64_t(blockIdx.x) * 2 * s.dim + i] = v;
+      for (int q = 0; q < kThreads / 32; ++q) v += sums[q][e];
+      part[int64_t(blockIdx.x) * s.dim + e] = v;
     }
   }
 }
 
-// dw[e] = the sum of the CTAs' parts: a CTA per 32 of the 2 dim columns.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int parts, int dim, float* dwq, float* dwk) {
+// dw[e] = the sum of the CTAs' parts: a CTA per 32 columns of a kind.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int ctas_q, int ctas_k, int dim, float* dwq,
+                                                       float* dwk) {
   __shared__ double rows[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const int kind = blockIdx.y, col = blockIdx.x * 32 + lane;
+  const int first = kind ? ctas_q : 0, last = kind ? ctas_q + ctas_k : ctas_q;
   double v = 0.0;
-  if (col < 2 * dim)
-    for (int i = warp; i < parts; i += 32) v += part[int64_t(i) * 2 * dim + col];
+  if (col < dim)
+    for (int i = first + warp; i < last; i += 32) v += part[int64_t(i) * dim + col];
   rows[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && col < 2 * dim) {
+  if (warp == 0 && col < dim) {
     double sum = 0.0;
+#pragma unroll
     for (int i = 0; i < 32; ++i) sum += rows[i][lane];
-    (col < dim ? dwq : dwk)[col < dim ? col : col - dim] = static_cast<float>(sum);
+    (kind ? dwk : dwq)[col] = static_cast<float>(sum);
   }
 }
 
-struct RopePlan {
-  int g, runs, per;
-  int64_t grid;
-};
-
-// How the heads are handed out: a group takes up to 8 heads of a token, fewer
-// where the GPU would not be full (2048 threads an SM).
-RopePlan plan_rope(int64_t T, int heads, int kv_heads, int dim, int backward) {
-  RopePlan p;
-  p.g = dim <= 64 ? 8 : dim <= 128 ? 16 : 32;
-  const int all = heads + kv_heads;
-  const int64_t resident = int64_t(152) * 2048 / p.g;
+// A group takes up to 8 heads of a token, fewer where the GPU would not be full; as many CTAs as run at once, each (of
+// the backward) with a part of dw.
+RopePlan plan_rope(int64_t T, const int (&heads)[2], int dim, int rot, int bf16, int backward) {
+  RopePlan p{};
+  p.run = bf16 && dim % 16 == 0 && rot % 16 == 0 ? 8 : 4;
+  const int lanes = (dim + 2 * p.run - 1) / (2 * p.run);
+  const int most = 32 / (p.run / 4);  // lanes of the longest head
+  p.group = lanes <= most / 4 ? most / 4 : lanes <= most / 2 ? most / 2 : most;
+  const int64_t all = heads[0] + heads[1];
+  const int64_t resident = int64_t(152) * 512 / p.group;
   int64_t per = T * all / resident;
   per = per < 1 ? 1 : per > 8 ? 8 : per;
-  p.runs = static_cast<int>((all + per - 1) / per);
-  p.per = (all + p.runs - 1) / p.runs;
-  const int groups = kThreads / p.g;
-  const int64_t ctas = (T * p.runs + groups - 1) / groups;
-  const int64_t most = backward ? kMaxGrid : 152 * 16;
-  p.grid = ctas < most ? ctas : most;
+  const int groups = kThreads / p.group;
+  for (int k = 0; k < 2; ++k) {
+    p.runs[k] = static_cast<int>((heads[k] + per - 1) / per);
+    p.per[k] = (heads[k] + p.runs[k] - 1) / p.runs[k];
+    const int64_t ctas = (T * p.runs[k] + groups - 1) / groups;
+    int64_t cap = int64_t(152 * (backward ? 2 : 3)) * heads[k] / all;
+    if (cap < 1) cap = 1;
+    p.ctas[k] = static_cast<int>(ctas < cap ? ctas : cap);
+  }
   return p;
 }
 
-template <typename T, int G>
+template <typename T, int RUN, int G>
 cudaError_t launch_rope(const RopeCall& c, const RopePlan& p, cudaStream_t s) {
-  return launch_pdl(c.backward ? rope_kernel<T, G, true> : rope_kernel<T, G, false>, dim3(static_cast<unsigned>(p.grid)),
-                    dim3(kThreads), 0, s, c, p.runs, p.per, static_cast<float*>(c.ws));
+  return launch_pdl(c.backward ? rope_kernel<T, RUN, G, true> : rope_kernel<T, RUN, G, false>,
+                    dim3(static_cast<unsigned>(p.ctas[0] + p.ctas[1])), dim3(kThreads), 0, s, c, p,
+                    static_cast<float*>(c.ws));
+}
+
+template <typename T, int RUN>
+cudaError_t launch_rope(const RopeCall& c, const RopePlan& p, cudaStream_t s) {
+  constexpr int M = 32 / (RUN / 4);
+  return p.group == M / 4   ? launch_rope<T, RUN, M / 4>(c, p, s)
+         : p.group == M / 2 ? launch_rope<T, RUN, M / 2>(c, p, s)
+                            : launch_rope<T, RUN, M>(c, p, s);
 }
 
 }  // namespace
 
 size_t rope_backward_workspace(int64_t T, int heads, int kv_heads, int dim) {
   if (T == 0) return 0;
-  return static_cast<size_t>(plan_rope(T, heads, kv_heads, dim, 1).grid) * 2 * dim * sizeof(float);
+  // The most CTAs of any type and rot.
+  const int h[2] = {heads, kv_heads};
+  int ctas = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const RopePlan p = plan_rope(T, h, dim, 0, bf16, 1);
+    if (p.ctas[0] + p.ctas[1] > ctas) ctas = p.ctas[0] + p.ctas[1];
+  }
+  return static_cast<size_t>(ctas) * dim * sizeof(float);
 }
 
 cudaError_t run_qk_rope(const RopeCall& c, cudaStream_t s) {
@@ -324,17 +381,13 @@ cudaError_t run_qk_rope(const RopeCall& c, cudaStream_t s) {
     }
     return cudaSuccess;
   }
-  const RopePlan p = plan_rope(c.s.T, c.s.heads[0], c.s.heads[1], c.s.dim, c.backward);
-  cudaError_t e;
-  if (c.bf16)
-    e = p.g == 8 ? launch_rope<__nv_bfloat16, 8>(c, p, s) : p.g == 16 ? launch_rope<__nv_bfloat16, 16>(c, p, s)
-                                                                      : launch_rope<__nv_bfloat16, 32>(c, p, s);
-  else
-    e = p.g == 8 ? launch_rope<float, 8>(c, p, s) : p.g == 16 ? launch_rope<float, 16>(c, p, s)
-                                                              : launch_rope<float, 32>(c, p, s);
+  const RopePlan p = plan_rope(c.s.T, c.s.heads, c.s.dim, c.s.rot, c.bf16, c.backward);
+  cudaError_t e = !c.bf16      ? launch_rope<float, 4>(c, p, s)
+                  : p.run == 8 ? launch_rope<__nv_bfloat16, 8>(c, p, s)
+                               : launch_rope<__nv_bfloat16, 4>(c, p, s);
   if (e != cudaSuccess || !c.backward || !norm) return e;
-  return launch_pdl(rope_dw_kernel, dim3((2 * c.s.dim + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(c.ws),
-                    static_cast<int>(p.grid), c.s.dim, c.dw[0], c.dw[1]);
+  return launch_pdl(rope_dw_kernel, dim3((c.s.dim + 31) / 32, 2), dim3(1024), 0, s, static_cast<const float*>(c.ws),
+                    p.ctas[0], p.ctas[1], c.s.dim, c.dw[0], c.dw[1]);
 }
 
 }  // namespace tpmlp
