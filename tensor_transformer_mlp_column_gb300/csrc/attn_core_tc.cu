@@ -25,8 +25,8 @@
 // tokens are cleared in shared memory, so that no value of another sequence, not
 // even a NaN, meets a weight of zero.
 //
-// Warps: 8 for the softmax (warp w reads tensor memory lanes 32 (w % 4) ..), one
-// issuing products, one issuing loads. Every wait is bounded; after a failure
+// Warps: 4 to 16 for the softmax (warp w reads tensor memory lanes 32 (w % 4) ..),
+// one issuing products, one issuing loads. Every wait is bounded; after a failure
 // copies and products in flight are waited for and tensor memory is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,11 +44,6 @@ namespace {
 
 constexpr int kRows = 128;                   // tokens of a tile
 constexpr uint32_t kChunk = kRows * 128;     // 64 elements of its rows
-constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
-constexpr int kTcThreads = (kSoftWarps + 2) * 32;
-constexpr int kRowWarp = kSoftWarps + 2;  // dK, dV: lse and delta of the queries
-constexpr int kDkvThreads = (kSoftWarps + 3) * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -62,6 +57,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// True in one lane of a converged warp. Under a branch on this the compiler knows that a single thread issues the
+// products and keeps their operands in uniform registers; under `lane == 0` each tcgen05.mma cost 130 cycles of issue,
+// with it 60, less than the 64 that a 128 x 128 x 16 product takes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Box of 64 elements x 1 head x 64 tokens.
@@ -152,8 +156,6 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[32]) { tmem_st_32(taddr, v); }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st_16(taddr, v); }
 
 // N = 32 or 64 columns of this warp's lanes.
 template <int N>
@@ -219,6 +221,19 @@ struct Ring {
     for (int i = n > SLOTS ? n - SLOTS : 0; i < n; ++i) wait_drain(full + i % SLOTS, (i / SLOTS) & 1, limit_ns);
   }
 };
+
+// The softmax warps' own barrier.
+template <int THREADS>
+__device__ __forceinline__ void softmax_barrier() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int GROUPS>
+__device__ __forceinline__ float row_sum(const float* s_sum, int row) {
+  float v = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) v += s_sum[g * kRows + row];
+  return v;
+}
 
 // sum + the products of eight bf16 pairs.
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float sum) {
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ring.init();
     mbar_init(q_full, 1);
@@ -349,7 +364,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   int issued = 0;  // fills of the ring (loading warp)
 
   if (warp == kLoad) {
-    if (lane == 0) {
+    if (elect_one()) {
       int tiles = 0;
       for (int a = 0; a < NQ; ++a) tiles += n[a] > 0;
       mbar_arrive_expect_tx(q_full, tiles * C::TILE);
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
     for (int i = 0; i < 2 * n_max; ++i) {
       if (!ring.wait_empty(i, guard)) break;
       if (i + 1 == p.withhold) continue;
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(ring.full + i % C::SLOTS, C::TILE);
         load_tile<DH>(s_ring + (i % C::SLOTS) * C::TILE, i & 1 ? &p.v : &p.k, kv, it.row0 + (i >> 1) * kRows,
                       ring.full + i % C::SLOTS);
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
     bool ok = warp_wait(q_full, 0, guard, kSiteMmaFull) && ring.wait_full(0, guard);
     if (ok) {
       tc_fence_after_sync();
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int a = 0; a < NQ; ++a)
           if (n[a] > 0) {
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
           ok = ok && warp_wait(p_full + a, j & 1, guard, kSiteMmaAcc);
           if (!ok) break;
           tc_fence_after_sync();
-          if (lane == 0) {
+          if (elect_one()) {
             product_tokens<DH, kRows, kRows>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 0);
             if (j + 1 == n[a]) tc_commit(o_done + a);
             if (j + 1 < n[a]) {  // over P, whose product comes first
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
           }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_commit(ring.empty + vn % C::SLOTS);
           if (j + 1 < n_max) tc_commit(ring.empty + kn % C::SLOTS);
         }
@@ -500,11 +515,11 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   }
   __syncthreads();
   if (*abort_flag) {
-    if (warp == kLoad && lane == 0) {
+    if (warp == kLoad && elect_one()) {
       wait_drain(q_full, 0, p.wait_ns);
       ring.drain(issued, p.wait_ns);
     }
-    if (warp == kMma && lane == 0) {
+    if (warp == kMma && elect_one()) {
       tc_commit(drain);
       wait_drain(drain, 0, p.wait_ns);
     }
@@ -526,7 +541,10 @@ struct DqCfg {
   static constexpr uint32_t S = 0, DP = 2 * W, DQ = 3 * W;  // columns: S twice, dP, dQ
   static constexpr uint32_t TMEM = 3 * W + DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
-  static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + 1024 + 256;
+  // Softmax warps: 32 columns each. With two of 64 columns a scheduler, the time of a tile is the latency of their steps.
+  static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;
+  static constexpr int THREADS = (WARPS + 2) * 32;
+  static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + GROUPS * 512 + 256;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -536,17 +554,17 @@ struct DqCfg {
 // is off, and is added to it for the kernel of dK. Rows with a single key tile
 // take their own sum of P dP from the start.
 template <int DH, int W>
-__global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
   using C = DqCfg<DH, W>;
-  constexpr int H = W / 2;  // columns of a thread
+  constexpr int H = C::COLUMNS, kMmaWarp = C::WARPS, kLoadWarp = C::WARPS + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(smem, p.status)) return;
   uint8_t* s_q = smem;
   uint8_t* s_do = s_q + C::TILE;
   uint8_t* s_k = s_do + C::TILE;
   uint8_t* s_v = s_k + C::KS * C::NARROW;
-  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::NARROW);  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_sum + 2 * kRows);
+  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::NARROW);  // [GROUPS][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_sum + C::GROUPS * kRows);
   const Ring<C::KS> ring_k{bars, bars + C::KS};
   bars += 2 * C::KS;
   const Ring<C::VS> ring_v{bars, bars + C::VS};
@@ -560,14 +578,14 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ring_k.init();
     ring_v.init();
     mbar_init(q_full, 1);
     mbar_init(sd_full, 1);
-    mbar_init(dp_read, kSoftWarps);
-    mbar_init(ds_full, kSoftWarps);
+    mbar_init(dp_read, C::WARPS);
+    mbar_init(ds_full, C::WARPS);
     mbar_init(done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -589,7 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
   int issued_k = 0, issued_v = 0;
 
   if (warp == kLoadWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(q_full, 2 * C::TILE);
       load_tile<DH>(s_q, &p.q, it.head, it.row0 + q0, q_full);
       load_tile<DH>(s_do, &p.d_o, it.head, it.row0 + q0, q_full);
@@ -597,14 +615,14 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
     for (int j = 0; j < n; ++j) {
       if (!ring_k.wait_empty(j, guard)) break;
       if (j + 1 != p.withhold) {
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(ring_k.full + j % C::KS, C::NARROW);
           load_tile<DH, W>(s_k + (j % C::KS) * C::NARROW, &p.k, kv, it.row0 + j * W, ring_k.full + j % C::KS);
         }
         issued_k = j + 1;
       }
       if (!ring_v.wait_empty(j, guard)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(ring_v.full + j % C::VS, C::NARROW);
         load_tile<DH, W>(s_v + (j % C::VS) * C::NARROW, &p.v, kv, it.row0 + j * W, ring_v.full + j % C::VS);
       }
@@ -619,11 +637,11 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
         uint8_t* k_tile = s_k + (j % C::KS) * C::NARROW;
         if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
         // S_j over dS_{j-2}, whose product was issued before.
-        if (lane == 0) product_rows<DH, W>(tmem + C::S + (j & 1) * W, s_q, k_tile);
+        if (elect_one()) product_rows<DH, W>(tmem + C::S + (j & 1) * W, s_q, k_tile);
         ok = ring_v.wait_full(j, guard) && (j == 0 || warp_wait(dp_read, (j - 1) & 1, guard, kSiteMmaAcc));
         if (!ok) break;
         tc_fence_after_sync();
-        if (lane == 0) {
+        if (elect_one()) {
           product_rows<DH, W>(tmem + C::DP, s_do, s_v + (j % C::VS) * C::NARROW);
           tc_commit(sd_full);
           tc_commit(ring_v.empty + j % C::VS);
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
         ok = warp_wait(ds_full, (j - 1) & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
-        if (lane == 0) {
+        if (elect_one()) {
           product_tokens<DH, W, H>(tmem + C::DQ, tmem + C::S + ((j - 1) & 1) * W, s_k + ((j - 1) % C::KS) * C::NARROW, j > 1, H);
           tc_commit(ring_k.empty + (j - 1) % C::KS);
           if (j == n) tc_commit(done);
@@ -643,7 +661,7 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
       }
     }
   } else {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int qi = q0 + row;
     const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
@@ -651,32 +669,33 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
     float delta = 0.f;
     bool ok = true;
     if (n > 1) {
-      // delta of 16 rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
-      uint4 o[DH / 16];
+      // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
+      constexpr int R = kRows / C::WARPS / 4, N = R * (DH / 64);
+      uint4 o[N];
 #pragma unroll
-      for (int x = 0; x < DH / 16; ++x) {
-        const int r = warp * 16 + (x & 3) * 4 + (lane >> 3), e = (x >> 2) * 64 + (lane & 7) * 8;
+      for (int x = 0; x < N; ++x) {
+        const int r = (warp * R + x % R) * 4 + (lane >> 3), e = (x / R) * 64 + (lane & 7) * 8;
         o[x] = make_uint4(0, 0, 0, 0);
         if (q0 + r < it.len && e < p.s.dim)
           o[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o.p) + (it.row0 + q0 + r) * p.o.token +
                                                  it.head * p.o.head + e);
       }
       ok = warp_wait(q_full, 0, guard, kSiteMmaFull);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      float sum[R];
 #pragma unroll
-      for (int x = 0; x < DH / 16; ++x) {
-        const int r = warp * 16 + (x & 3) * 4 + (lane >> 3);
-        const uint4 g = *reinterpret_cast<const uint4*>(s_do + (x >> 2) * kChunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-        part[x & 3] = dot8(o[x], g, part[x & 3]);
+      for (int x = 0; x < N; ++x) {
+        const int r = (warp * R + x % R) * 4 + (lane >> 3);
+        const uint4 g = *reinterpret_cast<const uint4*>(s_do + (x / R) * kChunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        sum[x % R] = dot8(o[x], g, x < R ? 0.f : sum[x % R]);
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        part[x] += __shfl_xor_sync(kAll, part[x], 4);
-        part[x] += __shfl_xor_sync(kAll, part[x], 2);
-        part[x] += __shfl_xor_sync(kAll, part[x], 1);
-        if ((lane & 7) == 0) s_sum[warp * 16 + x * 4 + (lane >> 3)] = part[x];
+      for (int x = 0; x < R; ++x) {
+        sum[x] += __shfl_xor_sync(kAll, sum[x], 4);
+        sum[x] += __shfl_xor_sync(kAll, sum[x], 2);
+        sum[x] += __shfl_xor_sync(kAll, sum[x], 1);
+        if ((lane & 7) == 0) s_sum[(warp * R + x) * 4 + (lane >> 3)] = sum[x];
       }
-      asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+      softmax_barrier<C::WARPS * 32>();
       // The sums of dS go there no sooner than every warp has read dP of the first tile, which is after this.
       delta = s_sum[row];
     }
@@ -684,13 +703,13 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
     for (int j = 0; j < n; ++j) {
       ok = ok && warp_wait(sd_full, j & 1, guard, kSiteMmaFull);
       if (!ok) {
-        if (n == 1) asm volatile("barrier.cta.sync 1, 256;" ::: "memory");  // the others may stand at it
+        if (n == 1) softmax_barrier<C::WARPS * 32>();  // the others may stand at it
         break;
       }
       tc_fence_after_sync();
-      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * W + H * half;
+      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * W + H * part;
       float s[H], dp[H];
-      tmem_ld<H>(tmem + lanes + C::DP + H * half, dp);
+      tmem_ld<H>(tmem + lanes + C::DP + H * part, dp);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(dp_read);
@@ -704,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
         s[e + 1] = exp2_fast(s[e + 1]);
       }
       if (k0 + W > it.len || (p.s.causal && k0 + W > q0)) {
-        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * half;
+        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;
 #pragma unroll
         for (int e = 0; e < H; ++e) {
           s[e] = e < end ? s[e] : 0.f;
@@ -715,9 +734,9 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < H; ++e) sum = fmaf(s[e], dp[e], sum);
-        s_sum[half * kRows + row] = sum;
-        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
-        delta = s_sum[row] + s_sum[kRows + row];
+        s_sum[part * kRows + row] = sum;
+        softmax_barrier<C::WARPS * 32>();
+        delta = row_sum<C::GROUPS>(s_sum, row);
       }
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
       const uint64_t d2 = pair(-delta, -delta);
@@ -730,7 +749,7 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
         unpair(ds, x0, x1);
         w[e / 2] = pack_bf16(x0, x1);
       }
-      tmem_st(t_s, w);
+      tmem_st_16(t_s, w);
       float x0, x1;
       unpair(add_pair(sum[0], sum[1]), x0, x1);
       total += x0 + x1;
@@ -740,15 +759,15 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
       if (lane == 0) mbar_arrive(ds_full);
     }
     // All softmax warps come here alike: a failed wait ends in the same barrier.
-    if (n > 1) s_sum[half * kRows + row] = total;
-    asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+    if (n > 1) s_sum[part * kRows + row] = total;
+    softmax_barrier<C::WARPS * 32>();
     ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
     if (ok) {
       tc_fence_after_sync();
-      if (half == 0 && qi < it.len) p.delta[at] = n > 1 ? delta + (s_sum[row] + s_sum[kRows + row]) : delta;
+      if (part == 0 && qi < it.len) p.delta[at] = n > 1 ? delta + row_sum<C::GROUPS>(s_sum, row) : delta;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
 #pragma unroll 1
-      for (int x = half * (DH / 2); x < (half + 1) * (DH / 2); x += 32) {
+      for (int x = part * 32; x < DH; x += C::GROUPS * 32) {
         float o[32];
         tmem_ld_32cols(tmem + lanes + C::DQ + x, o);
         if (qi < it.len) store_row(dst, o, p.s.scale, x, p.s.dim);
@@ -757,12 +776,12 @@ __global__ void __launch_bounds__(kTcThreads, DqCfg<DH, W>::CTAS) dq_kernel(cons
   }
   __syncthreads();
   if (*abort_flag) {
-    if (warp == kLoadWarp && lane == 0) {
+    if (warp == kLoadWarp && elect_one()) {
       wait_drain(q_full, 0, p.wait_ns);
       ring_k.drain(issued_k, p.wait_ns);
       ring_v.drain(issued_v, p.wait_ns);
     }
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp && elect_one()) {
       tc_commit(drain);
       wait_drain(drain, 0, p.wait_ns);
     }
@@ -784,6 +803,8 @@ struct DkvCfg {
   static constexpr uint32_t S = 0, DP = W, DV = 2 * W, DK = 2 * W + DH;
   static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
+  static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;  // softmax warps, as in dQ
+  static constexpr int THREADS = (WARPS + 3) * 32;
   static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + 256;
   static_assert(SMEM <= 227 * 1024 && CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
@@ -792,9 +813,11 @@ struct DkvCfg {
 // made while the threads work on dS of tile i, its dP while they work on P of
 // tile i + 1.
 template <int DH, int W>
-__global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
+    dkv_kernel(const __grid_constant__ TcParams p) {
   using C = DkvCfg<DH, W>;
-  constexpr int H = W / 2;  // columns of a thread
+  constexpr int H = C::COLUMNS, kMmaWarp = C::WARPS, kLoadWarp = C::WARPS + 1;
+  constexpr int kRowWarp = C::WARPS + 2;  // lse and delta of the queries
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(smem, p.status)) return;
   uint8_t* s_k = smem;
@@ -819,16 +842,16 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ring_q.init();
     ring_d.init();
-    ring_r.init(32, kSoftWarps);
+    ring_r.init(32, C::WARPS);
     mbar_init(kv_full, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_full, kSoftWarps);
+    mbar_init(p_full, C::WARPS);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, kSoftWarps);
+    mbar_init(ds_full, C::WARPS);
     mbar_init(done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -846,102 +869,107 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
   const uint32_t tmem = *tmem_slot;
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
-  // Query tiles first .. last of every head of the group; pass i is head i / per, tile first + i % per.
+  // Query tiles first .. last of every head of the group, head by head.
   const int first = p.s.causal ? k0 / W : 0;
   const int per = (it.len + W - 1) / W - first;
   const int n = per * group;
   int issued_q = 0, issued_d = 0;
 
   if (warp == kLoadWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
       load_tile<DH>(s_k, &p.k, it.head, it.row0 + k0, kv_full);
       load_tile<DH>(s_v, &p.v, it.head, it.row0 + k0, kv_full);
     }
+    int h = it.head * group, x = 0;  // head and query tile of pass i
     for (int i = 0; i < n; ++i) {
-      const int h = it.head * group + i / per;
-      const int64_t row = it.row0 + (first + i % per) * W;
+      const int64_t row = it.row0 + (first + x) * W;
       if (!ring_q.wait_empty(i, guard)) break;
       if (i + 1 != p.withhold) {
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(ring_q.full + i % C::QS, C::NARROW);
           load_tile<DH, W>(s_q + (i % C::QS) * C::NARROW, &p.q, h, row, ring_q.full + i % C::QS);
         }
         issued_q = i + 1;
       }
       if (!ring_d.wait_empty(i, guard)) break;
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(ring_d.full + i % C::DS, C::NARROW);
         load_tile<DH, W>(s_do + (i % C::DS) * C::NARROW, &p.d_o, h, row, ring_d.full + i % C::DS);
       }
       issued_d = i + 1;
+      if (++x == per) x = 0, ++h;
     }
   } else if (warp == kRowWarp) {
     // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them.
+    int h = it.head * group, x = 0;
     for (int i = 0; i < n; ++i) {
-      const int h = it.head * group + i / per, q0 = (first + i % per) * W;
+      const int q0 = (first + x) * W;
       const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
       float nl[W / 32], nd[W / 32];
 #pragma unroll
-      for (int x = 0; x < W / 32; ++x) {
-        const int r = x * 32 + lane;
+      for (int y = 0; y < W / 32; ++y) {
+        const int r = y * 32 + lane;
         const bool on = q0 + r < it.len;
-        nl[x] = on ? -p.lse[at + r] * kLog2e : 0.f;
-        nd[x] = on ? -p.delta[at + r] : 0.f;
+        nl[y] = on ? -p.lse[at + r] * kLog2e : 0.f;
+        nd[y] = on ? -p.delta[at + r] : 0.f;
       }
       if (!ring_r.wait_empty(i, guard)) break;
       float* rows = s_row + (i % C::RS) * 2 * W;
 #pragma unroll
-      for (int x = 0; x < W / 32; ++x) {
-        rows[x * 32 + lane] = nl[x];
-        rows[W + x * 32 + lane] = nd[x];
+      for (int y = 0; y < W / 32; ++y) {
+        rows[y * 32 + lane] = nl[y];
+        rows[W + y * 32 + lane] = nd[y];
       }
       mbar_arrive(ring_r.full + i % C::RS);
+      if (++x == per) x = 0, ++h;
     }
   } else if (warp == kMmaWarp) {
-    // Tile i of a ring, its rows of the next sequence cleared.
-    auto take_q = [&](int i) {
+    // Tile i of a ring (query tile x), its rows of the next sequence cleared.
+    auto take_q = [&](int i, int x) {
       if (!ring_q.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + i % per) * W;
+      const int rows = it.len - (first + x) * W;
       if (rows < W) clear_rows<DH, W>(s_q + (i % C::QS) * C::NARROW, rows, lane);
       return true;
     };
-    auto take_d = [&](int i) {
+    auto take_d = [&](int i, int x) {
       if (!ring_d.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + i % per) * W;
+      const int rows = it.len - (first + x) * W;
       if (rows < W) clear_rows<DH, W>(s_do + (i % C::DS) * C::NARROW, rows, lane);
       return true;
     };
-    bool ok = warp_wait(kv_full, 0, guard, kSiteMmaFull) && take_q(0);
+    bool ok = warp_wait(kv_full, 0, guard, kSiteMmaFull) && take_q(0, 0);
     if (ok) {
-      if (lane == 0) {
+      if (elect_one()) {
         product_rows<DH, W>(tmem + C::S, s_k, s_q);
         tc_commit(s_full);
       }
       __syncwarp();
-      ok = take_d(0);
+      ok = take_d(0, 0);
     }
     if (ok) {
-      if (lane == 0) {
+      if (elect_one()) {
         product_rows<DH, W>(tmem + C::DP, s_v, s_do);
         tc_commit(dp_full);
       }
       __syncwarp();
+      int x = 0;  // query tile of pass i + 1
       for (int i = 0; i < n; ++i) {
+        if (++x == per) x = 0;
         const uint8_t* d_tile = s_do + (i % C::DS) * C::NARROW;
         const uint8_t* q_tile = s_q + (i % C::QS) * C::NARROW;
         ok = warp_wait(p_full, i & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
-        if (lane == 0) {
+        if (elect_one()) {
           product_tokens<DH, W, H>(tmem + C::DV, tmem + C::S, d_tile, i > 0, H);
           tc_commit(ring_d.empty + i % C::DS);
         }
         __syncwarp();
         if (i + 1 < n) {
-          ok = take_q(i + 1);
+          ok = take_q(i + 1, x);
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             product_rows<DH, W>(tmem + C::S, s_k, s_q + ((i + 1) % C::QS) * C::NARROW);
             tc_commit(s_full);
           }
@@ -950,16 +978,16 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
         ok = warp_wait(ds_full, i & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
-        if (lane == 0) {
+        if (elect_one()) {
           product_tokens<DH, W, H>(tmem + C::DK, tmem + C::DP, q_tile, i > 0, H);
           tc_commit(ring_q.empty + i % C::QS);
           if (i + 1 == n) tc_commit(done);
         }
         __syncwarp();
         if (i + 1 < n) {
-          ok = take_d(i + 1);
+          ok = take_d(i + 1, x);
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((i + 1) % C::DS) * C::NARROW);
             tc_commit(dp_full);
           }
@@ -968,14 +996,16 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
       }
     }
   } else {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + C::S + H * half, t_dp = tmem + lanes + C::DP + H * half;
+    const uint32_t t_s = tmem + lanes + C::S + H * part, t_dp = tmem + lanes + C::DP + H * part;
     const int kj = k0 + row;
     bool ok = true;
+    int x = 0;
     for (int i = 0; i < n; ++i) {
-      const int q0 = (first + i % per) * W + H * half;  // of this warp's columns
-      const float* rows = s_row + (i % C::RS) * 2 * W + H * half;
+      const int q0 = (first + x) * W + H * part;  // of this warp's columns
+      if (++x == per) x = 0;
+      const float* rows = s_row + (i % C::RS) * 2 * W + H * part;
       ok = ring_r.wait_full(i, guard) && warp_wait(s_full, i & 1, guard, kSiteMmaFull);
       if (!ok) break;
       tc_fence_after_sync();
@@ -999,7 +1029,7 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
       uint32_t w[H / 2];
 #pragma unroll
       for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
-      tmem_st(t_s, w);
+      tmem_st_16(t_s, w);
       tmem_wait_st();
       tc_fence_before_sync();
       __syncwarp();
@@ -1022,7 +1052,7 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
         w[e / 2] = pack_bf16(x0, x1);
         w[e / 2 + 1] = pack_bf16(x2, x3);
       }
-      tmem_st(t_dp, w);
+      tmem_st_16(t_dp, w);
       tmem_wait_st();
       tc_fence_before_sync();
       __syncwarp();
@@ -1037,7 +1067,7 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
       __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + (it.row0 + kj) * p.dv.token + it.head * p.dv.head;
       __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + (it.row0 + kj) * p.dk.token + it.head * p.dk.head;
 #pragma unroll 1
-      for (int x = half * (DH / 2); x < (half + 1) * (DH / 2); x += 32) {
+      for (int x = part * 32; x < DH; x += C::GROUPS * 32) {
         float o[32];
         tmem_ld_32cols(tmem + lanes + C::DV + x, o);
         if (kj < it.len) store_row(dv, o, 1.f, x, p.s.dim);
@@ -1048,12 +1078,12 @@ __global__ void __launch_bounds__(kDkvThreads, DkvCfg<DH, W>::CTAS) dkv_kernel(c
   }
   __syncthreads();
   if (*abort_flag) {
-    if (warp == kLoadWarp && lane == 0) {
+    if (warp == kLoadWarp && elect_one()) {
       wait_drain(kv_full, 0, p.wait_ns);
       ring_q.drain(issued_q, p.wait_ns);
       ring_d.drain(issued_d, p.wait_ns);
     }
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp && elect_one()) {
       tc_commit(drain);
       wait_drain(drain, 0, p.wait_ns);
     }
@@ -1119,6 +1149,17 @@ cudaError_t launch_fwd(TcParams& p, cudaStream_t s) {
   return launch<fwd_kernel<DH, NQ>>(p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, s);
 }
 
+template <int DH, int W>
+cudaError_t launch_dq(TcParams& p, cudaStream_t s) {
+  using C = DqCfg<DH, W>;
+  return launch<dq_kernel<DH, W>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, s);
+}
+template <int DH, int W>
+cudaError_t launch_dkv(TcParams& p, cudaStream_t s) {
+  using C = DkvCfg<DH, W>;
+  return launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads, C::THREADS, C::SMEM, s);
+}
+
 }  // namespace
 
 cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t s) {
@@ -1141,13 +1182,11 @@ cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStr
   const bool small = c.s.dim <= 64;
   {
     TraceScope trace("attn_core_dq", s);
-    e = small ? launch<dq_kernel<64, 64>>(p, kRows, c.s.heads, kTcThreads, DqCfg<64, 64>::SMEM, s)
-              : launch<dq_kernel<128, 128>>(p, kRows, c.s.heads, kTcThreads, DqCfg<128, 128>::SMEM, s);
+    e = small ? launch_dq<64, 64>(p, s) : launch_dq<128, 128>(p, s);
   }
   if (e != cudaSuccess) return e;
   TraceScope trace("attn_core_dkv", s);
-  return small ? launch<dkv_kernel<64, 64>>(p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<64, 64>::SMEM, s)
-               : launch<dkv_kernel<128, 128>>(p, kRows, c.s.kv_heads, kDkvThreads, DkvCfg<128, 128>::SMEM, s);
+  return small ? launch_dkv<64, 64>(p, s) : launch_dkv<128, 128>(p, s);
 }
 
 }  // namespace tpmlp
