@@ -2,13 +2,13 @@
 // backward pass on the tensor cores (bf16, head sizes up to 128; the formulas
 // stand in attn_core.cu).
 //
-// Three kernels, tiles of 128 tokens, head sizes padded to DH = 64 or 128 by
+// Three persistent kernels, tiles of 128 tokens, head sizes padded to DH = 64 or 128 by
 // TMA's zero fill:
-//   forward  a CTA per NQ query tiles of one head: S = Q K^T, P = exp(S - max),
+//   forward  items of NQ query tiles of one head: S = Q K^T, P = exp(S - max),
 //            O += P V, with a running maximum and sum for each row.
-//   dQ       a CTA per query tile: S = Q K^T, dP = dO V^T, dS = P (dP - delta),
+//   dQ       items of a query tile: S = Q K^T, dP = dO V^T, dS = P (dP - delta),
 //            dQ += dS K.
-//   dK, dV   a CTA per key tile of a kv head, over the query tiles of all heads
+//   dK, dV   items of a key tile of a kv head, over the query tiles of all heads
 //            that share it: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 // Making S and dP twice costs 7 products in the place of 5, but every sum has
 // one owner: no atomics, no order that changes, no fp32 dQ in memory.
@@ -222,11 +222,7 @@ struct Ring {
   }
 };
 
-// The softmax warps' own barrier.
-template <int THREADS>
-__device__ __forceinline__ void softmax_barrier() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
+// A row's sums of all groups of columns.
 template <int GROUPS>
 __device__ __forceinline__ float row_sum(const float* s_sum, int row) {
   float v = 0.f;
@@ -263,28 +259,33 @@ struct TcParams {
   float* lse;    // forward: written; backward: read
   float* delta;  // backward
   float scale_log2;
-  int tiles;     // tiles (forward: runs of NQ tiles) of the longest sequence
-  int withhold;  // test hook: > 0: that load of the CTA's first ring is not issued
+  int tiles;       // tiles (forward: runs of NQ tiles) of the longest sequence
+  uint32_t items;  // tiles x heads x sequences
+  int withhold;    // test hook: > 0: that load of the CTA's first ring is not issued
   uint64_t wait_ns;
   int* status;
 };
 
 // What a CTA works on. Items of one tile index follow one another, those with
-// the most work first.
+// the most work first, and a CTA takes one of every gridDim.x, from the front and
+// from the back in turn, so that all get about the same work.
 struct Item {
   int tile, head, len;
   int64_t row0;
 };
-__device__ __forceinline__ Item item_of(const TcParams& p, int heads, bool last_first) {
-  Item it;
-  const int64_t per = int64_t(heads) * p.s.batch;
-  const int64_t i = blockIdx.x;
+__device__ __forceinline__ bool item_of(const TcParams& p, int round, int heads, bool last_first, Item& it) {
+  const uint32_t g = gridDim.x, place = round & 1 ? g - 1 - blockIdx.x : blockIdx.x;
+  const uint64_t at = uint64_t(round) * g + place;
+  if (at >= p.items) return false;
+  const uint32_t i = static_cast<uint32_t>(at), per = static_cast<uint32_t>(heads) * p.s.batch, in = i % per;
   it.tile = static_cast<int>(i / per);
   if (last_first) it.tile = p.tiles - 1 - it.tile;
-  it.head = static_cast<int>(i % per % heads);
-  it.len = core_sequence(p.s, static_cast<int>(i % per / heads), it.row0, p.status);
-  return it;
+  it.head = static_cast<int>(in % heads);
+  it.len = core_sequence(p.s, static_cast<int>(in / heads), it.row0, p.status);
+  return true;
 }
+// The rounds of this CTA.
+__device__ __forceinline__ int rounds_of(const TcParams& p) { return static_cast<int>((p.items + gridDim.x - 1) / gridDim.x); }
 
 // Shared memory of a kernel: tiles, then rows of floats, then barriers. There is no slack to align it in: the dynamic
 // shared memory begins on a multiple of 1024 bytes, which the swizzled tiles need, and which is checked.
@@ -303,13 +304,18 @@ struct FwdCfg {
   static constexpr uint32_t TMEM = NQ == 2 ? 512 : 256;
   static constexpr int CTAS = NQ == 1 && DH == 64 ? 2 : 1;  // an SM's
   static constexpr uint32_t O = NQ * 128;  // columns: S of each tile, then O of each
-  static constexpr size_t SMEM = (NQ + SLOTS) * TILE + 256;
+  static constexpr size_t BARS = 8 * (2 * SLOTS + 3 + 3 * NQ + 1);  // barriers; the last place holds two words
+  static constexpr size_t SMEM = (NQ + SLOTS) * TILE + BARS;
   static constexpr int THREADS = (4 * NQ + 2) * 32;
   static_assert(O + NQ * DH <= TMEM, "tensor memory");
 };
 
 // The row's maximum so far, raised where the tile's is above it by more than
 // 2^8 in weight: until then weights stay below 2^8 and O needs no factor.
+//
+// Two query tiles take turns: one's products run while the other is in the
+// softmax. An item's Q is fetched once the last item's scores are made, under its
+// last softmax, product and output.
 template <int DH, int NQ>
 __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS) fwd_kernel(const __grid_constant__ TcParams p) {
   using C = FwdCfg<DH, NQ>;
@@ -321,9 +327,10 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ring + C::SLOTS * C::TILE);
   const Ring<C::SLOTS> ring{bars, bars + C::SLOTS};
   uint64_t* q_full = bars + 2 * C::SLOTS;
-  uint64_t* s_full = q_full + 1;   // [NQ] scores of a tile are there
+  uint64_t* q_free = q_full + 1;   // the item's scores are all made
+  uint64_t* s_full = q_free + 1;   // [NQ] scores of a tile are there
   uint64_t* p_full = s_full + NQ;  // [NQ] its probabilities are there, and O has the new maximum
-  uint64_t* o_done = p_full + NQ;  // [NQ]
+  uint64_t* o_done = p_full + NQ;  // [NQ] an item's O is there
   uint64_t* drain = o_done + NQ;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -332,6 +339,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   if (threadIdx.x == 0) {
     ring.init();
     mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
     for (int a = 0; a < NQ; ++a) {
       mbar_init(s_full + a, 1);
       mbar_init(p_full + a, 4);
@@ -341,69 +349,95 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  const Item it = item_of(p, p.s.heads, p.s.causal);
-  const int q0 = it.tile * NQ * kRows;
-  if (q0 >= it.len) return;  // every thread, before tensor memory is taken
   if (warp == kMma) tmem_alloc(tmem_slot, C::TMEM);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int kv = it.head / (p.s.heads / p.s.kv_heads);
-  // Key tiles of each query tile.
-  int n[NQ], n_max = 0;
+  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  // Key tiles of the item's query tile a.
+  auto tiles_of = [&](const Item& it, int a) {
+    const int first = (it.tile * NQ + a) * kRows;
+    return first >= it.len ? 0 : ((p.s.causal ? min(it.len, first + kRows) : it.len) + kRows - 1) / kRows;
+  };
+  // Of any of them: causal, the last one that there is has the most.
+  auto most_of = [&](const Item& it) {
+    int n = tiles_of(it, 0);
 #pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    const int first = q0 + a * kRows;
-    n[a] = first >= it.len ? 0 : (p.s.causal ? min(it.len, first + kRows) + kRows - 1 : it.len + kRows - 1) / kRows;
-    n_max = max(n_max, n[a]);
-  }
-  int issued = 0;  // fills of the ring (loading warp)
+    for (int a = 1; a < NQ; ++a) n = max(n, tiles_of(it, a));
+    return n;
+  };
+  int issued = 0, items = 0;  // fills of the ring; items with work
 
   if (warp == kLoad) {
-    if (elect_one()) {
-      int tiles = 0;
-      for (int a = 0; a < NQ; ++a) tiles += n[a] > 0;
-      mbar_arrive_expect_tx(q_full, tiles * C::TILE);
-      for (int a = 0; a < tiles; ++a) load_tile<DH>(s_q + a * C::TILE, &p.q, it.head, it.row0 + q0 + a * kRows, q_full);
-    }
-    for (int i = 0; i < 2 * n_max; ++i) {
-      if (!ring.wait_empty(i, guard)) break;
-      if (i + 1 == p.withhold) continue;
+    bool ok = true;
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      const int n = most_of(it), kv = it.head / group;
+      if (n == 0) continue;
+      ok = items == 0 || warp_wait(q_free, (items - 1) & 1, guard, kSiteProducer);
+      if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(ring.full + i % C::SLOTS, C::TILE);
-        load_tile<DH>(s_ring + (i % C::SLOTS) * C::TILE, i & 1 ? &p.v : &p.k, kv, it.row0 + (i >> 1) * kRows,
-                      ring.full + i % C::SLOTS);
+        int tiles = 0;
+        for (int a = 0; a < NQ; ++a) tiles += tiles_of(it, a) > 0;
+        mbar_arrive_expect_tx(q_full, tiles * C::TILE);
+        for (int a = 0; a < tiles; ++a)
+          load_tile<DH>(s_q + a * C::TILE, &p.q, it.head, it.row0 + (it.tile * NQ + a) * kRows, q_full);
       }
-      issued = i + 1;
+      ++items;
+      for (int i = 0; i < 2 * n; ++i) {
+        ok = ring.wait_empty(issued, guard);
+        if (!ok) break;
+        if (issued + 1 != p.withhold && elect_one()) {
+          mbar_arrive_expect_tx(ring.full + issued % C::SLOTS, C::TILE);
+          load_tile<DH>(s_ring + (issued % C::SLOTS) * C::TILE, i & 1 ? &p.v : &p.k, kv, it.row0 + (i >> 1) * kRows,
+                        ring.full + issued % C::SLOTS);
+        }
+        ++issued;
+      }
     }
   } else if (warp == kMma) {
-    bool ok = warp_wait(q_full, 0, guard, kSiteMmaFull) && ring.wait_full(0, guard);
-    if (ok) {
-      tc_fence_after_sync();
+    bool ok = true;
+    int at = 0;            // ring position of the item's first key tile
+    int done[NQ] = {};     // tiles of each query tile so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      int n[NQ], n_max = 0;
+#pragma unroll
+      for (int a = 0; a < NQ; ++a) n[a] = tiles_of(it, a), n_max = max(n_max, n[a]);
+      if (n_max == 0) continue;
+      ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull) && ring.wait_full(at, guard);
+      if (!ok) break;
+      ++items;
       if (elect_one()) {
 #pragma unroll
         for (int a = 0; a < NQ; ++a)
           if (n[a] > 0) {
-            product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, s_ring);
+            product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, s_ring + (at % C::SLOTS) * C::TILE);
             tc_commit(s_full + a);
           }
-        tc_commit(ring.empty);
+        tc_commit(ring.empty + at % C::SLOTS);
+        if (n_max == 1) tc_commit(q_free);
       }
+      __syncwarp();
       for (int j = 0; j < n_max; ++j) {
-        const int kn = 2 * j + 2, vn = 2 * j + 1;
+        const int vn = at + 2 * j + 1, kn = vn + 1;
         uint8_t* v_tile = s_ring + (vn % C::SLOTS) * C::TILE;
         const uint8_t* k_next = s_ring + (kn % C::SLOTS) * C::TILE;
-        if (!ring.wait_full(vn, guard)) break;
+        ok = ring.wait_full(vn, guard);
+        if (!ok) break;
         if (it.len - j * kRows < kRows) clear_rows<DH>(v_tile, it.len - j * kRows, lane);
-        if (j + 1 < n_max && !ring.wait_full(kn, guard)) break;
+        ok = j + 1 >= n_max || ring.wait_full(kn, guard);
+        if (!ok) break;
 #pragma unroll
         for (int a = 0; a < NQ; ++a) {
           if (j >= n[a]) continue;
-          ok = ok && warp_wait(p_full + a, j & 1, guard, kSiteMmaAcc);
+          ok = ok && warp_wait(p_full + a, (done[a] + j) & 1, guard, kSiteMmaAcc);
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
@@ -414,93 +448,95 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
               tc_commit(s_full + a);
             }
           }
+          __syncwarp();
         }
         if (!ok) break;
         if (elect_one()) {
           tc_commit(ring.empty + vn % C::SLOTS);
           if (j + 1 < n_max) tc_commit(ring.empty + kn % C::SLOTS);
+          if (j + 2 == n_max) tc_commit(q_free);
         }
         __syncwarp();
       }
+      at += 2 * n_max;
+#pragma unroll
+      for (int a = 0; a < NQ; ++a) done[a] += n[a];
     }
   } else {
     const int a = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + a * 128, t_o = tmem + lanes + C::O + a * DH;
-    const int first = q0 + a * kRows, tiles = n[a];
-    const int qi = first + row;
     const float c = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
-      ok = warp_wait(s_full + a, j & 1, guard, kSiteMmaFull);
-      if (!ok) break;
-      tc_fence_after_sync();
-      float s[128];
-      {
-        uint32_t r[4][32];
+    int done = 0;  // tiles so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      const int tiles = tiles_of(it, a), first = (it.tile * NQ + a) * kRows, qi = first + row;
+      if (tiles == 0) continue;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        ok = warp_wait(s_full + a, (done + j) & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after_sync();
+        float s[128];
+        tmem_ld<128>(t_s, s);
+        const int k0 = j * kRows;
+        if (k0 + kRows > it.len || (p.s.causal && k0 + kRows > first)) {
+          const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0;  // columns that count
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld_32cols_issue(t_s + 32 * x, r[x]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          tmem_ld_wait(r[x]);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[32 * x + e] = __uint_as_float(r[x][e]);
+          for (int e = 0; e < 128; ++e) s[e] = e < end ? s[e] : -INFINITY;
         }
-      }
-      const int k0 = j * kRows;
-      if (k0 + kRows > it.len || (p.s.causal && k0 + kRows > first)) {
-        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0;  // columns that count
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; ++e) s[e] = e < end ? s[e] : -INFINITY;
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 128; e += 2)
-        asm("max.f32 %0, %0, %1, %2;" : "+f"(m4[(e >> 1) & 3]) : "f"(s[e]), "f"(s[e + 1]));
-      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      const float m_new = (top - m) * c > 8.f ? top : m;  // at a row's first finite score: top
-      const float alpha = m_new == m ? 1.f : exp2_fast((m - m_new) * c);
-      const float base = m_new == -INFINITY ? 0.f : m_new * c;  // no score above -inf yet: weights of zero, not NaN
-      m = m_new;
-      if (j > 0 && __any_sync(kAll, alpha != 1.f)) {
-        // The scores' arrival came after the previous product's end: O holds still.
+        for (int e = 0; e < 128; e += 2)
+          asm("max.f32 %0, %0, %1, %2;" : "+f"(m4[(e >> 1) & 3]) : "f"(s[e]), "f"(s[e + 1]));
+        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float m_new = (top - m) * c > 8.f ? top : m;  // at a row's first finite score: top
+        const float alpha = m_new == m ? 1.f : exp2_fast((m - m_new) * c);
+        const float base = m_new == -INFINITY ? 0.f : m_new * c;  // no score above -inf yet: weights of zero, not NaN
+        m = m_new;
+        if (j > 0 && __any_sync(kAll, alpha != 1.f)) {
+          // The scores' arrival came after the previous product's end: O holds still.
 #pragma unroll 1
-        for (int x = 0; x < DH; x += 32) {
-          float o[32];
+          for (int x = 0; x < DH; x += 32) {
+            float o[32];
+            uint32_t w[32];
+            tmem_ld_32cols(t_o + x, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
+            tmem_st_32(t_o + x, w);
+          }
+        }
+        const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
           uint32_t w[32];
-          tmem_ld_32cols(t_o + x, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha);
-          tmem_st_32(t_o + x, w);
+          for (int e = 0; e < 64; e += 2) {
+            float e0, e1;
+            unpair(fma_pair(pair(s[64 * x + e], s[64 * x + e + 1]), c2, b2), e0, e1);
+            e0 = exp2_fast(e0);
+            e1 = exp2_fast(e1);
+            sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], pair(e0, e1));
+            w[e / 2] = pack_bf16(e0, e1);
+          }
+          tmem_st_32(t_s + 32 * x, w);
         }
+        float x0, x1;
+        unpair(add_pair(sum[0], sum[1]), x0, x1);
+        l = l * alpha + (x0 + x1);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + a);
       }
-      const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
-      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float e0, e1;
-          unpair(fma_pair(pair(s[64 * x + e], s[64 * x + e + 1]), c2, b2), e0, e1);
-          e0 = exp2_fast(e0);
-          e1 = exp2_fast(e1);
-          sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], pair(e0, e1));
-          w[e / 2] = pack_bf16(e0, e1);
-        }
-        tmem_st_32(t_s + 32 * x, w);
-      }
-      float x0, x1;
-      unpair(add_pair(sum[0], sum[1]), x0, x1);
-      l = l * alpha + (x0 + x1);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + a);
-    }
-    ok = ok && tiles > 0 && warp_wait(o_done + a, 0, guard, kSiteEpilogue);
-    if (ok) {
+      if (!ok) break;
+      done += tiles;
+      ok = warp_wait(o_done + a, items & 1, guard, kSiteEpilogue);
+      if (!ok) break;
+      ++items;  // those with a query tile a
       tc_fence_after_sync();
       const float inv = 1.f / l;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o.p) + (it.row0 + qi) * p.o.token + it.head * p.o.head;
@@ -510,13 +546,15 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
         tmem_ld_32cols(t_o + x, o);
         if (qi < it.len) store_row(dst, o, inv, x, p.s.dim);
       }
+      // O is in registers: the next item's first product, which waits for this warp's next probabilities, overwrites it.
+      tc_fence_before_sync();
       if (qi < it.len) p.lse[int64_t(it.head) * p.s.T + it.row0 + qi] = m * p.s.scale + logf(l);
     }
   }
   __syncthreads();
   if (*abort_flag) {
     if (warp == kLoad && elect_one()) {
-      wait_drain(q_full, 0, p.wait_ns);
+      if (items > 0) wait_drain(q_full, (items - 1) & 1, p.wait_ns);
       ring.drain(issued, p.wait_ns);
     }
     if (warp == kMma && elect_one()) {
@@ -544,7 +582,8 @@ struct DqCfg {
   // Softmax warps: 32 columns each. With two of 64 columns a scheduler, the time of a tile is the latency of their steps.
   static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;
   static constexpr int THREADS = (WARPS + 2) * 32;
-  static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + GROUPS * 512 + 256;
+  static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 8 + 1);
+  static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + (GROUPS + 1) * 512 + BARS;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -563,19 +602,22 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   uint8_t* s_do = s_q + C::TILE;
   uint8_t* s_k = s_do + C::TILE;
   uint8_t* s_v = s_k + C::KS * C::NARROW;
-  float* s_sum = reinterpret_cast<float*>(s_v + C::VS * C::NARROW);  // [GROUPS][128]
+  float* s_delta = reinterpret_cast<float*>(s_v + C::VS * C::NARROW);  // [128]
+  float* s_sum = s_delta + kRows;                                      // [GROUPS][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_sum + C::GROUPS * kRows);
   const Ring<C::KS> ring_k{bars, bars + C::KS};
   bars += 2 * C::KS;
   const Ring<C::VS> ring_v{bars, bars + C::VS};
   bars += 2 * C::VS;
   uint64_t* q_full = bars;       // Q and dO
-  uint64_t* sd_full = bars + 1;  // S and dP of a tile
-  uint64_t* dp_read = bars + 2;  // dP is in registers
-  uint64_t* ds_full = bars + 3;
-  uint64_t* done = bars + 4;
-  uint64_t* drain = bars + 5;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
+  uint64_t* q_free = bars + 1;   // the item's S and dP are all made
+  uint64_t* sd_full = bars + 2;  // S and dP of a tile
+  uint64_t* dp_read = bars + 3;  // dP is in registers
+  uint64_t* ds_full = bars + 4;
+  uint64_t* done = bars + 5;     // an item's dQ is there
+  uint64_t* meet = bars + 6;     // the softmax warps' sums are in shared memory
+  uint64_t* drain = bars + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -583,188 +625,233 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
     ring_k.init();
     ring_v.init();
     mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
     mbar_init(sd_full, 1);
     mbar_init(dp_read, C::WARPS);
     mbar_init(ds_full, C::WARPS);
     mbar_init(done, 1);
+    mbar_init(meet, C::WARPS);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  const Item it = item_of(p, p.s.heads, p.s.causal);
-  const int q0 = it.tile * kRows;
-  if (q0 >= it.len) return;
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::TMEM);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int kv = it.head / (p.s.heads / p.s.kv_heads);
-  const int n = ((p.s.causal ? min(it.len, q0 + kRows) : it.len) + W - 1) / W;
-  int issued_k = 0, issued_v = 0;
+  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  // Key tiles of an item.
+  auto tiles_of = [&](const Item& it) {
+    const int q0 = it.tile * kRows;
+    return q0 >= it.len ? 0 : ((p.s.causal ? min(it.len, q0 + kRows) : it.len) + W - 1) / W;
+  };
+  int items = 0, issued_k = 0, issued_v = 0;
 
   if (warp == kLoadWarp) {
-    if (elect_one()) {
-      mbar_arrive_expect_tx(q_full, 2 * C::TILE);
-      load_tile<DH>(s_q, &p.q, it.head, it.row0 + q0, q_full);
-      load_tile<DH>(s_do, &p.d_o, it.head, it.row0 + q0, q_full);
-    }
-    for (int j = 0; j < n; ++j) {
-      if (!ring_k.wait_empty(j, guard)) break;
-      if (j + 1 != p.withhold) {
-        if (elect_one()) {
-          mbar_arrive_expect_tx(ring_k.full + j % C::KS, C::NARROW);
-          load_tile<DH, W>(s_k + (j % C::KS) * C::NARROW, &p.k, kv, it.row0 + j * W, ring_k.full + j % C::KS);
-        }
-        issued_k = j + 1;
-      }
-      if (!ring_v.wait_empty(j, guard)) break;
+    bool ok = true;
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      const int n = tiles_of(it), kv = it.head / group;
+      if (n == 0) continue;
+      ok = items == 0 || warp_wait(q_free, (items - 1) & 1, guard, kSiteProducer);
+      if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(ring_v.full + j % C::VS, C::NARROW);
-        load_tile<DH, W>(s_v + (j % C::VS) * C::NARROW, &p.v, kv, it.row0 + j * W, ring_v.full + j % C::VS);
+        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        load_tile<DH>(s_q, &p.q, it.head, it.row0 + it.tile * kRows, q_full);
+        load_tile<DH>(s_do, &p.d_o, it.head, it.row0 + it.tile * kRows, q_full);
       }
-      issued_v = j + 1;
+      ++items;
+      for (int j = 0; j < n; ++j) {
+        ok = ring_k.wait_empty(issued_k, guard);
+        if (!ok) break;
+        if (issued_k + 1 != p.withhold && elect_one()) {
+          mbar_arrive_expect_tx(ring_k.full + issued_k % C::KS, C::NARROW);
+          load_tile<DH, W>(s_k + (issued_k % C::KS) * C::NARROW, &p.k, kv, it.row0 + j * W, ring_k.full + issued_k % C::KS);
+        }
+        ++issued_k;
+        ok = ring_v.wait_empty(issued_v, guard);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(ring_v.full + issued_v % C::VS, C::NARROW);
+          load_tile<DH, W>(s_v + (issued_v % C::VS) * C::NARROW, &p.v, kv, it.row0 + j * W, ring_v.full + issued_v % C::VS);
+        }
+        ++issued_v;
+      }
     }
   } else if (warp == kMmaWarp) {
-    bool ok = warp_wait(q_full, 0, guard, kSiteMmaFull);
-    for (int j = 0; ok && j <= n; ++j) {
-      if (j < n) {
-        ok = ring_k.wait_full(j, guard);
-        if (!ok) break;
-        uint8_t* k_tile = s_k + (j % C::KS) * C::NARROW;
-        if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
-        // S_j over dS_{j-2}, whose product was issued before.
-        if (elect_one()) product_rows<DH, W>(tmem + C::S + (j & 1) * W, s_q, k_tile);
-        ok = ring_v.wait_full(j, guard) && (j == 0 || warp_wait(dp_read, (j - 1) & 1, guard, kSiteMmaAcc));
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (elect_one()) {
-          product_rows<DH, W>(tmem + C::DP, s_do, s_v + (j % C::VS) * C::NARROW);
-          tc_commit(sd_full);
-          tc_commit(ring_v.empty + j % C::VS);
+    bool ok = true;
+    int g = 0;  // tiles so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      const int n = tiles_of(it);
+      if (n == 0) continue;
+      ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull);
+      if (!ok) break;
+      ++items;
+      for (int j = 0; j <= n; ++j, ++g) {
+        if (j < n) {
+          ok = ring_k.wait_full(g, guard);
+          if (!ok) break;
+          uint8_t* k_tile = s_k + (g % C::KS) * C::NARROW;
+          if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
+          // S over dS of two tiles before, whose product was issued before.
+          if (elect_one()) product_rows<DH, W>(tmem + C::S + (g & 1) * W, s_q, k_tile);
+          __syncwarp();
+          ok = ring_v.wait_full(g, guard) && (g == 0 || warp_wait(dp_read, (g - 1) & 1, guard, kSiteMmaAcc));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            product_rows<DH, W>(tmem + C::DP, s_do, s_v + (g % C::VS) * C::NARROW);
+            tc_commit(sd_full);
+            tc_commit(ring_v.empty + g % C::VS);
+            if (j + 1 == n) tc_commit(q_free);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (j > 0) {
-        ok = warp_wait(ds_full, (j - 1) & 1, guard, kSiteMmaAcc);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (elect_one()) {
-          product_tokens<DH, W, H>(tmem + C::DQ, tmem + C::S + ((j - 1) & 1) * W, s_k + ((j - 1) % C::KS) * C::NARROW, j > 1, H);
-          tc_commit(ring_k.empty + (j - 1) % C::KS);
-          if (j == n) tc_commit(done);
+        if (j > 0) {
+          const int last = g - 1;
+          ok = warp_wait(ds_full, last & 1, guard, kSiteMmaAcc);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            product_tokens<DH, W, H>(tmem + C::DQ, tmem + C::S + (last & 1) * W, s_k + (last % C::KS) * C::NARROW, j > 1, H);
+            tc_commit(ring_k.empty + last % C::KS);
+            if (j == n) tc_commit(done);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      --g;  // the pass of the last dS took no tile
     }
   } else {
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int qi = q0 + row;
-    const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
-    const float nl = -p.lse[at] * kLog2e;
-    float delta = 0.f;
+    int g = 0, met = 0;  // tiles; uses of `meet`
+    auto meet_all = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      return warp_wait(meet, met++ & 1, guard, kSiteEpilogue);
+    };
     bool ok = true;
-    if (n > 1) {
-      // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
-      constexpr int R = kRows / C::WARPS / 4, N = R * (DH / 64);
-      uint4 o[N];
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+      const int n = tiles_of(it), q0 = it.tile * kRows, qi = q0 + row;
+      if (n == 0) continue;
+      const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
+      const float nl = -p.lse[at] * kLog2e;
+      float delta = 0.f;
+      if (n > 1) {
+        // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
+        constexpr int R = kRows / C::WARPS / 4, N = R * (DH / 64);
+        uint4 o[N];
 #pragma unroll
-      for (int x = 0; x < N; ++x) {
-        const int r = (warp * R + x % R) * 4 + (lane >> 3), e = (x / R) * 64 + (lane & 7) * 8;
-        o[x] = make_uint4(0, 0, 0, 0);
-        if (q0 + r < it.len && e < p.s.dim)
-          o[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o.p) + (it.row0 + q0 + r) * p.o.token +
-                                                 it.head * p.o.head + e);
-      }
-      ok = warp_wait(q_full, 0, guard, kSiteMmaFull);
-      float sum[R];
-#pragma unroll
-      for (int x = 0; x < N; ++x) {
-        const int r = (warp * R + x % R) * 4 + (lane >> 3);
-        const uint4 g = *reinterpret_cast<const uint4*>(s_do + (x / R) * kChunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-        sum[x % R] = dot8(o[x], g, x < R ? 0.f : sum[x % R]);
-      }
-#pragma unroll
-      for (int x = 0; x < R; ++x) {
-        sum[x] += __shfl_xor_sync(kAll, sum[x], 4);
-        sum[x] += __shfl_xor_sync(kAll, sum[x], 2);
-        sum[x] += __shfl_xor_sync(kAll, sum[x], 1);
-        if ((lane & 7) == 0) s_sum[(warp * R + x) * 4 + (lane >> 3)] = sum[x];
-      }
-      softmax_barrier<C::WARPS * 32>();
-      // The sums of dS go there no sooner than every warp has read dP of the first tile, which is after this.
-      delta = s_sum[row];
-    }
-    float total = 0.f;  // of dS
-    for (int j = 0; j < n; ++j) {
-      ok = ok && warp_wait(sd_full, j & 1, guard, kSiteMmaFull);
-      if (!ok) {
-        if (n == 1) softmax_barrier<C::WARPS * 32>();  // the others may stand at it
-        break;
-      }
-      tc_fence_after_sync();
-      const uint32_t t_s = tmem + lanes + C::S + (j & 1) * W + H * part;
-      float s[H], dp[H];
-      tmem_ld<H>(tmem + lanes + C::DP + H * part, dp);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(dp_read);
-      tmem_ld<H>(t_s, s);
-      const int k0 = j * W;
-      const uint64_t c2 = pair(p.scale_log2, p.scale_log2), n2 = pair(nl, nl);
-#pragma unroll
-      for (int e = 0; e < H; e += 2) {
-        unpair(fma_pair(pair(s[e], s[e + 1]), c2, n2), s[e], s[e + 1]);
-        s[e] = exp2_fast(s[e]);
-        s[e + 1] = exp2_fast(s[e + 1]);
-      }
-      if (k0 + W > it.len || (p.s.causal && k0 + W > q0)) {
-        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;
-#pragma unroll
-        for (int e = 0; e < H; ++e) {
-          s[e] = e < end ? s[e] : 0.f;
-          dp[e] = e < end ? dp[e] : 0.f;
+        for (int x = 0; x < N; ++x) {
+          const int y = (warp * R + x % R) * 4 + (lane >> 3), e = (x / R) * 64 + (lane & 7) * 8;
+          o[x] = make_uint4(0, 0, 0, 0);
+          if (q0 + y < it.len && e < p.s.dim)
+            o[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o.p) + (it.row0 + q0 + y) * p.o.token +
+                                                   it.head * p.o.head + e);
         }
-      }
-      if (n == 1) {
-        float sum = 0.f;
+        ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        float sum[R];
 #pragma unroll
-        for (int e = 0; e < H; ++e) sum = fmaf(s[e], dp[e], sum);
-        s_sum[part * kRows + row] = sum;
-        softmax_barrier<C::WARPS * 32>();
-        delta = row_sum<C::GROUPS>(s_sum, row);
-      }
-      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-      const uint64_t d2 = pair(-delta, -delta);
-      uint32_t w[H / 2];
+        for (int x = 0; x < N; ++x) {
+          const int y = (warp * R + x % R) * 4 + (lane >> 3);
+          const uint4 d = *reinterpret_cast<const uint4*>(s_do + (x / R) * kChunk + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+          sum[x % R] = dot8(o[x], d, x < R ? 0.f : sum[x % R]);
+        }
 #pragma unroll
-      for (int e = 0; e < H; e += 2) {
-        const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
-        sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], ds);
+        for (int x = 0; x < R; ++x) {
+          sum[x] += __shfl_xor_sync(kAll, sum[x], 4);
+          sum[x] += __shfl_xor_sync(kAll, sum[x], 2);
+          sum[x] += __shfl_xor_sync(kAll, sum[x], 1);
+          if ((lane & 7) == 0) s_delta[(warp * R + x) * 4 + (lane >> 3)] = sum[x];
+        }
+        fence_proxy_async_smem();  // the reads of dO, before the next item's comes there
+        ok = meet_all();
+        if (!ok) break;
+        delta = s_delta[row];
+      } else {
+        ok = meet_all();  // s_sum is written in the loop: no warp reads the last item's any more
+        if (!ok) break;
+      }
+      ++items;
+      float total = 0.f;  // of dS
+      for (int j = 0; j < n; ++j, ++g) {
+        ok = warp_wait(sd_full, g & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t t_s = tmem + lanes + C::S + (g & 1) * W + H * part;
+        float s[H], dp[H];
+        tmem_ld<H>(tmem + lanes + C::DP + H * part, dp);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dp_read);
+        tmem_ld<H>(t_s, s);
+        const int k0 = j * W;
+        const uint64_t c2 = pair(p.scale_log2, p.scale_log2), n2 = pair(nl, nl);
+#pragma unroll
+        for (int e = 0; e < H; e += 2) {
+          unpair(fma_pair(pair(s[e], s[e + 1]), c2, n2), s[e], s[e + 1]);
+          s[e] = exp2_fast(s[e]);
+          s[e + 1] = exp2_fast(s[e + 1]);
+        }
+        if (k0 + W > it.len || (p.s.causal && k0 + W > q0)) {
+          const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            s[e] = e < end ? s[e] : 0.f;
+            dp[e] = e < end ? dp[e] : 0.f;
+          }
+        }
+        if (n == 1) {
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < H; ++e) sum = fmaf(s[e], dp[e], sum);
+          s_sum[part * kRows + row] = sum;
+          ok = meet_all();
+          if (!ok) break;
+          delta = row_sum<C::GROUPS>(s_sum, row);
+        }
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const uint64_t d2 = pair(-delta, -delta);
+        uint32_t w[H / 2];
+#pragma unroll
+        for (int e = 0; e < H; e += 2) {
+          const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
+          sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], ds);
+          float x0, x1;
+          unpair(ds, x0, x1);
+          w[e / 2] = pack_bf16(x0, x1);
+        }
+        tmem_st_16(t_s, w);
         float x0, x1;
-        unpair(ds, x0, x1);
-        w[e / 2] = pack_bf16(x0, x1);
+        unpair(add_pair(sum[0], sum[1]), x0, x1);
+        total += x0 + x1;
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
       }
-      tmem_st_16(t_s, w);
-      float x0, x1;
-      unpair(add_pair(sum[0], sum[1]), x0, x1);
-      total += x0 + x1;
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
-    }
-    // All softmax warps come here alike: a failed wait ends in the same barrier.
-    if (n > 1) s_sum[part * kRows + row] = total;
-    softmax_barrier<C::WARPS * 32>();
-    ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
-    if (ok) {
+      if (!ok) break;
+      if (n > 1) {
+        s_sum[part * kRows + row] = total;
+        ok = meet_all();
+        if (!ok) break;
+        if (part == 0) delta += row_sum<C::GROUPS>(s_sum, row);
+      }
+      if (part == 0 && qi < it.len) p.delta[at] = delta;
+      ok = warp_wait(done, (items - 1) & 1, guard, kSiteEpilogue);
+      if (!ok) break;
       tc_fence_after_sync();
-      if (part == 0 && qi < it.len) p.delta[at] = n > 1 ? delta + row_sum<C::GROUPS>(s_sum, row) : delta;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
 #pragma unroll 1
       for (int x = part * 32; x < DH; x += C::GROUPS * 32) {
@@ -772,12 +859,13 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         tmem_ld_32cols(tmem + lanes + C::DQ + x, o);
         if (qi < it.len) store_row(dst, o, p.s.scale, x, p.s.dim);
       }
+      tc_fence_before_sync();  // dQ is in registers; the next item's waits for this warp's next dS
     }
   }
   __syncthreads();
   if (*abort_flag) {
     if (warp == kLoadWarp && elect_one()) {
-      wait_drain(q_full, 0, p.wait_ns);
+      if (items > 0) wait_drain(q_full, (items - 1) & 1, p.wait_ns);
       ring_k.drain(issued_k, p.wait_ns);
       ring_v.drain(issued_v, p.wait_ns);
     }
@@ -805,7 +893,8 @@ struct DkvCfg {
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
   static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;  // softmax warps, as in dQ
   static constexpr int THREADS = (WARPS + 3) * 32;
-  static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + 256;
+  static constexpr size_t BARS = 8 * (2 * QS + 2 * DS + 2 * RS + 8 + 1);
+  static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + BARS;
   static_assert(SMEM <= 227 * 1024 && CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -833,13 +922,14 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   const Ring<C::RS> ring_r{bars, bars + C::RS};
   bars += 2 * C::RS;
   uint64_t* kv_full = bars;
-  uint64_t* s_full = bars + 1;
-  uint64_t* p_full = bars + 2;
-  uint64_t* dp_full = bars + 3;
-  uint64_t* ds_full = bars + 4;
-  uint64_t* done = bars + 5;
-  uint64_t* drain = bars + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7);
+  uint64_t* kv_free = bars + 1;  // the item's S and dP are all made
+  uint64_t* s_full = bars + 2;
+  uint64_t* p_full = bars + 3;
+  uint64_t* dp_full = bars + 4;
+  uint64_t* ds_full = bars + 5;
+  uint64_t* done = bars + 6;  // an item's dK and dV are there
+  uint64_t* drain = bars + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -848,6 +938,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     ring_d.init();
     ring_r.init(32, C::WARPS);
     mbar_init(kv_full, 1);
+    mbar_init(kv_free, 1);
     mbar_init(s_full, 1);
     mbar_init(p_full, C::WARPS);
     mbar_init(dp_full, 1);
@@ -857,139 +948,168 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  const Item it = item_of(p, p.s.kv_heads, false);
-  const int k0 = it.tile * kRows;
-  if (k0 >= it.len) return;
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::TMEM);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int group = p.s.heads / p.s.kv_heads;
-  // Query tiles first .. last of every head of the group, head by head.
-  const int first = p.s.causal ? k0 / W : 0;
-  const int per = (it.len + W - 1) / W - first;
-  const int n = per * group;
-  int issued_q = 0, issued_d = 0;
+  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  // Query tiles of an item: `per` from `first` on of every head of the group, head by head.
+  struct Passes {
+    int first, per, n;
+  };
+  auto passes_of = [&](const Item& it) {
+    Passes x;
+    x.first = p.s.causal ? it.tile * kRows / W : 0;
+    x.per = it.tile * kRows >= it.len ? 0 : (it.len + W - 1) / W - x.first;
+    x.n = x.per * group;
+    return x;
+  };
+  int items = 0, issued_q = 0, issued_d = 0;
 
   if (warp == kLoadWarp) {
-    if (elect_one()) {
-      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-      load_tile<DH>(s_k, &p.k, it.head, it.row0 + k0, kv_full);
-      load_tile<DH>(s_v, &p.v, it.head, it.row0 + k0, kv_full);
-    }
-    int h = it.head * group, x = 0;  // head and query tile of pass i
-    for (int i = 0; i < n; ++i) {
-      const int64_t row = it.row0 + (first + x) * W;
-      if (!ring_q.wait_empty(i, guard)) break;
-      if (i + 1 != p.withhold) {
-        if (elect_one()) {
-          mbar_arrive_expect_tx(ring_q.full + i % C::QS, C::NARROW);
-          load_tile<DH, W>(s_q + (i % C::QS) * C::NARROW, &p.q, h, row, ring_q.full + i % C::QS);
-        }
-        issued_q = i + 1;
-      }
-      if (!ring_d.wait_empty(i, guard)) break;
+    bool ok = true;
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+      const Passes ps = passes_of(it);
+      if (ps.n == 0) continue;
+      ok = items == 0 || warp_wait(kv_free, (items - 1) & 1, guard, kSiteProducer);
+      if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(ring_d.full + i % C::DS, C::NARROW);
-        load_tile<DH, W>(s_do + (i % C::DS) * C::NARROW, &p.d_o, h, row, ring_d.full + i % C::DS);
+        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+        load_tile<DH>(s_k, &p.k, it.head, it.row0 + it.tile * kRows, kv_full);
+        load_tile<DH>(s_v, &p.v, it.head, it.row0 + it.tile * kRows, kv_full);
       }
-      issued_d = i + 1;
-      if (++x == per) x = 0, ++h;
+      ++items;
+      int h = it.head * group, x = 0;  // head and query tile of pass i
+      for (int i = 0; i < ps.n; ++i) {
+        const int64_t row = it.row0 + (ps.first + x) * W;
+        ok = ring_q.wait_empty(issued_q, guard);
+        if (!ok) break;
+        if (issued_q + 1 != p.withhold && elect_one()) {
+          mbar_arrive_expect_tx(ring_q.full + issued_q % C::QS, C::NARROW);
+          load_tile<DH, W>(s_q + (issued_q % C::QS) * C::NARROW, &p.q, h, row, ring_q.full + issued_q % C::QS);
+        }
+        ++issued_q;
+        ok = ring_d.wait_empty(issued_d, guard);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(ring_d.full + issued_d % C::DS, C::NARROW);
+          load_tile<DH, W>(s_do + (issued_d % C::DS) * C::NARROW, &p.d_o, h, row, ring_d.full + issued_d % C::DS);
+        }
+        ++issued_d;
+        if (++x == ps.per) x = 0, ++h;
+      }
     }
   } else if (warp == kRowWarp) {
     // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them.
-    int h = it.head * group, x = 0;
-    for (int i = 0; i < n; ++i) {
-      const int q0 = (first + x) * W;
-      const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
-      float nl[W / 32], nd[W / 32];
+    bool ok = true;
+    int g = 0;  // passes so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+      const Passes ps = passes_of(it);
+      int h = it.head * group, x = 0;
+      for (int i = 0; i < ps.n; ++i, ++g) {
+        const int q0 = (ps.first + x) * W;
+        const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
+        float nl[W / 32], nd[W / 32];
 #pragma unroll
-      for (int y = 0; y < W / 32; ++y) {
-        const int r = y * 32 + lane;
-        const bool on = q0 + r < it.len;
-        nl[y] = on ? -p.lse[at + r] * kLog2e : 0.f;
-        nd[y] = on ? -p.delta[at + r] : 0.f;
-      }
-      if (!ring_r.wait_empty(i, guard)) break;
-      float* rows = s_row + (i % C::RS) * 2 * W;
+        for (int y = 0; y < W / 32; ++y) {
+          const int q = y * 32 + lane;
+          const bool on = q0 + q < it.len;
+          nl[y] = on ? -p.lse[at + q] * kLog2e : 0.f;
+          nd[y] = on ? -p.delta[at + q] : 0.f;
+        }
+        ok = ring_r.wait_empty(g, guard);
+        if (!ok) break;
+        float* rows = s_row + (g % C::RS) * 2 * W;
 #pragma unroll
-      for (int y = 0; y < W / 32; ++y) {
-        rows[y * 32 + lane] = nl[y];
-        rows[W + y * 32 + lane] = nd[y];
+        for (int y = 0; y < W / 32; ++y) {
+          rows[y * 32 + lane] = nl[y];
+          rows[W + y * 32 + lane] = nd[y];
+        }
+        mbar_arrive(ring_r.full + g % C::RS);
+        if (++x == ps.per) x = 0, ++h;
       }
-      mbar_arrive(ring_r.full + i % C::RS);
-      if (++x == per) x = 0, ++h;
     }
   } else if (warp == kMmaWarp) {
-    // Tile i of a ring (query tile x), its rows of the next sequence cleared.
-    auto take_q = [&](int i, int x) {
-      if (!ring_q.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + x) * W;
-      if (rows < W) clear_rows<DH, W>(s_q + (i % C::QS) * C::NARROW, rows, lane);
-      return true;
-    };
-    auto take_d = [&](int i, int x) {
-      if (!ring_d.wait_full(i, guard)) return false;
-      const int rows = it.len - (first + x) * W;
-      if (rows < W) clear_rows<DH, W>(s_do + (i % C::DS) * C::NARROW, rows, lane);
-      return true;
-    };
-    bool ok = warp_wait(kv_full, 0, guard, kSiteMmaFull) && take_q(0, 0);
-    if (ok) {
+    bool ok = true;
+    int g = 0;  // passes so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+      const Passes ps = passes_of(it);
+      if (ps.n == 0) continue;
+      // Position i of a ring (query tile x), its rows of the next sequence cleared.
+      auto take_q = [&](int i, int x) {
+        if (!ring_q.wait_full(i, guard)) return false;
+        const int rows = it.len - (ps.first + x) * W;
+        if (rows < W) clear_rows<DH, W>(s_q + (i % C::QS) * C::NARROW, rows, lane);
+        return true;
+      };
+      auto take_d = [&](int i, int x) {
+        if (!ring_d.wait_full(i, guard)) return false;
+        const int rows = it.len - (ps.first + x) * W;
+        if (rows < W) clear_rows<DH, W>(s_do + (i % C::DS) * C::NARROW, rows, lane);
+        return true;
+      };
+      ok = warp_wait(kv_full, items & 1, guard, kSiteMmaFull) && take_q(g, 0);
+      if (!ok) break;
+      ++items;
       if (elect_one()) {
-        product_rows<DH, W>(tmem + C::S, s_k, s_q);
+        product_rows<DH, W>(tmem + C::S, s_k, s_q + (g % C::QS) * C::NARROW);
         tc_commit(s_full);
       }
       __syncwarp();
-      ok = take_d(0, 0);
-    }
-    if (ok) {
+      ok = take_d(g, 0);
+      if (!ok) break;
       if (elect_one()) {
-        product_rows<DH, W>(tmem + C::DP, s_v, s_do);
+        product_rows<DH, W>(tmem + C::DP, s_v, s_do + (g % C::DS) * C::NARROW);
         tc_commit(dp_full);
+        if (ps.n == 1) tc_commit(kv_free);
       }
       __syncwarp();
       int x = 0;  // query tile of pass i + 1
-      for (int i = 0; i < n; ++i) {
-        if (++x == per) x = 0;
-        const uint8_t* d_tile = s_do + (i % C::DS) * C::NARROW;
-        const uint8_t* q_tile = s_q + (i % C::QS) * C::NARROW;
-        ok = warp_wait(p_full, i & 1, guard, kSiteMmaAcc);
+      for (int i = 0; i < ps.n; ++i, ++g) {
+        if (++x == ps.per) x = 0;
+        ok = warp_wait(p_full, g & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          product_tokens<DH, W, H>(tmem + C::DV, tmem + C::S, d_tile, i > 0, H);
-          tc_commit(ring_d.empty + i % C::DS);
+          product_tokens<DH, W, H>(tmem + C::DV, tmem + C::S, s_do + (g % C::DS) * C::NARROW, i > 0, H);
+          tc_commit(ring_d.empty + g % C::DS);
         }
         __syncwarp();
-        if (i + 1 < n) {
-          ok = take_q(i + 1, x);
+        if (i + 1 < ps.n) {
+          ok = take_q(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::S, s_k, s_q + ((i + 1) % C::QS) * C::NARROW);
+            product_rows<DH, W>(tmem + C::S, s_k, s_q + ((g + 1) % C::QS) * C::NARROW);
             tc_commit(s_full);
           }
           __syncwarp();
         }
-        ok = warp_wait(ds_full, i & 1, guard, kSiteMmaAcc);
+        ok = warp_wait(ds_full, g & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          product_tokens<DH, W, H>(tmem + C::DK, tmem + C::DP, q_tile, i > 0, H);
-          tc_commit(ring_q.empty + i % C::QS);
-          if (i + 1 == n) tc_commit(done);
+          product_tokens<DH, W, H>(tmem + C::DK, tmem + C::DP, s_q + (g % C::QS) * C::NARROW, i > 0, H);
+          tc_commit(ring_q.empty + g % C::QS);
+          if (i + 1 == ps.n) tc_commit(done);
         }
         __syncwarp();
-        if (i + 1 < n) {
-          ok = take_d(i + 1, x);
+        if (i + 1 < ps.n) {
+          ok = take_d(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((i + 1) % C::DS) * C::NARROW);
+            product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((g + 1) % C::DS) * C::NARROW);
             tc_commit(dp_full);
+            if (i + 2 == ps.n) tc_commit(kv_free);
           }
           __syncwarp();
         }
@@ -999,87 +1119,96 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + C::S + H * part, t_dp = tmem + lanes + C::DP + H * part;
-    const int kj = k0 + row;
     bool ok = true;
-    int x = 0;
-    for (int i = 0; i < n; ++i) {
-      const int q0 = (first + x) * W + H * part;  // of this warp's columns
-      if (++x == per) x = 0;
-      const float* rows = s_row + (i % C::RS) * 2 * W + H * part;
-      ok = ring_r.wait_full(i, guard) && warp_wait(s_full, i & 1, guard, kSiteMmaFull);
+    int g = 0;  // passes so far
+    Item it;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+      const Passes ps = passes_of(it);
+      if (ps.n == 0) continue;
+      const int k0 = it.tile * kRows, kj = k0 + row;
+      int x = 0;
+      for (int i = 0; i < ps.n; ++i, ++g) {
+        const int q0 = (ps.first + x) * W + H * part;  // of this warp's columns
+        if (++x == ps.per) x = 0;
+        const float* rows = s_row + (g % C::RS) * 2 * W + H * part;
+        ok = ring_r.wait_full(g, guard) && warp_wait(s_full, g & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
+        float s[H];
+        tmem_ld<H>(t_s, s);
+#pragma unroll
+        for (int e = 0; e < H; e += 4) {
+          const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(rows + e);
+          unpair(fma_pair(pair(s[e], s[e + 1]), c2, nl.x), s[e], s[e + 1]);
+          unpair(fma_pair(pair(s[e + 2], s[e + 3]), c2, nl.y), s[e + 2], s[e + 3]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[e + y] = exp2_fast(s[e + y]);
+        }
+        const int begin = p.s.causal ? kj - q0 : 0, end = it.len - q0;  // columns that count
+        const bool masked = end < H || (p.s.causal && q0 < k0 + kRows);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < H; ++e) s[e] = e >= begin && e < end ? s[e] : 0.f;
+        }
+        uint32_t w[H / 2];
+#pragma unroll
+        for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
+        tmem_st_16(t_s, w);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ok = warp_wait(dp_full, g & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after_sync();
+        float dp[H];
+        tmem_ld<H>(t_dp, dp);
+        if (masked) {  // what stands there may be no number
+#pragma unroll
+          for (int e = 0; e < H; ++e) dp[e] = e >= begin && e < end ? dp[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < H; e += 4) {
+          const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + W + e);
+          float x0, x1, x2, x3;
+          unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), x0, x1);
+          unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), x2, x3);
+          w[e / 2] = pack_bf16(x0, x1);
+          w[e / 2 + 1] = pack_bf16(x2, x3);
+        }
+        tmem_st_16(t_dp, w);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(ring_r.empty + g % C::RS);
+        }
+      }
       if (!ok) break;
-      tc_fence_after_sync();
-      const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
-      float s[H];
-      tmem_ld<H>(t_s, s);
-#pragma unroll
-      for (int e = 0; e < H; e += 4) {
-        const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(rows + e);
-        unpair(fma_pair(pair(s[e], s[e + 1]), c2, nl.x), s[e], s[e + 1]);
-        unpair(fma_pair(pair(s[e + 2], s[e + 3]), c2, nl.y), s[e + 2], s[e + 3]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[e + x] = exp2_fast(s[e + x]);
-      }
-      const int begin = p.s.causal ? kj - q0 : 0, end = it.len - q0;  // columns that count
-      const bool masked = end < H || (p.s.causal && q0 < k0 + kRows);
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < H; ++e) s[e] = e >= begin && e < end ? s[e] : 0.f;
-      }
-      uint32_t w[H / 2];
-#pragma unroll
-      for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
-      tmem_st_16(t_s, w);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-      ok = warp_wait(dp_full, i & 1, guard, kSiteMmaFull);
+      ok = warp_wait(done, items & 1, guard, kSiteEpilogue);
       if (!ok) break;
-      tc_fence_after_sync();
-      float dp[H];
-      tmem_ld<H>(t_dp, dp);
-      if (masked) {  // what stands there may be no number
-#pragma unroll
-        for (int e = 0; e < H; ++e) dp[e] = e >= begin && e < end ? dp[e] : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < H; e += 4) {
-        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + W + e);
-        float x0, x1, x2, x3;
-        unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), x0, x1);
-        unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), x2, x3);
-        w[e / 2] = pack_bf16(x0, x1);
-        w[e / 2 + 1] = pack_bf16(x2, x3);
-      }
-      tmem_st_16(t_dp, w);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_full);
-        mbar_arrive(ring_r.empty + i % C::RS);
-      }
-    }
-    ok = ok && warp_wait(done, 0, guard, kSiteEpilogue);
-    if (ok) {
+      ++items;
       tc_fence_after_sync();
       __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + (it.row0 + kj) * p.dv.token + it.head * p.dv.head;
       __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + (it.row0 + kj) * p.dk.token + it.head * p.dk.head;
 #pragma unroll 1
-      for (int x = part * 32; x < DH; x += C::GROUPS * 32) {
+      for (int y = part * 32; y < DH; y += C::GROUPS * 32) {
         float o[32];
-        tmem_ld_32cols(tmem + lanes + C::DV + x, o);
-        if (kj < it.len) store_row(dv, o, 1.f, x, p.s.dim);
-        tmem_ld_32cols(tmem + lanes + C::DK + x, o);
-        if (kj < it.len) store_row(dk, o, p.s.scale, x, p.s.dim);
+        tmem_ld_32cols(tmem + lanes + C::DV + y, o);
+        if (kj < it.len) store_row(dv, o, 1.f, y, p.s.dim);
+        tmem_ld_32cols(tmem + lanes + C::DK + y, o);
+        if (kj < it.len) store_row(dk, o, p.s.scale, y, p.s.dim);
       }
+      tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
     }
   }
   __syncthreads();
   if (*abort_flag) {
     if (warp == kLoadWarp && elect_one()) {
-      wait_drain(kv_full, 0, p.wait_ns);
+      if (items > 0) wait_drain(kv_full, (items - 1) & 1, p.wait_ns);
       ring_q.drain(issued_q, p.wait_ns);
       ring_d.drain(issued_d, p.wait_ns);
     }
@@ -1134,30 +1263,31 @@ cudaError_t params_of(const C& c, TcParams* p) {
 }
 
 template <auto Kernel>
-cudaError_t launch(TcParams& p, int rows, int heads, int threads, size_t smem, cudaStream_t s) {
+cudaError_t launch(TcParams& p, int rows, int heads, int threads, size_t smem, int ctas, cudaStream_t s) {
   static std::atomic<uint64_t> devices{0};
   p.tiles = (p.s.max_seq + rows - 1) / rows;
   cudaError_t e = allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
-  const int64_t items = int64_t(p.tiles) * heads * p.s.batch;
-  return launch_pdl(Kernel, dim3(static_cast<unsigned>(items)), dim3(threads), smem, s, p);
+  p.items = static_cast<uint32_t>(int64_t(p.tiles) * heads * p.s.batch);
+  const uint32_t most = static_cast<uint32_t>(num_sms()) * ctas;
+  return launch_pdl(Kernel, dim3(p.items < most ? p.items : most), dim3(threads), smem, s, p);
 }
 
 template <int DH, int NQ>
 cudaError_t launch_fwd(TcParams& p, cudaStream_t s) {
   using C = FwdCfg<DH, NQ>;
-  return launch<fwd_kernel<DH, NQ>>(p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, s);
+  return launch<fwd_kernel<DH, NQ>>(p, NQ * kRows, p.s.heads, C::THREADS, C::SMEM, C::CTAS, s);
 }
 
 template <int DH, int W>
 cudaError_t launch_dq(TcParams& p, cudaStream_t s) {
   using C = DqCfg<DH, W>;
-  return launch<dq_kernel<DH, W>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, s);
+  return launch<dq_kernel<DH, W>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, C::CTAS, s);
 }
 template <int DH, int W>
 cudaError_t launch_dkv(TcParams& p, cudaStream_t s) {
   using C = DkvCfg<DH, W>;
-  return launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads, C::THREADS, C::SMEM, s);
+  return launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads, C::THREADS, C::SMEM, C::CTAS, s);
 }
 
 }  // namespace
