@@ -2,8 +2,8 @@
 // backward pass on the tensor cores (bf16, head sizes up to 128; the formulas
 // stand in attn_core.cu).
 //
-// Three persistent kernels, tiles of 128 tokens, head sizes padded to DH = 64 or 128 by
-// TMA's zero fill:
+// Three persistent kernels, tiles of 128 tokens, head sizes padded to DH = 64 or
+// 128 by TMA's zero fill (products take the head in steps of 16):
 //   forward  items of NQ query tiles of one head: S = Q K^T, P = exp(S - max),
 //            O += P V, with a running maximum and sum for each row.
 //   dQ       items of a query tile: S = Q K^T, dP = dO V^T, dS = P (dP - delta),
@@ -104,21 +104,23 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
          (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (static_cast<uint64_t>(2u) << 61);
 }
 
-// d = A B^T over the head's DH elements, both tiles K-major, A of 128 tokens, B of W: a 128 x W matrix.
+// d = A B^T over the head's first 16 `steps` elements, both tiles K-major, A of 128 tokens, B of W: a 128 x W matrix.
 template <int DH, int W = kRows>
-__device__ __forceinline__ void product_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
+__device__ __forceinline__ void product_rows(uint32_t d, const uint8_t* a, const uint8_t* b, int steps) {
   constexpr uint32_t id = idesc_bf16_f32(128, W);
   const uint32_t sa = smem_addr(a), sb = smem_addr(b);
 #pragma unroll
   for (int k = 0; k < DH / 16; ++k)
-    tc_mma_bf16(d, smem_desc_sw128(sa + (k / 4) * kChunk + (k % 4) * 32),
-                smem_desc_sw128(sb + (k / 4) * (W * 128) + (k % 4) * 32), id, k > 0);
+    if (k < steps)
+      tc_mma_bf16(d, smem_desc_sw128(sa + (k / 4) * kChunk + (k % 4) * 32),
+                  smem_desc_sw128(sb + (k / 4) * (W * 128) + (k % 4) * 32), id, k > 0);
 }
-// d (+)= M B over W tokens: M a 128 x W bf16 matrix in tensor memory, its columns in runs of RUN (of 16 bits) that
-// begin `step` columns (of 32 bits) apart.
-template <int DH, int W, int RUN>
-__device__ __forceinline__ void product_tokens(uint32_t d, uint32_t m, const uint8_t* b, bool accumulate, uint32_t step) {
-  constexpr uint32_t id = idesc_bf16_f32(128, DH, 0, 1);
+// d (+)= M B over W tokens, the first 16 `steps` elements of the head: M a 128 x W bf16 matrix in tensor memory, its
+// columns in runs of RUN (of 16 bits) that begin `step` columns (of 32 bits) apart.
+template <int W, int RUN>
+__device__ __forceinline__ void product_tokens(uint32_t d, uint32_t m, const uint8_t* b, bool accumulate, uint32_t step,
+                                               int steps) {
+  const uint32_t id = idesc_bf16_f32(128, 16 * steps, 0, 1);
   const uint32_t sb = smem_addr(b);
 #pragma unroll
   for (int k = 0; k < W / 16; ++k)
@@ -259,6 +261,7 @@ struct TcParams {
   float* lse;    // forward: written; backward: read
   float* delta;  // backward
   float scale_log2;
+  int steps;       // of 16 elements: what products over or of the head take
   int tiles;       // tiles (forward: runs of NQ tiles) of the longest sequence
   uint32_t items;  // tiles x heads x sequences
   int withhold;    // test hook: > 0: that load of the CTA's first ring is not issued
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
 #pragma unroll
         for (int a = 0; a < NQ; ++a)
           if (n[a] > 0) {
-            product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, s_ring + (at % C::SLOTS) * C::TILE);
+            product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, s_ring + (at % C::SLOTS) * C::TILE, p.steps);
             tc_commit(s_full + a);
           }
         tc_commit(ring.empty + at % C::SLOTS);
@@ -441,10 +444,10 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            product_tokens<DH, kRows, kRows>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 0);
+            product_tokens<kRows, kRows>(tmem + C::O + a * DH, tmem + a * 128, v_tile, j > 0, 0, p.steps);
             if (j + 1 == n[a]) tc_commit(o_done + a);
             if (j + 1 < n[a]) {  // over P, whose product comes first
-              product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, k_next);
+              product_rows<DH>(tmem + a * 128, s_q + a * C::TILE, k_next, p.steps);
               tc_commit(s_full + a);
             }
           }
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
         if (j > 0 && __any_sync(kAll, alpha != 1.f)) {
           // The scores' arrival came after the previous product's end: O holds still.
 #pragma unroll 1
-          for (int x = 0; x < DH; x += 32) {
+          for (int x = 0; x < DH && x < p.s.dim; x += 32) {
             float o[32];
             uint32_t w[32];
             tmem_ld_32cols(t_o + x, o);
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
       const float inv = 1.f / l;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o.p) + (it.row0 + qi) * p.o.token + it.head * p.o.head;
 #pragma unroll 1
-      for (int x = 0; x < DH; x += 32) {
+      for (int x = 0; x < DH && x < p.s.dim; x += 32) {
         float o[32];
         tmem_ld_32cols(t_o + x, o);
         if (qi < it.len) store_row(dst, o, inv, x, p.s.dim);
@@ -701,13 +704,13 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           uint8_t* k_tile = s_k + (g % C::KS) * C::NARROW;
           if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
           // S over dS of two tiles before, whose product was issued before.
-          if (elect_one()) product_rows<DH, W>(tmem + C::S + (g & 1) * W, s_q, k_tile);
+          if (elect_one()) product_rows<DH, W>(tmem + C::S + (g & 1) * W, s_q, k_tile, p.steps);
           __syncwarp();
           ok = ring_v.wait_full(g, guard) && (g == 0 || warp_wait(dp_read, (g - 1) & 1, guard, kSiteMmaAcc));
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::DP, s_do, s_v + (g % C::VS) * C::NARROW);
+            product_rows<DH, W>(tmem + C::DP, s_do, s_v + (g % C::VS) * C::NARROW, p.steps);
             tc_commit(sd_full);
             tc_commit(ring_v.empty + g % C::VS);
             if (j + 1 == n) tc_commit(q_free);
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            product_tokens<DH, W, H>(tmem + C::DQ, tmem + C::S + (last & 1) * W, s_k + (last % C::KS) * C::NARROW, j > 1, H);
+            product_tokens<W, H>(tmem + C::DQ, tmem + C::S + (last & 1) * W, s_k + (last % C::KS) * C::NARROW, j > 1, H, p.steps);
             tc_commit(ring_k.empty + last % C::KS);
             if (j == n) tc_commit(done);
           }
@@ -748,7 +751,9 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
       const float nl = -p.lse[at] * kLog2e;
       float delta = 0.f;
       if (n > 1) {
-        // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile.
+        // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile. (Asked
+        // for before the last item's output, O takes registers that the tiles' loop then lacks: 8 x 2048 tokens, 32 heads
+        // of 128, 373 -> 393 us.)
         constexpr int R = kRows / C::WARPS / 4, N = R * (DH / 64);
         uint4 o[N];
 #pragma unroll
@@ -854,10 +859,10 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
       tc_fence_after_sync();
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
 #pragma unroll 1
-      for (int x = part * 32; x < DH; x += C::GROUPS * 32) {
-        float o[32];
-        tmem_ld_32cols(tmem + lanes + C::DQ + x, o);
-        if (qi < it.len) store_row(dst, o, p.s.scale, x, p.s.dim);
+      for (int x = part * 32; x < DH && x < p.s.dim; x += C::GROUPS * 32) {
+        float v[32];
+        tmem_ld_32cols(tmem + lanes + C::DQ + x, v);
+        if (qi < it.len) store_row(dst, v, p.s.scale, x, p.s.dim);
       }
       tc_fence_before_sync();  // dQ is in registers; the next item's waits for this warp's next dS
     }
@@ -1062,14 +1067,14 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       if (!ok) break;
       ++items;
       if (elect_one()) {
-        product_rows<DH, W>(tmem + C::S, s_k, s_q + (g % C::QS) * C::NARROW);
+        product_rows<DH, W>(tmem + C::S, s_k, s_q + (g % C::QS) * C::NARROW, p.steps);
         tc_commit(s_full);
       }
       __syncwarp();
       ok = take_d(g, 0);
       if (!ok) break;
       if (elect_one()) {
-        product_rows<DH, W>(tmem + C::DP, s_v, s_do + (g % C::DS) * C::NARROW);
+        product_rows<DH, W>(tmem + C::DP, s_v, s_do + (g % C::DS) * C::NARROW, p.steps);
         tc_commit(dp_full);
         if (ps.n == 1) tc_commit(kv_free);
       }
@@ -1081,7 +1086,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          product_tokens<DH, W, H>(tmem + C::DV, tmem + C::S, s_do + (g % C::DS) * C::NARROW, i > 0, H);
+          product_tokens<W, H>(tmem + C::DV, tmem + C::S, s_do + (g % C::DS) * C::NARROW, i > 0, H, p.steps);
           tc_commit(ring_d.empty + g % C::DS);
         }
         __syncwarp();
@@ -1089,7 +1094,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           ok = take_q(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::S, s_k, s_q + ((g + 1) % C::QS) * C::NARROW);
+            product_rows<DH, W>(tmem + C::S, s_k, s_q + ((g + 1) % C::QS) * C::NARROW, p.steps);
             tc_commit(s_full);
           }
           __syncwarp();
@@ -1098,7 +1103,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          product_tokens<DH, W, H>(tmem + C::DK, tmem + C::DP, s_q + (g % C::QS) * C::NARROW, i > 0, H);
+          product_tokens<W, H>(tmem + C::DK, tmem + C::DP, s_q + (g % C::QS) * C::NARROW, i > 0, H, p.steps);
           tc_commit(ring_q.empty + g % C::QS);
           if (i + 1 == ps.n) tc_commit(done);
         }
@@ -1107,7 +1112,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           ok = take_d(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((g + 1) % C::DS) * C::NARROW);
+            product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((g + 1) % C::DS) * C::NARROW, p.steps);
             tc_commit(dp_full);
             if (i + 2 == ps.n) tc_commit(kv_free);
           }
@@ -1195,7 +1200,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + (it.row0 + kj) * p.dv.token + it.head * p.dv.head;
       __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + (it.row0 + kj) * p.dk.token + it.head * p.dk.head;
 #pragma unroll 1
-      for (int y = part * 32; y < DH; y += C::GROUPS * 32) {
+      for (int y = part * 32; y < DH && y < p.s.dim; y += C::GROUPS * 32) {
         float o[32];
         tmem_ld_32cols(tmem + lanes + C::DV + y, o);
         if (kj < it.len) store_row(dv, o, 1.f, y, p.s.dim);
@@ -1253,6 +1258,7 @@ cudaError_t params_of(const C& c, TcParams* p) {
   p->o = c.o;
   p->lse = const_cast<float*>(c.lse);
   p->scale_log2 = c.s.scale * kLog2e;
+  p->steps = (c.s.dim + 15) / 16;
   p->withhold = c.withhold;
   p->wait_ns = c.wait_ns;
   p->status = c.status;
