@@ -7,10 +7,10 @@
 //   forward  items of NQ query tiles of one head: S = Q K^T, P = exp(S - max),
 //            O += P V, with a running maximum and sum for each row.
 //   dQ       items of a query tile: S = Q K^T, dP = dO V^T, dS = P (dP - delta),
-//            dQ += dS K.
+//            dQ += dS K, and P K, which puts dQ right for what delta is off.
 //   dK, dV   items of a key tile of a kv head, over the query tiles of all heads
 //            that share it: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
-// Making S and dP twice costs 7 products in the place of 5, but every sum has
+// Making S and dP twice costs 8 products in the place of 5, but every sum has
 // one owner: no atomics, no order that changes, no fp32 dQ in memory.
 //
 // All tiles come by TMA through a 3-D map (element, head, token) that knows any
@@ -579,22 +579,27 @@ template <int DH, int W>
 struct DqCfg {
   static constexpr uint32_t TILE = DH / 64 * kChunk, NARROW = DH / 64 * W * 128;  // of the queries, of the keys
   static constexpr int KS = DH == 64 ? 4 : 3, VS = DH == 64 ? 3 : 2;
-  static constexpr uint32_t S = 0, DP = 2 * W, DQ = 3 * W;  // columns: S twice, dP, dQ
-  static constexpr uint32_t TMEM = 3 * W + DH <= 256 ? 256 : 512;
+  static constexpr uint32_t S = 0, DP = W, DQ = 2 * W, KM = 2 * W + DH;  // columns: S, dP, dQ, the mean key
+  static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
   // Softmax warps: 32 columns each. With two of 64 columns a scheduler, the time of a tile is the latency of their steps.
   static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;
   static constexpr int THREADS = (WARPS + 2) * 32;
-  static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 8 + 1);
+  static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 9 + 1);
   static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + (GROUPS + 1) * 512 + BARS;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
-// Tile j: the products of tile j + 1 run while the softmax warps work on j. dS
-// goes over the scores it came from. delta comes in as dO . O with the O that the
-// forward rounded; the row's sum of dS, zero for the exact delta, says how far it
-// is off, and is added to it for the kernel of dK. Rows with a single key tile
-// take their own sum of P dP from the start.
+// P goes over S, dS over dP; the scores of tile j + 1 are made while the threads
+// work on dS of tile j, its dP while they work on P of tile j + 1.
+//
+// delta comes in as dO . O with the O that the forward rounded to bf16, which is
+// as far off as dQ's own rounding. But the row's sum of dS, zero for the exact
+// delta, says how far: e = sum of p dp - delta. dK's kernel gets delta + e, and dQ
+// is put right with the row's mean key, dQ = sum of dS k - e sum of P k: a fourth
+// product, for 0.0023 in the place of 0.0030 as dQ's error (8 x 2048 tokens, 32
+// heads of 128). Rows with a single key tile take their own sum of p dp from the
+// start.
 template <int DH, int W>
 __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
   using C = DqCfg<DH, W>;
@@ -614,13 +619,14 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   bars += 2 * C::VS;
   uint64_t* q_full = bars;       // Q and dO
   uint64_t* q_free = bars + 1;   // the item's S and dP are all made
-  uint64_t* sd_full = bars + 2;  // S and dP of a tile
-  uint64_t* dp_read = bars + 3;  // dP is in registers
-  uint64_t* ds_full = bars + 4;
-  uint64_t* done = bars + 5;     // an item's dQ is there
-  uint64_t* meet = bars + 6;     // the softmax warps' sums are in shared memory
-  uint64_t* drain = bars + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+  uint64_t* s_full = bars + 2;
+  uint64_t* p_full = bars + 3;
+  uint64_t* dp_full = bars + 4;
+  uint64_t* ds_full = bars + 5;
+  uint64_t* done = bars + 6;     // an item's dQ and mean key are there
+  uint64_t* meet = bars + 7;     // the softmax warps' sums are in shared memory
+  uint64_t* drain = bars + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -629,8 +635,9 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
     ring_v.init();
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
-    mbar_init(sd_full, 1);
-    mbar_init(dp_read, C::WARPS);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, C::WARPS);
+    mbar_init(dp_full, 1);
     mbar_init(ds_full, C::WARPS);
     mbar_init(done, 1);
     mbar_init(meet, C::WARPS);
@@ -697,44 +704,70 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
       ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull);
       if (!ok) break;
       ++items;
-      for (int j = 0; j <= n; ++j, ++g) {
-        if (j < n) {
-          ok = ring_k.wait_full(g, guard);
+      // Key tile j of the item at ring position i, its rows of the next sequence cleared.
+      auto take_k = [&](int i, int j) {
+        if (!ring_k.wait_full(i, guard)) return false;
+        if (it.len - j * W < W) clear_rows<DH, W>(s_k + (i % C::KS) * C::NARROW, it.len - j * W, lane);
+        return true;
+      };
+      ok = take_k(g, 0);
+      if (!ok) break;
+      if (elect_one()) {
+        product_rows<DH, W>(tmem + C::S, s_q, s_k + (g % C::KS) * C::NARROW, p.steps);
+        tc_commit(s_full);
+      }
+      __syncwarp();
+      ok = ring_v.wait_full(g, guard);
+      if (!ok) break;
+      if (elect_one()) {
+        product_rows<DH, W>(tmem + C::DP, s_do, s_v + (g % C::VS) * C::NARROW, p.steps);
+        tc_commit(dp_full);
+        tc_commit(ring_v.empty + g % C::VS);
+        if (n == 1) tc_commit(q_free);
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j, ++g) {
+        const uint8_t* k_tile = s_k + (g % C::KS) * C::NARROW;
+        ok = warp_wait(p_full, g & 1, guard, kSiteMmaAcc);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) product_tokens<W, H>(tmem + C::KM, tmem + C::S, k_tile, j > 0, H, p.steps);
+        __syncwarp();
+        if (j + 1 < n) {
+          ok = take_k(g + 1, j + 1);
           if (!ok) break;
-          uint8_t* k_tile = s_k + (g % C::KS) * C::NARROW;
-          if (it.len - j * W < W) clear_rows<DH, W>(k_tile, it.len - j * W, lane);
-          // S over dS of two tiles before, whose product was issued before.
-          if (elect_one()) product_rows<DH, W>(tmem + C::S + (g & 1) * W, s_q, k_tile, p.steps);
-          __syncwarp();
-          ok = ring_v.wait_full(g, guard) && (g == 0 || warp_wait(dp_read, (g - 1) & 1, guard, kSiteMmaAcc));
-          if (!ok) break;
-          tc_fence_after_sync();
           if (elect_one()) {
-            product_rows<DH, W>(tmem + C::DP, s_do, s_v + (g % C::VS) * C::NARROW, p.steps);
-            tc_commit(sd_full);
-            tc_commit(ring_v.empty + g % C::VS);
-            if (j + 1 == n) tc_commit(q_free);
+            product_rows<DH, W>(tmem + C::S, s_q, s_k + ((g + 1) % C::KS) * C::NARROW, p.steps);
+            tc_commit(s_full);
           }
           __syncwarp();
         }
-        if (j > 0) {
-          const int last = g - 1;
-          ok = warp_wait(ds_full, last & 1, guard, kSiteMmaAcc);
+        ok = warp_wait(ds_full, g & 1, guard, kSiteMmaAcc);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          product_tokens<W, H>(tmem + C::DQ, tmem + C::DP, k_tile, j > 0, H, p.steps);
+          tc_commit(ring_k.empty + g % C::KS);
+          if (j + 1 == n) tc_commit(done);
+        }
+        __syncwarp();
+        if (j + 1 < n) {
+          ok = ring_v.wait_full(g + 1, guard);
           if (!ok) break;
-          tc_fence_after_sync();
           if (elect_one()) {
-            product_tokens<W, H>(tmem + C::DQ, tmem + C::S + (last & 1) * W, s_k + (last % C::KS) * C::NARROW, j > 1, H, p.steps);
-            tc_commit(ring_k.empty + last % C::KS);
-            if (j == n) tc_commit(done);
+            product_rows<DH, W>(tmem + C::DP, s_do, s_v + ((g + 1) % C::VS) * C::NARROW, p.steps);
+            tc_commit(dp_full);
+            tc_commit(ring_v.empty + (g + 1) % C::VS);
+            if (j + 2 == n) tc_commit(q_free);
           }
           __syncwarp();
         }
       }
-      --g;  // the pass of the last dS took no tile
     }
   } else {
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + C::S + H * part, t_dp = tmem + lanes + C::DP + H * part;
     int g = 0, met = 0;  // tiles; uses of `meet`
     auto meet_all = [&] {
       __syncwarp();
@@ -791,17 +824,11 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
       ++items;
       float total = 0.f;  // of dS
       for (int j = 0; j < n; ++j, ++g) {
-        ok = warp_wait(sd_full, g & 1, guard, kSiteMmaFull);
+        ok = warp_wait(s_full, g & 1, guard, kSiteMmaFull);
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t t_s = tmem + lanes + C::S + (g & 1) * W + H * part;
-        float s[H], dp[H];
-        tmem_ld<H>(tmem + lanes + C::DP + H * part, dp);
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dp_read);
+        float s[H];
         tmem_ld<H>(t_s, s);
-        const int k0 = j * W;
         const uint64_t c2 = pair(p.scale_log2, p.scale_log2), n2 = pair(nl, nl);
 #pragma unroll
         for (int e = 0; e < H; e += 2) {
@@ -809,13 +836,29 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           s[e] = exp2_fast(s[e]);
           s[e + 1] = exp2_fast(s[e + 1]);
         }
-        if (k0 + W > it.len || (p.s.causal && k0 + W > q0)) {
-          const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;
+        const int k0 = j * W;
+        const bool masked = k0 + W > it.len || (p.s.causal && k0 + W > q0);
+        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;  // columns that count
+        if (masked) {
 #pragma unroll
-          for (int e = 0; e < H; ++e) {
-            s[e] = e < end ? s[e] : 0.f;
-            dp[e] = e < end ? dp[e] : 0.f;
-          }
+          for (int e = 0; e < H; ++e) s[e] = e < end ? s[e] : 0.f;
+        }
+        uint32_t w[H / 2];
+#pragma unroll
+        for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
+        tmem_st_16(t_s, w);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ok = warp_wait(dp_full, g & 1, guard, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after_sync();
+        float dp[H];
+        tmem_ld<H>(t_dp, dp);
+        if (masked) {  // what stands there may be no number
+#pragma unroll
+          for (int e = 0; e < H; ++e) dp[e] = e < end ? dp[e] : 0.f;
         }
         if (n == 1) {
           float sum = 0.f;
@@ -828,7 +871,6 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         }
         uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
         const uint64_t d2 = pair(-delta, -delta);
-        uint32_t w[H / 2];
 #pragma unroll
         for (int e = 0; e < H; e += 2) {
           const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
@@ -837,7 +879,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           unpair(ds, x0, x1);
           w[e / 2] = pack_bf16(x0, x1);
         }
-        tmem_st_16(t_s, w);
+        tmem_st_16(t_dp, w);
         float x0, x1;
         unpair(add_pair(sum[0], sum[1]), x0, x1);
         total += x0 + x1;
@@ -847,24 +889,28 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         if (lane == 0) mbar_arrive(ds_full);
       }
       if (!ok) break;
+      float off = 0.f;  // how far delta is
       if (n > 1) {
         s_sum[part * kRows + row] = total;
         ok = meet_all();
         if (!ok) break;
-        if (part == 0) delta += row_sum<C::GROUPS>(s_sum, row);
+        off = row_sum<C::GROUPS>(s_sum, row);
       }
-      if (part == 0 && qi < it.len) p.delta[at] = delta;
+      if (part == 0 && qi < it.len) p.delta[at] = delta + off;
       ok = warp_wait(done, (items - 1) & 1, guard, kSiteEpilogue);
       if (!ok) break;
       tc_fence_after_sync();
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
 #pragma unroll 1
       for (int x = part * 32; x < DH && x < p.s.dim; x += C::GROUPS * 32) {
-        float v[32];
+        float v[32], k[32];
         tmem_ld_32cols(tmem + lanes + C::DQ + x, v);
+        tmem_ld_32cols(tmem + lanes + C::KM + x, k);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = fmaf(-off, k[e], v[e]);
         if (qi < it.len) store_row(dst, v, p.s.scale, x, p.s.dim);
       }
-      tc_fence_before_sync();  // dQ is in registers; the next item's waits for this warp's next dS
+      tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
     }
   }
   __syncthreads();
