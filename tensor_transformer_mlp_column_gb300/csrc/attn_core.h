@@ -43,7 +43,7 @@ __device__ __forceinline__ int core_sequence(const CoreShape& s, int b, int64_t&
   const int64_t begin = s.starts[b], end = s.starts[b + 1];
   row0 = begin;
   if (begin >= 0 && end >= begin && end <= s.T && end - begin <= s.max_seq) return static_cast<int>(end - begin);
-  if (threadIdx.x == 0) atomicCAS(status, 0, kSiteBoundsBase + kChkSequence);
+  atomicCAS(status, 0, kSiteBoundsBase + kChkSequence);
   return 0;
 }
 

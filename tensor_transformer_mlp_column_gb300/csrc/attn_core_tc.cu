@@ -159,7 +159,10 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
       : "memory");
 }
 
-// N = 32 or 64 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[32]) { tmem_st_32(taddr, v); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) { tmem_st_16(taddr, v); }
+
+// N columns, a multiple of 32, of this warp's lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
   uint32_t r[N / 32][32];
@@ -269,26 +272,124 @@ struct TcParams {
   int* status;
 };
 
-// What a CTA works on. Items of one tile index follow one another, those with
-// the most work first, and a CTA takes one of every gridDim.x, from the front and
-// from the back in turn, so that all get about the same work.
+// What a CTA works on: `rows` tokens (a tile or a run of tiles) of a head of a sequence.
 struct Item {
-  int tile, head, len;
   int64_t row0;
+  int tile, head, len;  // len 0: no more items
 };
-__device__ __forceinline__ bool item_of(const TcParams& p, int round, int heads, bool last_first, Item& it) {
-  const uint32_t g = gridDim.x, place = round & 1 ? g - 1 - blockIdx.x : blockIdx.x;
-  const uint64_t at = uint64_t(round) * g + place;
-  if (at >= p.items) return false;
-  const uint32_t i = static_cast<uint32_t>(at), per = static_cast<uint32_t>(heads) * p.s.batch, in = i % per;
-  it.tile = static_cast<int>(i / per);
-  if (last_first) it.tile = p.tiles - 1 - it.tile;
-  it.head = static_cast<int>(in % heads);
-  it.len = core_sequence(p.s, static_cast<int>(in / heads), it.row0, p.status);
-  return true;
-}
-// The rounds of this CTA.
-__device__ __forceinline__ int rounds_of(const TcParams& p) { return static_cast<int>((p.items + gridDim.x - 1) / gridDim.x); }
+
+// The items of a CTA, found by its loading warp. They are in order of their work, the most first, and a CTA takes one of
+// every gridDim.x, from the front and from the back in turn, so that all get about the same. Of up to 64 sequences of any
+// lengths those in order are the ones with at least d tiles, d from the longest's down (their d-th tile from the front, or
+// from the back); of more, or of equal ones, all tiles of one index, of which those past a sequence's end are skipped.
+// (13 sequences of 1 to 1500 tokens, 12 heads: the fullest CTA of dQ has 49 key tiles this way, 86 the other.)
+struct Walk {
+  const TcParams& p;
+  int heads, rows;
+  bool last_first;  // the last tiles of a sequence have the most work
+  int lane;
+  bool sorted;
+  int c0, c1, d;          // tiles of sequences `lane` and `lane` + 32; those with at least d are next
+  uint32_t m0, m1;        // which these are
+  uint64_t first, count;  // place of their first item, and how many there are
+  uint64_t round = 0;
+
+  __device__ __forceinline__ Walk(const TcParams& p_, int heads_, int rows_, bool last_first_, int lane_)
+      : p(p_), heads(heads_), rows(rows_), last_first(last_first_), lane(lane_), sorted(p_.s.starts && p_.s.batch <= 64) {
+    if (!sorted) return;
+    int64_t row0;
+    c0 = lane < p.s.batch ? (core_sequence(p.s, lane, row0, p.status) + rows - 1) / rows : 0;
+    c1 = lane + 32 < p.s.batch ? (core_sequence(p.s, lane + 32, row0, p.status) + rows - 1) / rows : 0;
+    d = __reduce_max_sync(kAll, max(c0, c1));
+    first = 0;
+    choose();
+  }
+  __device__ __forceinline__ void choose() {
+    m0 = __ballot_sync(kAll, c0 >= d);
+    m1 = __ballot_sync(kAll, c1 >= d);
+    count = static_cast<uint64_t>(__popc(m0) + __popc(m1)) * heads;
+  }
+  // The k-th of a mask's set bits.
+  __device__ __forceinline__ static int bit_of(uint32_t mask, int k) {
+    for (; k > 0; --k) mask &= mask - 1;
+    return __ffs(mask) - 1;
+  }
+  // All lanes together.
+  __device__ __forceinline__ bool next(Item& it) {
+    const uint32_t g = gridDim.x;
+    for (;; ++round) {
+      const uint64_t at = round * g + (round & 1 ? g - 1 - blockIdx.x : blockIdx.x);
+      if (sorted) {
+        while (d > 0 && at >= first + count) {
+          first += count;
+          if (--d > 0) choose();
+        }
+        // Places grow from round to round, whether from the front or the back.
+        if (d <= 0) return false;
+        const uint32_t in = static_cast<uint32_t>(at - first);
+        const int k = in / heads, n0 = __popc(m0);
+        const int b = k < n0 ? bit_of(m0, k) : 32 + bit_of(m1, k - n0);
+        const int c = __shfl_sync(kAll, b < 32 ? c0 : c1, b & 31);
+        it.head = in % heads;
+        it.tile = last_first ? d - 1 : c - d;
+        it.len = core_sequence(p.s, b, it.row0, p.status);
+      } else {
+        if (at >= p.items) return false;
+        const uint32_t i = static_cast<uint32_t>(at), per = static_cast<uint32_t>(heads) * p.s.batch, in = i % per;
+        it.tile = static_cast<int>(i / per);
+        if (last_first) it.tile = p.tiles - 1 - it.tile;
+        it.head = static_cast<int>(in % heads);
+        it.len = core_sequence(p.s, static_cast<int>(in / heads), it.row0, p.status);
+        if (int64_t(it.tile) * rows >= it.len) continue;
+      }
+      ++round;
+      return true;
+    }
+  }
+};
+
+// Items on their way from the loading warp to the others.
+constexpr int kItemSlots = 2;
+constexpr size_t kItemBytes = kItemSlots * (sizeof(Item) + 16);
+struct ItemRing {
+  Item* items;
+  uint64_t *full, *empty;
+  __device__ __forceinline__ explicit ItemRing(void* at)
+      : items(static_cast<Item*>(at)),
+        full(reinterpret_cast<uint64_t*>(items + kItemSlots)),
+        empty(full + kItemSlots) {}
+  __device__ __forceinline__ void init(uint32_t readers) const {
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, readers);
+    }
+  }
+  // The k-th item goes out; all lanes of the loading warp.
+  __device__ __forceinline__ bool give(int k, const Item& it, int lane, const WaitGuard& g) const {
+    if (!warp_wait(empty + k % kItemSlots, ((k / kItemSlots) & 1) ^ 1u, g, kSiteProducer)) return false;
+    if (lane == 0) {
+      items[k % kItemSlots] = it;
+      mbar_arrive(full + k % kItemSlots);
+    }
+    return true;
+  }
+  // The k-th item, or false after the last one or a failure.
+  __device__ __forceinline__ bool take(int k, Item& it, int lane, const WaitGuard& g) const {
+    if (!hold(k, g)) return false;
+    it = items[k % kItemSlots];
+    release(k, lane);
+    return true;
+  }
+  // The same for a warp that reads the item (held()) where it needs it, until it releases it.
+  __device__ __forceinline__ bool hold(int k, const WaitGuard& g) const {
+    return warp_wait(full + k % kItemSlots, (k / kItemSlots) & 1, g, kSiteMmaFull) && held(k).len > 0;
+  }
+  __device__ __forceinline__ const volatile Item& held(int k) const { return items[k % kItemSlots]; }
+  __device__ __forceinline__ void release(int k, int lane) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + k % kItemSlots);
+  }
+};
 
 // Shared memory of a kernel: tiles, then rows of floats, then barriers. There is no slack to align it in: the dynamic
 // shared memory begins on a multiple of 1024 bytes, which the swizzled tiles need, and which is checked.
@@ -307,7 +408,7 @@ struct FwdCfg {
   static constexpr uint32_t TMEM = NQ == 2 ? 512 : 256;
   static constexpr int CTAS = NQ == 1 && DH == 64 ? 2 : 1;  // an SM's
   static constexpr uint32_t O = NQ * 128;  // columns: S of each tile, then O of each
-  static constexpr size_t BARS = 8 * (2 * SLOTS + 3 + 3 * NQ + 1);  // barriers; the last place holds two words
+  static constexpr size_t BARS = 8 * (2 * SLOTS + 3 + 3 * NQ) + kItemBytes + 8;  // barriers, items, two words
   static constexpr size_t SMEM = (NQ + SLOTS) * TILE + BARS;
   static constexpr int THREADS = (4 * NQ + 2) * 32;
   static_assert(O + NQ * DH <= TMEM, "tensor memory");
@@ -335,7 +436,8 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   uint64_t* p_full = s_full + NQ;  // [NQ] its probabilities are there, and O has the new maximum
   uint64_t* o_done = p_full + NQ;  // [NQ] an item's O is there
   uint64_t* drain = o_done + NQ;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const ItemRing ring_i(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -349,6 +451,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
       mbar_init(o_done + a, 1);
     }
     mbar_init(drain, 1);
+    ring_i.init(4 * NQ + 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -360,7 +463,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   pdl_wait();
   pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  const int group = p.s.heads / p.s.kv_heads;
   // Key tiles of the item's query tile a.
   auto tiles_of = [&](const Item& it, int a) {
     const int first = (it.tile * NQ + a) * kRows;
@@ -378,10 +481,10 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   if (warp == kLoad) {
     bool ok = true;
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+    for (Walk walk(p, p.s.heads, NQ * kRows, true, lane); ok && walk.next(it);) {
+      ok = ring_i.give(items, it, lane, guard);
+      if (!ok) break;
       const int n = most_of(it), kv = it.head / group;
-      if (n == 0) continue;
       ok = items == 0 || warp_wait(q_free, (items - 1) & 1, guard, kSiteProducer);
       if (!ok) break;
       if (elect_one()) {
@@ -403,17 +506,17 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
         ++issued;
       }
     }
+    it.len = 0;
+    if (ok) ring_i.give(items, it, lane, guard);
   } else if (warp == kMma) {
     bool ok = true;
     int at = 0;            // ring position of the item's first key tile
     int done[NQ] = {};     // tiles of each query tile so far
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+    for (int i = 0; ok && ring_i.take(i, it, lane, guard); ++i) {
       int n[NQ], n_max = 0;
 #pragma unroll
       for (int a = 0; a < NQ; ++a) n[a] = tiles_of(it, a), n_max = max(n_max, n[a]);
-      if (n_max == 0) continue;
       ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull) && ring.wait_full(at, guard);
       if (!ok) break;
       ++items;
@@ -473,8 +576,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
     bool ok = true;
     int done = 0;  // tiles so far
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+    for (int i = 0; ok && ring_i.take(i, it, lane, guard); ++i) {
       const int tiles = tiles_of(it, a), first = (it.tile * NQ + a) * kRows, qi = first + row;
       if (tiles == 0) continue;
       float m = -INFINITY, l = 0.f;
@@ -582,10 +684,11 @@ struct DqCfg {
   static constexpr uint32_t S = 0, DP = W, DQ = 2 * W, KM = 2 * W + DH;  // columns: S, dP, dQ, the mean key
   static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
-  // Softmax warps: 32 columns each. With two of 64 columns a scheduler, the time of a tile is the latency of their steps.
-  static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;
+  // Columns of a softmax warp: 64, but 32 for short heads, whose tiles are half as wide (8 x 2048 tokens, 32 heads of 128:
+  // 417 us with 64, 434 with 32; 16 heads of 64: 145 and 140).
+  static constexpr int COLUMNS = DH == 64 ? 32 : 64, GROUPS = W / COLUMNS, WARPS = 4 * GROUPS;
   static constexpr int THREADS = (WARPS + 2) * 32;
-  static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 9 + 1);
+  static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 9) + kItemBytes + 8;
   static constexpr size_t SMEM = 2 * TILE + (KS + VS) * NARROW + (GROUPS + 1) * 512 + BARS;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
@@ -626,7 +729,8 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   uint64_t* done = bars + 6;     // an item's dQ and mean key are there
   uint64_t* meet = bars + 7;     // the softmax warps' sums are in shared memory
   uint64_t* drain = bars + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
+  const ItemRing ring_i(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -642,6 +746,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
     mbar_init(done, 1);
     mbar_init(meet, C::WARPS);
     mbar_init(drain, 1);
+    ring_i.init(C::WARPS + 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -653,7 +758,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   pdl_wait();
   pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  const int group = p.s.heads / p.s.kv_heads;
   // Key tiles of an item.
   auto tiles_of = [&](const Item& it) {
     const int q0 = it.tile * kRows;
@@ -664,10 +769,10 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   if (warp == kLoadWarp) {
     bool ok = true;
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+    for (Walk walk(p, p.s.heads, kRows, true, lane); ok && walk.next(it);) {
+      ok = ring_i.give(items, it, lane, guard);
+      if (!ok) break;
       const int n = tiles_of(it), kv = it.head / group;
-      if (n == 0) continue;
       ok = items == 0 || warp_wait(q_free, (items - 1) & 1, guard, kSiteProducer);
       if (!ok) break;
       if (elect_one()) {
@@ -693,14 +798,14 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         ++issued_v;
       }
     }
+    it.len = 0;
+    if (ok) ring_i.give(items, it, lane, guard);
   } else if (warp == kMmaWarp) {
     bool ok = true;
     int g = 0;  // tiles so far
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
+    for (int i = 0; ok && ring_i.take(i, it, lane, guard); ++i) {
       const int n = tiles_of(it);
-      if (n == 0) continue;
       ok = warp_wait(q_full, items & 1, guard, kSiteMmaFull);
       if (!ok) break;
       ++items;
@@ -775,13 +880,11 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
       return warp_wait(meet, met++ & 1, guard, kSiteEpilogue);
     };
     bool ok = true;
-    Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.heads, p.s.causal, it)) continue;
-      const int n = tiles_of(it), q0 = it.tile * kRows, qi = q0 + row;
-      if (n == 0) continue;
-      const int64_t at = int64_t(it.head) * p.s.T + it.row0 + min(qi, it.len - 1);
-      const float nl = -p.lse[at] * kLog2e;
+    for (int i = 0; ok && ring_i.hold(i, guard); ++i) {
+      const volatile Item& it = ring_i.held(i);
+      const int len = it.len, q0 = it.tile * kRows, qi = q0 + row;
+      const int n = ((p.s.causal ? min(len, q0 + kRows) : len) + W - 1) / W;
+      const float nl = -p.lse[int64_t(it.head) * p.s.T + it.row0 + min(qi, len - 1)] * kLog2e;
       float delta = 0.f;
       if (n > 1) {
         // delta of 128 / WARPS rows by each warp: eight lanes a row, whole lines of O from memory, dO from its tile. (Asked
@@ -793,7 +896,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         for (int x = 0; x < N; ++x) {
           const int y = (warp * R + x % R) * 4 + (lane >> 3), e = (x / R) * 64 + (lane & 7) * 8;
           o[x] = make_uint4(0, 0, 0, 0);
-          if (q0 + y < it.len && e < p.s.dim)
+          if (q0 + y < len && e < p.s.dim)
             o[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o.p) + (it.row0 + q0 + y) * p.o.token +
                                                    it.head * p.o.head + e);
         }
@@ -837,8 +940,8 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           s[e + 1] = exp2_fast(s[e + 1]);
         }
         const int k0 = j * W;
-        const bool masked = k0 + W > it.len || (p.s.causal && k0 + W > q0);
-        const int end = (p.s.causal ? min(it.len, qi + 1) : it.len) - k0 - H * part;  // columns that count
+        const bool masked = k0 + W > len || (p.s.causal && k0 + W > q0);
+        const int end = (p.s.causal ? min(len, qi + 1) : len) - k0 - H * part;  // columns that count
         if (masked) {
 #pragma unroll
           for (int e = 0; e < H; ++e) s[e] = e < end ? s[e] : 0.f;
@@ -846,7 +949,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         uint32_t w[H / 2];
 #pragma unroll
         for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
-        tmem_st_16(t_s, w);
+        tmem_st(t_s, w);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -879,7 +982,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
           unpair(ds, x0, x1);
           w[e / 2] = pack_bf16(x0, x1);
         }
-        tmem_st_16(t_dp, w);
+        tmem_st(t_dp, w);
         float x0, x1;
         unpair(add_pair(sum[0], sum[1]), x0, x1);
         total += x0 + x1;
@@ -896,11 +999,14 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         if (!ok) break;
         off = row_sum<C::GROUPS>(s_sum, row);
       }
-      if (part == 0 && qi < it.len) p.delta[at] = delta + off;
+      const int64_t row0 = it.row0;
+      const int head = it.head;
+      ring_i.release(i, lane);
+      if (part == 0 && qi < len) p.delta[int64_t(head) * p.s.T + row0 + qi] = delta + off;
       ok = warp_wait(done, (items - 1) & 1, guard, kSiteEpilogue);
       if (!ok) break;
       tc_fence_after_sync();
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (it.row0 + qi) * p.dq.token + it.head * p.dq.head;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.p) + (row0 + qi) * p.dq.token + head * p.dq.head;
 #pragma unroll 1
       for (int x = part * 32; x < DH && x < p.s.dim; x += C::GROUPS * 32) {
         float v[32], k[32];
@@ -908,7 +1014,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         tmem_ld_32cols(tmem + lanes + C::KM + x, k);
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = fmaf(-off, k[e], v[e]);
-        if (qi < it.len) store_row(dst, v, p.s.scale, x, p.s.dim);
+        if (qi < len) store_row(dst, v, p.s.scale, x, p.s.dim);
       }
       tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
     }
@@ -942,9 +1048,10 @@ struct DkvCfg {
   static constexpr uint32_t S = 0, DP = W, DV = 2 * W, DK = 2 * W + DH;
   static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
-  static constexpr int WARPS = W / 8, GROUPS = WARPS / 4, COLUMNS = W / GROUPS;  // softmax warps, as in dQ
-  static constexpr int THREADS = (WARPS + 3) * 32;
-  static constexpr size_t BARS = 8 * (2 * QS + 2 * DS + 2 * RS + 8 + 1);
+  // Columns of a softmax warp: 64 (8 x 2048 tokens, 32 heads of 128: 370 us, with 32 385; 16 heads of 64: 154 and 154).
+  static constexpr int COLUMNS = 64, GROUPS = W / COLUMNS, WARPS = 4 * GROUPS;
+  static constexpr int THREADS = (WARPS + 2) * 32;
+  static constexpr size_t BARS = 8 * (2 * QS + 2 * DS + 2 * RS + 8) + kItemBytes + 8;
   static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + BARS;
   static_assert(SMEM <= 227 * 1024 && CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
@@ -957,7 +1064,6 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     dkv_kernel(const __grid_constant__ TcParams p) {
   using C = DkvCfg<DH, W>;
   constexpr int H = C::COLUMNS, kMmaWarp = C::WARPS, kLoadWarp = C::WARPS + 1;
-  constexpr int kRowWarp = C::WARPS + 2;  // lse and delta of the queries
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(smem, p.status)) return;
   uint8_t* s_k = smem;
@@ -980,7 +1086,8 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   uint64_t* ds_full = bars + 5;
   uint64_t* done = bars + 6;  // an item's dK and dV are there
   uint64_t* drain = bars + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+  const ItemRing ring_i(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -996,6 +1103,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     mbar_init(ds_full, C::WARPS);
     mbar_init(done, 1);
     mbar_init(drain, 1);
+    ring_i.init(C::WARPS + 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -1007,7 +1115,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   pdl_wait();
   pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
-  const int group = p.s.heads / p.s.kv_heads, rounds = rounds_of(p);
+  const int group = p.s.heads / p.s.kv_heads;
   // Query tiles of an item: `per` from `first` on of every head of the group, head by head.
   struct Passes {
     int first, per, n;
@@ -1024,10 +1132,10 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   if (warp == kLoadWarp) {
     bool ok = true;
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+    for (Walk walk(p, p.s.kv_heads, kRows, false, lane); ok && walk.next(it);) {
+      ok = ring_i.give(items, it, lane, guard);
+      if (!ok) break;
       const Passes ps = passes_of(it);
-      if (ps.n == 0) continue;
       ok = items == 0 || warp_wait(kv_free, (items - 1) & 1, guard, kSiteProducer);
       if (!ok) break;
       if (elect_one()) {
@@ -1036,7 +1144,21 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         load_tile<DH>(s_v, &p.v, it.head, it.row0 + it.tile * kRows, kv_full);
       }
       ++items;
+      // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them, a pass ahead of their store.
+      float nl[W / 32], nd[W / 32];
+      auto fetch = [&](int h, int x) {
+        const int q0 = (ps.first + x) * W;
+        const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
+#pragma unroll
+        for (int y = 0; y < W / 32; ++y) {
+          const int q = y * 32 + lane;
+          const bool on = q0 + q < it.len;
+          nl[y] = on ? -p.lse[at + q] * kLog2e : 0.f;
+          nd[y] = on ? -p.delta[at + q] : 0.f;
+        }
+      };
       int h = it.head * group, x = 0;  // head and query tile of pass i
+      fetch(h, x);
       for (int i = 0; i < ps.n; ++i) {
         const int64_t row = it.row0 + (ps.first + x) * W;
         ok = ring_q.wait_empty(issued_q, guard);
@@ -1045,6 +1167,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           mbar_arrive_expect_tx(ring_q.full + issued_q % C::QS, C::NARROW);
           load_tile<DH, W>(s_q + (issued_q % C::QS) * C::NARROW, &p.q, h, row, ring_q.full + issued_q % C::QS);
         }
+        __syncwarp();
         ++issued_q;
         ok = ring_d.wait_empty(issued_d, guard);
         if (!ok) break;
@@ -1052,50 +1175,29 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           mbar_arrive_expect_tx(ring_d.full + issued_d % C::DS, C::NARROW);
           load_tile<DH, W>(s_do + (issued_d % C::DS) * C::NARROW, &p.d_o, h, row, ring_d.full + issued_d % C::DS);
         }
-        ++issued_d;
-        if (++x == ps.per) x = 0, ++h;
-      }
-    }
-  } else if (warp == kRowWarp) {
-    // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them.
-    bool ok = true;
-    int g = 0;  // passes so far
-    Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
-      const Passes ps = passes_of(it);
-      int h = it.head * group, x = 0;
-      for (int i = 0; i < ps.n; ++i, ++g) {
-        const int q0 = (ps.first + x) * W;
-        const int64_t at = int64_t(h) * p.s.T + it.row0 + q0;
-        float nl[W / 32], nd[W / 32];
-#pragma unroll
-        for (int y = 0; y < W / 32; ++y) {
-          const int q = y * 32 + lane;
-          const bool on = q0 + q < it.len;
-          nl[y] = on ? -p.lse[at + q] * kLog2e : 0.f;
-          nd[y] = on ? -p.delta[at + q] : 0.f;
-        }
-        ok = ring_r.wait_empty(g, guard);
+        __syncwarp();
+        ok = ring_r.wait_empty(issued_d, guard);
         if (!ok) break;
-        float* rows = s_row + (g % C::RS) * 2 * W;
+        float* rows = s_row + (issued_d % C::RS) * 2 * W;
 #pragma unroll
         for (int y = 0; y < W / 32; ++y) {
           rows[y * 32 + lane] = nl[y];
           rows[W + y * 32 + lane] = nd[y];
         }
-        mbar_arrive(ring_r.full + g % C::RS);
+        mbar_arrive(ring_r.full + issued_d % C::RS);
+        ++issued_d;
         if (++x == ps.per) x = 0, ++h;
+        if (i + 1 < ps.n) fetch(h, x);
       }
     }
+    it.len = 0;
+    if (ok) ring_i.give(items, it, lane, guard);
   } else if (warp == kMmaWarp) {
     bool ok = true;
     int g = 0;  // passes so far
     Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
+    for (int i = 0; ok && ring_i.take(i, it, lane, guard); ++i) {
       const Passes ps = passes_of(it);
-      if (ps.n == 0) continue;
       // Position i of a ring (query tile x), its rows of the next sequence cleared.
       auto take_q = [&](int i, int x) {
         if (!ring_q.wait_full(i, guard)) return false;
@@ -1172,16 +1274,12 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     const uint32_t t_s = tmem + lanes + C::S + H * part, t_dp = tmem + lanes + C::DP + H * part;
     bool ok = true;
     int g = 0;  // passes so far
-    Item it;
-    for (int r = 0; ok && r < rounds; ++r) {
-      if (!item_of(p, r, p.s.kv_heads, false, it)) continue;
-      const Passes ps = passes_of(it);
-      if (ps.n == 0) continue;
-      const int k0 = it.tile * kRows, kj = k0 + row;
-      int x = 0;
-      for (int i = 0; i < ps.n; ++i, ++g) {
-        const int q0 = (ps.first + x) * W + H * part;  // of this warp's columns
-        if (++x == ps.per) x = 0;
+    for (int i = 0; ok && ring_i.hold(i, guard); ++i) {
+      const volatile Item& it = ring_i.held(i);
+      const int len = it.len, k0 = it.tile * kRows, kj = k0 + row;
+      const int first = p.s.causal ? k0 : 0;  // a multiple of W
+      int q0 = first + H * part;              // of this warp's columns
+      for (int left = ((len - first + W - 1) / W) * group; left > 0; --left, ++g) {
         const float* rows = s_row + (g % C::RS) * 2 * W + H * part;
         ok = ring_r.wait_full(g, guard) && warp_wait(s_full, g & 1, guard, kSiteMmaFull);
         if (!ok) break;
@@ -1197,7 +1295,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
 #pragma unroll
           for (int y = 0; y < 4; ++y) s[e + y] = exp2_fast(s[e + y]);
         }
-        const int begin = p.s.causal ? kj - q0 : 0, end = it.len - q0;  // columns that count
+        const int begin = p.s.causal ? kj - q0 : 0, end = len - q0;  // columns that count
         const bool masked = end < H || (p.s.causal && q0 < k0 + kRows);
         if (masked) {
 #pragma unroll
@@ -1206,7 +1304,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         uint32_t w[H / 2];
 #pragma unroll
         for (int e = 0; e < H; e += 2) w[e / 2] = pack_bf16(s[e], s[e + 1]);
-        tmem_st_16(t_s, w);
+        tmem_st(t_s, w);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -1229,7 +1327,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           w[e / 2] = pack_bf16(x0, x1);
           w[e / 2 + 1] = pack_bf16(x2, x3);
         }
-        tmem_st_16(t_dp, w);
+        tmem_st(t_dp, w);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -1237,21 +1335,26 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           mbar_arrive(ds_full);
           mbar_arrive(ring_r.empty + g % C::RS);
         }
+        q0 += W;
+        if (q0 - H * part >= len) q0 = first + H * part;  // the next head's first
       }
       if (!ok) break;
+      const int64_t at = it.row0 + kj;
+      const int head = it.head;
+      ring_i.release(i, lane);
       ok = warp_wait(done, items & 1, guard, kSiteEpilogue);
       if (!ok) break;
       ++items;
       tc_fence_after_sync();
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + (it.row0 + kj) * p.dv.token + it.head * p.dv.head;
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + (it.row0 + kj) * p.dk.token + it.head * p.dk.head;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + at * p.dv.token + head * p.dv.head;
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + at * p.dk.token + head * p.dk.head;
 #pragma unroll 1
       for (int y = part * 32; y < DH && y < p.s.dim; y += C::GROUPS * 32) {
         float o[32];
         tmem_ld_32cols(tmem + lanes + C::DV + y, o);
-        if (kj < it.len) store_row(dv, o, 1.f, y, p.s.dim);
+        if (kj < len) store_row(dv, o, 1.f, y, p.s.dim);
         tmem_ld_32cols(tmem + lanes + C::DK + y, o);
-        if (kj < it.len) store_row(dk, o, p.s.scale, y, p.s.dim);
+        if (kj < len) store_row(dk, o, p.s.scale, y, p.s.dim);
       }
       tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
     }

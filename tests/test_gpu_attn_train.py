@@ -163,6 +163,16 @@ def test_lengths(tp, lengths, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("count", [31, 32, 33, 63, 64, 65, 150])
+def test_many_sequences(tp, count, causal, dtype):
+    # Up to 64 sequences are handed out by their lengths, more of them tile by tile.
+    lengths = [(37 * i * i + 11 * i) % 300 for i in range(count)]
+    lengths[count // 2] = 700
+    _check(tp, lengths, 2, 1, 64 if count % 2 else 128, dtype, causal, seed=count)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [8, 16, 24, 40, 56, 64, 72, 80, 96, 120, 128])
 def test_head_sizes(tp, dim, dtype):
     _check(tp, [150, 33], 2, 1, dim, dtype, True, seed=dim)
