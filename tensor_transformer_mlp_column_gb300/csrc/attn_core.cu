@@ -217,17 +217,17 @@ __host__ __device__ constexpr int tile_floats() {
 }
 
 // Queries, then two buffers of keys and values, then the probabilities.
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 constexpr size_t forward_smem() {
-  return sizeof(float) * (tile_floats<DH, ROWS>() + 4 * tile_floats<DH, kWide>() + ROWS * kPitchP);
+  return sizeof(float) * (tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + ROWS * kPitchP);
 }
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_constant__ CoreForward c) {
   constexpr int THREADS = 4 * ROWS, W = tile_floats<DH, kWide>();
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
-  float* skv = sq + tile_floats<DH, ROWS>();  // [2][2]
-  float* sp = skv + 4 * W;
+  float* skv = sq + tile_floats<DH, ROWS>();  // [BUFS][2]
+  float* sp = skv + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
   int tile, h, b;
@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_con
   const int kv = h / (c.s.heads / c.s.kv_heads);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   auto copy = [&](int n) {
-    copy_tile<DH, kWide, THREADS>(skv + (n & 1) * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(skv + (n & 1) * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
     copies_commit();
   };
   copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
@@ -252,14 +252,15 @@ __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_con
   for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
   const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
   for (int n = 0; n < tiles; ++n) {
-    if (n + 1 < tiles) {
+    if (BUFS == 1 && n > 0) copy(n);
+    if (BUFS == 2 && n + 1 < tiles) {
       copy(n + 1);
       copies_wait<1>();
     } else {
       copies_wait<0>();
     }
     __syncthreads();
-    const float* sk = skv + (n & 1) * 2 * W;
+    const float* sk = skv + n % BUFS * 2 * W;
     const int k0 = n * kWide;
     float s[4][4];
     dot_tiles<DH, 16>(s, sq, sk, ty, tx);
@@ -343,18 +344,18 @@ __device__ __forceinline__ void probabilities(const CoreShape& c, float (&s)[4][
 }
 
 // Keys and values, then two buffers of queries and dO, then P, and in its place dS.
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 constexpr size_t dkv_smem() {
-  return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 4 * tile_floats<DH, kWide>() + kWide * (ROWS + 4));
+  return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + kWide * (ROWS + 4));
 }
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   constexpr int THREADS = 4 * ROWS, TX = ROWS / 4, W = tile_floats<DH, kWide>(), PITCH = ROWS + 4;
   extern __shared__ __align__(16) float smem[];
   float* sk = smem;
   float* sv = sk + tile_floats<DH, ROWS>();
-  float* sqd = sv + tile_floats<DH, ROWS>();  // [2][2]
-  float* sp = sqd + 4 * W;
+  float* sqd = sv + tile_floats<DH, ROWS>();  // [BUFS][2]
+  float* sp = sqd + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
   int tile, kv, b;
@@ -370,8 +371,8 @@ __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constan
   const int per = (len + kWide - 1) / kWide - first, passes = per * group;
   auto copy = [&](int n) {
     const int h = kv * group + n / per, q0 = (first + n % per) * kWide;
-    copy_tile<DH, kWide, THREADS>(sqd + (n & 1) * 2 * W, c.q, row0, q0, len, h, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(sqd + (n & 1) * 2 * W + W, c.d_o, row0, q0, len, h, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W, c.q, row0, q0, len, h, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W + W, c.d_o, row0, q0, len, h, c.s.dim);
     copies_commit();
   };
   copy_tile<DH, ROWS, THREADS>(sk, c.k, row0, k0, len, kv, c.s.dim);
@@ -389,14 +390,15 @@ __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constan
       lse[i] = c.lse[at];
       del[i] = delta[at];
     }
-    if (n + 1 < passes) {
+    if (BUFS == 1 && n > 0) copy(n);
+    if (BUFS == 2 && n + 1 < passes) {
       copy(n + 1);
       copies_wait<1>();
     } else {
       copies_wait<0>();
     }
     __syncthreads();
-    const float* sq = sqd + (n & 1) * 2 * W;
+    const float* sq = sqd + n % BUFS * 2 * W;
     float s[4][4], dp[4][4], ds[4][4];
     dot_tiles<DH, TX>(s, sq, sk, sy, sx);
     dot_tiles<DH, TX>(dp, sq + W, sv, sy, sx);
@@ -422,18 +424,18 @@ __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constan
 }
 
 // Queries and dO, then two buffers of keys and values, then dS.
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 constexpr size_t dq_smem() {
-  return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 4 * tile_floats<DH, kWide>() + ROWS * kPitchP);
+  return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + ROWS * kPitchP);
 }
-template <int DH, int ROWS>
+template <int DH, int ROWS, int BUFS>
 __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   constexpr int THREADS = 4 * ROWS, W = tile_floats<DH, kWide>();
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
   float* sd = sq + tile_floats<DH, ROWS>();
-  float* skv = sd + tile_floats<DH, ROWS>();  // [2][2]
-  float* ss = skv + 4 * W;
+  float* skv = sd + tile_floats<DH, ROWS>();  // [BUFS][2]
+  float* ss = skv + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
   int tile, h, b;
@@ -445,8 +447,8 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
   const int kv = h / (c.s.heads / c.s.kv_heads);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   auto copy = [&](int n) {
-    copy_tile<DH, kWide, THREADS>(skv + (n & 1) * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(skv + (n & 1) * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
+    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
     copies_commit();
   };
   copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
@@ -463,14 +465,15 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
   clear<DH>(dq);
   const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
   for (int n = 0; n < tiles; ++n) {
-    if (n + 1 < tiles) {
+    if (BUFS == 1 && n > 0) copy(n);
+    if (BUFS == 2 && n + 1 < tiles) {
       copy(n + 1);
       copies_wait<1>();
     } else {
       copies_wait<0>();
     }
     __syncthreads();
-    const float* sk = skv + (n & 1) * 2 * W;
+    const float* sk = skv + n % BUFS * 2 * W;
     float s[4][4], dp[4][4], ds[4][4];
     dot_tiles<DH, 16>(s, sq, sk, ty, tx);
     dot_tiles<DH, 16>(dp, sd, sk + W, ty, tx);
@@ -498,18 +501,21 @@ cudaError_t launch(const CoreShape& s, int rows, int heads, size_t smem, cudaStr
 
 template <int DH, int ROWS>
 cudaError_t simt_forward(const CoreForward& c, cudaStream_t s) {
-  return launch<core_forward_kernel<DH, ROWS>>(c.s, ROWS, c.s.heads, forward_smem<DH, ROWS>(), s, c);
+  return launch<core_forward_kernel<DH, ROWS, 2>>(c.s, ROWS, c.s.heads, forward_smem<DH, ROWS, 2>(), s, c);
 }
 
-template <int DH, int ROWS>
-cudaError_t simt_backward(const CoreBackward& c, const float* delta, cudaStream_t s) {
-  {
-    TraceScope trace("attn_core_dkv", s);
-    cudaError_t e = launch<core_dkv_kernel<DH, ROWS>>(c.s, ROWS, c.s.kv_heads, dkv_smem<DH, ROWS>(), s, c, delta);
-    if (e != cudaSuccess) return e;
-  }
-  TraceScope trace("attn_core_dq", s);
-  return launch<core_dq_kernel<DH, ROWS>>(c.s, ROWS, c.s.heads, dq_smem<DH, ROWS>(), s, c, delta);
+template <int DH, int ROWS, int BUFS>
+cudaError_t simt_dkv(const CoreBackward& c, const float* delta, cudaStream_t s) {
+  return launch<core_dkv_kernel<DH, ROWS, BUFS>>(c.s, ROWS, c.s.kv_heads, dkv_smem<DH, ROWS, BUFS>(), s, c, delta);
+}
+template <int DH, int ROWS, int BUFS>
+cudaError_t simt_dq(const CoreBackward& c, const float* delta, cudaStream_t s) {
+  return launch<core_dq_kernel<DH, ROWS, BUFS>>(c.s, ROWS, c.s.heads, dq_smem<DH, ROWS, BUFS>(), s, c, delta);
+}
+
+// CTAs of `rows` tokens of each head and sequence that fill the GPU four times over.
+bool many(const CoreShape& s, int rows, int heads) {
+  return int64_t((s.max_seq + rows - 1) / rows) * heads * s.batch >= 4 * num_sms();
 }
 
 }  // namespace
@@ -523,8 +529,7 @@ cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {
   // 1024 tokens: 239 us with 64 rows, 282 with 32; 8 heads, 4 x 384: 40 and 33. Longer heads fill an SM's shared memory
   // either way, and 64 rows bring twice the warps (16 heads of 128, 4 x 1024: 461 us and 621; 8 heads, 2 x 512: 70 and 91).
   if (c.s.dim > 64) return simt_forward<128, 64>(c, s);
-  const int64_t items = int64_t((c.s.max_seq + 63) / 64) * c.s.heads * c.s.batch;
-  return items >= 4 * num_sms() ? simt_forward<64, 64>(c, s) : simt_forward<64, 32>(c, s);
+  return many(c.s, 64, c.s.heads) ? simt_forward<64, 64>(c, s) : simt_forward<64, 32>(c, s);
 }
 
 cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
@@ -537,8 +542,21 @@ cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   // As in the forward, but the backward of short heads stays ahead with 32 rows (16 heads of 64, 4 x 1024 tokens: 893 us
-  // and 950 with 64; 16 heads of 128: 2050 with 32 and 1780 with 64).
-  return c.s.dim <= 64 ? simt_backward<64, 32>(c, delta, s) : simt_backward<128, 64>(c, delta, s);
+  // and 950 with 64; 16 heads of 128: 2050 with 32 and 1780 with 64). A second buffer takes the copies' time out of the
+  // loop, but without it four CTAs fit an SM in the place of two, and the others' work hides the copies: better where there
+  // are that many (the same 16 heads of 64: 815 us with one buffer, 893 with two; 8 heads, 4 x 384: 107 and 97).
+  const bool small = c.s.dim <= 64;
+  {
+    TraceScope trace("attn_core_dkv", s);
+    cudaError_t e = !small                         ? simt_dkv<128, 64, 2>(c, delta, s)
+                    : many(c.s, 32, c.s.kv_heads) ? simt_dkv<64, 32, 1>(c, delta, s)
+                                                  : simt_dkv<64, 32, 2>(c, delta, s);
+    if (e != cudaSuccess) return e;
+  }
+  TraceScope trace("attn_core_dq", s);
+  return !small                      ? simt_dq<128, 64, 2>(c, delta, s)
+         : many(c.s, 32, c.s.heads) ? simt_dq<64, 32, 1>(c, delta, s)
+                                    : simt_dq<64, 32, 2>(c, delta, s);
 }
 
 }  // namespace tpmlp
