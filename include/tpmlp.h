@@ -465,10 +465,10 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  *             claim (starts that go back) is undefined.
  *   scale     finite, > 0 (1 / sqrt(head_dim) is usual).
  *   lse       device fp32 [heads, T]; tpmlp_attn_core_backward needs it.
- * Rows of no sequence are neither read nor written, whatever they hold. A value
- * that is not finite spreads within its own sequence only.
- * Products, maxima and sums in fp32; bf16 rounds the probabilities (at most 1,
- * or 2^8 while a row's maximum still grows) to bf16 as an operand, and o once. */
+ * Rows of no sequence are left as they were, and it does not matter what they
+ * hold. A value that is not finite spreads within its own sequence only.
+ * Products, maxima and sums in fp32; bf16 rounds the probabilities to bf16 as an
+ * operand (their sum is of the unrounded ones), and o once. Bitwise reproducible. */
 int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* starts,
                             int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
                             int causal, tpmlp_dtype dt, void* o, float* lse, tpmlp_stream_t stream);
@@ -488,11 +488,24 @@ size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int h
  *   strides   of q, k, v, o, do, dq, dk, dv.
  *   workspace at least tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim, dt) bytes.
  * Every sum has a fixed order: bitwise reproducible. bf16 rounds p and ds to bf16
- * as operands and each result once. */
+ * as operands and each result once; what delta is off because o was rounded is
+ * found as the sum of a row's ds and taken out of ds's products again. */
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
                              const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq,
                              int heads, int kv_heads, int head_dim, float scale, int causal, tpmlp_dtype dt, void* dq,
                              void* dk, void* dv, void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* Test hook for the time limits inside the bf16 kernels of the two calls above:
+ * one sequence of T tokens, no mask, tensors [T, heads, head_dim] without gaps,
+ * with load number `load` (1-based, counted by each CTA) of the keys and values
+ * (dK and dV: of the queries) never issued and a wait limit of limit_ms (1..10000).
+ * Every CTA that reaches that load gives up, drains its copies and MMAs, frees its
+ * tensor memory and records TPMLP_ERR_TIMEOUT for the next tpmlp_check_status();
+ * outputs are left partly written. backward = 0: the forward, which writes o and
+ * lse (the other pointers are not looked at); else both kernels of the backward. */
+int tpmlp_selftest_attn_core_timeout(const void* q, const void* k, const void* v, void* o, float* lse, const void* d_o,
+                                     int64_t T, int heads, int head_dim, void* dq, void* dk, void* dv, void* workspace,
+                                     size_t workspace_bytes, int backward, int load, int limit_ms, tpmlp_stream_t stream);
 
 /* The norm of every head of q and k, and the rotation of its pairs by their
  * tokens' positions:

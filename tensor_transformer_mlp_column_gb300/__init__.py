@@ -99,6 +99,7 @@ SIGNATURES = {
     "tpmlp_attn_core_forward": (_I, [_P] * 5 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I, _P, _P, _P]),
     "tpmlp_attn_core_workspace_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
     "tpmlp_attn_core_backward": (_I, [_P] * 8 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I] + [_P] * 4 + [_SZ, _P]),
+    "tpmlp_selftest_attn_core_timeout": (_I, [_P] * 6 + [_I64, _I, _I] + [_P] * 4 + [_SZ, _I, _I, _I, _P]),
     "tpmlp_qk_rope_forward": (_I, [_P] * 5 + [ctypes.c_float] + [_P] * 3 + [_I64] + [_I] * 7 + [_P] * 3),
     "tpmlp_qk_rope_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
     "tpmlp_qk_rope_backward": (_I, [_P] * 7 + [ctypes.c_float] + [_P] * 3 + [_I64] + [_I] * 7 + [_P] * 5 + [_SZ, _P]),
@@ -1067,3 +1068,19 @@ def tpmlp_selftest_xent_stage_timeout(X: torch.Tensor, W: torch.Tensor, targets:
         ws, wp, wn = _space(_xent_workspace(dev, T, D, V, dt, 0), None, dev)
         _check(l.tpmlp_selftest_xent_stage_timeout(x, w, t, T, D, V, dt, lp, ep, stage, limit_ms, wp, wn, on.raw),
                "tpmlp_selftest_xent_stage_timeout")
+
+
+def tpmlp_selftest_attn_core_timeout(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, backward: bool, load: int,
+                                     limit_ms: int, stream=None) -> None:
+    """Runs the bf16 attention's forward or backward on one sequence with load `load` of every CTA withheld (test hook)."""
+    T, heads, dim = q.shape
+    with _On(stream) as on:
+        q, k, v = (t.contiguous() for t in (q, k, v))
+        o, do, dq, dk, dv = (torch.zeros_like(q) for _ in range(5))
+        lse = torch.zeros((heads, T), dtype=torch.float32, device="cuda")
+        ws, wp, wn = _space(_core_workspace(T, heads, heads, dim, TPMLP_BF16), None, on.dev)
+        p = [_ptr(t, on.dev, "q, k or v") for t in (q, k, v)]
+        _check(lib().tpmlp_selftest_attn_core_timeout(*p, o.data_ptr(), lse.data_ptr(), do.data_ptr(), T, heads, dim,
+                                                      dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wn,
+                                                      1 if backward else 0, load, limit_ms, on.raw),
+               "tpmlp_selftest_attn_core_timeout")

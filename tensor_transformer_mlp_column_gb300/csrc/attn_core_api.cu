@@ -114,6 +114,67 @@ CoreShape core_shape(const int32_t* starts, int64_t T, int64_t batch, int64_t ma
                    causal != 0};
 }
 
+// The load that every CTA withholds (test hook; 0: none), and the limit of a wait.
+struct Hook {
+  int withhold;
+  uint64_t limit_ns;
+};
+
+int core_forward(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* starts,
+                            int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
+                            int causal, tpmlp_dtype dt, void* o, float* lse, Hook hook, cudaStream_t stream) {
+  int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
+  if (rc) return rc;
+  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
+  CoreForward c{};
+  VIEW(c.q, q, 0, "q", heads);
+  VIEW(c.k, k, 1, "k", kv_heads);
+  VIEW(c.v, v, 2, "v", kv_heads);
+  VIEW(c.o, o, 3, "o", heads);
+  if (!lse || !aligned(lse, 4)) return set_error(lse ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "lse must not be NULL and 4-byte aligned");
+  if ((rc = current_sm103())) return rc;
+  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  c.lse = lse;
+  c.bf16 = dt == TPMLP_BF16;
+  c.withhold = hook.withhold;
+  c.wait_ns = hook.limit_ns;
+  c.status = device_status_word();
+  CORE_TRY(run_core_forward(c, stream));
+  return TPMLP_OK;
+}
+
+int core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                             const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq,
+                             int heads, int kv_heads, int head_dim, float scale, int causal, tpmlp_dtype dt, void* dq,
+                             void* dk, void* dv, void* ws, size_t ws_bytes, Hook hook, cudaStream_t stream) {
+  int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
+  if (rc) return rc;
+  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
+  CoreBackward c{};
+  VIEW(c.q, q, 0, "q", heads);
+  VIEW(c.k, k, 1, "k", kv_heads);
+  VIEW(c.v, v, 2, "v", kv_heads);
+  VIEW(c.o, o, 3, "o", heads);
+  VIEW(c.d_o, d_o, 4, "do", heads);
+  VIEW(c.dq, dq, 5, "dq", heads);
+  VIEW(c.dk, dk, 6, "dk", kv_heads);
+  VIEW(c.dv, dv, 7, "dv", kv_heads);
+  if (!lse || !ws) return set_error(TPMLP_ERR_ARG, "lse and workspace must not be NULL");
+  if (!aligned(lse, 4) || !aligned(ws, 16)) return set_error(TPMLP_ERR_ALIGN, "workspace must be 16-byte aligned, lse 4");
+  const size_t need = core_backward_workspace(T, heads);
+  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if ((rc = current_sm103())) return rc;
+  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  c.lse = lse;
+  c.bf16 = dt == TPMLP_BF16;
+  c.ws = ws;
+  c.withhold = hook.withhold;
+  c.wait_ns = hook.limit_ns;
+  c.status = device_status_word();
+  CORE_TRY(run_core_backward(c, stream));
+  return TPMLP_OK;
+}
+
 // Both forms of the rotation: dy, dq.. are the backward's. strides: q, k, (dyq, dyk,) and the two outputs.
 int qk_rope(int backward, const void* dyq, const void* dyk, const void* q, const void* k, const int64_t* strides,
             const void* wq, const void* wk, float eps, const int64_t* pos, const double* freqs, const uint8_t* axis,
@@ -210,23 +271,8 @@ int tpmlp_qk_rope_backward(const void* dyq, const void* dyk, const void* q, cons
 int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* starts,
                             int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
                             int causal, tpmlp_dtype dt, void* o, float* lse, tpmlp_stream_t stream) {
-  int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
-  if (rc) return rc;
-  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
-  CoreForward c{};
-  VIEW(c.q, q, 0, "q", heads);
-  VIEW(c.k, k, 1, "k", kv_heads);
-  VIEW(c.v, v, 2, "v", kv_heads);
-  VIEW(c.o, o, 3, "o", heads);
-  if (!lse || !aligned(lse, 4)) return set_error(lse ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "lse must not be NULL and 4-byte aligned");
-  if ((rc = current_sm103())) return rc;
-  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
-  c.lse = lse;
-  c.bf16 = dt == TPMLP_BF16;
-  c.wait_ns = wait_ns();
-  c.status = device_status_word();
-  CORE_TRY(run_core_forward(c, stream));
-  return TPMLP_OK;
+  return core_forward(q, k, v, strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal, dt, o, lse,
+                      Hook{0, wait_ns()}, stream);
 }
 
 size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt) {
@@ -238,31 +284,24 @@ int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const 
                              const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq,
                              int heads, int kv_heads, int head_dim, float scale, int causal, tpmlp_dtype dt, void* dq,
                              void* dk, void* dv, void* ws, size_t ws_bytes, tpmlp_stream_t stream) {
-  int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
-  if (rc) return rc;
-  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
-  CoreBackward c{};
-  VIEW(c.q, q, 0, "q", heads);
-  VIEW(c.k, k, 1, "k", kv_heads);
-  VIEW(c.v, v, 2, "v", kv_heads);
-  VIEW(c.o, o, 3, "o", heads);
-  VIEW(c.d_o, d_o, 4, "do", heads);
-  VIEW(c.dq, dq, 5, "dq", heads);
-  VIEW(c.dk, dk, 6, "dk", kv_heads);
-  VIEW(c.dv, dv, 7, "dv", kv_heads);
-  if (!lse || !ws) return set_error(TPMLP_ERR_ARG, "lse and workspace must not be NULL");
-  if (!aligned(lse, 4) || !aligned(ws, 16)) return set_error(TPMLP_ERR_ALIGN, "workspace must be 16-byte aligned, lse 4");
-  const size_t need = core_backward_workspace(T, heads);
-  if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
-  if ((rc = current_sm103())) return rc;
-  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
-  c.lse = lse;
-  c.bf16 = dt == TPMLP_BF16;
-  c.ws = ws;
-  c.wait_ns = wait_ns();
-  c.status = device_status_word();
-  CORE_TRY(run_core_backward(c, stream));
-  return TPMLP_OK;
+  return core_backward(q, k, v, o, lse, d_o, strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal, dt,
+                       dq, dk, dv, ws, ws_bytes, Hook{0, wait_ns()}, stream);
+}
+
+int tpmlp_selftest_attn_core_timeout(const void* q, const void* k, const void* v, void* o, float* lse, const void* d_o,
+                                     int64_t T, int heads, int head_dim, void* dq, void* dk, void* dv, void* ws,
+                                     size_t ws_bytes, int backward, int load, int limit_ms, tpmlp_stream_t stream) {
+  if (load < 1) return set_error(TPMLP_ERR_ARG, "load = %d must be >= 1", load);
+  if (limit_ms < 1 || limit_ms > 10000) return set_error(TPMLP_ERR_ARG, "limit_ms = %d outside 1..10000", limit_ms);
+  if (T < 1) return set_error(TPMLP_ERR_ARG, "T = %lld must be >= 1", static_cast<long long>(T));
+  int64_t strides[16];
+  for (int i = 0; i < 8; ++i) strides[2 * i] = int64_t(heads) * head_dim, strides[2 * i + 1] = head_dim;
+  const Hook hook{load, static_cast<uint64_t>(limit_ms) * 1000000ull};
+  const float scale = 1.f / sqrtf(static_cast<float>(head_dim));
+  return backward ? core_backward(q, k, v, o, lse, d_o, strides, nullptr, T, 1, T, heads, heads, head_dim, scale, 0,
+                                  TPMLP_BF16, dq, dk, dv, ws, ws_bytes, hook, stream)
+                  : core_forward(q, k, v, strides, nullptr, T, 1, T, heads, heads, head_dim, scale, 0, TPMLP_BF16, o, lse,
+                                 hook, stream);
 }
 
 }  // extern "C"

@@ -190,6 +190,16 @@ def test_workspace_sizes(tp):
     assert rope(1 << 20, 32, 8, 128) <= 1 << 20
 
 
+@pytest.mark.parametrize("kw", [dict(load=0), dict(limit=0), dict(limit=10001), dict(T=0), dict(dim=60), dict(heads=0),
+                                dict(nb=0, backward=1)])
+def test_timeout_hook_refuses(tp, kw):
+    a = dict(T=300, heads=2, dim=64, backward=0, load=1, limit=50, nb=WS)
+    a.update(kw)
+    assert tp.lib().tpmlp_selftest_attn_core_timeout(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, a["T"], a["heads"], a["dim"], FAKE,
+                                                     FAKE, FAKE, FAKE, a["nb"], a["backward"], a["load"], a["limit"],
+                                                     None) < 0
+
+
 def test_binding_refuses(tp):
     import torch
 

@@ -691,3 +691,53 @@ def test_rows_beyond_32_bit_offsets(tp):
     zq, zk = tp.tpmlp_qk_rope_forward(p[0], p[1], pos[:n], _freqs(64))
     assert torch.equal(yq[T - n:], zq) and torch.equal(yk[T - n:], zk)
     tp.tpmlp_check_status()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("load", [1, 2, 5])
+def test_a_load_that_never_comes(tp, load, backward, dim):
+    # Every wait has a limit: the CTAs give up, report it, and the next calls are as before.
+    q, k, v, do = _inputs(700, 4, 4, dim, "bf16", 41, layout="apart")
+    o, lse = tp.tpmlp_attn_core_forward(q, k, v, causal=False)
+    want = (o, lse, *tp.tpmlp_attn_core_backward(q, k, v, o, lse, do, causal=False))
+    tp.tpmlp_check_status()
+    tp.tpmlp_selftest_attn_core_timeout(q, k, v, backward, load, 50)
+    with pytest.raises(tp.TpmlpError) as e:
+        tp.tpmlp_check_status()
+    assert e.value.code == tp.TPMLP_ERR_TIMEOUT
+    o, lse = tp.tpmlp_attn_core_forward(q, k, v, causal=False)
+    got = (o, lse, *tp.tpmlp_attn_core_backward(q, k, v, o, lse, do, causal=False))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    tp.tpmlp_check_status()
+
+
+def test_captured_before_any_other_call(tp):
+    # The first calls of a process may be captured: nothing is allocated or looked up on the stream.
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import tensor_transformer_mlp_column_gb300 as tp
+x = torch.randn(300, 6, 64, device="cuda").bfloat16()
+q, k, v = x[:, :4], x[:, 4:5], x[:, 5:]
+do = torch.randn(300, 4, 64, device="cuda").bfloat16()
+pos = torch.arange(300, device="cuda")
+freqs = [10000.0 ** (-i / 32) for i in range(32)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def step():
+    a, b = tp.tpmlp_qk_rope_forward(q, k, pos, freqs)
+    o, lse = tp.tpmlp_attn_core_forward(a, b, v)
+    return (o, lse, *tp.tpmlp_attn_core_backward(a, b, v, o, lse, do))
+with torch.cuda.graph(g):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+tp.tpmlp_check_status()
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
