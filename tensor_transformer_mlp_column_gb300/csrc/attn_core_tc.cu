@@ -1050,6 +1050,9 @@ struct DkvCfg {
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
   // Columns of a softmax warp: 64 (8 x 2048 tokens, 32 heads of 128: 370 us, with 32 385; 16 heads of 64: 154 and 154).
   static constexpr int COLUMNS = 64, GROUPS = W / COLUMNS, WARPS = 4 * GROUPS;
+  // Whether the next pass's tiles are waited for before this pass's P and dS: their rings are deep enough for short heads
+  // (8192 tokens, 16 heads of 64: 486 -> 461 us), not for long ones (of 128: 635 -> 643).
+  static constexpr bool EARLY = DH == 64;
   static constexpr int THREADS = (WARPS + 2) * 32;
   static constexpr size_t BARS = 8 * (2 * QS + 2 * DS + 2 * RS + 8) + kItemBytes + 8;
   static constexpr size_t SMEM = 2 * TILE + (QS + DS) * NARROW + RS * 2 * W * 4 + BARS;
@@ -1230,7 +1233,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       int x = 0;  // query tile of pass i + 1
       for (int i = 0; i < ps.n; ++i, ++g) {
         if (++x == ps.per) x = 0;
-        ok = warp_wait(p_full, g & 1, guard, kSiteMmaAcc);
+        ok = (!C::EARLY || i + 1 == ps.n || take_q(g + 1, x)) && warp_wait(p_full, g & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
@@ -1239,7 +1242,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         }
         __syncwarp();
         if (i + 1 < ps.n) {
-          ok = take_q(g + 1, x);
+          ok = C::EARLY || take_q(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
             product_rows<DH, W>(tmem + C::S, s_k, s_q + ((g + 1) % C::QS) * C::NARROW, p.steps);
@@ -1247,7 +1250,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           }
           __syncwarp();
         }
-        ok = warp_wait(ds_full, g & 1, guard, kSiteMmaAcc);
+        ok = (!C::EARLY || i + 1 == ps.n || take_d(g + 1, x)) && warp_wait(ds_full, g & 1, guard, kSiteMmaAcc);
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
@@ -1257,7 +1260,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         }
         __syncwarp();
         if (i + 1 < ps.n) {
-          ok = take_d(g + 1, x);
+          ok = C::EARLY || take_d(g + 1, x);
           if (!ok) break;
           if (elect_one()) {
             product_rows<DH, W>(tmem + C::DP, s_v, s_do + ((g + 1) % C::DS) * C::NARROW, p.steps);
