@@ -473,7 +473,10 @@ int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const i
                             int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
                             int causal, tpmlp_dtype dt, void* o, float* lse, tpmlp_stream_t stream);
 
-/* Workspace bytes of tpmlp_attn_core_backward; 0 for T = 0 and on bad arguments. */
+/* Workspace bytes of tpmlp_attn_core_backward; 0 for T = 0 and on bad arguments:
+ * 4 T heads, and in bf16, where ceil(T / 128) kv_heads tiles of keys do not fill the
+ * GPU, fp32 sums of up to 32 (about 228 by that number; head_dim <= 64: 456) times
+ * 2 T kv_heads head_dim elements. */
 size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt);
 
 /* Gradients of L = sum(o * do) of tpmlp_attn_core_forward for the same q, k, v,

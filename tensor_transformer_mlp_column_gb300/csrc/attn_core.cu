@@ -520,7 +520,16 @@ bool many(const CoreShape& s, int rows, int heads) {
 
 }  // namespace
 
-size_t core_backward_workspace(int64_t T, int heads) { return static_cast<size_t>(T) * heads * sizeof(float); }
+namespace {
+// delta, on whole lines, then the sums of splits.
+size_t delta_bytes(int64_t T, int heads) { return (static_cast<size_t>(T) * heads * sizeof(float) + 255) / 256 * 256; }
+}  // namespace
+
+size_t core_backward_workspace(int64_t T, int heads, int kv_heads, int dim, int bf16) {
+  if (T == 0) return 0;
+  const int splits = bf16 ? core_splits_tc(T, heads, kv_heads, dim) : 1;
+  return delta_bytes(T, heads) + (splits > 1 ? size_t(2) * splits * T * kv_heads * dim * sizeof(float) : 0);
+}
 
 cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {
   TraceScope trace("attn_core_forward", s);
@@ -534,7 +543,8 @@ cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {
 
 cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
   float* delta = static_cast<float*>(c.ws);
-  if (c.bf16) return launch_core_backward_tc(c, delta, s);
+  if (c.bf16)
+    return launch_core_backward_tc(c, delta, delta + delta_bytes(c.s.T, c.s.heads) / sizeof(float), s);
   {
     TraceScope trace("attn_core_delta", s);
     const unsigned grid = static_cast<unsigned>((c.s.T * c.s.heads + 31) / 32);

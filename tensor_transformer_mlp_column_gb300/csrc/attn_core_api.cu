@@ -101,7 +101,7 @@ int check_core(const int64_t* strides, const int32_t* starts, int64_t T, int64_t
     return set_error(TPMLP_ERR_ARG, "without starts T = %lld must be batch * max_seq = %lld * %lld", static_cast<long long>(T),
                      static_cast<long long>(batch), static_cast<long long>(max_seq));
   if (!(scale > 0.f) || !std::isfinite(scale)) return set_error(TPMLP_ERR_ARG, "scale = %g must be finite and > 0", double(scale));
-  if ((max_seq + 63) / 64 * batch > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
+  if ((max_seq + 31) / 32 * batch > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
     return set_error(TPMLP_ERR_ARG, "too many sequences, heads and rows for one call");
   if (T > 0 && !strides) return set_error(TPMLP_ERR_ARG, "strides must not be NULL");
   if (!aligned(starts, 4)) return set_error(TPMLP_ERR_ALIGN, "starts must be 4-byte aligned");
@@ -161,7 +161,7 @@ int core_backward(const void* q, const void* k, const void* v, const void* o, co
   VIEW(c.dv, dv, 7, "dv", kv_heads);
   if (!lse || !ws) return set_error(TPMLP_ERR_ARG, "lse and workspace must not be NULL");
   if (!aligned(lse, 4) || !aligned(ws, 16)) return set_error(TPMLP_ERR_ALIGN, "workspace must be 16-byte aligned, lse 4");
-  const size_t need = core_backward_workspace(T, heads);
+  const size_t need = core_backward_workspace(T, heads, kv_heads, head_dim, dt == TPMLP_BF16);
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if ((rc = current_sm103())) return rc;
   c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
@@ -277,7 +277,7 @@ int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const i
 
 size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt) {
   if (check_heads(T, heads, kv_heads, head_dim, 128, dt) || heads % kv_heads != 0 || T > (int64_t(1) << 35) / heads) return 0;
-  return core_backward_workspace(T, heads);
+  return core_backward_workspace(T, heads, kv_heads, head_dim, dt == TPMLP_BF16);
 }
 
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,

@@ -257,12 +257,22 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[3
                      pack_bf16(v[8 * u + 4] * f, v[8 * u + 5] * f), pack_bf16(v[8 * u + 6] * f, v[8 * u + 7] * f));
 }
 
+// The same as fp32.
+__device__ __forceinline__ void store_sums(float* dst, const float (&v)[32], int column, int dim) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (column + 4 * u < dim)
+      *reinterpret_cast<float4*>(dst + column + 4 * u) = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+}
+
 struct TcParams {
   CoreShape s;
   CUtensorMap q, k, v, d_o;
   HeadsView o, dq, dk, dv;
   float* lse;    // forward: written; backward: read
   float* delta;  // backward
+  int splits;    // dK, dV: runs of a tile's passes
+  float* part;   // [2][splits][T][kv_heads][dim] where splits > 1: sums of dV, of dK
   float scale_log2;
   int steps;       // of 16 elements: what products over or of the head take
   int tiles;       // tiles (forward: runs of NQ tiles) of the longest sequence
@@ -1062,6 +1072,10 @@ struct DkvCfg {
 // Query tile i: P^T goes over S^T, dS^T over dP^T. The scores of tile i + 1 are
 // made while the threads work on dS of tile i, its dP while they work on P of
 // tile i + 1.
+//
+// Few key tiles for many queries (one kv head for all heads, say) would leave SMs
+// idle: then an item is one of p.splits runs of a tile's passes, which writes fp32
+// sums, and a last kernel adds them in order.
 template <int DH, int W>
 __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     dkv_kernel(const __grid_constant__ TcParams p) {
@@ -1119,32 +1133,40 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
-  // Query tiles of an item: `per` from `first` on of every head of the group, head by head.
+  // Passes of an item: the query tiles `first` .. `first` + `per` - 1 of every head of the group, head by head; of these n
+  // from head `head`, tile `first` + `x` on. An item's head counts the splits of a kv head.
   struct Passes {
-    int first, per, n;
+    int first, per, n, head, x;
   };
-  auto passes_of = [&](const Item& it) {
-    Passes x;
-    x.first = p.s.causal ? it.tile * kRows / W : 0;
-    x.per = it.tile * kRows >= it.len ? 0 : (it.len + W - 1) / W - x.first;
-    x.n = x.per * group;
-    return x;
+  auto passes_of = [&](int tile, int split_head, int len) {
+    Passes y;
+    y.first = p.s.causal ? tile * kRows / W : 0;
+    y.per = (len + W - 1) / W - y.first;
+    const int kv = split_head / p.splits, split = split_head % p.splits;
+    const int64_t all = int64_t(y.per) * group;
+    const int begin = static_cast<int>(all * split / p.splits);
+    y.n = static_cast<int>(all * (split + 1) / p.splits) - begin;
+    y.head = kv * group + begin / y.per;
+    y.x = begin % y.per;
+    return y;
   };
-  int items = 0, issued_q = 0, issued_d = 0;
+  int given = 0, items = 0, issued_q = 0, issued_d = 0;  // items, those with passes
 
   if (warp == kLoadWarp) {
     bool ok = true;
     Item it;
-    for (Walk walk(p, p.s.kv_heads, kRows, false, lane); ok && walk.next(it);) {
-      ok = ring_i.give(items, it, lane, guard);
+    for (Walk walk(p, p.s.kv_heads * p.splits, kRows, false, lane); ok && walk.next(it);) {
+      ok = ring_i.give(given++, it, lane, guard);
       if (!ok) break;
-      const Passes ps = passes_of(it);
+      const Passes ps = passes_of(it.tile, it.head, it.len);
+      if (ps.n == 0) continue;
+      const int kv = it.head / p.splits;
       ok = items == 0 || warp_wait(kv_free, (items - 1) & 1, guard, kSiteProducer);
       if (!ok) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-        load_tile<DH>(s_k, &p.k, it.head, it.row0 + it.tile * kRows, kv_full);
-        load_tile<DH>(s_v, &p.v, it.head, it.row0 + it.tile * kRows, kv_full);
+        load_tile<DH>(s_k, &p.k, kv, it.row0 + it.tile * kRows, kv_full);
+        load_tile<DH>(s_v, &p.v, kv, it.row0 + it.tile * kRows, kv_full);
       }
       ++items;
       // lse and delta of a tile's queries: they begin on any 4 bytes, so threads copy them, a pass ahead of their store.
@@ -1160,7 +1182,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           nd[y] = on ? -p.delta[at + q] : 0.f;
         }
       };
-      int h = it.head * group, x = 0;  // head and query tile of pass i
+      int h = ps.head, x = ps.x;  // head and query tile of pass i
       fetch(h, x);
       for (int i = 0; i < ps.n; ++i) {
         const int64_t row = it.row0 + (ps.first + x) * W;
@@ -1194,13 +1216,14 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       }
     }
     it.len = 0;
-    if (ok) ring_i.give(items, it, lane, guard);
+    if (ok) ring_i.give(given, it, lane, guard);
   } else if (warp == kMmaWarp) {
     bool ok = true;
     int g = 0;  // passes so far
     Item it;
     for (int i = 0; ok && ring_i.take(i, it, lane, guard); ++i) {
-      const Passes ps = passes_of(it);
+      const Passes ps = passes_of(it.tile, it.head, it.len);
+      if (ps.n == 0) continue;
       // Position i of a ring (query tile x), its rows of the next sequence cleared.
       auto take_q = [&](int i, int x) {
         if (!ring_q.wait_full(i, guard)) return false;
@@ -1214,7 +1237,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         if (rows < W) clear_rows<DH, W>(s_do + (i % C::DS) * C::NARROW, rows, lane);
         return true;
       };
-      ok = warp_wait(kv_full, items & 1, guard, kSiteMmaFull) && take_q(g, 0);
+      ok = warp_wait(kv_full, items & 1, guard, kSiteMmaFull) && take_q(g, ps.x);
       if (!ok) break;
       ++items;
       if (elect_one()) {
@@ -1222,7 +1245,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         tc_commit(s_full);
       }
       __syncwarp();
-      ok = take_d(g, 0);
+      ok = take_d(g, ps.x);
       if (!ok) break;
       if (elect_one()) {
         product_rows<DH, W>(tmem + C::DP, s_v, s_do + (g % C::DS) * C::NARROW, p.steps);
@@ -1230,7 +1253,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         if (ps.n == 1) tc_commit(kv_free);
       }
       __syncwarp();
-      int x = 0;  // query tile of pass i + 1
+      int x = ps.x;  // query tile of pass i + 1
       for (int i = 0; i < ps.n; ++i, ++g) {
         if (++x == ps.per) x = 0;
         ok = (!C::EARLY || i + 1 == ps.n || take_q(g + 1, x)) && warp_wait(p_full, g & 1, guard, kSiteMmaAcc);
@@ -1281,8 +1304,13 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       const volatile Item& it = ring_i.held(i);
       const int len = it.len, k0 = it.tile * kRows, kj = k0 + row;
       const int first = p.s.causal ? k0 : 0;  // a multiple of W
-      int q0 = first + H * part;              // of this warp's columns
-      for (int left = ((len - first + W - 1) / W) * group; left > 0; --left, ++g) {
+      int q0, n;                              // the first query of this warp's columns; passes
+      {
+        const Passes ps = passes_of(it.tile, it.head, len);
+        q0 = (ps.first + ps.x) * W + H * part;
+        n = ps.n;
+      }
+      for (int left = n; left > 0; --left, ++g) {
         const float* rows = s_row + (g % C::RS) * 2 * W + H * part;
         ok = ring_r.wait_full(g, guard) && warp_wait(s_full, g & 1, guard, kSiteMmaFull);
         if (!ok) break;
@@ -1345,19 +1373,33 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       const int64_t at = it.row0 + kj;
       const int head = it.head;
       ring_i.release(i, lane);
-      ok = warp_wait(done, items & 1, guard, kSiteEpilogue);
-      if (!ok) break;
-      ++items;
-      tc_fence_after_sync();
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + at * p.dv.token + head * p.dv.head;
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + at * p.dk.token + head * p.dk.head;
+      if (n > 0) {
+        ok = warp_wait(done, items & 1, guard, kSiteEpilogue);
+        if (!ok) break;
+        ++items;
+        tc_fence_after_sync();
+      }
+      const int kv = head / p.splits;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv.p) + at * p.dv.token + kv * p.dv.head;
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk.p) + at * p.dk.token + kv * p.dk.head;
 #pragma unroll 1
       for (int y = part * 32; y < DH && y < p.s.dim; y += C::GROUPS * 32) {
-        float o[32];
-        tmem_ld_32cols(tmem + lanes + C::DV + y, o);
-        if (kj < len) store_row(dv, o, 1.f, y, p.s.dim);
-        tmem_ld_32cols(tmem + lanes + C::DK + y, o);
-        if (kj < len) store_row(dk, o, p.s.scale, y, p.s.dim);
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {  // dV, dK
+          float o[32];
+          if (n > 0) {
+            tmem_ld_32cols(tmem + lanes + (z ? C::DK : C::DV) + y, o);
+          } else {  // a split without a pass
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (kj >= len) continue;
+          if (p.splits == 1)
+            store_row(z ? dk : dv, o, z ? p.s.scale : 1.f, y, p.s.dim);
+          else
+            store_sums(p.part + ((int64_t(z * p.splits + head % p.splits) * p.s.T + at) * p.s.kv_heads + kv) * p.s.dim, o, y,
+                       p.s.dim);
+        }
       }
       tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
     }
@@ -1380,6 +1422,47 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::TMEM);
   }
+}
+
+// dV and dK of a tile of keys as the sums of their splits, in order. Eight elements a thread; blockIdx.y a 256th of theirs.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t per = int64_t(p.s.kv_heads) * p.s.batch;
+  const int tile = static_cast<int>(blockIdx.x / per), in = static_cast<int>(blockIdx.x % per);
+  const int kv = in % p.s.kv_heads;
+  int64_t row0;
+  const int len = core_sequence(p.s, in / p.s.kv_heads, row0, p.status);
+  const int units = p.s.dim / 8, i = blockIdx.y * 256 + threadIdx.x;  // of 2 x 128 x units
+  const int z = i / (kRows * units), row = tile * kRows + i / units % kRows, e = i % units * 8;
+  if (row >= len) return;
+  const int64_t at = row0 + row, step = p.s.T * p.s.kv_heads * p.s.dim;
+  const float* from = p.part + ((int64_t(z * p.splits) * p.s.T + at) * p.s.kv_heads + kv) * p.s.dim + e;
+  float sum[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s, from += step) {
+    const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+    sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+  }
+  const HeadsView& v = z ? p.dk : p.dv;
+  const float f = z ? p.s.scale : 1.f;
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(v.p) + at * v.token + kv * v.head + e) =
+      make_uint4(pack_bf16(sum[0] * f, sum[1] * f), pack_bf16(sum[2] * f, sum[3] * f), pack_bf16(sum[4] * f, sum[5] * f),
+                 pack_bf16(sum[6] * f, sum[7] * f));
+}
+
+// Runs that a key tile's passes are cut into: where the key tiles do not fill the GPU, enough for one and a half items a
+// CTA, of four tiles of 128 queries at least. (One sequence, causal, heads of 128, whole -> in runs: 4096 tokens, 32 heads on
+// one kv head 1418 -> 209 us, 8192 tokens, 2 on one 186 -> 68; 512 tokens, 8 on one 61 -> 24; 1024 tokens, 4 on 4 22.5 ->
+// 23.4. Two runs where the tiles do fill it, for more even CTAs, gain 3 % at 16384 tokens, 8 heads on 2, and lose 60 % at
+// 4096, 8 on 8.)
+constexpr int kMaxSplits = 32;
+int splits_of(int64_t items, int64_t passes, int ctas) {
+  const int64_t full = int64_t(num_sms()) * ctas;
+  int64_t n = items < full ? (3 * full + 2 * items - 1) / (2 * items) : 1;
+  if (n > passes / 4) n = passes / 4;
+  return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
 // ------------------------------------------------------------------ launches
@@ -1445,7 +1528,9 @@ cudaError_t launch_dq(TcParams& p, cudaStream_t s) {
 template <int DH, int W>
 cudaError_t launch_dkv(TcParams& p, cudaStream_t s) {
   using C = DkvCfg<DH, W>;
-  return launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads, C::THREADS, C::SMEM, C::CTAS, s);
+  cudaError_t e = launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads * p.splits, C::THREADS, C::SMEM, C::CTAS, s);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_pdl(join_kernel, dim3(static_cast<unsigned>(p.items / p.splits), p.s.dim / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -1454,10 +1539,21 @@ cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t s) {
   TcParams p;
   cudaError_t e = params_of(c, &p);
   if (e != cudaSuccess) return e;
-  return c.s.dim <= 64 ? launch_fwd<64, 1>(p, s) : launch_fwd<128, 2>(p, s);
+  // Short heads: one tile a CTA and two CTAs an SM. Long ones: two tiles that take turns, but one where the pairs do not
+  // fill the GPU (8192 tokens, 2 heads of 128: 96 -> 90 us; 1024 tokens, 4 heads: 22 -> 18.5).
+  if (c.s.dim <= 64) return launch_fwd<64, 1>(p, s);
+  const int64_t pairs = int64_t((c.s.max_seq + 2 * kRows - 1) / (2 * kRows)) * c.s.heads * c.s.batch;
+  return pairs < num_sms() ? launch_fwd<128, 1>(p, s) : launch_fwd<128, 2>(p, s);
 }
 
-cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStream_t s) {
+// What the sums of splits may take: those of one sequence of all T rows, which has the fewest key tiles and the most
+// passes for each.
+int core_splits_tc(int64_t T, int heads, int kv_heads, int dim) {
+  const int64_t tiles = (T + kRows - 1) / kRows;
+  return splits_of(tiles * kv_heads, tiles * (heads / kv_heads), dim <= 64 ? DkvCfg<64, 64>::CTAS : DkvCfg<128, 128>::CTAS);
+}
+
+cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, float* part, cudaStream_t s) {
   TcParams p;
   cudaError_t e = params_of(c, &p);
   if (e != cudaSuccess) return e;
@@ -1466,6 +1562,12 @@ cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, cudaStr
   p.dk = c.dk;
   p.dv = c.dv;
   p.delta = delta;
+  p.part = part;
+  const int64_t tiles = (c.s.max_seq + kRows - 1) / kRows;
+  p.splits = splits_of(tiles * c.s.kv_heads * c.s.batch, tiles * (c.s.heads / c.s.kv_heads),
+                       c.s.dim <= 64 ? DkvCfg<64, 64>::CTAS : DkvCfg<128, 128>::CTAS);
+  const int most = core_splits_tc(c.s.T, c.s.heads, c.s.kv_heads, c.s.dim);
+  if (p.splits > most) p.splits = most;
   // Heads of up to 64 elements: 64 keys (queries) at a time and half of the tensor memory, so that two CTAs share an SM.
   const bool small = c.s.dim <= 64;
   {

@@ -186,6 +186,15 @@ def test_shared_heads(tp, heads, kv, dtype):
     _check(tp, [140], heads, kv, 128, dtype, False, seed=heads + 1)
 
 
+@pytest.mark.parametrize("dim", [40, 64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,heads,kv", [([1000], 8, 1), ([700, 130, 1, 0, 300], 16, 1), ([520, 520], 12, 2),
+                                              ([2100], 2, 1), ([1], 16, 1), ([129] * 3, 32, 1)])
+def test_few_keys_for_many_queries(tp, lengths, heads, kv, causal, dim):
+    # The passes over a key tile are cut into runs, some of them without a pass, whose sums are added.
+    _check(tp, lengths, heads, kv, dim, "bf16", causal, seed=heads + dim, first=3, behind=5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["packed", "apart", "heads_first"])
 def test_layouts(tp, layout, dtype):
