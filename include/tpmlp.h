@@ -473,11 +473,12 @@ int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const i
                             int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, float scale,
                             int causal, tpmlp_dtype dt, void* o, float* lse, tpmlp_stream_t stream);
 
-/* Workspace bytes of tpmlp_attn_core_backward; 0 for T = 0 and on bad arguments:
- * 4 T heads, and in bf16, where ceil(T / 128) kv_heads tiles of keys do not fill the
- * GPU, fp32 sums of up to 32 (about 228 by that number; head_dim <= 64: 456) times
- * 2 T kv_heads head_dim elements. */
-size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt);
+/* Workspace bytes of tpmlp_attn_core_backward for the same sizes; 0 where there is
+ * nothing to do and on bad arguments: 4 T heads, and in bf16, where the batch *
+ * ceil(max_seq / 128) * kv_heads tiles of keys do not fill the GPU, up to 32 times
+ * fp32 sums of dk and dv of that many tiles (at most about 50 MB). */
+size_t tpmlp_attn_core_workspace_bytes(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim,
+                                       tpmlp_dtype dt);
 
 /* Gradients of L = sum(o * do) of tpmlp_attn_core_forward for the same q, k, v,
  * sequences, scale and mask. The probabilities p_ij = exp(s_ij - lse_i) are made
@@ -489,8 +490,10 @@ size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int h
  *   do        device [T, heads, head_dim] of type dt.
  *   dq, dk, dv  device, as q, k, v, written.
  *   strides   of q, k, v, o, do, dq, dk, dv.
- *   workspace at least tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim, dt) bytes.
- * Every sum has a fixed order: bitwise reproducible. bf16 rounds p and ds to bf16
+ *   workspace at least tpmlp_attn_core_workspace_bytes(T, batch, max_seq, heads,
+ *             kv_heads, head_dim, dt) bytes.
+ * Every sum has a fixed order: bitwise reproducible in calls of the same batch,
+ * max_seq and heads (how sums of dk and dv are cut follows these). bf16 rounds p and ds to bf16
  * as operands and each result once; what delta is off because o was rounded is
  * found as the sum of a row's ds and taken out of ds's products again. */
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,

@@ -97,7 +97,7 @@ SIGNATURES = {
     "tpmlp_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _SZ, _P]),
     "tpmlp_grad_clip": (_I, [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "tpmlp_attn_core_forward": (_I, [_P] * 5 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I, _P, _P, _P]),
-    "tpmlp_attn_core_workspace_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "tpmlp_attn_core_workspace_bytes": (_SZ, [_I64] * 3 + [_I] * 4),
     "tpmlp_attn_core_backward": (_I, [_P] * 8 + [_I64] * 3 + [_I] * 3 + [ctypes.c_float, _I, _I] + [_P] * 4 + [_SZ, _P]),
     "tpmlp_selftest_attn_core_timeout": (_I, [_P] * 6 + [_I64, _I, _I] + [_P] * 4 + [_SZ, _I, _I, _I, _P]),
     "tpmlp_qk_rope_forward": (_I, [_P] * 5 + [ctypes.c_float] + [_P] * 3 + [_I64] + [_I] * 7 + [_P] * 3),
@@ -860,14 +860,16 @@ def tpmlp_attn_core_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s
     return o, lse
 
 
-def tpmlp_attn_core_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype) -> int:
-    return int(lib().tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim,
-                                                     TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32))
-
-
 @functools.lru_cache(maxsize=1024)
-def _core_workspace(T: int, heads: int, kv_heads: int, head_dim: int, dt: int) -> int:
-    return int(lib().tpmlp_attn_core_workspace_bytes(T, heads, kv_heads, head_dim, dt))
+def _core_workspace(dev: int, T: int, batch: int, max_seq: int, heads: int, kv_heads: int, head_dim: int, dt: int) -> int:
+    return int(lib().tpmlp_attn_core_workspace_bytes(T, batch, max_seq, heads, kv_heads, head_dim, dt))
+
+
+def tpmlp_attn_core_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype, batch: int = 1,
+                                    max_seq: Optional[int] = None) -> int:
+    """Of tpmlp_attn_core_backward on `batch` sequences of at most max_seq tokens (default T / batch)."""
+    return int(lib().tpmlp_attn_core_workspace_bytes(T, batch, T // batch if max_seq is None else max_seq, heads, kv_heads,
+                                                     head_dim, TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32))
 
 
 def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
@@ -890,7 +892,7 @@ def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         dq, dqp = _heads_output(dq, T, heads, dim, q.dtype, dev, strides, "dq")
         dk, dkp = _heads_output(dk, T, kv, dim, q.dtype, dev, strides, "dk")
         dv, dvp = _heads_output(dv, T, kv, dim, q.dtype, dev, strides, "dv")
-        ws, wp, wn = _space(_core_workspace(T, heads, kv, dim, dt), workspace, dev)
+        ws, wp, wn = _space(_core_workspace(dev, T, n, most, heads, kv, dim, dt), workspace, dev)
         strides = array("q", strides)
         _check(l.tpmlp_attn_core_backward(qp, kp, vp, op, _like(lse, (heads, T), torch.float32, dev, "lse"), gp,
                                           strides.buffer_info()[0], sp, T, n, most, heads, kv, dim,
@@ -1078,7 +1080,7 @@ def tpmlp_selftest_attn_core_timeout(q: torch.Tensor, k: torch.Tensor, v: torch.
         q, k, v = (t.contiguous() for t in (q, k, v))
         o, do, dq, dk, dv = (torch.zeros_like(q) for _ in range(5))
         lse = torch.zeros((heads, T), dtype=torch.float32, device="cuda")
-        ws, wp, wn = _space(_core_workspace(T, heads, heads, dim, TPMLP_BF16), None, on.dev)
+        ws, wp, wn = _space(_core_workspace(on.dev, T, 1, T, heads, heads, dim, TPMLP_BF16), None, on.dev)
         p = [_ptr(t, on.dev, "q, k or v") for t in (q, k, v)]
         _check(lib().tpmlp_selftest_attn_core_timeout(*p, o.data_ptr(), lse.data_ptr(), do.data_ptr(), T, heads, dim,
                                                       dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wn,

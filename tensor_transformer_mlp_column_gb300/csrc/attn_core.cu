@@ -525,10 +525,11 @@ namespace {
 size_t delta_bytes(int64_t T, int heads) { return (static_cast<size_t>(T) * heads * sizeof(float) + 255) / 256 * 256; }
 }  // namespace
 
-size_t core_backward_workspace(int64_t T, int heads, int kv_heads, int dim, int bf16) {
-  if (T == 0) return 0;
-  const int splits = bf16 ? core_splits_tc(T, heads, kv_heads, dim) : 1;
-  return delta_bytes(T, heads) + (splits > 1 ? size_t(2) * splits * T * kv_heads * dim * sizeof(float) : 0);
+size_t core_backward_workspace(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int dim, int bf16) {
+  if (T == 0 || batch == 0 || max_seq == 0) return 0;
+  const int splits = bf16 ? core_splits_tc(batch, max_seq, heads, kv_heads, dim) : 1;
+  const size_t keys = static_cast<size_t>(batch) * ((max_seq + 127) / 128) * 128 * kv_heads;
+  return delta_bytes(T, heads) + (splits > 1 ? 2 * splits * keys * dim * sizeof(float) : 0);
 }
 
 cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {

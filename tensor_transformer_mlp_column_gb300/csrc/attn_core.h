@@ -81,11 +81,11 @@ struct CoreBackward {
   uint64_t wait_ns;
   int* status;
 };
-size_t core_backward_workspace(int64_t T, int heads, int kv_heads, int dim, int bf16);
+size_t core_backward_workspace(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int dim, int bf16);
 cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t stream);
-// The bf16 forms (attn_core_tc.cu). delta [heads][T]: the row sums of dO . O; part [2][splits][T][kv_heads][dim]: sums of
-// dV and dK, where core_splits_tc() is above 1.
-int core_splits_tc(int64_t T, int heads, int kv_heads, int dim);
+// The bf16 forms (attn_core_tc.cu). delta [heads][T]: the row sums of dO . O; part: where core_splits_tc() is above 1, that
+// many times fp32 sums of dV and dK of batch x ceil(max_seq / 128) tiles of 128 keys.
+int core_splits_tc(int64_t batch, int64_t max_seq, int heads, int kv_heads, int dim);
 cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t stream);
 cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, float* part, cudaStream_t stream);
 

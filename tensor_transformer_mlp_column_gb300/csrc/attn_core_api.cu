@@ -88,8 +88,7 @@ int make_view(HeadsView* v, const void* p, const int64_t* strides, int i, const 
     if (rc_) return rc_;                                                                                  \
   } while (0)
 
-int check_core(const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq, int heads,
-               int kv_heads, int head_dim, float scale, tpmlp_dtype dt) {
+int check_shape(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim, tpmlp_dtype dt) {
   int rc = check_heads(T, heads, kv_heads, head_dim, 128, dt);
   if (rc) return rc;
   if (heads % kv_heads != 0)
@@ -97,12 +96,19 @@ int check_core(const int64_t* strides, const int32_t* starts, int64_t T, int64_t
   if (batch < 0 || max_seq < 0 || batch > kMaxT || max_seq > T)
     return set_error(TPMLP_ERR_ARG, "batch = %lld must be in [0, 2^30] and max_seq = %lld in [0, T]",
                      static_cast<long long>(batch), static_cast<long long>(max_seq));
+  if ((max_seq + 31) / 32 * batch > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
+    return set_error(TPMLP_ERR_ARG, "too many sequences, heads and rows for one call");
+  return TPMLP_OK;
+}
+
+int check_core(const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq, int heads,
+               int kv_heads, int head_dim, float scale, tpmlp_dtype dt) {
+  int rc = check_shape(T, batch, max_seq, heads, kv_heads, head_dim, dt);
+  if (rc) return rc;
   if (!starts && batch * max_seq != T)
     return set_error(TPMLP_ERR_ARG, "without starts T = %lld must be batch * max_seq = %lld * %lld", static_cast<long long>(T),
                      static_cast<long long>(batch), static_cast<long long>(max_seq));
   if (!(scale > 0.f) || !std::isfinite(scale)) return set_error(TPMLP_ERR_ARG, "scale = %g must be finite and > 0", double(scale));
-  if ((max_seq + 31) / 32 * batch > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
-    return set_error(TPMLP_ERR_ARG, "too many sequences, heads and rows for one call");
   if (T > 0 && !strides) return set_error(TPMLP_ERR_ARG, "strides must not be NULL");
   if (!aligned(starts, 4)) return set_error(TPMLP_ERR_ALIGN, "starts must be 4-byte aligned");
   return TPMLP_OK;
@@ -161,7 +167,7 @@ int core_backward(const void* q, const void* k, const void* v, const void* o, co
   VIEW(c.dv, dv, 7, "dv", kv_heads);
   if (!lse || !ws) return set_error(TPMLP_ERR_ARG, "lse and workspace must not be NULL");
   if (!aligned(lse, 4) || !aligned(ws, 16)) return set_error(TPMLP_ERR_ALIGN, "workspace must be 16-byte aligned, lse 4");
-  const size_t need = core_backward_workspace(T, heads, kv_heads, head_dim, dt == TPMLP_BF16);
+  const size_t need = core_backward_workspace(T, batch, max_seq, heads, kv_heads, head_dim, dt == TPMLP_BF16);
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if ((rc = current_sm103())) return rc;
   c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
@@ -275,9 +281,10 @@ int tpmlp_attn_core_forward(const void* q, const void* k, const void* v, const i
                       Hook{0, wait_ns()}, stream);
 }
 
-size_t tpmlp_attn_core_workspace_bytes(int64_t T, int heads, int kv_heads, int head_dim, tpmlp_dtype dt) {
-  if (check_heads(T, heads, kv_heads, head_dim, 128, dt) || heads % kv_heads != 0 || T > (int64_t(1) << 35) / heads) return 0;
-  return core_backward_workspace(T, heads, kv_heads, head_dim, dt == TPMLP_BF16);
+size_t tpmlp_attn_core_workspace_bytes(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_heads, int head_dim,
+                                       tpmlp_dtype dt) {
+  if (check_shape(T, batch, max_seq, heads, kv_heads, head_dim, dt)) return 0;
+  return core_backward_workspace(T, batch, max_seq, heads, kv_heads, head_dim, dt == TPMLP_BF16);
 }
 
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,

@@ -257,7 +257,7 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[3
                      pack_bf16(v[8 * u + 4] * f, v[8 * u + 5] * f), pack_bf16(v[8 * u + 6] * f, v[8 * u + 7] * f));
 }
 
-// The same as fp32.
+// As fp32.
 __device__ __forceinline__ void store_sums(float* dst, const float (&v)[32], int column, int dim) {
 #pragma unroll
   for (int u = 0; u < 8; ++u)
@@ -272,7 +272,7 @@ struct TcParams {
   float* lse;    // forward: written; backward: read
   float* delta;  // backward
   int splits;    // dK, dV: runs of a tile's passes
-  float* part;   // [2][splits][T][kv_heads][dim] where splits > 1: sums of dV, of dK
+  float* part;   // where splits > 1: sums of dV, of dK, in the places that part_of() gives
   float scale_log2;
   int steps;       // of 16 elements: what products over or of the head take
   int tiles;       // tiles (forward: runs of NQ tiles) of the longest sequence
@@ -282,10 +282,16 @@ struct TcParams {
   int* status;
 };
 
+// A split's sums of a row of a key tile: [dV, dK][splits][batch][tiles][kv_heads][128][dim].
+__device__ __forceinline__ float* part_of(const TcParams& p, int z, int split, int seq, int tile, int kv, int row) {
+  const int64_t at = ((int64_t(z * p.splits + split) * p.s.batch + seq) * p.tiles + tile) * p.s.kv_heads + kv;
+  return p.part + (at * kRows + row) * p.s.dim;
+}
+
 // What a CTA works on: `rows` tokens (a tile or a run of tiles) of a head of a sequence.
 struct Item {
   int64_t row0;
-  int tile, head, len;  // len 0: no more items
+  int tile, head, len, seq;  // len 0: no more items
 };
 
 // The items of a CTA, found by its loading warp. They are in order of their work, the most first, and a CTA takes one of
@@ -342,6 +348,7 @@ struct Walk {
         const int c = __shfl_sync(kAll, b < 32 ? c0 : c1, b & 31);
         it.head = in % heads;
         it.tile = last_first ? d - 1 : c - d;
+        it.seq = b;
         it.len = core_sequence(p.s, b, it.row0, p.status);
       } else {
         if (at >= p.items) return false;
@@ -349,7 +356,8 @@ struct Walk {
         it.tile = static_cast<int>(i / per);
         if (last_first) it.tile = p.tiles - 1 - it.tile;
         it.head = static_cast<int>(in % heads);
-        it.len = core_sequence(p.s, static_cast<int>(in / heads), it.row0, p.status);
+        it.seq = static_cast<int>(in / heads);
+        it.len = core_sequence(p.s, it.seq, it.row0, p.status);
         if (int64_t(it.tile) * rows >= it.len) continue;
       }
       ++round;
@@ -1371,7 +1379,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       }
       if (!ok) break;
       const int64_t at = it.row0 + kj;
-      const int head = it.head;
+      const int head = it.head, seq = it.seq;
       ring_i.release(i, lane);
       if (n > 0) {
         ok = warp_wait(done, items & 1, guard, kSiteEpilogue);
@@ -1397,8 +1405,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           if (p.splits == 1)
             store_row(z ? dk : dv, o, z ? p.s.scale : 1.f, y, p.s.dim);
           else
-            store_sums(p.part + ((int64_t(z * p.splits + head % p.splits) * p.s.T + at) * p.s.kv_heads + kv) * p.s.dim, o, y,
-                       p.s.dim);
+            store_sums(part_of(p, z, head % p.splits, seq, k0 / kRows, kv, row), o, y, p.s.dim);
         }
       }
       tc_fence_before_sync();  // both are in registers; the next item's wait for this warp's next P and dS
@@ -1430,14 +1437,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
   pdl_launch_dependents();
   const int64_t per = int64_t(p.s.kv_heads) * p.s.batch;
   const int tile = static_cast<int>(blockIdx.x / per), in = static_cast<int>(blockIdx.x % per);
-  const int kv = in % p.s.kv_heads;
+  const int kv = in % p.s.kv_heads, seq = in / p.s.kv_heads;
   int64_t row0;
-  const int len = core_sequence(p.s, in / p.s.kv_heads, row0, p.status);
+  const int len = core_sequence(p.s, seq, row0, p.status);
   const int units = p.s.dim / 8, i = blockIdx.y * 256 + threadIdx.x;  // of 2 x 128 x units
-  const int z = i / (kRows * units), row = tile * kRows + i / units % kRows, e = i % units * 8;
-  if (row >= len) return;
-  const int64_t at = row0 + row, step = p.s.T * p.s.kv_heads * p.s.dim;
-  const float* from = p.part + ((int64_t(z * p.splits) * p.s.T + at) * p.s.kv_heads + kv) * p.s.dim + e;
+  const int z = i / (kRows * units), row = i / units % kRows, e = i % units * 8;
+  if (tile * kRows + row >= len) return;
+  const int64_t at = row0 + tile * kRows + row;
+  const float* from = part_of(p, z, 0, seq, tile, kv, row) + e;
+  const int64_t step = int64_t(p.s.batch) * p.tiles * p.s.kv_heads * kRows * p.s.dim;
   float sum[8] = {};
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s, from += step) {
@@ -1546,11 +1554,10 @@ cudaError_t launch_core_forward_tc(const CoreForward& c, cudaStream_t s) {
   return pairs < num_sms() ? launch_fwd<128, 1>(p, s) : launch_fwd<128, 2>(p, s);
 }
 
-// What the sums of splits may take: those of one sequence of all T rows, which has the fewest key tiles and the most
-// passes for each.
-int core_splits_tc(int64_t T, int heads, int kv_heads, int dim) {
-  const int64_t tiles = (T + kRows - 1) / kRows;
-  return splits_of(tiles * kv_heads, tiles * (heads / kv_heads), dim <= 64 ? DkvCfg<64, 64>::CTAS : DkvCfg<128, 128>::CTAS);
+int core_splits_tc(int64_t batch, int64_t max_seq, int heads, int kv_heads, int dim) {
+  const int64_t tiles = (max_seq + kRows - 1) / kRows;
+  return splits_of(tiles * kv_heads * batch, tiles * (heads / kv_heads),
+                   dim <= 64 ? DkvCfg<64, 64>::CTAS : DkvCfg<128, 128>::CTAS);
 }
 
 cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, float* part, cudaStream_t s) {
@@ -1563,11 +1570,7 @@ cudaError_t launch_core_backward_tc(const CoreBackward& c, float* delta, float* 
   p.dv = c.dv;
   p.delta = delta;
   p.part = part;
-  const int64_t tiles = (c.s.max_seq + kRows - 1) / kRows;
-  p.splits = splits_of(tiles * c.s.kv_heads * c.s.batch, tiles * (c.s.heads / c.s.kv_heads),
-                       c.s.dim <= 64 ? DkvCfg<64, 64>::CTAS : DkvCfg<128, 128>::CTAS);
-  const int most = core_splits_tc(c.s.T, c.s.heads, c.s.kv_heads, c.s.dim);
-  if (p.splits > most) p.splits = most;
+  p.splits = core_splits_tc(c.s.batch, c.s.max_seq, c.s.heads, c.s.kv_heads, c.s.dim);
   // Heads of up to 64 elements: 64 keys (queries) at a time and half of the tensor memory, so that two CTAs share an SM.
   const bool small = c.s.dim <= 64;
   {

@@ -181,9 +181,11 @@ def test_rope_backward_argument_errors(tp, kw, code):
 def test_workspace_sizes(tp):
     l = tp.lib()
     core = l.tpmlp_attn_core_workspace_bytes
-    assert core(0, 4, 2, 64, 1) == 0 and core(100, 4, 3, 64, 1) == 0 and core(100, 4, 2, 60, 1) == 0
-    assert core(100, 4, 2, 64, 5) == 0 and core(-1, 4, 2, 64, 1) == 0
-    assert core(100, 4, 2, 64, 1) >= 1600
+    assert core(0, 1, 0, 4, 2, 64, 1) == 0 and core(100, 1, 100, 4, 3, 64, 1) == 0 and core(100, 1, 100, 4, 2, 60, 1) == 0
+    assert core(100, 1, 100, 4, 2, 64, 5) == 0 and core(-1, 1, 0, 4, 2, 64, 1) == 0 and core(100, 1, 101, 4, 2, 64, 1) == 0
+    assert core(100, -1, 100, 4, 2, 64, 1) == 0 and core(100, 0, 100, 4, 2, 64, 1) == 0
+    assert core(100, 1, 100, 4, 2, 64, 1) >= 1600 and core(100, 2, 50, 4, 2, 64, 0) == 1792
+    assert core(1 << 20, 1, 1 << 20, 32, 32, 128, 1) == 128 << 20
     rope = l.tpmlp_qk_rope_workspace_bytes
     assert rope(0, 4, 2, 64) == 0 and rope(10, 4, 2, 65) == 0 and rope(10, 0, 2, 64) == 0
     assert rope(1, 4, 2, 64) == 512
