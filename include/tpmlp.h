@@ -550,7 +550,7 @@ size_t tpmlp_qk_rope_workspace_bytes(int64_t T, int heads, int kv_heads, int hea
  *   dwq, dwk  device fp32 [head_dim], written (zero for T = 0); with wq and wk NULL not looked at.
  *   workspace at least tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim)
  *             bytes; with wq and wk NULL not looked at.
- * Sums in fp32, those of many parts in fp64, in a fixed order: bitwise reproducible. */
+ * Sums in fp32, in a fixed order that the sizes give: bitwise reproducible. */
 int tpmlp_qk_rope_backward(const void* dyq, const void* dyk, const void* q, const void* k, const int64_t* strides,
                            const void* wq, const void* wk, float eps, const int64_t* pos, const double* freqs,
                            const uint8_t* axis, int64_t T, int heads, int kv_heads, int head_dim, int rot, int axes,
