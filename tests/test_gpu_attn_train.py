@@ -166,10 +166,17 @@ def test_lengths(tp, lengths, causal, dtype):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("count", [31, 32, 33, 63, 64, 65, 150])
 def test_many_sequences(tp, count, causal, dtype):
-    # Up to 64 sequences are handed out by their lengths, more of them tile by tile.
+    # bf16 hands them out by their lengths, 64 at a time.
     lengths = [(37 * i * i + 11 * i) % 300 for i in range(count)]
     lengths[count // 2] = 700
     _check(tp, lengths, 2, 1, 64 if count % 2 else 128, dtype, causal, seed=count)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[5, 300] + [0] * 130 + [257, 1, 0, 40], [0] * 200 + [130], [0] * 64 + [1] * 64 + [0] * 64,
+                                     [200] * 64 + [3] + [0] * 63])
+def test_many_empty_sequences(tp, lengths, dtype):
+    _check(tp, lengths, 2, 2, 64, dtype, seed=len(lengths), max_seq=sum(lengths))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
