@@ -868,7 +868,7 @@ def _core_workspace(dev: int, T: int, batch: int, max_seq: int, heads: int, kv_h
 def tpmlp_attn_core_workspace_bytes(T: int, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype, batch: int = 1,
                                     max_seq: Optional[int] = None) -> int:
     """Of tpmlp_attn_core_backward on `batch` sequences of at most max_seq tokens (default T / batch)."""
-    return int(lib().tpmlp_attn_core_workspace_bytes(T, batch, T // batch if max_seq is None else max_seq, heads, kv_heads,
+    return int(lib().tpmlp_attn_core_workspace_bytes(T, batch, T // max(batch, 1) if max_seq is None else max_seq, heads, kv_heads,
                                                      head_dim, TPMLP_BF16 if dtype == torch.bfloat16 else TPMLP_F32))
 
 
@@ -904,7 +904,7 @@ def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 @functools.lru_cache(maxsize=64)
 def _turns(freqs: tuple, axis: Optional[tuple], axes: int):
     """The frequencies and their axes as host arrays, and the arrays' addresses."""
-    if axis is not None and (len(axis) != len(freqs) or any(a < 0 or a >= axes for a in axis)):
+    if axis is not None and (len(axis) != len(freqs) or any(a < 0 or a >= min(axes, 256) for a in axis)):
         raise ValueError(f"axis must give one of {axes} axes for each of the {len(freqs)} frequencies")
     f, a = array("d", freqs), None if axis is None else array("B", axis)
     return f, a, f.buffer_info()[0], None if a is None else a.buffer_info()[0]
@@ -923,11 +923,12 @@ def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
     # A program's frequencies are the same in every call: the last call's arrays serve while its values are equal.
     global _last_turns
     last = _last_turns
-    if last[0] == freqs and last[1] == axis and last[2] == axes:
+    plain = isinstance(freqs, (list, tuple)) and (axis is None or isinstance(axis, (list, tuple)))
+    if plain and last[0] == freqs and last[1] == axis and last[2] == axes:
         keep = last[3]
     else:
-        keep = _turns(tuple(freqs), None if axis is None else tuple(axis), axes)
-        if isinstance(freqs, (list, tuple)) and (axis is None or isinstance(axis, (list, tuple))):
+        keep = _turns(tuple(map(float, freqs)), None if axis is None else tuple(map(int, axis)), axes)
+        if plain:
             _last_turns = (freqs[:], None if axis is None else axis[:], axes, keep)
     wqp = 0 if wq is None else _like(wq, (dim,), q.dtype, dev, "wq")
     wkp = 0 if wk is None else _like(wk, (dim,), q.dtype, dev, "wk")
@@ -1075,6 +1076,8 @@ def tpmlp_selftest_xent_stage_timeout(X: torch.Tensor, W: torch.Tensor, targets:
 def tpmlp_selftest_attn_core_timeout(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, backward: bool, load: int,
                                      limit_ms: int, stream=None) -> None:
     """Runs the bf16 attention's forward or backward on one sequence with load `load` of every CTA withheld (test hook)."""
+    if q.dim() != 3 or k.shape != q.shape or v.shape != q.shape or {q.dtype, k.dtype, v.dtype} != {torch.bfloat16}:
+        raise ValueError("q, k and v must be torch.bfloat16 of one shape [T, heads, head_dim]")
     T, heads, dim = q.shape
     with _On(stream) as on:
         q, k, v = (t.contiguous() for t in (q, k, v))

@@ -68,7 +68,7 @@ int make_view(HeadsView* v, const void* p, const int64_t* strides, int i, const 
   if (!aligned(p, 16)) return set_error(TPMLP_ERR_ALIGN, "%s must be 16-byte aligned", name);
   int64_t token = strides[2 * i], head = strides[2 * i + 1];
   if (heads == 1) head = dim;
-  if (T <= 1) token = heads == 1 ? dim : head * heads;
+  if (T <= 1) token = dim;
   const int64_t per = 16 / esz(dt);
   if (token < 1 || head < 1 || token > kMaxStride || head > kMaxStride || token % per != 0 || head % per != 0)
     return set_error(TPMLP_ERR_ALIGN, "the strides of %s (token %lld, head %lld) must be positive multiples of %lld elements",

@@ -237,3 +237,46 @@ def test_binding_refuses(tp):
     with pytest.raises(ValueError, match="positions"):
         tp._rope_args(q, k, pos.int(), f, None, False, None, None, 1e-6, 0)
     assert tp._turns((1.0, 2.0), (0, 1), 2)[0].tolist() == [1.0, 2.0]
+
+
+def test_frequencies_of_any_kind(tp):
+    import numpy as np
+    import torch
+
+    # Lists, tuples, arrays and tensors, one after another and again: the values count, not where they stand.
+    q, k, pos = torch.zeros(6, 4, 64), torch.zeros(6, 2, 64), torch.zeros(2, 6, dtype=torch.int64)
+
+    def made(f, a):
+        keep = tp._rope_args(q, k, pos, f, a, False, None, None, 1e-6, -1)[2]
+        return keep[0].tolist(), None if keep[1] is None else keep[1].tolist()
+
+    f, a = [2.0 ** -i for i in range(16)], [i % 2 for i in range(16)]
+    for ff, aa in [(f, a), (np.array(f), a), (f, np.array(a)), (torch.tensor(f), torch.tensor(a)), (tuple(f), tuple(a)),
+                   (np.array(f, np.float32), None), (f, a)] * 2:
+        assert made(ff, aa) == (f, None if aa is None else a)
+    f[3] = 0.5
+    assert made(f, a) == (f, a)
+    a[3] = 0
+    assert made(f, a) == (f, a)
+    with pytest.raises(ValueError, match="axis"):
+        tp._turns((1.0, 2.0), (0, 299), 300)
+
+
+def test_sizes_of_no_sequences_and_hook_shapes(tp):
+    import torch
+
+    assert tp.tpmlp_attn_core_workspace_bytes(16, 4, 2, 64, torch.bfloat16, batch=0) == 0
+    q = torch.zeros(6, 4, 64, dtype=torch.bfloat16)
+    for k in (q[:5], q.float(), q[0]):
+        with pytest.raises(ValueError, match="one shape"):
+            tp.tpmlp_selftest_attn_core_timeout(q, k, q, False, 1, 50)
+
+
+def test_one_token_of_a_large_layout(tp):
+    # One token of [heads, tokens, 64]: the head stride is large, and no other one counts.
+    for head in (1 << 20, 1 << 33):
+        one = array("q", [8, head] * 8)
+        rc = _core(tp, strides=one, T=1, batch=1, max_seq=1, heads=64, kv=64, lse=None)
+        assert rc == "TPMLP_ERR_ARG" and "lse" in tp.tpmlp_last_error()
+    assert _core(tp, strides=array("q", [64, 1 << 62] * 8), T=1, batch=1, max_seq=1) == "TPMLP_ERR_ALIGN"
+    assert _core(tp, strides=array("q", [64, 56] * 8), T=1, batch=1, max_seq=1) == "TPMLP_ERR_ARG"

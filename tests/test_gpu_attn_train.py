@@ -373,6 +373,27 @@ def test_nothing_to_do(tp):
     tp.tpmlp_check_status()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_token_of_a_large_layout(tp, dtype):
+    # One token of buffers [heads, tokens, 64]: the token stride is less than a row of all heads, and not used.
+    big = torch.full((9, 5000, 64), math.nan, device="cuda", dtype=DT[dtype])
+    big[:, 4999] = torch.randn(9, 64, generator=torch.Generator("cuda").manual_seed(5), device="cuda").to(DT[dtype])
+    one = big.transpose(0, 1)[4999:]
+    q, k, v, do = one[:, :4], one[:, 4:6], one[:, 6:8], one[:, 5:9]
+    pos, f = torch.full((1,), 77, device="cuda"), _freqs(64)
+
+    def run(q, k, v, do, out):
+        yq, yk = tp.tpmlp_qk_rope_forward(q, k, pos, f, yq=out(4), yk=out(2))
+        o, lse = tp.tpmlp_attn_core_forward(yq, yk, v, o=out(4))
+        dq, dk, dv = tp.tpmlp_attn_core_backward(yq, yk, v, o, lse, do, dq=out(4), dk=out(2), dv=out(2))
+        return o, lse, dv, *tp.tpmlp_qk_rope_backward(dq, dk, q, k, pos, f, dq=out(4), dk=out(2))[:2]
+
+    far = run(q, k, v, do, lambda n: torch.empty(n, 3000, 64, device="cuda", dtype=DT[dtype]).transpose(0, 1)[2999:])
+    near = run(*(t.contiguous() for t in (q, k, v, do)), lambda n: None)
+    tp.tpmlp_check_status()
+    assert all(torch.equal(a, b) for a, b in zip(far, near)) and bool(torch.isfinite(far[0]).all())
+
+
 # ------------------------------------------------------------------ norms and rotation
 
 
