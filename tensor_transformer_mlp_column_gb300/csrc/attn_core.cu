@@ -19,6 +19,9 @@
 // behind a sequence's end are read as zero, whatever they hold.
 #include "attn_core.h"
 
+#include <algorithm>
+
+#include "attn_core_walk.cuh"
 #include "device.cuh"
 #include "internal.h"
 #include "trace.h"
@@ -201,15 +204,31 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// Item i of a launch: tile, head and sequence. Causal: the tiles with the most
-// work (`last_first`: the last ones) come first.
-__device__ __forceinline__ void item_of(int64_t i, int tiles, int heads, bool last_first, int& tile, int& head, int& b) {
-  const int64_t per = int64_t(heads) * (gridDim.x / (int64_t(tiles) * heads));  // items of one tile index
-  tile = static_cast<int>(i / per);
-  if (last_first) tile = tiles - 1 - tile;
-  head = static_cast<int>(i % per % heads);
-  b = static_cast<int>(i % per / heads);
-}
+// What a CTA works on. Without WALK one item, given by its index: all heads and sequences of a tile index, causal the
+// tiles with the most work (`last_first`: the last ones) first; a tile that its sequence does not have is no work. With it
+// persistent CTAs walk over the tiles that there are.
+template <bool WALK, int ROWS>
+struct Work {
+  SequenceWalk walk;
+  int round = 0;
+  __device__ __forceinline__ Work(const CoreShape& s, int* status, int heads, bool last_first)
+      : walk(s, status, heads, ROWS, last_first, threadIdx.x & 31) {}
+  __device__ __forceinline__ bool next(Item& it) {
+    const CoreShape& s = walk.s;
+    if constexpr (WALK) {
+      if (!walk.find(walk_place(round++), it)) return false;
+    } else {
+      if (round++ > 0) return false;
+      const int64_t i = blockIdx.x, per = int64_t(walk.heads) * s.batch;  // items of one tile index
+      it.tile = static_cast<int>(i / per);
+      if (walk.last_first && s.causal) it.tile = (s.max_seq + ROWS - 1) / ROWS - 1 - it.tile;
+      it.head = static_cast<int>(i % per % walk.heads);
+      it.seq = static_cast<int>(i % per / walk.heads);
+    }
+    it.len = core_sequence(s, it.seq, it.row0, walk.status);
+    return it.tile * ROWS < it.len;
+  }
+};
 
 template <int DH, int N>
 __host__ __device__ constexpr int tile_floats() {
@@ -221,7 +240,7 @@ template <int DH, int ROWS, int BUFS>
 constexpr size_t forward_smem() {
   return sizeof(float) * (tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + ROWS * kPitchP);
 }
-template <int DH, int ROWS, int BUFS>
+template <int DH, int ROWS, int BUFS, bool WALK>
 __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_constant__ CoreForward c) {
   constexpr int THREADS = 4 * ROWS, W = tile_floats<DH, kWide>();
   extern __shared__ __align__(16) float smem[];
@@ -230,76 +249,75 @@ __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_con
   float* sp = skv + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
-  int tile, h, b;
-  item_of(blockIdx.x, (c.s.max_seq + ROWS - 1) / ROWS, c.s.heads, c.s.causal, tile, h, b);
-  int64_t row0;
-  const int len = core_sequence(c.s, b, row0, c.status);
-  const int q0 = tile * ROWS;
-  if (q0 >= len) return;
-  const int kv = h / (c.s.heads / c.s.kv_heads);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  auto copy = [&](int n) {
-    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
-    copies_commit();
-  };
-  copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
-  copy(0);
-  float m[4], l[4];
-  Rows<DH> acc;
-  clear<DH>(acc);
+  Item it;
+  for (Work<WALK, ROWS> work(c.s, c.status, c.s.heads, true); work.next(it);) {
+    const int64_t row0 = it.row0;
+    const int h = it.head, len = it.len, q0 = it.tile * ROWS;
+    const int kv = h / (c.s.heads / c.s.kv_heads);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto copy = [&](int n) {
+      copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
+      copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
+      copies_commit();
+    };
+    copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
+    copy(0);
+    float m[4], l[4];
+    Rows<DH> acc;
+    clear<DH>(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
-  const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
-  for (int n = 0; n < tiles; ++n) {
-    if (BUFS == 1 && n > 0) copy(n);
-    if (BUFS == 2 && n + 1 < tiles) {
-      copy(n + 1);
-      copies_wait<1>();
-    } else {
-      copies_wait<0>();
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
+    for (int n = 0; n < tiles; ++n) {
+      if (BUFS == 1 && n > 0) copy(n);
+      if (BUFS == 2 && n + 1 < tiles) {
+        copy(n + 1);
+        copies_wait<1>();
+      } else {
+        copies_wait<0>();
+      }
+      __syncthreads();
+      const float* sk = skv + n % BUFS * 2 * W;
+      const int k0 = n * kWide;
+      float s[4][4];
+      dot_tiles<DH, 16>(s, sq, sk, ty, tx);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int qi = q0 + 4 * ty + i;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int kj = k0 + tx + 16 * j;
+          s[i][j] = kj < len && (!c.s.causal || kj <= qi) ? s[i][j] * c.s.scale : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+        const float m_new = fmaxf(m[i], max16(mx));
+        const float base = m_new == -INFINITY ? 0.f : m_new;  // no score above -inf yet: weights of zero, not NaN
+        const float alpha = expf(m[i] - base);
+        m[i] = m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = expf(s[i][j] - base);
+          sum += p;
+          sp[(4 * ty + i) * kPitchP + tx + 16 * j] = p;
+        }
+        l[i] = l[i] * alpha + sum16(sum);
+        scale_row<DH>(acc, i, alpha);
+      }
+      __syncwarp();  // a warp's rows of P are read by the same warp
+      add_rows<DH>(acc, sp, sk + W, ty, tx);
+      __syncthreads();
     }
-    __syncthreads();
-    const float* sk = skv + n % BUFS * 2 * W;
-    const int k0 = n * kWide;
-    float s[4][4];
-    dot_tiles<DH, 16>(s, sq, sk, ty, tx);
+    float f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      f[i] = 1.0f / l[i];
       const int qi = q0 + 4 * ty + i;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kj = k0 + tx + 16 * j;
-        s[i][j] = kj < len && (!c.s.causal || kj <= qi) ? s[i][j] * c.s.scale : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
-      }
-      const float m_new = fmaxf(m[i], max16(mx));
-      const float base = m_new == -INFINITY ? 0.f : m_new;  // no score above -inf yet: weights of zero, not NaN
-      const float alpha = expf(m[i] - base);
-      m[i] = m_new;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = expf(s[i][j] - base);
-        sum += p;
-        sp[(4 * ty + i) * kPitchP + tx + 16 * j] = p;
-      }
-      l[i] = l[i] * alpha + sum16(sum);
-      scale_row<DH>(acc, i, alpha);
+      if (tx == 0 && qi < len) c.lse[int64_t(h) * c.s.T + row0 + qi] = m[i] + logf(l[i]);
     }
-    __syncwarp();  // a warp's rows of P are read by the same warp
-    add_rows<DH>(acc, sp, sk + W, ty, tx);
-    __syncthreads();
+    store_rows<DH>(c.o, row0, q0, len, h, c.s.dim, acc, f, ty, tx);
   }
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = 1.0f / l[i];
-    const int qi = q0 + 4 * ty + i;
-    if (tx == 0 && qi < len) c.lse[int64_t(h) * c.s.T + row0 + qi] = m[i] + logf(l[i]);
-  }
-  store_rows<DH>(c.o, row0, q0, len, h, c.s.dim, acc, f, ty, tx);
 }
 
 // delta[h][t] = sum over the head of dO * O: eight lanes a row of a head.
@@ -348,7 +366,7 @@ template <int DH, int ROWS, int BUFS>
 constexpr size_t dkv_smem() {
   return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + kWide * (ROWS + 4));
 }
-template <int DH, int ROWS, int BUFS>
+template <int DH, int ROWS, int BUFS, bool WALK>
 __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   constexpr int THREADS = 4 * ROWS, TX = ROWS / 4, W = tile_floats<DH, kWide>(), PITCH = ROWS + 4;
   extern __shared__ __align__(16) float smem[];
@@ -358,69 +376,68 @@ __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constan
   float* sp = sqd + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
-  int tile, kv, b;
-  item_of(blockIdx.x, (c.s.max_seq + ROWS - 1) / ROWS, c.s.kv_heads, false, tile, kv, b);
-  int64_t row0;
-  const int len = core_sequence(c.s, b, row0, c.status);
-  const int k0 = tile * ROWS;
-  if (k0 >= len) return;
-  const int group = c.s.heads / c.s.kv_heads;
-  const int sx = threadIdx.x % TX, sy = threadIdx.x / TX;    // of the scores: 64 queries x ROWS keys
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;    // of the outputs: ROWS keys
-  const int first = c.s.causal ? k0 / kWide : 0;
-  const int per = (len + kWide - 1) / kWide - first, passes = per * group;
-  auto copy = [&](int n) {
-    const int h = kv * group + n / per, q0 = (first + n % per) * kWide;
-    copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W, c.q, row0, q0, len, h, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W + W, c.d_o, row0, q0, len, h, c.s.dim);
-    copies_commit();
-  };
-  copy_tile<DH, ROWS, THREADS>(sk, c.k, row0, k0, len, kv, c.s.dim);
-  copy_tile<DH, ROWS, THREADS>(sv, c.v, row0, k0, len, kv, c.s.dim);
-  copy(0);
-  Rows<DH> dk, dv;
-  clear<DH>(dk);
-  clear<DH>(dv);
-  for (int n = 0; n < passes; ++n) {
-    const int h = kv * group + n / per, q0 = (first + n % per) * kWide;
-    float lse[4], del[4];
+  Item it;
+  for (Work<WALK, ROWS> work(c.s, c.status, c.s.kv_heads, false); work.next(it);) {
+    const int64_t row0 = it.row0;
+    const int kv = it.head, len = it.len, k0 = it.tile * ROWS;
+    const int group = c.s.heads / c.s.kv_heads;
+    const int sx = threadIdx.x % TX, sy = threadIdx.x / TX;    // of the scores: 64 queries x ROWS keys
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;    // of the outputs: ROWS keys
+    const int first = c.s.causal ? k0 / kWide : 0;
+    const int per = (len + kWide - 1) / kWide - first, passes = per * group;
+    auto copy = [&](int n) {
+      const int h = kv * group + n / per, q0 = (first + n % per) * kWide;
+      copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W, c.q, row0, q0, len, h, c.s.dim);
+      copy_tile<DH, kWide, THREADS>(sqd + n % BUFS * 2 * W + W, c.d_o, row0, q0, len, h, c.s.dim);
+      copies_commit();
+    };
+    copy_tile<DH, ROWS, THREADS>(sk, c.k, row0, k0, len, kv, c.s.dim);
+    copy_tile<DH, ROWS, THREADS>(sv, c.v, row0, k0, len, kv, c.s.dim);
+    copy(0);
+    Rows<DH> dk, dv;
+    clear<DH>(dk);
+    clear<DH>(dv);
+    for (int n = 0; n < passes; ++n) {
+      const int h = kv * group + n / per, q0 = (first + n % per) * kWide;
+      float lse[4], del[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = int64_t(h) * c.s.T + row0 + min(q0 + 4 * sy + i, len - 1);
-      lse[i] = c.lse[at];
-      del[i] = delta[at];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = int64_t(h) * c.s.T + row0 + min(q0 + 4 * sy + i, len - 1);
+        lse[i] = c.lse[at];
+        del[i] = delta[at];
+      }
+      if (BUFS == 1 && n > 0) copy(n);
+      if (BUFS == 2 && n + 1 < passes) {
+        copy(n + 1);
+        copies_wait<1>();
+      } else {
+        copies_wait<0>();
+      }
+      __syncthreads();
+      const float* sq = sqd + n % BUFS * 2 * W;
+      float s[4][4], dp[4][4], ds[4][4];
+      dot_tiles<DH, TX>(s, sq, sk, sy, sx);
+      dot_tiles<DH, TX>(dp, sq + W, sv, sy, sx);
+      probabilities<TX>(c.s, s, dp, lse, del, q0 + 4 * sy, k0 + sx, len, ds);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[(4 * sy + i) * PITCH + sx + TX * j] = s[i][j];
+      __syncthreads();
+      add_columns<DH>(dv, sp, PITCH, sq + W, ty, tx);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[(4 * sy + i) * PITCH + sx + TX * j] = ds[i][j];
+      __syncthreads();
+      add_columns<DH>(dk, sp, PITCH, sq, ty, tx);
+      __syncthreads();
     }
-    if (BUFS == 1 && n > 0) copy(n);
-    if (BUFS == 2 && n + 1 < passes) {
-      copy(n + 1);
-      copies_wait<1>();
-    } else {
-      copies_wait<0>();
-    }
-    __syncthreads();
-    const float* sq = sqd + n % BUFS * 2 * W;
-    float s[4][4], dp[4][4], ds[4][4];
-    dot_tiles<DH, TX>(s, sq, sk, sy, sx);
-    dot_tiles<DH, TX>(dp, sq + W, sv, sy, sx);
-    probabilities<TX>(c.s, s, dp, lse, del, q0 + 4 * sy, k0 + sx, len, ds);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sp[(4 * sy + i) * PITCH + sx + TX * j] = s[i][j];
-    __syncthreads();
-    add_columns<DH>(dv, sp, PITCH, sq + W, ty, tx);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sp[(4 * sy + i) * PITCH + sx + TX * j] = ds[i][j];
-    __syncthreads();
-    add_columns<DH>(dk, sp, PITCH, sq, ty, tx);
-    __syncthreads();
+    const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
+    store_rows<DH>(c.dv, row0, k0, len, kv, c.s.dim, dv, one, ty, tx);
+    store_rows<DH>(c.dk, row0, k0, len, kv, c.s.dim, dk, sc, ty, tx);
   }
-  const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
-  store_rows<DH>(c.dv, row0, k0, len, kv, c.s.dim, dv, one, ty, tx);
-  store_rows<DH>(c.dk, row0, k0, len, kv, c.s.dim, dk, sc, ty, tx);
 }
 
 // Queries and dO, then two buffers of keys and values, then dS.
@@ -428,7 +445,7 @@ template <int DH, int ROWS, int BUFS>
 constexpr size_t dq_smem() {
   return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + ROWS * kPitchP);
 }
-template <int DH, int ROWS, int BUFS>
+template <int DH, int ROWS, int BUFS, bool WALK>
 __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
   constexpr int THREADS = 4 * ROWS, W = tile_floats<DH, kWide>();
   extern __shared__ __align__(16) float smem[];
@@ -438,79 +455,92 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
   float* ss = skv + 2 * BUFS * W;
   pdl_wait();
   pdl_launch_dependents();
-  int tile, h, b;
-  item_of(blockIdx.x, (c.s.max_seq + ROWS - 1) / ROWS, c.s.heads, c.s.causal, tile, h, b);
-  int64_t row0;
-  const int len = core_sequence(c.s, b, row0, c.status);
-  const int q0 = tile * ROWS;
-  if (q0 >= len) return;
-  const int kv = h / (c.s.heads / c.s.kv_heads);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  auto copy = [&](int n) {
-    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
-    copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
-    copies_commit();
-  };
-  copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
-  copy_tile<DH, ROWS, THREADS>(sd, c.d_o, row0, q0, len, h, c.s.dim);
-  copy(0);
-  float lse[4], del[4];
+  Item it;
+  for (Work<WALK, ROWS> work(c.s, c.status, c.s.heads, true); work.next(it);) {
+    const int64_t row0 = it.row0;
+    const int h = it.head, len = it.len, q0 = it.tile * ROWS;
+    const int kv = h / (c.s.heads / c.s.kv_heads);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto copy = [&](int n) {
+      copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W, c.k, row0, n * kWide, len, kv, c.s.dim);
+      copy_tile<DH, kWide, THREADS>(skv + n % BUFS * 2 * W + W, c.v, row0, n * kWide, len, kv, c.s.dim);
+      copies_commit();
+    };
+    copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
+    copy_tile<DH, ROWS, THREADS>(sd, c.d_o, row0, q0, len, h, c.s.dim);
+    copy(0);
+    float lse[4], del[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = int64_t(h) * c.s.T + row0 + min(q0 + 4 * ty + i, len - 1);
-    lse[i] = c.lse[at];
-    del[i] = delta[at];
-  }
-  Rows<DH> dq;
-  clear<DH>(dq);
-  const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
-  for (int n = 0; n < tiles; ++n) {
-    if (BUFS == 1 && n > 0) copy(n);
-    if (BUFS == 2 && n + 1 < tiles) {
-      copy(n + 1);
-      copies_wait<1>();
-    } else {
-      copies_wait<0>();
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = int64_t(h) * c.s.T + row0 + min(q0 + 4 * ty + i, len - 1);
+      lse[i] = c.lse[at];
+      del[i] = delta[at];
     }
-    __syncthreads();
-    const float* sk = skv + n % BUFS * 2 * W;
-    float s[4][4], dp[4][4], ds[4][4];
-    dot_tiles<DH, 16>(s, sq, sk, ty, tx);
-    dot_tiles<DH, 16>(dp, sd, sk + W, ty, tx);
-    probabilities<16>(c.s, s, dp, lse, del, q0 + 4 * ty, n * kWide + tx, len, ds);
+    Rows<DH> dq;
+    clear<DH>(dq);
+    const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
+    for (int n = 0; n < tiles; ++n) {
+      if (BUFS == 1 && n > 0) copy(n);
+      if (BUFS == 2 && n + 1 < tiles) {
+        copy(n + 1);
+        copies_wait<1>();
+      } else {
+        copies_wait<0>();
+      }
+      __syncthreads();
+      const float* sk = skv + n % BUFS * 2 * W;
+      float s[4][4], dp[4][4], ds[4][4];
+      dot_tiles<DH, 16>(s, sq, sk, ty, tx);
+      dot_tiles<DH, 16>(dp, sd, sk + W, ty, tx);
+      probabilities<16>(c.s, s, dp, lse, del, q0 + 4 * ty, n * kWide + tx, len, ds);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ss[(4 * ty + i) * kPitchP + tx + 16 * j] = ds[i][j];
-    __syncwarp();  // a warp's rows of dS are read by the same warp
-    add_rows<DH>(dq, ss, sk, ty, tx);
-    __syncthreads();
+        for (int j = 0; j < 4; ++j) ss[(4 * ty + i) * kPitchP + tx + 16 * j] = ds[i][j];
+      __syncwarp();  // a warp's rows of dS are read by the same warp
+      add_rows<DH>(dq, ss, sk, ty, tx);
+      __syncthreads();
+    }
+    const float sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
+    store_rows<DH>(c.dq, row0, q0, len, h, c.s.dim, dq, sc, ty, tx);
   }
-  const float sc[4] = {c.s.scale, c.s.scale, c.s.scale, c.s.scale};
-  store_rows<DH>(c.dq, row0, q0, len, h, c.s.dim, dq, sc, ty, tx);
 }
 
-template <auto Kernel, typename... Args>
+// Whether a launch over all tiles of the longest length would be mostly of tiles that no sequence has: of sequences back to
+// back there are at most T / rows + batch. (Forward, one CTA a tile of the launch and walked. 1000 sequences in 65536 tokens,
+// 8 heads of 64, max_seq left at T: 16529 and 553 us; 13 in 4096, 12 heads, at T: 109 and 101; the same with a tight
+// max_seq: 91 and 101, as the GPU hands out CTAs when others end, and the walk does not know when that is.)
+bool walked(const CoreShape& s, int rows) {
+  return s.starts && int64_t((s.max_seq + rows - 1) / rows) * s.batch > 2 * (s.T / rows + s.batch);
+}
+
+template <auto Kernel, auto Walking, typename... Args>
 cudaError_t launch(const CoreShape& s, int rows, int heads, size_t smem, cudaStream_t stream, Args... args) {
-  static std::atomic<uint64_t> devices{0};
-  cudaError_t e = allow_smem(Kernel, smem, devices);
+  static std::atomic<uint64_t> devices{0}, walking{0};
+  const bool walk = walked(s, rows);
+  cudaError_t e = walk ? allow_smem(Walking, smem, walking) : allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
-  const int64_t items = int64_t((s.max_seq + rows - 1) / rows) * heads * s.batch;
-  return launch_pdl(Kernel, dim3(static_cast<unsigned>(items)), dim3(4 * rows), smem, stream, args...);
+  int64_t items = int64_t((s.max_seq + rows - 1) / rows) * heads * s.batch;
+  // As many as an SM's shared memory takes.
+  if (walk) items = std::min(items, int64_t(num_sms()) * static_cast<int64_t>(228 * 1024 / (smem + 1024)));
+  return launch_pdl(walk ? Walking : Kernel, dim3(static_cast<unsigned>(items)), dim3(4 * rows), smem, stream, args...);
 }
 
 template <int DH, int ROWS>
 cudaError_t simt_forward(const CoreForward& c, cudaStream_t s) {
-  return launch<core_forward_kernel<DH, ROWS, 2>>(c.s, ROWS, c.s.heads, forward_smem<DH, ROWS, 2>(), s, c);
+  return launch<core_forward_kernel<DH, ROWS, 2, false>, core_forward_kernel<DH, ROWS, 2, true>>(
+      c.s, ROWS, c.s.heads, forward_smem<DH, ROWS, 2>(), s, c);
 }
 
 template <int DH, int ROWS, int BUFS>
 cudaError_t simt_dkv(const CoreBackward& c, const float* delta, cudaStream_t s) {
-  return launch<core_dkv_kernel<DH, ROWS, BUFS>>(c.s, ROWS, c.s.kv_heads, dkv_smem<DH, ROWS, BUFS>(), s, c, delta);
+  return launch<core_dkv_kernel<DH, ROWS, BUFS, false>, core_dkv_kernel<DH, ROWS, BUFS, true>>(
+      c.s, ROWS, c.s.kv_heads, dkv_smem<DH, ROWS, BUFS>(), s, c, delta);
 }
 template <int DH, int ROWS, int BUFS>
 cudaError_t simt_dq(const CoreBackward& c, const float* delta, cudaStream_t s) {
-  return launch<core_dq_kernel<DH, ROWS, BUFS>>(c.s, ROWS, c.s.heads, dq_smem<DH, ROWS, BUFS>(), s, c, delta);
+  return launch<core_dq_kernel<DH, ROWS, BUFS, false>, core_dq_kernel<DH, ROWS, BUFS, true>>(
+      c.s, ROWS, c.s.heads, dq_smem<DH, ROWS, BUFS>(), s, c, delta);
 }
 
 // CTAs of `rows` tokens of each head and sequence that fill the GPU four times over.
@@ -554,7 +584,7 @@ cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
   }
   // As in the forward, but the backward of short heads stays ahead with 32 rows (16 heads of 64, 4 x 1024 tokens: 893 us
   // and 950 with 64; 16 heads of 128: 2050 with 32 and 1780 with 64). A second buffer takes the copies' time out of the
-  // loop, but without it four CTAs fit an SM in the place of two, and the others' work hides the copies: better where there
+  // loop, but without it three CTAs fit an SM in the place of two, and the others' work hides the copies: better where there
   // are that many (the same 16 heads of 64: 815 us with one buffer, 893 with two; 8 heads, 4 x 384: 107 and 97).
   const bool small = c.s.dim <= 64;
   {

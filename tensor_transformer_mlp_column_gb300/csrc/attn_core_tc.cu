@@ -34,6 +34,7 @@
 #include <string.h>
 
 #include "attn_core.h"
+#include "attn_core_walk.cuh"
 #include "device.cuh"
 #include "internal.h"
 #include "trace.h"
@@ -45,7 +46,6 @@ namespace {
 constexpr int kRows = 128;                   // tokens of a tile
 constexpr uint32_t kChunk = kRows * 128;     // 64 elements of its rows
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ pieces
 
@@ -288,84 +288,28 @@ __device__ __forceinline__ float* part_of(const TcParams& p, int z, int split, i
   return p.part + (at * kRows + row) * p.s.dim;
 }
 
-// What a CTA works on: `rows` tokens (a tile or a run of tiles) of a head of a sequence.
-struct Item {
-  int64_t row0;
-  int tile, head, len, seq;  // len 0: no more items
-};
-
-// The items of a CTA, found by its loading warp. They are in order of their work, the most first, and a CTA takes one of
-// every gridDim.x, from the front and from the back in turn, so that all get about the same. Of equal sequences those in
-// order are all tiles of one index. Of sequences of any lengths, 64 at a time, they are the ones with at least d tiles, d
-// from the longest's down (their d-th tile from the front, or from the back). All tiles of one index, of which
-// those past a sequence's end are skipped, was worse: of 13 sequences of 1 to 1500 tokens, 12 heads, the fullest CTA of dQ
-// had 86 key tiles in the place of 49, and of 1000 sequences in 65536 tokens, 32 heads of 128 on 8, it took dQ 888 us in the
-// place of 756, and 16600 where max_seq was left at 65536.
+// The items of a CTA, found by its loading warp, in order of their work (attn_core_walk.cuh); of equal sequences those in
+// order are all tiles of one index.
 struct Walk {
   const TcParams& p;
-  int heads, rows;
-  bool last_first;  // the last tiles of a sequence have the most work
-  int lane;
-  int base = -64;                 // the first of the 64 sequences
-  int c0, c1, d = 1;              // tiles of sequences base + `lane` and + 32; those with at least d are next, 0: no more
-  uint32_t m0, m1;                // which these are
-  uint64_t first = 0, count = 0;  // place of their first item, and how many there are
+  SequenceWalk sequences;
+  bool last_first;
   uint64_t round = 0;
 
-  __device__ __forceinline__ Walk(const TcParams& p_, int heads_, int rows_, bool last_first_, int lane_)
-      : p(p_), heads(heads_), rows(rows_), last_first(last_first_), lane(lane_) {}
-  // The tiles of the next 64 sequences that have any.
-  __device__ __forceinline__ void take() {
-    for (base += 64, d = 0; base < p.s.batch; base += 64) {
-      c0 = tiles_of(base + lane);
-      c1 = tiles_of(base + lane + 32);
-      d = __reduce_max_sync(kAll, max(c0, c1));
-      if (d > 0) return choose();
-    }
-  }
-  __device__ __forceinline__ int tiles_of(int b) const {
-    int64_t row0;
-    return b < p.s.batch ? (core_sequence(p.s, b, row0, p.status) + rows - 1) / rows : 0;
-  }
-  __device__ __forceinline__ void choose() {
-    m0 = __ballot_sync(kAll, c0 >= d);
-    m1 = __ballot_sync(kAll, c1 >= d);
-    count = static_cast<uint64_t>(__popc(m0) + __popc(m1)) * heads;
-  }
-  // The k-th of a mask's set bits.
-  __device__ __forceinline__ static int bit_of(uint32_t mask, int k) {
-    for (; k > 0; --k) mask &= mask - 1;
-    return __ffs(mask) - 1;
-  }
+  __device__ __forceinline__ Walk(const TcParams& p_, int heads, int rows, bool last_first_, int lane)
+      : p(p_), sequences(p_.s, p_.status, heads, rows, last_first_, lane), last_first(last_first_) {}
   // All lanes together.
   __device__ __forceinline__ bool next(Item& it) {
-    const uint32_t g = gridDim.x;
-    const uint64_t at = round * g + (round & 1 ? g - 1 - blockIdx.x : blockIdx.x);
-    ++round;
+    const uint64_t at = walk_place(round++);
     if (!p.s.starts) {
       if (at >= p.items) return false;
-      const uint32_t i = static_cast<uint32_t>(at), per = static_cast<uint32_t>(heads) * p.s.batch, in = i % per;
+      const uint32_t heads = sequences.heads, i = static_cast<uint32_t>(at), per = heads * p.s.batch, in = i % per;
       it.tile = static_cast<int>(i / per);
       if (last_first) it.tile = p.tiles - 1 - it.tile;
       it.head = static_cast<int>(in % heads);
       it.seq = static_cast<int>(in / heads);
-    } else {
-      // Places grow from round to round, whether from the front or the back.
-      while (d > 0 && at >= first + count) {
-        first += count;
-        if (--d > 0)
-          choose();
-        else
-          take();
-      }
-      if (d <= 0) return false;
-      const uint32_t in = static_cast<uint32_t>(at - first);
-      const int k = in / heads, n0 = __popc(m0);
-      const int b = k < n0 ? bit_of(m0, k) : 32 + bit_of(m1, k - n0);
-      const int c = __shfl_sync(kAll, b < 32 ? c0 : c1, b & 31);
-      it.head = in % heads;
-      it.tile = last_first ? d - 1 : c - d;
-      it.seq = base + b;
+    } else if (!sequences.find(at, it)) {
+      return false;
     }
     it.len = core_sequence(p.s, it.seq, it.row0, p.status);
     return true;

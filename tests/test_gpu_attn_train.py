@@ -180,6 +180,15 @@ def test_many_empty_sequences(tp, lengths, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths", [[5, 300] + [0] * 130 + [257, 1, 0, 40], [700] + [1] * 70 + [33], [0] * 70 + [65] * 5,
+                                     [64] * 40, [1, 2, 1000]])
+@pytest.mark.parametrize("dim", [64, 96])
+def test_longest_length_left_at_all_tokens(tp, lengths, causal, dim, dtype):
+    _check(tp, lengths, 6, 2, dim, dtype, causal, seed=len(lengths) + 3, first=3, behind=45, max_seq=48 + sum(lengths))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [8, 16, 24, 40, 56, 64, 72, 80, 96, 120, 128])
 def test_head_sizes(tp, dim, dtype):
     _check(tp, [150, 33], 2, 1, dim, dtype, True, seed=dim)
