@@ -522,7 +522,7 @@ int tpmlp_selftest_attn_core_timeout(const void* q, const void* k, const void* v
  *   q, yq     device [T, heads, head_dim], k, yk device [T, kv_heads, head_dim], of
  *             type dt; head_dim a multiple of 8 in 8 .. 256, rot one in 0 ..
  *             head_dim (TPMLP_ERR_SHAPE). yq may be q and yk may be k, with the
- *             same strides.
+ *             same strides (TPMLP_ERR_ARG).
  *   strides   of q, k, yq, yk.
  *   wq, wk    device [head_dim] of type dt, 16-byte aligned, or both NULL.
  *   pos       device int64 [axes, T], axes in 1 .. 8; any value.
@@ -545,7 +545,7 @@ size_t tpmlp_qk_rope_workspace_bytes(int64_t T, int heads, int kv_heads, int hea
  *   dw = sum over tokens and heads of g * n,
  *   dx = (g * w - n mean(g * w * n)) / sqrt(mean(x^2) + eps)  (no norm: dx = g).
  *   dyq, dyk  device, of type dt; dq, dk device, of type dt, written; dq may be
- *             dyq (or q) and dk dyk (or k), with the same strides.
+ *             dyq (or q) and dk dyk (or k), with the same strides (TPMLP_ERR_ARG).
  *   strides   of q, k, dyq, dyk, dq, dk.
  *   dwq, dwk  device fp32 [head_dim], written (zero for T = 0); with wq and wk NULL not looked at.
  *   workspace at least tpmlp_qk_rope_workspace_bytes(T, heads, kv_heads, head_dim)

@@ -243,6 +243,10 @@ int qk_rope(int backward, const void* dyq, const void* dyk, const void* q, const
       if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     }
   }
+  for (int i = 0; T > 0 && i < 2; ++i)
+    for (const HeadsView* in : {&c.x[i], &c.dy[i]})
+      if (in->p == c.y[i].p && (in->token != c.y[i].token || in->head != c.y[i].head))
+        return set_error(TPMLP_ERR_ARG, "an output in the place of its input must have the input's strides");
   if ((rc = current_sm103())) return rc;
   CORE_TRY(run_qk_rope(c, stream));
   return TPMLP_OK;

@@ -178,6 +178,15 @@ def test_rope_backward_argument_errors(tp, kw, code):
     assert _rope(tp, back=True, **kw) == code, tp.tpmlp_last_error()
 
 
+def test_rope_in_place_needs_the_same_strides(tp):
+    # (token, head) of q, k, (dyq, dyk,) and the outputs, of which every address is the same here.
+    for back, n, places in ((False, 4, (0, 2, 4, 6)), (True, 6, (0, 2, 4, 6, 8, 10))):
+        for i in places:
+            s = array("q", [512, 64] * n)
+            s[i] = 1024
+            assert _rope(tp, back, strides=s) == "TPMLP_ERR_ARG" and "place" in tp.tpmlp_last_error()
+
+
 def test_workspace_sizes(tp):
     l = tp.lib()
     core = l.tpmlp_attn_core_workspace_bytes
