@@ -494,8 +494,10 @@ size_t tpmlp_attn_core_workspace_bytes(int64_t T, int64_t batch, int64_t max_seq
  *             kv_heads, head_dim, dt) bytes.
  * Every sum has a fixed order: bitwise reproducible in calls of the same batch,
  * max_seq and heads (how sums of dk and dv are cut follows these). bf16 rounds p and ds to bf16
- * as operands and each result once; what delta is off because o was rounded is
- * found as the sum of a row's ds and taken out of ds's products again. */
+ * as operands and each result once; the rest of ds goes in as a second bf16 number in dq of
+ * heads below 64 and, where max_seq is at most 64 (heads above 64: 128), in dq and dk. What
+ * delta is off because o was rounded is found as the sum of a row's ds and taken out of ds's
+ * products again. */
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
                              const int64_t* strides, const int32_t* starts, int64_t T, int64_t batch, int64_t max_seq,
                              int heads, int kv_heads, int head_dim, float scale, int causal, tpmlp_dtype dt, void* dq,

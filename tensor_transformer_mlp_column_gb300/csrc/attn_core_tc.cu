@@ -247,6 +247,14 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float sum) {
   return sum;
 }
 
+// What rounding pairs of `v` to `w` left, as bf16.
+template <int N>
+__device__ __forceinline__ void rests(const float (&v)[N], uint32_t (&w)[N / 2]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2)
+    w[e / 2] = pack_bf16(v[e] - __uint_as_float(w[e / 2] << 16), v[e + 1] - __uint_as_float(w[e / 2] & 0xffff0000u));
+}
+
 // The first `dim` of a row's columns at `column` .. column + 31 as bf16, times f.
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&v)[32], float f, int column, int dim) {
 #pragma unroll
@@ -664,6 +672,16 @@ struct DqCfg {
 // P goes over S, dS over dP; the scores of tile j + 1 are made while the threads
 // work on dS of tile j, its dP while they work on P of tile j + 1.
 //
+// FINE: what rounding dS to bf16 leaves goes into dQ by a product of its own (and
+// into dK by one there). Otherwise that rounding leaves dQ about as far off as the
+// rounding of dQ itself, sqrt(2) of it together, more where a row's keys are alike:
+// 0.0025 in the place of 0.0017 for heads of 8 and 16, and for the few numbers of
+// short sequences, which are what it is for (dQ of heads below 64, dQ and dK where
+// max_seq is within the tile of W). 8 x 2048 tokens, 16 heads of 32: 124 -> 142 us,
+// 0.0024 -> 0.0017; 128 x 100 tokens, 32 heads of 128 on 8: 117 -> 131, dK and dV 94
+// -> 104. With longer heads and sequences, where all sums are long, it is left out
+// (8 x 2048 tokens, 32 heads of 128 on 8: 0.0024 and 415 us, with it 508).
+//
 // delta comes in as dO . O with the O that the forward rounded to bf16, which is
 // as far off as dQ's own rounding. But the row's sum of dS, zero for the exact
 // delta, says how far: e = sum of p dp - delta. dK's kernel gets delta + e, and dQ
@@ -671,7 +689,7 @@ struct DqCfg {
 // product, for 0.0023 in the place of 0.0030 as dQ's error (8 x 2048 tokens, 32
 // heads of 128). Rows with a single key tile take their own sum of p dp from the
 // start.
-template <int DH, int W>
+template <int DH, int W, bool FINE>
 __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
   using C = DqCfg<DH, W>;
   constexpr int H = C::COLUMNS, kMmaWarp = C::WARPS, kLoadWarp = C::WARPS + 1;
@@ -820,6 +838,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         tc_fence_after_sync();
         if (elect_one()) {
           product_tokens<W, H>(tmem + C::DQ, tmem + C::DP, k_tile, j > 0, H, p.steps);
+          if constexpr (FINE) product_tokens<W, H>(tmem + C::DQ, tmem + C::DP + H / 2, k_tile, true, H, p.steps);
           tc_commit(ring_k.empty + g % C::KS);
           if (j + 1 == n) tc_commit(done);
         }
@@ -946,11 +965,14 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         for (int e = 0; e < H; e += 2) {
           const uint64_t ds = mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), d2));
           sum[(e >> 1) & 1] = add_pair(sum[(e >> 1) & 1], ds);
-          float x0, x1;
-          unpair(ds, x0, x1);
-          w[e / 2] = pack_bf16(x0, x1);
+          unpair(ds, s[e], s[e + 1]);
+          w[e / 2] = pack_bf16(s[e], s[e + 1]);
         }
         tmem_st(t_dp, w);
+        if constexpr (FINE) {
+          rests<H>(s, w);
+          tmem_st(t_dp + H / 2, w);
+        }
         float x0, x1;
         unpair(add_pair(sum[0], sum[1]), x0, x1);
         total += x0 + x1;
@@ -1034,7 +1056,7 @@ struct DkvCfg {
 // Few key tiles for many queries (one kv head for all heads, say) would leave SMs
 // idle: then an item is one of p.splits runs of a tile's passes, which writes fp32
 // sums, and a last kernel adds them in order.
-template <int DH, int W>
+template <int DH, int W, bool FINE>
 __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
     dkv_kernel(const __grid_constant__ TcParams p) {
   using C = DkvCfg<DH, W>;
@@ -1236,6 +1258,8 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         tc_fence_after_sync();
         if (elect_one()) {
           product_tokens<W, H>(tmem + C::DK, tmem + C::DP, s_q + (g % C::QS) * C::NARROW, i > 0, H, p.steps);
+          if constexpr (FINE)
+            product_tokens<W, H>(tmem + C::DK, tmem + C::DP + H / 2, s_q + (g % C::QS) * C::NARROW, true, H, p.steps);
           tc_commit(ring_q.empty + g % C::QS);
           if (i + 1 == ps.n) tc_commit(done);
         }
@@ -1310,13 +1334,16 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
 #pragma unroll
         for (int e = 0; e < H; e += 4) {
           const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(rows + W + e);
-          float x0, x1, x2, x3;
-          unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), x0, x1);
-          unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), x2, x3);
-          w[e / 2] = pack_bf16(x0, x1);
-          w[e / 2 + 1] = pack_bf16(x2, x3);
+          unpair(mul_pair(pair(s[e], s[e + 1]), add_pair(pair(dp[e], dp[e + 1]), nd.x)), s[e], s[e + 1]);
+          unpair(mul_pair(pair(s[e + 2], s[e + 3]), add_pair(pair(dp[e + 2], dp[e + 3]), nd.y)), s[e + 2], s[e + 3]);
+          w[e / 2] = pack_bf16(s[e], s[e + 1]);
+          w[e / 2 + 1] = pack_bf16(s[e + 2], s[e + 3]);
         }
         tmem_st(t_dp, w);
+        if constexpr (FINE) {
+          rests<H>(s, w);
+          tmem_st(t_dp + H / 2, w);
+        }
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -1481,12 +1508,16 @@ cudaError_t launch_fwd(TcParams& p, cudaStream_t s) {
 template <int DH, int W>
 cudaError_t launch_dq(TcParams& p, cudaStream_t s) {
   using C = DqCfg<DH, W>;
-  return launch<dq_kernel<DH, W>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, C::CTAS, s);
+  return p.s.dim < 64 || p.s.max_seq <= W
+             ? launch<dq_kernel<DH, W, true>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, C::CTAS, s)
+             : launch<dq_kernel<DH, W, false>>(p, kRows, p.s.heads, C::THREADS, C::SMEM, C::CTAS, s);
 }
 template <int DH, int W>
 cudaError_t launch_dkv(TcParams& p, cudaStream_t s) {
   using C = DkvCfg<DH, W>;
-  cudaError_t e = launch<dkv_kernel<DH, W>>(p, kRows, p.s.kv_heads * p.splits, C::THREADS, C::SMEM, C::CTAS, s);
+  const int heads = p.s.kv_heads * p.splits;
+  cudaError_t e = p.s.max_seq <= W ? launch<dkv_kernel<DH, W, true>>(p, kRows, heads, C::THREADS, C::SMEM, C::CTAS, s)
+                                   : launch<dkv_kernel<DH, W, false>>(p, kRows, heads, C::THREADS, C::SMEM, C::CTAS, s);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_pdl(join_kernel, dim3(static_cast<unsigned>(p.items / p.splits), p.s.dim / 8), dim3(256), 0, s, p);
 }

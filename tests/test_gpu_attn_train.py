@@ -195,6 +195,51 @@ def test_head_sizes(tp, dim, dtype):
     _check(tp, [150, 33], 2, 1, dim, dtype, False, seed=dim + 1)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths,dim", [([1, 2, 3, 9, 40, 64], 64), ([64, 33], 8), ([128, 127, 5, 1], 128), ([100] * 5, 72),
+                                         ([700], 16), ([130, 64, 1, 1000], 40), ([65, 300], 56)])
+def test_both_pieces_of_ds(tp, lengths, dim, causal):
+    # Short sequences' dq and dk, and narrow heads' dq, are as far off as their own rounding to bf16 and fp32 sums make
+    # them: ds enters in two bf16 pieces (off by U16^2), and what delta is off (U16 of sum |do o|, rows of more than a
+    # tile) is taken out again with probabilities rounded to bf16, which leaves U16 of it.
+    T = sum(lengths)
+    q, k, v, do = _inputs(T, 3, 3, dim, "bf16", 77 + dim)
+    ends = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
+    kw = dict(starts=ends, max_seq=max(lengths), causal=causal)
+    o, lse = tp.tpmlp_attn_core_forward(q, k, v, **kw)
+    dq, dk, _ = tp.tpmlp_attn_core_backward(q, k, v, o, lse, do, **kw)
+    scale, c_dim, at = dim ** -0.5, _sum(dim, "bf16"), 0
+    short = max(lengths) <= (64 if dim <= 64 else 128)
+    for n in lengths:
+        r = slice(at, at + n)
+        at += n
+        c_n = _sum(n, "bf16")
+        hide = torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1) & causal
+        for h in range(3):
+            Q, K, V, G = (t[r, h].double() for t in (q, k, v, do))
+            s = (Q @ K.T * scale).masked_fill(hide, -math.inf)
+            mag = (Q.abs() @ K.abs().T * scale).masked_fill(hide, 0.0).max(dim=1).values
+            l = torch.logsumexp(s, 1)
+            p = torch.exp(s - l[:, None])
+            e_s = mag * (c_dim + 4 * U32) + 8 * U32 * (mag + l.abs() + 1)
+            e_p = (1.01 * (3 * e_s + (n + 4) * U32 + 8 * U32 * (l.abs() + 1)) + 8 * U32)[:, None]
+            O = p @ V
+            dp = G @ V.T
+            delta = (G * O).sum(1)[:, None]
+            e_dp = (G.abs() @ V.abs().T) * c_dim + 2 * U32 * (dp.abs() + delta.abs())
+            E = ((G.abs() * O.abs()).sum(1) * 1.02 * U16 + (G.abs() * (p @ V.abs())).sum(1) * 1.02 * U16)[:, None]
+            e_d = (p * e_dp).sum(1, True) + 2 * (e_p + c_n) * (p * (dp.abs() + delta.abs() + E)).sum(1, True) + 1.02 * U16 * E
+            ds = p * (dp - delta)
+            big = ds.abs() + p * E
+            e_ds = 1.02 * p * (e_dp + e_d) + big * (e_p + 8 * U32 + 1.02 * U16 * U16)
+            ref = ds @ K * scale
+            _close(dq[r, h], ref, scale * ((e_ds + c_n * big) @ K.abs() + c_n * E * (p @ K.abs())) + 1.01 * U16 * ref.abs() + 1e-30,
+                   f"dq {n}")
+            if short:
+                ref = ds.T @ Q * scale
+                _close(dk[r, h], ref, scale * ((e_ds + c_n * big).T @ Q.abs()) + 1.01 * U16 * ref.abs() + 1e-30, f"dk {n}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("heads,kv", [(1, 1), (3, 1), (8, 2), (6, 3), (12, 4), (5, 5), (16, 1)])
 def test_shared_heads(tp, heads, kv, dtype):
