@@ -445,7 +445,8 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  * at), rows of heads may not overlap (TPMLP_ERR_ARG), and the addresses are
  * 16-byte aligned. lse, dwq, dwk: 4 bytes, pos: 8. Outputs and workspace overlap
  * neither an input nor one another, unless a call says so. T is at most 2^30,
- * heads and kv_heads at most 4096.
+ * heads and kv_heads at most 4096, heads times the tiles of 32 rows of the
+ * attention's sequences (at most T / 32 + batch) below 2^31 (TPMLP_ERR_ARG).
  * ---------------------------------------------------------------------- */
 
 /* Softmax attention, for each sequence and each query head h, which reads kv

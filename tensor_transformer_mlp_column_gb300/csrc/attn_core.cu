@@ -514,14 +514,15 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
 // back there are at most T / rows + batch. (Forward, one CTA a tile of the launch and walked. 1000 sequences in 65536 tokens,
 // 8 heads of 64, max_seq left at T: 16529 and 553 us; 13 in 4096, 12 heads, at T: 109 and 101; the same with a tight
 // max_seq: 91 and 101, as the GPU hands out CTAs when others end, and the walk does not know when that is.)
-bool walked(const CoreShape& s, int rows) {
-  return s.starts && int64_t((s.max_seq + rows - 1) / rows) * s.batch > 2 * (s.T / rows + s.batch);
+bool walked(const CoreShape& s, int rows, int heads) {
+  const int64_t tiles = int64_t((s.max_seq + rows - 1) / rows) * s.batch;
+  return s.starts && (tiles > 2 * (s.T / rows + s.batch) || tiles * heads > INT32_MAX);
 }
 
 template <auto Kernel, auto Walking, typename... Args>
 cudaError_t launch(const CoreShape& s, int rows, int heads, size_t smem, cudaStream_t stream, Args... args) {
   static std::atomic<uint64_t> devices{0}, walking{0};
-  const bool walk = walked(s, rows);
+  const bool walk = walked(s, rows, heads);
   cudaError_t e = walk ? allow_smem(Walking, smem, walking) : allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
   int64_t items = int64_t((s.max_seq + rows - 1) / rows) * heads * s.batch;

@@ -3,6 +3,7 @@
 // workspace sizes; the work is launched by attn_core.cu and qk_rope.cu.
 #include "tpmlp.h"
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -96,7 +97,9 @@ int check_shape(int64_t T, int64_t batch, int64_t max_seq, int heads, int kv_hea
   if (batch < 0 || max_seq < 0 || batch > kMaxT || max_seq > T)
     return set_error(TPMLP_ERR_ARG, "batch = %lld must be in [0, 2^30] and max_seq = %lld in [0, T]",
                      static_cast<long long>(batch), static_cast<long long>(max_seq));
-  if ((max_seq + 31) / 32 * batch > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
+  // Tiles of 32 rows: as many as the longest length gives every sequence, but no more than T rows back to back can have.
+  const int64_t tiles = std::min((max_seq + 31) / 32 * batch, T / 32 + batch);
+  if (tiles > ((int64_t(1) << 31) - 1) / heads || T > (int64_t(1) << 35) / heads)
     return set_error(TPMLP_ERR_ARG, "too many sequences, heads and rows for one call");
   return TPMLP_OK;
 }

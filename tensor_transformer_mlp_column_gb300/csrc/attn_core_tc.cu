@@ -38,6 +38,8 @@
 #include <cudaTypedefs.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "attn_core.h"
 #include "attn_core_walk.cuh"
 #include "device.cuh"
@@ -289,7 +291,7 @@ struct TcParams {
   float scale_log2;
   int steps;       // of 16 elements: what products over or of the head take
   int tiles;       // tiles (forward: runs of NQ tiles) of the longest sequence
-  uint32_t items;  // tiles x heads x sequences
+  uint32_t items;  // tiles x heads x sequences, or 2^31 - 1 where that is less (with starts only, which do not need it)
   int withhold;    // test hook: > 0: that load of the CTA's first ring is not issued
   uint64_t wait_ns;
   int* status;
@@ -1499,7 +1501,7 @@ cudaError_t launch(TcParams& p, int rows, int heads, int threads, size_t smem, i
   p.tiles = (p.s.max_seq + rows - 1) / rows;
   cudaError_t e = allow_smem(Kernel, smem, devices);
   if (e != cudaSuccess) return e;
-  p.items = static_cast<uint32_t>(int64_t(p.tiles) * heads * p.s.batch);
+  p.items = static_cast<uint32_t>(std::min(int64_t(p.tiles) * heads * p.s.batch, int64_t(INT32_MAX)));
   const uint32_t most = static_cast<uint32_t>(num_sms()) * ctas;
   return launch_pdl(Kernel, dim3(p.items < most ? p.items : most), dim3(threads), smem, s, p);
 }

@@ -187,6 +187,14 @@ def test_rope_in_place_needs_the_same_strides(tp):
             assert _rope(tp, back, strides=s) == "TPMLP_ERR_ARG" and "place" in tp.tpmlp_last_error()
 
 
+def test_many_sequences_of_no_stated_length(tp):
+    # What counts is the tiles that T rows can have, not max_seq for every sequence.
+    l = tp.lib()
+    assert l.tpmlp_attn_core_workspace_bytes(1 << 18, 1 << 14, 1 << 18, 32, 8, 64, 1) > 0
+    assert l.tpmlp_attn_core_workspace_bytes(1 << 18, 1 << 14, 1 << 18, 32, 8, 64, 0) > 0
+    assert l.tpmlp_attn_core_workspace_bytes(1 << 18, 1 << 28, 1 << 18, 32, 8, 64, 0) == 0
+
+
 def test_workspace_sizes(tp):
     l = tp.lib()
     core = l.tpmlp_attn_core_workspace_bytes

@@ -195,6 +195,25 @@ def test_head_sizes(tp, dim, dtype):
     _check(tp, [150, 33], 2, 1, dim, dtype, False, seed=dim + 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences_of_no_stated_length(tp, dtype):
+    # max_seq for every sequence would be 2^32 tiles of 32 rows; what there is to do is as with the longest length given.
+    T, n, heads = 1 << 17, 1 << 15, 32
+    g = torch.Generator().manual_seed(3)
+    ends = torch.cat([torch.zeros(1, dtype=torch.long), torch.randint(0, 8, (n,), generator=g).cumsum(0)])
+    longest, starts = int((ends[1:] - ends[:-1]).max()), ends.to(torch.int32).cuda()
+    q, k, v, do = _inputs(T, heads, 1, 8, dtype, 31)
+    got = []
+    for most in (longest, None):
+        o, lse = tp.tpmlp_attn_core_forward(q, k, v, starts=starts, max_seq=most, o=torch.zeros_like(q),
+                                            lse=torch.zeros(heads, T, device="cuda"))
+        dq, _, dv = tp.tpmlp_attn_core_backward(q, k, v, o, lse, do, starts=starts, max_seq=most, dq=torch.zeros_like(q),
+                                                dv=torch.zeros_like(v))
+        got.append((o, lse, dq, dv))
+    tp.tpmlp_check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][0].float().abs().sum().item() > 0
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lengths,dim", [([1, 2, 3, 9, 40, 64], 64), ([64, 33], 8), ([128, 127, 5, 1], 128), ([100] * 5, 72),
                                          ([700], 16), ([130, 64, 1, 1000], 40), ([65, 300], 56)])
