@@ -23,9 +23,9 @@ __device__ __forceinline__ uint64_t walk_place(uint64_t round) {
 
 // The items of sequences of any lengths in order of their work: 64 sequences at a time, the ones with at least d tiles, d
 // from the longest's down (their d-th tile from the front, or from the back). All tiles of one index, of which
-// those past a sequence's end are skipped, was worse: of 13 sequences of 1 to 1500 tokens, 12 heads, the fullest CTA of dQ
-// (bf16) had 86 key tiles in the place of 49, and of 1000 sequences in 65536 tokens, 32 heads of 128 on 8, it took dQ 888 us
-// in the place of 756, and 16600 where max_seq was left at 65536.
+// those past a sequence's end are skipped, was worse: of 13 sequences of 1 to 1500 tokens, 12 heads, causal, the fullest
+// CTA of dQ (bf16) had 66 key tiles in the place of 36 (33.6 on average), and of 1000 sequences in 65536 tokens, 32 heads of
+// 128 on 8, it took dQ 888 us in the place of 756, and 16600 where max_seq was left at 65536.
 struct SequenceWalk {
   const CoreShape& s;
   int* status;
