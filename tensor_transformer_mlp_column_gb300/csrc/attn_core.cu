@@ -7,10 +7,10 @@
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
 //
 // The scores are never stored: the forward keeps a running maximum and sum for
-// each row, the backward makes the probabilities again from lse. dK and dV
-// come from one kernel (a CTA per ROWS keys of a kv head, walking over the
-// queries of every head that shares them) and dQ from another (a CTA per ROWS
-// queries), so every sum has one owner and a fixed order, without atomics.
+// each row, the backward makes the probabilities again from lse. dQ (with
+// delta) comes from one kernel (a CTA per ROWS queries), dK and dV from the next (a
+// CTA per ROWS keys of a kv head, walking over the queries of every head that
+// shares them), so every sum has one owner and a fixed order, without atomics.
 //
 // A CTA holds ROWS x 64 scores, 4 x 4 for each of its 4 ROWS threads, and its
 // tiles in shared memory, rows 4 words longer than the head so that 8 rows read
@@ -18,9 +18,13 @@
 // cp.async, one ahead. Products go two at a time (packed fp32 pairs). Rows
 // behind a sequence's end are read as zero, whatever they hold.
 //
+// The kernels do not let the stream's next one in early: its CTAs would wait in the
+// places that this one's second round needs, unevenly (2 x 300 tokens, 8 heads of 64
+// on 2, a step: 205 us so, 174 without; 4 x 384, 8 heads: 129 and 117).
+//
 // Bound by issue and shared memory: 16 heads of 128, 4 x 1024 tokens, causal, 463,
-// 690 (dQ) and 976 us (dK, dV), 37, 37 and 35 TFLOP/s of about 75; 16 heads of 64
-// 239, 352 and 462.
+// 706 (dQ) and 976 us (dK, dV), 37, 37 and 35 TFLOP/s of about 75; 16 heads of 64
+// 239, 358 and 462.
 #include "attn_core.h"
 
 #include <algorithm>
@@ -252,7 +256,6 @@ __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_con
   float* skv = sq + tile_floats<DH, ROWS>();  // [BUFS][2]
   float* sp = skv + 2 * BUFS * W;
   pdl_wait();
-  pdl_launch_dependents();
   Item it;
   for (Work<WALK, ROWS> work(c.s, c.status, c.s.heads, true); work.next(it);) {
     const int64_t row0 = it.row0;
@@ -324,28 +327,6 @@ __global__ void __launch_bounds__(4 * ROWS) core_forward_kernel(const __grid_con
   }
 }
 
-// delta[h][t] = sum over the head of dO * O: eight lanes a row of a head.
-__global__ void __launch_bounds__(256) core_delta_kernel(HeadsView o, HeadsView d_o, int64_t T_, int heads, int dim,
-                                                         float* delta) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 8;  // head fastest: neighbours in memory
-  if (i >= T_ * heads) return;  // all eight lanes of a row at once, and the shuffles name only them
-  const int lane = threadIdx.x & 7, h = static_cast<int>(i % heads);
-  const int64_t t = i / heads;
-  const float* a = row_of(o, t, h);
-  const float* b = row_of(d_o, t, h);
-  float sum = 0.f;
-  for (int c = 4 * lane; c < dim; c += 32) {
-    const float4 x = load4(a + c), y = load4(b + c);
-    sum = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sum))));
-  }
-  const uint32_t mask = 0xffu << (threadIdx.x & 24);
-#pragma unroll
-  for (int x = 4; x > 0; x >>= 1) sum += __shfl_xor_sync(mask, sum, x);
-  if (lane == 0) delta[int64_t(h) * T_ + t] = sum;
-}
-
 // p and ds of a thread's 4 x 4 scores (rows: queries from q, columns: keys k, k + TX ..). Both are zero wherever a
 // query or a key does not count.
 template <int TX>
@@ -379,7 +360,6 @@ __global__ void __launch_bounds__(4 * ROWS) core_dkv_kernel(const __grid_constan
   float* sqd = sv + tile_floats<DH, ROWS>();  // [BUFS][2]
   float* sp = sqd + 2 * BUFS * W;
   pdl_wait();
-  pdl_launch_dependents();
   Item it;
   for (Work<WALK, ROWS> work(c.s, c.status, c.s.kv_heads, false); work.next(it);) {
     const int64_t row0 = it.row0;
@@ -450,7 +430,7 @@ constexpr size_t dq_smem() {
   return sizeof(float) * (2 * tile_floats<DH, ROWS>() + 2 * BUFS * tile_floats<DH, kWide>() + ROWS * kPitchP);
 }
 template <int DH, int ROWS, int BUFS, bool WALK>
-__global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant__ CoreBackward c, const float* delta) {
+__global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant__ CoreBackward c, float* delta) {
   constexpr int THREADS = 4 * ROWS, W = tile_floats<DH, kWide>();
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
@@ -458,7 +438,6 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
   float* skv = sd + tile_floats<DH, ROWS>();  // [BUFS][2]
   float* ss = skv + 2 * BUFS * W;
   pdl_wait();
-  pdl_launch_dependents();
   Item it;
   for (Work<WALK, ROWS> work(c.s, c.status, c.s.heads, true); work.next(it);) {
     const int64_t row0 = it.row0;
@@ -472,14 +451,32 @@ __global__ void __launch_bounds__(4 * ROWS) core_dq_kernel(const __grid_constant
     };
     copy_tile<DH, ROWS, THREADS>(sq, c.q, row0, q0, len, h, c.s.dim);
     copy_tile<DH, ROWS, THREADS>(sd, c.d_o, row0, q0, len, h, c.s.dim);
+    copies_commit();
     copy(0);
+    // delta: four lanes a row, all of them in the warp that takes the row's scores below; O while dO comes.
+    const int r = threadIdx.x >> 2;
+    float4 o[DH / 16];
+#pragma unroll
+    for (int x = 0; x < DH / 16; ++x) {
+      const int e = 16 * x + 4 * (threadIdx.x & 3);
+      o[x] = q0 + r < len && e < c.s.dim ? load4(row_of(c.o, row0 + q0 + r, h) + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float lse[4], del[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = int64_t(h) * c.s.T + row0 + min(q0 + 4 * ty + i, len - 1);
-      lse[i] = c.lse[at];
-      del[i] = delta[at];
+    for (int i = 0; i < 4; ++i) lse[i] = c.lse[int64_t(h) * c.s.T + row0 + min(q0 + 4 * ty + i, len - 1)];
+    copies_wait<1>();
+    __syncthreads();
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < DH / 16; ++x) {
+      const float4 d = load4(sd + r * (DH + 4) + 16 * x + 4 * (threadIdx.x & 3));
+      sum = fmaf(o[x].x, d.x, fmaf(o[x].y, d.y, fmaf(o[x].z, d.z, fmaf(o[x].w, d.w, sum))));
     }
+    sum += __shfl_xor_sync(kAll, sum, 2);
+    sum += __shfl_xor_sync(kAll, sum, 1);
+    if ((threadIdx.x & 3) == 0 && q0 + r < len) delta[int64_t(h) * c.s.T + row0 + q0 + r] = sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) del[i] = __shfl_sync(kAll, sum, 16 * (ty & 1) + 4 * i);
     Rows<DH> dq;
     clear<DH>(dq);
     const int tiles = ((c.s.causal ? min(len, q0 + ROWS) : len) + kWide - 1) / kWide;
@@ -543,7 +540,7 @@ cudaError_t simt_dkv(const CoreBackward& c, const float* delta, cudaStream_t s) 
       c.s, ROWS, c.s.kv_heads, dkv_smem<DH, ROWS, BUFS>(), s, c, delta);
 }
 template <int DH, int ROWS, int BUFS>
-cudaError_t simt_dq(const CoreBackward& c, const float* delta, cudaStream_t s) {
+cudaError_t simt_dq(const CoreBackward& c, float* delta, cudaStream_t s) {
   return launch<core_dq_kernel<DH, ROWS, BUFS, false>, core_dq_kernel<DH, ROWS, BUFS, true>>(
       c.s, ROWS, c.s.heads, dq_smem<DH, ROWS, BUFS>(), s, c, delta);
 }
@@ -581,28 +578,22 @@ cudaError_t run_core_backward(const CoreBackward& c, cudaStream_t s) {
   float* delta = static_cast<float*>(c.ws);
   if (c.bf16)
     return launch_core_backward_tc(c, delta, delta + delta_bytes(c.s.T, c.s.heads) / sizeof(float), s);
-  {
-    TraceScope trace("attn_core_delta", s);
-    const unsigned grid = static_cast<unsigned>((c.s.T * c.s.heads + 31) / 32);
-    cudaError_t e = launch_pdl(core_delta_kernel, dim3(grid), dim3(256), 0, s, c.o, c.d_o, c.s.T, c.s.heads, c.s.dim, delta);
-    if (e != cudaSuccess) return e;
-  }
   // As in the forward, but the backward of short heads stays ahead with 32 rows (16 heads of 64, 4 x 1024 tokens: 893 us
   // and 950 with 64; 16 heads of 128: 2050 with 32 and 1780 with 64). A second buffer takes the copies' time out of the
   // loop, but without it three CTAs fit an SM in the place of two, and the others' work hides the copies: better where there
   // are that many (the same 16 heads of 64: 815 us with one buffer, 893 with two; 8 heads, 4 x 384: 107 and 97).
   const bool small = c.s.dim <= 64;
-  {
-    TraceScope trace("attn_core_dkv", s);
-    cudaError_t e = !small                         ? simt_dkv<128, 64, 2>(c, delta, s)
-                    : many(c.s, 32, c.s.kv_heads) ? simt_dkv<64, 32, 1>(c, delta, s)
-                                                  : simt_dkv<64, 32, 2>(c, delta, s);
+  {  // makes delta as well, which dK needs
+    TraceScope trace("attn_core_dq", s);
+    cudaError_t e = !small                      ? simt_dq<128, 64, 2>(c, delta, s)
+                    : many(c.s, 32, c.s.heads) ? simt_dq<64, 32, 1>(c, delta, s)
+                                               : simt_dq<64, 32, 2>(c, delta, s);
     if (e != cudaSuccess) return e;
   }
-  TraceScope trace("attn_core_dq", s);
-  return !small                      ? simt_dq<128, 64, 2>(c, delta, s)
-         : many(c.s, 32, c.s.heads) ? simt_dq<64, 32, 1>(c, delta, s)
-                                    : simt_dq<64, 32, 2>(c, delta, s);
+  TraceScope trace("attn_core_dkv", s);
+  return !small                         ? simt_dkv<128, 64, 2>(c, delta, s)
+         : many(c.s, 32, c.s.kv_heads) ? simt_dkv<64, 32, 1>(c, delta, s)
+                                       : simt_dkv<64, 32, 2>(c, delta, s);
 }
 
 }  // namespace tpmlp
