@@ -30,6 +30,12 @@
 // dK and dV 665 us, 1.65), by the chain from S to P and dS where they are short
 // (heads of 64: 310, 463 and 578 us, 0.89, 1.19 and 0.95 PFLOP/s).
 //
+// The next kernel of the stream is let in by the loading warp when it has fetched its
+// last item. Let in at the start, its CTAs waited in places beside the ones still at
+// work, and unevenly (13 sequences of 1 to 1500 tokens, 12 heads of 80, a step: 202
+// us, at the end 184; 8 x 512 tokens, 16 heads of 64: 78.5 and 74; 3 x 17 tokens: 23
+// and 20).
+//
 // Warps: 4 or 8 for the softmax (warp w reads tensor memory lanes 32 (w % 4) ..),
 // one issuing products, one issuing loads. Every wait is bounded; after a failure
 // copies and products in flight are waited for and tensor memory is freed.
@@ -444,7 +450,6 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
   // Key tiles of the item's query tile a.
@@ -489,6 +494,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
         ++issued;
       }
     }
+    pdl_launch_dependents();
     it.len = 0;
     if (ok) ring_i.give(items, it, lane, guard);
   } else if (warp == kMma) {
@@ -749,7 +755,6 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
   // Key tiles of an item.
@@ -791,6 +796,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
         ++issued_v;
       }
     }
+    pdl_launch_dependents();
     it.len = 0;
     if (ok) ring_i.give(items, it, lane, guard);
   } else if (warp == kMmaWarp) {
@@ -1117,7 +1123,6 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  pdl_launch_dependents();
   const WaitGuard guard{abort_flag, p.wait_ns, p.status};
   const int group = p.s.heads / p.s.kv_heads;
   // Passes of an item: the query tiles `first` .. `first` + `per` - 1 of every head of the group, head by head; of these n
@@ -1202,6 +1207,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
         if (i + 1 < ps.n) fetch(h, x);
       }
     }
+    pdl_launch_dependents();
     it.len = 0;
     if (ok) ring_i.give(given, it, lane, guard);
   } else if (warp == kMmaWarp) {
@@ -1418,7 +1424,6 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
 // dV and dK of a tile of keys as the sums of their splits, in order. Eight elements a thread; blockIdx.y a 256th of theirs.
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcParams p) {
   pdl_wait();
-  pdl_launch_dependents();
   const int64_t per = int64_t(p.s.kv_heads) * p.s.batch;
   const int tile = static_cast<int>(blockIdx.x / per), in = static_cast<int>(blockIdx.x % per);
   const int kv = in % p.s.kv_heads, seq = in / p.s.kv_heads;
