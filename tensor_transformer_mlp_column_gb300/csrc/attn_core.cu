@@ -22,7 +22,9 @@
 // places that this one's second round needs, unevenly (2 x 300 tokens, 8 heads of 64
 // on 2, a step: 205 us so, 174 without; 4 x 384, 8 heads: 129 and 117).
 //
-// Bound by issue and shared memory: 16 heads of 128, 4 x 1024 tokens, causal, 463,
+// Bound by what shared memory returns to the registers, 16 bytes a lane eight times
+// for 64 multiply-adds a lane (65 to 78 % of that path busy, 54 to 60 of the FMA pipe;
+// which lanes read the same line makes no difference): 16 heads of 128, 4 x 1024 tokens, causal, 463,
 // 706 (dQ) and 976 us (dK, dV), 37, 37 and 35 TFLOP/s of about 75; 16 heads of 64
 // 239, 358 and 462.
 #include "attn_core.h"
