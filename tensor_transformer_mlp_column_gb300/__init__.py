@@ -911,6 +911,11 @@ def _turns(freqs: tuple, axis: Optional[tuple], axes: int):
 
 
 _last_turns = (None, None, 0, None)
+_NUMBERS = {int, float}
+
+
+def _own_numbers(x) -> bool:
+    return isinstance(x, (list, tuple)) and set(map(type, x)) <= _NUMBERS
 
 
 def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
@@ -920,10 +925,12 @@ def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
     if pos.dtype != torch.int64 or len(at) not in (1, 2) or at[-1] != T:
         raise ValueError(f"pos must be an int64 tensor of {T} positions, or [axes, {T}]")
     axes = at[0] if len(at) == 2 else 1
-    # A program's frequencies are the same in every call: the last call's arrays serve while its values are equal.
+    # A program's frequencies are the same in every call: the last call's arrays serve while its values are equal. Only
+    # Python's own numbers are compared so: 0-dim tensors and arrays may be views whose values change, in the kept copy of
+    # the list too, and compare in their own precision.
     global _last_turns
     last = _last_turns
-    plain = isinstance(freqs, (list, tuple)) and (axis is None or isinstance(axis, (list, tuple)))
+    plain = _own_numbers(freqs) and (axis is None or _own_numbers(axis))
     if plain and last[0] == freqs and last[1] == axis and last[2] == axes:
         keep = last[3]
     else:

@@ -297,3 +297,35 @@ def test_one_token_of_a_large_layout(tp):
         assert rc == "TPMLP_ERR_ARG" and "lse" in tp.tpmlp_last_error()
     assert _core(tp, strides=array("q", [64, 1 << 62] * 8), T=1, batch=1, max_seq=1) == "TPMLP_ERR_ALIGN"
     assert _core(tp, strides=array("q", [64, 56] * 8), T=1, batch=1, max_seq=1) == "TPMLP_ERR_ARG"
+
+
+def test_frequencies_changed_in_place(tp):
+    import numpy as np
+    import torch
+
+    # Elements that are views (0-dim tensors, arrays) change with their tensor: every call takes the values of its time.
+    q, k, pos = torch.zeros(6, 4, 64), torch.zeros(6, 2, 64), torch.zeros(2, 6, dtype=torch.int64)
+
+    def made(f, a):
+        keep = tp._rope_args(q, k, pos, f, a, False, None, None, 1e-6, -1)[2]
+        return keep[0].tolist(), None if keep[1] is None else keep[1].tolist()
+
+    want = [2.0 ** -i for i in range(16)]
+    for make in (lambda: torch.tensor(want), lambda: torch.tensor(want, dtype=torch.float64)):
+        for kind in (list, tuple):
+            t, a = make(), torch.arange(16) % 2
+            f, ax = kind(t), kind(a)
+            assert made(f, ax) == (want, [i % 2 for i in range(16)])
+            t.mul_(0.5)
+            a[0] = 1
+            half = ([0.5 * w for w in want], [1] + [i % 2 for i in range(1, 16)])
+            assert made(kind(t), kind(a)) == half  # new views of the same memory
+            assert made(f, ax) == half             # the same list as before
+    f = [np.array(w) for w in want]
+    assert made(f, None)[0] == want
+    f[2][...] = 9.0
+    assert made(f, None)[0] == want[:2] + [9.0] + want[3:]
+    # Numbers that compare equal in 32 bits but are not: 0.1 and the nearest 32-bit number.
+    assert made([0.1] * 4, None)[0] == [0.1] * 4
+    assert made(list(np.full(4, 0.1, np.float32)), None)[0] == [float(np.float32(0.1))] * 4
+    assert made([0.1] * 4, None)[0] == [0.1] * 4
