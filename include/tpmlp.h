@@ -533,7 +533,7 @@ int tpmlp_selftest_attn_core_timeout(const void* q, const void* k, const void* v
  *             scaled for long contexts); read during the call.
  *   axis      host [rot / 2], below axes, or NULL: all 0; read during the call.
  * Computed in fp32 and rounded once. An angle keeps its fraction of a turn to
- * about 2^-53 |pos| turns, however far the position. */
+ * 2^-64 |pos| turns, however far the position, for |freqs[i]| up to 2^40. */
 int tpmlp_qk_rope_forward(const void* q, const void* k, const int64_t* strides, const void* wq, const void* wk, float eps,
                           const int64_t* pos, const double* freqs, const uint8_t* axis, int64_t T, int heads, int kv_heads,
                           int head_dim, int rot, int axes, int interleaved, tpmlp_dtype dt, void* yq, void* yk,

@@ -184,6 +184,17 @@ int core_backward(const void* q, const void* k, const void* v, const void* o, co
   return TPMLP_OK;
 }
 
+// f / (2 pi) modulo 1 as a 64-bit binary fraction, off by less than 2^-64 for |f| up to 2^40: the quotient as the sum of two
+// doubles, 1 / (2 pi) being two (together off by 2^-110), each without its whole part, which is taken off exactly.
+uint64_t turn_of(double f) {
+  const double inv = 0x1.45f306dc9c883p-3, inv_rest = -0x1.6b01ec5417056p-57, unit = 18446744073709551616.0;
+  const volatile double rounded = f * inv;  // volatile: the product is not to be fused with what follows
+  const double product = rounded, rest = std::fma(f, inv_rest, std::fma(f, inv, -product));
+  const double x = (product - std::rint(product)) * unit, y = (rest - std::rint(rest)) * unit;  // each at most 2^63
+  const double whole = std::floor(x);
+  return static_cast<uint64_t>(static_cast<__int128>(whole) + static_cast<__int128>(std::rint((x - whole) + y)));
+}
+
 // Both forms of the rotation: dy, dq.. are the backward's. strides: q, k, (dyq, dyk,) and the two outputs.
 int qk_rope(int backward, const void* dyq, const void* dyk, const void* q, const void* k, const int64_t* strides,
             const void* wq, const void* wk, float eps, const int64_t* pos, const double* freqs, const uint8_t* axis,
@@ -202,10 +213,7 @@ int qk_rope(int backward, const void* dyq, const void* dyk, const void* q, const
   for (int i = 0; i < rot / 2; ++i) {
     if (!std::isfinite(freqs[i])) return set_error(TPMLP_ERR_ARG, "freqs[%d] must be finite", i);
     if (axis && axis[i] >= axes) return set_error(TPMLP_ERR_ARG, "axis[%d] = %d must be below axes = %d", i, int(axis[i]), axes);
-    // Turns per position as a 64-bit binary fraction; whole turns do not count.
-    const double turns = freqs[i] / 6.283185307179586477;
-    const double part = turns - std::floor(turns);
-    c.s.turn[i] = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
+    c.s.turn[i] = turn_of(freqs[i]);
     c.s.axis[i] = axis ? axis[i] : 0;
   }
   if (backward && wq && (!dwq || !dwk || !aligned(dwq, 4) || !aligned(dwk, 4)))

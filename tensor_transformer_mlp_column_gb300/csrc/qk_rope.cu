@@ -7,9 +7,9 @@
 //         dx = r (g * w - n mean(g * w * n))
 //
 // The angle of a pair is a number of turns, pos * f / (2 pi), of which only the
-// fraction counts: with f / (2 pi) as a 64-bit binary fraction the product
-// modulo 2^64 is that fraction to 2^-64 pos, at any position, without 64-bit
-// floating point.
+// fraction counts: with f / (2 pi) as a 64-bit binary fraction (made by the host,
+// off by less than 2^-64) the product modulo 2^64 is that fraction to 2^-64 pos, at
+// any position, without 64-bit floating point here.
 //
 // Bound by memory: x is read once (backward: x and dy) and y written once (16384
 // tokens, 32 + 8 heads of 128, bf16: 62 us, 5.4 TB/s, and 97 us, 5.2 TB/s; fp32 107

@@ -851,3 +851,44 @@ print("captured")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+_PI = 3141592653589793238462643383279502884197169399375105820974944592307816  # 10^69 pi
+
+
+def _angle(pos, f):
+    """pos * f without its whole turns, from integers: off by less than 2^-50 of a turn for |pos f| < 2^150."""
+    n, d = f.as_integer_ratio()
+    unit = 2 * _PI * d  # a whole turn, in units of 1 / (10^69 d)
+    part = pos * n * 10 ** 69 % unit
+    return 2 * math.pi * (part / unit)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_fast_frequencies_and_far_positions(tp, inter, dtype):
+    # The turn is off by 2^-64 |pos| (2^-24 here), whatever the frequency. fp32: the angle as a fraction of half a turn and
+    # sincospi's argument, pi U32, its result 2 U32, the turn's products and sum 3 U32 of |a| + |b|. bf16: 32 bits of the
+    # turn, a rounded argument, pi U32 twice, and 2^-21.19 of the special-function unit: below 2^-20.
+    freqs = [1.0, 7.0, 6.283185307179586, 100.3, 1.0e4, 123456.789, 3.1e9, 2.0 ** 40, -3.7, -1.0e4, -1e-12, 1e-12, -2.0 ** -60,
+             0.1, 1 / 3, 0.0]
+    pos = [0, 1, -1, 5, 10 ** 9 + 7, -10 ** 9 + 1, 2 ** 38 + 12345, -2 ** 38 + 3, 2 ** 40 - 1, -2 ** 40 + 77, 2 ** 39 + 1]
+    dim, rot, T = 40, 2 * len(freqs), len(pos)
+    q, k, _, _, dy = _rope_inputs(T, 3, 2, dim, dtype, 1, 51, norm=False)
+    p = torch.tensor(pos, device="cuda")
+    ang = torch.tensor([[_angle(at, f) for f in freqs] for at in pos], dtype=torch.float64, device="cuda")[:, None]
+    c, s = torch.cos(ang), torch.sin(ang)
+    far = 2 * math.pi * 2.0 ** -64 * p.abs().double()[:, None, None]
+    unit = (10 * U32 if dtype == "f32" else 2.0 ** -20 + 10 * U32) + far
+    u_out = 1.01 * (U32 if dtype == "f32" else U16)
+    ia = torch.arange(0, rot, 2) if inter else torch.arange(rot // 2)
+    ib = ia + 1 if inter else ia + rot // 2
+    y = tp.tpmlp_qk_rope_forward(q, k, p, freqs, interleaved=inter)
+    d = tp.tpmlp_qk_rope_backward(*dy, q, k, p, freqs, interleaved=inter)
+    for name, x, got, sn in (("yq", q, y[0], s), ("yk", k, y[1], s), ("dq", dy[0], d[0], -s), ("dk", dy[1], d[1], -s)):
+        a, b = x[..., ia].double(), x[..., ib].double()
+        ref, tol = x.double().clone(), torch.zeros_like(x, dtype=torch.float64)
+        ref[..., ia], ref[..., ib] = a * c - b * sn, a * sn + b * c
+        tol[..., ia] = tol[..., ib] = (a.abs() + b.abs()) * unit
+        _close(got, ref, tol + u_out * ref.abs() + 1e-30, name)
+    tp.tpmlp_check_status()
