@@ -462,8 +462,8 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  *             possibly none. NULL: T = batch * max_seq tokens in equal sequences.
  *             A sequence that is out of order, outside the T rows or longer than
  *             max_seq is left out and recorded as TPMLP_ERR_BOUNDS (check 10) for
- *             the next tpmlp_check_status(). What rows hold that two sequences
- *             claim (starts that go back) is undefined.
+ *             the next tpmlp_check_status(), also where T or max_seq is 0. What
+ *             rows hold that two sequences claim (starts that go back) is undefined.
  *   scale     finite, > 0 (1 / sqrt(head_dim) is usual).
  *   lse       device fp32 [heads, T]; tpmlp_attn_core_backward needs it.
  * Rows of no sequence are left as they were, and it does not matter what they

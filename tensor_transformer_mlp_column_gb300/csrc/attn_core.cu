@@ -547,6 +547,15 @@ cudaError_t simt_dq(const CoreBackward& c, float* delta, cudaStream_t s) {
       c.s, ROWS, c.s.heads, dq_smem<DH, ROWS, BUFS>(), s, c, delta);
 }
 
+// The records of core_sequence() alone.
+__global__ void __launch_bounds__(256) core_sequences_kernel(CoreShape s, int* status) {
+  pdl_wait();
+  for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b < s.batch; b += int64_t(gridDim.x) * 256) {
+    int64_t row0;
+    core_sequence(s, static_cast<int>(b), row0, status);
+  }
+}
+
 // CTAs of `rows` tokens of each head and sequence that fill the GPU four times over.
 bool many(const CoreShape& s, int rows, int heads) {
   return int64_t((s.max_seq + rows - 1) / rows) * heads * s.batch >= 4 * num_sms();
@@ -564,6 +573,12 @@ size_t core_backward_workspace(int64_t T, int64_t batch, int64_t max_seq, int he
   const int splits = bf16 ? core_splits_tc(batch, max_seq, heads, kv_heads, dim) : 1;
   const size_t keys = static_cast<size_t>(batch) * ((max_seq + 127) / 128) * 128 * kv_heads;
   return delta_bytes(T, heads) + (splits > 1 ? 2 * splits * keys * dim * sizeof(float) : 0);
+}
+
+cudaError_t check_core_sequences(const CoreShape& s, int* status, cudaStream_t stream) {
+  const int64_t ctas = (int64_t(s.batch) + 255) / 256, most = 4 * num_sms();
+  return launch_pdl(core_sequences_kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256), 0, stream, s,
+                    status);
 }
 
 cudaError_t run_core_forward(const CoreForward& c, cudaStream_t s) {

@@ -60,6 +60,10 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& devices) {
   return e;
 }
 
+// Calls that compute nothing (no rows, or max_seq = 0) look at their sequences all the same: the ones that have tokens, or lie
+// outside of the rows, are recorded.
+cudaError_t check_core_sequences(const CoreShape& s, int* status, cudaStream_t stream);
+
 struct CoreForward {
   CoreShape s;
   HeadsView q, k, v, o;

@@ -123,6 +123,15 @@ CoreShape core_shape(const int32_t* starts, int64_t T, int64_t batch, int64_t ma
                    causal != 0};
 }
 
+// A call without rows or with max_seq = 0: nothing to compute, but sequences that are given are looked at.
+int nothing_to_compute(const CoreShape& s, cudaStream_t stream) {
+  if (!s.starts || s.batch == 0) return TPMLP_OK;
+  int rc = current_sm103();
+  if (rc) return rc;
+  CORE_TRY(check_core_sequences(s, device_status_word(), stream));
+  return TPMLP_OK;
+}
+
 // The load that every CTA withholds (test hook; 0: none), and the limit of a wait.
 struct Hook {
   int withhold;
@@ -134,7 +143,8 @@ int core_forward(const void* q, const void* k, const void* v, const int64_t* str
                             int causal, tpmlp_dtype dt, void* o, float* lse, Hook hook, cudaStream_t stream) {
   int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
   if (rc) return rc;
-  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
+  const CoreShape shape = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  if (T == 0 || batch == 0 || max_seq == 0) return nothing_to_compute(shape, stream);
   CoreForward c{};
   VIEW(c.q, q, 0, "q", heads);
   VIEW(c.k, k, 1, "k", kv_heads);
@@ -142,7 +152,7 @@ int core_forward(const void* q, const void* k, const void* v, const int64_t* str
   VIEW(c.o, o, 3, "o", heads);
   if (!lse || !aligned(lse, 4)) return set_error(lse ? TPMLP_ERR_ALIGN : TPMLP_ERR_ARG, "lse must not be NULL and 4-byte aligned");
   if ((rc = current_sm103())) return rc;
-  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  c.s = shape;
   c.lse = lse;
   c.bf16 = dt == TPMLP_BF16;
   c.withhold = hook.withhold;
@@ -158,7 +168,8 @@ int core_backward(const void* q, const void* k, const void* v, const void* o, co
                              void* dk, void* dv, void* ws, size_t ws_bytes, Hook hook, cudaStream_t stream) {
   int rc = check_core(strides, starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, dt);
   if (rc) return rc;
-  if (T == 0 || batch == 0 || max_seq == 0) return TPMLP_OK;
+  const CoreShape shape = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  if (T == 0 || batch == 0 || max_seq == 0) return nothing_to_compute(shape, stream);
   CoreBackward c{};
   VIEW(c.q, q, 0, "q", heads);
   VIEW(c.k, k, 1, "k", kv_heads);
@@ -173,7 +184,7 @@ int core_backward(const void* q, const void* k, const void* v, const void* o, co
   const size_t need = core_backward_workspace(T, batch, max_seq, heads, kv_heads, head_dim, dt == TPMLP_BF16);
   if (ws_bytes < need) return set_error(TPMLP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if ((rc = current_sm103())) return rc;
-  c.s = core_shape(starts, T, batch, max_seq, heads, kv_heads, head_dim, scale, causal);
+  c.s = shape;
   c.lse = lse;
   c.bf16 = dt == TPMLP_BF16;
   c.ws = ws;

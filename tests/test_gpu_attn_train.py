@@ -447,6 +447,52 @@ def test_nothing_to_do(tp):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("back", [False, True])
+def test_sequences_where_nothing_is_computed(tp, back, dtype):
+    # No rows, or a longest length of 0: nothing is written, and a sequence that has tokens all the same is recorded.
+    def call(q, k, v, do, starts, max_seq):
+        out = [torch.full_like(t, FILL) for t in (q, q, k, v)]
+        lse = torch.full((q.shape[1], q.shape[0]), FILL, device="cuda")
+        s = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        if back:
+            tp.tpmlp_attn_core_backward(q, k, v, q, lse, do, starts=s, max_seq=max_seq, dq=out[1], dk=out[2], dv=out[3])
+        else:
+            tp.tpmlp_attn_core_forward(q, k, v, starts=s, max_seq=max_seq, o=out[0], lse=lse)
+        torch.cuda.synchronize()
+        assert all(bool((t == FILL).all()) for t in (*out, lse))
+
+    some, none = _inputs(300, 2, 1, 64, dtype, 42), _inputs(0, 2, 1, 64, dtype, 42)
+    for x, starts, max_seq, fine in ((some, [0, 0, 0], 0, True), (some, [7], 0, True), (some, [300, 300], 0, True),
+                                     (some, [0, 100, 300], 0, False), (some, [5] * 999 + [6], 0, False),
+                                     (some, [0, 0, -1, -1], 0, False), (some, [301, 301], 0, False),
+                                     (none, [0, 0, 0], None, True), (none, [0], None, True), (none, [0, 5], None, False),
+                                     (none, [0, 0, 0, 1], 0, False)):
+        call(*x, starts, max_seq)
+        if fine:
+            tp.tpmlp_check_status()
+            continue
+        with pytest.raises(tp.TpmlpError) as e:
+            tp.tpmlp_check_status()
+        assert e.value.code == tp.TPMLP_ERR_BOUNDS and "sequence" in str(e.value)
+    # Captured into a graph, the check is one of its nodes.
+    s, o = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda"), torch.full_like(some[0], FILL)
+    lse = torch.zeros(2, 300, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        if back:
+            tp.tpmlp_attn_core_backward(*some[:3], o, lse, some[3], starts=s, max_seq=0)
+        else:
+            tp.tpmlp_attn_core_forward(*some[:3], starts=s, max_seq=0, o=o, lse=lse)
+    tp.tpmlp_check_status()
+    g.replay()
+    with pytest.raises(tp.TpmlpError):
+        tp.tpmlp_check_status()
+    s.zero_()
+    g.replay()
+    tp.tpmlp_check_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_token_of_a_large_layout(tp, dtype):
     # One token of buffers [heads, tokens, 64]: the token stride is less than a row of all heads, and not used.
     big = torch.full((9, 5000, 64), math.nan, device="cuda", dtype=DT[dtype])
