@@ -87,17 +87,21 @@ const char* tpmlp_last_error(void);
 
 /* Waits for `stream`, then reads and clears the current device's status word.
  * Returns TPMLP_OK, TPMLP_ERR_TIMEOUT if a kernel gave up on a wait since the
- * last check, TPMLP_ERR_BOUNDS if a device-side check of the debug build
- * failed (see tpmlp_build_flags), or TPMLP_ERR_CUDA if the stream reports an
+ * last check, TPMLP_ERR_BOUNDS if one found an id at or above V or a sequence
+ * outside its rows (the calls below say what it did then), or a device-side check
+ * of the debug build failed (see tpmlp_build_flags), or TPMLP_ERR_CUDA if the stream reports an
  * error or a kernel found its dynamic shared memory misaligned (it then did
  * no work). The first failure since the last check is the one reported. */
 int tpmlp_check_status(tpmlp_stream_t stream);
 
 /* Build flags of the loaded library: bit 0 is set in the debug build
  * (compiled with TPMLP_DEBUG; the Python binding loads it as
- * libtpmlp_debug.so when TPMLP_DEBUG=1 is set). In that build the kernels
- * check their tile, TMA-coordinate, output, reduce-slice and attention-tile
- * indices on the device; a failed check skips the access it guards (the
+ * libtpmlp_debug.so when TPMLP_DEBUG=1 is set). In that build the kernels of
+ * the MLP, of the collectives and of both attentions check their tile,
+ * TMA-coordinate, output, reduce-slice and attention-tile indices on the device,
+ * those of a training step's attention also where their shared memory ends
+ * (the lookup's, the cross entropy's and the clipping's have the checks of ids
+ * alone, which every build has); a failed check skips the access it guards (the
  * kernel does not trap), stops the kernel's work where skipping would leave
  * it waiting, and records TPMLP_ERR_BOUNDS for tpmlp_check_status. The
  * results of the two builds are identical when no check fails. */

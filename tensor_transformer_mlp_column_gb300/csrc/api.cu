@@ -513,8 +513,8 @@ int tpmlp_check_status(tpmlp_stream_t stream) {
                   c == kChkTarget ? "target" : "token", c);
     if (c == kChkSequence)
       return fail(TPMLP_ERR_BOUNDS, "a sequence outside its rows or longer than max_seq; it was left out (check %d)", c);
-    return fail(TPMLP_ERR_BOUNDS, "a device-side check failed: %s (check %d)", c > 0 && c < kChkCount ? kNames[c] : "?",
-                c);
+    return fail(TPMLP_ERR_BOUNDS, "a device-side check failed: %s (check %d)",
+                c == kChkArea ? "barriers past their shared memory" : c > 0 && c < kChkCount ? kNames[c] : "?", c);
   }
   if (v) return fail(TPMLP_ERR_TIMEOUT, "a device-side wait ran out of time (site %d)", v);
   return TPMLP_OK;

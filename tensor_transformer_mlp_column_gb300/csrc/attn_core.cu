@@ -236,7 +236,7 @@ struct Work {
       it.seq = static_cast<int>(i % per / walk.heads);
     }
     it.len = core_sequence(s, it.seq, it.row0, walk.status);
-    return it.tile * ROWS < it.len;
+    return it.tile * ROWS < it.len && in_bounds(s, it, walk.heads, ROWS, walk.status);
   }
 };
 

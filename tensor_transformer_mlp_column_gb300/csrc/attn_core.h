@@ -118,6 +118,7 @@ struct RopeCall {
   float* dw[2];                 // [dim]
   void* ws;
   int bf16;
+  int* status;
 };
 size_t rope_backward_workspace(int64_t T, int heads, int kv_heads, int dim);
 cudaError_t run_qk_rope(const RopeCall& c, cudaStream_t stream);

@@ -270,6 +270,7 @@ int qk_rope(int backward, const void* dyq, const void* dyk, const void* q, const
       if (in->p == c.y[i].p && (in->token != c.y[i].token || in->head != c.y[i].head))
         return set_error(TPMLP_ERR_ARG, "an output in the place of its input must have the input's strides");
   if ((rc = current_sm103())) return rc;
+  c.status = device_status_word();
   CORE_TRY(run_qk_rope(c, stream));
   return TPMLP_OK;
 }

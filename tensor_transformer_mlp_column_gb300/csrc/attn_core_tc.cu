@@ -309,6 +309,13 @@ __device__ __forceinline__ float* part_of(const TcParams& p, int z, int split, i
   return p.part + (at * kRows + row) * p.s.dim;
 }
 
+// Debug build: whether there are such sums.
+__device__ __forceinline__ bool part_exists(const TcParams& p, int split, int seq, int tile, int kv) {
+  return TPMLP_DCHECK(split >= 0 && split < p.splits && seq >= 0 && seq < p.s.batch && tile >= 0 && tile < p.tiles && kv >= 0 &&
+                          kv < p.s.kv_heads,
+                      p.status, kChkReduce);
+}
+
 // The items of a CTA, found by its loading warp, in order of their work (attn_core_walk.cuh); of equal sequences those in
 // order are all tiles of one index.
 struct Walk {
@@ -333,7 +340,7 @@ struct Walk {
       return false;
     }
     it.len = core_sequence(p.s, it.seq, it.row0, p.status);
-    return true;
+    return in_bounds(p.s, it, sequences.heads, sequences.rows, p.status);
   }
 };
 
@@ -388,6 +395,11 @@ __device__ __forceinline__ bool misaligned(const uint8_t* smem, int* status) {
   return true;
 }
 
+// Debug build: whether what follows the barriers ends within the kernel's `bytes` of shared memory.
+__device__ __forceinline__ bool fits(const uint8_t* smem, size_t bytes, const volatile int* last, int* status) {
+  return TPMLP_DCHECK(smem_addr(const_cast<const int*>(last + 1)) <= smem_addr(smem) + bytes, status, kChkArea);
+}
+
 // ------------------------------------------------------------------ forward
 
 template <int DH, int NQ>
@@ -428,6 +440,7 @@ __global__ void __launch_bounds__(FwdCfg<DH, NQ>::THREADS, FwdCfg<DH, NQ>::CTAS)
   const ItemRing ring_i(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  if (!fits(smem, C::SMEM, abort_flag, p.status)) return;
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -731,6 +744,7 @@ __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_
   const ItemRing ring_i(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  if (!fits(smem, C::SMEM, abort_flag, p.status)) return;
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1099,6 +1113,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
   const ItemRing ring_i(drain + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_i.empty + kItemSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  if (!fits(smem, C::SMEM, abort_flag, p.status)) return;
 
   const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1178,6 +1193,11 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
       fetch(h, x);
       for (int i = 0; i < ps.n; ++i) {
         const int64_t row = it.row0 + (ps.first + x) * W;
+        ok = TPMLP_DCHECK(h < (kv + 1) * group && (ps.first + x) * W < it.len, p.status, kChkAttnTile);
+        if (!ok) {
+          *abort_flag = 1;
+          break;
+        }
         ok = ring_q.wait_empty(issued_q, guard);
         if (!ok) break;
         if (issued_q + 1 != p.withhold && elect_one()) {
@@ -1394,7 +1414,7 @@ __global__ void __launch_bounds__(DkvCfg<DH, W>::THREADS, DkvCfg<DH, W>::CTAS)
           if (kj >= len) continue;
           if (p.splits == 1)
             store_row(z ? dk : dv, o, z ? p.s.scale : 1.f, y, p.s.dim);
-          else
+          else if (part_exists(p, head % p.splits, seq, k0 / kRows, kv))
             store_sums(part_of(p, z, head % p.splits, seq, k0 / kRows, kv, row), o, y, p.s.dim);
         }
       }
@@ -1431,7 +1451,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
   const int len = core_sequence(p.s, seq, row0, p.status);
   const int units = p.s.dim / 8, i = blockIdx.y * 256 + threadIdx.x;  // of 2 x 128 x units
   const int z = i / (kRows * units), row = i / units % kRows, e = i % units * 8;
-  if (tile * kRows + row >= len) return;
+  if (tile * kRows + row >= len || !part_exists(p, p.splits - 1, seq, tile, kv)) return;
   const int64_t at = row0 + tile * kRows + row;
   const float* from = part_of(p, z, 0, seq, tile, kv, row) + e;
   const int64_t step = int64_t(p.s.batch) * p.tiles * p.s.kv_heads * kRows * p.s.dim;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attn_core.h"
+#include "device.cuh"
 
 namespace tpmlp {
 
@@ -13,6 +14,14 @@ struct Item {
   int64_t row0;
   int tile, head, len, seq;  // len 0: no more items
 };
+
+// Debug build: whether an item lies in its sequence and that in the T rows, so that everything read and written for it does.
+// A CTA whose item does not ends as after its last one.
+__device__ __forceinline__ bool in_bounds(const CoreShape& s, const Item& it, int heads, int rows, int* status) {
+  return TPMLP_DCHECK(it.seq >= 0 && it.seq < s.batch && it.head >= 0 && it.head < heads && it.tile >= 0 &&
+                          int64_t(it.tile) * rows < it.len && it.row0 >= 0 && it.row0 + it.len <= s.T,
+                      status, kChkAttnTile);
+}
 
 // The place of a CTA's item number `round` among all, which are in order of their work, the most first: a CTA takes one
 // of every gridDim.x, from the front and from the back in turn, so that all get about the same.

@@ -32,6 +32,7 @@ enum DebugCheck : int {
   kChkAttnTile = 5,  // an attention query tile, head or sequence outside the launch's bounds
   kChkSelftest = 6,  // tpmlp_selftest_bounds: the requested index is outside its 32-element array
   kChkCount = 7,
+  kChkArea = 11,  // barriers past the end of a kernel's shared memory (8 to 10 are of both builds: train.h, attn_core.h)
 };
 
 // Whether this library was built with the device-side checks (TPMLP_DEBUG).

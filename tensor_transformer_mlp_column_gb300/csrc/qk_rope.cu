@@ -180,7 +180,9 @@ __global__ void __launch_bounds__(kThreads, BACK ? 2 : 3) rope_kernel(const __gr
     // The next kernel's CTAs come when this one's last items are begun: any earlier they take the places of its own (2000
     // tokens, 16 + 4 heads of 128, forward and gradients: 19.9 us with the trigger at the start, 18.7 here).
     if (base + step >= items) pdl_launch_dependents();
-    const bool live = item < items && on;
+    const bool live = item < items && on &&
+                      TPMLP_DCHECK(t >= 0 && t < s.T && h0 >= 0 && h0 < heads && a + RUN <= s.dim && b + RUN <= s.dim, c.status,
+                                   kChkOutput);
     const int64_t pos = live && alike ? s.pos[s_axis[RUN * u] * s.T + t] : 0;
     const T* x = static_cast<const T*>(xv.p) + t * xv.token + h0 * xv.head;
     const T* g = BACK ? static_cast<const T*>(gv.p) + t * gv.token + h0 * gv.head : nullptr;
@@ -304,13 +306,14 @@ __global__ void __launch_bounds__(kThreads, BACK ? 2 : 3) rope_kernel(const __gr
 constexpr int kMostParts = 10;
 static_assert(152 * 2 <= 32 * kMostParts, "parts of the backward's CTAs");
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int ctas_q, int ctas_k, int dim, float* dwq,
-                                                       float* dwk) {
+                                                       float* dwk, int* status) {
   __shared__ float rows[32][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kind = blockIdx.y, col = blockIdx.x * 32 + lane;
   const int first = kind ? ctas_q : 0, last = kind ? ctas_q + ctas_k : ctas_q;
+  if (!TPMLP_DCHECK(last - first <= 32 * kMostParts, status, kChkReduce)) return;
   float x[kMostParts];
 #pragma unroll
   for (int j = 0; j < kMostParts; ++j) {
@@ -400,7 +403,7 @@ cudaError_t run_qk_rope(const RopeCall& c, cudaStream_t s) {
                                : launch_rope<__nv_bfloat16, 4>(c, p, s);
   if (e != cudaSuccess || !c.backward || !norm) return e;
   return launch_pdl(rope_dw_kernel, dim3((c.s.dim + 31) / 32, 2), dim3(1024), 0, s, static_cast<const float*>(c.ws),
-                    p.ctas[0], p.ctas[1], c.s.dim, c.dw[0], c.dw[1]);
+                    p.ctas[0], p.ctas[1], c.s.dim, c.dw[0], c.dw[1], c.status);
 }
 
 }  // namespace tpmlp

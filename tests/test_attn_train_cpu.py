@@ -329,3 +329,15 @@ def test_frequencies_changed_in_place(tp):
     assert made([0.1] * 4, None)[0] == [0.1] * 4
     assert made(list(np.full(4, 0.1, np.float32)), None)[0] == [float(np.float32(0.1))] * 4
     assert made([0.1] * 4, None)[0] == [0.1] * 4
+
+
+@pytest.mark.parametrize("name,least", [("attn_core.cu", 1), ("attn_core_tc.cu", 6), ("attn_core_walk.cuh", 1), ("qk_rope.cu", 2)])
+def test_debug_checks_stand_in_the_kernels(name, least):
+    # Items and shared-memory areas, sums of runs, elements of heads: what the debug build is said to check.
+    import os
+    import re
+
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tensor_transformer_mlp_column_gb300", "csrc")
+    with open(os.path.join(csrc, name)) as f:
+        text = f.read()
+    assert len(re.findall(r"\b(?:TPMLP_DCHECK|in_bounds|fits|part_exists)\(", text)) >= least
