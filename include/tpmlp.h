@@ -466,7 +466,8 @@ int tpmlp_attn_forward(const void* X, int64_t batch, int64_t seq, const tpmlp_at
  *             possibly none. NULL: T = batch * max_seq tokens in equal sequences.
  *             A sequence that is out of order, outside the T rows or longer than
  *             max_seq is left out and recorded as TPMLP_ERR_BOUNDS (check 10) for
- *             the next tpmlp_check_status(), also where T or max_seq is 0. What
+ *             the next tpmlp_check_status(), also where T or max_seq is 0. A max_seq
+ *             near the longest length is worth giving (see the backward). What
  *             rows hold that two sequences claim (starts that go back) is undefined.
  *   scale     finite, > 0 (1 / sqrt(head_dim) is usual).
  *   lse       device fp32 [heads, T]; tpmlp_attn_core_backward needs it.
@@ -500,7 +501,10 @@ size_t tpmlp_attn_core_workspace_bytes(int64_t T, int64_t batch, int64_t max_seq
  * Every sum has a fixed order: bitwise reproducible in calls of the same batch,
  * max_seq and heads (how sums of dk and dv are cut follows these). bf16 rounds p and ds to bf16
  * as operands and each result once; the rest of ds goes in as a second bf16 number in dq of
- * heads below 64 and, where max_seq is at most 64 (heads above 64: 128), in dq and dk. What
+ * heads below 64 and, where max_seq is at most 64 (heads above 64: 128), in dq and dk: with a
+ * max_seq above that the same short sequences' dq and dk are off by 0.0024 of their size in the
+ * place of 0.0017. How passes over few tiles of keys are cut goes by max_seq too (one kv head
+ * for 32, 8 sequences of 512 tokens: dk and dv 64 us, with max_seq left at T 211). What
  * delta is off because o was rounded is found as the sum of a row's ds and taken out of ds's
  * products again. */
 int tpmlp_attn_core_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,

@@ -841,8 +841,8 @@ def tpmlp_attn_core_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s
     """Softmax attention of q [T, heads, head_dim] over k, v [T, kv_heads, head_dim]: (o as q, lse [heads, T] fp32).
 
     The T tokens are `batch` equal sequences (default 1), or those from starts[b] to starts[b + 1] - 1 (int32 on the
-    GPU), none longer than max_seq (default T). Rows of no sequence are left as they were: undefined in an o or lse
-    that the call allocates. scale is 1 / sqrt(head_dim) by default."""
+    GPU), none longer than max_seq (default T; the longest length is the better value: see tpmlp_attn_core_backward).
+    Rows of no sequence are left as they were: undefined in an o or lse that the call allocates. scale is 1 / sqrt(head_dim) by default."""
     T, heads, kv, dim = _qkv_shape(q, k)
     dt, strides = _type(q), []
     with _On(stream) as on:
@@ -878,7 +878,10 @@ def tpmlp_attn_core_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
                              dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
                              dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of sum(o * do) of tpmlp_attn_core_forward with the same arguments: (dq, dk, dv), as q, k, v. The
-    probabilities are made again from lse. Rows of no sequence are left as they were."""
+    probabilities are made again from lse. Rows of no sequence are left as they were: undefined in gradients that the
+    call allocates. With max_seq far above the lengths, dk and dv of few sequences on few kv heads take longer (bf16, 8 of
+    512 tokens, 32 heads on one: 211 us in the place of 64), and dq and dk of sequences within 64 tokens (heads above 64:
+    128) are off by 0.0024 in the place of 0.0017."""
     T, heads, kv, dim = _qkv_shape(q, k)
     dt, l, strides = _type(q), lib(), []
     with _On(stream) as on:

@@ -26,7 +26,10 @@
 // for 64 multiply-adds a lane (65 to 78 % of that path busy, 54 to 60 of the FMA pipe;
 // which lanes read the same line makes no difference): 16 heads of 128, 4 x 1024 tokens, causal, 463,
 // 706 (dQ) and 976 us (dK, dV), 37, 37 and 35 TFLOP/s of about 75; 16 heads of 64
-// 239, 358 and 462.
+// 239, 358 and 462. A key tile walks over all queries of its group by itself, so dK
+// and dV take long where one kv head serves many (1024 tokens, 4 heads of 128 on 4:
+// 272 us, on one: 1062; 4096 tokens, 32 on one: 33.7 ms, the bf16 kernel, which cuts
+// such walks into runs, 0.2).
 #include "attn_core.h"
 
 #include <algorithm>

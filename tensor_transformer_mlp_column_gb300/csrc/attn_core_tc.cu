@@ -10,8 +10,9 @@
 //            dQ += dS K, and P K, which puts dQ right for what delta is off.
 //   dK, dV   items of a key tile of a kv head, over the query tiles of all heads
 //            that share it: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
-// Making S and dP twice costs 8 products in the place of 5, but every sum has
-// one owner: no atomics, no order that changes, no fp32 dQ in memory.
+// Making S and dP twice costs 7 products in the place of 5 (the mean key's is an
+// eighth), but every sum has one owner: no atomics, no order that changes, no
+// fp32 dQ in memory.
 //
 // All tiles come by TMA through a 3-D map (element, head, token) that knows any
 // strides. P and dS never leave the SM: the threads that read S from tensor
@@ -25,10 +26,13 @@
 // tokens are cleared in shared memory, so that no value of another sequence, not
 // even a NaN, meets a weight of zero.
 //
-// Bound by the tensor cores where heads are long (8192 tokens, 16 heads of 128, no
-// mask: forward 386 us, 1.43 PFLOP/s, dQ 614 us, 1.79 with the product of P and K,
-// dK and dV 665 us, 1.65), by the chain from S to P and dS where they are short
-// (heads of 64: 310, 463 and 578 us, 0.89, 1.19 and 0.95 PFLOP/s).
+// Bound by the chain from S to P and dS: scores out of tensor memory, exponentials,
+// bf16 numbers back into it. Beside it the tensor pipe is active for 49 % of the
+// cycles (forward), 56 to 65 (dQ) and 60 (dK, dV) where heads are long, of the 75
+// that a plain matrix product takes, and for 15 to 24 % where they are short (512
+// tokens, heads of 64). 8192 tokens, 16 heads of 128, no mask: forward 386 us, 1.43
+// PFLOP/s, dQ 614 us, 1.79 with the product of P and K, dK and dV 665 us, 1.65;
+// heads of 64: 310, 463 and 578 us, 0.89, 1.19 and 0.95 PFLOP/s.
 //
 // The next kernel of the stream is let in by the loading warp when it has fetched its
 // last item. Let in at the start, its CTAs waited in places beside the ones still at
@@ -416,7 +420,8 @@ struct FwdCfg {
 };
 
 // The row's maximum so far, raised where the tile's is above it by more than
-// 2^8 in weight: until then weights stay below 2^8 and O needs no factor.
+// 2^8 in weight: until then weights stay below 2^8 and O needs no factor (a
+// published method for attention on this generation of GPUs).
 //
 // Two query tiles take turns: one's products run while the other is in the
 // softmax. An item's Q is fetched once the last item's scores are made, under its
@@ -687,7 +692,7 @@ struct DqCfg {
   static constexpr uint32_t TMEM = 2 * W + 2 * DH <= 256 ? 256 : 512;
   static constexpr int CTAS = TMEM == 256 ? 2 : 1;  // an SM's
   // Columns of a softmax warp: 64, but 32 for short heads, whose tiles are half as wide (8 x 2048 tokens, 32 heads of 128:
-  // 417 us with 64, 434 with 32; 16 heads of 64: 145 and 140).
+  // with 32 4 % slower; 16 heads of 64: with 64 4 % slower).
   static constexpr int COLUMNS = DH == 64 ? 32 : 64, GROUPS = W / COLUMNS, WARPS = 4 * GROUPS;
   static constexpr int THREADS = (WARPS + 2) * 32;
   static constexpr size_t BARS = 8 * (2 * KS + 2 * VS + 9) + kItemBytes + 8;
@@ -706,14 +711,14 @@ struct DqCfg {
 // max_seq is within the tile of W). 8 x 2048 tokens, 16 heads of 32: 124 -> 142 us,
 // 0.0024 -> 0.0017; 128 x 100 tokens, 32 heads of 128 on 8: 117 -> 131, dK and dV 94
 // -> 104. With longer heads and sequences, where all sums are long, it is left out
-// (8 x 2048 tokens, 32 heads of 128 on 8: 0.0024 and 415 us, with it 508).
+// (8 x 2048 tokens, 32 heads of 128 on 8: 0.0024, and dQ 22 % slower with it).
 //
 // delta comes in as dO . O with the O that the forward rounded to bf16, which is
 // as far off as dQ's own rounding. But the row's sum of dS, zero for the exact
 // delta, says how far: e = sum of p dp - delta. dK's kernel gets delta + e, and dQ
 // is put right with the row's mean key, dQ = sum of dS k - e sum of P k: a fourth
-// product, for 0.0023 in the place of 0.0030 as dQ's error (8 x 2048 tokens, 32
-// heads of 128). Rows with a single key tile take their own sum of p dp from the
+// product, for 0.0024 in the place of 0.0030 as dQ's error (8 x 2048 tokens, 32
+// heads of 128; dQ 377 -> 407 us). Rows with a single key tile take their own sum of p dp from the
 // start.
 template <int DH, int W, bool FINE>
 __global__ void __launch_bounds__(DqCfg<DH, W>::THREADS, DqCfg<DH, W>::CTAS) dq_kernel(const __grid_constant__ TcParams p) {
@@ -1473,7 +1478,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcPar
 // CTA, of four tiles of 128 queries at least. (One sequence, causal, heads of 128, whole -> in runs: 4096 tokens, 32 heads on
 // one kv head 1418 -> 209 us, 8192 tokens, 2 on one 186 -> 68; 512 tokens, 8 on one 61 -> 24; 1024 tokens, 4 on 4 22.5 ->
 // 23.4. Two runs where the tiles do fill it, for more even CTAs, gain 3 % at 16384 tokens, 8 heads on 2, and lose 60 % at
-// 4096, 8 on 8.)
+// 4096, 8 on 8.) The tiles are those that max_seq gives every sequence, as the sums' places are: with max_seq far above the
+// lengths there are no runs (8 x 512 tokens, 32 heads of 128 on one kv head: 64 us with max_seq = 512, 211 with 4096).
 constexpr int kMaxSplits = 32;
 int splits_of(int64_t items, int64_t passes, int ctas) {
   const int64_t full = int64_t(num_sms()) * ctas;

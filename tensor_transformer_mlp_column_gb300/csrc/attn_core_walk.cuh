@@ -23,15 +23,19 @@ __device__ __forceinline__ bool in_bounds(const CoreShape& s, const Item& it, in
                       status, kChkAttnTile);
 }
 
-// The place of a CTA's item number `round` among all, which are in order of their work, the most first: a CTA takes one
-// of every gridDim.x, from the front and from the back in turn, so that all get about the same.
+// The place of a CTA's item number `round` among all: a CTA takes one of every gridDim.x, from the front and from the back in
+// turn, so that all get about the same where the items are in order of their work, the most first.
 __device__ __forceinline__ uint64_t walk_place(uint64_t round) {
   const uint32_t g = gridDim.x;
   return round * g + (round & 1 ? g - 1 - blockIdx.x : blockIdx.x);
 }
 
-// The items of sequences of any lengths in order of their work: 64 sequences at a time, the ones with at least d tiles, d
-// from the longest's down (their d-th tile from the front, or from the back). All tiles of one index, of which
+// The items of sequences of any lengths: 64 sequences at a time, the ones with at least d tiles, d from the longest's down
+// (their d-th tile from the front, or from the back). With a causal mask that is the order of their work. Without one every
+// tile of a sequence costs the whole length, and the longest sequences' last items come among those of short ones: of 13
+// sequences of 1 to 1500 tokens, 12 heads, the fullest CTA of 152 has 58 tiles of 128 keys where the average is 40.6 (in
+// order of the lengths it would have 42); 12 heads of 128: forward, dQ, dK and dV 71, 111 and 119 us, 13 equal sequences of
+// as many tokens, with 0.64 of the scores, 59, 80 and 84. With a causal mask: all tiles of one index, of which
 // those past a sequence's end are skipped, was worse: of 13 sequences of 1 to 1500 tokens, 12 heads, causal, the fullest
 // CTA of dQ (bf16) had 66 key tiles in the place of 36 (33.6 on average), and of 1000 sequences in 65536 tokens, 32 heads of
 // 128 on 8, it took dQ 888 us in the place of 756, and 16600 where max_seq was left at 65536.
