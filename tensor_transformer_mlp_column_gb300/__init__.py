@@ -917,8 +917,14 @@ _last_turns = (None, None, 0, None)
 _NUMBERS = {int, float}
 
 
-def _own_numbers(x) -> bool:
-    return isinstance(x, (list, tuple)) and set(map(type, x)) <= _NUMBERS
+def _axis_values(axis):
+    """The axes by value: their bytes, () for none, None where they are no list of small integers."""
+    if axis is None:
+        return ()
+    try:
+        return bytes(axis) if type(axis) in (list, tuple) else None
+    except (TypeError, ValueError, OverflowError):
+        return None
 
 
 def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
@@ -933,13 +939,14 @@ def _rope_args(q, k, pos, freqs, axis, interleaved, wq, wk, eps, dev):
     # the list too, and compare in their own precision.
     global _last_turns
     last = _last_turns
-    plain = _own_numbers(freqs) and (axis is None or _own_numbers(axis))
-    if plain and last[0] == freqs and last[1] == axis and last[2] == axes:
+    turned_by = _axis_values(axis)
+    plain = turned_by is not None and isinstance(freqs, (list, tuple)) and set(map(type, freqs)) <= _NUMBERS
+    if plain and last[0] == freqs and last[1] == turned_by and last[2] == axes:
         keep = last[3]
     else:
         keep = _turns(tuple(map(float, freqs)), None if axis is None else tuple(map(int, axis)), axes)
         if plain:
-            _last_turns = (freqs[:], None if axis is None else axis[:], axes, keep)
+            _last_turns = (freqs[:], turned_by, axes, keep)
     wqp = 0 if wq is None else _like(wq, (dim,), q.dtype, dev, "wq")
     wkp = 0 if wk is None else _like(wk, (dim,), q.dtype, dev, "wk")
     return (T, heads, kv, dim), (wqp, wkp, eps, _ptr(pos, dev, "pos"), keep[2], keep[3], T, heads, kv, dim,

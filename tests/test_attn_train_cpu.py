@@ -341,3 +341,22 @@ def test_debug_checks_stand_in_the_kernels(name, least):
     with open(os.path.join(csrc, name)) as f:
         text = f.read()
     assert len(re.findall(r"\b(?:TPMLP_DCHECK|in_bounds|fits|part_exists)\(", text)) >= least
+
+
+def test_axes_by_value(tp):
+    import torch
+
+    q, k, pos = torch.zeros(6, 4, 64), torch.zeros(6, 2, 64), torch.zeros(2, 6, dtype=torch.int64)
+
+    def made(a):
+        return tp._rope_args(q, k, pos, [1.0] * 4, a, False, None, None, 1e-6, -1)[2][1]
+
+    for _ in range(2):
+        assert made(None) is None
+        for bad in ([], [0], [0, 0, 0, 2], [0, 0, 0, -1], [0, 0, 0, 300], [0, 0, 0, 2 ** 70], [0] * 5):
+            with pytest.raises(ValueError, match="axis"):
+                made(bad)
+        for a in ([0, 1, 0, 1], (0, 1, 0, 1), [0.0, 1.0, 0.0, 1.0], torch.tensor([0, 1, 0, 1]), list(torch.tensor([0, 1, 0, 1])),
+                  [False, True, False, True]):
+            assert made(a).tolist() == [0, 1, 0, 1]
+        assert made([1, 1, 0, 0]).tolist() == [1, 1, 0, 0]
