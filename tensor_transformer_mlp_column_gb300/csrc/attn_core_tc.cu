@@ -320,8 +320,8 @@ __device__ __forceinline__ bool part_exists(const TcParams& p, int split, int se
                       p.status, kChkReduce);
 }
 
-// The items of a CTA, found by its loading warp, in order of their work (attn_core_walk.cuh); of equal sequences those in
-// order are all tiles of one index.
+// The items of a CTA, found by its loading warp, in the order that attn_core_walk.cuh gives sequences of any lengths; equal
+// sequences' are all tiles of one index after another, with a causal mask those with the most work first.
 struct Walk {
   const TcParams& p;
   SequenceWalk sequences;
